@@ -7,10 +7,12 @@ loaded, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -88,6 +90,15 @@ def library() -> ctypes.CDLL:
         L.attn_last_error_string.restype = ctypes.c_char_p
         L.attn_fwd_work_order.argtypes = [i, i, i, P, i]
         L.attn_fwd_work_order.restype = i
+        i64 = ctypes.c_longlong
+        L.attn_kv_write.argtypes = [P, P, i64, i64, P, P, P, P, P, i, i, i, i, i, i, P]
+        L.attn_kv_write.restype = i
+        L.attn_kv_read.argtypes = [P, P, P, P, P, i64, i, P, P, P, i, i, i, i, i, i, i, P]
+        L.attn_kv_read.restype = i
+        L.attn_fwd_paged_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
+        L.attn_fwd_paged_workspace_size.restype = sz
+        L.attn_fwd_paged.argtypes = [P, P, P, P, P, P, i, P, i64, i, P, P, P, i, i, i, i, i, i, i, i, i, f, P, sz, P]
+        L.attn_fwd_paged.restype = i
         _lib = L
         return _lib
 
@@ -486,6 +497,189 @@ def fp8_prepare_qkv(q, k, v, mode: int = MODE_BLOCK_HADAMARD, sign_seed: int = 0
         k8, ks = attn_fp8_prep_rope(k, c, s_, mode, sign_seed, il, stream=stream)
     v8, vs = attn_fp8_prep(v, mode, sign_seed, True, stream=stream)
     return q8, k8, v8, qs, ks, vs
+
+
+CACHE_BF16, CACHE_E4M3 = 0, 1
+
+
+class KVCache(NamedTuple):
+    """A paged key/value cache on the GPU: k and v are (num_pages, H_kv,
+    page_size, d), bf16, or e4m3 codes (uint8 or float8_e4m3fn) with the float32
+    row scales (num_pages, H_kv, page_size) beside them (None for bf16)."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor | None = None
+    v_scale: torch.Tensor | None = None
+
+
+def kv_cache(num_pages: int, page_size: int, H_kv: int, d: int, e4m3: bool = True, device=None) -> KVCache:
+    """A KVCache of zeros on `device` (default: the current one)."""
+    device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    shape = (num_pages, H_kv, page_size, d)
+    dtype = torch.uint8 if e4m3 else torch.bfloat16
+    k, v = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
+    if not e4m3:
+        return KVCache(k, v)
+    ks, vs = (torch.ones(shape[:3], dtype=torch.float32, device=device) for _ in range(2))
+    return KVCache(k, v, ks, vs)
+
+
+def _check_cache(cache):
+    """(num_pages, H_kv, page_size, d, cache dtype) of a KVCache."""
+    k, v, ks, vs = cache
+    if not k.is_cuda or k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+        raise ValueError("cache k and v must be CUDA tensors of one (num_pages, H_kv, page_size, d) shape and dtype")
+    if not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError("cache k and v must be contiguous")
+    if k.dtype == torch.bfloat16:
+        if ks is not None or vs is not None:
+            raise ValueError("a bf16 cache has no scales")
+        return (*k.shape, CACHE_BF16)
+    if k.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        raise ValueError("cache k and v must be bf16 or e4m3 codes (uint8 or float8_e4m3fn)")
+    for s in (ks, vs):
+        if (s is None or s.dtype != torch.float32 or s.shape != k.shape[:3] or not s.is_contiguous()
+                or s.device != k.device):
+            raise ValueError("an e4m3 cache has contiguous float32 (num_pages, H_kv, page_size) scales")
+    return (*k.shape, CACHE_E4M3)
+
+
+def _check_table(block_table, seq_lens, B, device):
+    if (block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32
+            or block_table.device != device or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+        raise ValueError("block_table must be an int32 (B, max_pages) tensor with contiguous rows on the cache's device")
+    if seq_lens.shape != (B,) or seq_lens.dtype != torch.int32 or seq_lens.device != device or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be a contiguous int32 (B,) tensor on the cache's device")
+    max_pages = block_table.shape[1]
+    stride = block_table.stride(0) if B > 1 else max_pages
+    if stride < max_pages:
+        raise ValueError("the rows of block_table must not overlap")
+    return max_pages, stride
+
+
+def _torch_stream_scope(stream, device):
+    """Makes `stream` torch's current one (zeros written for its kernels must
+    be written on it)."""
+    return torch.cuda.stream(_torch_stream(stream, device)) if stream is not None else contextlib.nullcontext()
+
+
+def _on(device):
+    """Makes `device` the current one around a launch (a no-op where it is)."""
+    return torch.cuda.device(device)
+
+
+def _stream_on(stream, device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+
+
+def attn_kv_write(k, v, slots, cache: KVCache, stream=None) -> None:
+    """Writes the keys and values of T new tokens into their slots of the
+    cache, quantising each row for an e4m3 cache (scale = amax / 448 per token
+    and head).
+
+    k, v: bf16 (T, H_kv, d) CUDA tensors; a token's heads are contiguous, tokens
+    may be strided (columns of one projection).  slots: int64 (T,), page *
+    page_size + row; negative slots are skipped, those >= 0 must differ.  A slot
+    beyond the cache is skipped and reported by device_status().
+    """
+    pages, Hkv, ps, d, dtype = _check_cache(cache)
+    dev = cache.k.device
+    if k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (Hkv, d):
+        raise ValueError(f"k and v must be (T, {Hkv}, {d}) tensors")
+    T = k.shape[0]
+    for t in (k, v):
+        if t.dtype != torch.bfloat16 or t.device != dev:
+            raise ValueError("k and v must be bf16 tensors on the cache's device")
+        if t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != d):
+            raise ValueError("a token's heads must be contiguous in k and v")
+    if slots.shape != (T,) or slots.dtype != torch.int64 or slots.device != dev or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous int64 (T,) tensor on the cache's device")
+    with _on(dev):
+        rc = library().attn_kv_write(_ptr(k), _ptr(v), k.stride(0) if T > 1 else Hkv * d,
+                                     v.stride(0) if T > 1 else Hkv * d, _ptr(slots), _ptr(cache.k), _ptr(cache.v),
+                                     _ptr(cache.k_scale), _ptr(cache.v_scale), T, Hkv, d, pages, ps, dtype,
+                                     ctypes.c_void_p(_stream_on(stream, dev)))
+    _check("attn_kv_write", rc)
+
+
+def attn_kv_read(cache: KVCache, block_table, seq_lens, N: int, out_k=None, out_v=None, stream=None):
+    """The first min(seq_lens[b], N) tokens of every sequence as bf16 (B, N,
+    H_kv, d) keys and values (e4m3: scale * value, rounded once).
+
+    block_table: int32 (B, max_pages), rows may be strided; seq_lens: int32
+    (B,).  Rows from a sequence's length on are left as they were in out_k /
+    out_v (zeros where these are allocated here).  Returns (k, v).
+    """
+    pages, Hkv, ps, d, dtype = _check_cache(cache)
+    dev = cache.k.device
+    B = block_table.shape[0]
+    max_pages, stride = _check_table(block_table, seq_lens, B, dev)
+    shape = (B, N, Hkv, d)
+    with _on(dev), _torch_stream_scope(stream, dev):
+        k = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if out_k is None else out_k
+        v = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if out_v is None else out_v
+        for t in (k, v):
+            if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != dev:
+                raise ValueError(f"out_k and out_v must be contiguous bf16 {shape} tensors on the cache's device")
+        rc = library().attn_kv_read(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
+                                    _ptr(block_table), stride, max_pages, _ptr(seq_lens), _ptr(k), _ptr(v), B, N, Hkv,
+                                    d, pages, ps, dtype, ctypes.c_void_p(_stream_on(stream, dev)))
+    _check("attn_kv_read", rc)
+    return k, v
+
+
+def paged_workspace_bytes(B: int, Nq: int, H: int, H_kv: int, d: int, prefix_len: int, max_pages: int,
+                          page_size: int) -> int:
+    return int(library().attn_fwd_paged_workspace_size(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size))
+
+
+def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, prefix_len: int = 0,
+                   causal: bool = True, scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of Nq query tokens of each of B sequences over the paged cache:
+    the shared prefix (read once for the whole batch) followed by each
+    sequence's own tokens, whose last Nq are the queries.
+
+    q: bf16 (B, Nq, H, d); block_table: int32 (B, max_pages), the own pages (rows
+    may be strided, e.g. a full table without its shared columns); seq_lens:
+    int32 (B,), the own tokens; prefix_table: int32 (>= ceil(prefix_len /
+    page_size),); prefix_len: host int.  causal: query i sees own keys j <=
+    seq_lens[b] - Nq + i (all of them otherwise), and the whole prefix.
+    workspace: optional uint8 CUDA tensor of at least paged_workspace_bytes(...)
+    bytes, scratch.  Returns (O (B, Nq, H, d) bf16, LSE (B, H, Nq) float32).
+    """
+    pages, Hkv, ps, d, dtype = _check_cache(cache)
+    dev = cache.k.device
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or q.device != dev or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 (B, Nq, H, d) tensor on the cache's device")
+    B, Nq, H, dq = q.shape
+    if dq != d or H % Hkv != 0:
+        raise ValueError("q's head dim must be the cache's and its heads a multiple of the cache's")
+    max_pages, stride = _check_table(block_table, seq_lens, B, dev)
+    prefix_len = int(prefix_len)
+    if prefix_len > 0 and (prefix_table is None or prefix_table.dim() != 1 or prefix_table.dtype != torch.int32
+                           or prefix_table.device != dev or not prefix_table.is_contiguous()
+                           or prefix_table.shape[0] * ps < prefix_len):
+        raise ValueError("prefix_table must be a contiguous int32 tensor of prefix_len's pages on the cache's device")
+    with _on(dev):
+        out, lse = _outputs(q, out, lse)
+        if out.device != dev or lse.device != dev:
+            raise ValueError("out and lse must be on the cache's device")
+        own = workspace is None
+        if own:
+            need = paged_workspace_bytes(B, Nq, H, Hkv, d, prefix_len, max_pages, ps)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
+        rc = library().attn_fwd_paged(_ptr(q), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
+                                      _ptr(prefix_table) if prefix_len > 0 else None, prefix_len, _ptr(block_table),
+                                      stride, max_pages, _ptr(seq_lens), _ptr(out), _ptr(lse), B, Nq, H, Hkv, d, pages,
+                                      ps, dtype, int(bool(causal)), float(scale or 0.0), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                                      ctypes.c_void_p(_stream_on(stream, dev)))
+    _check("attn_fwd_paged", rc)
+    if own and workspace is not None and stream is not None:
+        _hold_until_done(workspace, stream)   # the launches run on `stream`, not torch's current one
+    return out, lse
 
 
 def device_status(stream=None):

@@ -17,6 +17,7 @@
 #include "attn_bwd_kernel.cuh"
 #include "attn_launch.cuh"
 #include "fp8_prep.cuh"
+#include "paged.cuh"
 
 #include <algorithm>
 #include <vector>
@@ -540,6 +541,12 @@ int attn_device_status(void* stream, int* site) {
         e = cudaMemcpy(ptr, &zero, sizeof zero, cudaMemcpyHostToDevice);
         if (e != cudaSuccess) return cuda_fail(e, "clearing the status word");
         if (site) *site = value;
+        if (value >= attn::SITE_BAD_INDEX)
+            return fail(ATTN_ERR_BAD_INDEX, "a kernel refused %s (site 0x%x)",
+                        value == attn::SITE_PAGED_SLOT   ? "a cache slot beyond the cache"
+                        : value == attn::SITE_PAGED_PAGE ? "a page index outside the cache"
+                                                         : "a sequence length beyond its page table",
+                        value);
         return fail(ATTN_ERR_DEVICE_TIMEOUT, "a kernel gave up waiting at site 0x%x", value);
     }
     return ATTN_OK;
@@ -908,6 +915,226 @@ int attn_bwd_host(const void* q, const void* k, const void* v, const void* o, co
                                              base + L.out_off[2], base + L.scratch_off, bwd_ws, nb, H, H_kv, N, d,
                                              causal, scale, window, s);
                          });
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The paged key/value cache (see include/attn.h).
+
+namespace {
+
+// Sizes and pointers of the cache that every entry shares.
+int check_cache(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, int H_kv, int d,
+                int num_pages, int page_size, int cache_dtype) {
+    if (d != 64 && d != 128 && d != 256) return fail(ATTN_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128, 256)", d);
+    if (cache_dtype != ATTN_CACHE_BF16 && cache_dtype != ATTN_CACHE_E4M3)
+        return fail(ATTN_ERR_INVALID_ARG, "cache_dtype %d (ATTN_CACHE_BF16 or ATTN_CACHE_E4M3)", cache_dtype);
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0)
+        return fail(ATTN_ERR_UNSUPPORTED, "page_size %d (supported: 16, 32, 64, 128, 256)", page_size);
+    if (H_kv <= 0) return fail(ATTN_ERR_INVALID_ARG, "key/value heads %d", H_kv);
+    if (num_pages < 0) return fail(ATTN_ERR_INVALID_ARG, "negative size (num_pages=%d)", num_pages);
+    if (num_pages > 0) {
+        if (!k_cache || !v_cache) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+        if (cache_dtype == ATTN_CACHE_E4M3 && (!k_scale || !v_scale))
+            return fail(ATTN_ERR_INVALID_ARG, "null scale pointer (an e4m3 cache has a scale per row)");
+    }
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
+        return fail(ATTN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    return ATTN_OK;
+}
+
+int log2_of(int page_size) {
+    int s = 0;
+    while ((1 << s) < page_size) ++s;
+    return s;
+}
+
+// A sequence's keys are counted in int with headroom for rounding up.
+constexpr long long kMaxKeys = 1ll << 30;
+
+int check_table(const int* table, long long table_stride, int max_pages, int page_size, const int* seq_lens) {
+    if (max_pages < 0) return fail(ATTN_ERR_INVALID_ARG, "negative size (max_pages=%d)", max_pages);
+    if (!seq_lens || (max_pages > 0 && !table)) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+    if (table_stride < max_pages)
+        return fail(ATTN_ERR_INVALID_ARG, "table_stride %lld < max_pages %d", table_stride, max_pages);
+    if (static_cast<long long>(max_pages) * page_size > kMaxKeys)
+        return fail(ATTN_ERR_INVALID_ARG, "a page table of more than 2^30 tokens");
+    if ((reinterpret_cast<uintptr_t>(table) & 3u) != 0 || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "page tables and lengths must be 4-byte aligned");
+    return ATTN_OK;
+}
+
+int check_paged_sizes(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size) {
+    if (B < 0 || Nq < 0 || H < 0 || prefix_len < 0 || max_pages < 0)
+        return fail(ATTN_ERR_INVALID_ARG, "negative size (B=%d Nq=%d H=%d prefix_len=%d max_pages=%d)", B, Nq, H,
+                    prefix_len, max_pages);
+    if (H_kv <= 0 || H % H_kv != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "key/value heads (%d) must divide query heads (%d)", H_kv, H);
+    if (d != 64 && d != 128 && d != 256) return fail(ATTN_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128, 256)", d);
+    if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)) != 0)
+        return fail(ATTN_ERR_UNSUPPORTED, "page_size %d (supported: 16, 32, 64, 128, 256)", page_size);
+    if (prefix_len > kMaxKeys || static_cast<long long>(max_pages) * page_size > kMaxKeys)
+        return fail(ATTN_ERR_INVALID_ARG, "more than 2^30 tokens in a prefix or a page table");
+    // Row indices are ints with headroom for the last tile, B a grid dimension
+    // of at most 65535.  (Row tiles x heads x parts then stay below 2^31: there
+    // are several parts only where there are fewer than 1216 tiles.)
+    if (B > 65535 || static_cast<long long>(B) * Nq > (1ll << 30) || static_cast<long long>(B) * Nq * H > (1ll << 30))
+        return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
+    return ATTN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_kv_write(const void* k, const void* v, long long k_stride, long long v_stride, const long long* slots,
+                  void* k_cache, void* v_cache, float* k_scale, float* v_scale, int T, int H_kv, int d, int num_pages,
+                  int page_size, int cache_dtype, void* stream) {
+    g_err[0] = '\0';
+    if (T < 0) return fail(ATTN_ERR_INVALID_ARG, "negative size (T=%d)", T);
+    int rc = check_cache(k_cache, v_cache, k_scale, v_scale, H_kv, d, num_pages, page_size, cache_dtype);
+    if (rc != ATTN_OK) return rc;
+    if (T == 0) return ATTN_OK;
+    if (!k || !v || !slots) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(k) || !aligned16(v)) return fail(ATTN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "slots must be 8-byte aligned");
+    if (k_stride % 8 != 0 || v_stride % 8 != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "token strides (%lld, %lld elements) must be multiples of 8", k_stride,
+                    v_stride);
+    if (static_cast<long long>(T) * H_kv * (d / 8) >= (1ll << 38))
+        return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
+    attn::KvWriteParams p{};
+    p.k = k;
+    p.v = v;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.slots = slots;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.T = T;
+    p.H_kv = H_kv;
+    p.d = d;
+    p.page_shift = log2_of(page_size);
+    p.num_slots = static_cast<long long>(num_pages) * page_size;
+    p.fp8 = cache_dtype == ATTN_CACHE_E4M3;
+    if ((rc = status_ptr(&p.status)) != ATTN_OK) return rc;
+    cudaError_t e = attn::run_kv_write(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "attn_kv_write launch");
+    return ATTN_OK;
+}
+
+int attn_kv_read(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                 const int* block_table, long long table_stride, int max_pages, const int* seq_lens, void* k, void* v,
+                 int B, int N, int H_kv, int d, int num_pages, int page_size, int cache_dtype, void* stream) {
+    g_err[0] = '\0';
+    if (B < 0 || N < 0) return fail(ATTN_ERR_INVALID_ARG, "negative size (B=%d N=%d)", B, N);
+    int rc = check_cache(k_cache, v_cache, k_scale, v_scale, H_kv, d, num_pages, page_size, cache_dtype);
+    if (rc != ATTN_OK) return rc;
+    if (B == 0 || N == 0) return ATTN_OK;
+    if ((rc = check_table(block_table, table_stride, max_pages, page_size, seq_lens)) != ATTN_OK) return rc;
+    if (!k || !v) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(k) || !aligned16(v)) return fail(ATTN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    if (B > 65535 || static_cast<long long>(N) * H_kv * (d / 8) >= (1ll << 38))
+        return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
+    attn::KvReadParams p{};
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.seq_lens = seq_lens;
+    p.k = k;
+    p.v = v;
+    p.B = B;
+    p.N = N;
+    p.H_kv = H_kv;
+    p.d = d;
+    p.num_pages = num_pages;
+    p.page_shift = log2_of(page_size);
+    p.max_pages = max_pages;
+    p.fp8 = cache_dtype == ATTN_CACHE_E4M3;
+    if ((rc = status_ptr(&p.status)) != ATTN_OK) return rc;
+    cudaError_t e = attn::run_kv_read(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "attn_kv_read launch");
+    return ATTN_OK;
+}
+
+size_t attn_fwd_paged_workspace_size(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages,
+                                     int page_size) {
+    if (check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size) != ATTN_OK) return 0;
+    if (static_cast<long long>(B) * Nq * H == 0) return 0;
+    return attn::paged_plan(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size).bytes;
+}
+
+int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                   const int* prefix_table, int prefix_len, const int* block_table, long long table_stride,
+                   int max_pages, const int* seq_lens, void* o, float* lse, int B, int Nq, int H, int H_kv, int d,
+                   int num_pages, int page_size, int cache_dtype, int causal, float scale, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+    g_err[0] = '\0';
+    int rc = check_cache(k_cache, v_cache, k_scale, v_scale, H_kv, d, num_pages, page_size, cache_dtype);
+    if (rc != ATTN_OK) return rc;
+    if ((rc = check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size)) != ATTN_OK) return rc;
+    if (static_cast<long long>(B) * Nq * H == 0) return ATTN_OK;
+    if ((rc = check_table(block_table, table_stride, max_pages, page_size, seq_lens)) != ATTN_OK) return rc;
+    if (!q || !o || !lse || (prefix_len > 0 && !prefix_table)) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(q) || !aligned16(o) || !aligned16(lse))
+        return fail(ATTN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(prefix_table) & 3u) != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "page tables and lengths must be 4-byte aligned");
+    const attn::PagedPlan plan = attn::paged_plan(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size);
+    if (plan.bytes > 0) {
+        if (!workspace) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+        if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+            return fail(ATTN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+        if (workspace_bytes < plan.bytes)
+            return fail(ATTN_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu bytes needed",
+                        workspace_bytes, plan.bytes);
+    }
+    attn::PagedParams p{};
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.prefix_table = prefix_table;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.seq_lens = seq_lens;
+    p.o = o;
+    p.lse = lse;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_o_bytes);
+    p.B = B;
+    p.Nq = Nq;
+    p.H = H;
+    p.H_kv = H_kv;
+    p.G = H / H_kv;
+    p.d = d;
+    p.num_pages = num_pages;
+    p.page_shift = log2_of(page_size);
+    p.max_pages = max_pages;
+    p.prefix_len = prefix_len;
+    p.causal = causal ? 1 : 0;
+    p.prefix_parts = plan.prefix_parts;
+    p.own_parts = plan.own_parts;
+    p.scale_log2 = resolve_scale(scale, d) * 1.4426950408889634f;
+    p.fp8 = cache_dtype == ATTN_CACHE_E4M3;
+    p.wait_limit = g_wait_limit.load();
+    if ((rc = status_ptr(&p.status)) != ATTN_OK) return rc;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const auto run = d == 64 ? attn::run_paged_stream_d64 : d == 128 ? attn::run_paged_stream_d128 : attn::run_paged_stream_d256;
+    cudaError_t e = cudaSuccess;
+    if (prefix_len > 0) e = run(p, true, false, s);
+    if (e == cudaSuccess) e = run(p, false, plan.direct, s);
+    if (e == cudaSuccess && !plan.direct) e = attn::run_paged_merge(p, s);
+    if (e != cudaSuccess) return cuda_fail(e, "attn_fwd_paged launch");
+    return ATTN_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,115 @@
+// The paged key/value cache: launch parameters shared by the C ABI and the
+// kernels (write, read back, and the attention over a shared prefix and each
+// sequence's own pages).
+//
+// Cache layout: K and V are (num_pages, H_kv, page_size, d), d fastest, bf16 or
+// e4m3; an e4m3 cache has one float32 scale per row, (num_pages, H_kv,
+// page_size).  A head's rows of a page are contiguous, so a CTA that serves one
+// key/value head streams whole lines, and the scales of 16 keys share two
+// sectors.  Cache row of (page, head, row) = (page * H_kv + head) * page_size +
+// row: the index of its scale, and of its d elements.  Row indices and byte
+// offsets are 64-bit.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+namespace attn {
+
+// Device status codes of indices that a kernel refused (nothing is read or
+// written through them); codes below SITE_BAD_INDEX are waits that ran out.
+enum : int {
+    SITE_BAD_INDEX = 0x100,
+    SITE_PAGED_SLOT = 0x101,     // attn_kv_write: slot beyond the cache
+    SITE_PAGED_PAGE = 0x102,     // a page index outside [0, num_pages)
+    SITE_PAGED_LENGTH = 0x103,   // a sequence length beyond its table
+};
+
+struct KvWriteParams {
+    const void* k;               // bf16 rows: token t, head h at k + t * k_stride + h * d
+    const void* v;
+    long long k_stride, v_stride;
+    const long long* slots;      // (T,)
+    void* k_cache;
+    void* v_cache;
+    float* k_scale;
+    float* v_scale;
+    int T, H_kv, d, page_shift;
+    long long num_slots;         // num_pages * page_size
+    bool fp8;
+    int* status;
+};
+
+struct KvReadParams {
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    const int* table;            // (B, max_pages), row stride table_stride
+    long long table_stride;
+    const int* seq_lens;         // (B,)
+    void* k;                     // bf16 (B, N, H_kv, d)
+    void* v;
+    int B, N, H_kv, d, num_pages, page_shift, max_pages;
+    bool fp8;
+    int* status;
+};
+
+// The attention.  A query row is (sequence b, query token i, head h); the rows
+// of one key/value head's group share its keys.  Row index in q, o and the
+// partial results: (b * Nq + i) * H + h.
+struct PagedParams {
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const float* k_scale;
+    const float* v_scale;
+    const int* prefix_table;
+    const int* table;
+    long long table_stride;
+    const int* seq_lens;
+    void* o;                     // bf16 (B, Nq, H, d)
+    float* lse;                  // float32 (B, H, Nq)
+    float* part_o;               // float32 (parts, B * Nq * H, d): normalised per part
+    float* part_lse;             // float32 (parts, B * Nq * H): log2 units, -inf where the part is empty
+    int B, Nq, H, H_kv, G, d;
+    int num_pages, page_shift, max_pages;
+    int prefix_len;
+    int causal;
+    int prefix_parts, own_parts; // parts [0, prefix_parts) are the prefix's
+    float scale_log2;
+    bool fp8;
+    unsigned long long wait_limit;
+    int* status;
+};
+
+// How a call is cut up (host arithmetic only).
+struct PagedPlan {
+    int prefix_parts = 0;        // key ranges of the prefix, each a partial result
+    int own_parts = 1;           // key ranges of a sequence's own tokens
+    bool direct = false;         // one part in all: the kernel writes o and lse itself
+    size_t part_o_bytes = 0, bytes = 0;
+};
+
+// GB300 has 152 streaming multiprocessors; plans are made for that number on
+// every device, so that a workspace size does not depend on the current one.
+constexpr int kPlanSms = 152;
+
+// A sequence's own tokens are cut into ranges of at least this many keys: a
+// range's partial result (16 rows x d floats, written and read again) then
+// stays small beside the keys and values that it stands for.
+constexpr int kOwnChunk = 256;
+
+PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size);
+
+cudaError_t run_kv_write(const KvWriteParams& p, cudaStream_t stream);
+cudaError_t run_kv_read(const KvReadParams& p, cudaStream_t stream);
+// The streaming kernel over the prefix (prefix) or the own tokens, one
+// translation unit per head dim; direct: it writes o and lse itself.
+cudaError_t run_paged_stream_d64(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream);
+cudaError_t run_paged_stream_d128(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream);
+cudaError_t run_paged_stream_d256(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream);
+cudaError_t run_paged_merge(const PagedParams& p, cudaStream_t stream);
+
+}  // namespace attn

@@ -52,7 +52,8 @@ typedef enum {
     ATTN_ERR_INVALID_ARG = -1,    /* bad pointer, size, alignment or mode      */
     ATTN_ERR_UNSUPPORTED = -2,    /* head_dim / device not supported           */
     ATTN_ERR_CUDA = -3,           /* a CUDA runtime / driver call failed       */
-    ATTN_ERR_DEVICE_TIMEOUT = -4  /* a kernel gave up waiting (see below)      */
+    ATTN_ERR_DEVICE_TIMEOUT = -4, /* a kernel gave up waiting (see below)      */
+    ATTN_ERR_BAD_INDEX = -5       /* a kernel refused a page, slot or length   */
 } attn_status;
 
 /*
@@ -337,11 +338,122 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
                      int N, int d, int causal, float scale, int window, void* stream);
 
 /*
+ * The paged key/value cache: attn_kv_write, attn_kv_read, attn_fwd_paged (no
+ * counterpart in the pages; what a decoding loop needs next to attn_fwd).
+ *
+ *   k_cache, v_cache : (num_pages, H_kv, page_size, d), contiguous, device;
+ *                      bf16 (ATTN_CACHE_BF16) or e4m3 (ATTN_CACHE_E4M3)
+ *   k_scale, v_scale : e4m3 cache: float32 (num_pages, H_kv, page_size), the
+ *                      scale of each row (one token, one head); a row's real
+ *                      values are scale * e4m3 value.  Ignored (may be NULL) for
+ *                      bf16.
+ *   page_size        : 16, 32, 64, 128 or 256 tokens;  d: 64, 128 or 256
+ *   slot of a token  : page * page_size + its row in the page
+ *   block table      : row b lists the pages of sequence b in order; token n
+ *                      is row n % page_size of page [n / page_size].  Entries
+ *                      past the sequence's last token are never read.
+ *
+ * Slots, page indices and lengths are device data that no host check can
+ * see.  A kernel reads and writes nothing through an index outside the cache
+ * or beyond its table; it goes on without it (below) and records a site that
+ * attn_device_status returns as ATTN_ERR_BAD_INDEX.
+ */
+enum { ATTN_CACHE_BF16 = 0, ATTN_CACHE_E4M3 = 1 };
+
+/*
+ * attn_kv_write -- T new tokens' keys and values into their slots, quantised
+ * on the way for an e4m3 cache.
+ *   k, v     : const bf16 rows: token t, head h at k + t * k_stride + h * d
+ *              (strides in elements, multiples of 8: k and v may be columns of
+ *              one projection)
+ *   slots    : const int64 (T,), device; a negative slot skips its token
+ *              (padding), one >= num_pages * page_size is refused: skipped and
+ *              recorded.  The slots >= 0 of one call must differ: of two tokens
+ *              with the same slot it is not said whose elements and scales are
+ *              kept.
+ * e4m3: scale = amax / 448 of the row's d elements (1 for a row of zeros), each
+ * element x / scale rounded to nearest even and saturated at +-448; amax, the
+ * scale and the division are float32.  A row with an infinity or a NaN gets a
+ * NaN scale: all of it reads back as NaN.  Rows of other slots are not touched.
+ */
+int attn_kv_write(const void* k, const void* v, long long k_stride, long long v_stride,
+                  const long long* slots, void* k_cache, void* v_cache, float* k_scale,
+                  float* v_scale, int T, int H_kv, int d, int num_pages, int page_size,
+                  int cache_dtype, void* stream);
+
+/*
+ * attn_kv_read -- the first min(seq_lens[b], N) tokens of every sequence back
+ * as contiguous bf16 (for attn_fwd and the other dense entries); an e4m3
+ * element is scale * value in float32, rounded once.
+ *   block_table : const int32, device; row b at block_table + b * table_stride
+ *                 (max_pages entries, table_stride >= max_pages)
+ *   seq_lens    : const int32 (B,), device; <= 0 is an empty sequence.  A length
+ *                 beyond max_pages * page_size is recorded and cut to it.
+ *   k, v        : bf16 (B, N, H_kv, d).  Rows from the sequence's length on,
+ *                 and rows whose page index is outside the cache (recorded),
+ *                 are left as they were.
+ */
+int attn_kv_read(const void* k_cache, const void* v_cache, const float* k_scale,
+                 const float* v_scale, const int* block_table, long long table_stride,
+                 int max_pages, const int* seq_lens, void* k, void* v, int B, int N, int H_kv,
+                 int d, int num_pages, int page_size, int cache_dtype, void* stream);
+
+/*
+ * attn_fwd_paged_workspace_size / attn_fwd_paged -- attention of Nq query
+ * tokens of each of B sequences over the paged cache.  The keys of sequence b
+ * are the prefix, which every sequence shares and which is read and multiplied
+ * once for the whole batch, followed by the sequence's own tokens:
+ *     O   = softmax(scale * q K^T) V,   LSE = log(sum_j exp(scale * q . k_j))
+ * per query row over its visible keys.  The queries are the last Nq of the own
+ * tokens (already written to the cache): Nq = 1 is a decoding step, a few are
+ * drafts to verify, many are a chunk of a prompt.
+ *   q             : const bf16 (B, Nq, H, d), contiguous
+ *   prefix_table  : const int32 (ceil(prefix_len / page_size),), device: the
+ *                   prefix's pages; NULL when prefix_len is 0
+ *   prefix_len    : tokens of the prefix (0: nothing is shared)
+ *   block_table, table_stride, max_pages, seq_lens : each sequence's own
+ *                   pages and token count (attn_kv_read's conventions; the
+ *                   prefix is not counted)
+ *   causal        : nonzero: query i of sequence b sees the own keys
+ *                   j <= seq_lens[b] - Nq + i; 0: all own keys.  The prefix is
+ *                   visible to every query.
+ *   o             : bf16 (B, Nq, H, d), written
+ *   lse           : float32 (B, H, Nq), written (natural log)
+ *   workspace     : device, at least attn_fwd_paged_workspace_size(...) bytes
+ *                   (0 is possible: NULL is then accepted), 256-byte aligned,
+ *                   owned by the caller: scratch that every call overwrites, so
+ *                   calls (and captured graphs) that share one must be ordered
+ * H_kv must divide H (query head h reads key/value head h / (H / H_kv)).
+ * scale <= 0 or non-finite selects 1 / sqrt(d).  A row with no visible key gets
+ * O = 0 and LSE = -inf.  A page index outside the cache hides its tokens
+ * (recorded); a length is cut as in attn_kv_read.  Cache rows that are not
+ * visible to a query row (past the length, or behind the causal limit) do not
+ * reach it whatever they hold, NaN included.  A bf16 V row with an infinity or a
+ * NaN that lies among the last Nq own tokens makes the whole O row and the LSE
+ * of every query that sees it NaN.
+ * The workspace size depends on its arguments alone.  prefix_len, max_pages
+ * and the launches are the host's: a captured graph replays them with new
+ * table entries, lengths, queries and cache contents.  Errors: before any
+ * launch, as attn_fwd_gqa; page_size or d not listed above is
+ * ATTN_ERR_UNSUPPORTED, a prefix or a table of more than 2^30 tokens or a
+ * too small workspace ATTN_ERR_INVALID_ARG.
+ */
+size_t attn_fwd_paged_workspace_size(int B, int Nq, int H, int H_kv, int d, int prefix_len,
+                                     int max_pages, int page_size);
+int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                   const float* v_scale, const int* prefix_table, int prefix_len,
+                   const int* block_table, long long table_stride, int max_pages,
+                   const int* seq_lens, void* o, float* lse, int B, int Nq, int H, int H_kv, int d,
+                   int num_pages, int page_size, int cache_dtype, int causal, float scale,
+                   void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * attn_device_status -- waits for `stream`, then reads and clears the
  * library's device status word.  Every wait inside the kernels is bounded;
  * a kernel that gives up records the site in this word and returns instead
- * of hanging.  Returns ATTN_OK, ATTN_ERR_DEVICE_TIMEOUT (*site, if not NULL,
- * receives the site code) or ATTN_ERR_CUDA.
+ * of hanging.  Returns ATTN_OK, ATTN_ERR_DEVICE_TIMEOUT or, where a kernel
+ * refused an index, ATTN_ERR_BAD_INDEX (*site, if not NULL, receives the site
+ * code), or ATTN_ERR_CUDA.
  */
 int attn_device_status(void* stream, int* site);
 
