@@ -1123,15 +1123,21 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
     p.causal = causal ? 1 : 0;
     p.prefix_parts = plan.prefix_parts;
     p.own_parts = plan.own_parts;
+    p.prefix_items = plan.prefix_items;
+    p.prefix_ctas = plan.prefix_ctas;
+    p.own_items = plan.own_items;
+    p.own_ctas = plan.own_ctas;
     p.scale_log2 = resolve_scale(scale, d) * 1.4426950408889634f;
     p.fp8 = cache_dtype == ATTN_CACHE_E4M3;
     p.wait_limit = g_wait_limit.load();
     if ((rc = status_ptr(&p.status)) != ATTN_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const auto run = d == 64 ? attn::run_paged_stream_d64 : d == 128 ? attn::run_paged_stream_d128 : attn::run_paged_stream_d256;
+    const auto rows = d == 64 ? attn::run_paged_stream_d64 : d == 128 ? attn::run_paged_stream_d128 : attn::run_paged_stream_d256;
+    const auto tiles = d == 64 ? attn::run_paged_tile_d64 : d == 128 ? attn::run_paged_tile_d128 : attn::run_paged_tile_d256;
     cudaError_t e = cudaSuccess;
-    if (prefix_len > 0) e = run(p, true, false, s);
-    if (e == cudaSuccess) e = run(p, false, plan.direct, s);
+    if (plan.prefix_items + plan.own_items > 0) e = tiles(p, plan.direct, s);
+    if (e == cudaSuccess && plan.prefix_stream) e = rows(p, true, false, s);
+    if (e == cudaSuccess && plan.own_items == 0) e = rows(p, false, plan.direct, s);
     if (e == cudaSuccess && !plan.direct) e = attn::run_paged_merge(p, s);
     if (e != cudaSuccess) return cuda_fail(e, "attn_fwd_paged launch");
     return ATTN_OK;

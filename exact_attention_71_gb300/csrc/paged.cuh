@@ -78,6 +78,8 @@ struct PagedParams {
     int prefix_len;
     int causal;
     int prefix_parts, own_parts; // parts [0, prefix_parts) are the prefix's
+    int prefix_items, prefix_ctas;   // tile kernel: work items of the prefix; CTAs that share a row tile's keys
+    int own_items, own_ctas;         // the same for the own tokens (0: the streaming kernel has them)
     float scale_log2;
     bool fp8;
     unsigned long long wait_limit;
@@ -88,6 +90,9 @@ struct PagedParams {
 struct PagedPlan {
     int prefix_parts = 0;        // key ranges of the prefix, each a partial result
     int own_parts = 1;           // key ranges of a sequence's own tokens
+    int prefix_items = 0, prefix_ctas = 0;   // tile kernel (see PagedParams)
+    int own_items = 0, own_ctas = 0;
+    bool prefix_stream = false;  // the streaming kernel has the prefix
     bool direct = false;         // one part in all: the kernel writes o and lse itself
     size_t part_o_bytes = 0, bytes = 0;
 };
@@ -101,6 +106,11 @@ constexpr int kPlanSms = 152;
 // stays small beside the keys and values that it stands for.
 constexpr int kOwnChunk = 256;
 
+// Query rows of one key/value head (of one sequence; over the prefix, of all)
+// up to which the streaming kernel takes them.
+constexpr int kStreamRows = 32;
+constexpr int kStreamPrefixRows = 16;
+
 PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size);
 
 cudaError_t run_kv_write(const KvWriteParams& p, cudaStream_t stream);
@@ -110,6 +120,10 @@ cudaError_t run_kv_read(const KvReadParams& p, cudaStream_t stream);
 cudaError_t run_paged_stream_d64(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream);
 cudaError_t run_paged_stream_d128(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream);
 cudaError_t run_paged_stream_d256(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream);
+// The tile kernel over its prefix_items and own_items.
+cudaError_t run_paged_tile_d64(const PagedParams& p, bool direct, cudaStream_t stream);
+cudaError_t run_paged_tile_d128(const PagedParams& p, bool direct, cudaStream_t stream);
+cudaError_t run_paged_tile_d256(const PagedParams& p, bool direct, cudaStream_t stream);
 cudaError_t run_paged_merge(const PagedParams& p, cudaStream_t stream);
 
 }  // namespace attn

@@ -14,18 +14,59 @@
 
 namespace attn {
 
+namespace {
+
+long long up(long long a, long long b) { return (a + b - 1) / b; }
+
+// CTAs that share a row tile's keys (tile kernel, one CTA an SM): as few waves
+// x key tiles per CTA as possible, a CTA's fixed cost (query load, pipeline
+// fill, epilogue) counted as three key tiles.
+int tile_ctas(long long units, long long tiles) {
+    int best = 1;
+    long long best_cost = -1;
+    for (int s = 1; s <= 64 && s <= tiles; ++s) {
+        const long long cost = up(units * s, kPlanSms) * (up(tiles, s) + 3);
+        if (best_cost < 0 || cost < best_cost) {
+            best = s;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
 PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size) {
     PagedPlan plan;
-    const long long rows = static_cast<long long>(Nq) * (H / H_kv);
-    const auto up = [](long long a, long long b) { return (a + b - 1) / b; };
+    const long long rows = static_cast<long long>(Nq) * (H / H_kv);      // of one sequence and key/value head
+    const long long own = static_cast<long long>(max_pages) * page_size;
+    const int bn = d == 256 ? 64 : 128;
     // About four waves of two CTAs an SM, in ranges of kOwnChunk keys or more.
     const long long target = 8LL * kPlanSms;
-    const long long own = static_cast<long long>(max_pages) * page_size;
-    const long long own_units = B * static_cast<long long>(H_kv) * up(rows, 16);
-    plan.own_parts = static_cast<int>(std::max(1LL, std::min({up(own, kOwnChunk), up(target, own_units), 128LL})));
+    const auto stream_parts = [&](long long keys, long long units) {
+        return static_cast<int>(std::max(1LL, std::min({up(keys, kOwnChunk), up(target, units), 128LL})));
+    };
+    if (rows > kStreamRows) {
+        const long long tiles = up(rows, 128), groups = d == 256 ? tiles : up(tiles, 2);
+        const bool alt = d != 256 && tiles == 1;
+        plan.own_ctas = tile_ctas(B * static_cast<long long>(H_kv) * groups, up(own, bn));
+        plan.own_items = static_cast<int>(B * static_cast<long long>(H_kv) * groups * plan.own_ctas);
+        plan.own_parts = plan.own_ctas * (alt ? 2 : 1);
+    } else {
+        plan.own_parts = stream_parts(own, B * static_cast<long long>(H_kv) * up(rows, 16));
+    }
     if (prefix_len > 0) {
-        const long long units = static_cast<long long>(H_kv) * up(B * rows, 16);
-        plan.prefix_parts = static_cast<int>(std::max(1LL, std::min({up(prefix_len, kOwnChunk), up(target, units), 128LL})));
+        const long long all = B * rows;
+        if (all > kStreamPrefixRows) {
+            const long long tiles = up(all, 128), groups = d == 256 ? tiles : up(tiles, 2);
+            const bool alt = d != 256 && tiles == 1;
+            plan.prefix_ctas = tile_ctas(H_kv * groups, up(prefix_len, bn));
+            plan.prefix_items = static_cast<int>(H_kv * groups * plan.prefix_ctas);
+            plan.prefix_parts = plan.prefix_ctas * (alt ? 2 : 1);
+        } else {
+            plan.prefix_stream = true;
+            plan.prefix_parts = stream_parts(prefix_len, H_kv * up(all, 16));
+        }
     }
     const int parts = plan.prefix_parts + plan.own_parts;
     plan.direct = parts == 1;

@@ -99,13 +99,15 @@ struct StreamCfg {
 };
 
 // Replaces the infinities and NaN among this thread's V chunks (value rows 2t,
-// 2t+1, 2t+8, 2t+9 of the step) by 0; bit r of the result: the step's row r had
+// 2t+1, 2t+8, 2t+9 of the step, those from `from` on) by 0; bit r of the result: the step's row r had
 // one.  Called by whole warps.
 template <class Cfg>
-__device__ __noinline__ uint32_t clear_nonfinite(uint8_t* sv, int t) {
+__device__ __noinline__ uint32_t clear_nonfinite(uint8_t* sv, int t, int from) {
     uint32_t hit = 0;
     for (int x = 0; x < 4; ++x) {
+        const int row = 2 * t + (x & 1) + (x >> 1) * 8;
         bool any = false;
+        if (row < from) continue;
         for (int c = 0; c < Cfg::VC; ++c) {
             uint32_t* at = reinterpret_cast<uint32_t*>(sv + (x * Cfg::VC + c) * Cfg::VB * Cfg::THREADS);
             for (int y = 0; y < Cfg::VB / 4; ++y) {
@@ -115,7 +117,7 @@ __device__ __noinline__ uint32_t clear_nonfinite(uint8_t* sv, int t) {
                 at[y] = w;
             }
         }
-        if (any) hit |= 1u << (2 * t + (x & 1) + (x >> 1) * 8);
+        if (any) hit |= 1u << row;
     }
     return __reduce_or_sync(0xffffffffu, hit);
 }
@@ -363,8 +365,8 @@ __global__ void __launch_bounds__(Cfg::THREADS) paged_stream_kernel(const PagedP
             // 0 * NaN is NaN: where rows of the tile see different keys, a
             // non-finite value is taken out of the product and the rows that
             // do see its key become NaN as a whole.
-            if (step * 16 + 16 > diag) {
-                const uint32_t hit = clear_nonfinite<Cfg>(const_cast<uint8_t*>(sv), t);
+            if (diag < len && step * 16 + 16 > diag) {
+                const uint32_t hit = clear_nonfinite<Cfg>(const_cast<uint8_t*>(sv), t, diag - step * 16);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int n = min(max(min(limit[r], k1) - step * 16, 0), 16);

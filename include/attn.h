@@ -429,8 +429,9 @@ int attn_kv_read(const void* k_cache, const void* v_cache, const float* k_scale,
  * (recorded); a length is cut as in attn_kv_read.  Cache rows that are not
  * visible to a query row (past the length, or behind the causal limit) do not
  * reach it whatever they hold, NaN included.  A bf16 V row with an infinity or a
- * NaN that lies among the last Nq own tokens makes the whole O row and the LSE
- * of every query that sees it NaN.
+ * NaN among the own tokens that not every query sees (the last Nq - 1 under
+ * the causal mask) makes the whole O row and the LSE of the queries that do see
+ * it NaN.
  * The workspace size depends on its arguments alone.  prefix_len, max_pages
  * and the launches are the host's: a captured graph replays them with new
  * table entries, lengths, queries and cache contents.  Errors: before any
