@@ -944,6 +944,24 @@ int check_cache(const void* k_cache, const void* v_cache, const float* k_scale, 
     return ATTN_OK;
 }
 
+// A bf16 cache tensor as {d, page_size, H_kv, num_pages}, a box of 64 columns x
+// `rows` rows of one head of one page.
+int make_cache_map(CUtensorMap* map, const void* base, int num_pages, int H_kv, int page_size, int d, int rows) {
+    auto enc = encode_fn();
+    if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t head = static_cast<cuuint64_t>(page_size) * d * 2;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size),
+                          static_cast<cuuint64_t>(H_kv), static_cast<cuuint64_t>(num_pages)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, head, head * static_cast<cuuint64_t>(H_kv)};
+    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
+    cuuint32_t estride[4] = {1, 1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estride,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled (cache) failed (CUresult %d)", static_cast<int>(r));
+    return ATTN_OK;
+}
+
 int log2_of(int page_size) {
     int s = 0;
     while ((1 << s) < page_size) ++s;
@@ -1003,7 +1021,7 @@ int attn_kv_write(const void* k, const void* v, long long k_stride, long long v_
     if (k_stride % 8 != 0 || v_stride % 8 != 0)
         return fail(ATTN_ERR_INVALID_ARG, "token strides (%lld, %lld elements) must be multiples of 8", k_stride,
                     v_stride);
-    if (static_cast<long long>(T) * H_kv * (d / 8) >= (1ll << 38))
+    if (static_cast<long long>(T) * H_kv > (1ll << 30))
         return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
     attn::KvWriteParams p{};
     p.k = k;
@@ -1038,7 +1056,7 @@ int attn_kv_read(const void* k_cache, const void* v_cache, const float* k_scale,
     if ((rc = check_table(block_table, table_stride, max_pages, page_size, seq_lens)) != ATTN_OK) return rc;
     if (!k || !v) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
     if (!aligned16(k) || !aligned16(v)) return fail(ATTN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
-    if (B > 65535 || static_cast<long long>(N) * H_kv * (d / 8) >= (1ll << 38))
+    if (B > 65535 || static_cast<long long>(N) * H_kv > (1ll << 30))
         return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
     attn::KvReadParams p{};
     p.k_cache = k_cache;
@@ -1135,7 +1153,16 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
     const auto rows = d == 64 ? attn::run_paged_stream_d64 : d == 128 ? attn::run_paged_stream_d128 : attn::run_paged_stream_d256;
     const auto tiles = d == 64 ? attn::run_paged_tile_d64 : d == 128 ? attn::run_paged_tile_d128 : attn::run_paged_tile_d256;
     cudaError_t e = cudaSuccess;
-    if (plan.prefix_items + plan.own_items > 0) e = tiles(p, plan.direct, s);
+    if (plan.prefix_items + plan.own_items > 0) {
+        attn::PagedMaps maps{};
+        // (an empty cache: every page is refused, no copy is made)
+        if (!p.fp8 && num_pages > 0) {
+            const int bn = d == 256 ? 64 : 128, rows_per_box = page_size < bn ? page_size : bn;
+            if ((rc = make_cache_map(&maps.k, k_cache, num_pages, H_kv, page_size, d, rows_per_box)) != ATTN_OK) return rc;
+            if ((rc = make_cache_map(&maps.v, v_cache, num_pages, H_kv, page_size, d, rows_per_box)) != ATTN_OK) return rc;
+        }
+        e = tiles(maps, p, plan.direct, s);
+    }
     if (e == cudaSuccess && plan.prefix_stream) e = rows(p, true, false, s);
     if (e == cudaSuccess && plan.own_items == 0) e = rows(p, false, plan.direct, s);
     if (e == cudaSuccess && !plan.direct) e = attn::run_paged_merge(p, s);

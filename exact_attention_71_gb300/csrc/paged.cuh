@@ -11,6 +11,7 @@
 // offsets are 64-bit.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
@@ -104,7 +105,7 @@ constexpr int kPlanSms = 152;
 // A sequence's own tokens are cut into ranges of at least this many keys: a
 // range's partial result (16 rows x d floats, written and read again) then
 // stays small beside the keys and values that it stands for.
-constexpr int kOwnChunk = 256;
+constexpr int kOwnChunk = 128;
 
 // Query rows of one key/value head (of one sequence; over the prefix, of all)
 // up to which the streaming kernel takes them.
@@ -120,10 +121,16 @@ cudaError_t run_kv_read(const KvReadParams& p, cudaStream_t stream);
 cudaError_t run_paged_stream_d64(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream);
 cudaError_t run_paged_stream_d128(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream);
 cudaError_t run_paged_stream_d256(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream);
+// bf16 caches: K and V as 4-D {d, page_size, H_kv, num_pages} tensors with a box
+// of 64 columns x min(page_size, key tile) rows, 128-byte swizzle.
+struct PagedMaps {
+    CUtensorMap k, v;
+};
+
 // The tile kernel over its prefix_items and own_items.
-cudaError_t run_paged_tile_d64(const PagedParams& p, bool direct, cudaStream_t stream);
-cudaError_t run_paged_tile_d128(const PagedParams& p, bool direct, cudaStream_t stream);
-cudaError_t run_paged_tile_d256(const PagedParams& p, bool direct, cudaStream_t stream);
+cudaError_t run_paged_tile_d64(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream);
+cudaError_t run_paged_tile_d128(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream);
+cudaError_t run_paged_tile_d256(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream);
 cudaError_t run_paged_merge(const PagedParams& p, cudaStream_t stream);
 
 }  // namespace attn

@@ -59,20 +59,17 @@ __device__ __forceinline__ uint2 quantise_row(const uint4& x, float& scale) {
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams p) {
     constexpr int LANES = D / 8;
-    const long long rows = static_cast<long long>(p.T) * p.H_kv;
-    const long long row = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / LANES;
+    // (32-bit indices: a 64-bit division would cost more than the row's work)
+    const unsigned row = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
     const int lane = threadIdx.x % LANES;
-    const bool in = row < rows;
-    const int t = in ? static_cast<int>(row / p.H_kv) : 0;
-    const int h = in ? static_cast<int>(row % p.H_kv) : 0;
+    const bool in = row < static_cast<unsigned>(p.T) * p.H_kv;
+    const unsigned t = in ? row / p.H_kv : 0, h = in ? row % p.H_kv : 0;
     uint4 k = make_uint4(0, 0, 0, 0), v = k;
     long long slot = -1;
     if (in) {
         slot = __ldg(p.slots + t);
-        k = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride +
-                                                 static_cast<long long>(h) * D) + lane);
-        v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride +
-                                                 static_cast<long long>(h) * D) + lane);
+        k = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.k) + t * p.k_stride + h * D) + lane);
+        v = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.v) + t * p.v_stride + h * D) + lane);
     }
     const bool store = slot >= 0 && slot < p.num_slots;
     if (slot >= p.num_slots) report(p.status, SITE_PAGED_SLOT);
@@ -121,24 +118,23 @@ template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p) {
     constexpr int LANES = D / 8;
     const int b = blockIdx.y;
-    const long long row = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) / LANES;
+    const unsigned row = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
     const int lane = threadIdx.x % LANES;
-    const long long n = row / p.H_kv;
-    const int h = static_cast<int>(row % p.H_kv);
+    const int n = static_cast<int>(row / p.H_kv), h = static_cast<int>(row % p.H_kv);
     int len = __ldg(p.seq_lens + b);
     const long long room = static_cast<long long>(p.max_pages) << p.page_shift;
     if (len > room) {
         report(p.status, SITE_PAGED_LENGTH);
         len = static_cast<int>(room);
     }
-    if (n >= p.N || n >= len) return;
+    if (n >= min(p.N, len)) return;
     const int page = __ldg(p.table + b * p.table_stride + (n >> p.page_shift));
     if (page < 0 || page >= p.num_pages) {
         report(p.status, SITE_PAGED_PAGE);
         return;
     }
     const long long at = ((static_cast<long long>(page) * p.H_kv + h) << p.page_shift) +
-                         (n & ((1ll << p.page_shift) - 1));
+                         (n & ((1 << p.page_shift) - 1));
     const long long to = ((static_cast<long long>(b) * p.N + n) * p.H_kv + h) * D;
     uint4 k, v;
     if constexpr (FP8) {

@@ -41,10 +41,20 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     const long long rows = static_cast<long long>(Nq) * (H / H_kv);      // of one sequence and key/value head
     const long long own = static_cast<long long>(max_pages) * page_size;
     const int bn = d == 256 ? 64 : 128;
-    // About four waves of two CTAs an SM, in ranges of kOwnChunk keys or more.
-    const long long target = 8LL * kPlanSms;
+    // Streaming kernel: as few waves x keys per CTA as possible, a CTA's fixed
+    // cost (page table, first loads, join) counted as 128 keys.
+    const long long slots = static_cast<long long>(kPlanSms) * (d == 64 ? 4 : d == 128 ? 3 : 2);
     const auto stream_parts = [&](long long keys, long long units) {
-        return static_cast<int>(std::max(1LL, std::min({up(keys, kOwnChunk), up(target, units), 128LL})));
+        int best = 1;
+        long long best_cost = -1;
+        for (int s = 1; s <= 64 && (s == 1 || s * static_cast<long long>(kOwnChunk) < keys + kOwnChunk); ++s) {
+            const long long cost = up(units * s, slots) * (up(keys, s) + 128);
+            if (best_cost < 0 || cost < best_cost) {
+                best = s;
+                best_cost = cost;
+            }
+        }
+        return best;
     };
     if (rows > kStreamRows) {
         const long long tiles = up(rows, 128), groups = d == 256 ? tiles : up(tiles, 2);
@@ -80,44 +90,85 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
 
 namespace {
 
-// One warp per row; D / 32 columns a lane.
-template <int D>
+// W warps per row, D / 32 columns a lane; a warp takes the parts w, w + W, ..,
+// four at a time (independent loads), and the warps' sums meet in shared
+// memory.  The weights are computed once per part, by the lanes.
+template <int D, int W>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
     constexpr int V = D / 32;
+    __shared__ float joined[4][D + 1];
     const long long rows = static_cast<long long>(p.B) * p.Nq * p.H;
-    const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= rows) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long row = static_cast<long long>(blockIdx.x) * (4 / W) + warp / W;
+    const int w = warp % W;
     const int parts = p.prefix_parts + p.own_parts;
-    float mm = -INFINITY;
-    for (int x = lane; x < parts; x += 32) mm = fmaxf(mm, p.part_lse[x * rows + row]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-    const float ref = mm == -INFINITY ? 0.0f : mm;
-    float sum = 0.0f, acc[V];
+    const bool in = row < rows;
+    float sum = 0.0f, ref = 0.0f, acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-    for (int x = 0; x < parts; ++x) {
-        const float l2 = p.part_lse[x * rows + row];
-        if (l2 == -INFINITY) continue;                 // an empty part: its O was not written
-        const float w = ex2_approx(l2 - ref);
-        sum += w;
-        const float* src = p.part_o + (x * rows + row) * D + lane * V;
-        if constexpr (V == 2) {
-            const float2 f = *reinterpret_cast<const float2*>(src);
-            acc[0] += w * f.x;
-            acc[1] += w * f.y;
-        } else {
+    if (in) {
+        float mm = -INFINITY;
+        for (int x = lane; x < parts; x += 32) mm = fmaxf(mm, p.part_lse[x * rows + row]);
 #pragma unroll
-            for (int v = 0; v < V; v += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(src + v);
-                acc[v] += w * f.x;
-                acc[v + 1] += w * f.y;
-                acc[v + 2] += w * f.z;
-                acc[v + 3] += w * f.w;
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+        ref = mm == -INFINITY ? 0.0f : mm;
+        for (int base = 0; base < parts; base += 32 * W) {
+            // lane x holds the weight of part base + x * W + w
+            const int mine = base + lane * W + w;
+            const float l2 = mine < parts ? p.part_lse[mine * rows + row] : -INFINITY;
+            const float wt = l2 == -INFINITY ? 0.0f : ex2_approx(l2 - ref);
+            sum += wt;
+            const int n = min(32, (parts - base - w + W - 1) / W);
+            for (int x = 0; x < n; x += 4) {
+                float f[4][V], g[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    g[y] = __shfl_sync(0xffffffffu, wt, (x + y) & 31);
+                    if (x + y >= n) g[y] = 0.0f;
+                    // an empty part's O was not written: it is not read
+                    const float* src = p.part_o + (static_cast<long long>(base + (x + y) * W + w) * rows + row) * D + lane * V;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) f[y][v] = 0.0f;
+                    if (g[y] != 0.0f) {
+                        if constexpr (V == 2) {
+                            const float2 q = *reinterpret_cast<const float2*>(src);
+                            f[y][0] = q.x;
+                            f[y][1] = q.y;
+                        } else {
+#pragma unroll
+                            for (int v = 0; v < V; v += 4) {
+                                const float4 q = *reinterpret_cast<const float4*>(src + v);
+                                f[y][v] = q.x;
+                                f[y][v + 1] = q.y;
+                                f[y][v + 2] = q.z;
+                                f[y][v + 3] = q.w;
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) acc[v] += g[y] * f[y][v];
             }
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) joined[warp][lane * V + v] = acc[v];
+        if (lane == 0) joined[warp][D] = sum;
+        __syncthreads();
+        if (w != 0) return;
+#pragma unroll
+        for (int x = 1; x < W; ++x) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] += joined[warp + x][lane * V + v];
+            sum += joined[warp + x][D];
+        }
+    }
+    if (!in) return;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + row * D + lane * V);
 #pragma unroll
@@ -131,15 +182,20 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
     }
 }
 
+template <int D>
+cudaError_t merge_d(const PagedParams& p, cudaStream_t stream) {
+    const long long rows = static_cast<long long>(p.B) * p.Nq * p.H;
+    // A warp sums 8 parts in two rounds of loads; with more, four warps share
+    // a row.
+    if (p.prefix_parts + p.own_parts > 8) paged_merge_kernel<D, 4><<<static_cast<unsigned>(rows), 128, 0, stream>>>(p);
+    else paged_merge_kernel<D, 1><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t run_paged_merge(const PagedParams& p, cudaStream_t stream) {
-    const long long rows = static_cast<long long>(p.B) * p.Nq * p.H;
-    const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
-    if (p.d == 64) paged_merge_kernel<64><<<grid, 128, 0, stream>>>(p);
-    else if (p.d == 128) paged_merge_kernel<128><<<grid, 128, 0, stream>>>(p);
-    else paged_merge_kernel<256><<<grid, 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    return p.d == 64 ? merge_d<64>(p, stream) : p.d == 128 ? merge_d<128>(p, stream) : merge_d<256>(p, stream);
 }
 
 }  // namespace attn

@@ -91,11 +91,13 @@ struct StreamCfg {
     static constexpr int V_BYTES = 4 * VC * VB * THREADS;
     static constexpr int S_BYTES = FP8 ? 4 * 8 * THREADS : 0;      // scales: K and V, two key pairs each
     static constexpr int STAGE_BYTES = K_BYTES + V_BYTES + S_BYTES;
-    static constexpr int STAGES = D == 256 ? (FP8 ? 3 : 3) : (FP8 ? 4 : 3);
+    static constexpr int CTAS = D == 64 ? 4 : D == 128 ? 3 : FP8 ? 2 : 1;     // per SM
+    static constexpr int STAGES = D == 64 ? (FP8 ? 4 : 3) : D == 128 ? (FP8 ? 3 : 2) : 3;
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
     static constexpr int JOIN_BYTES = WARPS * 16 * (D + 2) * 4;
     static constexpr int SMEM_BYTES = RING_BYTES > JOIN_BYTES ? RING_BYTES : JOIN_BYTES;
     static constexpr int NT = D / 8;                               // O's column tiles
+    static_assert(CTAS * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory");
 };
 
 // Replaces the infinities and NaN among this thread's V chunks (value rows 2t,
@@ -126,7 +128,7 @@ __device__ __noinline__ uint32_t clear_nonfinite(uint8_t* sv, int t, int from) {
 // one sequence's (blockIdx.y) over its own tokens.  DIRECT: this is the only
 // part, o and lse are written; otherwise a partial result.
 template <class Cfg, bool PREFIX, bool DIRECT>
-__global__ void __launch_bounds__(Cfg::THREADS) paged_stream_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS) paged_stream_kernel(const PagedParams p) {
     constexpr int D = Cfg::D, KC = Cfg::KC, VC = Cfg::VC, NT = Cfg::NT, STAGES = Cfg::STAGES;
     constexpr bool FP8 = Cfg::FP8;
     extern __shared__ __align__(16) uint8_t smem[];

@@ -3,8 +3,8 @@
 
 namespace attn {
 
-cudaError_t run_paged_tile_d128(const PagedParams& p, bool direct, cudaStream_t stream) {
-    return launch_paged_tile<128>(p, direct, stream);
+cudaError_t run_paged_tile_d128(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream) {
+    return launch_paged_tile<128>(m, p, direct, stream);
 }
 
 }  // namespace attn

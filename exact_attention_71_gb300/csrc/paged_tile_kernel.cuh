@@ -13,21 +13,26 @@
 // leaves a partial result of its own, so that one stream's softmax still runs
 // beside the other's products.  At d = 256 tensor memory holds one stream.
 //
-//   warps [0, 4 NS)       softmax (one thread per row)
-//   next warpgroup        loaders: gather K and V rows through the page table
-//                         into 128-byte-swizzled tiles (a ring of half stages,
-//                         K and V alternating); e4m3 rows pass through a queue
-//                         of raw 16-byte chunks that each thread fills with
-//                         cp.async, reads back and converts to bf16 (exact; the
-//                         row scales go to the scores and to P)
-//   next warp             issues tcgen05.mma: S = Q K^T, O += P V
+//   warps [0, 4 NS)       softmax (one thread per row); they also bring in Q
+//   e4m3: 4 warps         convert the raw codes of a K or V tile to bf16 (exact;
+//                         the row scales go to the scores and to P)
+//   load warp             walks the page table: a head's rows of a page are
+//                         contiguous, so a bf16 tile is BN / page_size TMA boxes
+//                         per 64 columns, written swizzled into a ring of half
+//                         stages (K and V alternating), and an e4m3 tile is
+//                         BN / page_size bulk copies into a ring of raw tiles
+//   MMA warps             one per stream, issue tcgen05.mma: S = Q K^T, O += P V
+//                         (one warp for both streams left the pipe idle between
+//                         steps: 3150 cycles a step of two 128 x 128 x 128 tiles)
 //
-// The rows of a tile past the range are zero-filled (stale cache contents never
-// reach a product) and their scores masked; so are the rows of a page outside
-// the cache.
+// The scores of rows past the range, and of a page outside the cache, are
+// masked; their V rows are zeroed before a product reads them (0 times stale NaN
+// would be NaN).
 #pragma once
 
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "paged.cuh"
 #include "paged_stream_kernel.cuh"
@@ -52,7 +57,6 @@ template <int D_, bool FP8_>
 struct TileCfg {
     static constexpr int D = D_;
     static constexpr bool FP8 = FP8_;
-    static constexpr int ES = FP8 ? 1 : 2;
     static constexpr int BM = 128;
     static constexpr int BN = D == 256 ? 64 : 128;
     static constexpr int NS = D == 256 ? 1 : 2;                    // streams
@@ -60,22 +64,25 @@ struct TileCfg {
     static constexpr int Q_BYTES = BM * D * 2;
     static constexpr int HALF_BYTES = BN * D * 2;                  // one K or V tile
     static constexpr int NH = D == 64 ? (FP8 ? 6 : 8) : (FP8 ? 3 : 5);
-    static constexpr int AHEAD = 2;                                // bf16: copies in flight per thread (half stages)
-    static constexpr int RAW_BYTES = FP8 ? BN * D : 0;
+    static constexpr int RAW_BYTES = FP8 ? BN * D : 0;             // the same tile as codes
     static constexpr int NR = FP8 ? (D == 64 ? 5 : 3) : 0;
     static constexpr int SLOTS = 8;                                // key tiles whose scales are held
     static constexpr int SC_BYTES = FP8 ? SLOTS * 2 * BN * 4 : 0;
     static constexpr int DIAG_TILES = 8;
-    static constexpr int LOAD_WARP = 4 * NS, MMA_WARP = 4 * NS + 4;
-    static constexpr int THREADS = NS * 128 + 256;
-    static constexpr int LAUNCH_REGS = (65536 / THREADS) / 8 * 8;
-    static constexpr int LOAD_REGS = 72, MMA_REGS = 40;
-    static constexpr int HIGH_RAW = (LAUNCH_REGS * THREADS - (LOAD_REGS + MMA_REGS) * 128) / (NS * 128) / 8 * 8;
+    static constexpr int CONV_WARP = 4 * NS;                       // e4m3: 4 converting warps
+    static constexpr int LOAD_WARP = 4 * NS + (FP8 ? 4 : 0), MMA_WARP = LOAD_WARP + 1;   // one MMA warp per stream
+    static constexpr int THREADS = NS * 128 + (FP8 ? 256 : 128);
+    static constexpr int LAUNCH_REGS = 65536 / THREADS > 255 ? 248 : (65536 / THREADS) / 8 * 8;
+    static constexpr int CONV_REGS = FP8 ? 80 : 0, LOW_REGS = FP8 ? 64 : 104;
+    static constexpr int HIGH_RAW = (LAUNCH_REGS * THREADS - (CONV_REGS + LOW_REGS) * 128) / (NS * 128) / 8 * 8;
     static constexpr int HIGH_REGS = HIGH_RAW > 248 ? 248 : HIGH_RAW;
     static constexpr int BAR_BYTES = 1024;
-    static constexpr int SMEM_BYTES = 1024 + NS * Q_BYTES + NH * HALF_BYTES + NR * RAW_BYTES + SC_BYTES + BAR_BYTES;
-    static_assert(HIGH_REGS * NS * 128 + (LOAD_REGS + MMA_REGS) * 128 <= LAUNCH_REGS * THREADS, "register split");
-    static_assert(AHEAD < NH && (!FP8 || NR >= 2), "ring depth");
+    // Output staging: 4 KB per softmax warp, over query tiles that no product
+    // reads any more (d = 64: its query tiles are too small for that).
+    static constexpr int EPI_BYTES = D == 64 ? NS * 16384 : 0;
+    static constexpr int SMEM_BYTES = 1024 + NS * Q_BYTES + NH * HALF_BYTES + NR * RAW_BYTES + SC_BYTES +
+                                      EPI_BYTES + BAR_BYTES;
+    static_assert(HIGH_REGS * NS * 128 + (CONV_REGS + LOW_REGS) * 128 <= LAUNCH_REGS * THREADS, "register split");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
     // A slot (validity bits, scales) is rewritten at least 15 ring entries after
     // its tile's K; the entry NH + NR before that has been released by then.  It
@@ -85,9 +92,10 @@ struct TileCfg {
 };
 
 struct TileBarriers {
-    uint64_t q_full, loaded, drain;
+    uint64_t q_full, loaded, drain[2], fix;
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t ring_full[8], ring_empty[8];
+    uint64_t raw_full[8], raw_empty[8];
     uint64_t sc_full[8];
     uint32_t valid[8][4];          // per slot: bit per key of the tile
     uint32_t poison[8][4];         // per diagonal tile: bit per key whose V row is not finite
@@ -114,6 +122,57 @@ __device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ bool tile_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                                const PagedParams& p, int site) {
     return __all_sync(0xffffffffu, tile_wait(bar, parity, abort_flag, p, site));
+}
+
+// Teardown wait for the CTA's own asynchronous work, which always completes: it
+// ignores the abort flag and lasts at least a second.
+__device__ __forceinline__ void tile_drain(uint64_t* bar, uint32_t parity, const PagedParams& p, int site) {
+    const unsigned long long lim = p.wait_limit > 2000000000ull ? p.wait_limit : 2000000000ull;
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity)) {
+        if (static_cast<unsigned long long>(clock64() - t0) > lim) {
+            atomicCAS(p.status, 0, site);
+            return;
+        }
+    }
+}
+
+// Byte offset of 16-byte chunk c of row r in a swizzled K / V tile.
+template <class Cfg>
+__device__ __forceinline__ uint32_t tile_offset(int r, int c) { 
+    return static_cast<uint32_t>((c >> 3) * (Cfg::BN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// One warp's pass over a bf16 V tile in shared memory: rows that were not
+// copied, or lie past the range (row >= len), become 0; in rows from `diag` on
+// infinities and NaN become 0 and the row's bit in poison is set.
+template <class Cfg>
+__device__ __noinline__ void fix_v_tile(uint8_t* tile, uint32_t copies, int log2_box, int len, int diag,
+                                        uint32_t* poison, int lane) {
+    constexpr int CPR = Cfg::D / 8, LPR = CPR < 32 ? CPR : 32;     // 16-byte chunks, lanes of a row
+    // Rows below `from` are as they should be.
+    int from = max(min(len, diag), 0);
+    const uint32_t missing = ~copies & ((1u << (Cfg::BN >> log2_box)) - 1u);
+    if (missing) from = min(from, (__ffs(missing) - 1) << log2_box);
+    for (int r = from + lane / LPR; r < Cfg::BN; r += 32 / LPR) {
+        const bool have = r < len && ((copies >> (r >> log2_box)) & 1u);
+        if (have && r < diag) continue;
+        bool bad = false;
+#pragma unroll
+        for (int c = lane % LPR; c < CPR; c += LPR) {
+            uint4* at = reinterpret_cast<uint4*>(tile + tile_offset<Cfg>(r, c));
+            uint4 v = have ? *at : make_uint4(0, 0, 0, 0);
+            uint32_t* w = &v.x;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                if ((w[y] & 0x7f80u) == 0x7f80u) { w[y] &= 0xffff0000u; bad = true; }
+                if ((w[y] & 0x7f800000u) == 0x7f800000u) { w[y] &= 0xffffu; bad = true; }
+            }
+            *at = v;
+        }
+        if (bad) atomicOr(&poison[r >> 5], 1u << (r & 31));
+    }
+    __syncwarp();
 }
 
 // What a CTA computes; every role derives it alike.
@@ -215,13 +274,30 @@ __device__ __forceinline__ void tile_entries(const TileItem& w, F&& f) {
     }
 }
 
+// Ring index of stream t's V_(u-1) (is_v) or K_u in tile_entries order.
 template <class Cfg>
-__device__ __forceinline__ uint32_t tile_offset(int r, int c) {     // 16-byte chunk c of row r
-    return static_cast<uint32_t>((c >> 3) * (Cfg::BN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+__device__ __forceinline__ uint32_t tile_entry(const TileItem& w, int t, int u, bool is_v) {
+    if (w.pair || Cfg::NS == 1) return is_v ? 2 * u - 1 : 2 * u;
+    const int b = max(u - 1, 0);
+    int x = min(b, w.n[0]) + min(u, w.n[0]) + min(b, w.n[1]) + min(u, w.n[1]);      // rounds before u
+    const int v0 = u >= 1 && u <= w.n[0], k0 = u < w.n[0], v1 = u >= 1 && u <= w.n[1];
+    if (t == 1) x += v0 + k0;
+    if (!is_v) x += t == 0 ? v0 : v1;
+    return static_cast<uint32_t>(x);
 }
 
+// Position of stream t's key tile u among the K entries (its scale slot).
+template <class Cfg>
+__device__ __forceinline__ int tile_slot(const TileItem& w, int t, int u) {
+    if (w.pair || Cfg::NS == 1) return u;
+    return u + (t == 0 ? min(u, w.n[1]) : min(u + 1, w.n[0]));
+}
+
+
 template <class Cfg, bool DIRECT>
-__global__ void __launch_bounds__(Cfg::THREADS, 1) paged_tile_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
+    paged_tile_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                      const __grid_constant__ PagedParams p) {
     constexpr int D = Cfg::D, BN = Cfg::BN, BM = Cfg::BM, NS = Cfg::NS, NH = Cfg::NH;
     constexpr bool FP8 = Cfg::FP8;
     extern __shared__ uint8_t smem_raw[];
@@ -234,26 +310,66 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) paged_tile_kernel(const Paged
     volatile int* abort_flag = &bars->abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    if (tid == 0) {
-        mbar_init(&bars->q_full, 128);
-        mbar_init(&bars->loaded, 128);
-        mbar_init(&bars->drain, 1);
+    const TileItem w = tile_item<Cfg>(p);
+    // From this key on the CTA's rows may see different keys; its tile.
+    int diag_key = w.len;
+    if (!w.prefix && p.causal) diag_key = row_limit(p, w, max(w.rt[0], 0) * BM);
+    const int diag = diag_key < w.len ? diag_key / BN : w.len / BN + 1;
+
+    // Softmax threads: their query row, and its copy on the way before anything
+    // else.  A warp brings in its 32 rows of the tile, swizzled, zero where there
+    // is none; in alt mode both streams use stream 0's tile.
+    const int stream = warp >> 2;
+    const int row = (stream == 0 ? w.rt[0] : w.rt[1]) * BM + (tid & 127);
+    bool in = false;
+    long long out = 0;
+    int lse_at = 0;
+    if (warp < 4 * NS) {
+        in = (stream == 0 ? w.rt[0] : w.rt[1]) >= 0 && row < w.rows;
+        if (in) {
+            const int per = p.Nq * p.G;
+            const int b = w.prefix ? row / per : w.seq, i = (w.prefix ? row % per : row) / p.G;
+            const int h = w.kvh * p.G + row % p.G;
+            out = (static_cast<long long>(b) * p.Nq + i) * p.H + h;
+            lse_at = (b * p.H + h) * p.Nq + i;
+        }
+        if (w.pair || stream == 0) {
+            constexpr int LPR = D / 8 < 32 ? D / 8 : 32;           // lanes per row (16 bytes each)
+            const long long mine = in ? out : -1;
+#pragma unroll 4
+            for (int x = 0; x < LPR; ++x) {
+                const int rr = x * (32 / LPR) + lane / LPR;        // row of the warp
+                const long long src = __shfl_sync(0xffffffffu, mine, rr);
+                const int rq = (warp & 3) * 32 + rr, c = lane % LPR;
+                cp_async16(smem_u32(sQ) + stream * Cfg::Q_BYTES + (c >> 3) * (BM * 128) + rq * 128 + (((c & 7) ^ (rq & 7)) << 4),
+                           static_cast<const __nv_bfloat16*>(p.q) + (src < 0 ? 0 : src * D) + c * 8, src >= 0);
+            }
+        }
+        cp_async_commit();
+    }
+    if (tid == Cfg::LOAD_WARP * 32) {
+        mbar_init(&bars->q_full, NS * 128);
+        mbar_init(&bars->loaded, 1);
+        mbar_init(&bars->fix, 1);
         for (int t = 0; t < 2; ++t) {
+            mbar_init(&bars->drain[t], 1);
             mbar_init(&bars->s_full[t], 1);
             mbar_init(&bars->p_full[t], 128);
             mbar_init(&bars->o_full[t], 1);
         }
         for (int s = 0; s < 8; ++s) {
-            mbar_init(&bars->ring_full[s], 128);
-            mbar_init(&bars->ring_empty[s], 1);
-            mbar_init(&bars->sc_full[s], 128);
+            mbar_init(&bars->ring_full[s], FP8 ? 128 : 1);
+            mbar_init(&bars->ring_empty[s], w.pair ? 2 : 1);       // the MMA warps that use an entry
+            mbar_init(&bars->raw_full[s], 1);
+            mbar_init(&bars->raw_empty[s], 128);
+            mbar_init(&bars->sc_full[s], 1);
             for (int x = 0; x < 4; ++x) bars->poison[s][x] = 0;
         }
         bars->abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
     }
-    if (warp == 0) {
+    if (warp == Cfg::MMA_WARP) {
         tmem_alloc(&bars->tmem_base, 512);
         tmem_relinquish();
     }
@@ -261,348 +377,263 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) paged_tile_kernel(const Paged
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
-    const TileItem w = tile_item<Cfg>(p);
-    // From this key on the CTA's rows may see different keys; its tile.
-    int diag_key = w.len;
-    if (!w.prefix && p.causal) diag_key = row_limit(p, w, max(w.rt[0], 0) * BM);
-    const int diag = diag_key < w.len ? diag_key / BN : w.len / BN + 1;
 
-    if (warp >= Cfg::MMA_WARP) {
-        regs_decrease<Cfg::MMA_REGS>();
-        if (warp == Cfg::MMA_WARP) {
-            // -------------------------------------------------------- MMA issuer
+    if (warp >= Cfg::LOAD_WARP) {
+        regs_decrease<Cfg::LOW_REGS>();
+        if (warp >= Cfg::MMA_WARP && warp < Cfg::MMA_WARP + NS) {
+            // -------------------------------------------------------- MMA issuers
+            // Step u of a stream: O += P(u-1) V(u-1), then S(u).  In pair mode
+            // both warps release every ring entry, always after waiting for it.
             constexpr uint32_t idesc_s = make_idesc(1u, 128, BN, 0), idesc_o = make_idesc(1u, 128, D, 1);
+            const int t = warp - Cfg::MMA_WARP;
+            const int nt = t == 0 ? w.n[0] : w.n[1];
+            const int n = w.pair ? max(w.n[0], w.n[1]) : nt;
             const uint32_t ring = smem_u32(sRing);
-            uint32_t e = 0;                         // ring entries consumed
-            uint32_t pc[2] = {0, 0};                // P tiles consumed per stream
-            bool ok = (w.n[0] + w.n[1] == 0) || tile_warp_wait(&bars->q_full, 0, abort_flag, p, SITE_TILE_Q);
-            auto entry = [&](uint32_t x) { return tile_warp_wait(&bars->ring_full[x % NH], (x / NH) & 1, abort_flag, p, SITE_TILE_FULL); };
-            auto issue_s = [&](int t, uint32_t x) {
-                const uint64_t qd = sdesc_sw128(smem_u32(sQ) + (w.pair ? t : 0) * Cfg::Q_BYTES, 16, 1024);
-                const uint64_t kd = sdesc_sw128(ring + (x % NH) * Cfg::HALF_BYTES, 16, 1024);
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t a = (kk / 4) * (BM * 128) + (kk % 4) * 32, b = (kk / 4) * (BN * 128) + (kk % 4) * 32;
-                        mma_f16_ss(tmem + t * 128, qd + (a >> 4), kd + (b >> 4), idesc_s, kk > 0 ? 1u : 0u);
-                    }
-                    mma_commit(&bars->s_full[t]);
-                }
-                __syncwarp();
-            };
-            auto issue_o = [&](int t, uint32_t x, bool acc, bool last) {
-                const uint64_t vd = sdesc_sw128(ring + (x % NH) * Cfg::HALF_BYTES, BN * 128, 1024);
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < BN / 16; ++kk)
-                        mma_f16_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8, vd + ((kk * 16 * 128) >> 4), idesc_o,
-                                   (kk > 0 || acc) ? 1u : 0u);
-                    if (last) mma_commit(&bars->o_full[t]);
-                }
-                __syncwarp();
-            };
-            auto release = [&](uint32_t x) {
-                if (elect_one()) mma_commit(&bars->ring_empty[x % NH]);
-                __syncwarp();
-            };
-            auto wait_p = [&](int t) {
-                const bool r = tile_warp_wait(&bars->p_full[t], pc[t] & 1, abort_flag, p, SITE_TILE_P);
-                ++pc[t];
-                tc_fence_after();
-                return r;
-            };
-            const int n = max(w.n[0], w.n[1]);
-            if (w.pair || NS == 1) {
-                // Step u: per stream O += P(u-1) V(u-1), then S(u).
-                for (int u = 0; u <= n && ok; ++u) {
-                    const uint32_t ev = 2 * u - 1, ek = 2 * u;
-                    if (u > 0) ok = entry(ev);
-                    if (ok && u < n) ok = entry(ek);
+            const uint32_t s_tmem = tmem + t * 128, o_tmem = tmem + 256 + t * D;
+            const uint64_t qd = sdesc_sw128(smem_u32(sQ) + (w.pair ? t : 0) * Cfg::Q_BYTES, 16, 1024);
+            bool ok = n == 0 || tile_warp_wait(&bars->q_full, 0, abort_flag, p, SITE_TILE_Q);
+            for (int u = 0; u <= n && ok; ++u) {
+                if (u > 0) {
+                    const uint32_t x = tile_entry<Cfg>(w, t, u, true);
+                    ok = tile_warp_wait(&bars->ring_full[x % NH], (x / NH) & 1, abort_flag, p, SITE_TILE_FULL);
                     if (!ok) break;
-                    tc_fence_after();
+                    if (u <= nt) {
+                        ok = tile_warp_wait(&bars->p_full[t], (u - 1) & 1, abort_flag, p, SITE_TILE_P);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vd = sdesc_sw128(ring + (x % NH) * Cfg::HALF_BYTES, BN * 128, 1024);
+                        if (elect_one()) {
 #pragma unroll
-                    for (int t = 0; t < NS; ++t) {
-                        if (u > 0 && u <= w.n[t]) {
-                            if (!wait_p(t)) { ok = false; break; }
-                            issue_o(t, ev, u > 1, u == w.n[t]);
+                            for (int kk = 0; kk < BN / 16; ++kk)
+                                mma_f16_ts(o_tmem, s_tmem + kk * 8, vd + ((kk * 16 * 128) >> 4), idesc_o,
+                                           (kk > 0 || u > 1) ? 1u : 0u);
+                            if (u == nt) mma_commit(&bars->o_full[t]);
+                            mma_commit(&bars->ring_empty[x % NH]);
                         }
-                        if (u < w.n[t]) issue_s(t, ek);
+                    } else if (elect_one()) {
+                        mbar_arrive(&bars->ring_empty[x % NH]);
                     }
-                    if (!ok) break;
-                    if (u > 0) release(ev);
-                    if (u < n) release(ek);
+                    __syncwarp();
                 }
-            } else {
-                for (int u = 0; u <= n && ok; ++u) {
+                if (u < n) {
+                    const uint32_t x = tile_entry<Cfg>(w, t, u, false);
+                    ok = tile_warp_wait(&bars->ring_full[x % NH], (x / NH) & 1, abort_flag, p, SITE_TILE_FULL);
+                    if (!ok) break;
+                    if (u < nt) {
+                        tc_fence_after();
+                        const uint64_t kd = sdesc_sw128(ring + (x % NH) * Cfg::HALF_BYTES, 16, 1024);
+                        if (elect_one()) {
 #pragma unroll
-                    for (int t = 0; t < NS; ++t) {
-                        if (!ok) continue;
-                        if (u >= 1 && u <= w.n[t]) {
-                            ok = entry(e) && wait_p(t);
-                            if (!ok) continue;
-                            tc_fence_after();
-                            issue_o(t, e, u > 1, u == w.n[t]);
-                            release(e);
-                            ++e;
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t a = (kk / 4) * (BM * 128) + (kk % 4) * 32, b = (kk / 4) * (BN * 128) + (kk % 4) * 32;
+                                mma_f16_ss(s_tmem, qd + (a >> 4), kd + (b >> 4), idesc_s, kk > 0 ? 1u : 0u);
+                            }
+                            mma_commit(&bars->s_full[t]);
+                            mma_commit(&bars->ring_empty[x % NH]);
                         }
-                        if (u < w.n[t]) {
-                            ok = entry(e);
-                            if (!ok) continue;
-                            tc_fence_after();
-                            issue_s(t, e);
-                            release(e);
-                            ++e;
-                        }
+                    } else if (elect_one()) {
+                        mbar_arrive(&bars->ring_empty[x % NH]);
                     }
+                    __syncwarp();
                 }
             }
             // Every MMA issued here has finished before teardown.
             if (elect_one()) {
-                mma_commit(&bars->drain);
-                const long long t0 = clock64();
-                const unsigned long long lim = p.wait_limit > 2000000000ull ? p.wait_limit : 2000000000ull;
-                while (!mbar_try_wait(&bars->drain, 0)) {
-                    if (static_cast<unsigned long long>(clock64() - t0) > lim) {
-                        atomicCAS(p.status, 0, SITE_TILE_DRAIN);
-                        break;
-                    }
-                }
+                mma_commit(&bars->drain[t]);
+                tile_drain(&bars->drain[t], 0, p, SITE_TILE_DRAIN);
             }
             __syncwarp();
         }
-    } else if (warp >= Cfg::LOAD_WARP) {
-        regs_decrease<Cfg::LOAD_REGS>();
-        // ------------------------------------------------------------ loaders
-        const int lt = tid - Cfg::LOAD_WARP * 32;
-        const int mask = (1 << p.page_shift) - 1;
-        // Q: rows of the segment, zero where there are none.
-        {
-            const int per = p.Nq * p.G;
-            const int tiles = w.pair ? 2 : 1;
-            for (int x = lt; x < tiles * BM * (D / 8); x += 128) {
-                const int c = x % (D / 8), r = x / (D / 8) % BM, t = x / (D / 8) / BM;
-                const int row = w.rt[t] * BM + r;
-                const bool in = w.rt[t] >= 0 && row < w.rows;
-                long long src = 0;
-                if (in) {
-                    const int b = w.prefix ? row / per : w.seq, i = (w.prefix ? row % per : row) / p.G;
-                    src = ((static_cast<long long>(b) * p.Nq + i) * p.H + w.kvh * p.G + row % p.G) * D + c * 8;
-                }
-                cp_async16(smem_u32(sQ) + t * Cfg::Q_BYTES + (c >> 3) * (BM * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-                           static_cast<const __nv_bfloat16*>(p.q) + src, in);
-            }
-            cp_async_commit();
-            cp_async_wait<0>();
-            fence_proxy_async_smem();
-            mbar_arrive(&bars->q_full);
-        }
-        // Cache row of key `key` (its page's row when it is inside the cache),
-        // -1 where there is none.
-        auto cache_row = [&](int key) -> long long {
-            if (key >= w.len) return -1;
-            const int page = __ldg(w.table + (key >> p.page_shift));
-            if (page < 0 || page >= p.num_pages) {
-                atomicCAS(p.status, 0, SITE_PAGED_PAGE);
-                return -1;
-            }
-            return ((static_cast<long long>(page) * p.H_kv + w.kvh) << p.page_shift) + (key & mask);
-        };
-        constexpr int CPR = D * Cfg::ES / 16;               // 16-byte chunks of a cache row
-        constexpr int RPP = 128 / CPR;                      // rows per pass of the 128 threads
-        constexpr int PASSES = BN / RPP;
-        const int c = lt % CPR, r0 = lt / CPR;
-        // The tile's validity bits and (e4m3) scales: at its K entry.
-        auto tile_meta = [&](int key0, int slot) {
-            const int k = lt;
-            long long row = -1;
-            if (k < BN) row = cache_row(key0 + k);
-            const uint32_t bits = __ballot_sync(0xffffffffu, row >= 0);
-            if (k < BN && lane == 0) bars->valid[slot][k >> 5] = bits;
-            if constexpr (FP8) {
-                if (k < BN) {
-                    const uint32_t dst = smem_u32(sScale) + (slot * 2 * BN + k) * 4;
-                    const float* ks = p.k_scale + (row < 0 ? 0 : row);
-                    const float* vs = p.v_scale + (row < 0 ? 0 : row);
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(ks), "r"(row < 0 ? 0 : 4) : "memory");
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + BN * 4), "l"(vs), "r"(row < 0 ? 0 : 4) : "memory");
-                }
-            }
-        };
-        auto copy_rows = [&](const void* cache, int key0, auto&& dst) {
-            const uint8_t* base = static_cast<const uint8_t*>(cache) + c * 16;
-#pragma unroll
-            for (int i = 0; i < PASSES; ++i) {
-                const int r = r0 + i * RPP;
-                const long long row = cache_row(key0 + r);
-                cp_async16(dst(r, i), base + (row < 0 ? 0 : row * (D * Cfg::ES)), row >= 0);
-            }
-        };
-        const uint32_t ring = smem_u32(sRing), raw = smem_u32(sRaw);
-        bool ok = true;
-        uint32_t ktile = 0;                                 // key tiles so far (scale slots)
-        if constexpr (!FP8) {
-            uint32_t e = 0, done = 0;                       // entries issued; signalled
-            uint32_t kinds = 0;                             // bit (e & 31): entry e is a V
-            int keys[Cfg::AHEAD + 1];
-#pragma unroll
-            for (int x = 0; x <= Cfg::AHEAD; ++x) keys[x] = 0;
-            uint32_t kdone = 0;
-            auto signal = [&](uint32_t x, int key0) {
-                if ((kinds >> (x & 31)) & 1u) {
-                    if (key0 / BN >= diag) {
-                        // Non-finite values leave the products of tiles that
-                        // only some rows see; the rows that see them learn it
-                        // from the poison bits.
-                        uint8_t* tile = sRing + (x % NH) * Cfg::HALF_BYTES;
-#pragma unroll 1
-                        for (int i = 0; i < PASSES; ++i) {
-                            const int r = r0 + i * RPP;
-                            uint32_t* at = reinterpret_cast<uint32_t*>(tile + tile_offset<Cfg>(r, c));
-                            bool any = false;
-                            if (key0 + r < diag_key) continue;
-#pragma unroll 1
-                            for (int y = 0; y < 4; ++y) {
-                                uint32_t v = at[y];
-                                if ((v & 0x7f80u) == 0x7f80u) { v &= 0xffff0000u; any = true; }
-                                if ((v & 0x7f800000u) == 0x7f800000u) { v &= 0xffffu; any = true; }
-                                at[y] = v;
-                            }
-                            if (any) atomicOr(&bars->poison[min(key0 / BN - diag, Cfg::DIAG_TILES - 1)][r >> 5], 1u << (r & 31));
-                        }
-                    }
-                } else {
-                    mbar_arrive(&bars->sc_full[kdone++ % Cfg::SLOTS]);
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&bars->ring_full[x % NH]);
+        if (warp == Cfg::LOAD_WARP) {
+            // -------------------------------------------------------- load warp
+            const int ps = 1 << p.page_shift;
+            const int box = min(ps, BN), boxes = BN / box;      // rows of a copy; copies of a tile (per 64 columns)
+            const uint64_t pol = l2_policy_evict_last();
+            uint32_t e = 0, ktiles = 0, fixes = 0;
+            // Lane x < boxes looks up the page of copy x; the next tile's page
+            // is fetched while this one is copied.
+            auto page_of = [&](int key0) -> int {
+                const int key = key0 + lane * box;
+                return lane < boxes && key < w.len ? __ldg(w.table + (key >> p.page_shift)) : -1;
             };
             tile_entries<Cfg>(w, [&](int t, int u, bool is_v) -> bool {
-                if (!tile_wait(&bars->ring_empty[e % NH], ((e / NH) & 1) ^ 1, abort_flag, p, SITE_TILE_EMPTY)) {
-                    ok = false;
-                    return false;
+                const int key0 = ((t == 0 ? w.j0[0] : w.j0[1]) + u) * BN;
+                const int key = key0 + lane * box;
+                const int page = page_of(key0);
+                const bool want = lane < boxes && key < w.len;
+                const bool have = want && page >= 0 && page < p.num_pages;
+                const uint32_t copies = __ballot_sync(0xffffffffu, have);
+                const int row = key & (ps - 1);
+                const uint32_t slot = tile_slot<Cfg>(w, t, u) % Cfg::SLOTS;
+                uint64_t* gate = FP8 ? &bars->raw_empty[e % (FP8 ? Cfg::NR : 1)] : &bars->ring_empty[e % NH];
+                const uint32_t round = e / (FP8 ? Cfg::NR : NH);
+                if (!tile_warp_wait(gate, (round & 1) ^ 1, abort_flag, p, SITE_TILE_EMPTY)) return false;
+                if (!is_v) {
+                    // Validity of the tile's keys (the slot is free: see SLOTS).
+                    if (want && !have) atomicCAS(p.status, 0, SITE_PAGED_PAGE);
+                    if (lane < BN / 32) {
+                        uint32_t bits = 0;
+                        if (box >= 32) bits = (copies >> (lane * 32 / box)) & 1u ? 0xffffffffu : 0u;
+                        else bits = ((copies >> (2 * lane)) & 1u ? 0xffffu : 0u) | ((copies >> (2 * lane + 1)) & 1u ? 0xffff0000u : 0u);
+                        const int n = min(max(w.len - key0 - lane * 32, 0), 32);
+                        bars->valid[slot][lane] = bits & (n == 32 ? 0xffffffffu : (1u << n) - 1u);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(&bars->sc_full[slot], FP8 ? __popc(copies) * box * 8 : 0);
+                    __syncwarp();
+                    if constexpr (FP8) {
+                        if (have) {
+                            const long long at = ((static_cast<long long>(page) * p.H_kv + w.kvh) << p.page_shift) + row;
+                            float* dst = sScale + slot * 2 * BN + lane * box;
+                            bulk_load(dst, p.k_scale + at, box * 4, &bars->sc_full[slot]);
+                            bulk_load(dst + BN, p.v_scale + at, box * 4, &bars->sc_full[slot]);
+                        }
+                    }
+                    ++ktiles;
                 }
-                const int key0 = (w.j0[t] + u) * BN;
-                if (!is_v) tile_meta(key0, static_cast<int>(ktile++ % Cfg::SLOTS));
-                const uint32_t at = ring + (e % NH) * Cfg::HALF_BYTES;
-                copy_rows(is_v ? p.v_cache : p.k_cache, key0, [&](int r, int) { return at + tile_offset<Cfg>(r, c); });
-                cp_async_commit();
-                kinds = is_v ? kinds | (1u << (e & 31)) : kinds & ~(1u << (e & 31));
+                if constexpr (FP8) {
+                    uint64_t* full = &bars->raw_full[e % (FP8 ? Cfg::NR : 1)];
+                    if (lane == 0) mbar_arrive_expect_tx(full, __popc(copies) * box * D);
+                    __syncwarp();
+                    if (have) {
+                        const long long at = ((static_cast<long long>(page) * p.H_kv + w.kvh) << p.page_shift) + row;
+                        bulk_load(sRaw + (e % (FP8 ? Cfg::NR : 1)) * Cfg::RAW_BYTES + lane * box * D,
+                                  static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) + at * D, box * D, full);
+                    }
+                } else {
+                    // A V tile with rows that must not reach the product as they
+                    // are: past the range, of a refused page, or not finite where
+                    // only some query rows see them.
+                    const bool fix = is_v && (key0 + BN > w.len || __popc(copies) != boxes || key0 / BN >= diag);
+                    uint64_t* full = fix ? &bars->fix : &bars->ring_full[e % NH];
+                    uint8_t* tile = sRing + (e % NH) * Cfg::HALF_BYTES;
+                    if (lane == 0) mbar_arrive_expect_tx(full, __popc(copies) * box * D * 2);
+                    __syncwarp();
+                    if (have) {
 #pragma unroll
-                for (int x = Cfg::AHEAD; x > 0; --x) keys[x] = keys[x - 1];
-                keys[0] = key0;
-                ++e;
-                if (e > Cfg::AHEAD) {
-                    cp_async_wait<Cfg::AHEAD>();
-                    signal(done++, keys[Cfg::AHEAD]);
+                        for (int cb = 0; cb < Cfg::NCB; ++cb)
+                            tma_load_4d(tile + cb * (BN * 128) + lane * box * 128, is_v ? &tmap_v : &tmap_k, full, cb * 64,
+                                        row, w.kvh, page, pol);
+                    }
+                    if (fix) {
+                        __syncwarp();
+                        tile_drain(&bars->fix, fixes++ & 1, p, SITE_TILE_LOADED);
+                        fix_v_tile<Cfg>(tile, copies, __ffs(box) - 1, w.len - key0, max(diag_key - key0, 0),
+                                        bars->poison[min(max(key0 / BN - diag, 0), Cfg::DIAG_TILES - 1)], lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars->ring_full[e % NH]);
+                    }
                 }
+                __syncwarp();
+                ++e;
                 return true;
             });
-            cp_async_wait<0>();
-            if (ok) {
-#pragma unroll
-                for (int x = Cfg::AHEAD - 1; x >= 0; --x)
-                    if (static_cast<int>(e) > x) signal(done++, keys[x]);
+            if (lane == 0) mbar_arrive(&bars->loaded);
+            // Every copy issued here lands before the CTA can exit (on the normal
+            // path these phases have completed already).
+            if constexpr (FP8) {
+                constexpr uint32_t NR = FP8 ? Cfg::NR : 1;
+                for (uint32_t x = e > NR ? e - NR : 0; x < e; ++x)
+                    tile_drain(&bars->raw_full[x % NR], (x / NR) & 1, p, SITE_TILE_DRAIN);
+                for (uint32_t x = ktiles > Cfg::SLOTS ? ktiles - Cfg::SLOTS : 0; x < ktiles; ++x)
+                    tile_drain(&bars->sc_full[x % Cfg::SLOTS], (x / Cfg::SLOTS) & 1, p, SITE_TILE_DRAIN);
+            } else {
+                for (uint32_t x = e > NH ? e - NH : 0; x < e; ++x)
+                    tile_drain(&bars->ring_full[x % NH], (x / NH) & 1, p, SITE_TILE_DRAIN);
             }
-        } else {
-            // The raw queue runs NR - 1 entries ahead of the conversion: a
-            // second walk over the same entries.
-            uint32_t ei = 0, e = 0, kdone = 0;
-            const int total_n = max(w.n[0], w.n[1]);
-            const uint32_t total = w.pair || NS == 1 ? 2u * total_n : 2u * (w.n[0] + w.n[1]);
-            // Entry x of the walk: stream, tile, K or V.
-            int it_u = 0, it_phase = 0;                     // iterator of the issue side
-            auto next = [&](int& t, int& u, bool& is_v) {
-                // The next ring entry in tile_entries order.
-                if (w.pair || NS == 1) {
-                    t = 0;
-                    u = it_u;
-                    is_v = it_phase == 1;
-                    if (it_phase == 1) { it_phase = 0; ++it_u; }
-                    else it_phase = 1;
-                    return;
+        }
+    } else if (FP8 && warp >= Cfg::CONV_WARP) {
+        regs_decrease<Cfg::CONV_REGS>();
+        if constexpr (FP8) {
+            // ---------------------------------------------------- converting warps
+            // A thread's chunks (16 codes) lie in rows r0 + i * RPP.  For d >= 128 a
+            // quarter warp takes half of the chunk columns of two neighbouring
+            // rows: its two stores per chunk (16-byte columns 2c and 2c + 1 of
+            // the swizzle) then each cover all eight columns once.
+            constexpr int CPR = D / 16;                         // chunks of a row
+            constexpr int RPP = 128 / CPR;                      // rows per pass of the 128 threads
+            const int ct = tid - Cfg::CONV_WARP * 32;
+            int c, r0;
+            if constexpr (D == 64) {
+                c = ct % CPR;
+                r0 = ct / CPR;
+            } else {
+                constexpr int G4 = CPR / 4;                     // groups of four chunk columns
+                c = (ct & 3) + ((ct >> 3) % G4) * 4;
+                r0 = ((ct >> 2) & 1) + (ct >> 3) / G4 * 2;
+            }
+            uint32_t e = 0;
+            tile_entries<Cfg>(w, [&](int t, int u, bool is_v) -> bool {
+                constexpr uint32_t NR = Cfg::NR;
+                if (!tile_wait(&bars->raw_full[e % NR], (e / NR) & 1, abort_flag, p, SITE_TILE_FULL)) return false;
+                const int kt = tile_slot<Cfg>(w, t, u), slot = kt % Cfg::SLOTS;
+                const int key0 = ((t == 0 ? w.j0[0] : w.j0[1]) + u) * BN;
+                const uint32_t* valid = bars->valid[slot];
+                uint32_t all = valid[0] & valid[1];
+                if constexpr (BN == 128) all &= valid[2] & valid[3];
+                const bool whole = all == 0xffffffffu;
+                if (!is_v && (!whole || key0 / BN >= diag)) {
+                    // Scales that must not meet a weight of 0 as they are: of keys
+                    // that are not there (stale), and NaN where only some query
+                    // rows see the key (those rows learn it from the poison bits).
+                    if (!tile_wait(&bars->sc_full[slot], (kt / Cfg::SLOTS) & 1, abort_flag, p, SITE_TILE_SCALE)) return false;
+                    if (ct < BN) {
+                        float* vs = sScale + slot * 2 * BN + BN + ct;
+                        const bool have = (valid[ct >> 5] >> (ct & 31)) & 1u;
+                        if (!have) {
+                            *vs = 0.0f;
+                        } else if (key0 + ct >= diag_key && !(fabsf(*vs) < INFINITY)) {
+                            *vs = 0.0f;
+                            atomicOr(&bars->poison[min(key0 / BN - diag, Cfg::DIAG_TILES - 1)][ct >> 5], 1u << (ct & 31));
+                        }
+                    }
                 }
-                while (true) {                              // phases: V of stream 0, K of 0, V of 1, K of 1
-                    const int ph = it_phase, uu = it_u;
-                    if (++it_phase == 4) { it_phase = 0; ++it_u; }
-                    t = ph >> 1;
-                    is_v = (ph & 1) == 0;
-                    u = is_v ? uu - 1 : uu;
-                    if (is_v ? (uu >= 1 && uu <= w.n[t]) : uu < w.n[t]) return;
-                    if (uu > total_n) return;
-                }
-            };
-            uint32_t kinds = 0;
-            auto issue = [&]() {
-                if (ei < total) {
-                    int t, u;
-                    bool is_v;
-                    next(t, u, is_v);
-                    const int key0 = (w.j0[t] + u) * BN;
-                    if (!is_v) tile_meta(key0, static_cast<int>(ktile++ % Cfg::SLOTS));
-                    const uint32_t at = raw + (ei % Cfg::NR) * Cfg::RAW_BYTES + lt * 16;
-                    copy_rows(is_v ? p.v_cache : p.k_cache, key0, [&](int, int i) { return at + i * 128 * 16; });
-                    kinds = is_v ? kinds | (1u << (ei & 31)) : kinds & ~(1u << (ei & 31));
-                    ++ei;
-                }
-                cp_async_commit();
-            };
-            for (int x = 0; x < Cfg::NR - 1; ++x) issue();
-            for (; e < total; ++e) {
-                issue();
-                cp_async_wait<Cfg::NR - 1>();
-                if (!((kinds >> (e & 31)) & 1u)) mbar_arrive(&bars->sc_full[kdone++ % Cfg::SLOTS]);
-                if (!tile_wait(&bars->ring_empty[e % NH], ((e / NH) & 1) ^ 1, abort_flag, p, SITE_TILE_EMPTY)) {
-                    ok = false;
-                    break;
-                }
-                const uint8_t* src = sRaw + (e % Cfg::NR) * Cfg::RAW_BYTES + lt * 16;
+                if (!tile_wait(&bars->ring_empty[e % NH], ((e / NH) & 1) ^ 1, abort_flag, p, SITE_TILE_EMPTY)) return false;
+                const uint8_t* src = sRaw + (e % NR) * Cfg::RAW_BYTES + r0 * D + c * 16;
                 uint8_t* dst = sRing + (e % NH) * Cfg::HALF_BYTES;
-#pragma unroll 4
-                for (int i = 0; i < PASSES; ++i) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + i * 128 * 16);
-                    const int r = r0 + i * RPP;
-                    const uint4 lo = make_uint4(e4m3_pair<0x9180>(v.x, 0), e4m3_pair<0xb3a2>(v.x, 0),
-                                                e4m3_pair<0x9180>(v.y, 0), e4m3_pair<0xb3a2>(v.y, 0));
-                    const uint4 hi = make_uint4(e4m3_pair<0x9180>(v.z, 0), e4m3_pair<0xb3a2>(v.z, 0),
-                                                e4m3_pair<0x9180>(v.w, 0), e4m3_pair<0xb3a2>(v.w, 0));
-                    *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c)) = lo;
-                    *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c + 1)) = hi;
-                }
+                auto convert = [&](auto check) {
+#pragma unroll
+                    for (int i = 0; i < BN / RPP; ++i) {
+                        const int r = r0 + i * RPP;
+                        uint4 v = *reinterpret_cast<const uint4*>(src + i * RPP * D);
+                        if constexpr (decltype(check)::value) {
+                            if (!((valid[r >> 5] >> (r & 31)) & 1u)) v = make_uint4(0, 0, 0, 0);
+                        }
+                        *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c)) =
+                            make_uint4(e4m3_pair<0x9180>(v.x, 0), e4m3_pair<0xb3a2>(v.x, 0), e4m3_pair<0x9180>(v.y, 0),
+                                       e4m3_pair<0xb3a2>(v.y, 0));
+                        *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c + 1)) =
+                            make_uint4(e4m3_pair<0x9180>(v.z, 0), e4m3_pair<0xb3a2>(v.z, 0), e4m3_pair<0x9180>(v.w, 0),
+                                       e4m3_pair<0xb3a2>(v.w, 0));
+                    }
+                };
+                if (whole) convert(std::false_type{});
+                else convert(std::true_type{});
                 fence_proxy_async_smem();
                 mbar_arrive(&bars->ring_full[e % NH]);
-            }
-            cp_async_wait<0>();
+                mbar_arrive(&bars->raw_empty[e % NR]);
+                ++e;
+                return true;
+            });
         }
-        if (ok) mbar_arrive(&bars->loaded);
     } else {
         regs_increase<Cfg::HIGH_REGS>();
         // ------------------------------------------------------------ softmax
-        const int t = warp >> 2;
-        const int r = (warp & 3) * 32 + lane;
+        const int t = stream;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + lane_off + t * 128, o_tmem = tmem + lane_off + 256 + t * D;
-        const int rt = t == 0 ? w.rt[0] : w.rt[1], nt = t == 0 ? w.n[0] : w.n[1];
+        const int nt = t == 0 ? w.n[0] : w.n[1];
         const int j0 = t == 0 ? w.j0[0] : w.j0[1], part = t == 0 ? w.part[0] : w.part[1];
-        const int row = rt * BM + r;
-        const bool in = rt >= 0 && row < w.rows;
-        const int per = p.Nq * p.G;
-        long long out = 0;
-        int lse_at = 0;
-        int limit = 0;
-        if (in) {
-            const int b = w.prefix ? row / per : w.seq, i = (w.prefix ? row % per : row) / p.G;
-            const int h = w.kvh * p.G + row % p.G;
-            out = (static_cast<long long>(b) * p.Nq + i) * p.H + h;
-            lse_at = (b * p.H + h) * p.Nq + i;
-            limit = row_limit(p, w, row);
-        }
-        const bool alt = NS == 2 && !w.pair;
+        const int limit = in ? row_limit(p, w, row) : 0;
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->q_full);
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int u = 0; u < nt; ++u) {
             // Scale slot of this tile: its position among the K entries.
-            int kt = u;
-            if (alt) kt = u < min(w.n[0], w.n[1]) ? 2 * u + t : min(w.n[0], w.n[1]) + u;
+            const int kt = tile_slot<Cfg>(w, t, u);
             const int slot = kt % Cfg::SLOTS;
             bool wt = tile_wait(&bars->sc_full[slot], (kt / Cfg::SLOTS) & 1, abort_flag, p, SITE_TILE_SCALE);
             wt = wt && tile_wait(&bars->s_full[t], u & 1, abort_flag, p, SITE_TILE_S);
@@ -618,12 +649,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) paged_tile_kernel(const Paged
 #pragma unroll
             for (int c = 0; c < BN / 32; ++c) reg_fence32(sr + c * 32);
             if constexpr (FP8) {
-                const float2* ks = reinterpret_cast<const float2*>(sScale + slot * 2 * BN);
+                const float4* ks = reinterpret_cast<const float4*>(sScale + slot * 2 * BN);
 #pragma unroll
-                for (int x = 0; x < BN; x += 2) {
-                    const float2 v = __fmul2_rn(make_float2(__uint_as_float(sr[x]), __uint_as_float(sr[x + 1])), ks[x / 2]);
-                    sr[x] = __float_as_uint(v.x);
-                    sr[x + 1] = __float_as_uint(v.y);
+                for (int x = 0; x < BN; x += 4) {
+                    const float4 k4 = ks[x / 4];
+                    const float2 v0 = __fmul2_rn(make_float2(__uint_as_float(sr[x]), __uint_as_float(sr[x + 1])), make_float2(k4.x, k4.y));
+                    const float2 v1 = __fmul2_rn(make_float2(__uint_as_float(sr[x + 2]), __uint_as_float(sr[x + 3])), make_float2(k4.z, k4.w));
+                    sr[x] = __float_as_uint(v0.x);
+                    sr[x + 1] = __float_as_uint(v0.y);
+                    sr[x + 2] = __float_as_uint(v1.x);
+                    sr[x + 3] = __float_as_uint(v1.y);
                 }
             }
             const int key0 = (j0 + u) * BN;
@@ -660,30 +695,29 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) paged_tile_kernel(const Paged
             const float alpha = mn == m ? 1.0f : ex2_approx(m - ref);
             const float2 mul2 = make_float2(p.scale_log2, p.scale_log2), neg2 = make_float2(-ref, -ref);
             float2 acc0 = make_float2(0.0f, 0.0f), acc1 = make_float2(0.0f, 0.0f);
-            const float2* vs = reinterpret_cast<const float2*>(sScale + slot * 2 * BN + BN);
+            const float4* vs = reinterpret_cast<const float4*>(sScale + slot * 2 * BN + BN);
 #pragma unroll
             for (int c = 0; c < BN / 32; ++c) {
                 uint32_t pk[16];
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
+                for (int x = 0; x < 16; x += 2) {
                     const int e = c * 32 + 2 * x;
                     float2 f = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), mul2, neg2);
+                    float2 g = __ffma2_rn(make_float2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])), mul2, neg2);
                     f.x = ex2_approx(f.x);
                     f.y = ex2_approx(f.y);
-                    if (x & 1) acc1 = __fadd2_rn(acc1, f);
-                    else acc0 = __fadd2_rn(acc0, f);
+                    g.x = ex2_approx(g.x);
+                    g.y = ex2_approx(g.y);
+                    acc0 = __fadd2_rn(acc0, f);
+                    acc1 = __fadd2_rn(acc1, g);
                     if constexpr (FP8) {
                         // V's row scale rides on P; l sums the plain weights.
-                        const float2 g = __fmul2_rn(f, vs[e / 2]);
-                        if (masked) {
-                            // 0 times a NaN scale of a key this row does not see
-                            f.x = f.x == 0.0f ? 0.0f : g.x;
-                            f.y = f.y == 0.0f ? 0.0f : g.y;
-                        } else {
-                            f = g;
-                        }
+                        const float4 v4 = vs[e / 4];
+                        f = __fmul2_rn(f, make_float2(v4.x, v4.y));
+                        g = __fmul2_rn(g, make_float2(v4.z, v4.w));
                     }
                     pk[x] = pack_bf16x2(f.x, f.y);
+                    pk[x + 1] = pack_bf16x2(g.x, g.y);
                 }
                 tmem_st16(s_tmem + c * 16, pk);
             }
@@ -714,7 +748,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) paged_tile_kernel(const Paged
         }
         if (ok) {
             tc_fence_after();
-            if (!FP8 && diag < j0 + nt) {
+            if (diag < j0 + nt) {
                 for (int x = max(diag, j0); x < j0 + nt; ++x) {
 #pragma unroll
                     for (int c = 0; c < BN / 32; ++c) {
@@ -732,40 +766,60 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1) paged_tile_kernel(const Paged
             } else {
                 if (in) p.part_lse[part * rows_all + out] = lse2;
             }
+            // O leaves through this warp's 4 KB of shared memory (32 rows x 128
+            // bytes, swizzled by 16-byte chunk), so that every store instruction
+            // writes whole 128-byte lines instead of 16 bytes of 32 rows.  (An
+            // empty part's O is not written: the join does not read it.)
+            uint8_t* epi = D == 64 ? reinterpret_cast<uint8_t*>(bars) - Cfg::EPI_BYTES + t * 16384
+                         : w.pair || NS == 1 ? sQ + t * Cfg::Q_BYTES
+                                             : sQ + Cfg::Q_BYTES + t * 16384;
+            epi += (warp & 3) * 4096;
+            const long long mine = in && (DIRECT || l != 0.0f) ? out : -1;
+            constexpr int COLS = DIRECT ? 64 : 32;             // columns per 128 bytes
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
+            for (int c = 0; c < D / COLS; ++c) {
+                uint32_t o[COLS];
                 if (some) {
-                    tmem_ld32(o_tmem + c * 32, o);
+#pragma unroll
+                    for (int y = 0; y < COLS; y += 32) tmem_ld32(o_tmem + c * COLS + y, o + y);
                     tmem_wait_ld();
-                    reg_fence32(o);
+#pragma unroll
+                    for (int y = 0; y < COLS; y += 32) reg_fence32(o + y);
                 }
                 __syncwarp();
-                if constexpr (DIRECT) {
-                    if (in) {
-                    uint32_t pk[16];
 #pragma unroll
-                    for (int x = 0; x < 16; ++x)
-                        pk[x] = some ? pack_bf16x2(__uint_as_float(o[2 * x]) * inv, __uint_as_float(o[2 * x + 1]) * inv) : 0u;
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + out * D + c * 32);
+                for (int x = 0; x < 8; ++x) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (some) {
+                        uint32_t* q = &v.x;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) dst[x] = make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+                        for (int y = 0; y < 4; ++y)
+                            q[y] = DIRECT ? pack_bf16x2(__uint_as_float(o[(DIRECT ? 8 : 4) * x + 2 * y]) * inv,
+                                                        __uint_as_float(o[(DIRECT ? 8 : 4) * x + 2 * y + 1]) * inv)
+                                          : __float_as_uint(__uint_as_float(o[4 * x + y]) * inv);
                     }
-                } else if (in && l != 0.0f) {
-                    float4* dst = reinterpret_cast<float4*>(p.part_o + (part * rows_all + out) * D + c * 32);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        dst[x] = make_float4(__uint_as_float(o[4 * x]) * inv, __uint_as_float(o[4 * x + 1]) * inv,
-                                             __uint_as_float(o[4 * x + 2]) * inv, __uint_as_float(o[4 * x + 3]) * inv);
+                    *reinterpret_cast<uint4*>(epi + lane * 128 + ((x ^ (lane & 7)) << 4)) = v;
                 }
                 __syncwarp();
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+                    const int rr = x * 4 + lane / 8, ch = lane % 8;
+                    const long long dst = __shfl_sync(0xffffffffu, mine, rr);
+                    const uint4 v = *reinterpret_cast<const uint4*>(epi + rr * 128 + ((ch ^ (rr & 7)) << 4));
+                    if (dst >= 0) {
+                        if constexpr (DIRECT)
+                            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + dst * D + c * COLS)[ch] = v;
+                        else
+                            reinterpret_cast<uint4*>(p.part_o + (part * rows_all + dst) * D + c * COLS)[ch] = v;
+                    }
+                }
             }
         }
     }
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == Cfg::MMA_WARP) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }

@@ -6,7 +6,7 @@
 namespace attn {
 
 template <class Cfg, bool DIRECT>
-cudaError_t launch_paged_tile_one(const PagedParams& p, cudaStream_t stream) {
+cudaError_t launch_paged_tile_one(const PagedMaps& m, const PagedParams& p, cudaStream_t stream) {
     auto kernel = paged_tile_kernel<Cfg, DIRECT>;
     // The register split (setmaxnreg) assumes exactly LAUNCH_REGS registers a
     // thread at launch; another count could make the increase wait forever, so
@@ -18,18 +18,18 @@ cudaError_t launch_paged_tile_one(const PagedParams& p, cudaStream_t stream) {
     // Per function and per device; cheap and idempotent.
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    kernel<<<p.prefix_items + p.own_items, Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(p);
+    kernel<<<p.prefix_items + p.own_items, Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(m.k, m.v, p);
     return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_paged_tile(const PagedParams& p, bool direct, cudaStream_t stream) {
+cudaError_t launch_paged_tile(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream) {
     if (p.fp8) {
         using C = TileCfg<D, true>;
-        return direct ? launch_paged_tile_one<C, true>(p, stream) : launch_paged_tile_one<C, false>(p, stream);
+        return direct ? launch_paged_tile_one<C, true>(m, p, stream) : launch_paged_tile_one<C, false>(m, p, stream);
     }
     using C = TileCfg<D, false>;
-    return direct ? launch_paged_tile_one<C, true>(p, stream) : launch_paged_tile_one<C, false>(p, stream);
+    return direct ? launch_paged_tile_one<C, true>(m, p, stream) : launch_paged_tile_one<C, false>(m, p, stream);
 }
 
 }  // namespace attn
