@@ -7,8 +7,8 @@ loaded, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -37,6 +37,8 @@ class AttnError(RuntimeError):
 def library() -> ctypes.CDLL:
     """Load the shared library (built by ``exact_attention_71_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -524,52 +526,66 @@ def kv_cache(num_pages: int, page_size: int, H_kv: int, d: int, e4m3: bool = Tru
     return KVCache(k, v, ks, vs)
 
 
+# The paged entries are called once per layer and decoding step, where the host
+# is the bound: one pass of checks, plain integers to ctypes, no context manager
+# unless the device or the stream asks for one.
+
 def _check_cache(cache):
-    """(num_pages, H_kv, page_size, d, cache dtype) of a KVCache."""
+    """(num_pages, H_kv, page_size, d, cache dtype, device, pointers) of a KVCache."""
     k, v, ks, vs = cache
-    if not k.is_cuda or k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+    shape, dtype, dev = k.shape, k.dtype, k.device
+    if not k.is_cuda or len(shape) != 4 or v.shape != shape or v.dtype != dtype or v.device != dev:
         raise ValueError("cache k and v must be CUDA tensors of one (num_pages, H_kv, page_size, d) shape and dtype")
     if not k.is_contiguous() or not v.is_contiguous():
         raise ValueError("cache k and v must be contiguous")
-    if k.dtype == torch.bfloat16:
+    pages, Hkv, ps, d = shape
+    if dtype == torch.bfloat16:
         if ks is not None or vs is not None:
             raise ValueError("a bf16 cache has no scales")
-        return (*k.shape, CACHE_BF16)
-    if k.dtype not in (torch.uint8, torch.float8_e4m3fn):
+        return pages, Hkv, ps, d, CACHE_BF16, dev, (k.data_ptr(), v.data_ptr(), None, None)
+    if dtype != torch.uint8 and dtype != torch.float8_e4m3fn:
         raise ValueError("cache k and v must be bf16 or e4m3 codes (uint8 or float8_e4m3fn)")
     for s in (ks, vs):
-        if (s is None or s.dtype != torch.float32 or s.shape != k.shape[:3] or not s.is_contiguous()
-                or s.device != k.device):
+        if (s is None or s.dtype != torch.float32 or s.shape != shape[:3] or not s.is_contiguous()
+                or s.device != dev):
             raise ValueError("an e4m3 cache has contiguous float32 (num_pages, H_kv, page_size) scales")
-    return (*k.shape, CACHE_E4M3)
+    return pages, Hkv, ps, d, CACHE_E4M3, dev, (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr())
 
 
 def _check_table(block_table, seq_lens, B, device):
-    if (block_table.dim() != 2 or block_table.shape[0] != B or block_table.dtype != torch.int32
-            or block_table.device != device or (block_table.shape[1] > 1 and block_table.stride(1) != 1)):
+    """(max_pages, row stride) of a block table."""
+    shape = block_table.shape
+    if (len(shape) != 2 or shape[0] != B or block_table.dtype != torch.int32
+            or block_table.device != device or (shape[1] > 1 and block_table.stride(1) != 1)):
         raise ValueError("block_table must be an int32 (B, max_pages) tensor with contiguous rows on the cache's device")
-    if seq_lens.shape != (B,) or seq_lens.dtype != torch.int32 or seq_lens.device != device or not seq_lens.is_contiguous():
+    if (len(seq_lens.shape) != 1 or seq_lens.shape[0] != B or seq_lens.dtype != torch.int32
+            or seq_lens.device != device or not seq_lens.is_contiguous()):
         raise ValueError("seq_lens must be a contiguous int32 (B,) tensor on the cache's device")
-    max_pages = block_table.shape[1]
+    max_pages = shape[1]
     stride = block_table.stride(0) if B > 1 else max_pages
     if stride < max_pages:
         raise ValueError("the rows of block_table must not overlap")
     return max_pages, stride
 
 
-def _torch_stream_scope(stream, device):
-    """Makes `stream` torch's current one (zeros written for its kernels must
-    be written on it)."""
-    return torch.cuda.stream(_torch_stream(stream, device)) if stream is not None else contextlib.nullcontext()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _on(device):
-    """Makes `device` the current one around a launch (a no-op where it is)."""
-    return torch.cuda.device(device)
-
-
-def _stream_on(stream, device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream)
+def _launch(fn, name, device, stream, args):
+    """Calls entry `fn` with `args` and the stream, with `device` current."""
+    if stream is not None:
+        raw = _stream(stream)
+    elif _raw_stream is not None:
+        raw = _raw_stream(device.index)
+    else:
+        raw = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, raw)
+    if rc != 0:
+        _check(name, rc)
 
 
 def attn_kv_write(k, v, slots, cache: KVCache, stream=None) -> None:
@@ -582,24 +598,24 @@ def attn_kv_write(k, v, slots, cache: KVCache, stream=None) -> None:
     page_size + row; negative slots are skipped, those >= 0 must differ.  A slot
     beyond the cache is skipped and reported by device_status().
     """
-    pages, Hkv, ps, d, dtype = _check_cache(cache)
-    dev = cache.k.device
-    if k.dim() != 3 or k.shape != v.shape or k.shape[1:] != (Hkv, d):
+    pages, Hkv, ps, d, dtype, dev, ptrs = _check_cache(cache)
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape or shape[1] != Hkv or shape[2] != d:
         raise ValueError(f"k and v must be (T, {Hkv}, {d}) tensors")
-    T = k.shape[0]
+    T = shape[0]
+    strides = []
     for t in (k, v):
         if t.dtype != torch.bfloat16 or t.device != dev:
             raise ValueError("k and v must be bf16 tensors on the cache's device")
-        if t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != d):
+        s0, s1, s2 = t.stride()
+        if s2 != 1 or (Hkv > 1 and s1 != d):
             raise ValueError("a token's heads must be contiguous in k and v")
-    if slots.shape != (T,) or slots.dtype != torch.int64 or slots.device != dev or not slots.is_contiguous():
+        strides.append(s0 if T > 1 else Hkv * d)
+    if (len(slots.shape) != 1 or slots.shape[0] != T or slots.dtype != torch.int64 or slots.device != dev
+            or not slots.is_contiguous()):
         raise ValueError("slots must be a contiguous int64 (T,) tensor on the cache's device")
-    with _on(dev):
-        rc = library().attn_kv_write(_ptr(k), _ptr(v), k.stride(0) if T > 1 else Hkv * d,
-                                     v.stride(0) if T > 1 else Hkv * d, _ptr(slots), _ptr(cache.k), _ptr(cache.v),
-                                     _ptr(cache.k_scale), _ptr(cache.v_scale), T, Hkv, d, pages, ps, dtype,
-                                     ctypes.c_void_p(_stream_on(stream, dev)))
-    _check("attn_kv_write", rc)
+    _launch(library().attn_kv_write, "attn_kv_write", dev, stream,
+            (k.data_ptr(), v.data_ptr(), *strides, slots.data_ptr(), *ptrs, T, Hkv, d, pages, ps, dtype))
 
 
 def attn_kv_read(cache: KVCache, block_table, seq_lens, N: int, out_k=None, out_v=None, stream=None):
@@ -610,24 +626,25 @@ def attn_kv_read(cache: KVCache, block_table, seq_lens, N: int, out_k=None, out_
     (B,).  Rows from a sequence's length on are left as they were in out_k /
     out_v (zeros where these are allocated here).  Returns (k, v).
     """
-    pages, Hkv, ps, d, dtype = _check_cache(cache)
-    dev = cache.k.device
+    pages, Hkv, ps, d, dtype, dev, ptrs = _check_cache(cache)
     B = block_table.shape[0]
     max_pages, stride = _check_table(block_table, seq_lens, B, dev)
     shape = (B, N, Hkv, d)
-    with _on(dev), _torch_stream_scope(stream, dev):
-        k = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if out_k is None else out_k
-        v = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if out_v is None else out_v
-        for t in (k, v):
-            if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != dev:
-                raise ValueError(f"out_k and out_v must be contiguous bf16 {shape} tensors on the cache's device")
-        rc = library().attn_kv_read(_ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
-                                    _ptr(block_table), stride, max_pages, _ptr(seq_lens), _ptr(k), _ptr(v), B, N, Hkv,
-                                    d, pages, ps, dtype, ctypes.c_void_p(_stream_on(stream, dev)))
-    _check("attn_kv_read", rc)
-    return k, v
+    if out_k is None or out_v is None:
+        # (the zeros are written on the launch's stream)
+        with torch.cuda.stream(_torch_stream(stream, dev)):
+            out_k = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if out_k is None else out_k
+            out_v = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if out_v is None else out_v
+    for t in (out_k, out_v):
+        if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"out_k and out_v must be contiguous bf16 {shape} tensors on the cache's device")
+    _launch(library().attn_kv_read, "attn_kv_read", dev, stream,
+            (*ptrs, block_table.data_ptr(), stride, max_pages, seq_lens.data_ptr(), out_k.data_ptr(), out_v.data_ptr(),
+             B, N, Hkv, d, pages, ps, dtype))
+    return out_k, out_v
 
 
+@functools.lru_cache(maxsize=1024)
 def paged_workspace_bytes(B: int, Nq: int, H: int, H_kv: int, d: int, prefix_len: int, max_pages: int,
                           page_size: int) -> int:
     return int(library().attn_fwd_paged_workspace_size(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size))
@@ -647,37 +664,46 @@ def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, 
     workspace: optional uint8 CUDA tensor of at least paged_workspace_bytes(...)
     bytes, scratch.  Returns (O (B, Nq, H, d) bf16, LSE (B, H, Nq) float32).
     """
-    pages, Hkv, ps, d, dtype = _check_cache(cache)
-    dev = cache.k.device
-    if q.dim() != 4 or q.dtype != torch.bfloat16 or q.device != dev or not q.is_contiguous():
+    pages, Hkv, ps, d, dtype, dev, ptrs = _check_cache(cache)
+    shape = q.shape
+    if len(shape) != 4 or q.dtype != torch.bfloat16 or q.device != dev or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 (B, Nq, H, d) tensor on the cache's device")
-    B, Nq, H, dq = q.shape
-    if dq != d or H % Hkv != 0:
+    B, Nq, H, dq = shape
+    if dq != d or Hkv == 0 or H % Hkv != 0:
         raise ValueError("q's head dim must be the cache's and its heads a multiple of the cache's")
     max_pages, stride = _check_table(block_table, seq_lens, B, dev)
     prefix_len = int(prefix_len)
-    if prefix_len > 0 and (prefix_table is None or prefix_table.dim() != 1 or prefix_table.dtype != torch.int32
-                           or prefix_table.device != dev or not prefix_table.is_contiguous()
-                           or prefix_table.shape[0] * ps < prefix_len):
-        raise ValueError("prefix_table must be a contiguous int32 tensor of prefix_len's pages on the cache's device")
-    with _on(dev):
-        out, lse = _outputs(q, out, lse)
-        if out.device != dev or lse.device != dev:
-            raise ValueError("out and lse must be on the cache's device")
-        own = workspace is None
-        if own:
-            need = paged_workspace_bytes(B, Nq, H, Hkv, d, prefix_len, max_pages, ps)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        elif workspace.device != dev or not workspace.is_contiguous():
+    prefix = None
+    if prefix_len > 0:
+        if (prefix_table is None or len(prefix_table.shape) != 1 or prefix_table.dtype != torch.int32
+                or prefix_table.device != dev or not prefix_table.is_contiguous()
+                or prefix_table.shape[0] * ps < prefix_len):
+            raise ValueError("prefix_table must be a contiguous int32 tensor of prefix_len's pages on the cache's device")
+        prefix = prefix_table.data_ptr()
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous bf16 (B, Nq, H, d) tensor on the cache's device")
+    if lse is None:
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+    elif lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
+        raise ValueError("lse must be a contiguous float32 (B, H, Nq) tensor on the cache's device")
+    own = workspace is None
+    ws, need = None, 0
+    if own:
+        need = paged_workspace_bytes(B, Nq, H, Hkv, d, prefix_len, max_pages, ps)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws = workspace.data_ptr()
+    else:
+        if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
-        rc = library().attn_fwd_paged(_ptr(q), _ptr(cache.k), _ptr(cache.v), _ptr(cache.k_scale), _ptr(cache.v_scale),
-                                      _ptr(prefix_table) if prefix_len > 0 else None, prefix_len, _ptr(block_table),
-                                      stride, max_pages, _ptr(seq_lens), _ptr(out), _ptr(lse), B, Nq, H, Hkv, d, pages,
-                                      ps, dtype, int(bool(causal)), float(scale or 0.0), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                                      ctypes.c_void_p(_stream_on(stream, dev)))
-    _check("attn_fwd_paged", rc)
-    if own and workspace is not None and stream is not None:
+        ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _launch(library().attn_fwd_paged, "attn_fwd_paged", dev, stream,
+            (q.data_ptr(), *ptrs, prefix, prefix_len, block_table.data_ptr(), stride, max_pages, seq_lens.data_ptr(),
+             out.data_ptr(), lse.data_ptr(), B, Nq, H, Hkv, d, pages, ps, dtype, 1 if causal else 0,
+             float(scale or 0.0), ws, need))
+    if own and ws is not None and stream is not None:
         _hold_until_done(workspace, stream)   # the launches run on `stream`, not torch's current one
     return out, lse
 

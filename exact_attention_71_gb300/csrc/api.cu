@@ -944,21 +944,29 @@ int check_cache(const void* k_cache, const void* v_cache, const float* k_scale, 
     return ATTN_OK;
 }
 
-// A bf16 cache tensor as {d, page_size, H_kv, num_pages}, a box of 64 columns x
-// `rows` rows of one head of one page.
-int make_cache_map(CUtensorMap* map, const void* base, int num_pages, int H_kv, int page_size, int d, int rows) {
+// K and V of the cache as {d, page_size, H_kv, num_pages}: a box of `rows` rows of
+// up to 128 bytes of one head of one page, swizzled.
+int make_cache_maps(attn::PagedMaps* maps, const void* k, const void* v, int num_pages, int H_kv, int page_size, int d,
+                    int elem_bytes, int rows) {
+    if (num_pages == 0) return ATTN_OK;      // every page is refused: no copy is made
     auto enc = encode_fn();
     if (!enc) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const cuuint64_t head = static_cast<cuuint64_t>(page_size) * d * 2;
+    const int span = d * elem_bytes < 128 ? 64 : 128;
+    const cuuint64_t row = static_cast<cuuint64_t>(d) * elem_bytes, head = row * page_size;
     cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size),
                           static_cast<cuuint64_t>(H_kv), static_cast<cuuint64_t>(num_pages)};
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, head, head * static_cast<cuuint64_t>(H_kv)};
-    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
+    cuuint64_t strides[3] = {row, head, head * static_cast<cuuint64_t>(H_kv)};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(span / elem_bytes), static_cast<cuuint32_t>(rows), 1, 1};
     cuuint32_t estride[4] = {1, 1, 1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estride,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled (cache) failed (CUresult %d)", static_cast<int>(r));
+    for (int x = 0; x < 2; ++x) {
+        CUresult r = enc(x ? &maps->v : &maps->k,
+                         elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+                         const_cast<void*>(x ? v : k), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         span == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        if (r != CUDA_SUCCESS)
+            return fail(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled (cache) failed (CUresult %d)", static_cast<int>(r));
+    }
     return ATTN_OK;
 }
 
@@ -1153,18 +1161,19 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
     const auto rows = d == 64 ? attn::run_paged_stream_d64 : d == 128 ? attn::run_paged_stream_d128 : attn::run_paged_stream_d256;
     const auto tiles = d == 64 ? attn::run_paged_tile_d64 : d == 128 ? attn::run_paged_tile_d128 : attn::run_paged_tile_d256;
     cudaError_t e = cudaSuccess;
+    attn::PagedMaps maps{};
+    const int es = p.fp8 ? 1 : 2;
     if (plan.prefix_items + plan.own_items > 0) {
-        attn::PagedMaps maps{};
-        // (an empty cache: every page is refused, no copy is made)
-        if (!p.fp8 && num_pages > 0) {
-            const int bn = d == 256 ? 64 : 128, rows_per_box = page_size < bn ? page_size : bn;
-            if ((rc = make_cache_map(&maps.k, k_cache, num_pages, H_kv, page_size, d, rows_per_box)) != ATTN_OK) return rc;
-            if ((rc = make_cache_map(&maps.v, v_cache, num_pages, H_kv, page_size, d, rows_per_box)) != ATTN_OK) return rc;
-        }
+        const int bn = d == 256 ? 64 : 128;
+        if (!p.fp8 && (rc = make_cache_maps(&maps, k_cache, v_cache, num_pages, H_kv, page_size, d, es,
+                                            page_size < bn ? page_size : bn)) != ATTN_OK)
+            return rc;
         e = tiles(maps, p, plan.direct, s);
     }
-    if (e == cudaSuccess && plan.prefix_stream) e = rows(p, true, false, s);
-    if (e == cudaSuccess && plan.own_items == 0) e = rows(p, false, plan.direct, s);
+    if (e == cudaSuccess && (plan.prefix_stream || plan.own_items == 0)) {
+        if ((rc = make_cache_maps(&maps, k_cache, v_cache, num_pages, H_kv, page_size, d, es, 16)) != ATTN_OK) return rc;
+        e = rows(maps, p, plan.prefix_stream, plan.own_items == 0, plan.direct, s);
+    }
     if (e == cudaSuccess && !plan.direct) e = attn::run_paged_merge(p, s);
     if (e != cudaSuccess) return cuda_fail(e, "attn_fwd_paged launch");
     return ATTN_OK;

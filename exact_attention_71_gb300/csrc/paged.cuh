@@ -13,6 +13,7 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -114,19 +115,37 @@ constexpr int kStreamPrefixRows = 16;
 
 PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size);
 
+// Runs `set` once per device (bit per ordinal; racing threads may run it twice,
+// which is harmless).
+template <class F>
+inline cudaError_t once_per_device(std::atomic<unsigned long long>& done, F&& set) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    if ((e = set()) != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_release);
+    return cudaSuccess;
+}
+
 cudaError_t run_kv_write(const KvWriteParams& p, cudaStream_t stream);
 cudaError_t run_kv_read(const KvReadParams& p, cudaStream_t stream);
-// The streaming kernel over the prefix (prefix) or the own tokens, one
-// translation unit per head dim; direct: it writes o and lse itself.
-cudaError_t run_paged_stream_d64(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream);
-cudaError_t run_paged_stream_d128(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream);
-cudaError_t run_paged_stream_d256(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream);
-// bf16 caches: K and V as 4-D {d, page_size, H_kv, num_pages} tensors with a box
-// of 64 columns x min(page_size, key tile) rows, 128-byte swizzle.
+// K and V of the cache as 4-D {d, page_size, H_kv, num_pages} tensors.  Box of the
+// streaming kernel: 16 rows of up to 128 bytes; of the tile kernel (bf16): 64
+// columns x min(page_size, key tile) rows.  128-byte swizzle (64-byte rows: 64).
 struct PagedMaps {
     CUtensorMap k, v;
 };
 
+// The streaming kernel over the prefix and / or the own tokens, one translation
+// unit per head dim; direct: it writes o and lse itself.
+cudaError_t run_paged_stream_d64(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct,
+                                 cudaStream_t stream);
+cudaError_t run_paged_stream_d128(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct,
+                                  cudaStream_t stream);
+cudaError_t run_paged_stream_d256(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct,
+                                  cudaStream_t stream);
 // The tile kernel over its prefix_items and own_items.
 cudaError_t run_paged_tile_d64(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream);
 cudaError_t run_paged_tile_d128(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream);

@@ -3,8 +3,9 @@
 
 namespace attn {
 
-cudaError_t run_paged_stream_d128(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream) {
-    return launch_paged_stream<128>(p, prefix, direct, stream);
+cudaError_t run_paged_stream_d128(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct,
+                                 cudaStream_t stream) {
+    return launch_paged_stream<128>(m, p, prefix, own, direct, stream);
 }
 
 }  // namespace attn

@@ -16,33 +16,35 @@
 // MMA with operands in registers: tcgen05 would leave 112 of its 128 tile rows
 // empty and need the tile to be assembled in shared memory first.
 //
-// No data crosses threads on the way in.  The MMA's k index may be permuted
-// freely (both operands alike), and so may O's columns, so each thread is given
-// whole 16-byte chunks of the rows its B fragments need:
-//   S = Q K^T   thread (g, t) = (lane / 4, lane % 4) holds key rows g and 8 + g,
-//               d elements [c * 4E + t * E, + E) of them (E elements a chunk)
-//   O += P V    it holds value rows 2t, 2t+1, 2t+8, 2t+9, columns
-//               [c * 8E + g * E, + E); pairs of rows are interleaved by byte
+// Way in: 16 rows of one head of one page are contiguous, so a warp's step is a
+// few TMA boxes of 16 rows (bf16: 64 columns, e4m3: up to 128), written with the
+// 128-byte swizzle (64 for 64-byte rows) into the warp's own ring and awaited on
+// the warp's own barriers: nothing crosses warps, no thread computes addresses.
+// (A version that copied 16 bytes a thread with cp.async moved 1.5 times the
+// bytes through the L2 and kept the load/store pipe busy: 31 us against ...)
+// The MMA's k index may be permuted freely (both operands alike), and so may O's
+// columns and the keys, so each thread takes whole 16-byte chunks from the rows
+// that its B fragments need, chosen so that the 8 threads of a shared-memory
+// phase meet 8 different chunk columns of the swizzle:
+//   S = Q K^T   thread (g, t) = (lane / 4, lane % 4) reads key rows pi(g) and
+//               8 + pi(g), 16-byte chunks 4c + t;  pi(g) = g / 2 + 4 (g % 2)
+//   O += P V    value rows t, t + 4, t + 8, t + 12 (the keys pi(2t), pi(2t + 1),
+//               ..), chunks 8c + pi(g); pairs of rows are interleaved by byte
 //               permutes, which for e4m3 is part of the conversion to bf16
-// A thread copies its own chunks with cp.async into its own slots of a
-// shared-memory ring and reads them back after cp.async.wait_group: a
-// per-thread queue, STAGES - 1 steps deep, without any barrier.
 #pragma once
 
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
+#include "sm103_bulk.cuh"
 #include "sm103_ptx.cuh"
 
 namespace attn {
 
-// 16 (or 8) bytes global -> shared; nothing is read and zeros are written when
-// `valid` is false.
+// 16 bytes global -> shared; nothing is read and zeros are written when `valid`
+// is false.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -79,99 +81,215 @@ struct StreamCfg {
     static constexpr int D = D_;
     static constexpr bool FP8 = FP8_;
     static constexpr int ES = FP8 ? 1 : 2;
+    static constexpr int ROW = D * ES;                             // bytes of a row
+    static constexpr int SW = ROW >= 128 ? 128 : 64;               // swizzle span: bytes of a box row
+    static constexpr int NB = ROW / SW;                            // boxes of 16 rows
     static constexpr int E = 16 / ES;                              // elements of a K chunk
     static constexpr int KC = D / (4 * E);                         // K chunks per row and thread
-    static constexpr int VB = D * ES / 8 >= 16 ? 16 : 8;           // bytes of a V chunk
+    static constexpr int VB = ROW / 8 >= 16 ? 16 : 8;              // bytes of a V chunk
     static constexpr int VE = VB / ES;
     static constexpr int VC = D / (8 * VE);                        // V chunks per row and thread
     static constexpr int WARPS = 4;
     static constexpr int THREADS = WARPS * 32;
-    static constexpr int STEP = 16;                                // keys per warp step
-    static constexpr int K_BYTES = 2 * KC * 16 * THREADS;
-    static constexpr int V_BYTES = 4 * VC * VB * THREADS;
-    static constexpr int S_BYTES = FP8 ? 4 * 8 * THREADS : 0;      // scales: K and V, two key pairs each
-    static constexpr int STAGE_BYTES = K_BYTES + V_BYTES + S_BYTES;
+    static constexpr int TILE = 16 * ROW;                          // a step's K or V rows
+    static constexpr int SCALES = FP8 ? 128 : 0;                   // its 16 K and 16 V scales
     static constexpr int CTAS = D == 64 ? 4 : D == 128 ? 3 : FP8 ? 2 : 1;     // per SM
-    static constexpr int STAGES = D == 64 ? (FP8 ? 4 : 3) : D == 128 ? (FP8 ? 3 : 2) : 3;
-    static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+    static constexpr int STAGES = D == 64 ? (FP8 ? 5 : 3) : D == 128 ? (FP8 ? 4 : 2) : 3;
+    static constexpr int WARP_BYTES = STAGES * 2 * TILE;
+    static constexpr int RING_BYTES = WARPS * WARP_BYTES;
     static constexpr int JOIN_BYTES = WARPS * 16 * (D + 2) * 4;
-    static constexpr int SMEM_BYTES = RING_BYTES > JOIN_BYTES ? RING_BYTES : JOIN_BYTES;
+    static constexpr int MAIN_BYTES = RING_BYTES > JOIN_BYTES ? RING_BYTES : JOIN_BYTES;
+    static constexpr int SCALE_BYTES = WARPS * STAGES * SCALES;
+    static constexpr int SMEM_BYTES = 1024 + MAIN_BYTES + SCALE_BYTES + WARPS * STAGES * 16;
     static constexpr int NT = D / 8;                               // O's column tiles
     static_assert(CTAS * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory");
 };
 
-// Replaces the infinities and NaN among this thread's V chunks (value rows 2t,
-// 2t+1, 2t+8, 2t+9 of the step, those from `from` on) by 0; bit r of the result: the step's row r had
-// one.  Called by whole warps.
-template <class Cfg>
-__device__ __noinline__ uint32_t clear_nonfinite(uint8_t* sv, int t, int from) {
-    uint32_t hit = 0;
-    for (int x = 0; x < 4; ++x) {
-        const int row = 2 * t + (x & 1) + (x >> 1) * 8;
-        bool any = false;
-        if (row < from) continue;
-        for (int c = 0; c < Cfg::VC; ++c) {
-            uint32_t* at = reinterpret_cast<uint32_t*>(sv + (x * Cfg::VC + c) * Cfg::VB * Cfg::THREADS);
-            for (int y = 0; y < Cfg::VB / 4; ++y) {
-                uint32_t w = at[y];
-                if ((w & 0x7f80u) == 0x7f80u) { w &= 0xffff0000u; any = true; }
-                if ((w & 0x7f800000u) == 0x7f800000u) { w &= 0xffffu; any = true; }
-                at[y] = w;
+enum : int { SITE_STREAM_K = 0xb1, SITE_STREAM_V = 0xb2, SITE_STREAM_DRAIN = 0xb3 };
+
+// Bounded wait of a whole warp.
+__device__ __forceinline__ bool stream_wait(uint64_t* bar, uint32_t parity, unsigned long long limit, int* status,
+                                            int site) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+        const long long t0 = clock64();
+        while (!ok) {
+            ok = mbar_try_wait(bar, parity);
+            if (!ok && static_cast<unsigned long long>(clock64() - t0) > limit) {
+                atomicCAS(status, 0, site);
+                break;
             }
         }
-        if (any) hit |= 1u << row;
+        ok = __all_sync(0xffffffffu, ok);
     }
+    return ok;
+}
+
+// Byte offset of the 16-byte chunk c of row r in a step's tile.
+template <class Cfg>
+__device__ __forceinline__ uint32_t stream_chunk(int r, int c) {
+    constexpr int PER = Cfg::SW / 16;
+    const int x = Cfg::SW == 128 ? (c % PER) ^ (r & 7) : (c % PER) ^ ((r >> 1) & 3);
+    return static_cast<uint32_t>((c / PER) * (16 * Cfg::SW) + r * Cfg::SW + (x << 4));
+}
+
+// One warp's pass over a step's bf16 V rows: those from n on become 0 (stale),
+// infinities and NaN in those from `diag` on become 0; bit r of the result: row r
+// had one.
+template <class Cfg>
+__device__ __noinline__ uint32_t fix_v_step(uint8_t* tile, int n, int diag, int lane) {
+    constexpr int CPR = Cfg::ROW / 16;
+    uint32_t hit = 0;
+    for (int x = lane; x < 16 * CPR; x += 32) {
+        const int r = x / CPR;
+        if (r < n && r < diag) continue;
+        uint4* at = reinterpret_cast<uint4*>(tile + stream_chunk<Cfg>(r, x % CPR));
+        uint4 v = r < n ? *at : make_uint4(0, 0, 0, 0);
+        uint32_t* w = &v.x;
+        bool bad = false;
+        for (int y = 0; y < 4; ++y) {
+            if ((w[y] & 0x7f80u) == 0x7f80u) { w[y] &= 0xffff0000u; bad = true; }
+            if ((w[y] & 0x7f800000u) == 0x7f800000u) { w[y] &= 0xffffu; bad = true; }
+        }
+        *at = v;
+        if (bad) hit |= 1u << r;
+    }
+    fence_proxy_async_smem();              // the ring slot's next copy comes after these writes
     return __reduce_or_sync(0xffffffffu, hit);
 }
 
-// PREFIX: the rows are all sequences' rows over the shared prefix; otherwise
-// one sequence's (blockIdx.y) over its own tokens.  DIRECT: this is the only
-// part, o and lse are written; otherwise a partial result.
-template <class Cfg, bool PREFIX, bool DIRECT>
-__global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS) paged_stream_kernel(const PagedParams p) {
+// DIRECT: the own tokens are one part and there is no prefix: o and lse are
+// written; otherwise partial results.  Blocks below prefix_blocks have the
+// prefix and all sequences' rows, the others one sequence's own tokens.
+template <class Cfg, bool DIRECT>
+__global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
+    paged_stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                        const __grid_constant__ PagedParams p, const unsigned prefix_blocks) {
     constexpr int D = Cfg::D, KC = Cfg::KC, VC = Cfg::VC, NT = Cfg::NT, STAGES = Cfg::STAGES;
     constexpr bool FP8 = Cfg::FP8;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int rows = (PREFIX ? p.B : 1) * p.Nq * p.G;
-    const int tiles = (rows + 15) / 16;
-    // Row tiles of the same keys run next to one another.
-    const int tile = blockIdx.x % tiles;
-    const int kvh = blockIdx.x / tiles % p.H_kv, part = blockIdx.x / tiles / p.H_kv;
-    const int seq = PREFIX ? 0 : blockIdx.y;
+    // Permutations of the swizzled layout (see above); 64-byte rows need none.
+    constexpr bool PI = Cfg::SW == 128;
+    const int pig = PI ? (g >> 1) | ((g & 1) << 2) : g;            // K row, V chunk
+    const int ka = PI ? t : 2 * t, kb = PI ? t + 4 : 2 * t + 1;    // keys of S columns 2t, 2t + 1
+
+    unsigned x0 = blockIdx.x;
+    const bool prefix = !DIRECT && x0 < prefix_blocks;
+    if (!prefix) x0 -= prefix_blocks;
+    const int rows = (prefix ? p.B : 1) * p.Nq * p.G;
+    const unsigned tiles = (rows + 15) / 16;
+    const int parts = prefix ? p.prefix_parts : p.own_parts;
+    // Row tiles and heads of the same pages run next to one another.
+    const int tile = x0 % tiles;
+    x0 /= tiles;
+    const int kvh = x0 % p.H_kv;
+    x0 /= p.H_kv;
+    const int part = x0 % parts;
+    const int seq = prefix ? 0 : x0 / parts;
 
     // The key range.
-    int len = PREFIX ? p.prefix_len : __ldg(p.seq_lens + seq);
-    const long long room = static_cast<long long>(p.max_pages) << p.page_shift;
-    if (!PREFIX && len > room) {
-        if (tid == 0) atomicCAS(p.status, 0, SITE_PAGED_LENGTH);
-        len = static_cast<int>(room);
+    int len = prefix ? p.prefix_len : __ldg(p.seq_lens + seq);
+    if (!prefix) {
+        const long long room = static_cast<long long>(p.max_pages) << p.page_shift;
+        if (len > room) {
+            if (tid == 0) atomicCAS(p.status, 0, SITE_PAGED_LENGTH);
+            len = static_cast<int>(room);
+        }
+        len = max(len, 0);
     }
-    len = max(len, 0);
-    const int parts = PREFIX ? p.prefix_parts : p.own_parts;
-    const int chunk = max(((len + parts - 1) / parts + 63) / 64 * 64, PREFIX ? 64 : kOwnChunk);
+    const int chunk = max(((len + parts - 1) / parts + 63) / 64 * 64, kOwnChunk);
     const int k0 = static_cast<int>(min(static_cast<long long>(part) * chunk, static_cast<long long>(len)));
     const int k1 = min(k0 + chunk, len);
-    const int* table = PREFIX ? p.prefix_table : p.table + seq * p.table_stride;
+    const int* table = prefix ? p.prefix_table : p.table + seq * p.table_stride;
+
+    const int first = k0 / 16 + warp;                      // this warp's steps: first, first + 4, ...
+    const int steps_end = k0 < k1 ? (k1 + 15) / 16 : 0;    // an empty range ends at len, inside a step
+    uint8_t* ring = smem + warp * Cfg::WARP_BYTES;         // (stage, K / V, TILE)
+    float* scales = reinterpret_cast<float*>(smem + Cfg::MAIN_BYTES + warp * STAGES * Cfg::SCALES);
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + Cfg::MAIN_BYTES + Cfg::SCALE_BYTES) + warp * 2 * STAGES;
+    uint64_t* vfull = kfull + STAGES;
+    if (lane == 0) {
+        for (int s = 0; s < 2 * STAGES; ++s) mbar_init(kfull + s, 1);
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    __syncwarp();
+
+    uint32_t bad = 0;                                      // bit (step / 4) & 31: the step's page is refused
+    auto page_of = [&](int step) -> int { return step < steps_end ? __ldg(table + ((step * 16) >> p.page_shift)) : 0; };
+    auto issue_k = [&](int step, int stage, int page) {
+        if (step >= steps_end) return;
+        const bool ok = page >= 0 && page < p.num_pages;
+        const uint32_t bit = 1u << ((step >> 2) & 31);
+        bad = ok ? bad & ~bit : bad | bit;
+        if (lane == 0) {
+            if (!ok) {
+                atomicCAS(p.status, 0, SITE_PAGED_PAGE);
+                mbar_arrive(kfull + stage);
+            } else {
+                const int row = (step * 16) & ((1 << p.page_shift) - 1);
+                mbar_arrive_expect_tx(kfull + stage, Cfg::TILE + Cfg::SCALES);
+                const uint64_t pol = l2_policy_evict_first();
+                if constexpr (FP8) {
+                    const long long at = ((static_cast<long long>(page) * p.H_kv + kvh) << p.page_shift) + row;
+                    bulk_load(scales + stage * 32, p.k_scale + at, 64, kfull + stage);
+                    bulk_load(scales + stage * 32 + 16, p.v_scale + at, 64, kfull + stage);
+                }
+#pragma unroll
+                for (int b = 0; b < Cfg::NB; ++b)
+                    tma_load_4d(ring + stage * 2 * Cfg::TILE + b * 16 * Cfg::SW, &tmap_k, kfull + stage, b * (Cfg::SW / Cfg::ES),
+                                row, kvh, page, pol);
+            }
+        }
+    };
+    auto issue_v = [&](int step, int stage, int page) {
+        if (step >= steps_end) return;
+        if (lane == 0) {
+            if (page < 0 || page >= p.num_pages) {
+                mbar_arrive(vfull + stage);
+            } else {
+                const int row = (step * 16) & ((1 << p.page_shift) - 1);
+                mbar_arrive_expect_tx(vfull + stage, Cfg::TILE);
+                const uint64_t pol = l2_policy_evict_first();
+#pragma unroll
+                for (int b = 0; b < Cfg::NB; ++b)
+                    tma_load_4d(ring + (stage * 2 + 1) * Cfg::TILE + b * 16 * Cfg::SW, &tmap_v, vfull + stage,
+                                b * (Cfg::SW / Cfg::ES), row, kvh, page, pol);
+            }
+        }
+    };
+    {
+        // The first steps' pages together, then their copies.
+        int pages[STAGES];
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s) pages[s] = page_of(first + 4 * s);
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s) {
+            issue_k(first + 4 * s, s, pages[s]);
+            issue_v(first + 4 * s, s, pages[s]);
+        }
+    }
+    int next_page = page_of(first + 4 * STAGES);
 
     // This thread's two query rows: g and g + 8 of the tile.
-    int row_out[2], limit[2];      // index in q / o / the partials (-1: none); keys it sees
+    int limit[2];                  // keys it sees
     uint32_t qa[2][D / 8];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int r = tile * 16 + g + 8 * x;
-        row_out[x] = -1;
         limit[x] = 0;
         const uint4* src = nullptr;
         if (r < rows) {
             const int per = p.Nq * p.G;
-            const int b = PREFIX ? r / per : seq, i = (PREFIX ? r % per : r) / p.G, h = kvh * p.G + r % p.G;
-            row_out[x] = (b * p.Nq + i) * p.H + h;
-            limit[x] = PREFIX || !p.causal ? len : max(0, len - p.Nq + 1 + i);
+            const int b = prefix ? r / per : seq, i = (prefix ? r % per : r) / p.G, h = kvh * p.G + r % p.G;
+            limit[x] = prefix || !p.causal ? len : max(0, len - p.Nq + 1 + i);
             src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                 static_cast<long long>(row_out[x]) * D);
+                                                 ((static_cast<long long>(b) * p.Nq + i) * p.H + h) * D);
         }
+        limit[x] = min(limit[x], k1);
         // chunk c of the k permutation: elements [c * 4E + t * E, + E)
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
@@ -186,96 +304,36 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS) paged_stream_kernel(c
             }
         }
     }
-
     // From this key on some row of the tile may not see what another does.
     int diag = len;
-    if (!PREFIX && p.causal) diag = max(0, len - p.Nq + 1 + (tile * 16) / p.G);
-
-    const int first = k0 / 16 + warp;                      // this warp's steps: first, first + 4, ...
-    const int steps_end = k0 < k1 ? (k1 + 15) / 16 : 0;    // an empty range ends at len, inside a step
-    const uint32_t ring = smem_u32(smem);
-    uint32_t bad = 0;                                      // bit (step / 4) & 31: the step's page is invalid
-
-    auto page_of = [&](int step) -> int { return step < steps_end ? __ldg(table + ((step * 16) >> p.page_shift)) : 0; };
-    auto issue = [&](int step, int stage, int page) {
-        if (step < steps_end) {
-            const bool ok = page >= 0 && page < p.num_pages;
-            const uint32_t bit = 1u << ((step >> 2) & 31);
-            bad = ok ? bad & ~bit : bad | bit;
-            if (!ok && lane == 0) atomicCAS(p.status, 0, SITE_PAGED_PAGE);
-            const int key0 = step * 16;
-            const long long at = ((static_cast<long long>(ok ? page : 0) * p.H_kv + kvh) << p.page_shift) +
-                                 (key0 & ((1 << p.page_shift) - 1));
-            const int n = ok ? min(k1 - key0, 16) : 0;     // valid rows of the step
-            const uint8_t* kb = static_cast<const uint8_t*>(p.k_cache) + at * (D * Cfg::ES);
-            const uint8_t* vb = static_cast<const uint8_t*>(p.v_cache) + at * (D * Cfg::ES);
-            const uint32_t ks = ring + stage * Cfg::STAGE_BYTES + tid * 16;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int r = x * 8 + g;
-                const uint8_t* src = kb + (r < n ? r : 0) * (D * Cfg::ES) + t * 16;
-#pragma unroll
-                for (int c = 0; c < KC; ++c) cp_async16(ks + (x * KC + c) * 16 * Cfg::THREADS, src + c * 64, r < n);
-            }
-            const uint32_t vs = ring + stage * Cfg::STAGE_BYTES + Cfg::K_BYTES + tid * Cfg::VB;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int r = 2 * t + (x & 1) + (x >> 1) * 8;
-                const uint8_t* src = vb + (r < n ? r : 0) * (D * Cfg::ES) + g * Cfg::VB;
-#pragma unroll
-                for (int c = 0; c < VC; ++c) {
-                    const uint32_t dst = vs + (x * VC + c) * Cfg::VB * Cfg::THREADS;
-                    if constexpr (Cfg::VB == 16) cp_async16(dst, src + c * 128, r < n);
-                    else cp_async8(dst, src + c * 64, r < n);
-                }
-            }
-            if constexpr (FP8) {
-                // Scales of keys 2t, 2t+1 and 2t+8, 2t+9.  Rows past n are
-                // never used (their scores are masked); the pair stays inside
-                // the page.
-                const uint32_t ss = ring + stage * Cfg::STAGE_BYTES + Cfg::K_BYTES + Cfg::V_BYTES + tid * 8;
-                cp_async8(ss, p.k_scale + at + 2 * t, 2 * t < n);
-                cp_async8(ss + 8 * Cfg::THREADS, p.k_scale + at + 2 * t + 8, 2 * t + 8 < n);
-                cp_async8(ss + 16 * Cfg::THREADS, p.v_scale + at + 2 * t, 2 * t < n);
-                cp_async8(ss + 24 * Cfg::THREADS, p.v_scale + at + 2 * t + 8, 2 * t + 8 < n);
-            }
-        }
-        cp_async_commit();
-    };
+    if (!prefix && p.causal) diag = max(0, len - p.Nq + 1 + (tile * 16) / p.G);
+    // Steps that reach it (or the range's end) are masked key by key.
+    const int plain_end = min(diag, k1);
 
     float o[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
 
-    int next_page = page_of(first);
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-        const int step = first + 4 * s;
-        const int page = next_page;
-        next_page = page_of(step + 4);
-        issue(step, s, page);
-    }
     int stage = 0;
-    for (int step = first; step < steps_end; step += 4) {
-        {
-            const int ahead = step + 4 * (STAGES - 1);
-            const int page = next_page;
-            next_page = page_of(ahead + 4);
-            issue(ahead, stage == 0 ? STAGES - 1 : stage - 1, page);
-        }
-        cp_async_wait<STAGES - 1>();
-        const uint8_t* st = smem + stage * Cfg::STAGE_BYTES;
-        stage = stage + 1 == STAGES ? 0 : stage + 1;
+    uint32_t parity = 0;
+    bool ok = true, ahead = false;         // ahead: this step's slot has the K of the next round
+    int step = first;
+    for (; step < steps_end; step += 4) {
+        const int page = next_page;
+        next_page = page_of(step + 4 * (STAGES + 1));
+        if (!(ok = stream_wait(kfull + stage, parity, p.wait_limit, p.status, SITE_STREAM_K))) break;
+        const uint8_t* st = ring + stage * 2 * Cfg::TILE;
 
         // ---------------------------------------------------------- S = Q K^T
         float s[2][4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.0f;
+        for (int x = 0; x < 2; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.0f;
 #pragma unroll
-            for (int c = 0; c < KC; ++c) {
-                const uint4 kk = *reinterpret_cast<const uint4*>(st + (x * KC + c) * 16 * Cfg::THREADS + tid * 16);
+        for (int c = 0; c < KC; ++c) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint4 kk = *reinterpret_cast<const uint4*>(st + stream_chunk<Cfg>(x * 8 + pig, c * 4 + t));
                 if constexpr (FP8) {
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
@@ -291,37 +349,53 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS) paged_stream_kernel(c
                 }
             }
         }
-        // s[x][0..1]: row g, keys x * 8 + 2t, + 1; s[x][2..3]: row g + 8.
-        float2 vscale[2];
-        const uint8_t* sc = st + Cfg::K_BYTES + Cfg::V_BYTES + tid * 8;
+        // s[x][0..1]: row g, keys x * 8 + ka, x * 8 + kb; s[x][2..3]: row g + 8.
         const bool skip = (bad >> ((step >> 2) & 31)) & 1u;
+        const bool special = skip || step * 16 + 16 > plain_end;
+        float2 vscale[2];
+        const float* sc = scales + stage * 32;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             float2 mul = make_float2(p.scale_log2, p.scale_log2);
             if constexpr (FP8) {
-                const float2 ks = *reinterpret_cast<const float2*>(sc + x * 8 * Cfg::THREADS);
-                vscale[x] = *reinterpret_cast<const float2*>(sc + (2 + x) * 8 * Cfg::THREADS);
-                mul.x *= ks.x;
-                mul.y *= ks.y;
+                mul.x *= sc[x * 8 + ka];
+                mul.y *= sc[x * 8 + kb];
+                vscale[x] = make_float2(sc[16 + x * 8 + ka], sc[16 + x * 8 + kb]);
             }
-            const int key = step * 16 + x * 8 + 2 * t;
-            // A masked score is -inf whatever was read for it.
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int lim = skip ? 0 : min(limit[r], k1);
-                s[x][2 * r] = key < lim ? s[x][2 * r] * mul.x : -INFINITY;
-                s[x][2 * r + 1] = key + 1 < lim ? s[x][2 * r + 1] * mul.y : -INFINITY;
+                s[x][2 * r] *= mul.x;
+                s[x][2 * r + 1] *= mul.y;
+            }
+        }
+        __syncwarp();
+        if constexpr (!FP8) {
+            issue_k(step + 4 * STAGES, stage, page);       // K's slot is free
+            ahead = step + 4 * STAGES < steps_end;
+        }
+        if (special) {
+            // A masked score is -inf whatever was read for it.
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int key = step * 16 + x * 8;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int lim = skip ? 0 : limit[r];
+                    if (key + ka >= lim) s[x][2 * r] = -INFINITY;
+                    if (key + kb >= lim) s[x][2 * r + 1] = -INFINITY;
+                }
             }
         }
         // ------------------------------------------------------ running maximum
-        // The reference moves only when some score exceeds it by more than 8
-        // (log2 units), so that the quad's shuffles and O's rescaling are rare;
-        // O and l share the reference, so the result does not depend on it.
-        const float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        const float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-        const bool move = x0 > m[0] + 8.0f || x1 > m[1] + 8.0f;
+        // A row's reference moves only when a score of the row exceeds it by
+        // more than 8 (log2 units), so that the quad's shuffles and O's
+        // rescaling are rare; O and l share the reference, so the result does
+        // not depend on it.
+        const float t0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        const float t1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        const bool move = t0 > m[0] + 8.0f || t1 > m[1] + 8.0f;
         if (__any_sync(0xffffffffu, move)) {
-            float mx[2] = {x0, x1};
+            float mx[2] = {t0, t1};
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
@@ -348,30 +422,39 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS) paged_stream_kernel(c
             l[0] += s[x][0] + s[x][1];
             l[1] += s[x][2] + s[x][3];
             if constexpr (FP8) {
-                // V's row scale rides on P; l sums the plain probabilities.
-                // A weight of 0 stays 0 beside a NaN scale: a row that does not
+                // V's row scale rides on P; l sums the plain probabilities.  A
+                // weight of 0 stays 0 beside a NaN scale: a row that does not
                 // see the key must not notice it.
-                s[x][0] = s[x][0] == 0.0f ? 0.0f : s[x][0] * vscale[x].x;
-                s[x][1] = s[x][1] == 0.0f ? 0.0f : s[x][1] * vscale[x].y;
-                s[x][2] = s[x][2] == 0.0f ? 0.0f : s[x][2] * vscale[x].x;
-                s[x][3] = s[x][3] == 0.0f ? 0.0f : s[x][3] * vscale[x].y;
+                if (special) {
+                    s[x][0] = s[x][0] == 0.0f ? 0.0f : s[x][0] * vscale[x].x;
+                    s[x][1] = s[x][1] == 0.0f ? 0.0f : s[x][1] * vscale[x].y;
+                    s[x][2] = s[x][2] == 0.0f ? 0.0f : s[x][2] * vscale[x].x;
+                    s[x][3] = s[x][3] == 0.0f ? 0.0f : s[x][3] * vscale[x].y;
+                } else {
+                    s[x][0] *= vscale[x].x;
+                    s[x][1] *= vscale[x].y;
+                    s[x][2] *= vscale[x].x;
+                    s[x][3] *= vscale[x].y;
+                }
             }
         }
-        // P is rounded to bf16 for the product (relative 2^-9 at most per
+        // P is rounded to bf16 for the product (relative 2^-8 at most per
         // weight, as the dense forward does); l keeps the unrounded values.
         const uint32_t a0 = pack_bf16x2(s[0][0], s[0][1]), a1 = pack_bf16x2(s[0][2], s[0][3]);
         const uint32_t a2 = pack_bf16x2(s[1][0], s[1][1]), a3 = pack_bf16x2(s[1][2], s[1][3]);
         // ---------------------------------------------------------- O += P V
-        const uint8_t* sv = st + Cfg::K_BYTES + tid * Cfg::VB;
-        if constexpr (!FP8 && !PREFIX) {
-            // 0 * NaN is NaN: where rows of the tile see different keys, a
-            // non-finite value is taken out of the product and the rows that
-            // do see its key become NaN as a whole.
-            if (diag < len && step * 16 + 16 > diag) {
-                const uint32_t hit = clear_nonfinite<Cfg>(const_cast<uint8_t*>(sv), t, diag - step * 16);
+        if (!(ok = stream_wait(vfull + stage, parity, p.wait_limit, p.status, SITE_STREAM_V))) break;
+        const uint8_t* sv = st + Cfg::TILE;
+        if constexpr (!FP8) {
+            // 0 * NaN is NaN: stale rows become 0, and where rows of the tile see
+            // different keys a non-finite value is taken out of the product and
+            // the rows that do see its key become NaN as a whole.
+            if (special) {
+                const uint32_t hit = fix_v_step<Cfg>(ring + (stage * 2 + 1) * Cfg::TILE, skip ? 0 : k1 - step * 16,
+                                                     diag - step * 16, lane);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int n = min(max(min(limit[r], k1) - step * 16, 0), 16);
+                    const int n = min(max(limit[r] - step * 16, 0), 16);
                     if (hit & ((1u << n) - 1u)) l[r] = __uint_as_float(0x7fc00000u);
                 }
             }
@@ -381,15 +464,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS) paged_stream_kernel(c
             uint32_t w[4][Cfg::VB / 4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const uint8_t* at = sv + (x * VC + c) * Cfg::VB * Cfg::THREADS;
+                const int r = (x & 1 ? kb : ka) + (x >> 1) * 8;
                 if constexpr (Cfg::VB == 16) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(at);
+                    const uint4 v = *reinterpret_cast<const uint4*>(sv + stream_chunk<Cfg>(r, c * 8 + pig));
                     w[x][0] = v.x;
                     w[x][1] = v.y;
                     w[x][Cfg::VB / 4 - 2] = v.z;
                     w[x][Cfg::VB / 4 - 1] = v.w;
                 } else {
-                    const uint2 v = *reinterpret_cast<const uint2*>(at);
+                    const uint2 v = *reinterpret_cast<const uint2*>(sv + stream_chunk<Cfg>(r, g >> 1) + (g & 1) * 8);
                     w[x][0] = v.x;
                     w[x][1] = v.y;
                 }
@@ -414,11 +497,31 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS) paged_stream_kernel(c
                 }
             }
         }
+        __syncwarp();
+        // (e4m3: K's slot also holds the scales, read until here)
+        if constexpr (FP8) issue_k(step + 4 * STAGES, stage, page);
+        issue_v(step + 4 * STAGES, stage, page);
+        ahead = false;
+        if (++stage == STAGES) {
+            stage = 0;
+            parity ^= 1;
+        }
     }
-    cp_async_wait<0>();
+    if (!ok) {
+        // A wait ran out: whatever copy is in flight lands before the CTA leaves.
+        for (int s = 0; s < STAGES; ++s) {
+            const int at = step + 4 * s;
+            if (at >= steps_end) break;
+            const int x = (stage + s) % STAGES;
+            const uint32_t ph = parity ^ (stage + s >= STAGES ? 1u : 0u);
+            stream_wait(kfull + x, ph, 2000000000ull, p.status, SITE_STREAM_DRAIN);
+            stream_wait(vfull + x, ph, 2000000000ull, p.status, SITE_STREAM_DRAIN);
+        }
+        if (ahead) stream_wait(kfull + stage, parity ^ 1u, 2000000000ull, p.status, SITE_STREAM_DRAIN);
+    }
 
     // ------------------------------------------------------------ join the warps
-    // o[c * VE + e][2r + z] is row g + 8r, column c * 8 * VE + (2t + z) * VE + e.
+    // o[c * VE + e][2r + z] is row g + 8r, column (8c + pi(2t + z)) * VE + e.
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -437,7 +540,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS) paged_stream_kernel(c
             for (int z = 0; z < 2; ++z)
 #pragma unroll
                 for (int e = 0; e < Cfg::VE; e += 4)
-                    *reinterpret_cast<float4*>(dst + c * 8 * Cfg::VE + (2 * t + z) * Cfg::VE + e) =
+                    *reinterpret_cast<float4*>(dst + (c * 8 + (z ? kb : ka)) * Cfg::VE + e) =
                         make_float4(o[c * Cfg::VE + e][2 * r + z], o[c * Cfg::VE + e + 1][2 * r + z],
                                     o[c * Cfg::VE + e + 2][2 * r + z], o[c * Cfg::VE + e + 3][2 * r + z]);
         if (t == 0) {
@@ -452,7 +555,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS) paged_stream_kernel(c
         const int r = tile * 16 + rr;
         if (r >= rows) continue;
         const int per = p.Nq * p.G;
-        const int b = PREFIX ? r / per : seq, i = (PREFIX ? r % per : r) / p.G, h = kvh * p.G + r % p.G;
+        const int b = prefix ? r / per : seq, i = (prefix ? r % per : r) / p.G, h = kvh * p.G + r % p.G;
         const long long out = (static_cast<long long>(b) * p.Nq + i) * p.H + h;
         float mm = jm[rr];
 #pragma unroll
@@ -482,7 +585,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS) paged_stream_kernel(c
                 make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
             if (c4 == 0) p.lse[(static_cast<long long>(b) * p.H + h) * p.Nq + i] = lse2 * 0.69314718055994530942f;
         } else {
-            const long long pr = static_cast<long long>(PREFIX ? part : p.prefix_parts + part) *
+            const long long pr = static_cast<long long>(prefix ? part : p.prefix_parts + part) *
                                      (static_cast<long long>(p.B) * p.Nq * p.H) + out;
             // An empty part's O is not read by the join.
             if (lse2 != -INFINITY) reinterpret_cast<float4*>(p.part_o + pr * D)[c4] = acc;

@@ -5,30 +5,32 @@
 
 namespace attn {
 
-template <class Cfg, bool PREFIX, bool DIRECT>
-cudaError_t launch_paged_stream_one(const PagedParams& p, cudaStream_t stream) {
-    auto kernel = paged_stream_kernel<Cfg, PREFIX, DIRECT>;
-    // Per function and per device; cheap and idempotent.
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+template <class Cfg, bool DIRECT>
+cudaError_t launch_paged_stream_one(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, cudaStream_t stream) {
+    auto kernel = paged_stream_kernel<Cfg, DIRECT>;
+    static std::atomic<unsigned long long> ready{0};
+    cudaError_t e = once_per_device(ready, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    });
     if (e != cudaSuccess) return e;
-    const unsigned tiles = ((PREFIX ? p.B : 1) * p.Nq * p.G + 15) / 16;
-    const dim3 grid(tiles * p.H_kv * (PREFIX ? p.prefix_parts : p.own_parts), PREFIX ? 1 : p.B);
-    kernel<<<grid, Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(p);
+    const unsigned per = p.Nq * p.G;
+    const unsigned prefix_blocks = prefix ? (p.B * per + 15) / 16 * p.H_kv * p.prefix_parts : 0;
+    const unsigned own_blocks = own ? (per + 15) / 16 * p.H_kv * p.own_parts * p.B : 0;
+    kernel<<<prefix_blocks + own_blocks, Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(m.k, m.v, p, prefix_blocks);
     return cudaGetLastError();
 }
 
 template <int D>
-cudaError_t launch_paged_stream(const PagedParams& p, bool prefix, bool direct, cudaStream_t stream) {
+cudaError_t launch_paged_stream(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct,
+                                cudaStream_t stream) {
     if (p.fp8) {
         using C = StreamCfg<D, true>;
-        if (prefix) return launch_paged_stream_one<C, true, false>(p, stream);
-        return direct ? launch_paged_stream_one<C, false, true>(p, stream)
-                      : launch_paged_stream_one<C, false, false>(p, stream);
+        return direct ? launch_paged_stream_one<C, true>(m, p, prefix, own, stream)
+                      : launch_paged_stream_one<C, false>(m, p, prefix, own, stream);
     }
     using C = StreamCfg<D, false>;
-    if (prefix) return launch_paged_stream_one<C, true, false>(p, stream);
-    return direct ? launch_paged_stream_one<C, false, true>(p, stream)
-                  : launch_paged_stream_one<C, false, false>(p, stream);
+    return direct ? launch_paged_stream_one<C, true>(m, p, prefix, own, stream)
+                  : launch_paged_stream_one<C, false>(m, p, prefix, own, stream);
 }
 
 }  // namespace attn

@@ -8,15 +8,17 @@ namespace attn {
 template <class Cfg, bool DIRECT>
 cudaError_t launch_paged_tile_one(const PagedMaps& m, const PagedParams& p, cudaStream_t stream) {
     auto kernel = paged_tile_kernel<Cfg, DIRECT>;
-    // The register split (setmaxnreg) assumes exactly LAUNCH_REGS registers a
-    // thread at launch; another count could make the increase wait forever, so
-    // such a build is refused.
-    cudaFuncAttributes attr;
-    cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs != Cfg::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
-    // Per function and per device; cheap and idempotent.
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    static std::atomic<unsigned long long> ready{0};
+    cudaError_t e = once_per_device(ready, [&] {
+        // The register split (setmaxnreg) assumes exactly LAUNCH_REGS registers
+        // a thread at launch; another count could make the increase wait
+        // forever, so such a build is refused.
+        cudaFuncAttributes attr;
+        cudaError_t r = cudaFuncGetAttributes(&attr, kernel);
+        if (r != cudaSuccess) return r;
+        if (attr.numRegs != Cfg::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    });
     if (e != cudaSuccess) return e;
     kernel<<<p.prefix_items + p.own_items, Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(m.k, m.v, p);
     return cudaGetLastError();
