@@ -30,7 +30,7 @@
 //               8 + pi(g), 16-byte chunks 4c + t;  pi(g) = g / 2 + 4 (g % 2)
 //   O += P V    value rows t, t + 4, t + 8, t + 12 (the keys pi(2t), pi(2t + 1),
 //               ..), chunks 8c + pi(g); pairs of rows are interleaved by byte
-//               permutes, which for e4m3 is part of the conversion to bf16
+//               permutes
 #pragma once
 
 #include <cuda_bf16.h>
@@ -61,19 +61,71 @@ __device__ __forceinline__ void mma_m16n8k16(float* d, uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 codes -> two bf16, exactly.  sel picks [code, sign, code, sign]
-// bytes (the sign byte by the permute's sign replication); shifted left by 4,
-// code bit 7 (and its copies) reach bit 15 and the exponent and mantissa bits
-// 10..4, i.e. a bf16 of value 2^-120 times the code's; the product with 2^120
-// is exact, subnormal codes included (they are subnormal bf16 before it).  A
-// NaN code becomes +-480: such rows have a NaN scale, which decides.
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t a, uint32_t b) {
-    uint32_t x, r;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(x) : "r"(a), "r"(b), "n"(SEL));
-    x = (x << 4) & 0x87f087f0u;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0x7b807b80u));
+// The same with fp16 operands.
+__device__ __forceinline__ void mma_m16n8k16_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                 uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An e4m3 cache is multiplied in fp16.  e4m3 values are fp16 values, and one
+// instruction converts two codes (to bf16 it takes four, which bounded the
+// kernels: 3.5 TB/s).  The other operands are brought into fp16's range by exact
+// powers of two:
+//   q    per row, so that its largest element lies in [2^14, 2^15): every bf16
+//        element down to 2^-31 of the largest is then exact
+//   P    times V's row scale / vref, a power of two that follows the scales and
+//        keeps the product below 2^15; rounded once to fp16 (2^-11; below 2^-14,
+//        2^-25 absolute)
+__device__ __forceinline__ uint32_t f16x2_of_lo(uint32_t codes) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(codes));
     return r;
+}
+__device__ __forceinline__ uint32_t f16x2_of_hi(uint32_t codes) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(codes));
+    return r;
+}
+
+// 2^n as a float, n in [-126, 127].
+__device__ __forceinline__ float pow2f(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
+
+// The power of two that brings a row of largest magnitude `bits` (bf16 bits)
+// into fp16's range, as its exponent: 0 for rows of zeros or with an infinity or
+// a NaN (which stay what they are).
+__device__ __forceinline__ int q_shift(uint32_t bits) {
+    const int e = static_cast<int>(bits >> 7);
+    if (e == 255 || bits == 0) return 0;
+    return max(-126, min(126, 141 - max(e, 1)));
+}
+
+// Eight bf16 times a power of two -> eight fp16.
+__device__ __forceinline__ uint4 q_to_f16(const uint4& v, float factor) {
+    uint4 r;
+    const uint32_t* in = &v.x;
+    uint32_t* out = &r.x;
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+        out[y] = pack_f16x2(__uint_as_float(in[y] << 16) * factor, __uint_as_float(in[y] & 0xffff0000u) * factor);
+    return r;
+}
+
+// The largest magnitude of eight bf16, as bf16 bits (unsigned comparison orders
+// finite < inf < NaN).
+__device__ __forceinline__ uint32_t bf16x8_amax(const uint4& v) {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs));
+    return max(m & 0xffffu, m >> 16);
+}
+
+// vref for a largest V scale vm: 2^4 below it, so that P vs / vref is at most
+// 2^8 * 2^5 until a scale is more than 2^2 above it (then vref moves).
+__device__ __forceinline__ float vref_of(float vm) {
+    const int e = static_cast<int>(__float_as_uint(vm) >> 23) - 127;
+    return pow2f(max(-126, min(120, e - 4)));
 }
 
 template <int D_, bool FP8_>
@@ -93,14 +145,18 @@ struct StreamCfg {
     static constexpr int THREADS = WARPS * 32;
     static constexpr int TILE = 16 * ROW;                          // a step's K or V rows
     static constexpr int SCALES = FP8 ? 128 : 0;                   // its 16 K and 16 V scales
-    static constexpr int CTAS = D == 64 ? 4 : D == 128 ? 3 : FP8 ? 2 : 1;     // per SM
-    static constexpr int STAGES = D == 64 ? (FP8 ? 5 : 3) : D == 128 ? (FP8 ? 4 : 2) : 3;
+    // e4m3 steps are bound by instructions (the conversion) and their latency:
+    // the query fragments stay in shared memory, which leaves room for one more
+    // CTA an SM.
+    static constexpr int CTAS = D == 64 ? (FP8 ? 5 : 4) : D == 128 ? (FP8 ? 4 : 3) : FP8 ? 2 : 1;     // per SM
+    static constexpr int STAGES = D == 64 ? (FP8 ? 4 : 3) : D == 128 ? (FP8 ? 3 : 2) : 3;
+    static constexpr int Q_BYTES = FP8 ? 16 * D * 2 : 0;
     static constexpr int WARP_BYTES = STAGES * 2 * TILE;
     static constexpr int RING_BYTES = WARPS * WARP_BYTES;
     static constexpr int JOIN_BYTES = WARPS * 16 * (D + 2) * 4;
     static constexpr int MAIN_BYTES = RING_BYTES > JOIN_BYTES ? RING_BYTES : JOIN_BYTES;
     static constexpr int SCALE_BYTES = WARPS * STAGES * SCALES;
-    static constexpr int SMEM_BYTES = 1024 + MAIN_BYTES + SCALE_BYTES + WARPS * STAGES * 16;
+    static constexpr int SMEM_BYTES = 1024 + MAIN_BYTES + SCALE_BYTES + Q_BYTES + WARPS * STAGES * 16;
     static constexpr int NT = D / 8;                               // O's column tiles
     static_assert(CTAS * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory");
 };
@@ -133,7 +189,7 @@ __device__ __forceinline__ uint32_t stream_chunk(int r, int c) {
     return static_cast<uint32_t>((c / PER) * (16 * Cfg::SW) + r * Cfg::SW + (x << 4));
 }
 
-// One warp's pass over a step's bf16 V rows: those from n on become 0 (stale),
+// One warp's pass over a step's V rows: those from n on become 0 (stale),
 // infinities and NaN in those from `diag` on become 0; bit r of the result: row r
 // had one.
 template <class Cfg>
@@ -148,13 +204,20 @@ __device__ __noinline__ uint32_t fix_v_step(uint8_t* tile, int n, int diag, int 
         uint32_t* w = &v.x;
         bool bad = false;
         for (int y = 0; y < 4; ++y) {
-            if ((w[y] & 0x7f80u) == 0x7f80u) { w[y] &= 0xffff0000u; bad = true; }
-            if ((w[y] & 0x7f800000u) == 0x7f800000u) { w[y] &= 0xffffu; bad = true; }
+            if constexpr (Cfg::FP8) {
+                const uint32_t nan = __vcmpeq4(w[y] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                w[y] &= ~nan;
+                bad |= nan != 0;
+            } else {
+                if ((w[y] & 0x7f80u) == 0x7f80u) { w[y] &= 0xffff0000u; bad = true; }
+                if ((w[y] & 0x7f800000u) == 0x7f800000u) { w[y] &= 0xffffu; bad = true; }
+            }
         }
         *at = v;
         if (bad) hit |= 1u << r;
     }
     fence_proxy_async_smem();              // the ring slot's next copy comes after these writes
+    __syncwarp();
     return __reduce_or_sync(0xffffffffu, hit);
 }
 
@@ -209,7 +272,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     const int steps_end = k0 < k1 ? (k1 + 15) / 16 : 0;    // an empty range ends at len, inside a step
     uint8_t* ring = smem + warp * Cfg::WARP_BYTES;         // (stage, K / V, TILE)
     float* scales = reinterpret_cast<float*>(smem + Cfg::MAIN_BYTES + warp * STAGES * Cfg::SCALES);
-    uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + Cfg::MAIN_BYTES + Cfg::SCALE_BYTES) + warp * 2 * STAGES;
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + Cfg::MAIN_BYTES + Cfg::SCALE_BYTES + Cfg::Q_BYTES) +
+                      warp * 2 * STAGES;
     uint64_t* vfull = kfull + STAGES;
     if (lane == 0) {
         for (int s = 0; s < 2 * STAGES; ++s) mbar_init(kfull + s, 1);
@@ -274,13 +338,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     }
     int next_page = page_of(first + 4 * STAGES);
 
-    // This thread's two query rows: g and g + 8 of the tile.
+    // This thread's two query rows: g and g + 8 of the tile.  Its fragments are
+    // chunk c of the k permutation, elements [c * 4E + t * E, + E) of each.
     int limit[2];                  // keys it sees
+    float to_log2[2];              // raw score -> log2 units
     uint32_t qa[2][D / 8];
+    uint4* sq = reinterpret_cast<uint4*>(smem + Cfg::MAIN_BYTES + Cfg::SCALE_BYTES) + lane;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int r = tile * 16 + g + 8 * x;
         limit[x] = 0;
+        to_log2[x] = p.scale_log2;
         const uint4* src = nullptr;
         if (r < rows) {
             const int per = p.Nq * p.G;
@@ -290,19 +358,39 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                                                  ((static_cast<long long>(b) * p.Nq + i) * p.H + h) * D);
         }
         limit[x] = min(limit[x], k1);
-        // chunk c of the k permutation: elements [c * 4E + t * E, + E)
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
 #pragma unroll
             for (int y = 0; y < Cfg::E / 8; ++y) {
+                const int at = c * (Cfg::E / 8) + y;
                 const uint4 v = src ? __ldg(src + (c * 4 + t) * (Cfg::E / 8) + y) : make_uint4(0, 0, 0, 0);
-                const int at = (c * (Cfg::E / 8) + y) * 4;
-                qa[x][at] = v.x;
-                qa[x][at + 1] = v.y;
-                qa[x][at + 2] = v.z;
-                qa[x][at + 3] = v.w;
+                qa[x][at * 4] = v.x;
+                qa[x][at * 4 + 1] = v.y;
+                qa[x][at * 4 + 2] = v.z;
+                qa[x][at * 4 + 3] = v.w;
             }
         }
+    }
+    if constexpr (FP8) {
+        // To fp16, into shared memory as (chunk half, row half, lane); each warp
+        // writes a quarter.
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int at = 0; at < D / 32; ++at)
+                top = max(top, bf16x8_amax(make_uint4(qa[x][at * 4], qa[x][at * 4 + 1], qa[x][at * 4 + 2], qa[x][at * 4 + 3])));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int shift = q_shift(top);
+            to_log2[x] *= pow2f(-shift);
+#pragma unroll
+            for (int at = 0; at < D / 32; ++at) {
+                if (at % Cfg::WARPS != warp) continue;
+                sq[(at * 2 + x) * 32] = q_to_f16(make_uint4(qa[x][at * 4], qa[x][at * 4 + 1], qa[x][at * 4 + 2], qa[x][at * 4 + 3]), pow2f(shift));
+            }
+        }
+        __syncthreads();
     }
     // From this key on some row of the tile may not see what another does.
     int diag = len;
@@ -314,6 +402,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 #pragma unroll
     for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float vref = FP8 ? 0.0f : 1.0f;
 
     int stage = 0;
     uint32_t parity = 0;
@@ -331,18 +420,28 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         for (int x = 0; x < 2; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.0f;
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
+            if constexpr (FP8) {
+                uint4 k4[2], q0[2], q1[2];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const uint4 kk = *reinterpret_cast<const uint4*>(st + stream_chunk<Cfg>(x * 8 + pig, c * 4 + t));
-                if constexpr (FP8) {
+                for (int x = 0; x < 2; ++x) {
+                    k4[x] = *reinterpret_cast<const uint4*>(st + stream_chunk<Cfg>(x * 8 + pig, c * 4 + t));
+                    q0[x] = sq[((c * 2 + x) * 2) * 32];            // row g, half x of the chunk
+                    q1[x] = sq[((c * 2 + x) * 2 + 1) * 32];        // row g + 8
+                }
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t word = w == 0 ? kk.x : w == 1 ? kk.y : w == 2 ? kk.z : kk.w;
-                        const int at = c * 8 + w * 2;
-                        mma_m16n8k16(s[x], qa[0][at], qa[1][at], qa[0][at + 1], qa[1][at + 1],
-                                     e4m3_pair<0x9180>(word, 0), e4m3_pair<0xb3a2>(word, 0));
+                for (int w = 0; w < 4; ++w) {
+                    const uint4 qg = q0[w >> 1], qh = q1[w >> 1];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t word = w == 0 ? k4[x].x : w == 1 ? k4[x].y : w == 2 ? k4[x].z : k4[x].w;
+                        mma_m16n8k16_f16(s[x], w & 1 ? qg.z : qg.x, w & 1 ? qh.z : qh.x, w & 1 ? qg.w : qg.y,
+                                         w & 1 ? qh.w : qh.y, f16x2_of_lo(word), f16x2_of_hi(word));
                     }
-                } else {
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const uint4 kk = *reinterpret_cast<const uint4*>(st + stream_chunk<Cfg>(x * 8 + pig, c * 4 + t));
                     const int at = c * 4;
                     mma_m16n8k16(s[x], qa[0][at], qa[1][at], qa[0][at + 1], qa[1][at + 1], kk.x, kk.y);
                     mma_m16n8k16(s[x], qa[0][at + 2], qa[1][at + 2], qa[0][at + 3], qa[1][at + 3], kk.z, kk.w);
@@ -356,16 +455,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         const float* sc = scales + stage * 32;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            float2 mul = make_float2(p.scale_log2, p.scale_log2);
+            float2 mul = make_float2(1.0f, 1.0f);
             if constexpr (FP8) {
-                mul.x *= sc[x * 8 + ka];
-                mul.y *= sc[x * 8 + kb];
+                mul = make_float2(sc[x * 8 + ka], sc[x * 8 + kb]);
                 vscale[x] = make_float2(sc[16 + x * 8 + ka], sc[16 + x * 8 + kb]);
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                s[x][2 * r] *= mul.x;
-                s[x][2 * r + 1] *= mul.y;
+                s[x][2 * r] *= mul.x * to_log2[r];
+                s[x][2 * r + 1] *= mul.y * to_log2[r];
             }
         }
         __syncwarp();
@@ -384,6 +482,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                     if (key + ka >= lim) s[x][2 * r] = -INFINITY;
                     if (key + kb >= lim) s[x][2 * r + 1] = -INFINITY;
                 }
+                if constexpr (FP8) {
+                    const int lim = skip ? 0 : k1;             // scales of rows that are not there
+                    if (key + ka >= lim) vscale[x].x = 0.0f;
+                    if (key + kb >= lim) vscale[x].y = 0.0f;
+                }
             }
         }
         // ------------------------------------------------------ running maximum
@@ -393,9 +496,24 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         // not depend on it.
         const float t0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
         const float t1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-        const bool move = t0 > m[0] + 8.0f || t1 > m[1] + 8.0f;
+        bool move = t0 > m[0] + 8.0f || t1 > m[1] + 8.0f;
+        float vm = 0.0f;
+        if constexpr (FP8) {
+            vm = fmaxf(fmaxf(vscale[0].x, vscale[0].y), fmaxf(vscale[1].x, vscale[1].y));
+            move = move || vm > 64.0f * vref;
+        }
         if (__any_sync(0xffffffffu, move)) {
             float mx[2] = {t0, t1};
+            float vfall = 1.0f;
+            if constexpr (FP8) {
+                // V scales are never negative: their bits order them.
+                vm = __uint_as_float(__reduce_max_sync(0xffffffffu, vm > 0.0f ? __float_as_uint(vm) : 0u));
+                if (vm > 64.0f * vref) {
+                    const float to = vref_of(vm);
+                    vfall = vref * (1.0f / to);                // (O is 0 while vref is)
+                    vref = to;
+                }
+            }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
@@ -405,14 +523,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 const float a = mn == m[r] ? 1.0f : ex2_approx(m[r] - mn);
                 m[r] = mn;
                 l[r] *= a;
+                const float ao = FP8 ? a * vfall : a;
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    o[j][2 * r] *= a;
-                    o[j][2 * r + 1] *= a;
+                    o[j][2 * r] *= ao;
+                    o[j][2 * r + 1] *= ao;
                 }
             }
         }
         const float n0 = m[0] == -INFINITY ? 0.0f : m[0], n1 = m[1] == -INFINITY ? 0.0f : m[1];
+        if constexpr (FP8) {
+            const float iv = vref == 0.0f ? 0.0f : 1.0f / vref;        // a power of two
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                vscale[x].x *= iv;
+                vscale[x].y *= iv;
+            }
+        }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             s[x][0] = ex2_approx(s[x][0] - n0);
@@ -439,13 +566,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             }
         }
         // P is rounded to bf16 for the product (relative 2^-8 at most per
-        // weight, as the dense forward does); l keeps the unrounded values.
-        const uint32_t a0 = pack_bf16x2(s[0][0], s[0][1]), a1 = pack_bf16x2(s[0][2], s[0][3]);
-        const uint32_t a2 = pack_bf16x2(s[1][0], s[1][1]), a3 = pack_bf16x2(s[1][2], s[1][3]);
+        // weight, as the dense forward does; e4m3 cache: fp16, see above); l keeps
+        // the unrounded values.
+        auto pack = [](float a, float b) { return FP8 ? pack_f16x2(a, b) : pack_bf16x2(a, b); };
+        const uint32_t a0 = pack(s[0][0], s[0][1]), a1 = pack(s[0][2], s[0][3]);
+        const uint32_t a2 = pack(s[1][0], s[1][1]), a3 = pack(s[1][2], s[1][3]);
         // ---------------------------------------------------------- O += P V
         if (!(ok = stream_wait(vfull + stage, parity, p.wait_limit, p.status, SITE_STREAM_V))) break;
         const uint8_t* sv = st + Cfg::TILE;
-        if constexpr (!FP8) {
+        {
             // 0 * NaN is NaN: stale rows become 0, and where rows of the tile see
             // different keys a non-finite value is taken out of the product and
             // the rows that do see its key become NaN as a whole.
@@ -481,14 +610,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             for (int y = 0; y < Cfg::VB / 4; ++y) {
                 float(*oo)[4] = &o[c * Cfg::VE + y * (4 / Cfg::ES)];
                 if constexpr (FP8) {
-                    mma_m16n8k16(oo[0], a0, a1, a2, a3, e4m3_pair<0xc480>(w[0][y], w[1][y]),
-                                 e4m3_pair<0xc480>(w[2][y], w[3][y]));
-                    mma_m16n8k16(oo[1], a0, a1, a2, a3, e4m3_pair<0xd591>(w[0][y], w[1][y]),
-                                 e4m3_pair<0xd591>(w[2][y], w[3][y]));
-                    mma_m16n8k16(oo[2], a0, a1, a2, a3, e4m3_pair<0xe6a2>(w[0][y], w[1][y]),
-                                 e4m3_pair<0xe6a2>(w[2][y], w[3][y]));
-                    mma_m16n8k16(oo[3], a0, a1, a2, a3, e4m3_pair<0xf7b3>(w[0][y], w[1][y]),
-                                 e4m3_pair<0xf7b3>(w[2][y], w[3][y]));
+                    // codes of two rows, interleaved: columns 0, 1 and 2, 3
+                    const uint32_t ab01 = __byte_perm(w[0][y], w[1][y], 0x5140), ab23 = __byte_perm(w[0][y], w[1][y], 0x7362);
+                    const uint32_t cd01 = __byte_perm(w[2][y], w[3][y], 0x5140), cd23 = __byte_perm(w[2][y], w[3][y], 0x7362);
+                    mma_m16n8k16_f16(oo[0], a0, a1, a2, a3, f16x2_of_lo(ab01), f16x2_of_lo(cd01));
+                    mma_m16n8k16_f16(oo[1], a0, a1, a2, a3, f16x2_of_hi(ab01), f16x2_of_hi(cd01));
+                    mma_m16n8k16_f16(oo[2], a0, a1, a2, a3, f16x2_of_lo(ab23), f16x2_of_lo(cd23));
+                    mma_m16n8k16_f16(oo[3], a0, a1, a2, a3, f16x2_of_hi(ab23), f16x2_of_hi(cd23));
                 } else {
                     mma_m16n8k16(oo[0], a0, a1, a2, a3, __byte_perm(w[0][y], w[1][y], 0x5410),
                                  __byte_perm(w[2][y], w[3][y], 0x5410));
@@ -526,6 +654,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     for (int r = 0; r < 2; ++r) {
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
         l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+    if constexpr (FP8) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            o[j][0] *= vref;
+            o[j][1] *= vref;
+            o[j][2] *= vref;
+            o[j][3] *= vref;
+        }
     }
     __syncthreads();                       // every warp is done with the ring
     float* js = reinterpret_cast<float*>(smem);                        // (warp, 16, D)

@@ -14,8 +14,10 @@
 // beside the other's products.  At d = 256 tensor memory holds one stream.
 //
 //   warps [0, 4 NS)       softmax (one thread per row); they also bring in Q
-//   e4m3: 4 warps         convert the raw codes of a K or V tile to bf16 (exact;
-//                         the row scales go to the scores and to P)
+//   e4m3: 4 warps         convert the raw codes of a K or V tile to fp16 (exact;
+//                         K's row scales go to the scores, V's to P, q and P are
+//                         brought into fp16's range by powers of two: see the
+//                         streaming kernel)
 //   load warp             walks the page table: a head's rows of a page are
 //                         contiguous, so a bf16 tile is BN / page_size TMA boxes
 //                         per 64 columns, written swizzled into a ring of half
@@ -76,7 +78,7 @@ struct TileCfg {
     static constexpr int CONV_REGS = FP8 ? 80 : 0, LOW_REGS = FP8 ? 64 : 104;
     static constexpr int HIGH_RAW = (LAUNCH_REGS * THREADS - (CONV_REGS + LOW_REGS) * 128) / (NS * 128) / 8 * 8;
     static constexpr int HIGH_REGS = HIGH_RAW > 248 ? 248 : HIGH_RAW;
-    static constexpr int BAR_BYTES = 1024;
+    static constexpr int BAR_BYTES = 2048;
     // Output staging: 4 KB per softmax warp, over query tiles that no product
     // reads any more (d = 64: its query tiles are too small for that).
     static constexpr int EPI_BYTES = D == 64 ? NS * 16384 : 0;
@@ -99,6 +101,9 @@ struct TileBarriers {
     uint64_t sc_full[8];
     uint32_t valid[8][4];          // per slot: bit per key of the tile
     uint32_t poison[8][4];         // per diagonal tile: bit per key whose V row is not finite
+    float vref[8];                 // e4m3, per slot: the slot's V scales are divided by it
+    float red[2][4];               // e4m3: the converting warps' maxima
+    float q_log2[128 * 2];         // e4m3: raw score -> log2 units, per query row
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -384,7 +389,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             // -------------------------------------------------------- MMA issuers
             // Step u of a stream: O += P(u-1) V(u-1), then S(u).  In pair mode
             // both warps release every ring entry, always after waiting for it.
-            constexpr uint32_t idesc_s = make_idesc(1u, 128, BN, 0), idesc_o = make_idesc(1u, 128, D, 1);
+            constexpr uint32_t fmt = FP8 ? 0u : 1u;            // fp16 or bf16 operands
+            constexpr uint32_t idesc_s = make_idesc(fmt, 128, BN, 0), idesc_o = make_idesc(fmt, 128, D, 1);
             const int t = warp - Cfg::MMA_WARP;
             const int nt = t == 0 ? w.n[0] : w.n[1];
             const int n = w.pair ? max(w.n[0], w.n[1]) : nt;
@@ -564,32 +570,50 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 r0 = ((ct >> 2) & 1) + (ct >> 3) / G4 * 2;
             }
             uint32_t e = 0;
+            float vref0 = 0.0f, vref1 = 0.0f;                   // per stream (pair: the first)
             tile_entries<Cfg>(w, [&](int t, int u, bool is_v) -> bool {
                 constexpr uint32_t NR = Cfg::NR;
-                if (!tile_wait(&bars->raw_full[e % NR], (e / NR) & 1, abort_flag, p, SITE_TILE_FULL)) return false;
+                // Every thread reaches the one barrier of an entry, whatever its
+                // waits say; all leave together.
+                bool ok = tile_wait(&bars->raw_full[e % NR], (e / NR) & 1, abort_flag, p, SITE_TILE_FULL);
                 const int kt = tile_slot<Cfg>(w, t, u), slot = kt % Cfg::SLOTS;
                 const int key0 = ((t == 0 ? w.j0[0] : w.j0[1]) + u) * BN;
                 const uint32_t* valid = bars->valid[slot];
                 uint32_t all = valid[0] & valid[1];
                 if constexpr (BN == 128) all &= valid[2] & valid[3];
                 const bool whole = all == 0xffffffffu;
-                if (!is_v && (!whole || key0 / BN >= diag)) {
-                    // Scales that must not meet a weight of 0 as they are: of keys
-                    // that are not there (stale), and NaN where only some query
-                    // rows see the key (those rows learn it from the poison bits).
-                    if (!tile_wait(&bars->sc_full[slot], (kt / Cfg::SLOTS) & 1, abort_flag, p, SITE_TILE_SCALE)) return false;
-                    if (ct < BN) {
-                        float* vs = sScale + slot * 2 * BN + BN + ct;
-                        const bool have = (valid[ct >> 5] >> (ct & 31)) & 1u;
-                        if (!have) {
-                            *vs = 0.0f;
-                        } else if (key0 + ct >= diag_key && !(fabsf(*vs) < INFINITY)) {
-                            *vs = 0.0f;
-                            atomicOr(&bars->poison[min(key0 / BN - diag, Cfg::DIAG_TILES - 1)][ct >> 5], 1u << (ct & 31));
+                const bool diagonal = key0 / BN >= diag;
+                uint32_t* poison = bars->poison[min(max(key0 / BN - diag, 0), Cfg::DIAG_TILES - 1)];
+                float v = 0.0f;
+                if (!is_v) {
+                    // The tile's V scales, divided by the stream's vref (which
+                    // follows their maximum).  0 for keys that are not there
+                    // (stale) and where only some query rows see a key with a NaN
+                    // scale: those rows learn it from the poison bits, since a
+                    // weight of 0 beside it must stay 0.
+                    ok = ok && tile_wait(&bars->sc_full[slot], (kt / Cfg::SLOTS) & 1, abort_flag, p, SITE_TILE_SCALE);
+                    if (ct < BN && ((valid[ct >> 5] >> (ct & 31)) & 1u)) {
+                        v = sScale[slot * 2 * BN + BN + ct];
+                        if (diagonal && key0 + ct >= diag_key && !(v < INFINITY)) {
+                            v = 0.0f;
+                            atomicOr(&poison[ct >> 5], 1u << (ct & 31));
                         }
                     }
+                    const uint32_t top = __reduce_max_sync(0xffffffffu, v > 0.0f && v < INFINITY ? __float_as_uint(v) : 0u);
+                    if (lane == 0) bars->red[kt & 1][ct >> 5] = __uint_as_float(top);
                 }
-                if (!tile_wait(&bars->ring_empty[e % NH], ((e / NH) & 1) ^ 1, abort_flag, p, SITE_TILE_EMPTY)) return false;
+                ok = ok && tile_wait(&bars->ring_empty[e % NH], ((e / NH) & 1) ^ 1, abort_flag, p, SITE_TILE_EMPTY);
+                if (!named_barrier_and(1, 128, ok)) return false;
+                if (!is_v) {
+                    const float* red = bars->red[kt & 1];
+                    const float vm = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+                    float ref = w.pair || t == 0 ? vref0 : vref1;
+                    if (vm > 64.0f * ref) ref = vref_of(vm);
+                    if (w.pair || t == 0) vref0 = ref;
+                    else vref1 = ref;
+                    if (ct < BN) sScale[slot * 2 * BN + BN + ct] = v * (ref == 0.0f ? 0.0f : 1.0f / ref);
+                    if (ct == 0) bars->vref[slot] = ref;
+                }
                 const uint8_t* src = sRaw + (e % NR) * Cfg::RAW_BYTES + r0 * D + c * 16;
                 uint8_t* dst = sRing + (e % NH) * Cfg::HALF_BYTES;
                 auto convert = [&](auto check) {
@@ -599,16 +623,25 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         uint4 v = *reinterpret_cast<const uint4*>(src + i * RPP * D);
                         if constexpr (decltype(check)::value) {
                             if (!((valid[r >> 5] >> (r & 31)) & 1u)) v = make_uint4(0, 0, 0, 0);
+                            if (is_v && diagonal && key0 + r >= diag_key) {
+                                uint32_t* wd = &v.x;
+                                uint32_t nan = 0;
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) {
+                                    const uint32_t n4 = __vcmpeq4(wd[y] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    wd[y] &= ~n4;
+                                    nan |= n4;
+                                }
+                                if (nan) atomicOr(&poison[r >> 5], 1u << (r & 31));
+                            }
                         }
                         *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c)) =
-                            make_uint4(e4m3_pair<0x9180>(v.x, 0), e4m3_pair<0xb3a2>(v.x, 0), e4m3_pair<0x9180>(v.y, 0),
-                                       e4m3_pair<0xb3a2>(v.y, 0));
+                            make_uint4(f16x2_of_lo(v.x), f16x2_of_hi(v.x), f16x2_of_lo(v.y), f16x2_of_hi(v.y));
                         *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c + 1)) =
-                            make_uint4(e4m3_pair<0x9180>(v.z, 0), e4m3_pair<0xb3a2>(v.z, 0), e4m3_pair<0x9180>(v.w, 0),
-                                       e4m3_pair<0xb3a2>(v.w, 0));
+                            make_uint4(f16x2_of_lo(v.z), f16x2_of_hi(v.z), f16x2_of_lo(v.w), f16x2_of_hi(v.w));
                     }
                 };
-                if (whole) convert(std::false_type{});
+                if (whole && !(is_v && diagonal)) convert(std::false_type{});
                 else convert(std::true_type{});
                 fence_proxy_async_smem();
                 mbar_arrive(&bars->ring_full[e % NH]);
@@ -627,8 +660,28 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int j0 = t == 0 ? w.j0[0] : w.j0[1], part = t == 0 ? w.part[0] : w.part[1];
         const int limit = in ? row_limit(p, w, row) : 0;
         cp_async_wait<0>();
+        if constexpr (FP8) {
+            // To fp16 in place, each lane the chunks that it brought in.
+            if (w.pair || t == 0) {
+                constexpr int LPR = D / 8 < 32 ? D / 8 : 32;
+#pragma unroll 4
+                for (int x = 0; x < LPR; ++x) {
+                    const int rq = (warp & 3) * 32 + x * (32 / LPR) + lane / LPR, c = lane % LPR;
+                    uint4* at = reinterpret_cast<uint4*>(sQ + t * Cfg::Q_BYTES + (c >> 3) * (BM * 128) + rq * 128 +
+                                                         (((c & 7) ^ (rq & 7)) << 4));
+                    const uint4 v = *at;
+                    uint32_t top = bf16x8_amax(v);
+#pragma unroll
+                    for (int y = LPR / 2; y > 0; y >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
+                    const int shift = q_shift(top);
+                    *at = q_to_f16(v, pow2f(shift));
+                    if (c == 0) bars->q_log2[t * 128 + rq] = p.scale_log2 * pow2f(-shift);
+                }
+            }
+        }
         fence_proxy_async_smem();
         mbar_arrive(&bars->q_full);
+        float to_log2 = p.scale_log2, vref = 0.0f;
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int u = 0; u < nt; ++u) {
@@ -642,6 +695,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 break;
             }
             tc_fence_after();
+            float vfall = 1.0f;                // O is in units of vref
+            if constexpr (FP8) {
+                if (u == 0) to_log2 = bars->q_log2[(w.pair ? t * 128 : 0) + (tid & 127)];
+                const float now = bars->vref[slot];
+                if (now != vref) {
+                    vfall = vref * (1.0f / now);
+                    vref = now;
+                }
+            }
             uint32_t sr[BN];
 #pragma unroll
             for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_tmem + c * 32, sr + c * 32);
@@ -687,13 +749,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             }
             mx0 = fmax3(mx0, mx1, __uint_as_float(sr[BN - 4]));
             mx2 = fmax3(mx2, mx3, __uint_as_float(sr[BN - 3]));
-            const float mx = fmax3(mx0, mx2, fmaxf(__uint_as_float(sr[BN - 2]), __uint_as_float(sr[BN - 1]))) * p.scale_log2;
+            const float mx = fmax3(mx0, mx2, fmaxf(__uint_as_float(sr[BN - 2]), __uint_as_float(sr[BN - 1]))) * to_log2;
             // The reference moves only by jumps of more than 8 (log2 units).
             float mn = m;
             if (mx > m + 8.0f) mn = mx;
             const float ref = mn == -INFINITY ? 0.0f : mn;
             const float alpha = mn == m ? 1.0f : ex2_approx(m - ref);
-            const float2 mul2 = make_float2(p.scale_log2, p.scale_log2), neg2 = make_float2(-ref, -ref);
+            const float2 mul2 = make_float2(to_log2, to_log2), neg2 = make_float2(-ref, -ref);
             float2 acc0 = make_float2(0.0f, 0.0f), acc1 = make_float2(0.0f, 0.0f);
             const float4* vs = reinterpret_cast<const float4*>(sScale + slot * 2 * BN + BN);
 #pragma unroll
@@ -716,13 +778,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         f = __fmul2_rn(f, make_float2(v4.x, v4.y));
                         g = __fmul2_rn(g, make_float2(v4.z, v4.w));
                     }
-                    pk[x] = pack_bf16x2(f.x, f.y);
-                    pk[x + 1] = pack_bf16x2(g.x, g.y);
+                    pk[x] = FP8 ? pack_f16x2(f.x, f.y) : pack_bf16x2(f.x, f.y);
+                    pk[x + 1] = FP8 ? pack_f16x2(g.x, g.y) : pack_bf16x2(g.x, g.y);
                 }
                 tmem_st16(s_tmem + c * 16, pk);
             }
             l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y));
-            if (u > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+            const float fall = FP8 ? alpha * vfall : alpha;
+            if (u > 0 && __any_sync(0xffffffffu, fall != 1.0f)) {
                 // The commit that signalled S(u) covers O += P(u-1) V(u-1).
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -731,7 +794,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     tmem_wait_ld();
                     reg_fence32(o);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                    for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fall);
                     tmem_st32(o_tmem + c * 32, o);
                 }
             }
@@ -758,7 +821,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     }
                 }
             }
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (FP8 ? vref : 1.0f);
             const float lse2 = l == 0.0f ? -INFINITY : m + __log2f(l);
             const bool some = nt > 0;
             if constexpr (DIRECT) {
