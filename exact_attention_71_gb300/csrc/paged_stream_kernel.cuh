@@ -143,25 +143,28 @@ struct StreamCfg {
     static constexpr int VC = D / (8 * VE);                        // V chunks per row and thread
     static constexpr int WARPS = 4;
     static constexpr int THREADS = WARPS * 32;
-    static constexpr int TILE = 16 * ROW;                          // a step's K or V rows
+    // 16-key blocks of a warp's step.  e4m3 steps are bound by instructions: two
+    // blocks share the waits, the copies' issue and the running maximum.  bf16
+    // steps are bound by bytes, and small steps keep more warps an SM.
+    static constexpr int H = FP8 ? 2 : 1;
+    static constexpr int STEP = 16 * H;
+    static constexpr int TILE = 16 * ROW;                          // a block's K or V rows
     static constexpr int SCALES = FP8 ? 128 : 0;                   // its 16 K and 16 V scales
-    // e4m3 steps are bound by instructions (the conversion) and their latency:
-    // the query fragments stay in shared memory, which leaves room for one more
-    // CTA an SM.
-    static constexpr int CTAS = D == 64 ? (FP8 ? 5 : 4) : D == 128 ? (FP8 ? 4 : 3) : FP8 ? 2 : 1;     // per SM
-    static constexpr int STAGES = D == 64 ? (FP8 ? 4 : 3) : D == 128 ? (FP8 ? 3 : 2) : 3;
-    static constexpr int Q_BYTES = FP8 ? 16 * D * 2 : 0;
-    static constexpr int WARP_BYTES = STAGES * 2 * TILE;
+    static constexpr int CTAS = D == 64 ? 4 : D == 128 ? 3 : FP8 ? 2 : 1;     // per SM
+    static constexpr int STAGES = D == 64 ? 3 : D == 128 ? 2 : FP8 ? 1 : 3;
+    static constexpr int STAGE_BYTES = H * 2 * TILE;               // (block, K / V, TILE)
+    static constexpr int WARP_BYTES = STAGES * STAGE_BYTES;
     static constexpr int RING_BYTES = WARPS * WARP_BYTES;
     static constexpr int JOIN_BYTES = WARPS * 16 * (D + 2) * 4;
     static constexpr int MAIN_BYTES = RING_BYTES > JOIN_BYTES ? RING_BYTES : JOIN_BYTES;
-    static constexpr int SCALE_BYTES = WARPS * STAGES * SCALES;
-    static constexpr int SMEM_BYTES = 1024 + MAIN_BYTES + SCALE_BYTES + Q_BYTES + WARPS * STAGES * 16;
+    static constexpr int SCALE_BYTES = WARPS * STAGES * H * SCALES;
+    static constexpr int Q_BYTES = FP8 ? 16 * D * 2 : 0;
+    static constexpr int SMEM_BYTES = 1024 + MAIN_BYTES + SCALE_BYTES + Q_BYTES + WARPS * STAGES * 8;
     static constexpr int NT = D / 8;                               // O's column tiles
     static_assert(CTAS * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory");
 };
 
-enum : int { SITE_STREAM_K = 0xb1, SITE_STREAM_V = 0xb2, SITE_STREAM_DRAIN = 0xb3 };
+enum : int { SITE_STREAM_FULL = 0xb1, SITE_STREAM_DRAIN = 0xb2 };
 
 // Bounded wait of a whole warp.
 __device__ __forceinline__ bool stream_wait(uint64_t* bar, uint32_t parity, unsigned long long limit, int* status,
@@ -268,75 +271,67 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     const int k1 = min(k0 + chunk, len);
     const int* table = prefix ? p.prefix_table : p.table + seq * p.table_stride;
 
-    const int first = k0 / 16 + warp;                      // this warp's steps: first, first + 4, ...
-    const int steps_end = k0 < k1 ? (k1 + 15) / 16 : 0;    // an empty range ends at len, inside a step
-    uint8_t* ring = smem + warp * Cfg::WARP_BYTES;         // (stage, K / V, TILE)
-    float* scales = reinterpret_cast<float*>(smem + Cfg::MAIN_BYTES + warp * STAGES * Cfg::SCALES);
-    uint64_t* kfull = reinterpret_cast<uint64_t*>(smem + Cfg::MAIN_BYTES + Cfg::SCALE_BYTES + Cfg::Q_BYTES) +
-                      warp * 2 * STAGES;
-    uint64_t* vfull = kfull + STAGES;
+    constexpr int H = Cfg::H, STEP = Cfg::STEP, STRIDE = STEP * Cfg::WARPS;
+    const int first = k0 + warp * STEP;                    // this warp's steps: keys first, first + STRIDE, ...
+    const int end = k0 < k1 ? k1 : 0;                      // (an empty range ends at len, inside a step)
+    uint8_t* ring = smem + warp * Cfg::WARP_BYTES;
+    float* scales = reinterpret_cast<float*>(smem + Cfg::MAIN_BYTES + warp * STAGES * H * Cfg::SCALES);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::MAIN_BYTES + Cfg::SCALE_BYTES + Cfg::Q_BYTES) + warp * STAGES;
     if (lane == 0) {
-        for (int s = 0; s < 2 * STAGES; ++s) mbar_init(kfull + s, 1);
+        for (int s = 0; s < STAGES; ++s) mbar_init(full + s, 1);
         fence_barrier_init();
         fence_proxy_async_smem();
     }
     __syncwarp();
 
-    uint32_t bad = 0;                                      // bit (step / 4) & 31: the step's page is refused
-    auto page_of = [&](int step) -> int { return step < steps_end ? __ldg(table + ((step * 16) >> p.page_shift)) : 0; };
-    auto issue_k = [&](int step, int stage, int page) {
-        if (step >= steps_end) return;
-        const bool ok = page >= 0 && page < p.num_pages;
-        const uint32_t bit = 1u << ((step >> 2) & 31);
-        bad = ok ? bad & ~bit : bad | bit;
-        if (lane == 0) {
-            if (!ok) {
-                atomicCAS(p.status, 0, SITE_PAGED_PAGE);
-                mbar_arrive(kfull + stage);
-            } else {
-                const int row = (step * 16) & ((1 << p.page_shift) - 1);
-                mbar_arrive_expect_tx(kfull + stage, Cfg::TILE + Cfg::SCALES);
-                const uint64_t pol = l2_policy_evict_first();
-                if constexpr (FP8) {
-                    const long long at = ((static_cast<long long>(page) * p.H_kv + kvh) << p.page_shift) + row;
-                    bulk_load(scales + stage * 32, p.k_scale + at, 64, kfull + stage);
-                    bulk_load(scales + stage * 32 + 16, p.v_scale + at, 64, kfull + stage);
-                }
-#pragma unroll
-                for (int b = 0; b < Cfg::NB; ++b)
-                    tma_load_4d(ring + stage * 2 * Cfg::TILE + b * 16 * Cfg::SW, &tmap_k, kfull + stage, b * (Cfg::SW / Cfg::ES),
-                                row, kvh, page, pol);
-            }
-        }
+    // Lane 2h + v (v: V instead of K) looks up the page of a step's block h and
+    // copies its rows.
+    const int my_block = lane >> 1;
+    const bool my_v = lane & 1;
+    const uint64_t policy = l2_policy_evict_first();
+    const CUtensorMap* my_map = my_v ? &tmap_v : &tmap_k;
+    uint32_t gone = 0;                                     // bit H * (round & 7) + h: the block's page is refused
+    auto page_of = [&](int key) -> int {
+        const int at = key + my_block * 16;
+        return my_block < H && at < end ? __ldg(table + (at >> p.page_shift)) : -1;
     };
-    auto issue_v = [&](int step, int stage, int page) {
-        if (step >= steps_end) return;
-        if (lane == 0) {
-            if (page < 0 || page >= p.num_pages) {
-                mbar_arrive(vfull + stage);
-            } else {
-                const int row = (step * 16) & ((1 << p.page_shift) - 1);
-                mbar_arrive_expect_tx(vfull + stage, Cfg::TILE);
-                const uint64_t pol = l2_policy_evict_first();
+    auto issue = [&](int key, int stage, int round, int page) {
+        if (key >= end) return;
+        const int at = key + my_block * 16;
+        const bool want = my_block < H && at < end;
+        const bool have = want && page >= 0 && page < p.num_pages;
+        const uint32_t copies = __ballot_sync(0xffffffffu, have), wanted = __ballot_sync(0xffffffffu, want);
+        if (copies != wanted) {
+            if (lane == 0) atomicCAS(p.status, 0, SITE_PAGED_PAGE);
+        }
+        uint32_t bits = 0;
 #pragma unroll
-                for (int b = 0; b < Cfg::NB; ++b)
-                    tma_load_4d(ring + (stage * 2 + 1) * Cfg::TILE + b * 16 * Cfg::SW, &tmap_v, vfull + stage,
-                                b * (Cfg::SW / Cfg::ES), row, kvh, page, pol);
+        for (int h = 0; h < H; ++h) bits |= (copies >> (2 * h)) & 1u ? 0u : 1u << h;
+        const int sh = H * (round & 7);
+        gone = (gone & ~(((1u << H) - 1u) << sh)) | (bits << sh);
+        if (lane == 0) mbar_arrive_expect_tx(full + stage, __popc(copies) * (Cfg::TILE + Cfg::SCALES / 2));
+        __syncwarp();
+        if (have) {
+            const int row = at & ((1 << p.page_shift) - 1);
+            uint8_t* dst = ring + stage * Cfg::STAGE_BYTES + lane * Cfg::TILE;
+            if constexpr (FP8) {
+                const long long r = ((static_cast<long long>(page) * p.H_kv + kvh) << p.page_shift) + row;
+                bulk_load(scales + (stage * H * 2 + lane) * 16, (my_v ? p.v_scale : p.k_scale) + r, 64, full + stage);
             }
+#pragma unroll
+            for (int b = 0; b < Cfg::NB; ++b)
+                tma_load_4d(dst + b * 16 * Cfg::SW, my_map, full + stage, b * (Cfg::SW / Cfg::ES), row, kvh, page, policy);
         }
     };
     {
         // The first steps' pages together, then their copies.
         int pages[STAGES];
 #pragma unroll
-        for (int s = 0; s < STAGES; ++s) pages[s] = page_of(first + 4 * s);
+        for (int s = 0; s < STAGES; ++s) pages[s] = page_of(first + STRIDE * s);
 #pragma unroll
-        for (int s = 0; s < STAGES; ++s) {
-            issue_k(first + 4 * s, s, pages[s]);
-            issue_v(first + 4 * s, s, pages[s]);
-        }
+        for (int s = 0; s < STAGES; ++s) issue(first + STRIDE * s, s, s, pages[s]);
     }
-    int next_page = page_of(first + 4 * STAGES);
+    int next_page = page_of(first + STRIDE * STAGES);
 
     // This thread's two query rows: g and g + 8 of the tile.  Its fragments are
     // chunk c of the k permutation, elements [c * 4E + t * E, + E) of each.
@@ -404,61 +399,67 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
     float vref = FP8 ? 0.0f : 1.0f;
 
-    int stage = 0;
+    // Shared-memory offsets of this thread's chunks (SW = 128: the chunk's column
+    // is xor-ed with the row, so the next four columns, and the rows four below,
+    // are one xor of 64 away).
+    uint32_t koff[2], voff[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        koff[x] = stream_chunk<Cfg>(pig, 4 * x + t) % (16 * Cfg::SW);
+        const int r = x ? kb : ka;
+        voff[x] = Cfg::VB == 16 ? stream_chunk<Cfg>(r, pig) : stream_chunk<Cfg>(r, g >> 1) + (g & 1) * 8;
+    }
+
+    int stage = 0, round = 0;
     uint32_t parity = 0;
-    bool ok = true, ahead = false;         // ahead: this step's slot has the K of the next round
-    int step = first;
-    for (; step < steps_end; step += 4) {
+    bool ok = true;
+    int key0 = first;
+    for (; key0 < end; key0 += STRIDE, ++round) {
         const int page = next_page;
-        next_page = page_of(step + 4 * (STAGES + 1));
-        if (!(ok = stream_wait(kfull + stage, parity, p.wait_limit, p.status, SITE_STREAM_K))) break;
-        const uint8_t* st = ring + stage * 2 * Cfg::TILE;
+        next_page = page_of(key0 + STRIDE * (STAGES + 1));
+        if (!(ok = stream_wait(full + stage, parity, p.wait_limit, p.status, SITE_STREAM_FULL))) break;
+        uint8_t* st = ring + stage * Cfg::STAGE_BYTES;
 
         // ---------------------------------------------------------- S = Q K^T
-        float s[2][4];
+        // s[x][0..1]: row g, keys 8 x + ka, 8 x + kb; s[x][2..3]: row g + 8.
+        float s[2 * H][4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.0f;
+        for (int x = 0; x < 2 * H; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.0f;
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
+            const uint32_t col = Cfg::SW == 128 ? koff[c & 1] + (c >> 1) * (16 * Cfg::SW) : koff[0];
             if constexpr (FP8) {
-                uint4 k4[2], q0[2], q1[2];
+                const uint4 q0 = sq[(c * 4) * 32], q1 = sq[(c * 4 + 1) * 32];          // rows g, g + 8
+                const uint4 q2 = sq[(c * 4 + 2) * 32], q3 = sq[(c * 4 + 3) * 32];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    k4[x] = *reinterpret_cast<const uint4*>(st + stream_chunk<Cfg>(x * 8 + pig, c * 4 + t));
-                    q0[x] = sq[((c * 2 + x) * 2) * 32];            // row g, half x of the chunk
-                    q1[x] = sq[((c * 2 + x) * 2 + 1) * 32];        // row g + 8
-                }
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint4 qg = q0[w >> 1], qh = q1[w >> 1];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const uint32_t word = w == 0 ? k4[x].x : w == 1 ? k4[x].y : w == 2 ? k4[x].z : k4[x].w;
-                        mma_m16n8k16_f16(s[x], w & 1 ? qg.z : qg.x, w & 1 ? qh.z : qh.x, w & 1 ? qg.w : qg.y,
-                                         w & 1 ? qh.w : qh.y, f16x2_of_lo(word), f16x2_of_hi(word));
-                    }
+                for (int x = 0; x < 2 * H; ++x) {
+                    const uint4 kk = *reinterpret_cast<const uint4*>(st + (x >> 1) * 2 * Cfg::TILE + (x & 1) * 8 * Cfg::SW + col);
+                    mma_m16n8k16_f16(s[x], q0.x, q1.x, q0.y, q1.y, f16x2_of_lo(kk.x), f16x2_of_hi(kk.x));
+                    mma_m16n8k16_f16(s[x], q0.z, q1.z, q0.w, q1.w, f16x2_of_lo(kk.y), f16x2_of_hi(kk.y));
+                    mma_m16n8k16_f16(s[x], q2.x, q3.x, q2.y, q3.y, f16x2_of_lo(kk.z), f16x2_of_hi(kk.z));
+                    mma_m16n8k16_f16(s[x], q2.z, q3.z, q2.w, q3.w, f16x2_of_lo(kk.w), f16x2_of_hi(kk.w));
                 }
             } else {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const uint4 kk = *reinterpret_cast<const uint4*>(st + stream_chunk<Cfg>(x * 8 + pig, c * 4 + t));
+                for (int x = 0; x < 2 * H; ++x) {
+                    const uint4 kk = *reinterpret_cast<const uint4*>(st + (x >> 1) * 2 * Cfg::TILE + (x & 1) * 8 * Cfg::SW + col);
                     const int at = c * 4;
                     mma_m16n8k16(s[x], qa[0][at], qa[1][at], qa[0][at + 1], qa[1][at + 1], kk.x, kk.y);
                     mma_m16n8k16(s[x], qa[0][at + 2], qa[1][at + 2], qa[0][at + 3], qa[1][at + 3], kk.z, kk.w);
                 }
             }
         }
-        // s[x][0..1]: row g, keys x * 8 + ka, x * 8 + kb; s[x][2..3]: row g + 8.
-        const bool skip = (bad >> ((step >> 2) & 31)) & 1u;
-        const bool special = skip || step * 16 + 16 > plain_end;
-        float2 vscale[2];
-        const float* sc = scales + stage * 32;
+        const uint32_t miss = (gone >> (H * (round & 7))) & ((1u << H) - 1u);
+        const bool special = miss != 0 || key0 + STEP > plain_end;
+        float2 vscale[2 * H];
+        const float* sc = scales + stage * H * 32;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < 2 * H; ++x) {
             float2 mul = make_float2(1.0f, 1.0f);
             if constexpr (FP8) {
-                mul = make_float2(sc[x * 8 + ka], sc[x * 8 + kb]);
-                vscale[x] = make_float2(sc[16 + x * 8 + ka], sc[16 + x * 8 + kb]);
+                const float* at = sc + (x >> 1) * 32 + (x & 1) * 8;
+                mul = make_float2(at[ka], at[kb]);
+                vscale[x] = make_float2(at[16 + ka], at[16 + kb]);
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -466,16 +467,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 s[x][2 * r + 1] *= mul.y * to_log2[r];
             }
         }
-        __syncwarp();
-        if constexpr (!FP8) {
-            issue_k(step + 4 * STAGES, stage, page);       // K's slot is free
-            ahead = step + 4 * STAGES < steps_end;
-        }
         if (special) {
             // A masked score is -inf whatever was read for it.
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int key = step * 16 + x * 8;
+            for (int x = 0; x < 2 * H; ++x) {
+                const bool skip = (miss >> (x >> 1)) & 1u;
+                const int key = key0 + x * 8;
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int lim = skip ? 0 : limit[r];
@@ -494,16 +491,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         // more than 8 (log2 units), so that the quad's shuffles and O's
         // rescaling are rare; O and l share the reference, so the result does
         // not depend on it.
-        const float t0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-        const float t1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-        bool move = t0 > m[0] + 8.0f || t1 > m[1] + 8.0f;
+        float mx[2] = {fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])};
+#pragma unroll
+        for (int x = 1; x < 2 * H; ++x) {
+            mx[0] = fmax3(mx[0], s[x][0], s[x][1]);
+            mx[1] = fmax3(mx[1], s[x][2], s[x][3]);
+        }
+        bool move = mx[0] > m[0] + 8.0f || mx[1] > m[1] + 8.0f;
         float vm = 0.0f;
         if constexpr (FP8) {
-            vm = fmaxf(fmaxf(vscale[0].x, vscale[0].y), fmaxf(vscale[1].x, vscale[1].y));
+            vm = fmaxf(vscale[0].x, vscale[0].y);
+#pragma unroll
+            for (int x = 1; x < 2 * H; ++x) vm = fmax3(vm, vscale[x].x, vscale[x].y);
             move = move || vm > 64.0f * vref;
         }
         if (__any_sync(0xffffffffu, move)) {
-            float mx[2] = {t0, t1};
             float vfall = 1.0f;
             if constexpr (FP8) {
                 // V scales are never negative: their bits order them.
@@ -532,16 +534,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             }
         }
         const float n0 = m[0] == -INFINITY ? 0.0f : m[0], n1 = m[1] == -INFINITY ? 0.0f : m[1];
-        if constexpr (FP8) {
-            const float iv = vref == 0.0f ? 0.0f : 1.0f / vref;        // a power of two
+        const float iv = FP8 ? (vref == 0.0f ? 0.0f : 1.0f / vref) : 1.0f;         // a power of two
+        uint32_t pa[H][4];             // P as the A operand of each block
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                vscale[x].x *= iv;
-                vscale[x].y *= iv;
-            }
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < 2 * H; ++x) {
             s[x][0] = ex2_approx(s[x][0] - n0);
             s[x][1] = ex2_approx(s[x][1] - n0);
             s[x][2] = ex2_approx(s[x][2] - n1);
@@ -552,84 +548,89 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 // V's row scale rides on P; l sums the plain probabilities.  A
                 // weight of 0 stays 0 beside a NaN scale: a row that does not
                 // see the key must not notice it.
+                const float va = vscale[x].x * iv, vb = vscale[x].y * iv;
                 if (special) {
-                    s[x][0] = s[x][0] == 0.0f ? 0.0f : s[x][0] * vscale[x].x;
-                    s[x][1] = s[x][1] == 0.0f ? 0.0f : s[x][1] * vscale[x].y;
-                    s[x][2] = s[x][2] == 0.0f ? 0.0f : s[x][2] * vscale[x].x;
-                    s[x][3] = s[x][3] == 0.0f ? 0.0f : s[x][3] * vscale[x].y;
+                    s[x][0] = s[x][0] == 0.0f ? 0.0f : s[x][0] * va;
+                    s[x][1] = s[x][1] == 0.0f ? 0.0f : s[x][1] * vb;
+                    s[x][2] = s[x][2] == 0.0f ? 0.0f : s[x][2] * va;
+                    s[x][3] = s[x][3] == 0.0f ? 0.0f : s[x][3] * vb;
                 } else {
-                    s[x][0] *= vscale[x].x;
-                    s[x][1] *= vscale[x].y;
-                    s[x][2] *= vscale[x].x;
-                    s[x][3] *= vscale[x].y;
+                    s[x][0] *= va;
+                    s[x][1] *= vb;
+                    s[x][2] *= va;
+                    s[x][3] *= vb;
                 }
+                pa[x >> 1][(x & 1) * 2] = pack_f16x2(s[x][0], s[x][1]);
+                pa[x >> 1][(x & 1) * 2 + 1] = pack_f16x2(s[x][2], s[x][3]);
+            } else {
+                // P is rounded to bf16 for the product (relative 2^-8 at most
+                // per weight, as the dense forward does; e4m3 cache: fp16, see
+                // above); l keeps the unrounded values.
+                pa[x >> 1][(x & 1) * 2] = pack_bf16x2(s[x][0], s[x][1]);
+                pa[x >> 1][(x & 1) * 2 + 1] = pack_bf16x2(s[x][2], s[x][3]);
             }
         }
-        // P is rounded to bf16 for the product (relative 2^-8 at most per
-        // weight, as the dense forward does; e4m3 cache: fp16, see above); l keeps
-        // the unrounded values.
-        auto pack = [](float a, float b) { return FP8 ? pack_f16x2(a, b) : pack_bf16x2(a, b); };
-        const uint32_t a0 = pack(s[0][0], s[0][1]), a1 = pack(s[0][2], s[0][3]);
-        const uint32_t a2 = pack(s[1][0], s[1][1]), a3 = pack(s[1][2], s[1][3]);
         // ---------------------------------------------------------- O += P V
-        if (!(ok = stream_wait(vfull + stage, parity, p.wait_limit, p.status, SITE_STREAM_V))) break;
-        const uint8_t* sv = st + Cfg::TILE;
-        {
+        if (special) {
             // 0 * NaN is NaN: stale rows become 0, and where rows of the tile see
             // different keys a non-finite value is taken out of the product and
             // the rows that do see its key become NaN as a whole.
-            if (special) {
-                const uint32_t hit = fix_v_step<Cfg>(ring + (stage * 2 + 1) * Cfg::TILE, skip ? 0 : k1 - step * 16,
-                                                     diag - step * 16, lane);
+#pragma unroll 1
+            for (int h = 0; h < H; ++h) {
+                const int at = key0 + h * 16;
+                const uint32_t hit = fix_v_step<Cfg>(st + (2 * h + 1) * Cfg::TILE, (miss >> h) & 1u ? 0 : k1 - at, diag - at, lane);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int n = min(max(limit[r] - step * 16, 0), 16);
+                    const int n = min(max(limit[r] - at, 0), 16);
                     if (hit & ((1u << n) - 1u)) l[r] = __uint_as_float(0x7fc00000u);
                 }
             }
         }
 #pragma unroll
-        for (int c = 0; c < VC; ++c) {
-            uint32_t w[4][Cfg::VB / 4];
+        for (int h = 0; h < H; ++h) {
+            const uint8_t* sv = st + (2 * h + 1) * Cfg::TILE;
+            const uint32_t a0 = pa[h][0], a1 = pa[h][1], a2 = pa[h][2], a3 = pa[h][3];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int r = (x & 1 ? kb : ka) + (x >> 1) * 8;
-                if constexpr (Cfg::VB == 16) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(sv + stream_chunk<Cfg>(r, c * 8 + pig));
-                    w[x][0] = v.x;
-                    w[x][1] = v.y;
-                    w[x][Cfg::VB / 4 - 2] = v.z;
-                    w[x][Cfg::VB / 4 - 1] = v.w;
-                } else {
-                    const uint2 v = *reinterpret_cast<const uint2*>(sv + stream_chunk<Cfg>(r, g >> 1) + (g & 1) * 8);
-                    w[x][0] = v.x;
-                    w[x][1] = v.y;
+            for (int c = 0; c < VC; ++c) {
+                uint32_t w[4][Cfg::VB / 4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    // value rows ka, kb, 8 + ka, 8 + kb
+                    const uint8_t* at = sv + voff[x & 1] + (x >> 1) * 8 * Cfg::SW + c * 16 * Cfg::SW;
+                    if constexpr (Cfg::VB == 16) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(at);
+                        w[x][0] = v.x;
+                        w[x][1] = v.y;
+                        w[x][Cfg::VB / 4 - 2] = v.z;
+                        w[x][Cfg::VB / 4 - 1] = v.w;
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2*>(at);
+                        w[x][0] = v.x;
+                        w[x][1] = v.y;
+                    }
                 }
-            }
 #pragma unroll
-            for (int y = 0; y < Cfg::VB / 4; ++y) {
-                float(*oo)[4] = &o[c * Cfg::VE + y * (4 / Cfg::ES)];
-                if constexpr (FP8) {
-                    // codes of two rows, interleaved: columns 0, 1 and 2, 3
-                    const uint32_t ab01 = __byte_perm(w[0][y], w[1][y], 0x5140), ab23 = __byte_perm(w[0][y], w[1][y], 0x7362);
-                    const uint32_t cd01 = __byte_perm(w[2][y], w[3][y], 0x5140), cd23 = __byte_perm(w[2][y], w[3][y], 0x7362);
-                    mma_m16n8k16_f16(oo[0], a0, a1, a2, a3, f16x2_of_lo(ab01), f16x2_of_lo(cd01));
-                    mma_m16n8k16_f16(oo[1], a0, a1, a2, a3, f16x2_of_hi(ab01), f16x2_of_hi(cd01));
-                    mma_m16n8k16_f16(oo[2], a0, a1, a2, a3, f16x2_of_lo(ab23), f16x2_of_lo(cd23));
-                    mma_m16n8k16_f16(oo[3], a0, a1, a2, a3, f16x2_of_hi(ab23), f16x2_of_hi(cd23));
-                } else {
-                    mma_m16n8k16(oo[0], a0, a1, a2, a3, __byte_perm(w[0][y], w[1][y], 0x5410),
-                                 __byte_perm(w[2][y], w[3][y], 0x5410));
-                    mma_m16n8k16(oo[1], a0, a1, a2, a3, __byte_perm(w[0][y], w[1][y], 0x7632),
-                                 __byte_perm(w[2][y], w[3][y], 0x7632));
+                for (int y = 0; y < Cfg::VB / 4; ++y) {
+                    float(*oo)[4] = &o[c * Cfg::VE + y * (4 / Cfg::ES)];
+                    if constexpr (FP8) {
+                        // codes of two rows, interleaved: columns 0, 1 and 2, 3
+                        const uint32_t ab01 = __byte_perm(w[0][y], w[1][y], 0x5140), ab23 = __byte_perm(w[0][y], w[1][y], 0x7362);
+                        const uint32_t cd01 = __byte_perm(w[2][y], w[3][y], 0x5140), cd23 = __byte_perm(w[2][y], w[3][y], 0x7362);
+                        mma_m16n8k16_f16(oo[0], a0, a1, a2, a3, f16x2_of_lo(ab01), f16x2_of_lo(cd01));
+                        mma_m16n8k16_f16(oo[1], a0, a1, a2, a3, f16x2_of_hi(ab01), f16x2_of_hi(cd01));
+                        mma_m16n8k16_f16(oo[2], a0, a1, a2, a3, f16x2_of_lo(ab23), f16x2_of_lo(cd23));
+                        mma_m16n8k16_f16(oo[3], a0, a1, a2, a3, f16x2_of_hi(ab23), f16x2_of_hi(cd23));
+                    } else {
+                        mma_m16n8k16(oo[0], a0, a1, a2, a3, __byte_perm(w[0][y], w[1][y], 0x5410),
+                                     __byte_perm(w[2][y], w[3][y], 0x5410));
+                        mma_m16n8k16(oo[1], a0, a1, a2, a3, __byte_perm(w[0][y], w[1][y], 0x7632),
+                                     __byte_perm(w[2][y], w[3][y], 0x7632));
+                    }
                 }
             }
         }
         __syncwarp();
-        // (e4m3: K's slot also holds the scales, read until here)
-        if constexpr (FP8) issue_k(step + 4 * STAGES, stage, page);
-        issue_v(step + 4 * STAGES, stage, page);
-        ahead = false;
+        issue(key0 + STRIDE * STAGES, stage, round + STAGES, page);
         if (++stage == STAGES) {
             stage = 0;
             parity ^= 1;
@@ -637,15 +638,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     }
     if (!ok) {
         // A wait ran out: whatever copy is in flight lands before the CTA leaves.
-        for (int s = 0; s < STAGES; ++s) {
-            const int at = step + 4 * s;
-            if (at >= steps_end) break;
-            const int x = (stage + s) % STAGES;
-            const uint32_t ph = parity ^ (stage + s >= STAGES ? 1u : 0u);
-            stream_wait(kfull + x, ph, 2000000000ull, p.status, SITE_STREAM_DRAIN);
-            stream_wait(vfull + x, ph, 2000000000ull, p.status, SITE_STREAM_DRAIN);
-        }
-        if (ahead) stream_wait(kfull + stage, parity ^ 1u, 2000000000ull, p.status, SITE_STREAM_DRAIN);
+        for (int s = 0; s < STAGES && key0 + STRIDE * s < end; ++s)
+            stream_wait(full + (stage + s) % STAGES, parity ^ (stage + s >= STAGES ? 1u : 0u), 2000000000ull, p.status,
+                        SITE_STREAM_DRAIN);
     }
 
     // ------------------------------------------------------------ join the warps
