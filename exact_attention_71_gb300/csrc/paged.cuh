@@ -113,6 +113,9 @@ constexpr int kOwnChunk = 128;
 constexpr int kStreamRows = 32;
 constexpr int kStreamPrefixRows = 16;
 
+// A streaming CTA's fixed cost, in keys.
+constexpr double kStreamFixed = 200.0;
+
 PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size);
 
 // Runs `set` once per device (bit per ordinal; racing threads may run it twice,

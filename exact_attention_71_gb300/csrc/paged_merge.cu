@@ -41,15 +41,17 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     const long long rows = static_cast<long long>(Nq) * (H / H_kv);      // of one sequence and key/value head
     const long long own = static_cast<long long>(max_pages) * page_size;
     const int bn = d == 256 ? 64 : 128;
-    // Streaming kernel: as few waves x keys per CTA as possible, a CTA's fixed
-    // cost (page table, first loads, join) counted as 128 keys.
-    const long long slots = static_cast<long long>(kPlanSms) * (d == 64 ? 4 : d == 128 ? 3 : 2);
+    // Streaming kernel.  A CTA's time is its keys plus a fixed cost (page table,
+    // first loads, join) worth about 200; beyond one wave CTAs replace one
+    // another as they finish, and half a CTA's time is lost at the end.
+    const double slots = kPlanSms * (d == 64 ? 4.0 : d == 128 ? 3.0 : 2.0);
     const auto stream_parts = [&](long long keys, long long units) {
         int best = 1;
-        long long best_cost = -1;
+        double best_cost = -1.0;
         for (int s = 1; s <= 64 && (s == 1 || s * static_cast<long long>(kOwnChunk) < keys + kOwnChunk); ++s) {
-            const long long cost = up(units * s, slots) * (up(keys, s) + 128);
-            if (best_cost < 0 || cost < best_cost) {
+            const double waves = static_cast<double>(units) * s / slots, cta = static_cast<double>(up(keys, s)) + kStreamFixed;
+            const double cost = waves <= 1.0 ? cta : (waves + 0.5) * cta;
+            if (best_cost < 0.0 || cost < best_cost) {
                 best = s;
                 best_cost = cost;
             }

@@ -333,59 +333,77 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     }
     int next_page = page_of(first + STRIDE * STAGES);
 
-    // This thread's two query rows: g and g + 8 of the tile.  Its fragments are
-    // chunk c of the k permutation, elements [c * 4E + t * E, + E) of each.
-    int limit[2];                  // keys it sees
+    // Query row r of the tile: its index in q and o, and the keys it sees.
+    const int per = p.Nq * p.G;
+    const int live = min(16, rows - tile * 16);            // rows of this tile
+    auto row_of = [&](int r, long long& out, int& lse_at) -> int {
+        const int x = tile * 16 + r;
+        const int b = prefix ? x / per : seq, i = (prefix ? x % per : x) / p.G, h = kvh * p.G + x % p.G;
+        out = (static_cast<long long>(b) * p.Nq + i) * p.H + h;
+        lse_at = (b * p.H + h) * p.Nq + i;
+        return i;
+    };
+    int limit[2];                  // keys that rows g and g + 8 see
     float to_log2[2];              // raw score -> log2 units
-    uint32_t qa[2][D / 8];
+    uint32_t qa[2][FP8 ? 1 : D / 8];
     uint4* sq = reinterpret_cast<uint4*>(smem + Cfg::MAIN_BYTES + Cfg::SCALE_BYTES) + lane;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        const int r = tile * 16 + g + 8 * x;
         limit[x] = 0;
         to_log2[x] = p.scale_log2;
         const uint4* src = nullptr;
-        if (r < rows) {
-            const int per = p.Nq * p.G;
-            const int b = prefix ? r / per : seq, i = (prefix ? r % per : r) / p.G, h = kvh * p.G + r % p.G;
-            limit[x] = prefix || !p.causal ? len : max(0, len - p.Nq + 1 + i);
-            src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                 ((static_cast<long long>(b) * p.Nq + i) * p.H + h) * D);
+        if (g + 8 * x < live) {
+            long long out;
+            int at;
+            const int i = row_of(g + 8 * x, out, at);
+            limit[x] = min(prefix || !p.causal ? len : max(0, len - p.Nq + 1 + i), k1);
+            src = reinterpret_cast<const uint4*>(q + out * D);
         }
-        limit[x] = min(limit[x], k1);
+        if constexpr (!FP8) {
+            // Fragments: chunk c of the k permutation, elements [c * 4E + t * E, + E).
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-#pragma unroll
-            for (int y = 0; y < Cfg::E / 8; ++y) {
-                const int at = c * (Cfg::E / 8) + y;
-                const uint4 v = src ? __ldg(src + (c * 4 + t) * (Cfg::E / 8) + y) : make_uint4(0, 0, 0, 0);
-                qa[x][at * 4] = v.x;
-                qa[x][at * 4 + 1] = v.y;
-                qa[x][at * 4 + 2] = v.z;
-                qa[x][at * 4 + 3] = v.w;
+            for (int c = 0; c < KC; ++c) {
+                const uint4 v = src ? __ldg(src + c * 4 + t) : make_uint4(0, 0, 0, 0);
+                qa[x][c * 4] = v.x;
+                qa[x][c * 4 + 1] = v.y;
+                qa[x][c * 4 + 2] = v.z;
+                qa[x][c * 4 + 3] = v.w;
             }
         }
     }
     if constexpr (FP8) {
-        // To fp16, into shared memory as (chunk half, row half, lane); each warp
-        // writes a quarter.
+        // To fp16, once per CTA: warp w takes rows 4w .. 4w + 3, eight lanes a
+        // row, and writes them as fragments (chunk half, row half, lane).
+        __shared__ float row_log2[16];
+        const int r = warp * 4 + (lane >> 3);
+        uint4 v[D / 64];
+        uint32_t top = 0;
+        const uint4* src = nullptr;
+        if (r < live) {
+            long long out;
+            int at;
+            row_of(r, out, at);
+            src = reinterpret_cast<const uint4*>(q + out * D);
+        }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            uint32_t top = 0;
+        for (int y = 0; y < D / 64; ++y) {
+            v[y] = src ? __ldg(src + y * 8 + (lane & 7)) : make_uint4(0, 0, 0, 0);
+            top = max(top, bf16x8_amax(v[y]));
+        }
 #pragma unroll
-            for (int at = 0; at < D / 32; ++at)
-                top = max(top, bf16x8_amax(make_uint4(qa[x][at * 4], qa[x][at * 4 + 1], qa[x][at * 4 + 2], qa[x][at * 4 + 3])));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int shift = q_shift(top);
-            to_log2[x] *= pow2f(-shift);
+        for (int y = 1; y < 8; y <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
+        const int shift = q_shift(top);
+        if ((lane & 7) == 0) row_log2[r] = p.scale_log2 * pow2f(-shift);
 #pragma unroll
-            for (int at = 0; at < D / 32; ++at) {
-                if (at % Cfg::WARPS != warp) continue;
-                sq[(at * 2 + x) * 32] = q_to_f16(make_uint4(qa[x][at * 4], qa[x][at * 4 + 1], qa[x][at * 4 + 2], qa[x][at * 4 + 3]), pow2f(shift));
-            }
+        for (int y = 0; y < D / 64; ++y) {
+            const int i8 = y * 8 + (lane & 7);             // eight elements: chunk i8 / 8, thread (i8 / 2) % 4, half i8 % 2
+            const int at = (i8 >> 3) * 2 + (i8 & 1);
+            (sq - lane)[(at * 2 + (r >> 3)) * 32 + (r & 7) * 4 + ((i8 >> 1) & 3)] = q_to_f16(v[y], pow2f(shift));
         }
         __syncthreads();
+        to_log2[0] = row_log2[g];
+        to_log2[1] = row_log2[g + 8];
     }
     // From this key on some row of the tile may not see what another does.
     int diag = len;
@@ -665,6 +683,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     float* jl = jm + Cfg::WARPS * 16;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+        if (g + 8 * r >= live) continue;
         float* dst = js + (warp * 16 + g + 8 * r) * D;
 #pragma unroll
         for (int c = 0; c < VC; ++c)
@@ -682,13 +701,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     }
     __syncthreads();
     // A thread takes 4 columns of a row at a time; D / 4 threads a row.
-    for (int x = tid; x < 16 * (D / 4); x += Cfg::THREADS) {
+    for (int x = tid; x < live * (D / 4); x += Cfg::THREADS) {
         const int rr = x / (D / 4), c4 = x % (D / 4);
-        const int r = tile * 16 + rr;
-        if (r >= rows) continue;
-        const int per = p.Nq * p.G;
-        const int b = prefix ? r / per : seq, i = (prefix ? r % per : r) / p.G, h = kvh * p.G + r % p.G;
-        const long long out = (static_cast<long long>(b) * p.Nq + i) * p.H + h;
+        long long out;
+        int lse_at;
+        row_of(rr, out, lse_at);
         float mm = jm[rr];
 #pragma unroll
         for (int w = 1; w < Cfg::WARPS; ++w) mm = fmaxf(mm, jm[w * 16 + rr]);
@@ -715,7 +732,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         if constexpr (DIRECT) {
             reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + out * D)[c4] =
                 make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-            if (c4 == 0) p.lse[(static_cast<long long>(b) * p.H + h) * p.Nq + i] = lse2 * 0.69314718055994530942f;
+            if (c4 == 0) p.lse[lse_at] = lse2 * 0.69314718055994530942f;
         } else {
             const long long pr = static_cast<long long>(prefix ? part : p.prefix_parts + part) *
                                      (static_cast<long long>(p.B) * p.Nq * p.H) + out;
