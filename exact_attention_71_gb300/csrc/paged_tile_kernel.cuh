@@ -53,6 +53,7 @@ enum : int {
     SITE_TILE_SCALE = 0xa7,
     SITE_TILE_LOADED = 0xa8,
     SITE_TILE_DRAIN = 0xa9,
+    SITE_TILE_TURN = 0xaa,
 };
 
 template <int D_, bool FP8_>
@@ -106,6 +107,7 @@ struct TileBarriers {
     float q_log2[128 * 2];         // e4m3: raw score -> log2 units, per query row
     uint32_t tmem_base;
     int abort_flag;
+    int turn;                      // blocks of products issued
 };
 
 // Bounded wait: false when the shared abort flag is raised or the cycle budget
@@ -127,6 +129,27 @@ __device__ __forceinline__ bool tile_wait(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ bool tile_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                                const PagedParams& p, int site) {
     return __all_sync(0xffffffffu, tile_wait(bar, parity, abort_flag, p, site));
+}
+
+// Bounded wait (whole warp) until `k` blocks of products have been issued.
+__device__ __forceinline__ bool tile_turn(volatile int* turn, int k, volatile int* abort_flag, const PagedParams& p) {
+    bool ok = true;
+    if (*turn < k) {
+        const long long t0 = clock64();
+        while (*turn < k) {
+            if (*abort_flag) {
+                ok = false;
+                break;
+            }
+            if (static_cast<unsigned long long>(clock64() - t0) > p.wait_limit) {
+                *abort_flag = 1;
+                atomicCAS(p.status, 0, SITE_TILE_TURN);
+                ok = false;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
 }
 
 // Teardown wait for the CTA's own asynchronous work, which always completes: it
@@ -178,6 +201,18 @@ __device__ __noinline__ void fix_v_tile(uint8_t* tile, uint32_t copies, int log2
         if (bad) atomicOr(&poison[r >> 5], 1u << (r & 31));
     }
     __syncwarp();
+}
+
+// Lane r's value of row r, from the accumulator layout (v[i] of the threads
+// 4 q .. 4 q + 3 belongs to row q + 8 i).
+__device__ __forceinline__ float to_row(const float (&v)[4], int lane) {
+    float r = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float x = __shfl_sync(0xffffffffu, v[i], (lane & 7) * 4);
+        if ((lane >> 3) == i) r = x;
+    }
+    return r;
 }
 
 // What a CTA computes; every role derives it alike.
@@ -371,6 +406,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             for (int x = 0; x < 4; ++x) bars->poison[s][x] = 0;
         }
         bars->abort_flag = 0;
+        bars->turn = 0;
         fence_barrier_init();
         fence_proxy_async_smem();
     }
@@ -387,61 +423,67 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         regs_decrease<Cfg::LOW_REGS>();
         if (warp >= Cfg::MMA_WARP && warp < Cfg::MMA_WARP + NS) {
             // -------------------------------------------------------- MMA issuers
-            // Step u of a stream: O += P(u-1) V(u-1), then S(u).  In pair mode
-            // both warps release every ring entry, always after waiting for it.
+            // Step u of a stream: O += P(u-1) V(u-1), then S(u), as one block.
+            // The streams' blocks go to the tensor pipe in turns, so that one
+            // stream's softmax runs beside the other's block (without turns the
+            // two interleave, finish together and leave the pipe idle while both
+            // exponentiate: 3350 cycles a step).  What a block waits for is
+            // awaited before its turn.  In pair mode both warps release every
+            // ring entry, always after waiting for it.
             constexpr uint32_t fmt = FP8 ? 0u : 1u;            // fp16 or bf16 operands
             constexpr uint32_t idesc_s = make_idesc(fmt, 128, BN, 0), idesc_o = make_idesc(fmt, 128, D, 1);
             const int t = warp - Cfg::MMA_WARP;
             const int nt = t == 0 ? w.n[0] : w.n[1];
-            const int n = w.pair ? max(w.n[0], w.n[1]) : nt;
+            const int rounds = max(w.n[0], w.n[1]);
+            const int n = w.pair ? rounds : nt;
             const uint32_t ring = smem_u32(sRing);
             const uint32_t s_tmem = tmem + t * 128, o_tmem = tmem + 256 + t * D;
             const uint64_t qd = sdesc_sw128(smem_u32(sQ) + (w.pair ? t : 0) * Cfg::Q_BYTES, 16, 1024);
+            volatile int* turn = &bars->turn;
             bool ok = n == 0 || tile_warp_wait(&bars->q_full, 0, abort_flag, p, SITE_TILE_Q);
-            for (int u = 0; u <= n && ok; ++u) {
-                if (u > 0) {
-                    const uint32_t x = tile_entry<Cfg>(w, t, u, true);
-                    ok = tile_warp_wait(&bars->ring_full[x % NH], (x / NH) & 1, abort_flag, p, SITE_TILE_FULL);
-                    if (!ok) break;
-                    if (u <= nt) {
-                        ok = tile_warp_wait(&bars->p_full[t], (u - 1) & 1, abort_flag, p, SITE_TILE_P);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t vd = sdesc_sw128(ring + (x % NH) * Cfg::HALF_BYTES, BN * 128, 1024);
-                        if (elect_one()) {
+            for (int u = 0; u <= rounds && ok; ++u) {
+                const bool has_v = u > 0 && u <= n, has_k = u < n;
+                const uint32_t xv = tile_entry<Cfg>(w, t, u, true), xk = tile_entry<Cfg>(w, t, u, false);
+                if (has_v) ok = tile_warp_wait(&bars->ring_full[xv % NH], (xv / NH) & 1, abort_flag, p, SITE_TILE_FULL);
+                if (ok && has_k) ok = tile_warp_wait(&bars->ring_full[xk % NH], (xk / NH) & 1, abort_flag, p, SITE_TILE_FULL);
+                if (ok && u > 0 && u <= nt) ok = tile_warp_wait(&bars->p_full[t], (u - 1) & 1, abort_flag, p, SITE_TILE_P);
+                if (NS > 1 && ok) ok = tile_turn(turn, 2 * u + t, abort_flag, p);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    if (has_v) {
+                        if (u <= nt) {
+                            const uint64_t vd = sdesc_sw128(ring + (xv % NH) * Cfg::HALF_BYTES, BN * 128, 1024);
 #pragma unroll
                             for (int kk = 0; kk < BN / 16; ++kk)
                                 mma_f16_ts(o_tmem, s_tmem + kk * 8, vd + ((kk * 16 * 128) >> 4), idesc_o,
                                            (kk > 0 || u > 1) ? 1u : 0u);
                             if (u == nt) mma_commit(&bars->o_full[t]);
-                            mma_commit(&bars->ring_empty[x % NH]);
+                            mma_commit(&bars->ring_empty[xv % NH]);
+                        } else {
+                            mbar_arrive(&bars->ring_empty[xv % NH]);
                         }
-                    } else if (elect_one()) {
-                        mbar_arrive(&bars->ring_empty[x % NH]);
                     }
-                    __syncwarp();
-                }
-                if (u < n) {
-                    const uint32_t x = tile_entry<Cfg>(w, t, u, false);
-                    ok = tile_warp_wait(&bars->ring_full[x % NH], (x / NH) & 1, abort_flag, p, SITE_TILE_FULL);
-                    if (!ok) break;
-                    if (u < nt) {
-                        tc_fence_after();
-                        const uint64_t kd = sdesc_sw128(ring + (x % NH) * Cfg::HALF_BYTES, 16, 1024);
-                        if (elect_one()) {
+                    if (has_k) {
+                        if (u < nt) {
+                            const uint64_t kd = sdesc_sw128(ring + (xk % NH) * Cfg::HALF_BYTES, 16, 1024);
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint32_t a = (kk / 4) * (BM * 128) + (kk % 4) * 32, b = (kk / 4) * (BN * 128) + (kk % 4) * 32;
                                 mma_f16_ss(s_tmem, qd + (a >> 4), kd + (b >> 4), idesc_s, kk > 0 ? 1u : 0u);
                             }
                             mma_commit(&bars->s_full[t]);
-                            mma_commit(&bars->ring_empty[x % NH]);
+                            mma_commit(&bars->ring_empty[xk % NH]);
+                        } else {
+                            mbar_arrive(&bars->ring_empty[xk % NH]);
                         }
-                    } else if (elect_one()) {
-                        mbar_arrive(&bars->ring_empty[x % NH]);
                     }
-                    __syncwarp();
+                    if (NS > 1) {
+                        __threadfence_block();
+                        *turn = 2 * u + t + 1;
+                    }
                 }
+                __syncwarp();
             }
             // Every MMA issued here has finished before teardown.
             if (elect_one()) {
@@ -553,22 +595,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         regs_decrease<Cfg::CONV_REGS>();
         if constexpr (FP8) {
             // ---------------------------------------------------- converting warps
-            // A thread's chunks (16 codes) lie in rows r0 + i * RPP.  For d >= 128 a
-            // quarter warp takes half of the chunk columns of two neighbouring
-            // rows: its two stores per chunk (16-byte columns 2c and 2c + 1 of
-            // the swizzle) then each cover all eight columns once.
+            // A thread's chunks (16 codes, column c) lie in rows r0 + i * RPP.  Its two
+            // stores per chunk go to 16-byte columns 2c and 2c + 1 of the swizzle;
+            // threads with c % 8 >= 4 do the second first, so that a quarter
+            // warp's store covers all eight columns once.
             constexpr int CPR = D / 16;                         // chunks of a row
             constexpr int RPP = 128 / CPR;                      // rows per pass of the 128 threads
             const int ct = tid - Cfg::CONV_WARP * 32;
-            int c, r0;
-            if constexpr (D == 64) {
-                c = ct % CPR;
-                r0 = ct / CPR;
-            } else {
-                constexpr int G4 = CPR / 4;                     // groups of four chunk columns
-                c = (ct & 3) + ((ct >> 3) % G4) * 4;
-                r0 = ((ct >> 2) & 1) + (ct >> 3) / G4 * 2;
-            }
+            const int c = ct % CPR, r0 = ct / CPR;
+            const bool odd = D != 64 && (c & 4);
             uint32_t e = 0;
             float vref0 = 0.0f, vref1 = 0.0f;                   // per stream (pair: the first)
             tile_entries<Cfg>(w, [&](int t, int u, bool is_v) -> bool {
@@ -635,10 +670,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                                 if (nan) atomicOr(&poison[r >> 5], 1u << (r & 31));
                             }
                         }
-                        *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c)) =
-                            make_uint4(f16x2_of_lo(v.x), f16x2_of_hi(v.x), f16x2_of_lo(v.y), f16x2_of_hi(v.y));
-                        *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c + 1)) =
-                            make_uint4(f16x2_of_lo(v.z), f16x2_of_hi(v.z), f16x2_of_lo(v.w), f16x2_of_hi(v.w));
+                        const uint4 lo = make_uint4(f16x2_of_lo(v.x), f16x2_of_hi(v.x), f16x2_of_lo(v.y), f16x2_of_hi(v.y));
+                        const uint4 hi = make_uint4(f16x2_of_lo(v.z), f16x2_of_hi(v.z), f16x2_of_lo(v.w), f16x2_of_hi(v.w));
+                        *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c + odd)) = odd ? hi : lo;
+                        *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c + !odd)) = odd ? lo : hi;
                     }
                 };
                 if (whole && !(is_v && diagonal)) convert(std::false_type{});
@@ -658,7 +693,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const uint32_t s_tmem = tmem + lane_off + t * 128, o_tmem = tmem + lane_off + 256 + t * D;
         const int nt = t == 0 ? w.n[0] : w.n[1];
         const int j0 = t == 0 ? w.j0[0] : w.j0[1], part = t == 0 ? w.part[0] : w.part[1];
-        const int limit = in ? row_limit(p, w, row) : 0;
+        const int limit = in ? row_limit(p, w, row) : w.len;   // (a row that is not there needs no mask)
         cp_async_wait<0>();
         if constexpr (FP8) {
             // To fp16 in place, each lane the chunks that it brought in.
@@ -681,7 +716,18 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
         fence_proxy_async_smem();
         mbar_arrive(&bars->q_full);
-        float to_log2 = p.scale_log2, vref = 0.0f;
+        // e4m3: rows lane / 4 + 8 i of the warp's 32 (see below).
+        float vref = 0.0f;
+        float tl4[4], m4[4], l4[4];
+        int limit4[4];
+        if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                tl4[i] = l4[i] = 0.0f;
+                m4[i] = -INFINITY;
+                limit4[i] = __shfl_sync(0xffffffffu, limit, (lane >> 2) + 8 * i);
+            }
+        }
         float m = -INFINITY, l = 0.0f;
         bool ok = true;
         for (int u = 0; u < nt; ++u) {
@@ -695,113 +741,223 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 break;
             }
             tc_fence_after();
-            float vfall = 1.0f;                // O is in units of vref
             if constexpr (FP8) {
-                if (u == 0) to_log2 = bars->q_log2[(w.pair ? t * 128 : 0) + (tid & 127)];
+                // A key's scales are common to all rows: in the accumulator layout
+                // (a thread has four rows and two of every eight columns) it reads a
+                // quarter of them; one row a thread read 512 bytes of K scales and 512
+                // of V scales a tile, which with the conversion's traffic bounded the
+                // kernel by shared memory (6300 cycles a step of two tiles).
+                float vfall = 1.0f;                // O is in units of vref
+                if (u == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        tl4[i] = bars->q_log2[(w.pair ? t * 128 : 0) + (warp & 3) * 32 + (lane >> 2) + 8 * i];
+                }
                 const float now = bars->vref[slot];
                 if (now != vref) {
                     vfall = vref * (1.0f / now);
                     vref = now;
                 }
-            }
-            uint32_t sr[BN];
+                constexpr int NG = BN / 8;
+                uint32_t sr[8 * NG];               // (half of the rows, group, row bit, column bit)
 #pragma unroll
-            for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_tmem + c * 32, sr + c * 32);
-            tmem_wait_ld();
+                for (int h = 0; h < 2; ++h) tmem_ld_frag<NG>(s_tmem + (static_cast<uint32_t>(16 * h) << 16), sr + h * 4 * NG);
+                tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < BN / 32; ++c) reg_fence32(sr + c * 32);
-            if constexpr (FP8) {
-                const float4* ks = reinterpret_cast<const float4*>(sScale + slot * 2 * BN);
+                for (int x = 0; x < 8 * NG; x += 32) reg_fence32(sr + x);
+                const float2* ks = reinterpret_cast<const float2*>(sScale + slot * 2 * BN) + (lane & 3);
+                const float2* vs = ks + BN / 2;
+                const int key0 = (j0 + u) * BN;
+                uint32_t all = 0xffffffffu;
 #pragma unroll
-                for (int x = 0; x < BN; x += 4) {
-                    const float4 k4 = ks[x / 4];
-                    const float2 v0 = __fmul2_rn(make_float2(__uint_as_float(sr[x]), __uint_as_float(sr[x + 1])), make_float2(k4.x, k4.y));
-                    const float2 v1 = __fmul2_rn(make_float2(__uint_as_float(sr[x + 2]), __uint_as_float(sr[x + 3])), make_float2(k4.z, k4.w));
-                    sr[x] = __float_as_uint(v0.x);
-                    sr[x + 1] = __float_as_uint(v0.y);
-                    sr[x + 2] = __float_as_uint(v1.x);
-                    sr[x + 3] = __float_as_uint(v1.y);
-                }
-            }
-            const int key0 = (j0 + u) * BN;
-            uint32_t seen[BN / 32];
-            uint32_t all = 0xffffffffu;
+                for (int c = 0; c < BN / 32; ++c) all &= bars->valid[slot][c];
+                const int low = min(min(limit4[0], limit4[1]), min(limit4[2], limit4[3]));
+                const bool masked = __any_sync(0xffffffffu, all != 0xffffffffu || key0 + BN > low);
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < BN / 32; ++c) {
-                const int n = min(max(limit - key0 - c * 32, 0), 32);
-                seen[c] = bars->valid[slot][c] & (n == 32 ? 0xffffffffu : (1u << n) - 1u);
-                all &= seen[c];
-            }
-            const bool masked = __any_sync(0xffffffffu, all != 0xffffffffu);
-            if (masked) {
+                for (int g = 0; g < NG; ++g) {
+                    const float2 k2 = ks[4 * g];
 #pragma unroll
-                for (int x = 0; x < BN; ++x)
-                    if (!((seen[x / 32] >> (x % 32)) & 1u)) sr[x] = 0xff800000u;
-            }
-            float mx0 = __uint_as_float(sr[0]), mx1 = __uint_as_float(sr[1]);
-            float mx2 = __uint_as_float(sr[2]), mx3 = __uint_as_float(sr[3]);
-#pragma unroll
-            for (int c = 4; c + 8 <= BN; c += 8) {
-                mx0 = fmax3(mx0, __uint_as_float(sr[c + 0]), __uint_as_float(sr[c + 1]));
-                mx1 = fmax3(mx1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
-                mx2 = fmax3(mx2, __uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5]));
-                mx3 = fmax3(mx3, __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
-            }
-            mx0 = fmax3(mx0, mx1, __uint_as_float(sr[BN - 4]));
-            mx2 = fmax3(mx2, mx3, __uint_as_float(sr[BN - 3]));
-            const float mx = fmax3(mx0, mx2, fmaxf(__uint_as_float(sr[BN - 2]), __uint_as_float(sr[BN - 1]))) * to_log2;
-            // The reference moves only by jumps of more than 8 (log2 units).
-            float mn = m;
-            if (mx > m + 8.0f) mn = mx;
-            const float ref = mn == -INFINITY ? 0.0f : mn;
-            const float alpha = mn == m ? 1.0f : ex2_approx(m - ref);
-            const float2 mul2 = make_float2(to_log2, to_log2), neg2 = make_float2(-ref, -ref);
-            float2 acc0 = make_float2(0.0f, 0.0f), acc1 = make_float2(0.0f, 0.0f);
-            const float4* vs = reinterpret_cast<const float4*>(sScale + slot * 2 * BN + BN);
-#pragma unroll
-            for (int c = 0; c < BN / 32; ++c) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int x = 0; x < 16; x += 2) {
-                    const int e = c * 32 + 2 * x;
-                    float2 f = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), mul2, neg2);
-                    float2 g = __ffma2_rn(make_float2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])), mul2, neg2);
-                    f.x = ex2_approx(f.x);
-                    f.y = ex2_approx(f.y);
-                    g.x = ex2_approx(g.x);
-                    g.y = ex2_approx(g.y);
-                    acc0 = __fadd2_rn(acc0, f);
-                    acc1 = __fadd2_rn(acc1, g);
-                    if constexpr (FP8) {
-                        // V's row scale rides on P; l sums the plain weights.
-                        const float4 v4 = vs[e / 4];
-                        f = __fmul2_rn(f, make_float2(v4.x, v4.y));
-                        g = __fmul2_rn(g, make_float2(v4.z, v4.w));
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t* e = sr + (i >> 1) * 4 * NG + g * 4 + (i & 1) * 2;
+                        const float2 v = __fmul2_rn(make_float2(__uint_as_float(e[0]), __uint_as_float(e[1])), k2);
+                        e[0] = __float_as_uint(v.x);
+                        e[1] = __float_as_uint(v.y);
                     }
-                    pk[x] = FP8 ? pack_f16x2(f.x, f.y) : pack_bf16x2(f.x, f.y);
-                    pk[x + 1] = FP8 ? pack_f16x2(g.x, g.y) : pack_bf16x2(g.x, g.y);
                 }
-                tmem_st16(s_tmem + c * 16, pk);
-            }
-            l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y));
-            const float fall = FP8 ? alpha * vfall : alpha;
-            if (u > 0 && __any_sync(0xffffffffu, fall != 1.0f)) {
-                // The commit that signalled S(u) covers O += P(u-1) V(u-1).
+                if (masked) {
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(o_tmem + c * 32, o);
-                    tmem_wait_ld();
-                    reg_fence32(o);
+                    for (int g = 0; g < NG; ++g) {
+                        const int key = 8 * g + 2 * (lane & 3);
+                        const uint32_t bits = bars->valid[slot][g / 4] >> (key & 31);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fall);
-                    tmem_st32(o_tmem + c * 32, o);
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t* e = sr + (i >> 1) * 4 * NG + g * 4 + (i & 1) * 2;
+                            if (!(bits & 1u) || key0 + key >= limit4[i]) e[0] = 0xff800000u;
+                            if (!(bits & 2u) || key0 + key + 1 >= limit4[i]) e[1] = 0xff800000u;
+                        }
+                    }
                 }
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t* e = sr + (i >> 1) * 4 * NG + g * 4 + (i & 1) * 2;
+                        mx[i] = fmax3(mx[i], __uint_as_float(e[0]), __uint_as_float(e[1]));
+                    }
+                // The references move only by jumps of more than 8 (log2 units), per
+                // row; O and l share them.
+                bool move = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mx[i] *= tl4[i];
+                    move = move || mx[i] > m4[i] + 8.0f;
+                }
+                float fall4[4] = {vfall, vfall, vfall, vfall};
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+                        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+                        const float mn = mx[i] > m4[i] + 8.0f ? mx[i] : m4[i];
+                        const float a = mn == m4[i] ? 1.0f : ex2_approx(m4[i] - mn);
+                        m4[i] = mn;
+                        l4[i] *= a;
+                        fall4[i] *= a;
+                    }
+                }
+                float2 acc[4];
+                float2 neg[4], mul[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float ref = m4[i] == -INFINITY ? 0.0f : m4[i];
+                    neg[i] = make_float2(-ref, -ref);
+                    mul[i] = make_float2(tl4[i], tl4[i]);
+                    acc[i] = make_float2(0.0f, 0.0f);
+                }
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    // V's row scale rides on P; l sums the plain weights.
+                    const float2 v2 = vs[4 * g];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t* e = sr + (i >> 1) * 4 * NG + g * 4 + (i & 1) * 2;
+                        float2 f = __ffma2_rn(make_float2(__uint_as_float(e[0]), __uint_as_float(e[1])), mul[i], neg[i]);
+                        f.x = ex2_approx(f.x);
+                        f.y = ex2_approx(f.y);
+                        acc[i] = __fadd2_rn(acc[i], f);
+                        f = __fmul2_rn(f, v2);
+                        // (packed into the half's first registers: all of it is read by now)
+                        sr[(i >> 1) * 4 * NG + g * 2 + (i & 1)] = pack_f16x2(f.x, f.y);
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) tmem_st_frag<NG>(s_tmem + (static_cast<uint32_t>(16 * h) << 16), sr + h * 4 * NG);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) l4[i] += acc[i].x + acc[i].y;
+                const bool fell = fall4[0] != 1.0f || fall4[1] != 1.0f || fall4[2] != 1.0f || fall4[3] != 1.0f;
+                if (u > 0 && __any_sync(0xffffffffu, fell)) {
+                    // O's rows lie one per lane.
+                    const float fall = to_row(fall4, lane);
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o_tmem + c * 32, o);
+                        tmem_wait_ld();
+                        reg_fence32(o);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fall);
+                        tmem_st32(o_tmem + c * 32, o);
+                    }
+                }
+            } else {
+                uint32_t sr[BN];
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c) tmem_ld32(s_tmem + c * 32, sr + c * 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c) reg_fence32(sr + c * 32);
+                const int key0 = (j0 + u) * BN;
+                uint32_t seen[BN / 32];
+                uint32_t all = 0xffffffffu;
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c) {
+                    const int n = min(max(limit - key0 - c * 32, 0), 32);
+                    seen[c] = bars->valid[slot][c] & (n == 32 ? 0xffffffffu : (1u << n) - 1u);
+                    all &= seen[c];
+                }
+                const bool masked = __any_sync(0xffffffffu, all != 0xffffffffu);
+                if (masked) {
+#pragma unroll
+                    for (int x = 0; x < BN; ++x)
+                        if (!((seen[x / 32] >> (x % 32)) & 1u)) sr[x] = 0xff800000u;
+                }
+                float mx0 = __uint_as_float(sr[0]), mx1 = __uint_as_float(sr[1]);
+                float mx2 = __uint_as_float(sr[2]), mx3 = __uint_as_float(sr[3]);
+#pragma unroll
+                for (int c = 4; c + 8 <= BN; c += 8) {
+                    mx0 = fmax3(mx0, __uint_as_float(sr[c + 0]), __uint_as_float(sr[c + 1]));
+                    mx1 = fmax3(mx1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+                    mx2 = fmax3(mx2, __uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5]));
+                    mx3 = fmax3(mx3, __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
+                }
+                mx0 = fmax3(mx0, mx1, __uint_as_float(sr[BN - 4]));
+                mx2 = fmax3(mx2, mx3, __uint_as_float(sr[BN - 3]));
+                const float mx = fmax3(mx0, mx2, fmaxf(__uint_as_float(sr[BN - 2]), __uint_as_float(sr[BN - 1]))) * p.scale_log2;
+                // The reference moves only by jumps of more than 8 (log2 units).
+                float mn = m;
+                if (mx > m + 8.0f) mn = mx;
+                const float ref = mn == -INFINITY ? 0.0f : mn;
+                const float alpha = mn == m ? 1.0f : ex2_approx(m - ref);
+                const float2 mul2 = make_float2(p.scale_log2, p.scale_log2), neg2 = make_float2(-ref, -ref);
+                float2 acc0 = make_float2(0.0f, 0.0f), acc1 = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int x = 0; x < 16; x += 2) {
+                        const int e = c * 32 + 2 * x;
+                        float2 f = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), mul2, neg2);
+                        float2 g = __ffma2_rn(make_float2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])), mul2, neg2);
+                        f.x = ex2_approx(f.x);
+                        f.y = ex2_approx(f.y);
+                        g.x = ex2_approx(g.x);
+                        g.y = ex2_approx(g.y);
+                        acc0 = __fadd2_rn(acc0, f);
+                        acc1 = __fadd2_rn(acc1, g);
+                        pk[x] = pack_bf16x2(f.x, f.y);
+                        pk[x + 1] = pack_bf16x2(g.x, g.y);
+                    }
+                    tmem_st16(s_tmem + c * 16, pk);
+                }
+                l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y));
+                if (u > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+                    // The commit that signalled S(u) covers O += P(u-1) V(u-1).
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o_tmem + c * 32, o);
+                        tmem_wait_ld();
+                        reg_fence32(o);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
+                        tmem_st32(o_tmem + c * 32, o);
+                    }
+                }
+                m = mn;
             }
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bars->p_full[t]);
-            m = mn;
+        }
+        if constexpr (FP8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                l4[i] += __shfl_xor_sync(0xffffffffu, l4[i], 1);
+                l4[i] += __shfl_xor_sync(0xffffffffu, l4[i], 2);
+            }
+            l = to_row(l4, lane);
+            m = to_row(m4, lane);
         }
         const long long rows_all = static_cast<long long>(p.B) * p.Nq * p.H;
         if (ok && nt > 0) {
