@@ -1172,7 +1172,7 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
     }
     if (e == cudaSuccess && (plan.prefix_stream || plan.own_items == 0)) {
         if ((rc = make_cache_maps(&maps, k_cache, v_cache, num_pages, H_kv, page_size, d, es, 16)) != ATTN_OK) return rc;
-        e = rows(maps, p, plan.prefix_stream, plan.own_items == 0, plan.direct, s);
+        e = rows(maps, p, plan.prefix_stream, plan.own_items == 0, plan.direct, plan.prefix_items + plan.own_items > 0, s);
     }
     if (e == cudaSuccess && !plan.direct) e = attn::run_paged_merge(p, s);
     if (e != cudaSuccess) return cuda_fail(e, "attn_fwd_paged launch");

@@ -16,6 +16,7 @@
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
+#include <utility>
 
 namespace attn {
 
@@ -132,6 +133,25 @@ inline cudaError_t once_per_device(std::atomic<unsigned long long>& done, F&& se
     return cudaSuccess;
 }
 
+// Launches `kernel`; after: it follows a kernel of the same call on this stream and
+// may start before that one has ended (it calls wait_prerequisites itself where
+// it needs the results).
+template <class... Params, class... Args>
+inline cudaError_t launch_kernel(void (*kernel)(Params...), unsigned grid, unsigned threads, unsigned smem, bool after,
+                                 cudaStream_t stream, Args&&... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = after ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 cudaError_t run_kv_write(const KvWriteParams& p, cudaStream_t stream);
 cudaError_t run_kv_read(const KvReadParams& p, cudaStream_t stream);
 // K and V of the cache as 4-D {d, page_size, H_kv, num_pages} tensors.  Box of the
@@ -142,12 +162,13 @@ struct PagedMaps {
 };
 
 // The streaming kernel over the prefix and / or the own tokens, one translation
-// unit per head dim; direct: it writes o and lse itself.
-cudaError_t run_paged_stream_d64(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct,
+// unit per head dim; direct: it writes o and lse itself; after: the tile kernel
+// runs before it.
+cudaError_t run_paged_stream_d64(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct, bool after,
                                  cudaStream_t stream);
-cudaError_t run_paged_stream_d128(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct,
+cudaError_t run_paged_stream_d128(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct, bool after,
                                   cudaStream_t stream);
-cudaError_t run_paged_stream_d256(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct,
+cudaError_t run_paged_stream_d256(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct, bool after,
                                   cudaStream_t stream);
 // The tile kernel over its prefix_items and own_items.
 cudaError_t run_paged_tile_d64(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream);

@@ -10,7 +10,7 @@
 #include <algorithm>
 
 #include "paged.cuh"
-#include "sm103_ptx.cuh"
+#include "sm103_bulk.cuh"
 
 namespace attn {
 
@@ -92,43 +92,50 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
 
 namespace {
 
-// W warps per row, D / 32 columns a lane; a warp takes the parts w, w + W, ..,
-// four at a time (independent loads), and the warps' sums meet in shared
-// memory.  The weights are computed once per part, by the lanes.
+// W warps per row, D / 32 columns a lane; lane x of a warp has the weight of part
+// 32 k + x; the warp sums the parts x = w, w + W, .., four at a time (independent
+// loads), and the warps' sums meet in shared memory.
 template <int D, int W>
-__global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ PagedParams p) {
     constexpr int V = D / 32;
-    __shared__ float joined[4][D + 1];
+    __shared__ float joined[4][D];
     const long long rows = static_cast<long long>(p.B) * p.Nq * p.H;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long row = static_cast<long long>(blockIdx.x) * (4 / W) + warp / W;
     const int w = warp % W;
     const int parts = p.prefix_parts + p.own_parts;
     const bool in = row < rows;
+    wait_prerequisites();
     float sum = 0.0f, ref = 0.0f, acc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
     if (in) {
-        float mm = -INFINITY;
-        for (int x = lane; x < parts; x += 32) mm = fmaxf(mm, p.part_lse[x * rows + row]);
+        // (128 parts at most: a prefix and a sequence have 64 each)
+        float l2[4], mm = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int x = 32 * k + lane;
+            l2[k] = x < parts ? p.part_lse[x * rows + row] : -INFINITY;
+            mm = fmaxf(mm, l2[k]);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
         ref = mm == -INFINITY ? 0.0f : mm;
-        for (int base = 0; base < parts; base += 32 * W) {
-            // lane x holds the weight of part base + x * W + w
-            const int mine = base + lane * W + w;
-            const float l2 = mine < parts ? p.part_lse[mine * rows + row] : -INFINITY;
-            const float wt = l2 == -INFINITY ? 0.0f : ex2_approx(l2 - ref);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (32 * k >= parts) break;
+            const float wt = l2[k] == -INFINITY ? 0.0f : ex2_approx(l2[k] - ref);
             sum += wt;
-            const int n = min(32, (parts - base - w + W - 1) / W);
-            for (int x = 0; x < n; x += 4) {
+            const int n = min(32, parts - 32 * k);
+            for (int x = w; x < n; x += 4 * W) {
                 float f[4][V], g[4];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    g[y] = __shfl_sync(0xffffffffu, wt, (x + y) & 31);
-                    if (x + y >= n) g[y] = 0.0f;
+                    const int at = x + y * W;
+                    g[y] = __shfl_sync(0xffffffffu, wt, at & 31);
+                    if (at >= n) g[y] = 0.0f;
                     // an empty part's O was not written: it is not read
-                    const float* src = p.part_o + (static_cast<long long>(base + (x + y) * W + w) * rows + row) * D + lane * V;
+                    const float* src = p.part_o + (static_cast<long long>(32 * k + at) * rows + row) * D + lane * V;
 #pragma unroll
                     for (int v = 0; v < V; ++v) f[y][v] = 0.0f;
                     if (g[y] != 0.0f) {
@@ -160,15 +167,12 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
     if constexpr (W > 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) joined[warp][lane * V + v] = acc[v];
-        if (lane == 0) joined[warp][D] = sum;
         __syncthreads();
         if (w != 0) return;
 #pragma unroll
-        for (int x = 1; x < W; ++x) {
+        for (int x = 1; x < W; ++x)
 #pragma unroll
             for (int v = 0; v < V; ++v) acc[v] += joined[warp + x][lane * V + v];
-            sum += joined[warp + x][D];
-        }
     }
     if (!in) return;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -176,11 +180,9 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const PagedParams p) {
 #pragma unroll
     for (int v = 0; v < V; v += 2) dst[v / 2] = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
     if (lane == 0) {
-        const int h = static_cast<int>(row % p.H);
-        const long long bi = row / p.H;
-        const int i = static_cast<int>(bi % p.Nq), b = static_cast<int>(bi / p.Nq);
-        p.lse[(static_cast<long long>(b) * p.H + h) * p.Nq + i] =
-            sum == 0.0f ? -INFINITY : (ref + __log2f(sum)) * 0.69314718055994530942f;
+        const unsigned r = static_cast<unsigned>(row);
+        const unsigned h = r % p.H, bi = r / p.H, i = bi % p.Nq, b = bi / p.Nq;
+        p.lse[(b * p.H + h) * p.Nq + i] = sum == 0.0f ? -INFINITY : (ref + __log2f(sum)) * 0.69314718055994530942f;
     }
 }
 
@@ -189,9 +191,9 @@ cudaError_t merge_d(const PagedParams& p, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.B) * p.Nq * p.H;
     // A warp sums 8 parts in two rounds of loads; with more, four warps share
     // a row.
-    if (p.prefix_parts + p.own_parts > 8) paged_merge_kernel<D, 4><<<static_cast<unsigned>(rows), 128, 0, stream>>>(p);
-    else paged_merge_kernel<D, 1><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (p.prefix_parts + p.own_parts > 8)
+        return launch_kernel(paged_merge_kernel<D, 4>, static_cast<unsigned>(rows), 128, 0, true, stream, p);
+    return launch_kernel(paged_merge_kernel<D, 1>, static_cast<unsigned>((rows + 3) / 4), 128, 0, true, stream, p);
 }
 
 }  // namespace

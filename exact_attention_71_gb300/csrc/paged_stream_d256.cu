@@ -3,9 +3,9 @@
 
 namespace attn {
 
-cudaError_t run_paged_stream_d256(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct,
+cudaError_t run_paged_stream_d256(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct, bool after,
                                  cudaStream_t stream) {
-    return launch_paged_stream<256>(m, p, prefix, own, direct, stream);
+    return launch_paged_stream<256>(m, p, prefix, own, direct, after, stream);
 }
 
 }  // namespace attn

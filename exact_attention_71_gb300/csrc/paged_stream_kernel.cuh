@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     const int pig = PI ? (g >> 1) | ((g & 1) << 2) : g;            // K row, V chunk
     const int ka = PI ? t : 2 * t, kb = PI ? t + 4 : 2 * t + 1;    // keys of S columns 2t, 2t + 1
 
+    launch_dependents();
     unsigned x0 = blockIdx.x;
     const bool prefix = !DIRECT && x0 < prefix_blocks;
     if (!prefix) x0 -= prefix_blocks;
@@ -741,6 +742,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             if (c4 == 0) p.part_lse[pr] = lse2;
         }
     }
+    // The join is launched after this kernel and waits for it alone, so this
+    // kernel does not end before the one before it (the tile kernel) has.
+    if (!DIRECT && blockIdx.x == gridDim.x - 1) wait_prerequisites();
 }
 
 }  // namespace attn

@@ -236,22 +236,22 @@ __device__ __forceinline__ int row_limit(const PagedParams& p, const TileItem& w
 template <class Cfg>
 __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
     TileItem w;
-    int x = blockIdx.x;
-    w.prefix = x < p.prefix_items;
+    unsigned x = blockIdx.x;
+    w.prefix = x < static_cast<unsigned>(p.prefix_items);
     if (!w.prefix) x -= p.prefix_items;
     const int per = p.Nq * p.G;
     w.rows = w.prefix ? p.B * per : per;
     const int tiles = (w.rows + Cfg::BM - 1) / Cfg::BM;
     w.pair = Cfg::NS == 2 && tiles > 1;
-    const int groups = w.pair ? (tiles + 1) / 2 : tiles;
+    const unsigned groups = w.pair ? (tiles + 1) / 2 : tiles;
     // Row groups of the same keys run next to one another.
     const int group = x % groups;
     x /= groups;
-    w.kvh = x % p.H_kv;
-    x /= p.H_kv;
+    w.kvh = x % static_cast<unsigned>(p.H_kv);
+    x /= static_cast<unsigned>(p.H_kv);
     // Streams that split a range count as two parts.
     const int per_cta = (Cfg::NS == 2 && !w.pair) ? 2 : 1;
-    const int ctas = w.prefix ? p.prefix_ctas : p.own_ctas;
+    const unsigned ctas = w.prefix ? p.prefix_ctas : p.own_ctas;
     const int split = x % ctas;
     w.seq = w.prefix ? 0 : x / ctas;
     w.table = w.prefix ? p.prefix_table : p.table + w.seq * p.table_stride;
@@ -265,7 +265,7 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
         }
     }
     w.len = len;
-    const int parts = ctas * per_cta;
+    const unsigned parts = ctas * per_cta;
     const int base = w.prefix ? 0 : p.prefix_parts;
     const int all = (len + Cfg::BN - 1) / Cfg::BN;
 #pragma unroll
@@ -279,9 +279,9 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
         if (w.rt[t] >= tiles) w.rt[t] = -1;
         const int part = w.pair || Cfg::NS == 1 ? split : 2 * split + t;
         w.part[t] = base + part;
-        // Even shares of the key tiles.
-        w.j0[t] = static_cast<int>(static_cast<long long>(all) * part / parts);
-        int j1 = static_cast<int>(static_cast<long long>(all) * (part + 1) / parts);
+        // Even shares of the key tiles (at most 2^24 of them, 128 parts).
+        w.j0[t] = static_cast<int>(static_cast<unsigned>(all) * part / parts);
+        int j1 = static_cast<int>(static_cast<unsigned>(all) * (part + 1) / parts);
         if (w.rt[t] >= 0) {
             // Tiles past what the tile's last row sees are left out.
             const int last = min(w.rt[t] * Cfg::BM + Cfg::BM, w.rows) - 1;
@@ -350,6 +350,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     volatile int* abort_flag = &bars->abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+    launch_dependents();           // (nothing of this call that follows reads what precedes it)
     const TileItem w = tile_item<Cfg>(p);
     // From this key on the CTA's rows may see different keys; its tile.
     int diag_key = w.len;
@@ -696,22 +697,22 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int limit = in ? row_limit(p, w, row) : w.len;   // (a row that is not there needs no mask)
         cp_async_wait<0>();
         if constexpr (FP8) {
-            // To fp16 in place, each lane the chunks that it brought in.
+            // To fp16 in place, one row a thread (the warp's own rows).
+            __syncwarp();
             if (w.pair || t == 0) {
-                constexpr int LPR = D / 8 < 32 ? D / 8 : 32;
-#pragma unroll 4
-                for (int x = 0; x < LPR; ++x) {
-                    const int rq = (warp & 3) * 32 + x * (32 / LPR) + lane / LPR, c = lane % LPR;
-                    uint4* at = reinterpret_cast<uint4*>(sQ + t * Cfg::Q_BYTES + (c >> 3) * (BM * 128) + rq * 128 +
-                                                         (((c & 7) ^ (rq & 7)) << 4));
-                    const uint4 v = *at;
-                    uint32_t top = bf16x8_amax(v);
+                const int rq = tid & 127;
+                uint8_t* tile = sQ + t * Cfg::Q_BYTES + rq * 128;
+                uint32_t top = 0;
 #pragma unroll
-                    for (int y = LPR / 2; y > 0; y >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
-                    const int shift = q_shift(top);
-                    *at = q_to_f16(v, pow2f(shift));
-                    if (c == 0) bars->q_log2[t * 128 + rq] = p.scale_log2 * pow2f(-shift);
+                for (int c = 0; c < D / 8; ++c)
+                    top = max(top, bf16x8_amax(*reinterpret_cast<const uint4*>(tile + (c >> 3) * (BM * 128) + (((c & 7) ^ (rq & 7)) << 4))));
+                const int shift = q_shift(top);
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * (BM * 128) + (((c & 7) ^ (rq & 7)) << 4));
+                    *at = q_to_f16(*at, pow2f(shift));
                 }
+                bars->q_log2[t * 128 + rq] = p.scale_log2 * pow2f(-shift);
             }
         }
         fence_proxy_async_smem();

@@ -20,8 +20,7 @@ cudaError_t launch_paged_tile_one(const PagedMaps& m, const PagedParams& p, cuda
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
     });
     if (e != cudaSuccess) return e;
-    kernel<<<p.prefix_items + p.own_items, Cfg::THREADS, Cfg::SMEM_BYTES, stream>>>(m.k, m.v, p);
-    return cudaGetLastError();
+    return launch_kernel(kernel, p.prefix_items + p.own_items, Cfg::THREADS, Cfg::SMEM_BYTES, false, stream, m.k, m.v, p);
 }
 
 template <int D>

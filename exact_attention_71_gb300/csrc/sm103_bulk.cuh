@@ -44,6 +44,13 @@ __device__ __forceinline__ void bulk_wait_group_read() {
 // Waits until every committed bulk group of this thread has completed.
 __device__ __forceinline__ void bulk_wait_group_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
+// Programmatic dependent launch: the next kernel of the stream, if it was launched
+// for it, may start once every CTA has called this (or left)...
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// ... and waits here until the kernel before it has completed and its writes are
+// visible (returns at once in a kernel launched without that attribute).
+__device__ __forceinline__ void wait_prerequisites() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Barrier `id` (1..15) among `count` threads (a multiple of 32).
 __device__ __forceinline__ void named_barrier(uint32_t id, uint32_t count) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
