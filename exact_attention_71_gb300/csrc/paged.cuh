@@ -114,6 +114,9 @@ constexpr int kOwnChunk = 128;
 constexpr int kStreamRows = 32;
 constexpr int kStreamPrefixRows = 16;
 
+// Key ranges of a prefix, and of a sequence's own tokens, at most.
+constexpr int kMaxParts = 256;
+
 // A streaming CTA's fixed cost, in keys.
 constexpr double kStreamFixed = 200.0;
 

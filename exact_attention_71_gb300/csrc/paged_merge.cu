@@ -21,10 +21,10 @@ long long up(long long a, long long b) { return (a + b - 1) / b; }
 // CTAs that share a row tile's keys (tile kernel, one CTA an SM): as few waves
 // x key tiles per CTA as possible, a CTA's fixed cost (query load, pipeline
 // fill, epilogue) counted as three key tiles.
-int tile_ctas(long long units, long long tiles) {
+int tile_ctas(long long units, long long tiles, int most) {
     int best = 1;
     long long best_cost = -1;
-    for (int s = 1; s <= 64 && s <= tiles; ++s) {
+    for (int s = 1; s <= most && s <= tiles; ++s) {
         const long long cost = up(units * s, kPlanSms) * (up(tiles, s) + 3);
         if (best_cost < 0 || cost < best_cost) {
             best = s;
@@ -48,7 +48,7 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     const auto stream_parts = [&](long long keys, long long units) {
         int best = 1;
         double best_cost = -1.0;
-        for (int s = 1; s <= 64 && (s == 1 || s * static_cast<long long>(kOwnChunk) < keys + kOwnChunk); ++s) {
+        for (int s = 1; s <= kMaxParts && (s == 1 || s * static_cast<long long>(kOwnChunk) < keys + kOwnChunk); ++s) {
             const double waves = static_cast<double>(units) * s / slots, cta = static_cast<double>(up(keys, s)) + kStreamFixed;
             const double cost = waves <= 1.0 ? cta : (waves + 0.5) * cta;
             if (best_cost < 0.0 || cost < best_cost) {
@@ -61,7 +61,7 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     if (rows > kStreamRows) {
         const long long tiles = up(rows, 128), groups = d == 256 ? tiles : up(tiles, 2);
         const bool alt = d != 256 && tiles == 1;
-        plan.own_ctas = tile_ctas(B * static_cast<long long>(H_kv) * groups, up(own, bn));
+        plan.own_ctas = tile_ctas(B * static_cast<long long>(H_kv) * groups, up(own, bn), alt ? kMaxParts / 2 : kMaxParts);
         plan.own_items = static_cast<int>(B * static_cast<long long>(H_kv) * groups * plan.own_ctas);
         plan.own_parts = plan.own_ctas * (alt ? 2 : 1);
     } else {
@@ -72,7 +72,7 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
         if (all > kStreamPrefixRows) {
             const long long tiles = up(all, 128), groups = d == 256 ? tiles : up(tiles, 2);
             const bool alt = d != 256 && tiles == 1;
-            plan.prefix_ctas = tile_ctas(H_kv * groups, up(prefix_len, bn));
+            plan.prefix_ctas = tile_ctas(H_kv * groups, up(prefix_len, bn), alt ? kMaxParts / 2 : kMaxParts);
             plan.prefix_items = static_cast<int>(H_kv * groups * plan.prefix_ctas);
             plan.prefix_parts = plan.prefix_ctas * (alt ? 2 : 1);
         } else {
@@ -110,21 +110,23 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.0f;
     if (in) {
-        // (128 parts at most: a prefix and a sequence have 64 each)
+        // The first 128 parts' weights stay in registers; there are seldom more.
+        auto part_lse = [&](int k) {
+            const int x = 32 * k + lane;
+            return x < parts ? p.part_lse[x * rows + row] : -INFINITY;
+        };
         float l2[4], mm = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const int x = 32 * k + lane;
-            l2[k] = x < parts ? p.part_lse[x * rows + row] : -INFINITY;
+            l2[k] = part_lse(k);
             mm = fmaxf(mm, l2[k]);
         }
+        for (int k = 4; 32 * k < parts; ++k) mm = fmaxf(mm, part_lse(k));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
         ref = mm == -INFINITY ? 0.0f : mm;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (32 * k >= parts) break;
-            const float wt = l2[k] == -INFINITY ? 0.0f : ex2_approx(l2[k] - ref);
+        auto add = [&](int k, float lse2) {
+            const float wt = lse2 == -INFINITY ? 0.0f : ex2_approx(lse2 - ref);
             sum += wt;
             const int n = min(32, parts - 32 * k);
             for (int x = w; x < n; x += 4 * W) {
@@ -160,7 +162,12 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
 #pragma unroll
                     for (int v = 0; v < V; ++v) acc[v] += g[y] * f[y][v];
             }
-        }
+        };
+        add(0, l2[0]);
+        if (parts > 32) add(1, l2[1]);
+        if (parts > 64) add(2, l2[2]);
+        if (parts > 96) add(3, l2[3]);
+        for (int k = 4; 32 * k < parts; ++k) add(k, part_lse(k));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }

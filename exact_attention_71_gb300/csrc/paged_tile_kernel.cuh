@@ -279,7 +279,8 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
         if (w.rt[t] >= tiles) w.rt[t] = -1;
         const int part = w.pair || Cfg::NS == 1 ? split : 2 * split + t;
         w.part[t] = base + part;
-        // Even shares of the key tiles (at most 2^24 of them, 128 parts).
+        // Even shares of the key tiles (at most 2^24 of them, 256 parts: the product
+        // stays below 2^32).
         w.j0[t] = static_cast<int>(static_cast<unsigned>(all) * part / parts);
         int j1 = static_cast<int>(static_cast<unsigned>(all) * (part + 1) / parts);
         if (w.rt[t] >= 0) {
