@@ -21,10 +21,10 @@ long long up(long long a, long long b) { return (a + b - 1) / b; }
 // CTAs that share a row tile's keys (tile kernel, one CTA an SM): as few waves
 // x key tiles per CTA as possible, a CTA's fixed cost (query load, pipeline
 // fill, epilogue) counted as three key tiles.
-int tile_ctas(long long units, long long tiles, int most) {
+int tile_ctas(long long units, long long tiles) {
     int best = 1;
     long long best_cost = -1;
-    for (int s = 1; s <= most && s <= tiles; ++s) {
+    for (int s = 1; s <= kPlanSms && s <= tiles; ++s) {
         const long long cost = up(units * s, kPlanSms) * (up(tiles, s) + 3);
         if (best_cost < 0 || cost < best_cost) {
             best = s;
@@ -60,10 +60,9 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     };
     if (rows > kStreamRows) {
         const long long tiles = up(rows, 128), groups = d == 256 ? tiles : up(tiles, 2);
-        const bool alt = d != 256 && tiles == 1;
-        plan.own_ctas = tile_ctas(B * static_cast<long long>(H_kv) * groups, up(own, bn), alt ? kMaxParts / 2 : kMaxParts);
+        plan.own_ctas = tile_ctas(B * static_cast<long long>(H_kv) * groups, up(own, bn));
         plan.own_items = static_cast<int>(B * static_cast<long long>(H_kv) * groups * plan.own_ctas);
-        plan.own_parts = plan.own_ctas * (alt ? 2 : 1);
+        plan.own_parts = plan.own_ctas;
     } else {
         plan.own_parts = stream_parts(own, B * static_cast<long long>(H_kv) * up(rows, 16));
     }
@@ -71,10 +70,9 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
         const long long all = B * rows;
         if (all > kStreamPrefixRows) {
             const long long tiles = up(all, 128), groups = d == 256 ? tiles : up(tiles, 2);
-            const bool alt = d != 256 && tiles == 1;
-            plan.prefix_ctas = tile_ctas(H_kv * groups, up(prefix_len, bn), alt ? kMaxParts / 2 : kMaxParts);
+            plan.prefix_ctas = tile_ctas(H_kv * groups, up(prefix_len, bn));
             plan.prefix_items = static_cast<int>(H_kv * groups * plan.prefix_ctas);
-            plan.prefix_parts = plan.prefix_ctas * (alt ? 2 : 1);
+            plan.prefix_parts = plan.prefix_ctas;
         } else {
             plan.prefix_stream = true;
             plan.prefix_parts = stream_parts(prefix_len, H_kv * up(all, 16));

@@ -9,9 +9,9 @@
 // tokens), one key/value head, one or two tiles of 128 query rows and a key
 // range.  Two softmax warpgroups ("streams") each hold one tile's S and O in
 // tensor memory.  With two row tiles (pair) both streams take every key tile;
-// with one (alt) each stream takes half of the range with the same rows and
-// leaves a partial result of its own, so that one stream's softmax still runs
-// beside the other's products.  At d = 256 tensor memory holds one stream.
+// with one (alt) each stream takes half of the range with the same rows, so that
+// one stream's softmax still runs beside the other's products, and the two
+// results are joined at the end.  At d = 256 tensor memory holds one stream.
 //
 //   warps [0, 4 NS)       softmax (one thread per row); they also bring in Q
 //   e4m3: 4 warps         convert the raw codes of a K or V tile to fp16 (exact;
@@ -54,6 +54,7 @@ enum : int {
     SITE_TILE_LOADED = 0xa8,
     SITE_TILE_DRAIN = 0xa9,
     SITE_TILE_TURN = 0xaa,
+    SITE_TILE_JOIN = 0xab,
 };
 
 template <int D_, bool FP8_>
@@ -95,7 +96,7 @@ struct TileCfg {
 };
 
 struct TileBarriers {
-    uint64_t q_full, loaded, drain[2], fix;
+    uint64_t q_full, loaded, drain[2], fix, joined;
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t ring_full[8], ring_empty[8];
     uint64_t raw_full[8], raw_empty[8];
@@ -105,6 +106,7 @@ struct TileBarriers {
     float vref[8];                 // e4m3, per slot: the slot's V scales are divided by it
     float red[2][4];               // e4m3: the converting warps' maxima
     float q_log2[128 * 2];         // e4m3: raw score -> log2 units, per query row
+    float lse1[128];               // alt mode: stream 1's result
     uint32_t tmem_base;
     int abort_flag;
     int turn;                      // blocks of products issued
@@ -221,7 +223,7 @@ struct TileItem {
     int seq, kvh;
     int rows;            // query rows of the segment for this head
     int rt[2];           // row tile of each stream (-1: none)
-    int part[2];         // part index of each stream's result
+    int part;            // part index of the result
     int j0[2], n[2];     // first key tile and number of key tiles of each stream
     int len;             // keys of the segment
     const int* table;
@@ -249,8 +251,6 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
     x /= groups;
     w.kvh = x % static_cast<unsigned>(p.H_kv);
     x /= static_cast<unsigned>(p.H_kv);
-    // Streams that split a range count as two parts.
-    const int per_cta = (Cfg::NS == 2 && !w.pair) ? 2 : 1;
     const unsigned ctas = w.prefix ? p.prefix_ctas : p.own_ctas;
     const int split = x % ctas;
     w.seq = w.prefix ? 0 : x / ctas;
@@ -265,24 +265,23 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
         }
     }
     w.len = len;
-    const unsigned parts = ctas * per_cta;
-    const int base = w.prefix ? 0 : p.prefix_parts;
+    w.part = (w.prefix ? 0 : p.prefix_parts) + split;
     const int all = (len + Cfg::BN - 1) / Cfg::BN;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         if (t >= Cfg::NS) {
             w.rt[t] = -1;
-            w.part[t] = w.j0[t] = w.n[t] = 0;
+            w.j0[t] = w.n[t] = 0;
             continue;
         }
         w.rt[t] = w.pair ? group * 2 + t : group;
         if (w.rt[t] >= tiles) w.rt[t] = -1;
-        const int part = w.pair || Cfg::NS == 1 ? split : 2 * split + t;
-        w.part[t] = base + part;
-        // Even shares of the key tiles (at most 2^24 of them, 256 parts: the product
-        // stays below 2^32).
-        w.j0[t] = static_cast<int>(static_cast<unsigned>(all) * part / parts);
-        int j1 = static_cast<int>(static_cast<unsigned>(all) * (part + 1) / parts);
+        // Even shares of the key tiles: at most 2^23 tiles for two streams of 152
+        // CTAs (2^24 for one), so the products stay below 2^32.
+        const bool two = Cfg::NS == 2 && !w.pair;
+        const unsigned share = two ? 2 * split + t : split, shares = two ? 2 * ctas : ctas;
+        w.j0[t] = static_cast<int>(static_cast<unsigned>(all) * share / shares);
+        int j1 = static_cast<int>(static_cast<unsigned>(all) * (share + 1) / shares);
         if (w.rt[t] >= 0) {
             // Tiles past what the tile's last row sees are left out.
             const int last = min(w.rt[t] * Cfg::BM + Cfg::BM, w.rows) - 1;
@@ -358,41 +357,26 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     if (!w.prefix && p.causal) diag_key = row_limit(p, w, max(w.rt[0], 0) * BM);
     const int diag = diag_key < w.len ? diag_key / BN : w.len / BN + 1;
 
-    // Softmax threads: their query row, and its copy on the way before anything
-    // else.  A warp brings in its 32 rows of the tile, swizzled, zero where there
-    // is none; in alt mode both streams use stream 0's tile.
+    // Softmax threads: their query row.
     const int stream = warp >> 2;
     const int row = (stream == 0 ? w.rt[0] : w.rt[1]) * BM + (tid & 127);
     bool in = false;
-    long long out = 0;
-    int lse_at = 0;
+    int out = -1, lse_at = 0;      // row index in q, o and the partials; in lse
     if (warp < 4 * NS) {
         in = (stream == 0 ? w.rt[0] : w.rt[1]) >= 0 && row < w.rows;
         if (in) {
             const int per = p.Nq * p.G;
             const int b = w.prefix ? row / per : w.seq, i = (w.prefix ? row % per : row) / p.G;
             const int h = w.kvh * p.G + row % p.G;
-            out = (static_cast<long long>(b) * p.Nq + i) * p.H + h;
+            out = (b * p.Nq + i) * p.H + h;
             lse_at = (b * p.H + h) * p.Nq + i;
         }
-        if (w.pair || stream == 0) {
-            constexpr int LPR = D / 8 < 32 ? D / 8 : 32;           // lanes per row (16 bytes each)
-            const long long mine = in ? out : -1;
-#pragma unroll 4
-            for (int x = 0; x < LPR; ++x) {
-                const int rr = x * (32 / LPR) + lane / LPR;        // row of the warp
-                const long long src = __shfl_sync(0xffffffffu, mine, rr);
-                const int rq = (warp & 3) * 32 + rr, c = lane % LPR;
-                cp_async16(smem_u32(sQ) + stream * Cfg::Q_BYTES + (c >> 3) * (BM * 128) + rq * 128 + (((c & 7) ^ (rq & 7)) << 4),
-                           static_cast<const __nv_bfloat16*>(p.q) + (src < 0 ? 0 : src * D) + c * 8, src >= 0);
-            }
-        }
-        cp_async_commit();
     }
     if (tid == Cfg::LOAD_WARP * 32) {
         mbar_init(&bars->q_full, NS * 128);
         mbar_init(&bars->loaded, 1);
         mbar_init(&bars->fix, 1);
+        mbar_init(&bars->joined, 128);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars->drain[t], 1);
             mbar_init(&bars->s_full[t], 1);
@@ -500,16 +484,27 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             const int box = min(ps, BN), boxes = BN / box;      // rows of a copy; copies of a tile (per 64 columns)
             const uint64_t pol = l2_policy_evict_last();
             uint32_t e = 0, ktiles = 0, fixes = 0;
-            // Lane x < boxes looks up the page of copy x; the next tile's page
-            // is fetched while this one is copied.
-            auto page_of = [&](int key0) -> int {
-                const int key = key0 + lane * box;
-                return lane < boxes && key < w.len ? __ldg(w.table + (key >> p.page_shift)) : -1;
+            // Lane x < boxes looks up the page of copy x, a tile ahead; V's entry
+            // uses its K's.
+            auto page_of = [&](int t, int u) -> int {
+                const int key = ((t == 0 ? w.j0[0] : w.j0[1]) + u) * BN + lane * box;
+                const bool any = u < (w.pair ? max(w.n[0], w.n[1]) : t == 0 ? w.n[0] : w.n[1]);
+                return any && lane < boxes && key < w.len ? __ldg(w.table + (key >> p.page_shift)) : -1;
             };
+            int page0 = -1, page1 = -1, next0 = page_of(0, 0), next1 = NS > 1 && !w.pair ? page_of(1, 0) : -1;
             tile_entries<Cfg>(w, [&](int t, int u, bool is_v) -> bool {
                 const int key0 = ((t == 0 ? w.j0[0] : w.j0[1]) + u) * BN;
                 const int key = key0 + lane * box;
-                const int page = page_of(key0);
+                if (!is_v) {
+                    if (t == 0) {
+                        page0 = next0;
+                        next0 = page_of(0, u + 1);
+                    } else {
+                        page1 = next1;
+                        next1 = page_of(1, u + 1);
+                    }
+                }
+                const int page = t == 0 ? page0 : page1;
                 const bool want = lane < boxes && key < w.len;
                 const bool have = want && page >= 0 && page < p.num_pages;
                 const uint32_t copies = __ballot_sync(0xffffffffu, have);
@@ -694,8 +689,22 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_tmem = tmem + lane_off + t * 128, o_tmem = tmem + lane_off + 256 + t * D;
         const int nt = t == 0 ? w.n[0] : w.n[1];
-        const int j0 = t == 0 ? w.j0[0] : w.j0[1], part = t == 0 ? w.part[0] : w.part[1];
+        const int j0 = t == 0 ? w.j0[0] : w.j0[1], part = w.part;
         const int limit = in ? row_limit(p, w, row) : w.len;   // (a row that is not there needs no mask)
+        // A warp brings in its 32 query rows, swizzled, zero where there is none;
+        // in alt mode both streams use stream 0's tile.
+        if (w.pair || t == 0) {
+            constexpr int LPR = D / 8 < 32 ? D / 8 : 32;           // lanes per row (16 bytes each)
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (lane % LPR) * 8;
+#pragma unroll 8
+            for (int x = 0; x < LPR; ++x) {
+                const int src = __shfl_sync(0xffffffffu, out, x * (32 / LPR) + lane / LPR);
+                const int rq = (warp & 3) * 32 + x * (32 / LPR) + lane / LPR, c = lane % LPR;
+                cp_async16(smem_u32(sQ) + t * Cfg::Q_BYTES + (c >> 3) * (BM * 128) + rq * 128 + (((c & 7) ^ (rq & 7)) << 4),
+                           q + static_cast<long long>(max(src, 0)) * D, src >= 0);
+            }
+        }
+        cp_async_commit();
         cp_async_wait<0>();
         if constexpr (FP8) {
             // To fp16 in place, one row a thread (the warp's own rows).
@@ -979,13 +988,60 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     }
                 }
             }
-            const float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (FP8 ? vref : 1.0f);
-            const float lse2 = l == 0.0f ? -INFINITY : m + __log2f(l);
+            float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (FP8 ? vref : 1.0f);
+            float lse2 = l == 0.0f ? -INFINITY : m + __log2f(l);
             const bool some = nt > 0;
-            if constexpr (DIRECT) {
-                if (in) p.lse[lse_at] = lse2 * 0.69314718055994530942f;
-            } else {
-                if (in) p.part_lse[part * rows_all + out] = lse2;
+            // alt: stream 1 leaves its rows in the ring (no product reads it any
+            // more once both streams are done), stream 0 adds them to its own.
+            const bool alt = NS == 2 && !w.pair;
+            float weight1 = 0.0f;
+            const uint8_t* other = sRing + (tid & 127) * (D * 4);
+            bool take = !(alt && t == 1);
+            if (alt) {
+                const int n_other = t == 0 ? w.n[1] : w.n[0];
+                bool wt = n_other == 0 || tile_wait(&bars->o_full[1 - t], 0, abort_flag, p, SITE_TILE_O);
+                if (t == 1) {
+                    if (__all_sync(0xffffffffu, wt)) {
+                        if (some) {
+                            uint8_t* mine = const_cast<uint8_t*>(other);
+#pragma unroll
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32(o_tmem + c * 32, o);
+                                tmem_wait_ld();
+                                reg_fence32(o);
+#pragma unroll
+                                for (int x = 0; x < 8; ++x)
+                                    *reinterpret_cast<float4*>(mine + (((c * 8 + x) ^ (lane & 7)) << 4)) =
+                                        make_float4(__uint_as_float(o[4 * x]) * inv, __uint_as_float(o[4 * x + 1]) * inv,
+                                                    __uint_as_float(o[4 * x + 2]) * inv, __uint_as_float(o[4 * x + 3]) * inv);
+                            }
+                        }
+                        bars->lse1[tid & 127] = lse2;
+                    }
+                    mbar_arrive(&bars->joined);
+                } else {
+                    wt = wt && tile_wait(&bars->joined, 0, abort_flag, p, SITE_TILE_JOIN);
+                    take = __all_sync(0xffffffffu, wt);
+                    if (take) {
+                        const float l1 = bars->lse1[tid & 127];
+                        if (l1 != -INFINITY) {             // (NaN included)
+                            const float top = fmaxf(lse2, l1), ref = top == -INFINITY ? 0.0f : top;
+                            const float a = lse2 == -INFINITY ? 0.0f : ex2_approx(lse2 - ref), b = ex2_approx(l1 - ref);
+                            const float s = 1.0f / (a + b);
+                            weight1 = b * s;
+                            inv *= a * s;
+                            lse2 = ref + __log2f(a + b);
+                        }
+                    }
+                }
+            }
+            if (take) {
+                if constexpr (DIRECT) {
+                    if (in) p.lse[lse_at] = lse2 * 0.69314718055994530942f;
+                } else {
+                    if (in) p.part_lse[part * rows_all + out] = lse2;
+                }
             }
             // O leaves through this warp's 4 KB of shared memory (32 rows x 128
             // bytes, swizzled by 16-byte chunk), so that every store instruction
@@ -995,10 +1051,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                          : w.pair || NS == 1 ? sQ + t * Cfg::Q_BYTES
                                              : sQ + Cfg::Q_BYTES + t * 16384;
             epi += (warp & 3) * 4096;
-            const long long mine = in && (DIRECT || l != 0.0f) ? out : -1;
+            const int mine = in && take && (DIRECT || lse2 != -INFINITY) ? out : -1;
+            const bool add = __any_sync(0xffffffffu, weight1 != 0.0f);
             constexpr int COLS = DIRECT ? 64 : 32;             // columns per 128 bytes
 #pragma unroll
             for (int c = 0; c < D / COLS; ++c) {
+                if (!take) break;
                 uint32_t o[COLS];
                 if (some) {
 #pragma unroll
@@ -1006,30 +1064,43 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     tmem_wait_ld();
 #pragma unroll
                     for (int y = 0; y < COLS; y += 32) reg_fence32(o + y);
+#pragma unroll
+                    for (int y = 0; y < COLS; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * inv);
+                } else {
+#pragma unroll
+                    for (int y = 0; y < COLS; ++y) o[y] = 0u;
+                }
+                if (add) {
+#pragma unroll
+                    for (int y = 0; y < COLS / 4; ++y) {
+                        const float4 v = *reinterpret_cast<const float4*>(other + (((c * (COLS / 4) + y) ^ (lane & 7)) << 4));
+                        const float* e = &v.x;
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            if (weight1 != 0.0f) o[4 * y + z] = __float_as_uint(__uint_as_float(o[4 * y + z]) + e[z] * weight1);
+                    }
                 }
                 __syncwarp();
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (some) {
-                        uint32_t* q = &v.x;
+                    uint4 v;
+                    uint32_t* q = &v.x;
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            q[y] = DIRECT ? pack_bf16x2(__uint_as_float(o[(DIRECT ? 8 : 4) * x + 2 * y]) * inv,
-                                                        __uint_as_float(o[(DIRECT ? 8 : 4) * x + 2 * y + 1]) * inv)
-                                          : __float_as_uint(__uint_as_float(o[4 * x + y]) * inv);
-                    }
+                    for (int y = 0; y < 4; ++y)
+                        q[y] = DIRECT ? pack_bf16x2(__uint_as_float(o[(DIRECT ? 8 : 4) * x + 2 * y]),
+                                                    __uint_as_float(o[(DIRECT ? 8 : 4) * x + 2 * y + 1]))
+                                      : o[4 * x + y];
                     *reinterpret_cast<uint4*>(epi + lane * 128 + ((x ^ (lane & 7)) << 4)) = v;
                 }
                 __syncwarp();
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
                     const int rr = x * 4 + lane / 8, ch = lane % 8;
-                    const long long dst = __shfl_sync(0xffffffffu, mine, rr);
+                    const int dst = __shfl_sync(0xffffffffu, mine, rr);
                     const uint4 v = *reinterpret_cast<const uint4*>(epi + rr * 128 + ((ch ^ (rr & 7)) << 4));
                     if (dst >= 0) {
                         if constexpr (DIRECT)
-                            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + dst * D + c * COLS)[ch] = v;
+                            reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + static_cast<long long>(dst) * D + c * COLS)[ch] = v;
                         else
                             reinterpret_cast<uint4*>(p.part_o + (part * rows_all + dst) * D + c * COLS)[ch] = v;
                     }
