@@ -292,25 +292,18 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
     return w;
 }
 
-// Calls f(stream, u, is_v) for every K and V tile in the order in which they are
-// brought in.  pair: K_u, V_u of the shared tiles (e4m3: K one tile ahead, see
-// tile_place); alt: the streams' tiles in the order in which the products use them.
+// Calls f(stream, u, is_v) for every ring entry in order: in pair mode K_u, V_u
+// of the shared tiles; in alt mode the streams' entries in the order in which
+// the products use them.
 template <class Cfg, class F>
 __device__ __forceinline__ void tile_entries(const TileItem& w, F&& f) {
-    const int n = max(w.n[0], w.n[1]);
     if (w.pair || Cfg::NS == 1) {
-        if constexpr (Cfg::FP8) {
-            if (n > 0 && !f(0, 0, false)) return;
-            for (int u = 0; u < n; ++u) {
-                if (u + 1 < n && !f(0, u + 1, false)) return;
-                if (!f(0, u, true)) return;
-            }
-        } else {
-            for (int u = 0; u < n; ++u) {
-                if (!f(0, u, false) || !f(0, u, true)) return;
-            }
+        const int n = max(w.n[0], w.n[1]);
+        for (int u = 0; u < n; ++u) {
+            if (!f(0, u, false) || !f(0, u, true)) return;
         }
     } else {
+        const int n = max(w.n[0], w.n[1]);
         for (int u = 0; u <= n; ++u) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -321,37 +314,16 @@ __device__ __forceinline__ void tile_entries(const TileItem& w, F&& f) {
     }
 }
 
-// The ring slot of stream t's tile u (K or V), and the slot's round.  The slots
-// are used in turn, except that e4m3 in pair mode has room for three converted
-// tiles only: two slots are K's and one is V's.  K_(u+1) is then converted while
-// the products of step u run, and only V_u's conversion lies between the product
-// that frees its slot and the one that reads it (in turn, K_(u+1) would wait for
-// the slot of V_(u-1): 4300 cycles a step against 3300).
-struct TilePlace {
-    uint32_t slot, round;
-};
+// Ring index of stream t's V_(u-1) (is_v) or K_u in tile_entries order.
 template <class Cfg>
-__device__ __forceinline__ TilePlace tile_place(const TileItem& w, int t, int u, bool is_v) {
-    uint32_t x;
-    if (w.pair || Cfg::NS == 1) {
-        if constexpr (Cfg::FP8 && Cfg::NH == 3) {
-            if (is_v) return {2u, static_cast<uint32_t>(u)};
-            return {static_cast<uint32_t>(u) & 1u, static_cast<uint32_t>(u) >> 1};
-        }
-        if constexpr (Cfg::FP8) x = is_v ? 2 * u + 2 : u == 0 ? 0 : 2 * u - 1;
-        else x = is_v ? 2 * u + 1 : 2 * u;
-        // (the last V follows its K at once: there is no K to go before it)
-        if (Cfg::FP8 && is_v && u + 1 == max(w.n[0], w.n[1])) x = 2 * u + 1;
-    } else {
-        // V_u is used in round u + 1: all tiles of the rounds before, then V0, K0,
-        // V1, K1 of this one.
-        const int r = is_v ? u + 1 : u, b = max(r - 1, 0);
-        x = min(b, w.n[0]) + min(r, w.n[0]) + min(b, w.n[1]) + min(r, w.n[1]);
-        const int v0 = r >= 1 && r <= w.n[0], k0 = r < w.n[0], v1 = r >= 1 && r <= w.n[1];
-        if (t == 1) x += v0 + k0;
-        if (!is_v) x += t == 0 ? v0 : v1;
-    }
-    return {x % Cfg::NH, x / Cfg::NH};
+__device__ __forceinline__ uint32_t tile_entry(const TileItem& w, int t, int u, bool is_v) {
+    if (w.pair || Cfg::NS == 1) return is_v ? 2 * u - 1 : 2 * u;
+    const int b = max(u - 1, 0);
+    int x = min(b, w.n[0]) + min(u, w.n[0]) + min(b, w.n[1]) + min(u, w.n[1]);      // rounds before u
+    const int v0 = u >= 1 && u <= w.n[0], k0 = u < w.n[0], v1 = u >= 1 && u <= w.n[1];
+    if (t == 1) x += v0 + k0;
+    if (!is_v) x += t == 0 ? v0 : v1;
+    return static_cast<uint32_t>(x);
 }
 
 // Position of stream t's key tile u among the K entries (its scale slot).
@@ -457,9 +429,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             bool ok = n == 0 || tile_warp_wait(&bars->q_full, 0, abort_flag, p, SITE_TILE_Q);
             for (int u = 0; u <= rounds && ok; ++u) {
                 const bool has_v = u > 0 && u <= n, has_k = u < n;
-                const TilePlace xv = tile_place<Cfg>(w, t, u - 1, true), xk = tile_place<Cfg>(w, t, u, false);
-                if (has_v) ok = tile_warp_wait(&bars->ring_full[xv.slot], xv.round & 1, abort_flag, p, SITE_TILE_FULL);
-                if (ok && has_k) ok = tile_warp_wait(&bars->ring_full[xk.slot], xk.round & 1, abort_flag, p, SITE_TILE_FULL);
+                const uint32_t xv = tile_entry<Cfg>(w, t, u, true), xk = tile_entry<Cfg>(w, t, u, false);
+                if (has_v) ok = tile_warp_wait(&bars->ring_full[xv % NH], (xv / NH) & 1, abort_flag, p, SITE_TILE_FULL);
+                if (ok && has_k) ok = tile_warp_wait(&bars->ring_full[xk % NH], (xk / NH) & 1, abort_flag, p, SITE_TILE_FULL);
                 if (ok && u > 0 && u <= nt) ok = tile_warp_wait(&bars->p_full[t], (u - 1) & 1, abort_flag, p, SITE_TILE_P);
                 if (NS > 1 && ok) ok = tile_turn(turn, 2 * u + t, abort_flag, p);
                 if (!ok) break;
@@ -467,29 +439,29 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 if (elect_one()) {
                     if (has_v) {
                         if (u <= nt) {
-                            const uint64_t vd = sdesc_sw128(ring + xv.slot * Cfg::HALF_BYTES, BN * 128, 1024);
+                            const uint64_t vd = sdesc_sw128(ring + (xv % NH) * Cfg::HALF_BYTES, BN * 128, 1024);
 #pragma unroll
                             for (int kk = 0; kk < BN / 16; ++kk)
                                 mma_f16_ts(o_tmem, s_tmem + kk * 8, vd + ((kk * 16 * 128) >> 4), idesc_o,
                                            (kk > 0 || u > 1) ? 1u : 0u);
                             if (u == nt) mma_commit(&bars->o_full[t]);
-                            mma_commit(&bars->ring_empty[xv.slot]);
+                            mma_commit(&bars->ring_empty[xv % NH]);
                         } else {
-                            mbar_arrive(&bars->ring_empty[xv.slot]);
+                            mbar_arrive(&bars->ring_empty[xv % NH]);
                         }
                     }
                     if (has_k) {
                         if (u < nt) {
-                            const uint64_t kd = sdesc_sw128(ring + xk.slot * Cfg::HALF_BYTES, 16, 1024);
+                            const uint64_t kd = sdesc_sw128(ring + (xk % NH) * Cfg::HALF_BYTES, 16, 1024);
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint32_t a = (kk / 4) * (BM * 128) + (kk % 4) * 32, b = (kk / 4) * (BN * 128) + (kk % 4) * 32;
                                 mma_f16_ss(s_tmem, qd + (a >> 4), kd + (b >> 4), idesc_s, kk > 0 ? 1u : 0u);
                             }
                             mma_commit(&bars->s_full[t]);
-                            mma_commit(&bars->ring_empty[xk.slot]);
+                            mma_commit(&bars->ring_empty[xk % NH]);
                         } else {
-                            mbar_arrive(&bars->ring_empty[xk.slot]);
+                            mbar_arrive(&bars->ring_empty[xk % NH]);
                         }
                     }
                     if (NS > 1) {
@@ -512,8 +484,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             const int box = min(ps, BN), boxes = BN / box;      // rows of a copy; copies of a tile (per 64 columns)
             const uint64_t pol = l2_policy_evict_last();
             uint32_t e = 0, ktiles = 0, fixes = 0;
-            // Lane x < boxes looks up the page of copy x, a tile ahead; V's copies use
-            // their K's.
+            // Lane x < boxes looks up the page of copy x, a tile ahead; V's entry
+            // uses its K's.
             auto page_of = [&](int t, int u) -> int {
                 const int key = ((t == 0 ? w.j0[0] : w.j0[1]) + u) * BN + lane * box;
                 const bool any = u < (w.pair ? max(w.n[0], w.n[1]) : t == 0 ? w.n[0] : w.n[1]);
@@ -523,15 +495,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             tile_entries<Cfg>(w, [&](int t, int u, bool is_v) -> bool {
                 const int key0 = ((t == 0 ? w.j0[0] : w.j0[1]) + u) * BN;
                 const int key = key0 + lane * box;
-                // (one stream's tiles: the pages of two tiles, by parity)
-                const bool first = w.pair || NS == 1 ? (u & 1) == 0 : t == 0;
                 if (!is_v) {
-                    if (first) page0 = t == 0 ? next0 : next1;
-                    else page1 = t == 0 ? next0 : next1;
-                    if (t == 0) next0 = page_of(0, u + 1);
-                    else next1 = page_of(1, u + 1);
+                    if (t == 0) {
+                        page0 = next0;
+                        next0 = page_of(0, u + 1);
+                    } else {
+                        page1 = next1;
+                        next1 = page_of(1, u + 1);
+                    }
                 }
-                const int page = first ? page0 : page1;
+                const int page = t == 0 ? page0 : page1;
                 const bool want = lane < boxes && key < w.len;
                 const bool have = want && page >= 0 && page < p.num_pages;
                 const uint32_t copies = __ballot_sync(0xffffffffu, have);
@@ -661,8 +634,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     const uint32_t top = __reduce_max_sync(0xffffffffu, v > 0.0f && v < INFINITY ? __float_as_uint(v) : 0u);
                     if (lane == 0) bars->red[kt & 1][ct >> 5] = __uint_as_float(top);
                 }
-                const TilePlace at = tile_place<Cfg>(w, t, u, is_v);
-                ok = ok && tile_wait(&bars->ring_empty[at.slot], (at.round & 1) ^ 1, abort_flag, p, SITE_TILE_EMPTY);
+                ok = ok && tile_wait(&bars->ring_empty[e % NH], ((e / NH) & 1) ^ 1, abort_flag, p, SITE_TILE_EMPTY);
                 if (!named_barrier_and(1, 128, ok)) return false;
                 if (!is_v) {
                     const float* red = bars->red[kt & 1];
@@ -675,7 +647,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     if (ct == 0) bars->vref[slot] = ref;
                 }
                 const uint8_t* src = sRaw + (e % NR) * Cfg::RAW_BYTES + r0 * D + c * 16;
-                uint8_t* dst = sRing + at.slot * Cfg::HALF_BYTES;
+                uint8_t* dst = sRing + (e % NH) * Cfg::HALF_BYTES;
                 auto convert = [&](auto check) {
 #pragma unroll
                     for (int i = 0; i < BN / RPP; ++i) {
@@ -704,7 +676,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 if (whole && !(is_v && diagonal)) convert(std::false_type{});
                 else convert(std::true_type{});
                 fence_proxy_async_smem();
-                mbar_arrive(&bars->ring_full[at.slot]);
+                mbar_arrive(&bars->ring_full[e % NH]);
                 mbar_arrive(&bars->raw_empty[e % NR]);
                 ++e;
                 return true;
