@@ -1165,8 +1165,8 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
     const int es = p.fp8 ? 1 : 2;
     if (plan.prefix_items + plan.own_items > 0) {
         const int bn = d == 256 ? 64 : 128;
-        if (!p.fp8 && (rc = make_cache_maps(&maps, k_cache, v_cache, num_pages, H_kv, page_size, d, es,
-                                            page_size < bn ? page_size : bn)) != ATTN_OK)
+        if ((rc = make_cache_maps(&maps, k_cache, v_cache, num_pages, H_kv, page_size, d, es,
+                                  page_size < bn ? page_size : bn)) != ATTN_OK)
             return rc;
         e = tiles(maps, p, plan.direct, s);
     }

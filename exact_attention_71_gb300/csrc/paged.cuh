@@ -158,8 +158,8 @@ inline cudaError_t launch_kernel(void (*kernel)(Params...), unsigned grid, unsig
 cudaError_t run_kv_write(const KvWriteParams& p, cudaStream_t stream);
 cudaError_t run_kv_read(const KvReadParams& p, cudaStream_t stream);
 // K and V of the cache as 4-D {d, page_size, H_kv, num_pages} tensors.  Box of the
-// streaming kernel: 16 rows of up to 128 bytes; of the tile kernel (bf16): 64
-// columns x min(page_size, key tile) rows.  128-byte swizzle (64-byte rows: 64).
+// streaming kernel: 16 rows of up to 128 bytes; of the tile kernel: min(page_size,
+// key tile) such rows.  128-byte swizzle (64-byte rows: 64).
 struct PagedMaps {
     CUtensorMap k, v;
 };

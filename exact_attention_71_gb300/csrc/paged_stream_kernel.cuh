@@ -93,13 +93,39 @@ __device__ __forceinline__ uint32_t f16x2_of_hi(uint32_t codes) {
 // 2^n as a float, n in [-126, 127].
 __device__ __forceinline__ float pow2f(int n) { return __uint_as_float(static_cast<uint32_t>(n + 127) << 23); }
 
-// The power of two that brings a row of largest magnitude `bits` (bf16 bits)
-// into fp16's range, as its exponent: 0 for rows of zeros or with an infinity or
-// a NaN (which stay what they are).
-__device__ __forceinline__ int q_shift(uint32_t bits) {
+// The power of two that brings a row of largest magnitude `bits` (bf16 bits) into
+// [2^to, 2^(to + 1)), as its exponent: 0 for rows of zeros or with an infinity or a
+// NaN (which stay what they are).
+__device__ __forceinline__ int q_shift(uint32_t bits, int to) {
     const int e = static_cast<int>(bits >> 7);
     if (e == 255 || bits == 0) return 0;
-    return max(-126, min(126, 141 - max(e, 1)));
+    return max(-126, min(126, 127 + to - max(e, 1)));
+}
+
+// Eight bf16 times a power of two that brings them below 2^8 -> two e4m3 parts of
+// each, x = q1 + q2.  The first has the leading four bits of x's eight, the second
+// the rest: exact for |x| >= 2^-2 (2^-10 of the row's largest), and within 2^-10
+// below that, where e4m3 ends.  An infinity or a NaN becomes a NaN in q1.
+__device__ __forceinline__ void q_split(const uint4& v, float factor, uint32_t& a1, uint32_t& b1, uint32_t& a2,
+                                        uint32_t& b2) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        float x[4];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            x[2 * z] = __uint_as_float(w[2 * y + z] << 16) * factor;
+            x[2 * z + 1] = __uint_as_float(w[2 * y + z] & 0xffff0000u) * factor;
+        }
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+            if (!(fabsf(x[z]) < INFINITY)) x[z] = __uint_as_float(0x7fc00000u);
+        const uint32_t c = pack_e4m3x4(x[0], x[1], x[2], x[3]);
+        const float2 lo = f16x2_to_float2(f16x2_of_lo(c)), hi = f16x2_to_float2(f16x2_of_hi(c));
+        const uint32_t r = pack_e4m3x4(x[0] - lo.x, x[1] - lo.y, x[2] - hi.x, x[3] - hi.y);
+        (y ? b1 : a1) = c;
+        (y ? b2 : a2) = r;
+    }
 }
 
 // Eight bf16 times a power of two -> eight fp16.
@@ -394,7 +420,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         }
 #pragma unroll
         for (int y = 1; y < 8; y <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
-        const int shift = q_shift(top);
+        const int shift = q_shift(top, 14);
         if ((lane & 7) == 0) row_log2[r] = p.scale_log2 * pow2f(-shift);
 #pragma unroll
         for (int y = 0; y < D / 64; ++y) {

@@ -14,10 +14,13 @@
 // results are joined at the end.  At d = 256 tensor memory holds one stream.
 //
 //   warps [0, 4 NS)       softmax (one thread per row); they also bring in Q
-//   e4m3: 4 warps         convert the raw codes of a K or V tile to fp16 (exact;
-//                         K's row scales go to the scores, V's to P, q and P are
-//                         brought into fp16's range by powers of two: see the
-//                         streaming kernel)
+//   e4m3: 4 warps         convert the codes of a V tile to fp16 (exact; V's row
+//                         scales go to P, which is brought into fp16's range by a
+//                         power of two: see the streaming kernel).  K is multiplied
+//                         as it is: q is split into two e4m3 parts, q = (q1 + q2)
+//                         2^shift, so that S = q1 K^T + q2 K^T in the 8-bit products
+//                         that run at twice the rate.  The tensor cores add them
+//                         up in 25 bits (measured: 2^-22 of sum |q k|).
 //   load warp             walks the page table: a head's rows of a page are
 //                         contiguous, so a bf16 tile is BN / page_size TMA boxes
 //                         per 64 columns, written swizzled into a ring of half
@@ -66,10 +69,14 @@ struct TileCfg {
     static constexpr int NS = D == 256 ? 1 : 2;                    // streams
     static constexpr int NCB = D / 64;                             // 128-byte column boxes per row
     static constexpr int Q_BYTES = BM * D * 2;
-    static constexpr int HALF_BYTES = BN * D * 2;                  // one K or V tile
-    static constexpr int NH = D == 64 ? (FP8 ? 6 : 8) : (FP8 ? 3 : 5);
-    static constexpr int RAW_BYTES = FP8 ? BN * D : 0;             // the same tile as codes
-    static constexpr int NR = FP8 ? (D == 64 ? 5 : 3) : 0;
+    static constexpr int HALF_BYTES = BN * D * 2;                  // one K or V tile, 16-bit
+    // bf16: one ring of K and V tiles.  e4m3: a ring of K tiles as they are, one of
+    // V tiles as they are (raw) and one of V tiles in fp16.
+    static constexpr int RAW_BYTES = FP8 ? BN * D : 0;
+    static constexpr int NH = FP8 ? (D == 64 ? 4 : 2) : (D == 64 ? 8 : 5);
+    static constexpr int NK = FP8 ? (D == 64 ? 6 : 3) : 0;
+    static constexpr int NR = FP8 ? (D == 64 ? 4 : 2) : 0;
+    static constexpr int SWK = D >= 128 ? 128 : 64;                // e4m3 K and q: swizzle span, 64-byte rows at d = 64
     static constexpr int SLOTS = 8;                                // key tiles whose scales are held
     static constexpr int SC_BYTES = FP8 ? SLOTS * 2 * BN * 4 : 0;
     static constexpr int DIAG_TILES = 8;
@@ -84,23 +91,25 @@ struct TileCfg {
     // Output staging: 4 KB per softmax warp, over query tiles that no product
     // reads any more (d = 64: its query tiles are too small for that).
     static constexpr int EPI_BYTES = D == 64 ? NS * 16384 : 0;
-    static constexpr int SMEM_BYTES = 1024 + NS * Q_BYTES + NH * HALF_BYTES + NR * RAW_BYTES + SC_BYTES +
+    static constexpr int SMEM_BYTES = 1024 + NS * Q_BYTES + NH * HALF_BYTES + (NK + NR) * RAW_BYTES + SC_BYTES +
                                       EPI_BYTES + BAR_BYTES;
     static_assert(HIGH_REGS * NS * 128 + (CONV_REGS + LOW_REGS) * 128 <= LAUNCH_REGS * THREADS, "register split");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-    // A slot (validity bits, scales) is rewritten at least 15 ring entries after
-    // its tile's K; the entry NH + NR before that has been released by then.  It
-    // is past the tile's V (at most 3 entries after its K), so the tile's softmax
-    // is done with the slot.
-    static_assert(15 - NH - NR >= 3, "scale slots");
+    // A slot (validity bits, scales) is rewritten for the eighth key tile after its
+    // own.  bf16: that is at least 15 ring entries after its K, when the entry NH
+    // before has been released; it is past the tile's V (at most 3 entries after
+    // its K).  e4m3: when the S of the tile NK before has been taken, which follows
+    // P V of all tiles but the last of each stream.
+    static_assert(FP8 ? 8 - NK >= 2 : 15 - NH >= 3, "scale slots");
+    static_assert(NS == 1 || NH * HALF_BYTES >= BM * D * 4, "the streams' join");
 };
 
 struct TileBarriers {
     uint64_t q_full, loaded, drain[2], fix, joined;
     uint64_t s_full[2], p_full[2], o_full[2];
     uint64_t ring_full[8], ring_empty[8];
-    uint64_t raw_full[8], raw_empty[8];
-    uint64_t sc_full[8];
+    uint64_t raw_full[8], raw_empty[8], k_full[8], k_empty[8];
+    uint64_t sc_full[8], vs_ready[8];
     uint32_t valid[8][4];          // per slot: bit per key of the tile
     uint32_t poison[8][4];         // per diagonal tile: bit per key whose V row is not finite
     float vref[8];                 // e4m3, per slot: the slot's V scales are divided by it
@@ -344,7 +353,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
     uint8_t* sRing = smem + NS * Cfg::Q_BYTES;
-    uint8_t* sRaw = sRing + NH * Cfg::HALF_BYTES;
+    uint8_t* sK = sRing + NH * Cfg::HALF_BYTES;                // e4m3: K tiles
+    uint8_t* sRaw = sK + Cfg::NK * Cfg::RAW_BYTES;             // e4m3: V tiles
     float* sScale = reinterpret_cast<float*>(sRaw + Cfg::NR * Cfg::RAW_BYTES);     // (slot, k / v, BN)
     TileBarriers* bars = reinterpret_cast<TileBarriers*>(reinterpret_cast<uint8_t*>(sScale) + Cfg::SC_BYTES);
     volatile int* abort_flag = &bars->abort_flag;
@@ -388,7 +398,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             mbar_init(&bars->ring_empty[s], w.pair ? 2 : 1);       // the MMA warps that use an entry
             mbar_init(&bars->raw_full[s], 1);
             mbar_init(&bars->raw_empty[s], 128);
+            mbar_init(&bars->k_full[s], 1);
+            mbar_init(&bars->k_empty[s], w.pair ? 2 : 1);
             mbar_init(&bars->sc_full[s], 1);
+            mbar_init(&bars->vs_ready[s], 128);
             for (int x = 0; x < 4; ++x) bars->poison[s][x] = 0;
         }
         bars->abort_flag = 0;
@@ -417,21 +430,26 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             // awaited before its turn.  In pair mode both warps release every
             // ring entry, always after waiting for it.
             constexpr uint32_t fmt = FP8 ? 0u : 1u;            // fp16 or bf16 operands
-            constexpr uint32_t idesc_s = make_idesc(fmt, 128, BN, 0), idesc_o = make_idesc(fmt, 128, D, 1);
+            constexpr uint32_t idesc_s = make_idesc(FP8 ? 0u : 1u, 128, BN, 0), idesc_o = make_idesc(fmt, 128, D, 1);
             const int t = warp - Cfg::MMA_WARP;
             const int nt = t == 0 ? w.n[0] : w.n[1];
             const int rounds = max(w.n[0], w.n[1]);
             const int n = w.pair ? rounds : nt;
             const uint32_t ring = smem_u32(sRing);
             const uint32_t s_tmem = tmem + t * 128, o_tmem = tmem + 256 + t * D;
-            const uint64_t qd = sdesc_sw128(smem_u32(sQ) + (w.pair ? t : 0) * Cfg::Q_BYTES, 16, 1024);
+            constexpr int SWQ = FP8 ? Cfg::SWK : 128;
+            const uint64_t qd = sdesc_swz<SWQ>(smem_u32(sQ) + (w.pair ? t : 0) * Cfg::Q_BYTES, 16, 8 * SWQ);
+            constexpr uint32_t NKR = FP8 ? Cfg::NK : NH;           // K's ring
+            uint64_t* const k_full = FP8 ? bars->k_full : bars->ring_full;
+            uint64_t* const k_empty = FP8 ? bars->k_empty : bars->ring_empty;
             volatile int* turn = &bars->turn;
             bool ok = n == 0 || tile_warp_wait(&bars->q_full, 0, abort_flag, p, SITE_TILE_Q);
             for (int u = 0; u <= rounds && ok; ++u) {
                 const bool has_v = u > 0 && u <= n, has_k = u < n;
-                const uint32_t xv = tile_entry<Cfg>(w, t, u, true), xk = tile_entry<Cfg>(w, t, u, false);
+                const uint32_t xv = FP8 ? tile_slot<Cfg>(w, t, max(u - 1, 0)) : tile_entry<Cfg>(w, t, u, true);
+                const uint32_t xk = FP8 ? tile_slot<Cfg>(w, t, u) : tile_entry<Cfg>(w, t, u, false);
                 if (has_v) ok = tile_warp_wait(&bars->ring_full[xv % NH], (xv / NH) & 1, abort_flag, p, SITE_TILE_FULL);
-                if (ok && has_k) ok = tile_warp_wait(&bars->ring_full[xk % NH], (xk / NH) & 1, abort_flag, p, SITE_TILE_FULL);
+                if (ok && has_k) ok = tile_warp_wait(&k_full[xk % NKR], (xk / NKR) & 1, abort_flag, p, SITE_TILE_FULL);
                 if (ok && u > 0 && u <= nt) ok = tile_warp_wait(&bars->p_full[t], (u - 1) & 1, abort_flag, p, SITE_TILE_P);
                 if (NS > 1 && ok) ok = tile_turn(turn, 2 * u + t, abort_flag, p);
                 if (!ok) break;
@@ -452,16 +470,25 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     }
                     if (has_k) {
                         if (u < nt) {
-                            const uint64_t kd = sdesc_sw128(ring + (xk % NH) * Cfg::HALF_BYTES, 16, 1024);
+                            const uint64_t kd = FP8 ? sdesc_swz<SWQ>(smem_u32(sK) + (xk % NKR) * Cfg::RAW_BYTES, 16, 8 * SWQ)
+                                                    : sdesc_sw128(ring + (xk % NKR) * Cfg::HALF_BYTES, 16, 1024);
+                            // 32 bytes of a row per instruction; e4m3: both parts of q.
+                            constexpr int KPB = SWQ / 32, STEPS = FP8 ? D / 32 : D / 16;
 #pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t a = (kk / 4) * (BM * 128) + (kk % 4) * 32, b = (kk / 4) * (BN * 128) + (kk % 4) * 32;
-                                mma_f16_ss(s_tmem, qd + (a >> 4), kd + (b >> 4), idesc_s, kk > 0 ? 1u : 0u);
-                            }
+                            for (int z = 0; z < (FP8 ? 2 : 1); ++z)
+#pragma unroll
+                                for (int kk = 0; kk < STEPS; ++kk) {
+                                    const uint32_t a = z * (BM * D) + (kk / KPB) * (BM * SWQ) + (kk % KPB) * 32;
+                                    const uint32_t b = (kk / KPB) * (BN * SWQ) + (kk % KPB) * 32;
+                                    if constexpr (FP8)
+                                        mma_f8_ss(s_tmem, qd + (a >> 4), kd + (b >> 4), idesc_s, z + kk > 0 ? 1u : 0u);
+                                    else
+                                        mma_f16_ss(s_tmem, qd + (a >> 4), kd + (b >> 4), idesc_s, kk > 0 ? 1u : 0u);
+                                }
                             mma_commit(&bars->s_full[t]);
-                            mma_commit(&bars->ring_empty[xk % NH]);
+                            mma_commit(&k_empty[xk % NKR]);
                         } else {
-                            mbar_arrive(&bars->ring_empty[xk % NH]);
+                            mbar_arrive(&k_empty[xk % NKR]);
                         }
                     }
                     if (NS > 1) {
@@ -509,9 +536,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 const bool have = want && page >= 0 && page < p.num_pages;
                 const uint32_t copies = __ballot_sync(0xffffffffu, have);
                 const int row = key & (ps - 1);
-                const uint32_t slot = tile_slot<Cfg>(w, t, u) % Cfg::SLOTS;
-                uint64_t* gate = FP8 ? &bars->raw_empty[e % (FP8 ? Cfg::NR : 1)] : &bars->ring_empty[e % NH];
-                const uint32_t round = e / (FP8 ? Cfg::NR : NH);
+                const uint32_t kt = tile_slot<Cfg>(w, t, u), slot = kt % Cfg::SLOTS;
+                constexpr uint32_t NK = FP8 ? Cfg::NK : 1, NR = FP8 ? Cfg::NR : 1;
+                uint64_t* gate = !FP8 ? &bars->ring_empty[e % NH] : is_v ? &bars->raw_empty[kt % NR] : &bars->k_empty[kt % NK];
+                const uint32_t round = !FP8 ? e / NH : is_v ? kt / NR : kt / NK;
                 if (!tile_warp_wait(gate, (round & 1) ^ 1, abort_flag, p, SITE_TILE_EMPTY)) return false;
                 if (!is_v) {
                     // Validity of the tile's keys (the slot is free: see SLOTS).
@@ -537,13 +565,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     ++ktiles;
                 }
                 if constexpr (FP8) {
-                    uint64_t* full = &bars->raw_full[e % (FP8 ? Cfg::NR : 1)];
+                    uint64_t* full = is_v ? &bars->raw_full[kt % NR] : &bars->k_full[kt % NK];
                     if (lane == 0) mbar_arrive_expect_tx(full, __popc(copies) * box * D);
                     __syncwarp();
                     if (have) {
-                        const long long at = ((static_cast<long long>(page) * p.H_kv + w.kvh) << p.page_shift) + row;
-                        bulk_load(sRaw + (e % (FP8 ? Cfg::NR : 1)) * Cfg::RAW_BYTES + lane * box * D,
-                                  static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) + at * D, box * D, full);
+                        if (is_v) {
+                            const long long at = ((static_cast<long long>(page) * p.H_kv + w.kvh) << p.page_shift) + row;
+                            bulk_load(sRaw + (kt % NR) * Cfg::RAW_BYTES + lane * box * D,
+                                      static_cast<const uint8_t*>(p.v_cache) + at * D, box * D, full);
+                        } else {
+                            uint8_t* tile = sK + (kt % NK) * Cfg::RAW_BYTES;
+#pragma unroll
+                            for (int cb = 0; cb < D / Cfg::SWK; ++cb)
+                                tma_load_4d(tile + cb * (BN * Cfg::SWK) + lane * box * Cfg::SWK, &tmap_k, full, cb * Cfg::SWK, row,
+                                            w.kvh, page, pol);
+                        }
                     }
                 } else {
                     // A V tile with rows that must not reach the product as they
@@ -578,9 +614,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             // Every copy issued here lands before the CTA can exit (on the normal
             // path these phases have completed already).
             if constexpr (FP8) {
-                constexpr uint32_t NR = FP8 ? Cfg::NR : 1;
-                for (uint32_t x = e > NR ? e - NR : 0; x < e; ++x)
+                constexpr uint32_t NK = FP8 ? Cfg::NK : 1, NR = FP8 ? Cfg::NR : 1;
+                const uint32_t vtiles = e - ktiles;
+                for (uint32_t x = vtiles > NR ? vtiles - NR : 0; x < vtiles; ++x)
                     tile_drain(&bars->raw_full[x % NR], (x / NR) & 1, p, SITE_TILE_DRAIN);
+                for (uint32_t x = ktiles > NK ? ktiles - NK : 0; x < ktiles; ++x)
+                    tile_drain(&bars->k_full[x % NK], (x / NK) & 1, p, SITE_TILE_DRAIN);
                 for (uint32_t x = ktiles > Cfg::SLOTS ? ktiles - Cfg::SLOTS : 0; x < ktiles; ++x)
                     tile_drain(&bars->sc_full[x % Cfg::SLOTS], (x / Cfg::SLOTS) & 1, p, SITE_TILE_DRAIN);
             } else {
@@ -601,15 +640,19 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             const int ct = tid - Cfg::CONV_WARP * 32;
             const int c = ct % CPR, r0 = ct / CPR;
             const bool odd = D != 64 && (c & 4);
-            uint32_t e = 0;
             float vref0 = 0.0f, vref1 = 0.0f;                   // per stream (pair: the first)
             tile_entries<Cfg>(w, [&](int t, int u, bool is_v) -> bool {
+                if (!is_v) return true;
                 constexpr uint32_t NR = Cfg::NR;
-                // Every thread reaches the one barrier of an entry, whatever its
-                // waits say; all leave together.
-                bool ok = tile_wait(&bars->raw_full[e % NR], (e / NR) & 1, abort_flag, p, SITE_TILE_FULL);
-                const int kt = tile_slot<Cfg>(w, t, u), slot = kt % Cfg::SLOTS;
+                const uint32_t e = tile_slot<Cfg>(w, t, u), slot = e % Cfg::SLOTS;
                 const int key0 = ((t == 0 ? w.j0[0] : w.j0[1]) + u) * BN;
+                // The tile's V scales, divided by the stream's vref (which follows
+                // their maximum).  0 for keys that are not there (stale) and where
+                // only some query rows see a key with a NaN scale: those rows learn
+                // it from the poison bits, since a weight of 0 beside it must stay
+                // 0.  Every thread reaches the one barrier of a tile, whatever its
+                // waits say; all leave together.
+                bool ok = tile_wait(&bars->sc_full[slot], (e / Cfg::SLOTS) & 1, abort_flag, p, SITE_TILE_SCALE);
                 const uint32_t* valid = bars->valid[slot];
                 uint32_t all = valid[0] & valid[1];
                 if constexpr (BN == 128) all &= valid[2] & valid[3];
@@ -617,27 +660,18 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 const bool diagonal = key0 / BN >= diag;
                 uint32_t* poison = bars->poison[min(max(key0 / BN - diag, 0), Cfg::DIAG_TILES - 1)];
                 float v = 0.0f;
-                if (!is_v) {
-                    // The tile's V scales, divided by the stream's vref (which
-                    // follows their maximum).  0 for keys that are not there
-                    // (stale) and where only some query rows see a key with a NaN
-                    // scale: those rows learn it from the poison bits, since a
-                    // weight of 0 beside it must stay 0.
-                    ok = ok && tile_wait(&bars->sc_full[slot], (kt / Cfg::SLOTS) & 1, abort_flag, p, SITE_TILE_SCALE);
-                    if (ct < BN && ((valid[ct >> 5] >> (ct & 31)) & 1u)) {
-                        v = sScale[slot * 2 * BN + BN + ct];
-                        if (diagonal && key0 + ct >= diag_key && !(v < INFINITY)) {
-                            v = 0.0f;
-                            atomicOr(&poison[ct >> 5], 1u << (ct & 31));
-                        }
+                if (ct < BN && ((valid[ct >> 5] >> (ct & 31)) & 1u)) {
+                    v = sScale[slot * 2 * BN + BN + ct];
+                    if (diagonal && key0 + ct >= diag_key && !(v < INFINITY)) {
+                        v = 0.0f;
+                        atomicOr(&poison[ct >> 5], 1u << (ct & 31));
                     }
-                    const uint32_t top = __reduce_max_sync(0xffffffffu, v > 0.0f && v < INFINITY ? __float_as_uint(v) : 0u);
-                    if (lane == 0) bars->red[kt & 1][ct >> 5] = __uint_as_float(top);
                 }
-                ok = ok && tile_wait(&bars->ring_empty[e % NH], ((e / NH) & 1) ^ 1, abort_flag, p, SITE_TILE_EMPTY);
+                const uint32_t top = __reduce_max_sync(0xffffffffu, v > 0.0f && v < INFINITY ? __float_as_uint(v) : 0u);
+                if (lane == 0) bars->red[e & 1][ct >> 5] = __uint_as_float(top);
                 if (!named_barrier_and(1, 128, ok)) return false;
-                if (!is_v) {
-                    const float* red = bars->red[kt & 1];
+                {
+                    const float* red = bars->red[e & 1];
                     const float vm = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
                     float ref = w.pair || t == 0 ? vref0 : vref1;
                     if (vm > 64.0f * ref) ref = vref_of(vm);
@@ -645,7 +679,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     else vref1 = ref;
                     if (ct < BN) sScale[slot * 2 * BN + BN + ct] = v * (ref == 0.0f ? 0.0f : 1.0f / ref);
                     if (ct == 0) bars->vref[slot] = ref;
+                    mbar_arrive(&bars->vs_ready[slot]);
                 }
+                if (!tile_wait(&bars->raw_full[e % NR], (e / NR) & 1, abort_flag, p, SITE_TILE_FULL)) ok = false;
+                if (ok && !tile_wait(&bars->ring_empty[e % NH], ((e / NH) & 1) ^ 1, abort_flag, p, SITE_TILE_EMPTY)) ok = false;
+                if (!named_barrier_and(1, 128, ok)) return false;
                 const uint8_t* src = sRaw + (e % NR) * Cfg::RAW_BYTES + r0 * D + c * 16;
                 uint8_t* dst = sRing + (e % NH) * Cfg::HALF_BYTES;
                 auto convert = [&](auto check) {
@@ -655,7 +693,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         uint4 v = *reinterpret_cast<const uint4*>(src + i * RPP * D);
                         if constexpr (decltype(check)::value) {
                             if (!((valid[r >> 5] >> (r & 31)) & 1u)) v = make_uint4(0, 0, 0, 0);
-                            if (is_v && diagonal && key0 + r >= diag_key) {
+                            if (diagonal && key0 + r >= diag_key) {
                                 uint32_t* wd = &v.x;
                                 uint32_t nan = 0;
 #pragma unroll
@@ -673,12 +711,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c + !odd)) = odd ? lo : hi;
                     }
                 };
-                if (whole && !(is_v && diagonal)) convert(std::false_type{});
+                if (whole && !diagonal) convert(std::false_type{});
                 else convert(std::true_type{});
                 fence_proxy_async_smem();
                 mbar_arrive(&bars->ring_full[e % NH]);
                 mbar_arrive(&bars->raw_empty[e % NR]);
-                ++e;
                 return true;
             });
         }
@@ -707,20 +744,32 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         cp_async_commit();
         cp_async_wait<0>();
         if constexpr (FP8) {
-            // To fp16 in place, one row a thread (the warp's own rows).
-            __syncwarp();
+            // Into two e4m3 parts, one row a thread, over the bf16 rows (which all
+            // threads have read by then).
             if (w.pair || t == 0) {
                 const int rq = tid & 127;
-                uint8_t* tile = sQ + t * Cfg::Q_BYTES + rq * 128;
+                uint8_t* tile = sQ + t * Cfg::Q_BYTES;
+                uint4 v[D / 8];
                 uint32_t top = 0;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    top = max(top, bf16x8_amax(*reinterpret_cast<const uint4*>(tile + (c >> 3) * (BM * 128) + (((c & 7) ^ (rq & 7)) << 4))));
-                const int shift = q_shift(top);
+                __syncwarp();
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
-                    uint4* at = reinterpret_cast<uint4*>(tile + (c >> 3) * (BM * 128) + (((c & 7) ^ (rq & 7)) << 4));
-                    *at = q_to_f16(*at, pow2f(shift));
+                    v[c] = *reinterpret_cast<const uint4*>(tile + (c >> 3) * (BM * 128) + rq * 128 + (((c & 7) ^ (rq & 7)) << 4));
+                    top = max(top, bf16x8_amax(v[c]));
+                }
+                named_barrier(2 + t, 128);
+                const int shift = q_shift(top, 7);
+                const float up = pow2f(shift);
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    uint4 q1, q2;
+                    q_split(v[2 * c], up, q1.x, q1.y, q2.x, q2.y);
+                    q_split(v[2 * c + 1], up, q1.z, q1.w, q2.z, q2.w);
+                    constexpr int PER = Cfg::SWK / 16;
+                    const int x = Cfg::SWK == 128 ? (c % PER) ^ (rq & 7) : (c % PER) ^ ((rq >> 1) & 3);
+                    uint8_t* at = tile + (c / PER) * (BM * Cfg::SWK) + rq * Cfg::SWK + (x << 4);
+                    *reinterpret_cast<uint4*>(at) = q1;
+                    *reinterpret_cast<uint4*>(at + BM * D) = q2;
                 }
                 bars->q_log2[t * 128 + rq] = p.scale_log2 * pow2f(-shift);
             }
@@ -746,6 +795,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             const int kt = tile_slot<Cfg>(w, t, u);
             const int slot = kt % Cfg::SLOTS;
             bool wt = tile_wait(&bars->sc_full[slot], (kt / Cfg::SLOTS) & 1, abort_flag, p, SITE_TILE_SCALE);
+            if (FP8) wt = wt && tile_wait(&bars->vs_ready[slot], (kt / Cfg::SLOTS) & 1, abort_flag, p, SITE_TILE_SCALE);
             wt = wt && tile_wait(&bars->s_full[t], u & 1, abort_flag, p, SITE_TILE_S);
             if (!__all_sync(0xffffffffu, wt)) {
                 ok = false;
