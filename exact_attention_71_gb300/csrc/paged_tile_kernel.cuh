@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     uint8_t* sK = sRing + NH * Cfg::HALF_BYTES;                // e4m3: K tiles
     uint8_t* sRaw = sK + Cfg::NK * Cfg::RAW_BYTES;             // e4m3: V tiles
     float* sScale = reinterpret_cast<float*>(sRaw + Cfg::NR * Cfg::RAW_BYTES);     // (slot, k / v, BN)
-    TileBarriers* bars = reinterpret_cast<TileBarriers*>(reinterpret_cast<uint8_t*>(sScale) + Cfg::SC_BYTES);
+    uint8_t* sEpi = reinterpret_cast<uint8_t*>(sScale) + Cfg::SC_BYTES;            // d = 64: output staging
+    TileBarriers* bars = reinterpret_cast<TileBarriers*>(sEpi + Cfg::EPI_BYTES);
     volatile int* abort_flag = &bars->abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -771,7 +772,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     *reinterpret_cast<uint4*>(at) = q1;
                     *reinterpret_cast<uint4*>(at + BM * D) = q2;
                 }
-                bars->q_log2[t * 128 + rq] = p.scale_log2 * pow2f(-shift);
+                // (not 0: -inf, the masked score, stays -inf when multiplied)
+                bars->q_log2[t * 128 + rq] = fmaxf(p.scale_log2 * pow2f(-shift), 0x1p-126f);
             }
         }
         fence_proxy_async_smem();
@@ -1097,7 +1099,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             // bytes, swizzled by 16-byte chunk), so that every store instruction
             // writes whole 128-byte lines instead of 16 bytes of 32 rows.  (An
             // empty part's O is not written: the join does not read it.)
-            uint8_t* epi = D == 64 ? reinterpret_cast<uint8_t*>(bars) - Cfg::EPI_BYTES + t * 16384
+            uint8_t* epi = D == 64 ? sEpi + t * 16384
                          : w.pair || NS == 1 ? sQ + t * Cfg::Q_BYTES
                                              : sQ + Cfg::Q_BYTES + t * 16384;
             epi += (warp & 3) * 4096;

@@ -106,6 +106,9 @@ class Problem:
             assert within, (b, float(dl.max()))
 
 
+# Every kernel and mode: few rows (streaming kernel) and many (tile kernel: one row
+# tile or pairs of them, an odd number of tiles), both over the prefix and over own
+# tokens; ranges that end inside a page, a key tile, a step; one part and many.
 SHAPES = [
     # lens, prefix, Nq, H, H_kv, d, page
     ([1], 0, 1, 1, 1, 64, 16),
@@ -123,7 +126,15 @@ SHAPES = [
     ([40] * 37, 300, 1, 8, 1, 128, 16),              # many rows behind the prefix
     ([600, 20], 1300, 2, 16, 1, 256, 64),
     ([5000], 0, 1, 4, 1, 128, 16),                   # several ranges
-    ([1, 2000], 3000, 3, 2, 2, 64, 32),
+    ([1, 2000], 2900, 3, 2, 2, 64, 32),
+    ([200, 150], 0, 40, 4, 2, 64, 16),               # own tokens in the tile kernel: one row tile
+    ([513, 400], 65, 100, 4, 1, 128, 32),            # four row tiles, then five
+    ([700], 129, 160, 4, 1, 64, 256),
+    ([129, 128, 127], 127, 64, 2, 1, 256, 128),
+    ([33], 4100, 1, 64, 1, 128, 64),                 # one row tile over a long prefix
+    ([5] * 65, 1000, 1, 8, 2, 256, 16),
+    ([9000], 0, 1, 2, 1, 64, 16),                    # more than 32 ranges
+    ([20000], 0, 2, 1, 1, 128, 64),                  # more than 128 ranges
 ]
 
 
@@ -414,6 +425,135 @@ def test_cache_beyond_32_bit_offsets():
     for x, y in zip(api.attn_fwd_paged(q, cache, order[None], lens * 0, order, N),
                     api.attn_fwd_paged(q, low, near, lens * 0, near[0].contiguous(), N)):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Nq", [3, 70])
+def test_rows_whose_first_keys_are_masked_or_far_below_the_later_ones(fp8, Nq):
+    """Scores of -800 before scores around 0 and the other way round: the running
+    reference has to follow, whatever kernel has the rows."""
+    p = Problem([300, 260], 400, Nq, 4, 2, 64, 32, fp8, seed=31)
+    # q has one large element; the prefix's keys and some own ones oppose it
+    p.q[..., 0] = 40.0
+    for b, ks in enumerate(p.k):
+        ks[..., 0] = 0.0
+        n = len(ks)
+        if b == 0:
+            ks[: n // 2, :, 0] = -160.0
+        else:
+            ks[n // 3:, :, 0] = -160.0 if b == 1 else 20.0
+        t = p.prefix_table if b == 0 else p.table[b - 1]
+        i = torch.arange(n, device=DEV)
+        api.attn_kv_write(ks, p.v[b], t.long()[i // 32] * 32 + i % 32, p.cache)
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("Nq", [1, 80])
+def test_value_scales_that_differ_by_orders_of_magnitude(Nq):
+    """e4m3: the values' row scales ride on the weights, which are kept in 16 bits."""
+    p = Problem([400, 90], 700, Nq, 4, 2, 128, 16, True, seed=33)
+    g = gen(34)
+    for b, vs in enumerate(p.v):
+        vs *= torch.exp2(torch.randint(-12, 13, (len(vs), 1, 1), generator=g, device=DEV).float()).to(torch.bfloat16)
+        vs[: len(vs) // 4] *= 2.0 ** -40
+        t = p.prefix_table if b == 0 else p.table[b - 1]
+        i = torch.arange(len(vs), device=DEV)
+        api.attn_kv_write(p.k[b], vs, t.long()[i // 16] * 16 + i % 16, p.cache)
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("Nq", [1, 80])
+def test_queries_of_any_magnitude(fp8, Nq):
+    """Rows of q from the smallest to the largest bf16 numbers (their scores are
+    brought back by the scale), rows of zeros, and one with a NaN."""
+    p = Problem([300, 200], 150, Nq, 4, 2, 128, 64, fp8, seed=35)
+    p.q[0] *= 2.0 ** 100
+    p.q[1] *= 2.0 ** -120
+    p.q[0, 0, 1] = 0.0
+    o, lse = p.run(scale=2.0 ** -103)
+    keep = p.q.clone()
+    p.q[1] = 0.0          # 2^-120 2^-103: the scores vanish
+    p.check(o, lse, scale=2.0 ** -103)
+    p.q.copy_(keep)
+    p.q[0, Nq - 1, 2, 77] = NAN
+    o2, l2 = p.run(scale=2.0 ** -103)
+    bad = torch.isnan(o2).all(-1)
+    assert bad.sum() == 1 and bool(bad[0, Nq - 1, 2]) and bool(torch.isnan(l2[0, 2, Nq - 1]))
+    o2[0, Nq - 1, 2] = o[0, Nq - 1, 2]
+    assert torch.equal(o2, o)
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Each with its own workspace, over one cache; both equal the calls alone."""
+    p = Problem([300, 200, 100, 40], 700, 2, 8, 2, 128, 16, True, seed=41)
+    r = Problem([600, 31], 300, 40, 8, 2, 128, 16, False, seed=42)
+    want = [p.run(), r.run()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        got = [x.run(stream=s) for x, s in zip((p, r), streams)]
+        for s in streams:
+            s.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_calls_in_a_row_share_a_workspace():
+    """Ordered on one stream, each overwrites it: shapes that use it differently."""
+    ps = [Problem([300, 77], 900, 3, 8, 2, 128, 16, True, seed=14), Problem([50] * 30, 200, 1, 8, 8, 128, 16, False, seed=15),
+          Problem([600], 130, 100, 8, 2, 128, 64, True, seed=16)]
+    need = max(api.paged_workspace_bytes(x.q.shape[0], x.q.shape[1], 8, x.hkv, 128, x.prefix, x.table.shape[1], x.ps) for x in ps)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    got = [x.run(workspace=ws) for x in ps] + [x.run(workspace=ws) for x in ps]
+    for x, g in zip(ps + ps, got):
+        x.check(*g)
+
+
+def test_a_full_reference_of_a_decoding_batch_of_many_sequences():
+    p = Problem([(7 * b) % 90 for b in range(200)], 333, 1, 4, 1, 64, 16, True, seed=43)
+    p.check(*p.run())
+
+
+def test_waits_that_run_out_are_reported_and_the_context_survives():
+    """A one-cycle limit makes the kernels give up: they return, the host sees the
+    status, and the next call is right."""
+    lib = api.library()
+    for Nq, fp8 in ((1, False), (1, True), (90, False), (90, True)):
+        p = Problem([2000, 1500], 2000, Nq, 8, 2, 128, 64, fp8, seed=44)
+        want = p.run()
+        torch.cuda.synchronize()
+        assert api.device_status()[0] == 0
+        assert lib.attn_set_wait_limit(1) == 0
+        try:
+            p.run()
+            rc, site = api.device_status()
+        finally:
+            lib.attn_set_wait_limit(0)
+        assert rc in (0, -4)
+        if rc:
+            assert 0xa1 <= site <= 0xab or site in (0xb1, 0xb2), hex(site)
+        assert api.device_status()[0] == 0
+        got = p.run()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        assert api.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("change, match", [
+    (dict(dtype=torch.float16), "bf16"), (dict(heads=3), "multiple"), (dict(dim=128), "head dim"),
+    (dict(table=torch.int64), "block_table"), (dict(lens=torch.int64), "seq_lens"), (dict(short=True), "prefix_table"),
+    (dict(flip=True), "contiguous"),
+])
+def test_binding_refusals(change, match):
+    c = api.kv_cache(8, 16, 2, 64)
+    q = torch.zeros(2, 1, change.get("heads", 4), change.get("dim", 64), dtype=change.get("dtype", torch.bfloat16), device=DEV)
+    if change.get("flip"):
+        q = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16, device=DEV).expand(2, 4, 2, 64).transpose(1, 2)
+    table = torch.zeros(2, 2, dtype=change.get("table", torch.int32), device=DEV)
+    lens = torch.ones(2, dtype=change.get("lens", torch.int32), device=DEV)
+    pre = torch.zeros(1 if change.get("short") else 4, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError, match=match):
+        api.attn_fwd_paged(q, c, table, lens, pre, 40)
 
 
 def test_repeated_calls_give_the_same_bits():
