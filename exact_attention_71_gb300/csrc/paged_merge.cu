@@ -18,17 +18,39 @@ namespace {
 
 long long up(long long a, long long b) { return (a + b - 1) / b; }
 
-// CTAs that share a row tile's keys (tile kernel, one CTA an SM): as few waves
-// x key tiles per CTA as possible, a CTA's fixed cost (query load, pipeline
-// fill, epilogue) counted as three key tiles.
-int tile_ctas(long long units, long long tiles) {
+// Times of the tile kernel, measured, in microseconds: a step of a CTA (d = 64 and
+// 128: a key tile against two row tiles, or two key tiles against one; d = 256: one
+// key tile), and what a CTA costs besides (launch, query rows, first copies,
+// epilogue).
+constexpr double kTileFixedUs = 7.0;
+double tile_step_us(int d) { return d == 256 ? 1.3 : 1.6; }
+
+// CTAs that share a row tile's keys (tile kernel, one CTA an SM).  By itself the
+// kernel is fastest with as few waves x steps as possible.  The streaming kernel
+// starts beside it on the SMs that it leaves free, and is bound by memory where
+// the tile kernel is bound by the tensor cores: with `other` SM-microseconds of
+// streaming work the total is what counts, and fewer, longer CTAs may serve it
+// better (decode_shared: 16 units x 9 CTAs and then the own tokens 73 us, 16 x 6
+// beside them 60).  That work is an estimate (the lengths are not known here), so
+// the tile kernel itself may become at most half as slow again by it.
+int tile_ctas(int d, long long units, long long steps, double other) {
+    const auto alone = [&](long long s) {
+        return static_cast<double>(up(units * s, kPlanSms)) * (static_cast<double>(up(steps, s)) * tile_step_us(d) + kTileFixedUs);
+    };
+    const long long most = std::min<long long>(kPlanSms, steps);
+    double least = alone(1);
+    for (long long s = 2; s <= most; ++s) least = std::min(least, alone(s));
     int best = 1;
-    long long best_cost = -1;
-    for (int s = 1; s <= kPlanSms && s <= tiles; ++s) {
-        const long long cost = up(units * s, kPlanSms) * (up(tiles, s) + 3);
-        if (best_cost < 0 || cost < best_cost) {
-            best = s;
-            best_cost = cost;
+    double best_total = -1.0;
+    for (long long s = 1; s <= most; ++s) {
+        const double t = alone(s);
+        if (t > 1.5 * least) continue;
+        const double free_sms = units * s < kPlanSms ? static_cast<double>(kPlanSms - units * s) : 0.0;
+        const double rest = other - free_sms * t;
+        const double total = rest > 0.0 ? t + rest / kPlanSms : std::max(t, free_sms > 0.0 ? other / free_sms : t);
+        if (best_total < 0.0 || total < best_total) {
+            best = static_cast<int>(s);
+            best_total = total;
         }
     }
     return best;
@@ -58,19 +80,26 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
         }
         return best;
     };
+    // Steps of a CTA over `keys`: two streams halve the tiles of a single row tile.
+    const auto steps_of = [&](long long keys, long long tiles) { return up(keys, bn * (d != 256 && tiles == 1 ? 2 : 1)); };
+    double streaming = 0.0;                                              // SM-microseconds
     if (rows > kStreamRows) {
         const long long tiles = up(rows, 128), groups = d == 256 ? tiles : up(tiles, 2);
-        plan.own_ctas = tile_ctas(B * static_cast<long long>(H_kv) * groups, up(own, bn));
+        plan.own_ctas = tile_ctas(d, B * static_cast<long long>(H_kv) * groups, steps_of(own, tiles), 0.0);
         plan.own_items = static_cast<int>(B * static_cast<long long>(H_kv) * groups * plan.own_ctas);
         plan.own_parts = plan.own_ctas;
     } else {
-        plan.own_parts = stream_parts(own, B * static_cast<long long>(H_kv) * up(rows, 16));
+        const long long units = B * static_cast<long long>(H_kv) * up(rows, 16);
+        plan.own_parts = stream_parts(own, units);
+        // (sequences fill three quarters of their tables, say; a key of one head
+        // takes an SM 0.08 d nanoseconds)
+        streaming = 0.75 * static_cast<double>(units) * static_cast<double>(own) * 0.08e-3 * d;
     }
     if (prefix_len > 0) {
         const long long all = B * rows;
         if (all > kStreamPrefixRows) {
             const long long tiles = up(all, 128), groups = d == 256 ? tiles : up(tiles, 2);
-            plan.prefix_ctas = tile_ctas(H_kv * groups, up(prefix_len, bn));
+            plan.prefix_ctas = tile_ctas(d, H_kv * groups, steps_of(prefix_len, tiles), streaming);
             plan.prefix_items = static_cast<int>(H_kv * groups * plan.prefix_ctas);
             plan.prefix_parts = plan.prefix_ctas;
         } else {
