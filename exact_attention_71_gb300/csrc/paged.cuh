@@ -118,7 +118,7 @@ constexpr int kStreamPrefixRows = 16;
 constexpr int kMaxParts = 256;
 
 // A streaming CTA's fixed cost, in keys.
-constexpr double kStreamFixed = 200.0;
+constexpr double kStreamFixed = 300.0;
 
 PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size);
 

@@ -3,8 +3,9 @@
 //
 // Both are streams: a row of a token is read once and written once, so the
 // bound is memory bandwidth, and the instructions have to stay below it.  A row is
-// d / 16 lanes x 16 elements (32 bytes of bf16, 16 of codes); K and V of a row go
-// through the same thread, which keeps four independent loads in flight.
+// d / 16 lanes, each with eight elements of either half of the row (so that the
+// lanes of a load or a store instruction are next to one another); K and V of a row
+// go through the same thread, which keeps four independent loads in flight.
 #include <cuda_bf16.h>
 
 #include "paged.cuh"
@@ -24,9 +25,31 @@ struct Row16 {
     uint4 lo, hi;                  // 16 bf16
 };
 
+template <int D>
 __device__ __forceinline__ Row16 load_row(const void* base, long long at, int lane) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at) + 2 * lane;
-    return {__ldg(src), __ldg(src + 1)};
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at) + lane;
+    return {__ldg(src), __ldg(src + D / 16)};
+}
+
+template <int D>
+__device__ __forceinline__ void store_row(void* base, long long at, int lane, const Row16& x) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at) + lane;
+    dst[0] = x.lo;
+    dst[D / 16] = x.hi;
+}
+
+template <int D>
+__device__ __forceinline__ void store_codes(void* base, long long at, int lane, const uint4& c) {
+    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + at) + lane;
+    dst[0] = make_uint2(c.x, c.y);
+    dst[D / 16] = make_uint2(c.z, c.w);
+}
+
+template <int D>
+__device__ __forceinline__ uint4 load_codes(const void* base, long long at, int lane) {
+    const uint2* src = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + at) + lane;
+    const uint2 a = __ldg(src), b = __ldg(src + D / 16);
+    return make_uint4(a.x, a.y, b.x, b.y);
 }
 
 // The largest |x| of a row held by LANES lanes, as bf16 bits.  Unsigned
@@ -97,8 +120,8 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams 
     long long slot = -1;
     if (in) {
         slot = __ldg(p.slots + t);
-        k = load_row(p.k, t * p.k_stride + h * D, lane);
-        v = load_row(p.v, t * p.v_stride + h * D, lane);
+        k = load_row<D>(p.k, t * p.k_stride + h * D, lane);
+        v = load_row<D>(p.v, t * p.v_stride + h * D, lane);
     }
     const bool store = slot >= 0 && slot < p.num_slots;
     if (slot >= p.num_slots) report(p.status, SITE_PAGED_SLOT);
@@ -109,20 +132,16 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams 
         float ks, vs;
         const uint4 kc = quantise_row<LANES>(k, ks), vc = quantise_row<LANES>(v, vs);
         if (store) {
-            reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.k_cache) + at * D)[lane] = kc;
-            reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.v_cache) + at * D)[lane] = vc;
+            store_codes<D>(p.k_cache, at * D, lane, kc);
+            store_codes<D>(p.v_cache, at * D, lane, vc);
             if (lane == 0) {
                 p.k_scale[at] = ks;
                 p.v_scale[at] = vs;
             }
         }
     } else if (store) {
-        uint4* kd = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k_cache) + at * D) + 2 * lane;
-        uint4* vd = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v_cache) + at * D) + 2 * lane;
-        kd[0] = k.lo;
-        kd[1] = k.hi;
-        vd[0] = v.lo;
-        vd[1] = v.hi;
+        store_row<D>(p.k_cache, at * D, lane, k);
+        store_row<D>(p.v_cache, at * D, lane, v);
     }
 }
 
@@ -167,20 +186,15 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p)
     const long long to = ((static_cast<long long>(b) * p.N + n) * p.H_kv + h) * D;
     Row16 k, v;
     if constexpr (FP8) {
-        const uint4 kc = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.k_cache) + at * D) + lane);
-        const uint4 vc = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.v_cache) + at * D) + lane);
+        const uint4 kc = load_codes<D>(p.k_cache, at * D, lane), vc = load_codes<D>(p.v_cache, at * D, lane);
         k = dequantise(kc, __ldg(p.k_scale + at));
         v = dequantise(vc, __ldg(p.v_scale + at));
     } else {
-        k = load_row(p.k_cache, at * D, lane);
-        v = load_row(p.v_cache, at * D, lane);
+        k = load_row<D>(p.k_cache, at * D, lane);
+        v = load_row<D>(p.v_cache, at * D, lane);
     }
-    uint4* kd = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.k) + to) + 2 * lane;
-    uint4* vd = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.v) + to) + 2 * lane;
-    kd[0] = k.lo;
-    kd[1] = k.hi;
-    vd[0] = v.lo;
-    vd[1] = v.hi;
+    store_row<D>(p.k, to, lane, k);
+    store_row<D>(p.v, to, lane, v);
 }
 
 template <int D>

@@ -64,7 +64,7 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     const long long own = static_cast<long long>(max_pages) * page_size;
     const int bn = d == 256 ? 64 : 128;
     // Streaming kernel.  A CTA's time is its keys plus a fixed cost (page table,
-    // first loads, join) worth about 200; beyond one wave CTAs replace one
+    // first loads, join) worth about 300; beyond one wave CTAs replace one
     // another as they finish, and half a CTA's time is lost at the end.
     const double slots = kPlanSms * (d == 64 ? 4.0 : d == 128 ? 3.0 : 2.0);
     const auto stream_parts = [&](long long keys, long long units) {
