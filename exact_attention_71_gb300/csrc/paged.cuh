@@ -110,9 +110,17 @@ constexpr int kPlanSms = 152;
 constexpr int kOwnChunk = 128;
 
 // Query rows of one key/value head (of one sequence; over the prefix, of all)
-// up to which the streaming kernel takes them.
-constexpr int kStreamRows = 32;
-constexpr int kStreamPrefixRows = 16;
+// up to which the streaming kernel takes them; it reads the keys once per 16
+// rows, the tile kernel once per 128.  Microseconds of the streaming | the tile
+// kernel, 8 heads, at 16, 32 and 48 rows (the prefix: 64):
+//   own tokens, 32 x 4096:  d = 64  bf16  39 | 61   51 | 61   72 | 59   e4m3  37 | 82   60 | 83   85 | 86
+//                           d = 128 bf16  69 | 89   89 | 89  122 | 86   e4m3  59 | 117  96 | 119  127 | 122
+//                           d = 256 bf16 156 | 162 266 | 164 386 | 161  e4m3 107 | 191 178 | 194  238 | 192
+//   prefix of 32768:        d = 64  bf16  22 | 30   23 | 31   31 | 33   e4m3  21 | 37   25 | 39   36 | 41
+//                           d = 128 bf16  32 | 46   33 | 46   50 | 49   e4m3  28 | 57   35 | 56   51 | 60
+//                           d = 256 bf16  60 | 62   89 | 65  158 | 68   e4m3  43 | 82   60 | 83   99 | 87
+// (a plan does not depend on the cache's type, so that a workspace fits both).
+constexpr int stream_rows(int d) { return d == 256 ? 16 : 32; }
 
 // Key ranges of a prefix, and of a sequence's own tokens, at most.
 constexpr int kMaxParts = 256;

@@ -30,8 +30,10 @@ double tile_step_us(int d) { return d == 256 ? 1.3 : 1.6; }
 // starts beside it on the SMs that it leaves free, and is bound by memory where
 // the tile kernel is bound by the tensor cores: with `other` SM-microseconds of
 // streaming work the total is what counts, and fewer, longer CTAs may serve it
-// better (decode_shared: 16 units x 9 CTAs and then the own tokens 73 us, 16 x 6
-// beside them 60).  That work is an estimate (the lengths are not known here), so
+// better (64 sequences x 4 query heads a key/value head, d = 128, behind a bf16
+// prefix of 8192 with 1024 tokens of their own: 9 CTAs for each of the 16 units of
+// the prefix, and the own tokens after them, 75 us; 6, with the own tokens beside
+// them, 62).  That work is an estimate (the lengths are not known here), so
 // the tile kernel itself may become at most half as slow again by it.
 int tile_ctas(int d, long long units, long long steps, double other) {
     const auto alone = [&](long long s) {
@@ -83,7 +85,7 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     // Steps of a CTA over `keys`: two streams halve the tiles of a single row tile.
     const auto steps_of = [&](long long keys, long long tiles) { return up(keys, bn * (d != 256 && tiles == 1 ? 2 : 1)); };
     double streaming = 0.0;                                              // SM-microseconds
-    if (rows > kStreamRows) {
+    if (rows > stream_rows(d)) {
         const long long tiles = up(rows, 128), groups = d == 256 ? tiles : up(tiles, 2);
         plan.own_ctas = tile_ctas(d, B * static_cast<long long>(H_kv) * groups, steps_of(own, tiles), 0.0);
         plan.own_items = static_cast<int>(B * static_cast<long long>(H_kv) * groups * plan.own_ctas);
@@ -97,7 +99,7 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     }
     if (prefix_len > 0) {
         const long long all = B * rows;
-        if (all > kStreamPrefixRows) {
+        if (all > stream_rows(d)) {
             const long long tiles = up(all, 128), groups = d == 256 ? tiles : up(tiles, 2);
             plan.prefix_ctas = tile_ctas(d, H_kv * groups, steps_of(prefix_len, tiles), streaming);
             plan.prefix_items = static_cast<int>(H_kv * groups * plan.prefix_ctas);

@@ -14,18 +14,23 @@
 // results are joined at the end.  At d = 256 tensor memory holds one stream.
 //
 //   warps [0, 4 NS)       softmax (one thread per row); they also bring in Q
-//   e4m3: 4 warps         convert the codes of a V tile to fp16 (exact; V's row
-//                         scales go to P, which is brought into fp16's range by a
-//                         power of two: see the streaming kernel).  K is multiplied
-//                         as it is: q is split into two e4m3 parts, q = (q1 + q2)
-//                         2^shift, so that S = q1 K^T + q2 K^T in the 8-bit products
-//                         that run at twice the rate.  The tensor cores add them
-//                         up in 25 bits (measured: 2^-22 of sum |q k|).
+//   e4m3: 4 warps         convert the codes of a V tile to fp16, times the row's
+//                         scale over vref (a power of two that keeps the products in
+//                         fp16's range: see the streaming kernel).  The ratio and
+//                         the product are rounded to fp16, 2^-11 each; with the
+//                         ratio on P instead, in the softmax, a chunk of 512
+//                         queries over 8192 keys took 165 us against 160.
+//                         K is multiplied as it is: q is split into two e4m3
+//                         parts, q = (q1 + q2) 2^shift, so that S = q1 K^T + q2 K^T
+//                         in the 8-bit products that run at twice the rate.  The
+//                         tensor cores add them up in 25 bits (measured: 2^-22 of
+//                         sum |q k|).
 //   load warp             walks the page table: a head's rows of a page are
 //                         contiguous, so a bf16 tile is BN / page_size TMA boxes
 //                         per 64 columns, written swizzled into a ring of half
-//                         stages (K and V alternating), and an e4m3 tile is
-//                         BN / page_size bulk copies into a ring of raw tiles
+//                         stages (K and V alternating); e4m3: K tiles likewise
+//                         (per 128 columns) into a ring of their own, and V tiles
+//                         as BN / page_size bulk copies into a ring of raw tiles
 //   MMA warps             one per stream, issue tcgen05.mma: S = Q K^T, O += P V
 //                         (one warp for both streams left the pipe idle between
 //                         steps: 3150 cycles a step of two 128 x 128 x 128 tiles)
@@ -687,6 +692,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 if (!named_barrier_and(1, 128, ok)) return false;
                 const uint8_t* src = sRaw + (e % NR) * Cfg::RAW_BYTES + r0 * D + c * 16;
                 uint8_t* dst = sRing + (e % NH) * Cfg::HALF_BYTES;
+                const float* vs = sScale + slot * 2 * BN + BN;
                 auto convert = [&](auto check) {
 #pragma unroll
                     for (int i = 0; i < BN / RPP; ++i) {
@@ -706,8 +712,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                                 if (nan) atomicOr(&poison[r >> 5], 1u << (r & 31));
                             }
                         }
-                        const uint4 lo = make_uint4(f16x2_of_lo(v.x), f16x2_of_hi(v.x), f16x2_of_lo(v.y), f16x2_of_hi(v.y));
-                        const uint4 hi = make_uint4(f16x2_of_lo(v.z), f16x2_of_hi(v.z), f16x2_of_lo(v.w), f16x2_of_hi(v.w));
+                        const float s1 = vs[r];
+                        const uint32_t s2 = pack_f16x2(s1, s1);
+                        const uint4 lo = make_uint4(mul_f16x2(f16x2_of_lo(v.x), s2), mul_f16x2(f16x2_of_hi(v.x), s2),
+                                                    mul_f16x2(f16x2_of_lo(v.y), s2), mul_f16x2(f16x2_of_hi(v.y), s2));
+                        const uint4 hi = make_uint4(mul_f16x2(f16x2_of_lo(v.z), s2), mul_f16x2(f16x2_of_hi(v.z), s2),
+                                                    mul_f16x2(f16x2_of_lo(v.w), s2), mul_f16x2(f16x2_of_hi(v.w), s2));
                         *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c + odd)) = odd ? hi : lo;
                         *reinterpret_cast<uint4*>(dst + tile_offset<Cfg>(r, 2 * c + !odd)) = odd ? lo : hi;
                     }
@@ -829,7 +839,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
                 for (int x = 0; x < 8 * NG; x += 32) reg_fence32(sr + x);
                 const float2* ks = reinterpret_cast<const float2*>(sScale + slot * 2 * BN) + (lane & 3);
-                const float2* vs = ks + BN / 2;
                 const int key0 = (j0 + u) * BN;
                 uint32_t all = 0xffffffffu;
 #pragma unroll
@@ -868,13 +877,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         const uint32_t* e = sr + (i >> 1) * 4 * NG + g * 4 + (i & 1) * 2;
                         mx[i] = fmax3(mx[i], __uint_as_float(e[0]), __uint_as_float(e[1]));
                     }
-                // The references move only by jumps of more than 8 (log2 units), per
-                // row; O and l share them.
+                // A reference is set 7 (log2 units) below its row's maximum and moves
+                // when that is more than 15 above it: P lies below 2^15, and what
+                // fp16 rounds to 0 below 2^-25 is 2^-32 of the largest weight.  O and
+                // l share them.
                 bool move = false;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     mx[i] *= tl4[i];
-                    move = move || mx[i] > m4[i] + 8.0f;
+                    move = move || mx[i] > m4[i] + 15.0f;
                 }
                 float fall4[4] = {vfall, vfall, vfall, vfall};
                 if (__any_sync(0xffffffffu, move)) {
@@ -882,7 +893,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     for (int i = 0; i < 4; ++i) {
                         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
                         mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-                        const float mn = mx[i] > m4[i] + 8.0f ? mx[i] : m4[i];
+                        const float mn = mx[i] > m4[i] + 15.0f ? mx[i] - 7.0f : m4[i];
                         const float a = mn == m4[i] ? 1.0f : ex2_approx(m4[i] - mn);
                         m4[i] = mn;
                         l4[i] *= a;
@@ -900,8 +911,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 }
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    // V's row scale rides on P; l sums the plain weights.
-                    const float2 v2 = vs[4 * g];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t* e = sr + (i >> 1) * 4 * NG + g * 4 + (i & 1) * 2;
@@ -909,7 +918,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         f.x = ex2_approx(f.x);
                         f.y = ex2_approx(f.y);
                         acc[i] = __fadd2_rn(acc[i], f);
-                        f = __fmul2_rn(f, v2);
                         // (packed into the half's first registers: all of it is read by now)
                         sr[(i >> 1) * 4 * NG + g * 2 + (i & 1)] = pack_f16x2(f.x, f.y);
                     }
