@@ -83,6 +83,7 @@ struct PagedParams {
     int prefix_parts, own_parts; // parts [0, prefix_parts) are the prefix's
     int prefix_items, prefix_ctas;   // tile kernel: work items of the prefix; CTAs that share a row tile's keys
     int own_items, own_ctas;         // the same for the own tokens (0: the streaming kernel has them)
+    int stream_tile;             // query rows of a streaming CTA: 8 or 16
     float scale_log2;
     bool fp8;
     unsigned long long wait_limit;
@@ -96,6 +97,7 @@ struct PagedPlan {
     int prefix_items = 0, prefix_ctas = 0;   // tile kernel (see PagedParams)
     int own_items = 0, own_ctas = 0;
     bool prefix_stream = false;  // the streaming kernel has the prefix
+    int stream_tile = 8;         // query rows of a streaming CTA
     bool direct = false;         // one part in all: the kernel writes o and lse itself
     size_t part_o_bytes = 0, bytes = 0;
 };

@@ -65,16 +65,23 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     const long long rows = static_cast<long long>(Nq) * (H / H_kv);      // of one sequence and key/value head
     const long long own = static_cast<long long>(max_pages) * page_size;
     const int bn = d == 256 ? 64 : 128;
+    const long long all = B * rows;                                      // the prefix's rows of a key/value head
+    const bool own_stream = rows <= stream_rows(d);
+    plan.prefix_stream = prefix_len > 0 && all <= stream_rows(d);
+    // (one launch for both, so one kind of CTA)
+    plan.stream_tile = (own_stream ? rows : 0) > 8 || (plan.prefix_stream && all > 8) ? 16 : 8;
     // Streaming kernel.  A CTA's time is its keys plus a fixed cost (page table,
     // first loads, join) worth about 300; beyond one wave CTAs replace one
-    // another as they finish, and half a CTA's time is lost at the end.
-    const double slots = kPlanSms * (d == 64 ? 4.0 : d == 128 ? 3.0 : 2.0);
+    // another as they finish, half a CTA's time is lost at the end, and sequences
+    // are seldom all as long as their tables (16 x 32768 tokens, 8 heads of 128,
+    // e4m3: 121 us in 16 parts against 133 in 3, which fit one wave).
+    const double slots = kPlanSms * (d == 64 ? 4.0 : d == 128 || plan.stream_tile == 8 ? 3.0 : 2.0);
     const auto stream_parts = [&](long long keys, long long units) {
         int best = 1;
         double best_cost = -1.0;
         for (int s = 1; s <= kMaxParts && (s == 1 || s * static_cast<long long>(kOwnChunk) < keys + kOwnChunk); ++s) {
             const double waves = static_cast<double>(units) * s / slots, cta = static_cast<double>(up(keys, s)) + kStreamFixed;
-            const double cost = waves <= 1.0 ? cta : (waves + 0.5) * cta;
+            const double cost = waves <= 1.0 ? cta : (0.8 * waves + 0.5) * cta;
             if (best_cost < 0.0 || cost < best_cost) {
                 best = s;
                 best_cost = cost;
@@ -85,28 +92,26 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     // Steps of a CTA over `keys`: two streams halve the tiles of a single row tile.
     const auto steps_of = [&](long long keys, long long tiles) { return up(keys, bn * (d != 256 && tiles == 1 ? 2 : 1)); };
     double streaming = 0.0;                                              // SM-microseconds
-    if (rows > stream_rows(d)) {
+    if (!own_stream) {
         const long long tiles = up(rows, 128), groups = d == 256 ? tiles : up(tiles, 2);
         plan.own_ctas = tile_ctas(d, B * static_cast<long long>(H_kv) * groups, steps_of(own, tiles), 0.0);
         plan.own_items = static_cast<int>(B * static_cast<long long>(H_kv) * groups * plan.own_ctas);
         plan.own_parts = plan.own_ctas;
     } else {
-        const long long units = B * static_cast<long long>(H_kv) * up(rows, 16);
+        const long long units = B * static_cast<long long>(H_kv) * up(rows, plan.stream_tile);
         plan.own_parts = stream_parts(own, units);
         // (sequences fill three quarters of their tables, say; a key of one head
         // takes an SM 0.08 d nanoseconds)
         streaming = 0.75 * static_cast<double>(units) * static_cast<double>(own) * 0.08e-3 * d;
     }
     if (prefix_len > 0) {
-        const long long all = B * rows;
-        if (all > stream_rows(d)) {
+        if (!plan.prefix_stream) {
             const long long tiles = up(all, 128), groups = d == 256 ? tiles : up(tiles, 2);
             plan.prefix_ctas = tile_ctas(d, H_kv * groups, steps_of(prefix_len, tiles), streaming);
             plan.prefix_items = static_cast<int>(H_kv * groups * plan.prefix_ctas);
             plan.prefix_parts = plan.prefix_ctas;
         } else {
-            plan.prefix_stream = true;
-            plan.prefix_parts = stream_parts(prefix_len, H_kv * up(all, 16));
+            plan.prefix_parts = stream_parts(prefix_len, H_kv * up(all, plan.stream_tile));
         }
     }
     const int parts = plan.prefix_parts + plan.own_parts;

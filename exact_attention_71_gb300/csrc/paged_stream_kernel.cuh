@@ -6,31 +6,36 @@
 //
 // taken in one pass over the keys with a running m, l and O.
 //
-// A CTA serves 16 query rows of one key/value head (the group's heads of one
-// sequence, or rows of several sequences over the prefix they share) and one
+// A CTA serves 8 or 16 query rows of one key/value head (the group's heads of
+// one sequence, or rows of several sequences over the prefix they share) and one
 // key range; its four warps take the range's 16-key steps in turn, each with
 // its own m, l and O, joined once at the end.  Every key row is read once per
-// CTA, so the bound is the cache's bytes: at 16 rows a step does 16 FLOP per
-// byte of K and V (bf16), a twentieth of what the tensor cores could do per
+// CTA, so the bound is the cache's bytes: at 8 rows a step does 8 FLOP per
+// byte of K and V (bf16), a thirtieth of what the tensor cores could do per
 // byte of HBM bandwidth.  The products therefore use the warp-level m16n8k16
-// MMA with operands in registers: tcgen05 would leave 112 of its 128 tile rows
+// MMA with operands in registers: tcgen05 would leave 120 of its 128 tile rows
 // empty and need the tile to be assembled in shared memory first.
+//
+// The keys and the value columns are the 16 rows of the products, the queries
+// the 8 columns: S^T = K Q^T, O^T = V^T P^T.  (The other way round 4 query rows
+// of a group would fill a quarter of 16 and every product cost twice as much.)
 //
 // Way in: 16 rows of one head of one page are contiguous, so a warp's step is a
 // few TMA boxes of 16 rows (bf16: 64 columns, e4m3: up to 128), written with the
 // 128-byte swizzle (64 for 64-byte rows) into the warp's own ring and awaited on
 // the warp's own barriers: nothing crosses warps, no thread computes addresses.
-// (A version that copied 16 bytes a thread with cp.async moved 1.5 times the
-// bytes through the L2 and kept the load/store pipe busy: 31 us against ...)
+// (Copying 16 bytes a thread with cp.async moved 1.5 times the bytes through the
+// L2 and kept the load/store pipe busy: one sequence of 16384 tokens, 16 heads of
+// 128, bf16, took 36 us instead of 27.)
 // The MMA's k index may be permuted freely (both operands alike), and so may O's
 // columns and the keys, so each thread takes whole 16-byte chunks from the rows
-// that its B fragments need, chosen so that the 8 threads of a shared-memory
-// phase meet 8 different chunk columns of the swizzle:
-//   S = Q K^T   thread (g, t) = (lane / 4, lane % 4) reads key rows pi(g) and
-//               8 + pi(g), 16-byte chunks 4c + t;  pi(g) = g / 2 + 4 (g % 2)
-//   O += P V    value rows t, t + 4, t + 8, t + 12 (the keys pi(2t), pi(2t + 1),
-//               ..), chunks 8c + pi(g); pairs of rows are interleaved by byte
-//               permutes
+// that its fragments need, chosen so that the 8 threads of a shared-memory phase
+// meet 8 different chunk columns of the swizzle:
+//   S^T = K Q^T      thread (g, t) = (lane / 4, lane % 4) reads key rows pi(g) and
+//                    8 + pi(g), 16-byte chunks 4c + t;  pi(g) = g / 2 + 4 (g % 2)
+//   O^T += V^T P^T   value rows t, t + 4, t + 8, t + 12 (the keys pi(2t), pi(2t + 1),
+//                    ..), chunks 8c + pi(g); pairs of rows are interleaved by byte
+//                    permutes, and P^T is S^T's 8 x 8 blocks transposed
 #pragma once
 
 #include <cuda_bf16.h>
@@ -52,22 +57,28 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// D (16 x 8, fp32) += A (16 x 16, bf16) B (16 x 8, bf16).
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16 or bf16 operands.
+template <bool F16>
 __device__ __forceinline__ void mma_m16n8k16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if constexpr (F16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The same with fp16 operands.
-__device__ __forceinline__ void mma_m16n8k16_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                                 uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+// Transposes an 8 x 8 matrix of 16-bit elements (thread (g, t): row g, columns 2t
+// and 2t + 1).
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
 }
 
 // An e4m3 cache is multiplied in fp16.  e4m3 values are fp16 values, and one
@@ -154,10 +165,11 @@ __device__ __forceinline__ float vref_of(float vm) {
     return pow2f(max(-126, min(120, e - 4)));
 }
 
-template <int D_, bool FP8_>
+template <int D_, bool FP8_, int R_>
 struct StreamCfg {
     static constexpr int D = D_;
     static constexpr bool FP8 = FP8_;
+    static constexpr int R = R_, ROWS = 8 * R;                     // query rows: R tiles of 8
     static constexpr int ES = FP8 ? 1 : 2;
     static constexpr int ROW = D * ES;                             // bytes of a row
     static constexpr int SW = ROW >= 128 ? 128 : 64;               // swizzle span: bytes of a box row
@@ -172,21 +184,27 @@ struct StreamCfg {
     // 16-key blocks of a warp's step.  e4m3 steps are bound by instructions: two
     // blocks share the waits, the copies' issue and the running maximum.  bf16
     // steps are bound by bytes, and small steps keep more warps an SM.
-    static constexpr int H = FP8 ? 2 : 1;
+    static constexpr int H = FP8 && D <= 128 ? 2 : 1;
     static constexpr int STEP = 16 * H;
     static constexpr int TILE = 16 * ROW;                          // a block's K or V rows
     static constexpr int SCALES = FP8 ? 128 : 0;                   // its 16 K and 16 V scales
-    static constexpr int CTAS = D == 64 ? 4 : D == 128 ? 3 : FP8 ? 2 : 1;     // per SM
-    static constexpr int STAGES = D == 64 ? 3 : D == 128 ? 2 : FP8 ? 1 : 3;
+    static constexpr int CTAS = D == 64 ? 4 : D == 128 ? 3 : FP8 ? (R == 1 ? 3 : 2) : 1;     // per SM
+    static constexpr int STAGES = D == 64 ? 3 : D == 128 ? 2 : FP8 ? (R == 1 ? 2 : 3) : 3;
     static constexpr int STAGE_BYTES = H * 2 * TILE;               // (block, K / V, TILE)
     static constexpr int WARP_BYTES = STAGES * STAGE_BYTES;
     static constexpr int RING_BYTES = WARPS * WARP_BYTES;
-    static constexpr int JOIN_BYTES = WARPS * 16 * (D + 2) * 4;
+    static constexpr int JD = D + 4;                               // row stride of the join (banks)
+    static constexpr int JOIN_BYTES = WARPS * ROWS * (JD + 2) * 4;
     static constexpr int MAIN_BYTES = RING_BYTES > JOIN_BYTES ? RING_BYTES : JOIN_BYTES;
     static constexpr int SCALE_BYTES = WARPS * STAGES * H * SCALES;
-    static constexpr int Q_BYTES = FP8 ? 16 * D * 2 : 0;
+    static constexpr int Q_BYTES = FP8 ? ROWS * D * 2 : 0;
     static constexpr int SMEM_BYTES = 1024 + MAIN_BYTES + SCALE_BYTES + Q_BYTES + WARPS * STAGES * 8;
-    static constexpr int NT = D / 8;                               // O's column tiles
+    static constexpr int NT = D / 16;                              // O's column tiles
+    // Chains of products that S is summed in (d = 256, bf16: 137 us with two, 140 with
+    // one; at d = 128 their registers cost more: 16 rows 72 us with one, 77 with two).
+    static constexpr int CH = D == 256 && !FP8 ? 2 : 1;
+    // e4m3: Q's fragments are read from shared memory where registers are short.
+    static constexpr bool QREG = !FP8 || R * D <= 128;
     static_assert(CTAS * (SMEM_BYTES + 1024) <= 228 * 1024, "shared memory");
 };
 
@@ -257,7 +275,7 @@ template <class Cfg, bool DIRECT>
 __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     paged_stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         const __grid_constant__ PagedParams p, const unsigned prefix_blocks) {
-    constexpr int D = Cfg::D, KC = Cfg::KC, VC = Cfg::VC, NT = Cfg::NT, STAGES = Cfg::STAGES;
+    constexpr int D = Cfg::D, KC = Cfg::KC, VC = Cfg::VC, NT = Cfg::NT, STAGES = Cfg::STAGES, R = Cfg::R;
     constexpr bool FP8 = Cfg::FP8;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -265,15 +283,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     // Permutations of the swizzled layout (see above); 64-byte rows need none.
     constexpr bool PI = Cfg::SW == 128;
-    const int pig = PI ? (g >> 1) | ((g & 1) << 2) : g;            // K row, V chunk
-    const int ka = PI ? t : 2 * t, kb = PI ? t + 4 : 2 * t + 1;    // keys of S columns 2t, 2t + 1
+    const int pig = PI ? (g >> 1) | ((g & 1) << 2) : g;            // K row (key of S^T row g), V chunk
+    const int ka = PI ? t : 2 * t, kb = PI ? t + 4 : 2 * t + 1;    // keys of P^T rows 2t, 2t + 1
 
     launch_dependents();
     unsigned x0 = blockIdx.x;
     const bool prefix = !DIRECT && x0 < prefix_blocks;
     if (!prefix) x0 -= prefix_blocks;
     const int rows = (prefix ? p.B : 1) * p.Nq * p.G;
-    const unsigned tiles = (rows + 15) / 16;
+    const unsigned tiles = (rows + Cfg::ROWS - 1) / Cfg::ROWS;
     const int parts = prefix ? p.prefix_parts : p.own_parts;
     // Row tiles and heads of the same pages run next to one another.
     const int tile = x0 % tiles;
@@ -362,57 +380,58 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 
     // Query row r of the tile: its index in q and o, and the keys it sees.
     const int per = p.Nq * p.G;
-    const int live = min(16, rows - tile * 16);            // rows of this tile
+    const int live = min(Cfg::ROWS, rows - tile * Cfg::ROWS);            // rows of this tile
     auto row_of = [&](int r, long long& out, int& lse_at) -> int {
-        const int x = tile * 16 + r;
+        const int x = tile * Cfg::ROWS + r;
         const int b = prefix ? x / per : seq, i = (prefix ? x % per : x) / p.G, h = kvh * p.G + x % p.G;
         out = (static_cast<long long>(b) * p.Nq + i) * p.H + h;
         lse_at = (b * p.H + h) * p.Nq + i;
         return i;
     };
-    int limit[2];                  // keys that rows g and g + 8 see
-    float to_log2[2];              // raw score -> log2 units
-    uint32_t qa[2][FP8 ? 1 : D / 8];
-    uint4* sq = reinterpret_cast<uint4*>(smem + Cfg::MAIN_BYTES + Cfg::SCALE_BYTES) + lane;
+    int limit[R][2];               // keys that rows 8n + 2t and 8n + 2t + 1 see
+    float to_log2[R][2];           // raw score -> log2 units
+    uint32_t qb[R][Cfg::QREG ? D / 8 : 1];         // row 8n + g: chunk c of the k permutation, elements [c * 4E + t * E, + E)
+    uint4* sq = reinterpret_cast<uint4*>(smem + Cfg::MAIN_BYTES + Cfg::SCALE_BYTES);
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
+    auto row_at = [&](int r) -> const uint4* {
+        if (r >= live) return nullptr;
+        long long out;
+        int at;
+        row_of(r, out, at);
+        return reinterpret_cast<const uint4*>(q + out * D);
+    };
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        limit[x] = 0;
-        to_log2[x] = p.scale_log2;
-        const uint4* src = nullptr;
-        if (g + 8 * x < live) {
+    for (int n = 0; n < R; ++n) {
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            const int r = 8 * n + 2 * t + z;
             long long out;
-            int at;
-            const int i = row_of(g + 8 * x, out, at);
-            limit[x] = min(prefix || !p.causal ? len : max(0, len - p.Nq + 1 + i), k1);
-            src = reinterpret_cast<const uint4*>(q + out * D);
+            int at, i = 0;
+            if (r < live) i = row_of(r, out, at);
+            limit[n][z] = r >= live ? 0 : min(prefix || !p.causal ? len : max(0, len - p.Nq + 1 + i), k1);
+            to_log2[n][z] = p.scale_log2;
         }
         if constexpr (!FP8) {
-            // Fragments: chunk c of the k permutation, elements [c * 4E + t * E, + E).
+            const uint4* src = row_at(8 * n + g);
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
                 const uint4 v = src ? __ldg(src + c * 4 + t) : make_uint4(0, 0, 0, 0);
-                qa[x][c * 4] = v.x;
-                qa[x][c * 4 + 1] = v.y;
-                qa[x][c * 4 + 2] = v.z;
-                qa[x][c * 4 + 3] = v.w;
+                qb[n][c * 4] = v.x;
+                qb[n][c * 4 + 1] = v.y;
+                qb[n][c * 4 + 2] = v.z;
+                qb[n][c * 4 + 3] = v.w;
             }
         }
     }
     if constexpr (FP8) {
-        // To fp16, once per CTA: warp w takes rows 4w .. 4w + 3, eight lanes a
-        // row, and writes them as fragments (chunk half, row half, lane).
-        __shared__ float row_log2[16];
-        const int r = warp * 4 + (lane >> 3);
+        // To fp16, once per CTA: a warp takes 2R rows, eight lanes a row, and
+        // writes them as fragments (chunk half, row tile, lane).
+        __shared__ float row_log2[Cfg::ROWS];
+        const int r = warp * (2 * R) + (lane >> 3);
+        const bool mine = (lane >> 3) < 2 * R;
         uint4 v[D / 64];
         uint32_t top = 0;
-        const uint4* src = nullptr;
-        if (r < live) {
-            long long out;
-            int at;
-            row_of(r, out, at);
-            src = reinterpret_cast<const uint4*>(q + out * D);
-        }
+        const uint4* src = mine ? row_at(r) : nullptr;
 #pragma unroll
         for (int y = 0; y < D / 64; ++y) {
             v[y] = src ? __ldg(src + y * 8 + (lane & 7)) : make_uint4(0, 0, 0, 0);
@@ -421,27 +440,49 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 #pragma unroll
         for (int y = 1; y < 8; y <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, y));
         const int shift = q_shift(top, 14);
-        if ((lane & 7) == 0) row_log2[r] = p.scale_log2 * pow2f(-shift);
+        if (mine) {
+            // (not 0: -inf, the masked score, stays -inf when multiplied)
+            if ((lane & 7) == 0) row_log2[r] = fmaxf(p.scale_log2 * pow2f(-shift), 0x1p-126f);
 #pragma unroll
-        for (int y = 0; y < D / 64; ++y) {
-            const int i8 = y * 8 + (lane & 7);             // eight elements: chunk i8 / 8, thread (i8 / 2) % 4, half i8 % 2
-            const int at = (i8 >> 3) * 2 + (i8 & 1);
-            (sq - lane)[(at * 2 + (r >> 3)) * 32 + (r & 7) * 4 + ((i8 >> 1) & 3)] = q_to_f16(v[y], pow2f(shift));
+            for (int y = 0; y < D / 64; ++y) {
+                const int i8 = y * 8 + (lane & 7);         // eight elements: chunk i8 / 8, thread (i8 / 2) % 4, half i8 % 2
+                const int at = (i8 >> 3) * 2 + (i8 & 1);
+                sq[(at * R + (r >> 3)) * 32 + (r & 7) * 4 + ((i8 >> 1) & 3)] = q_to_f16(v[y], pow2f(shift));
+            }
         }
         __syncthreads();
-        to_log2[0] = row_log2[g];
-        to_log2[1] = row_log2[g + 8];
+#pragma unroll
+        for (int n = 0; n < R; ++n) {
+            to_log2[n][0] = row_log2[8 * n + 2 * t];
+            to_log2[n][1] = row_log2[8 * n + 2 * t + 1];
+            if constexpr (Cfg::QREG) {
+#pragma unroll
+                for (int c = 0; c < 2 * KC; ++c) {
+                    const uint4 v = sq[(c * R + n) * 32 + lane];
+                    qb[n][c * 4] = v.x;
+                    qb[n][c * 4 + 1] = v.y;
+                    qb[n][c * 4 + 2] = v.z;
+                    qb[n][c * 4 + 3] = v.w;
+                }
+            }
+        }
     }
     // From this key on some row of the tile may not see what another does.
     int diag = len;
-    if (!prefix && p.causal) diag = max(0, len - p.Nq + 1 + (tile * 16) / p.G);
+    if (!prefix && p.causal) diag = max(0, len - p.Nq + 1 + (tile * Cfg::ROWS) / p.G);
     // Steps that reach it (or the range's end) are masked key by key.
     const int plain_end = min(diag, k1);
 
-    float o[NT][4];
+    // O^T: o[j][n][z] and o[j][n][2 + z] are the elements 2j and 2j + 1 (of VE a
+    // chunk) of query row 8n + 2t + z.
+    float o[NT][R][4], m[R][2], l[R][2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    for (int n = 0; n < R; ++n) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) o[j][n][0] = o[j][n][1] = o[j][n][2] = o[j][n][3] = 0.0f;
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.0f;
+    }
     float vref = FP8 ? 0.0f : 1.0f;
 
     // Shared-memory offsets of this thread's chunks (SW = 128: the chunk's column
@@ -465,89 +506,118 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         if (!(ok = stream_wait(full + stage, parity, p.wait_limit, p.status, SITE_STREAM_FULL))) break;
         uint8_t* st = ring + stage * Cfg::STAGE_BYTES;
 
-        // ---------------------------------------------------------- S = Q K^T
-        // s[x][0..1]: row g, keys 8 x + ka, 8 x + kb; s[x][2..3]: row g + 8.
-        float s[2 * H][4];
+        // -------------------------------------------------------- S^T = K Q^T
+        // s[h][n][z]: key 16h + pi(g), query row 8n + 2t + z; s[h][n][2 + z]: key 8 on.
+        float s[H][R][4], s1[Cfg::CH == 2 ? H : 1][R][4];
 #pragma unroll
-        for (int x = 0; x < 2 * H; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.0f;
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int n = 0; n < R; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[h][n][i] = 0.0f;
+                    if constexpr (Cfg::CH == 2) s1[h][n][i] = 0.0f;
+                }
 #pragma unroll
         for (int c = 0; c < KC; ++c) {
             const uint32_t col = Cfg::SW == 128 ? koff[c & 1] + (c >> 1) * (16 * Cfg::SW) : koff[0];
-            if constexpr (FP8) {
-                const uint4 q0 = sq[(c * 4) * 32], q1 = sq[(c * 4 + 1) * 32];          // rows g, g + 8
-                const uint4 q2 = sq[(c * 4 + 2) * 32], q3 = sq[(c * 4 + 3) * 32];
+            constexpr int W = FP8 ? 8 : 4;                 // Q's words of a chunk
+            uint32_t qw[R][W];
 #pragma unroll
-                for (int x = 0; x < 2 * H; ++x) {
-                    const uint4 kk = *reinterpret_cast<const uint4*>(st + (x >> 1) * 2 * Cfg::TILE + (x & 1) * 8 * Cfg::SW + col);
-                    mma_m16n8k16_f16(s[x], q0.x, q1.x, q0.y, q1.y, f16x2_of_lo(kk.x), f16x2_of_hi(kk.x));
-                    mma_m16n8k16_f16(s[x], q0.z, q1.z, q0.w, q1.w, f16x2_of_lo(kk.y), f16x2_of_hi(kk.y));
-                    mma_m16n8k16_f16(s[x], q2.x, q3.x, q2.y, q3.y, f16x2_of_lo(kk.z), f16x2_of_hi(kk.z));
-                    mma_m16n8k16_f16(s[x], q2.z, q3.z, q2.w, q3.w, f16x2_of_lo(kk.w), f16x2_of_hi(kk.w));
+            for (int n = 0; n < R; ++n)
+#pragma unroll
+                for (int y = 0; y < W / 4; ++y) {
+                    if constexpr (Cfg::QREG) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) qw[n][4 * y + i] = qb[n][c * W + 4 * y + i];
+                    } else {
+                        const uint4 v = sq[((c * 2 + y) * R + n) * 32 + lane];
+                        qw[n][4 * y] = v.x;
+                        qw[n][4 * y + 1] = v.y;
+                        qw[n][4 * y + 2] = v.z;
+                        qw[n][4 * y + 3] = v.w;
+                    }
                 }
-            } else {
 #pragma unroll
-                for (int x = 0; x < 2 * H; ++x) {
-                    const uint4 kk = *reinterpret_cast<const uint4*>(st + (x >> 1) * 2 * Cfg::TILE + (x & 1) * 8 * Cfg::SW + col);
-                    const int at = c * 4;
-                    mma_m16n8k16(s[x], qa[0][at], qa[1][at], qa[0][at + 1], qa[1][at + 1], kk.x, kk.y);
-                    mma_m16n8k16(s[x], qa[0][at + 2], qa[1][at + 2], qa[0][at + 3], qa[1][at + 3], kk.z, kk.w);
+            for (int h = 0; h < H; ++h) {
+                const uint8_t* at = st + h * 2 * Cfg::TILE + col;
+                const uint4 ka4 = *reinterpret_cast<const uint4*>(at);
+                const uint4 kb4 = *reinterpret_cast<const uint4*>(at + 8 * Cfg::SW);
+                const uint32_t a[4] = {ka4.x, ka4.y, ka4.z, ka4.w}, b[4] = {kb4.x, kb4.y, kb4.z, kb4.w};
+#pragma unroll
+                for (int y = 0; y < W / 2; ++y) {
+#pragma unroll
+                    for (int n = 0; n < R; ++n) {
+                        float* d = Cfg::CH == 2 && (y & 1) ? s1[Cfg::CH == 2 ? h : 0][n] : s[h][n];
+                        if constexpr (FP8)
+                            mma_m16n8k16<true>(d, f16x2_of_lo(a[y]), f16x2_of_lo(b[y]), f16x2_of_hi(a[y]), f16x2_of_hi(b[y]),
+                                               qw[n][2 * y], qw[n][2 * y + 1]);
+                        else
+                            mma_m16n8k16<false>(d, a[2 * y], b[2 * y], a[2 * y + 1], b[2 * y + 1], qw[n][2 * y],
+                                                qw[n][2 * y + 1]);
+                    }
                 }
             }
         }
         const uint32_t miss = (gone >> (H * (round & 7))) & ((1u << H) - 1u);
         const bool special = miss != 0 || key0 + STEP > plain_end;
-        float2 vscale[2 * H];
-        const float* sc = scales + stage * H * 32;
+        float vscale[H][2];
 #pragma unroll
-        for (int x = 0; x < 2 * H; ++x) {
-            float2 mul = make_float2(1.0f, 1.0f);
+        for (int h = 0; h < H; ++h) {
+            float mul[2] = {1.0f, 1.0f};
             if constexpr (FP8) {
-                const float* at = sc + (x >> 1) * 32 + (x & 1) * 8;
-                mul = make_float2(at[ka], at[kb]);
-                vscale[x] = make_float2(at[16 + ka], at[16 + kb]);
+                const float* at = scales + (stage * H + h) * 32 + pig;
+                mul[0] = at[0];
+                mul[1] = at[8];
+                vscale[h][0] = at[16];
+                vscale[h][1] = at[24];
             }
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                s[x][2 * r] *= mul.x * to_log2[r];
-                s[x][2 * r + 1] *= mul.y * to_log2[r];
-            }
+            for (int n = 0; n < R; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (Cfg::CH == 2) s[h][n][i] += s1[h][n][i];
+                    if constexpr (FP8) s[h][n][i] *= mul[i >> 1];
+                }
         }
         if (special) {
             // A masked score is -inf whatever was read for it.
 #pragma unroll
-            for (int x = 0; x < 2 * H; ++x) {
-                const bool skip = (miss >> (x >> 1)) & 1u;
-                const int key = key0 + x * 8;
+            for (int h = 0; h < H; ++h) {
+                const bool skip = (miss >> h) & 1u;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int lim = skip ? 0 : limit[r];
-                    if (key + ka >= lim) s[x][2 * r] = -INFINITY;
-                    if (key + kb >= lim) s[x][2 * r + 1] = -INFINITY;
-                }
-                if constexpr (FP8) {
-                    const int lim = skip ? 0 : k1;             // scales of rows that are not there
-                    if (key + ka >= lim) vscale[x].x = 0.0f;
-                    if (key + kb >= lim) vscale[x].y = 0.0f;
+                for (int x = 0; x < 2; ++x) {
+                    const int key = key0 + 16 * h + 8 * x + pig;
+#pragma unroll
+                    for (int n = 0; n < R; ++n)
+#pragma unroll
+                        for (int z = 0; z < 2; ++z)
+                            if (skip || key >= limit[n][z]) s[h][n][2 * x + z] = -INFINITY;
+                    // (scales of rows that are not there)
+                    if (FP8 && (skip || key >= k1)) vscale[h][x] = 0.0f;
                 }
             }
         }
         // ------------------------------------------------------ running maximum
         // A row's reference moves only when a score of the row exceeds it by
-        // more than 8 (log2 units), so that the quad's shuffles and O's
-        // rescaling are rare; O and l share the reference, so the result does
-        // not depend on it.
-        float mx[2] = {fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])};
+        // more than 8 (log2 units), so that the shuffles and O's rescaling are
+        // rare; O and l share the reference, so the result does not depend on it.
+        float mx[R][2];
+        bool move = false;
 #pragma unroll
-        for (int x = 1; x < 2 * H; ++x) {
-            mx[0] = fmax3(mx[0], s[x][0], s[x][1]);
-            mx[1] = fmax3(mx[1], s[x][2], s[x][3]);
-        }
-        bool move = mx[0] > m[0] + 8.0f || mx[1] > m[1] + 8.0f;
+        for (int n = 0; n < R; ++n)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                mx[n][z] = fmaxf(s[0][n][z], s[0][n][2 + z]);
+#pragma unroll
+                for (int h = 1; h < H; ++h) mx[n][z] = fmax3(mx[n][z], s[h][n][z], s[h][n][2 + z]);
+                mx[n][z] *= to_log2[n][z];
+                move = move || mx[n][z] > m[n][z] + 8.0f;
+            }
         float vm = 0.0f;
         if constexpr (FP8) {
-            vm = fmaxf(vscale[0].x, vscale[0].y);
 #pragma unroll
-            for (int x = 1; x < 2 * H; ++x) vm = fmax3(vm, vscale[x].x, vscale[x].y);
+            for (int h = 0; h < H; ++h) vm = fmax3(vm, vscale[h][0], vscale[h][1]);
             move = move || vm > 64.0f * vref;
         }
         if (__any_sync(0xffffffffu, move)) {
@@ -562,60 +632,58 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 }
             }
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-                mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-                // (per row: a row's result does not depend on its neighbours)
-                const float mn = mx[r] > m[r] + 8.0f ? mx[r] : m[r];
-                const float a = mn == m[r] ? 1.0f : ex2_approx(m[r] - mn);
-                m[r] = mn;
-                l[r] *= a;
-                const float ao = FP8 ? a * vfall : a;
+            for (int n = 0; n < R; ++n)
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    o[j][2 * r] *= ao;
-                    o[j][2 * r + 1] *= ao;
+                for (int z = 0; z < 2; ++z) {
+                    float x = mx[n][z];
+#pragma unroll
+                    for (int y = 4; y < 32; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
+                    // (per row: a row's result does not depend on its neighbours)
+                    const float was = m[n][z], mn = x > was + 8.0f ? x : was;
+                    const float a = mn == was ? 1.0f : ex2_approx(was - mn);
+                    m[n][z] = mn;
+                    l[n][z] *= a;
+                    const float ao = FP8 ? a * vfall : a;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        o[j][n][z] *= ao;
+                        o[j][n][2 + z] *= ao;
+                    }
                 }
-            }
         }
-        const float n0 = m[0] == -INFINITY ? 0.0f : m[0], n1 = m[1] == -INFINITY ? 0.0f : m[1];
         const float iv = FP8 ? (vref == 0.0f ? 0.0f : 1.0f / vref) : 1.0f;         // a power of two
-        uint32_t pa[H][4];             // P as the A operand of each block
+        uint32_t pb[H][R][2];          // P^T as the B operand of each block
 #pragma unroll
-        for (int x = 0; x < 2 * H; ++x) {
-            s[x][0] = ex2_approx(s[x][0] - n0);
-            s[x][1] = ex2_approx(s[x][1] - n0);
-            s[x][2] = ex2_approx(s[x][2] - n1);
-            s[x][3] = ex2_approx(s[x][3] - n1);
-            l[0] += s[x][0] + s[x][1];
-            l[1] += s[x][2] + s[x][3];
-            if constexpr (FP8) {
-                // V's row scale rides on P; l sums the plain probabilities.  A
-                // weight of 0 stays 0 beside a NaN scale: a row that does not
-                // see the key must not notice it.
-                const float va = vscale[x].x * iv, vb = vscale[x].y * iv;
-                if (special) {
-                    s[x][0] = s[x][0] == 0.0f ? 0.0f : s[x][0] * va;
-                    s[x][1] = s[x][1] == 0.0f ? 0.0f : s[x][1] * vb;
-                    s[x][2] = s[x][2] == 0.0f ? 0.0f : s[x][2] * va;
-                    s[x][3] = s[x][3] == 0.0f ? 0.0f : s[x][3] * vb;
-                } else {
-                    s[x][0] *= va;
-                    s[x][1] *= vb;
-                    s[x][2] *= va;
-                    s[x][3] *= vb;
+        for (int n = 0; n < R; ++n) {
+            const float n0 = m[n][0] == -INFINITY ? 0.0f : -m[n][0], n1 = m[n][1] == -INFINITY ? 0.0f : -m[n][1];
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float e0 = ex2_approx(fmaf(s[h][n][2 * x], to_log2[n][0], n0));
+                    float e1 = ex2_approx(fmaf(s[h][n][2 * x + 1], to_log2[n][1], n1));
+                    l[n][0] += e0;
+                    l[n][1] += e1;
+                    if constexpr (FP8) {
+                        // V's row scale rides on P; l sums the plain weights.  A
+                        // weight of 0 stays 0 beside a NaN scale: a row that does
+                        // not see the key must not notice it.
+                        const float vs = vscale[h][x] * iv;
+                        if (special) {
+                            e0 = e0 == 0.0f ? 0.0f : e0 * vs;
+                            e1 = e1 == 0.0f ? 0.0f : e1 * vs;
+                        } else {
+                            e0 *= vs;
+                            e1 *= vs;
+                        }
+                    }
+                    // P is rounded for the product: to fp16 (see above), or to
+                    // bf16 (2^-8 per weight, as in the dense forward); l keeps
+                    // the unrounded values.
+                    pb[h][n][x] = transpose_8x8(FP8 ? pack_f16x2(e0, e1) : pack_bf16x2(e0, e1));
                 }
-                pa[x >> 1][(x & 1) * 2] = pack_f16x2(s[x][0], s[x][1]);
-                pa[x >> 1][(x & 1) * 2 + 1] = pack_f16x2(s[x][2], s[x][3]);
-            } else {
-                // P is rounded to bf16 for the product (relative 2^-8 at most
-                // per weight, as the dense forward does; e4m3 cache: fp16, see
-                // above); l keeps the unrounded values.
-                pa[x >> 1][(x & 1) * 2] = pack_bf16x2(s[x][0], s[x][1]);
-                pa[x >> 1][(x & 1) * 2 + 1] = pack_bf16x2(s[x][2], s[x][3]);
-            }
         }
-        // ---------------------------------------------------------- O += P V
+        // ---------------------------------------------------------- O^T += V^T P^T
         if (special) {
             // 0 * NaN is NaN: stale rows become 0, and where rows of the tile see
             // different keys a non-finite value is taken out of the product and
@@ -625,16 +693,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 const int at = key0 + h * 16;
                 const uint32_t hit = fix_v_step<Cfg>(st + (2 * h + 1) * Cfg::TILE, (miss >> h) & 1u ? 0 : k1 - at, diag - at, lane);
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int n = min(max(limit[r] - at, 0), 16);
-                    if (hit & ((1u << n) - 1u)) l[r] = __uint_as_float(0x7fc00000u);
-                }
+                for (int n = 0; n < R; ++n)
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const int seen = min(max(limit[n][z] - at, 0), 16);
+                        if (hit & ((1u << seen) - 1u)) l[n][z] = __uint_as_float(0x7fc00000u);
+                    }
             }
         }
 #pragma unroll
         for (int h = 0; h < H; ++h) {
             const uint8_t* sv = st + (2 * h + 1) * Cfg::TILE;
-            const uint32_t a0 = pa[h][0], a1 = pa[h][1], a2 = pa[h][2], a3 = pa[h][3];
 #pragma unroll
             for (int c = 0; c < VC; ++c) {
                 uint32_t w[4][Cfg::VB / 4];
@@ -656,20 +725,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 }
 #pragma unroll
                 for (int y = 0; y < Cfg::VB / 4; ++y) {
-                    float(*oo)[4] = &o[c * Cfg::VE + y * (4 / Cfg::ES)];
+                    auto* oo = &o[(c * Cfg::VE + y * (4 / Cfg::ES)) / 2];
                     if constexpr (FP8) {
-                        // codes of two rows, interleaved: columns 0, 1 and 2, 3
+                        // codes of two rows, interleaved: elements 0, 1 and 2, 3
                         const uint32_t ab01 = __byte_perm(w[0][y], w[1][y], 0x5140), ab23 = __byte_perm(w[0][y], w[1][y], 0x7362);
                         const uint32_t cd01 = __byte_perm(w[2][y], w[3][y], 0x5140), cd23 = __byte_perm(w[2][y], w[3][y], 0x7362);
-                        mma_m16n8k16_f16(oo[0], a0, a1, a2, a3, f16x2_of_lo(ab01), f16x2_of_lo(cd01));
-                        mma_m16n8k16_f16(oo[1], a0, a1, a2, a3, f16x2_of_hi(ab01), f16x2_of_hi(cd01));
-                        mma_m16n8k16_f16(oo[2], a0, a1, a2, a3, f16x2_of_lo(ab23), f16x2_of_lo(cd23));
-                        mma_m16n8k16_f16(oo[3], a0, a1, a2, a3, f16x2_of_hi(ab23), f16x2_of_hi(cd23));
+#pragma unroll
+                        for (int n = 0; n < R; ++n) {
+                            mma_m16n8k16<true>(oo[0][n], f16x2_of_lo(ab01), f16x2_of_hi(ab01), f16x2_of_lo(cd01),
+                                               f16x2_of_hi(cd01), pb[h][n][0], pb[h][n][1]);
+                            mma_m16n8k16<true>(oo[1][n], f16x2_of_lo(ab23), f16x2_of_hi(ab23), f16x2_of_lo(cd23),
+                                               f16x2_of_hi(cd23), pb[h][n][0], pb[h][n][1]);
+                        }
                     } else {
-                        mma_m16n8k16(oo[0], a0, a1, a2, a3, __byte_perm(w[0][y], w[1][y], 0x5410),
-                                     __byte_perm(w[2][y], w[3][y], 0x5410));
-                        mma_m16n8k16(oo[1], a0, a1, a2, a3, __byte_perm(w[0][y], w[1][y], 0x7632),
-                                     __byte_perm(w[2][y], w[3][y], 0x7632));
+                        const uint32_t a0 = __byte_perm(w[0][y], w[1][y], 0x5410), a1 = __byte_perm(w[0][y], w[1][y], 0x7632);
+                        const uint32_t a2 = __byte_perm(w[2][y], w[3][y], 0x5410), a3 = __byte_perm(w[2][y], w[3][y], 0x7632);
+#pragma unroll
+                        for (int n = 0; n < R; ++n) mma_m16n8k16<false>(oo[0][n], a0, a1, a2, a3, pb[h][n][0], pb[h][n][1]);
                     }
                 }
             }
@@ -689,43 +761,38 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     }
 
     // ------------------------------------------------------------ join the warps
-    // o[c * VE + e][2r + z] is row g + 8r, column (8c + pi(2t + z)) * VE + e.
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-    }
-    if constexpr (FP8) {
+    for (int n = 0; n < R; ++n)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            o[j][0] *= vref;
-            o[j][1] *= vref;
-            o[j][2] *= vref;
-            o[j][3] *= vref;
+        for (int z = 0; z < 2; ++z) {
+#pragma unroll
+            for (int y = 4; y < 32; y <<= 1) l[n][z] += __shfl_xor_sync(0xffffffffu, l[n][z], y);
         }
-    }
     __syncthreads();                       // every warp is done with the ring
-    float* js = reinterpret_cast<float*>(smem);                        // (warp, 16, D)
-    float* jm = js + Cfg::WARPS * 16 * D;                              // (warp, 16)
-    float* jl = jm + Cfg::WARPS * 16;
+    constexpr int JD = Cfg::JD;
+    float* js = reinterpret_cast<float*>(smem);                        // (warp, ROWS, JD)
+    float* jm = js + Cfg::WARPS * Cfg::ROWS * JD;                      // (warp, ROWS)
+    float* jl = jm + Cfg::WARPS * Cfg::ROWS;
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        if (g + 8 * r >= live) continue;
-        float* dst = js + (warp * 16 + g + 8 * r) * D;
+    for (int n = 0; n < R; ++n)
 #pragma unroll
-        for (int c = 0; c < VC; ++c)
+        for (int z = 0; z < 2; ++z) {
+            const int r = 8 * n + 2 * t + z;
+            if (r >= live) continue;
+            float* dst = js + (warp * Cfg::ROWS + r) * JD;
 #pragma unroll
-            for (int z = 0; z < 2; ++z)
+            for (int c = 0; c < VC; ++c)
 #pragma unroll
-                for (int e = 0; e < Cfg::VE; e += 4)
-                    *reinterpret_cast<float4*>(dst + (c * 8 + (z ? kb : ka)) * Cfg::VE + e) =
-                        make_float4(o[c * Cfg::VE + e][2 * r + z], o[c * Cfg::VE + e + 1][2 * r + z],
-                                    o[c * Cfg::VE + e + 2][2 * r + z], o[c * Cfg::VE + e + 3][2 * r + z]);
-        if (t == 0) {
-            jm[warp * 16 + g + 8 * r] = m[r];
-            jl[warp * 16 + g + 8 * r] = l[r];
+                for (int e = 0; e < Cfg::VE; e += 4) {
+                    const int j = (c * Cfg::VE + e) / 2;
+                    *reinterpret_cast<float4*>(dst + (c * 8 + pig) * Cfg::VE + e) =
+                        make_float4(o[j][n][z] * vref, o[j][n][2 + z] * vref, o[j + 1][n][z] * vref, o[j + 1][n][2 + z] * vref);
+                }
+            if (g == 0) {
+                jm[warp * Cfg::ROWS + r] = m[n][z];
+                jl[warp * Cfg::ROWS + r] = l[n][z];
+            }
         }
-    }
     __syncthreads();
     // A thread takes 4 columns of a row at a time; D / 4 threads a row.
     for (int x = tid; x < live * (D / 4); x += Cfg::THREADS) {
@@ -735,15 +802,15 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         row_of(rr, out, lse_at);
         float mm = jm[rr];
 #pragma unroll
-        for (int w = 1; w < Cfg::WARPS; ++w) mm = fmaxf(mm, jm[w * 16 + rr]);
+        for (int w = 1; w < Cfg::WARPS; ++w) mm = fmaxf(mm, jm[w * Cfg::ROWS + rr]);
         const float ref = mm == -INFINITY ? 0.0f : mm;
         float ll = 0.0f;
         float4 acc = make_float4(0, 0, 0, 0);
 #pragma unroll
         for (int w = 0; w < Cfg::WARPS; ++w) {
-            const float a = ex2_approx(jm[w * 16 + rr] - ref);
-            const float4 v = *reinterpret_cast<const float4*>(js + (w * 16 + rr) * D + c4 * 4);
-            ll += a * jl[w * 16 + rr];
+            const float a = ex2_approx(jm[w * Cfg::ROWS + rr] - ref);
+            const float4 v = *reinterpret_cast<const float4*>(js + (w * Cfg::ROWS + rr) * JD + c4 * 4);
+            ll += a * jl[w * Cfg::ROWS + rr];
             acc.x += a * v.x;
             acc.y += a * v.y;
             acc.z += a * v.z;
