@@ -113,30 +113,29 @@ __device__ __forceinline__ int q_shift(uint32_t bits, int to) {
     return max(-126, min(126, 127 + to - max(e, 1)));
 }
 
+// Two fp16 -> two e4m3 codes, and back.
+__device__ __forceinline__ uint32_t pack_e4m3x2_f16(uint32_t x) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
+    return r;
+}
+
 // Eight bf16 times a power of two that brings them below 2^8 -> two e4m3 parts of
 // each, x = q1 + q2.  The first has the leading four bits of x's eight, the second
 // the rest: exact for |x| >= 2^-2 (2^-10 of the row's largest), and within 2^-10
-// below that, where e4m3 ends.  An infinity or a NaN becomes a NaN in q1.
-__device__ __forceinline__ void q_split(const uint4& v, float factor, uint32_t& a1, uint32_t& b1, uint32_t& a2,
-                                        uint32_t& b2) {
+// below that, where e4m3 ends (fp16 holds x and x - q1 exactly down to 2^-14).  A
+// factor of NaN makes all of them NaN.
+__device__ __forceinline__ void q_split(const uint4& v, float factor, uint2& q1, uint2& q2) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t a[4], b[4];
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-        float x[4];
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            x[2 * z] = __uint_as_float(w[2 * y + z] << 16) * factor;
-            x[2 * z + 1] = __uint_as_float(w[2 * y + z] & 0xffff0000u) * factor;
-        }
-#pragma unroll
-        for (int z = 0; z < 4; ++z)
-            if (!(fabsf(x[z]) < INFINITY)) x[z] = __uint_as_float(0x7fc00000u);
-        const uint32_t c = pack_e4m3x4(x[0], x[1], x[2], x[3]);
-        const float2 lo = f16x2_to_float2(f16x2_of_lo(c)), hi = f16x2_to_float2(f16x2_of_hi(c));
-        const uint32_t r = pack_e4m3x4(x[0] - lo.x, x[1] - lo.y, x[2] - hi.x, x[3] - hi.y);
-        (y ? b1 : a1) = c;
-        (y ? b2 : a2) = r;
+    for (int y = 0; y < 4; ++y) {
+        const uint32_t x = pack_f16x2(__uint_as_float(w[y] << 16) * factor, __uint_as_float(w[y] & 0xffff0000u) * factor);
+        a[y] = pack_e4m3x2_f16(x);
+        b[y] = pack_e4m3x2_f16(sub_f16x2(x, f16x2_of_lo(a[y])));
     }
+    q1 = make_uint2(a[0] | a[1] << 16, a[2] | a[3] << 16);
+    q2 = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
 }
 
 // Eight bf16 times a power of two -> eight fp16.

@@ -740,50 +740,60 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int j0 = t == 0 ? w.j0[0] : w.j0[1], part = w.part;
         const int limit = in ? row_limit(p, w, row) : w.len;   // (a row that is not there needs no mask)
         // A warp brings in its 32 query rows, swizzled, zero where there is none;
-        // in alt mode both streams use stream 0's tile.
+        // in alt mode both streams use stream 0's tile.  A lane has chunk qc of the
+        // rows q_row(x).
+        constexpr int LPR = D / 8 < 32 ? D / 8 : 32, RPI = 32 / LPR;   // lanes per row (16 bytes each), rows at a time
+        const int qc = lane % LPR;
+        auto q_row = [&](int x) { return (warp & 3) * 32 + x * RPI + lane / LPR; };
+        auto q_at = [&](int r) -> uint32_t { return (qc >> 3) * (BM * 128) + r * 128 + (((qc & 7) ^ (r & 7)) << 4); };
+        // (e4m3, d = 64: a row's two parts do not lie where its bf16 elements would)
+        uint8_t* const rows16 = FP8 && D == 64 ? sEpi + t * 16384 : sQ + t * Cfg::Q_BYTES;
         if (w.pair || t == 0) {
-            constexpr int LPR = D / 8 < 32 ? D / 8 : 32;           // lanes per row (16 bytes each)
-            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + (lane % LPR) * 8;
+            const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + qc * 8;
 #pragma unroll 8
             for (int x = 0; x < LPR; ++x) {
-                const int src = __shfl_sync(0xffffffffu, out, x * (32 / LPR) + lane / LPR);
-                const int rq = (warp & 3) * 32 + x * (32 / LPR) + lane / LPR, c = lane % LPR;
-                cp_async16(smem_u32(sQ) + t * Cfg::Q_BYTES + (c >> 3) * (BM * 128) + rq * 128 + (((c & 7) ^ (rq & 7)) << 4),
-                           q + static_cast<long long>(max(src, 0)) * D, src >= 0);
+                const int src = __shfl_sync(0xffffffffu, out, x * RPI + lane / LPR);
+                cp_async16(smem_u32(rows16) + q_at(q_row(x)), q + static_cast<long long>(max(src, 0)) * D, src >= 0);
             }
         }
         cp_async_commit();
         cp_async_wait<0>();
         if constexpr (FP8) {
-            // Into two e4m3 parts, one row a thread, over the bf16 rows (which all
-            // threads have read by then).
+            // Into two e4m3 parts, in place.  (A loop of few instructions: with a
+            // row a thread and everything unrolled, fetching the code took most of
+            // 21000 cycles.)
             if (w.pair || t == 0) {
-                const int rq = tid & 127;
                 uint8_t* tile = sQ + t * Cfg::Q_BYTES;
-                uint4 v[D / 8];
-                uint32_t top = 0;
-                __syncwarp();
+                constexpr int AT = 4;                              // row groups at a time (latency)
+#pragma unroll 1
+                for (int x = 0; x < LPR; x += AT) {
+                    uint4 v[AT];
+                    uint32_t top[AT];
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) {
-                    v[c] = *reinterpret_cast<const uint4*>(tile + (c >> 3) * (BM * 128) + rq * 128 + (((c & 7) ^ (rq & 7)) << 4));
-                    top = max(top, bf16x8_amax(v[c]));
-                }
-                named_barrier(2 + t, 128);
-                const int shift = q_shift(top, 7);
-                const float up = pow2f(shift);
+                    for (int i = 0; i < AT; ++i) {
+                        v[i] = *reinterpret_cast<const uint4*>(rows16 + q_at(q_row(x + i)));
+                        top[i] = bf16x8_amax(v[i]);
+                    }
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    uint4 q1, q2;
-                    q_split(v[2 * c], up, q1.x, q1.y, q2.x, q2.y);
-                    q_split(v[2 * c + 1], up, q1.z, q1.w, q2.z, q2.w);
-                    constexpr int PER = Cfg::SWK / 16;
-                    const int x = Cfg::SWK == 128 ? (c % PER) ^ (rq & 7) : (c % PER) ^ ((rq >> 1) & 3);
-                    uint8_t* at = tile + (c / PER) * (BM * Cfg::SWK) + rq * Cfg::SWK + (x << 4);
-                    *reinterpret_cast<uint4*>(at) = q1;
-                    *reinterpret_cast<uint4*>(at + BM * D) = q2;
+                    for (int y = 1; y < LPR; y <<= 1)
+#pragma unroll
+                        for (int i = 0; i < AT; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], y));
+#pragma unroll
+                    for (int i = 0; i < AT; ++i) {
+                        const int r = q_row(x + i), shift = q_shift(top[i], 7);
+                        uint2 q1, q2;
+                        q_split(v[i], top[i] >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2f(shift), q1, q2);
+                        const int c = qc >> 1;                     // 16 codes
+                        constexpr int PER = Cfg::SWK / 16;
+                        const int z = Cfg::SWK == 128 ? (c % PER) ^ (r & 7) : (c % PER) ^ ((r >> 1) & 3);
+                        uint8_t* at = tile + (c / PER) * (BM * Cfg::SWK) + r * Cfg::SWK + (z << 4) + (qc & 1) * 8;
+                        *reinterpret_cast<uint2*>(at) = q1;
+                        *reinterpret_cast<uint2*>(at + BM * D) = q2;
+                        // (not 0: -inf, the masked score, stays -inf when multiplied)
+                        if (qc == 0) bars->q_log2[t * 128 + r] = fmaxf(p.scale_log2 * pow2f(-shift), 0x1p-126f);
+                    }
+                    __syncwarp();
                 }
-                // (not 0: -inf, the masked score, stays -inf when multiplied)
-                bars->q_log2[t * 128 + rq] = fmaxf(p.scale_log2 * pow2f(-shift), 0x1p-126f);
             }
         }
         fence_proxy_async_smem();
