@@ -432,8 +432,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             // The streams' blocks go to the tensor pipe in turns, so that one
             // stream's softmax runs beside the other's block (without turns the
             // two interleave, finish together and leave the pipe idle while both
-            // exponentiate: 3350 cycles a step).  What a block waits for is
-            // awaited before its turn.  In pair mode both warps release every
+            // exponentiate: 3350 cycles a step; 2750 with them, of which the
+            // products, at 1370 cycles a block, take all but a few).  P comes
+            // last and is awaited last: a block starts as soon as it is there.  In pair mode both warps release every
             // ring entry, always after waiting for it.
             constexpr uint32_t fmt = FP8 ? 0u : 1u;            // fp16 or bf16 operands
             constexpr uint32_t idesc_s = make_idesc(FP8 ? 0u : 1u, 128, BN, 0), idesc_o = make_idesc(fmt, 128, D, 1);
@@ -456,8 +457,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 const uint32_t xk = FP8 ? tile_slot<Cfg>(w, t, u) : tile_entry<Cfg>(w, t, u, false);
                 if (has_v) ok = tile_warp_wait(&bars->ring_full[xv % NH], (xv / NH) & 1, abort_flag, p, SITE_TILE_FULL);
                 if (ok && has_k) ok = tile_warp_wait(&k_full[xk % NKR], (xk / NKR) & 1, abort_flag, p, SITE_TILE_FULL);
-                if (ok && u > 0 && u <= nt) ok = tile_warp_wait(&bars->p_full[t], (u - 1) & 1, abort_flag, p, SITE_TILE_P);
                 if (NS > 1 && ok) ok = tile_turn(turn, 2 * u + t, abort_flag, p);
+                if (ok && u > 0 && u <= nt) ok = tile_warp_wait(&bars->p_full[t], (u - 1) & 1, abort_flag, p, SITE_TILE_P);
                 if (!ok) break;
                 tc_fence_after();
                 if (elect_one()) {
@@ -818,6 +819,31 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             const int slot = kt % Cfg::SLOTS;
             bool wt = tile_wait(&bars->sc_full[slot], (kt / Cfg::SLOTS) & 1, abort_flag, p, SITE_TILE_SCALE);
             if (FP8) wt = wt && tile_wait(&bars->vs_ready[slot], (kt / Cfg::SLOTS) & 1, abort_flag, p, SITE_TILE_SCALE);
+            // What does not need S is done while the products run.
+            const int key0 = (j0 + u) * BN;
+            const float2* ks = reinterpret_cast<const float2*>(sScale + slot * 2 * BN) + (lane & 3);
+            constexpr int NG = BN / 8;
+            float vfall = 1.0f;                    // e4m3: O is in units of vref
+            uint32_t seen[BN / 32], all = 0xffffffffu;
+            if constexpr (FP8) {
+                const float now = bars->vref[slot];
+                if (now != vref) {
+                    vfall = vref * (1.0f / now);
+                    vref = now;
+                }
+                const int low = min(min(limit4[0], limit4[1]), min(limit4[2], limit4[3]));
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c) all &= bars->valid[slot][c];
+                if (key0 + BN > low) all = 0;
+            } else {
+#pragma unroll
+                for (int c = 0; c < BN / 32; ++c) {
+                    const int n = min(max(limit - key0 - c * 32, 0), 32);
+                    seen[c] = bars->valid[slot][c] & (n == 32 ? 0xffffffffu : (1u << n) - 1u);
+                    all &= seen[c];
+                }
+            }
+            const bool masked = __any_sync(0xffffffffu, all != 0xffffffffu);
             wt = wt && tile_wait(&bars->s_full[t], u & 1, abort_flag, p, SITE_TILE_S);
             if (!__all_sync(0xffffffffu, wt)) {
                 ok = false;
@@ -830,31 +856,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 // quarter of them; one row a thread read 512 bytes of K scales and 512
                 // of V scales a tile, which with the conversion's traffic bounded the
                 // kernel by shared memory (6300 cycles a step of two tiles).
-                float vfall = 1.0f;                // O is in units of vref
-                if (u == 0) {
+                if (u == 0) {                      // (in alt mode stream 0's threads wrote it: S comes after)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         tl4[i] = bars->q_log2[(w.pair ? t * 128 : 0) + (warp & 3) * 32 + (lane >> 2) + 8 * i];
                 }
-                const float now = bars->vref[slot];
-                if (now != vref) {
-                    vfall = vref * (1.0f / now);
-                    vref = now;
-                }
-                constexpr int NG = BN / 8;
                 uint32_t sr[8 * NG];               // (half of the rows, group, row bit, column bit)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) tmem_ld_frag<NG>(s_tmem + (static_cast<uint32_t>(16 * h) << 16), sr + h * 4 * NG);
                 tmem_wait_ld();
 #pragma unroll
                 for (int x = 0; x < 8 * NG; x += 32) reg_fence32(sr + x);
-                const float2* ks = reinterpret_cast<const float2*>(sScale + slot * 2 * BN) + (lane & 3);
-                const int key0 = (j0 + u) * BN;
-                uint32_t all = 0xffffffffu;
-#pragma unroll
-                for (int c = 0; c < BN / 32; ++c) all &= bars->valid[slot][c];
-                const int low = min(min(limit4[0], limit4[1]), min(limit4[2], limit4[3]));
-                const bool masked = __any_sync(0xffffffffu, all != 0xffffffffu || key0 + BN > low);
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
@@ -958,16 +970,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < BN / 32; ++c) reg_fence32(sr + c * 32);
-                const int key0 = (j0 + u) * BN;
-                uint32_t seen[BN / 32];
-                uint32_t all = 0xffffffffu;
-#pragma unroll
-                for (int c = 0; c < BN / 32; ++c) {
-                    const int n = min(max(limit - key0 - c * 32, 0), 32);
-                    seen[c] = bars->valid[slot][c] & (n == 32 ? 0xffffffffu : (1u << n) - 1u);
-                    all &= seen[c];
-                }
-                const bool masked = __any_sync(0xffffffffu, all != 0xffffffffu);
                 if (masked) {
 #pragma unroll
                     for (int x = 0; x < BN; ++x)
