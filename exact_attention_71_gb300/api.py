@@ -527,62 +527,70 @@ def kv_cache(num_pages: int, page_size: int, H_kv: int, d: int, e4m3: bool = Tru
 
 
 # The paged entries are called once per layer and decoding step, where the host
-# is the bound: one pass of checks, plain integers to ctypes, no context manager
-# unless the device or the stream asks for one.
+# is the bound: one pass of checks, devices compared by their index, plain
+# integers to ctypes, no context manager unless the device asks for one.
+
+_BF16, _F32, _I32, _I64, _U8, _E4M3 = (torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
+                                       torch.float8_e4m3fn)
+
 
 def _check_cache(cache):
-    """(num_pages, H_kv, page_size, d, cache dtype, device, pointers) of a KVCache."""
+    """(num_pages, H_kv, page_size, d, cache dtype, device index, pointers) of a KVCache."""
     k, v, ks, vs = cache
-    shape, dtype, dev = k.shape, k.dtype, k.device
-    if not k.is_cuda or len(shape) != 4 or v.shape != shape or v.dtype != dtype or v.device != dev:
+    shape, dtype, dev = k.shape, k.dtype, k.get_device()
+    if not k.is_cuda or len(shape) != 4 or v.shape != shape or v.dtype != dtype or v.get_device() != dev:
         raise ValueError("cache k and v must be CUDA tensors of one (num_pages, H_kv, page_size, d) shape and dtype")
     if not k.is_contiguous() or not v.is_contiguous():
         raise ValueError("cache k and v must be contiguous")
     pages, Hkv, ps, d = shape
-    if dtype == torch.bfloat16:
+    if dtype == _BF16:
         if ks is not None or vs is not None:
             raise ValueError("a bf16 cache has no scales")
         return pages, Hkv, ps, d, CACHE_BF16, dev, (k.data_ptr(), v.data_ptr(), None, None)
-    if dtype != torch.uint8 and dtype != torch.float8_e4m3fn:
+    if dtype != _U8 and dtype != _E4M3:
         raise ValueError("cache k and v must be bf16 or e4m3 codes (uint8 or float8_e4m3fn)")
-    for s in (ks, vs):
-        if (s is None or s.dtype != torch.float32 or s.shape != shape[:3] or not s.is_contiguous()
-                or s.device != dev):
-            raise ValueError("an e4m3 cache has contiguous float32 (num_pages, H_kv, page_size) scales")
+    rows = shape[:3]
+    if (ks is None or vs is None or ks.dtype != _F32 or vs.dtype != _F32 or ks.shape != rows or vs.shape != rows
+            or not ks.is_contiguous() or not vs.is_contiguous() or ks.get_device() != dev or vs.get_device() != dev):
+        raise ValueError("an e4m3 cache has contiguous float32 (num_pages, H_kv, page_size) scales on its device")
     return pages, Hkv, ps, d, CACHE_E4M3, dev, (k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr())
 
 
-def _check_table(block_table, seq_lens, B, device):
+def _check_table(block_table, seq_lens, B, dev):
     """(max_pages, row stride) of a block table."""
     shape = block_table.shape
-    if (len(shape) != 2 or shape[0] != B or block_table.dtype != torch.int32
-            or block_table.device != device or (shape[1] > 1 and block_table.stride(1) != 1)):
+    if len(shape) != 2 or shape[0] != B or block_table.dtype != _I32 or block_table.get_device() != dev:
         raise ValueError("block_table must be an int32 (B, max_pages) tensor with contiguous rows on the cache's device")
-    if (len(seq_lens.shape) != 1 or seq_lens.shape[0] != B or seq_lens.dtype != torch.int32
-            or seq_lens.device != device or not seq_lens.is_contiguous()):
-        raise ValueError("seq_lens must be a contiguous int32 (B,) tensor on the cache's device")
     max_pages = shape[1]
-    stride = block_table.stride(0) if B > 1 else max_pages
-    if stride < max_pages:
+    stride, step = block_table.stride()
+    if max_pages > 1 and step != 1:
+        raise ValueError("block_table must be an int32 (B, max_pages) tensor with contiguous rows on the cache's device")
+    if (seq_lens.shape != (B,) or seq_lens.dtype != _I32 or seq_lens.get_device() != dev
+            or not seq_lens.is_contiguous()):
+        raise ValueError("seq_lens must be a contiguous int32 (B,) tensor on the cache's device")
+    if B <= 1:
+        stride = max_pages
+    elif stride < max_pages:
         raise ValueError("the rows of block_table must not overlap")
     return max_pages, stride
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _launch(fn, name, device, stream, args):
-    """Calls entry `fn` with `args` and the stream, with `device` current."""
+def _launch(fn, name, dev, stream, args):
+    """Calls entry `fn` with `args` and the stream, with device `dev` current."""
     if stream is not None:
         raw = _stream(stream)
     elif _raw_stream is not None:
-        raw = _raw_stream(device.index)
+        raw = _raw_stream(dev)
     else:
-        raw = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    if _current_device() == dev:
         rc = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             rc = fn(*args, raw)
     if rc != 0:
         _check(name, rc)
@@ -605,14 +613,13 @@ def attn_kv_write(k, v, slots, cache: KVCache, stream=None) -> None:
     T = shape[0]
     strides = []
     for t in (k, v):
-        if t.dtype != torch.bfloat16 or t.device != dev:
+        if t.dtype != _BF16 or t.get_device() != dev:
             raise ValueError("k and v must be bf16 tensors on the cache's device")
         s0, s1, s2 = t.stride()
         if s2 != 1 or (Hkv > 1 and s1 != d):
             raise ValueError("a token's heads must be contiguous in k and v")
         strides.append(s0 if T > 1 else Hkv * d)
-    if (len(slots.shape) != 1 or slots.shape[0] != T or slots.dtype != torch.int64 or slots.device != dev
-            or not slots.is_contiguous()):
+    if slots.shape != (T,) or slots.dtype != _I64 or slots.get_device() != dev or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous int64 (T,) tensor on the cache's device")
     _launch(library().attn_kv_write, "attn_kv_write", dev, stream,
             (k.data_ptr(), v.data_ptr(), *strides, slots.data_ptr(), *ptrs, T, Hkv, d, pages, ps, dtype))
@@ -632,11 +639,11 @@ def attn_kv_read(cache: KVCache, block_table, seq_lens, N: int, out_k=None, out_
     shape = (B, N, Hkv, d)
     if out_k is None or out_v is None:
         # (the zeros are written on the launch's stream)
-        with torch.cuda.stream(_torch_stream(stream, dev)):
-            out_k = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if out_k is None else out_k
-            out_v = torch.zeros(shape, dtype=torch.bfloat16, device=dev) if out_v is None else out_v
+        with torch.cuda.stream(_torch_stream(stream, cache.k.device)):
+            out_k = torch.zeros(shape, dtype=_BF16, device=cache.k.device) if out_k is None else out_k
+            out_v = torch.zeros(shape, dtype=_BF16, device=cache.k.device) if out_v is None else out_v
     for t in (out_k, out_v):
-        if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != dev:
+        if t.shape != shape or t.dtype != _BF16 or not t.is_contiguous() or t.get_device() != dev:
             raise ValueError(f"out_k and out_v must be contiguous bf16 {shape} tensors on the cache's device")
     _launch(library().attn_kv_read, "attn_kv_read", dev, stream,
             (*ptrs, block_table.data_ptr(), stride, max_pages, seq_lens.data_ptr(), out_k.data_ptr(), out_v.data_ptr(),
@@ -666,7 +673,7 @@ def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, 
     """
     pages, Hkv, ps, d, dtype, dev, ptrs = _check_cache(cache)
     shape = q.shape
-    if len(shape) != 4 or q.dtype != torch.bfloat16 or q.device != dev or not q.is_contiguous():
+    if len(shape) != 4 or q.dtype != _BF16 or q.get_device() != dev or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 (B, Nq, H, d) tensor on the cache's device")
     B, Nq, H, dq = shape
     if dq != d or Hkv == 0 or H % Hkv != 0:
@@ -675,28 +682,28 @@ def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, 
     prefix_len = int(prefix_len)
     prefix = None
     if prefix_len > 0:
-        if (prefix_table is None or len(prefix_table.shape) != 1 or prefix_table.dtype != torch.int32
-                or prefix_table.device != dev or not prefix_table.is_contiguous()
+        if (prefix_table is None or len(prefix_table.shape) != 1 or prefix_table.dtype != _I32
+                or prefix_table.get_device() != dev or not prefix_table.is_contiguous()
                 or prefix_table.shape[0] * ps < prefix_len):
             raise ValueError("prefix_table must be a contiguous int32 tensor of prefix_len's pages on the cache's device")
         prefix = prefix_table.data_ptr()
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != shape or out.dtype != torch.bfloat16 or not out.is_contiguous() or out.device != dev:
+    elif out.shape != shape or out.dtype != _BF16 or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be a contiguous bf16 (B, Nq, H, d) tensor on the cache's device")
     if lse is None:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
-    elif lse.shape != (B, H, Nq) or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.device != dev:
+        lse = torch.empty((B, H, Nq), dtype=_F32, device=q.device)
+    elif lse.shape != (B, H, Nq) or lse.dtype != _F32 or not lse.is_contiguous() or lse.get_device() != dev:
         raise ValueError("lse must be a contiguous float32 (B, H, Nq) tensor on the cache's device")
     own = workspace is None
     ws, need = None, 0
     if own:
         need = paged_workspace_bytes(B, Nq, H, Hkv, d, prefix_len, max_pages, ps)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(need, dtype=_U8, device=q.device)
             ws = workspace.data_ptr()
     else:
-        if workspace.device != dev or not workspace.is_contiguous():
+        if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
         ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _launch(library().attn_fwd_paged, "attn_fwd_paged", dev, stream,
