@@ -107,21 +107,31 @@ struct PagedPlan {
 constexpr int kPlanSms = 152;
 
 // A sequence's own tokens are cut into ranges of at least this many keys: a
-// range's partial result (16 rows x d floats, written and read again) then
-// stays small beside the keys and values that it stands for.
-constexpr int kOwnChunk = 128;
+// range's partial result (d floats a row, written and read again) then stays
+// small beside the keys and values that it stands for.  16 sequences of 700 tokens
+// behind a prefix of 2048, d = 256, bf16: 20.7, 18.0 and 16.2 us with 64, 128 and
+// 256; 4 sequences of 97 behind 512, d = 128, e4m3: 8.4, 8.5 and 9.4 us.
+__host__ __device__ constexpr int own_chunk(int d) { return d == 256 ? 256 : 128; }
 
 // Query rows of one key/value head (of one sequence; over the prefix, of all)
-// up to which the streaming kernel takes them; it reads the keys once per 16
-// rows, the tile kernel once per 128.  Microseconds of the streaming | the tile
-// kernel, 8 heads, at 16, 32 and 48 rows (the prefix: 64):
-//   own tokens, 32 x 4096:  d = 64  bf16  39 | 61   51 | 61   72 | 59   e4m3  37 | 82   60 | 83   85 | 86
-//                           d = 128 bf16  69 | 89   89 | 89  122 | 86   e4m3  59 | 117  96 | 119  127 | 122
-//                           d = 256 bf16 156 | 162 266 | 164 386 | 161  e4m3 107 | 191 178 | 194  238 | 192
-//   prefix of 32768:        d = 64  bf16  22 | 30   23 | 31   31 | 33   e4m3  21 | 37   25 | 39   36 | 41
-//                           d = 128 bf16  32 | 46   33 | 46   50 | 49   e4m3  28 | 57   35 | 56   51 | 60
-//                           d = 256 bf16  60 | 62   89 | 65  158 | 68   e4m3  43 | 82   60 | 83   99 | 87
-// (a plan does not depend on the cache's type, so that a workspace fits both).
+// up to which the streaming kernel takes them; it reads the keys once per 8 or
+// 16 rows, the tile kernel once per 128.  Microseconds of the streaming | the
+// tile kernel at 8, 16, 32 and 48 rows, 8 heads:
+//   own tokens, 32 sequences of up to 4096
+//     d = 64   bf16   38 | 57    40 | 61    61 | 61    83 | 59
+//              e4m3   31 | 80    37 | 80    63 | 81    87 | 83
+//     d = 128  bf16   68 | 83    71 | 89    95 | 89   130 | 86
+//              e4m3   46 | 112   55 | 111   89 | 114  117 | 116
+//     d = 256  bf16  131 | 161  147 | 161  270 | 162  392 | 159
+//              e4m3   79 | 195  101 | 195  173 | 196  241 | 196
+//   and at 8, 16, 32 and 64 rows of a prefix of 32768 tokens
+//     d = 64   bf16   19 | 24    22 | 25    25 | 25    35 | 26
+//              e4m3   18 | 30    21 | 31    25 | 33    37 | 34
+//     d = 128  bf16   29 | 39    33 | 40    34 | 41    52 | 38
+//              e4m3   22 | 44    27 | 44    33 | 48    49 | 43
+//     d = 256  bf16   57 | 54    60 | 55    90 | 58   161 | 63
+//              e4m3   34 | 71    39 | 71    58 | 72    98 | 73
+// (A plan does not depend on the cache's type, so that a workspace fits both.)
 constexpr int stream_rows(int d) { return d == 256 ? 16 : 32; }
 
 // Key ranges of a prefix, and of a sequence's own tokens, at most.

@@ -27,6 +27,13 @@
 // (Copying 16 bytes a thread with cp.async moved 1.5 times the bytes through the
 // L2 and kept the load/store pipe busy: one sequence of 16384 tokens, 16 heads of
 // 128, bf16, took 36 us instead of 27.)
+//
+// Measured at d = 128: that sequence now 25.4 us, 5.3 TB/s; 8 heads with 4 query
+// heads each, 16 sequences of 23551 tokens on average, bf16 216 us, 7.2 TB/s, e4m3
+// 122 us, 6.5 TB/s; 32 sequences of 3143, bf16 66 us, 6.3 TB/s, e4m3 44 us, 4.9
+// TB/s.  Long ranges are bound by HBM; e4m3 also by its instructions (500 a step of
+// 32 keys, 128 of which convert codes), short ranges by a CTA's latency (page
+// table, first copy, join).
 // The MMA's k index may be permuted freely (both operands alike), and so may O's
 // columns and the keys, so each thread takes whole 16-byte chunks from the rows
 // that its fragments need, chosen so that the 8 threads of a shared-memory phase
@@ -89,7 +96,7 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
 //        element down to 2^-31 of the largest is then exact
 //   P    times V's row scale / vref, a power of two that follows the scales and
 //        keeps the product below 2^15; rounded once to fp16 (2^-11; below 2^-14,
-//        2^-25 absolute)
+//        2^-25 absolute, 2^-29 of the largest scale)
 __device__ __forceinline__ uint32_t f16x2_of_lo(uint32_t codes) {
     uint32_t r;
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(codes));
@@ -122,8 +129,8 @@ __device__ __forceinline__ uint32_t pack_e4m3x2_f16(uint32_t x) {
 
 // Eight bf16 times a power of two that brings them below 2^8 -> two e4m3 parts of
 // each, x = q1 + q2.  The first has the leading four bits of x's eight, the second
-// the rest: exact for |x| >= 2^-2 (2^-10 of the row's largest), and within 2^-10
-// below that, where e4m3 ends (fp16 holds x and x - q1 exactly down to 2^-14).  A
+// the rest: exact for |x| >= 2^-2 (2^-9 of the row's largest at most), and within
+// 2^-10 below that, where e4m3 ends (fp16 holds x and x - q1 exactly down to 2^-14).  A
 // factor of NaN makes all of them NaN.
 __device__ __forceinline__ void q_split(const uint4& v, float factor, uint2& q1, uint2& q2) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -181,8 +188,10 @@ struct StreamCfg {
     static constexpr int WARPS = 4;
     static constexpr int THREADS = WARPS * 32;
     // 16-key blocks of a warp's step.  e4m3 steps are bound by instructions: two
-    // blocks share the waits, the copies' issue and the running maximum.  bf16
-    // steps are bound by bytes, and small steps keep more warps an SM.
+    // blocks share the waits, the copies' issue and the running maximum (d = 64:
+    // 30 us against 38).  bf16 steps are bound by bytes, and small steps fill the
+    // ring more evenly (d = 128: 66 us against 68); so are e4m3 steps at d = 256 (81
+    // against 83, and 51 against 68 where sequences are short).
     static constexpr int H = FP8 && D <= 128 ? 2 : 1;
     static constexpr int STEP = 16 * H;
     static constexpr int TILE = 16 * ROW;                          // a block's K or V rows
@@ -310,7 +319,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         }
         len = max(len, 0);
     }
-    const int chunk = max(((len + parts - 1) / parts + 63) / 64 * 64, kOwnChunk);
+    const int chunk = max(((len + parts - 1) / parts + 63) / 64 * 64, own_chunk(D));
     const int k0 = static_cast<int>(min(static_cast<long long>(part) * chunk, static_cast<long long>(len)));
     const int k1 = min(k0 + chunk, len);
     const int* table = prefix ? p.prefix_table : p.table + seq * p.table_stride;

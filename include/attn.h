@@ -1,6 +1,6 @@
 /*
  * attn.h -- C ABI of the GB300 (sm_103a) fused exact attention (forward,
- * FP8 prep, backward).
+ * FP8 prep, backward, attention over a paged key/value cache).
  *
  * What is computed (FlashAttention-3 deep-reading report, "第三层" intro and
  * §3.1-§3.3; "Efficient Attention & FlashAttention", "数学机理"):
@@ -34,9 +34,9 @@
  *  - Return value: ATTN_OK or a negative attn_status.  The text of the last
  *    error of the calling thread is available from attn_last_error_string().
  *  - Under the causal and window masks alone every query sees at least
- *    itself.  Only attn_fwd_sparse can leave a row with no visible key (its
- *    block mask hides every key block of the row's query tile); such rows
- *    get O = 0 and LSE = -inf.
+ *    itself.  attn_fwd_sparse (its block mask hides every key block of the
+ *    row's query tile) and attn_fwd_paged (an empty sequence) can leave a row
+ *    with no visible key; such rows get O = 0 and LSE = -inf.
  */
 #ifndef ATTN_GB300_H
 #define ATTN_GB300_H
@@ -431,7 +431,14 @@ int attn_kv_read(const void* k_cache, const void* v_cache, const float* k_scale,
  * reach it whatever they hold, NaN included.  A bf16 V row with an infinity or a
  * NaN among the own tokens that not every query sees (the last Nq - 1 under
  * the causal mask) makes the whole O row and the LSE of the queries that do see
- * it NaN.
+ * it NaN; likewise an e4m3 V row with a NaN code or a scale that is not finite.
+ * Precision: scores and sums are float32.  bf16 cache: the weights are rounded
+ * to bf16 (2^-8) for the product with V, as in attn_fwd.  e4m3 cache: q and the
+ * codes enter the products exactly, but for elements of q below 2^-9 of the
+ * largest of their row, which may be rounded, by 2^-17 of it at most; weights and scaled V
+ * rows are rounded to fp16 (2^-11 each, three roundings at most); where a V row's
+ * scale is below 2^-18 of the largest V scale among the own tokens, or those of
+ * the prefix, by up to 2^-29 of that.
  * The workspace size depends on its arguments alone.  prefix_len, max_pages
  * and the launches are the host's: a captured graph replays them with new
  * table entries, lengths, queries and cache contents.  Errors: before any
