@@ -575,8 +575,23 @@ def _check_table(block_table, seq_lens, B, dev):
     return max_pages, stride
 
 
+# Entries of torch that may go away; without them the public ones are called (an
+# attention call of 22 us on the host then takes 26: the dispatcher's part of a
+# torch.empty costs more than the allocation).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_empty = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _empty(shape, dtype, dev):
+    """An uninitialised contiguous tensor on CUDA device `dev`."""
+    if _raw_empty is None or _current_device() != dev:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    stride, strides = 1, []
+    for n in reversed(shape):
+        strides.append(stride)
+        stride *= n or 1
+    return _raw_empty(tuple(shape), tuple(strides[::-1]), dtype)
 
 
 def _launch(fn, name, dev, stream, args):
@@ -688,11 +703,11 @@ def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, 
             raise ValueError("prefix_table must be a contiguous int32 tensor of prefix_len's pages on the cache's device")
         prefix = prefix_table.data_ptr()
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(shape, _BF16, dev)
     elif out.shape != shape or out.dtype != _BF16 or not out.is_contiguous() or out.get_device() != dev:
         raise ValueError("out must be a contiguous bf16 (B, Nq, H, d) tensor on the cache's device")
     if lse is None:
-        lse = torch.empty((B, H, Nq), dtype=_F32, device=q.device)
+        lse = _empty((B, H, Nq), _F32, dev)
     elif lse.shape != (B, H, Nq) or lse.dtype != _F32 or not lse.is_contiguous() or lse.get_device() != dev:
         raise ValueError("lse must be a contiguous float32 (B, H, Nq) tensor on the cache's device")
     own = workspace is None
@@ -700,7 +715,7 @@ def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, 
     if own:
         need = paged_workspace_bytes(B, Nq, H, Hkv, d, prefix_len, max_pages, ps)
         if need:
-            workspace = torch.empty(need, dtype=_U8, device=q.device)
+            workspace = _empty((need,), _U8, dev)
             ws = workspace.data_ptr()
     else:
         if workspace.get_device() != dev or not workspace.is_contiguous():

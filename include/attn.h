@@ -428,7 +428,8 @@ int attn_kv_read(const void* k_cache, const void* v_cache, const float* k_scale,
  * O = 0 and LSE = -inf.  A page index outside the cache hides its tokens
  * (recorded); a length is cut as in attn_kv_read.  Cache rows that are not
  * visible to a query row (past the length, or behind the causal limit) do not
- * reach it whatever they hold, NaN included.  A bf16 V row with an infinity or a
+ * reach it whatever they hold, NaN included (but see Precision for the V scales
+ * of an e4m3 cache behind the causal limit).  A bf16 V row with an infinity or a
  * NaN among the own tokens that not every query sees (the last Nq - 1 under
  * the causal mask) makes the whole O row and the LSE of the queries that do see
  * it NaN; likewise an e4m3 V row with a NaN code or a scale that is not finite.

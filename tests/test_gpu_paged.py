@@ -564,6 +564,18 @@ def test_repeated_calls_give_the_same_bits():
         assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
+def test_the_outputs_do_not_depend_on_how_torch_allocates_them(monkeypatch):
+    p = Problem([300, 77, 0], 900, 3, 8, 2, 128, 16, True, seed=15)
+    o, lse = p.run()
+    assert o.is_contiguous() and lse.is_contiguous() and o.dtype == torch.bfloat16 and lse.dtype == torch.float32
+    assert o.device == p.q.device and o.shape == p.q.shape and lse.shape == (3, 8, 3)
+    for name in ("_raw_empty", "_raw_stream"):
+        monkeypatch.setattr(api, name, None)
+    o2, l2 = p.run()
+    assert o2.stride() == o.stride() and l2.stride() == lse.stride()
+    assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
 def test_empty_problems():
     c = api.kv_cache(2, 16, 2, 64)
     none = torch.zeros((0, 1), dtype=torch.int32, device=DEV)
