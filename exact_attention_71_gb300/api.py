@@ -672,6 +672,20 @@ def paged_workspace_bytes(B: int, Nq: int, H: int, H_kv: int, d: int, prefix_len
     return int(library().attn_fwd_paged_workspace_size(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size))
 
 
+def _paged_buffers(out, lse, workspace, shape, Hkv, prefix_len, max_pages, page_size, dev):
+    """out, lse and workspace, allocated where they are None."""
+    B, Nq, H, d = shape
+    if out is None:
+        out = _empty(shape, _BF16, dev)
+    if lse is None:
+        lse = _empty((B, H, Nq), _F32, dev)
+    if workspace is None:
+        need = paged_workspace_bytes(B, Nq, H, Hkv, d, prefix_len, max_pages, page_size)
+        if need:
+            workspace = _empty((need,), _U8, dev)
+    return out, lse, workspace
+
+
 def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, prefix_len: int = 0,
                    causal: bool = True, scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
     """Attention of Nq query tokens of each of B sequences over the paged cache:
@@ -702,31 +716,25 @@ def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, 
                 or prefix_table.shape[0] * ps < prefix_len):
             raise ValueError("prefix_table must be a contiguous int32 tensor of prefix_len's pages on the cache's device")
         prefix = prefix_table.data_ptr()
-    if out is None:
-        out = _empty(shape, _BF16, dev)
-    elif out.shape != shape or out.dtype != _BF16 or not out.is_contiguous() or out.get_device() != dev:
+    if out is not None and (out.shape != shape or out.dtype != _BF16 or not out.is_contiguous()
+                            or out.get_device() != dev):
         raise ValueError("out must be a contiguous bf16 (B, Nq, H, d) tensor on the cache's device")
-    if lse is None:
-        lse = _empty((B, H, Nq), _F32, dev)
-    elif lse.shape != (B, H, Nq) or lse.dtype != _F32 or not lse.is_contiguous() or lse.get_device() != dev:
+    if lse is not None and (lse.shape != (B, H, Nq) or lse.dtype != _F32 or not lse.is_contiguous()
+                            or lse.get_device() != dev):
         raise ValueError("lse must be a contiguous float32 (B, H, Nq) tensor on the cache's device")
-    own = workspace is None
-    ws, need = None, 0
-    if own:
-        need = paged_workspace_bytes(B, Nq, H, Hkv, d, prefix_len, max_pages, ps)
-        if need:
-            workspace = _empty((need,), _U8, dev)
-            ws = workspace.data_ptr()
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    if stream is None:
+        out, lse, workspace = _paged_buffers(out, lse, workspace, shape, Hkv, prefix_len, max_pages, ps, dev)
     else:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the cache's device")
-        ws, need = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        # (memory of the launch's stream: that of another may still be in use there)
+        with torch.cuda.stream(_torch_stream(stream, q.device)):
+            out, lse, workspace = _paged_buffers(out, lse, workspace, shape, Hkv, prefix_len, max_pages, ps, dev)
+    ws, room = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
     _launch(library().attn_fwd_paged, "attn_fwd_paged", dev, stream,
             (q.data_ptr(), *ptrs, prefix, prefix_len, block_table.data_ptr(), stride, max_pages, seq_lens.data_ptr(),
              out.data_ptr(), lse.data_ptr(), B, Nq, H, Hkv, d, pages, ps, dtype, 1 if causal else 0,
-             float(scale or 0.0), ws, need))
-    if own and ws is not None and stream is not None:
-        _hold_until_done(workspace, stream)   # the launches run on `stream`, not torch's current one
+             float(scale or 0.0), ws, room))
     return out, lse
 
 

@@ -576,6 +576,24 @@ def test_the_outputs_do_not_depend_on_how_torch_allocates_them(monkeypatch):
     assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
+def test_buffers_made_for_another_stream_are_that_streams():
+    """Memory freed on the current stream may still be in use there."""
+    p = Problem([300, 77, 5], 900, 3, 8, 2, 128, 16, True, seed=16)
+    want = p.run()
+    need = api.paged_workspace_bytes(3, 3, 8, 2, 128, 900, p.table.shape[1], 16)
+    assert need > 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = [torch.empty_like(want[0]) for _ in range(8)] + [torch.empty_like(want[1]) for _ in range(8)]
+    addresses = {t.data_ptr() for t in freed}
+    del freed
+    for stream in (side, side.cuda_stream):
+        o, lse = p.run(stream=stream)
+        assert o.data_ptr() not in addresses and lse.data_ptr() not in addresses
+        side.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
 def test_empty_problems():
     c = api.kv_cache(2, 16, 2, 64)
     none = torch.zeros((0, 1), dtype=torch.int32, device=DEV)
