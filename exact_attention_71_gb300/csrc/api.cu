@@ -1154,6 +1154,7 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
     p.own_items = plan.own_items;
     p.own_ctas = plan.own_ctas;
     p.stream_tile = plan.stream_tile;
+    attn::paged_divisors(p);
     p.scale_log2 = resolve_scale(scale, d) * 1.4426950408889634f;
     p.fp8 = cache_dtype == ATTN_CACHE_E4M3;
     p.wait_limit = g_wait_limit.load();

@@ -59,6 +59,22 @@ struct KvReadParams {
     int* status;
 };
 
+// n / d for n < 2^31 by a multiplication (d from the host; Granlund and
+// Montgomery): with 2^s >= d and m = floor(2^32 (2^s - d) / d) + 1, n / d = (n +
+// floor(m n / 2^32)) >> s.  A CTA finds its place by half a dozen of them, one after
+// the other, before its first load; the compiler's own division by a variable
+// took 1800 cycles of a tile CTA there.
+struct FastDiv {
+    unsigned d = 1, m = 1, s = 0;
+    FastDiv() = default;
+    explicit FastDiv(unsigned by) : d(by) {
+        while ((1ull << s) < d) ++s;
+        m = static_cast<unsigned>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+    }
+    __device__ __forceinline__ unsigned div(unsigned n) const { return (__umulhi(n, m) + n) >> s; }
+    __device__ __forceinline__ unsigned mod(unsigned n) const { return n - div(n) * d; }
+};
+
 // The attention.  A query row is (sequence b, query token i, head h); the rows
 // of one key/value head's group share its keys.  Row index in q, o and the
 // partial results: (b * Nq + i) * H + h.
@@ -84,6 +100,11 @@ struct PagedParams {
     int prefix_items, prefix_ctas;   // tile kernel: work items of the prefix; CTAs that share a row tile's keys
     int own_items, own_ctas;         // the same for the own tokens (0: the streaming kernel has them)
     int stream_tile;             // query rows of a streaming CTA: 8 or 16
+    FastDiv by_G, by_per, by_heads;              // G, Nq G, H_kv
+    FastDiv by_prefix_parts, by_own_parts;
+    FastDiv by_prefix_rows, by_own_rows;         // streaming CTAs that share keys
+    FastDiv by_prefix_groups, by_own_groups;     // tile kernel: CTAs that share keys,
+    FastDiv by_prefix_shares, by_own_shares;     // and shares of a row tile's keys
     float scale_log2;
     bool fp8;
     unsigned long long wait_limit;
@@ -139,6 +160,9 @@ constexpr int kMaxParts = 256;
 
 // A streaming CTA's fixed cost, in keys.
 constexpr double kStreamFixed = 300.0;
+
+// Fills in the divisors, from the other parameters.
+void paged_divisors(PagedParams& p);
 
 PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size);
 

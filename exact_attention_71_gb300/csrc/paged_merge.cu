@@ -125,6 +125,26 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     return plan;
 }
 
+void paged_divisors(PagedParams& p) {
+    const unsigned per = static_cast<unsigned>(p.Nq * p.G), all = static_cast<unsigned>(p.B) * per;
+    p.by_G = FastDiv(p.G);
+    p.by_per = FastDiv(per);
+    p.by_heads = FastDiv(p.H_kv);
+    p.by_prefix_parts = FastDiv(std::max(p.prefix_parts, 1));
+    p.by_own_parts = FastDiv(p.own_parts);
+    const auto stream = [&](unsigned rows) { return FastDiv((rows + p.stream_tile - 1) / p.stream_tile); };
+    p.by_prefix_rows = stream(all);
+    p.by_own_rows = stream(per);
+    // (one row tile, d < 256: two streams halve a CTA's keys; more: a CTA takes two)
+    const auto tiles = [&](unsigned rows, int ctas, FastDiv& groups, FastDiv& shares) {
+        const unsigned n = (rows + 127) / 128;
+        groups = FastDiv(p.d == 256 ? n : (n + 1) / 2);
+        shares = FastDiv(static_cast<unsigned>(std::max(ctas, 1)) * (p.d != 256 && n == 1 ? 2 : 1));
+    };
+    tiles(all, p.prefix_ctas, p.by_prefix_groups, p.by_prefix_shares);
+    tiles(per, p.own_ctas, p.by_own_groups, p.by_own_shares);
+}
+
 namespace {
 
 // W warps per row, D / 32 columns a lane; lane x of a warp has the weight of part

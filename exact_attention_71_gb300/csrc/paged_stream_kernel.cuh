@@ -299,15 +299,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     const bool prefix = !DIRECT && x0 < prefix_blocks;
     if (!prefix) x0 -= prefix_blocks;
     const int rows = (prefix ? p.B : 1) * p.Nq * p.G;
-    const unsigned tiles = (rows + Cfg::ROWS - 1) / Cfg::ROWS;
-    const int parts = prefix ? p.prefix_parts : p.own_parts;
+    const FastDiv by_tiles = prefix ? p.by_prefix_rows : p.by_own_rows, by_parts = prefix ? p.by_prefix_parts : p.by_own_parts;
+    const int parts = by_parts.d;
     // Row tiles and heads of the same pages run next to one another.
-    const int tile = x0 % tiles;
-    x0 /= tiles;
-    const int kvh = x0 % p.H_kv;
-    x0 /= p.H_kv;
-    const int part = x0 % parts;
-    const int seq = prefix ? 0 : x0 / parts;
+    unsigned y0 = by_tiles.div(x0);
+    const int tile = x0 - y0 * by_tiles.d;
+    x0 = p.by_heads.div(y0);
+    const int kvh = y0 - x0 * p.H_kv;
+    y0 = by_parts.div(x0);
+    const int part = x0 - y0 * parts;
+    const int seq = prefix ? 0 : y0;
 
     // The key range.
     int len = prefix ? p.prefix_len : __ldg(p.seq_lens + seq);
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         }
         len = max(len, 0);
     }
-    const int chunk = max(((len + parts - 1) / parts + 63) / 64 * 64, own_chunk(D));
+    const int chunk = max((static_cast<int>(by_parts.div(len + parts - 1)) + 63) / 64 * 64, own_chunk(D));
     const int k0 = static_cast<int>(min(static_cast<long long>(part) * chunk, static_cast<long long>(len)));
     const int k1 = min(k0 + chunk, len);
     const int* table = prefix ? p.prefix_table : p.table + seq * p.table_stride;
@@ -391,7 +392,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     const int live = min(Cfg::ROWS, rows - tile * Cfg::ROWS);            // rows of this tile
     auto row_of = [&](int r, long long& out, int& lse_at) -> int {
         const int x = tile * Cfg::ROWS + r;
-        const int b = prefix ? x / per : seq, i = (prefix ? x % per : x) / p.G, h = kvh * p.G + x % p.G;
+        const int y = prefix ? p.by_per.div(x) : 0, z = x - y * per;               // row z of its sequence
+        const int b = prefix ? y : seq, i = p.by_G.div(z), h = kvh * p.G + z - i * p.G;
         out = (static_cast<long long>(b) * p.Nq + i) * p.H + h;
         lse_at = (b * p.H + h) * p.Nq + i;
         return i;
@@ -477,7 +479,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     }
     // From this key on some row of the tile may not see what another does.
     int diag = len;
-    if (!prefix && p.causal) diag = max(0, len - p.Nq + 1 + (tile * Cfg::ROWS) / p.G);
+    if (!prefix && p.causal) diag = max(0, len - p.Nq + 1 + static_cast<int>(p.by_G.div(tile * Cfg::ROWS)));
     // Steps that reach it (or the range's end) are masked key by key.
     const int plain_end = min(diag, k1);
 

@@ -256,7 +256,7 @@ struct TileItem {
 // Keys that row r of the segment sees.
 __device__ __forceinline__ int row_limit(const PagedParams& p, const TileItem& w, int r) {
     if (w.prefix || !p.causal) return w.len;
-    return max(0, w.len - p.Nq + 1 + r / p.G);
+    return max(0, w.len - p.Nq + 1 + static_cast<int>(p.by_G.div(r)));
 }
 
 template <class Cfg>
@@ -269,15 +269,16 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
     w.rows = w.prefix ? p.B * per : per;
     const int tiles = (w.rows + Cfg::BM - 1) / Cfg::BM;
     w.pair = Cfg::NS == 2 && tiles > 1;
-    const unsigned groups = w.pair ? (tiles + 1) / 2 : tiles;
     // Row groups of the same keys run next to one another.
-    const int group = x % groups;
-    x /= groups;
-    w.kvh = x % static_cast<unsigned>(p.H_kv);
-    x /= static_cast<unsigned>(p.H_kv);
-    const unsigned ctas = w.prefix ? p.prefix_ctas : p.own_ctas;
-    const int split = x % ctas;
-    w.seq = w.prefix ? 0 : x / ctas;
+    const FastDiv by_groups = w.prefix ? p.by_prefix_groups : p.by_own_groups;
+    const FastDiv by_ctas = w.prefix ? p.by_prefix_parts : p.by_own_parts;
+    unsigned y = by_groups.div(x);
+    const int group = x - y * by_groups.d;
+    x = p.by_heads.div(y);
+    w.kvh = y - x * p.H_kv;
+    y = by_ctas.div(x);
+    const int split = x - y * by_ctas.d;
+    w.seq = w.prefix ? 0 : y;
     w.table = w.prefix ? p.prefix_table : p.table + w.seq * p.table_stride;
     int len = p.prefix_len;
     if (!w.prefix) {
@@ -290,7 +291,11 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
     }
     w.len = len;
     w.part = (w.prefix ? 0 : p.prefix_parts) + split;
+    // Even shares of the key tiles; the first `more` have one tile more.
     const int all = (len + Cfg::BN - 1) / Cfg::BN;
+    const bool two = Cfg::NS == 2 && !w.pair;
+    const FastDiv by_shares = w.prefix ? p.by_prefix_shares : p.by_own_shares;
+    const int least = by_shares.div(all), more = all - least * static_cast<int>(by_shares.d);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         if (t >= Cfg::NS) {
@@ -300,12 +305,9 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
         }
         w.rt[t] = w.pair ? group * 2 + t : group;
         if (w.rt[t] >= tiles) w.rt[t] = -1;
-        // Even shares of the key tiles: at most 2^23 tiles for two streams of 152
-        // CTAs (2^24 for one), so the products stay below 2^32.
-        const bool two = Cfg::NS == 2 && !w.pair;
-        const unsigned share = two ? 2 * split + t : split, shares = two ? 2 * ctas : ctas;
-        w.j0[t] = static_cast<int>(static_cast<unsigned>(all) * share / shares);
-        int j1 = static_cast<int>(static_cast<unsigned>(all) * (share + 1) / shares);
+        const int share = two ? 2 * split + t : split;
+        w.j0[t] = least * share + min(share, more);
+        int j1 = w.j0[t] + least + (share < more ? 1 : 0);
         if (w.rt[t] >= 0) {
             // Tiles past what the tile's last row sees are left out.
             const int last = min(w.rt[t] * Cfg::BM + Cfg::BM, w.rows) - 1;
@@ -392,8 +394,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         in = (stream == 0 ? w.rt[0] : w.rt[1]) >= 0 && row < w.rows;
         if (in) {
             const int per = p.Nq * p.G;
-            const int b = w.prefix ? row / per : w.seq, i = (w.prefix ? row % per : row) / p.G;
-            const int h = w.kvh * p.G + row % p.G;
+            const int y = w.prefix ? p.by_per.div(row) : 0, z = row - y * per;             // row z of its sequence
+            const int b = w.prefix ? y : w.seq, i = p.by_G.div(z);
+            const int h = w.kvh * p.G + z - i * p.G;
             out = (b * p.Nq + i) * p.H + h;
             lse_at = (b * p.H + h) * p.Nq + i;
         }
