@@ -120,29 +120,28 @@ __device__ __forceinline__ int q_shift(uint32_t bits, int to) {
     return max(-126, min(126, 127 + to - max(e, 1)));
 }
 
-// Two fp16 -> two e4m3 codes, and back.
-__device__ __forceinline__ uint32_t pack_e4m3x2_f16(uint32_t x) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(x));
-    return r;
-}
-
 // Eight bf16 times a power of two that brings them below 2^8 -> two e4m3 parts of
-// each, x = q1 + q2.  The first has the leading four bits of x's eight, the second
-// the rest: exact for |x| >= 2^-2 (2^-9 of the row's largest at most), and within
-// 2^-10 below that, where e4m3 ends (fp16 holds x and x - q1 exactly down to 2^-14).  A
-// factor of NaN makes all of them NaN.
+// each, x = q1 + q2, by bits (conversions to e4m3 run at an eighth of the rate).  x 2^-8 as an
+// fp16 number has e4m3's exponent, its subnormal ones included, so its leading
+// bits are the code: q1 has the first four of x's eight significant bits, q2 the
+// rest, exact for |x| >= 2^-2 (2^-9 of the row's largest at most); below that q2
+// is rounded to e4m3's 2^-9.  A factor of NaN makes q1 NaN.
+__device__ __forceinline__ uint32_t e4m3_of_bits(uint32_t a, uint32_t b) {
+    const uint32_t x = a << 1 | (a & 0x80008000u), y = b << 1 | (b & 0x80008000u);
+    return __byte_perm(x, y, 0x7531);
+}
 __device__ __forceinline__ void q_split(const uint4& v, float factor, uint2& q1, uint2& q2) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const float f = factor * 0x1p-8f;
     uint32_t a[4], b[4];
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
-        const uint32_t x = pack_f16x2(__uint_as_float(w[y] << 16) * factor, __uint_as_float(w[y] & 0xffff0000u) * factor);
-        a[y] = pack_e4m3x2_f16(x);
-        b[y] = pack_e4m3x2_f16(sub_f16x2(x, f16x2_of_lo(a[y])));
+        const uint32_t x = pack_f16x2(__uint_as_float(w[y] << 16) * f, __uint_as_float(w[y] & 0xffff0000u) * f);
+        a[y] = x & 0xff80ff80u;
+        b[y] = sub_f16x2(x, a[y]) + 0x00400040u;       // (half of the last bit that is kept)
     }
-    q1 = make_uint2(a[0] | a[1] << 16, a[2] | a[3] << 16);
-    q2 = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+    q1 = make_uint2(e4m3_of_bits(a[0], a[1]), e4m3_of_bits(a[2], a[3]));
+    q2 = make_uint2(e4m3_of_bits(b[0], b[1]), e4m3_of_bits(b[2], b[3]));
 }
 
 // Eight bf16 times a power of two -> eight fp16.

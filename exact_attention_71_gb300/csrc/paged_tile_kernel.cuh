@@ -965,7 +965,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 if (u > 0 && __any_sync(0xffffffffu, fell)) {
                     // O's rows lie one per lane.
                     const float fall = to_row(fall4, lane);
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
                         tmem_ld32(o_tmem + c * 32, o);
@@ -1029,7 +1029,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y));
                 if (u > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
                     // The commit that signalled S(u) covers O += P(u-1) V(u-1).
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
                         tmem_ld32(o_tmem + c * 32, o);
@@ -1089,7 +1089,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     if (__all_sync(0xffffffffu, wt)) {
                         if (some) {
                             uint8_t* mine = const_cast<uint8_t*>(other);
-#pragma unroll
+#pragma unroll 1
                             for (int c = 0; c < D / 32; ++c) {
                                 uint32_t o[32];
                                 tmem_ld32(o_tmem + c * 32, o);
@@ -1139,8 +1139,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             const int mine = in && take && (DIRECT || lse2 != -INFINITY) ? out : -1;
             const bool add = __any_sync(0xffffffffu, weight1 != 0.0f);
             constexpr int COLS = DIRECT ? 64 : 32;             // columns per 128 bytes
-#pragma unroll
-            for (int c = 0; c < D / COLS; ++c) {
+#pragma unroll 1
+            for (int c = 0; c < D / COLS; ++c) {         // (not unrolled: its code is fetched cold, once)
                 if (!take) break;
                 uint32_t o[COLS];
                 if (some) {
