@@ -5,7 +5,7 @@
 // over the parts of a row (ranges of the shared prefix and of the sequence's
 // own tokens), in the order of the parts: the result does not depend on which
 // CTA finished first.  Bound by memory, and for few rows by latency: 32768 rows of
-// 128 in two parts, 33.5 MB read, 11 us behind the tile kernel.
+// 128 in two parts, 33.5 MB read, 8 us behind the tile kernel.
 #include <cuda_bf16.h>
 
 #include <algorithm>

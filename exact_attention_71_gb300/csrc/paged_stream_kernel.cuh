@@ -28,9 +28,9 @@
 // L2 and kept the load/store pipe busy: one sequence of 16384 tokens, 16 heads of
 // 128, bf16, took 36 us instead of 27.)
 //
-// Measured at d = 128: that sequence now 25.4 us, 5.3 TB/s; 8 heads with 4 query
+// Measured at d = 128: that sequence now 24.7 us, 5.4 TB/s; 8 heads with 4 query
 // heads each, 16 sequences of 23551 tokens on average, bf16 216 us, 7.2 TB/s, e4m3
-// 122 us, 6.5 TB/s; 32 sequences of 3143, bf16 66 us, 6.3 TB/s, e4m3 44 us, 4.9
+// 122 us, 6.5 TB/s; 32 sequences of 3143, bf16 66 us, 6.3 TB/s, e4m3 43 us, 5.0
 // TB/s.  Long ranges are bound by HBM; e4m3 also by its instructions (500 a step of
 // 32 keys, 128 of which convert codes), short ranges by a CTA's latency (page
 // table, first copy, join).

@@ -39,11 +39,11 @@
 // 128: bf16 337 us, 1630 TFLOP/s (83 % of the measured peak), 2770 cycles a step of
 // two tiles, of which the products take 2740: bound by the tensor pipe (a block of
 // P V and S takes 1370 cycles where the rate alone would be 1024: at N = 128 the
-// operands in shared memory ask for all of its bandwidth).  e4m3 451 us, 1220
+// operands in shared memory ask for all of its bandwidth).  e4m3 442 us, 1240
 // TFLOP/s: bound by the latency of the softmax, 1800 cycles a tile where bf16 takes
 // 1260 (the scales, and rows spread over four threads), which two streams do not
 // hide behind 1440 cycles of products.  A CTA costs 6 us besides (query rows, first
-// copies, epilogue).
+// copies, epilogue), 9 with an e4m3 cache.
 //
 // The scores of rows past the range, and of a page outside the cache, are
 // masked; their V rows are zeroed before a product reads them (0 times stale NaN
