@@ -1043,6 +1043,7 @@ int attn_kv_write(const void* k, const void* v, long long k_stride, long long v_
     p.v_scale = v_scale;
     p.T = T;
     p.H_kv = H_kv;
+    p.by_heads = attn::FastDiv(H_kv);
     p.d = d;
     p.page_shift = log2_of(page_size);
     p.num_slots = static_cast<long long>(num_pages) * page_size;
@@ -1079,6 +1080,7 @@ int attn_kv_read(const void* k_cache, const void* v_cache, const float* k_scale,
     p.B = B;
     p.N = N;
     p.H_kv = H_kv;
+    p.by_heads = attn::FastDiv(H_kv);
     p.d = d;
     p.num_pages = num_pages;
     p.page_shift = log2_of(page_size);

@@ -29,6 +29,22 @@ enum : int {
     SITE_PAGED_LENGTH = 0x103,   // a sequence length beyond its table
 };
 
+// n / d for n < 2^31 by a multiplication (d from the host; Granlund and
+// Montgomery): with 2^s >= d and m = floor(2^32 (2^s - d) / d) + 1, n / d = (n +
+// floor(m n / 2^32)) >> s.  A CTA finds its place by half a dozen of them, one after
+// the other, before its first load; the compiler's own division by a variable
+// took 1800 cycles of a tile CTA there.
+struct FastDiv {
+    unsigned d = 1, m = 1, s = 0;
+    FastDiv() = default;
+    explicit FastDiv(unsigned by) : d(by) {
+        while ((1ull << s) < d) ++s;
+        m = static_cast<unsigned>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+    }
+    __device__ __forceinline__ unsigned div(unsigned n) const { return (__umulhi(n, m) + n) >> s; }
+    __device__ __forceinline__ unsigned mod(unsigned n) const { return n - div(n) * d; }
+};
+
 struct KvWriteParams {
     const void* k;               // bf16 rows: token t, head h at k + t * k_stride + h * d
     const void* v;
@@ -39,6 +55,7 @@ struct KvWriteParams {
     float* k_scale;
     float* v_scale;
     int T, H_kv, d, page_shift;
+    FastDiv by_heads;            // H_kv
     long long num_slots;         // num_pages * page_size
     bool fp8;
     int* status;
@@ -55,24 +72,9 @@ struct KvReadParams {
     void* k;                     // bf16 (B, N, H_kv, d)
     void* v;
     int B, N, H_kv, d, num_pages, page_shift, max_pages;
+    FastDiv by_heads;            // H_kv
     bool fp8;
     int* status;
-};
-
-// n / d for n < 2^31 by a multiplication (d from the host; Granlund and
-// Montgomery): with 2^s >= d and m = floor(2^32 (2^s - d) / d) + 1, n / d = (n +
-// floor(m n / 2^32)) >> s.  A CTA finds its place by half a dozen of them, one after
-// the other, before its first load; the compiler's own division by a variable
-// took 1800 cycles of a tile CTA there.
-struct FastDiv {
-    unsigned d = 1, m = 1, s = 0;
-    FastDiv() = default;
-    explicit FastDiv(unsigned by) : d(by) {
-        while ((1ull << s) < d) ++s;
-        m = static_cast<unsigned>(((1ull << 32) * ((1ull << s) - d)) / d + 1);
-    }
-    __device__ __forceinline__ unsigned div(unsigned n) const { return (__umulhi(n, m) + n) >> s; }
-    __device__ __forceinline__ unsigned mod(unsigned n) const { return n - div(n) * d; }
 };
 
 // The attention.  A query row is (sequence b, query token i, head h); the rows
