@@ -121,11 +121,11 @@ __device__ __forceinline__ int q_shift(uint32_t bits, int to) {
 }
 
 // Eight bf16 times a power of two that brings them below 2^8 -> two e4m3 parts of
-// each, x = q1 + q2, by bits (conversions to e4m3 run at an eighth of the rate).  x 2^-8 as an
-// fp16 number has e4m3's exponent, its subnormal ones included, so its leading
-// bits are the code: q1 has the first four of x's eight significant bits, q2 the
-// rest, exact for |x| >= 2^-2 (2^-9 of the row's largest at most); below that q2
-// is rounded to e4m3's 2^-9.  A factor of NaN makes q1 NaN.
+// each, x = q1 + q2.  x 2^-8 as an fp16 number has e4m3's exponent, its subnormal
+// ones included, so its leading bits are the code: q1 has the first four of x's
+// eight significant bits, q2 the rest, exact for |x| >= 2^-2 (2^-9 of the row's
+// largest at most); below that q2 is rounded to e4m3's 2^-9.  A factor of NaN makes
+// q1 NaN.
 __device__ __forceinline__ uint32_t e4m3_of_bits(uint32_t a, uint32_t b) {
     const uint32_t x = a << 1 | (a & 0x80008000u), y = b << 1 | (b & 0x80008000u);
     return __byte_perm(x, y, 0x7531);

@@ -345,8 +345,8 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
  *                      bf16 (ATTN_CACHE_BF16) or e4m3 (ATTN_CACHE_E4M3)
  *   k_scale, v_scale : e4m3 cache: float32 (num_pages, H_kv, page_size), the
  *                      scale of each row (one token, one head); a row's real
- *                      values are scale * e4m3 value.  Ignored (may be NULL) for
- *                      bf16.
+ *                      values are scale * e4m3 value.  Positive or NaN, as
+ *                      attn_kv_write makes them.  Ignored (may be NULL) for bf16.
  *   page_size        : 16, 32, 64, 128 or 256 tokens;  d: 64, 128 or 256
  *   slot of a token  : page * page_size + its row in the page
  *   block table      : row b lists the pages of sequence b in order; token n
@@ -436,10 +436,11 @@ int attn_kv_read(const void* k_cache, const void* v_cache, const float* k_scale,
  * Precision: scores and sums are float32.  bf16 cache: the weights are rounded
  * to bf16 (2^-8) for the product with V, as in attn_fwd.  e4m3 cache: q and the
  * codes enter the products exactly, but for elements of q below 2^-9 of the
- * largest of their row, which may be rounded, by 2^-17 of it at most; weights and scaled V
- * rows are rounded to fp16 (2^-11 each, three roundings at most); where a V row's
- * scale is below 2^-18 of the largest V scale among the own tokens, or those of
- * the prefix, by up to 2^-29 of that.
+ * largest of their row, which may be rounded, by 2^-17 of it at most, and the
+ * products with K's scales stay finite for scales below 2^90; weights and scaled
+ * V rows are rounded to fp16 (2^-11 each, three roundings at most), and where a V
+ * row's scale is below 2^-18 of the largest V scale among the own tokens, or those
+ * of the prefix, by up to 2^-29 of that.
  * The workspace size depends on its arguments alone.  prefix_len, max_pages
  * and the launches are the host's: a captured graph replays them with new
  * table entries, lengths, queries and cache contents.  Errors: before any
