@@ -97,6 +97,8 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
 //   P    times V's row scale / vref, a power of two that follows the scales and
 //        keeps the product below 2^15; rounded once to fp16 (2^-11; below 2^-14,
 //        2^-25 absolute, 2^-29 of the largest scale)
+// (The warp-level e4m3 products, which would take K as it is, are slower here: 32
+// sequences of 3143 tokens, d = 128, 45 us against 43, with 16 rows 71 against 52.)
 __device__ __forceinline__ uint32_t f16x2_of_lo(uint32_t codes) {
     uint32_t r;
     asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(codes));

@@ -273,7 +273,7 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
     const FastDiv by_groups = w.prefix ? p.by_prefix_groups : p.by_own_groups;
     const FastDiv by_ctas = w.prefix ? p.by_prefix_parts : p.by_own_parts;
     unsigned y = by_groups.div(x);
-    const int group = x - y * by_groups.d;
+    const int group = by_groups.d - 1 - (x - y * by_groups.d);     // (those that see the most keys first)
     x = p.by_heads.div(y);
     w.kvh = y - x * p.H_kv;
     y = by_ctas.div(x);
