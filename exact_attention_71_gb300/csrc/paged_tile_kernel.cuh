@@ -208,36 +208,46 @@ __device__ __noinline__ void fix_v_tile(uint8_t* tile, uint32_t copies, int log2
     int from = max(min(len, diag), 0);
     const uint32_t missing = ~copies & ((1u << (Cfg::BN >> log2_box)) - 1u);
     if (missing) from = min(from, (__ffs(missing) - 1) << log2_box);
-    // Four row groups at a time: the loads' latency is most of the work (a row
-    // group after the other, 64 rows held up a tile by 6000 cycles).
-    constexpr int AT = 4, RPI = 32 / LPR;
+    // One warp does this while the products wait, so the usual case, finite rows, is
+    // kept short: eight row groups at a time (latency), and 2^7 added to an
+    // exponent field of ones carries into the sign bit.  (A row group after the
+    // other, with comparisons, held up a tile of 128 rows by 12000 cycles.)
+    constexpr int AT = 8, RPI = 32 / LPR;
     for (int r0 = from + lane / LPR; r0 < Cfg::BN; r0 += AT * RPI) {
 #pragma unroll
         for (int c = lane % LPR; c < CPR; c += LPR) {
             uint4 v[AT];
-            bool have[AT];
 #pragma unroll
             for (int i = 0; i < AT; ++i) {
                 const int r = r0 + i * RPI;
-                have[i] = r < len && r < Cfg::BN && ((copies >> (r >> log2_box)) & 1u);
-                v[i] = have[i] ? *reinterpret_cast<const uint4*>(tile + tile_offset<Cfg>(r, c)) : make_uint4(0, 0, 0, 0);
+                const bool have = r < len && r < Cfg::BN && ((copies >> (r >> log2_box)) & 1u);
+                if (have) v[i] = *reinterpret_cast<const uint4*>(tile + tile_offset<Cfg>(r, c));
+                else v[i] = make_uint4(0, 0, 0, 0);
+                if (!have && r < Cfg::BN) *reinterpret_cast<uint4*>(tile + tile_offset<Cfg>(r, c)) = v[i];
             }
+            uint32_t bad[AT], any = 0;
 #pragma unroll
             for (int i = 0; i < AT; ++i) {
-                const int r = r0 + i * RPI;
-                if (r >= Cfg::BN) continue;
-                uint32_t* w = &v[i].x;
-                uint32_t bad = 0;
-                if (r >= diag) {
+                const uint32_t* w = &v[i].x;
+                bad[i] = 0;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) bad[i] |= (w[y] & 0x7f807f80u) + 0x00800080u;
+                any |= bad[i];
+            }
+            if (any & 0x80008000u) {
+#pragma unroll
+                for (int i = 0; i < AT; ++i) {
+                    const int r = r0 + i * RPI;
+                    if (!(bad[i] & 0x80008000u) || r < diag) continue;
+                    uint32_t* w = &v[i].x;
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
-                        const uint32_t m = __vcmpeq2(w[y] & 0x7f807f80u, 0x7f807f80u);
-                        w[y] &= ~m;
-                        bad |= m;
+                        if ((w[y] & 0x7f80u) == 0x7f80u) w[y] &= 0xffff0000u;
+                        if ((w[y] & 0x7f800000u) == 0x7f800000u) w[y] &= 0xffffu;
                     }
+                    *reinterpret_cast<uint4*>(tile + tile_offset<Cfg>(r, c)) = v[i];
+                    atomicOr(&poison[r >> 5], 1u << (r & 31));
                 }
-                if (!have[i] || bad) *reinterpret_cast<uint4*>(tile + tile_offset<Cfg>(r, c)) = v[i];
-                if (bad) atomicOr(&poison[r >> 5], 1u << (r & 31));
             }
         }
     }
