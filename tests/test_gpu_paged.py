@@ -251,6 +251,35 @@ def test_what_a_row_does_not_see_cannot_reach_it(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_what_a_row_of_a_chunk_does_not_see_cannot_reach_it(d, fp8):
+    """The same for chunks (tile kernel, one row tile and two): a value row with an
+    infinity or a NaN five tokens before the end, then a key row."""
+    for Nq, G in ((80, 1), (80, 2)):
+        p = Problem([170, 93], 40, Nq, 2 * G, 2, d, 16, fp8, seed=6)
+        o0, l0 = p.run()
+        free = Nq - 5                      # the queries before it
+        for b, n in enumerate(p.lens):
+            at = n - 5
+            slot = torch.tensor([int(p.table[b, at // 16]) * 16 + at % 16], device=DEV)
+            y = p.v[b + 1][at:at + 1].clone()
+            y[..., 3] = NAN if b == 0 else -INF
+            api.attn_kv_write(p.k[b + 1][at:at + 1], y, slot, p.cache)
+        o1, l1 = p.run()
+        assert torch.equal(o1[:, :free], o0[:, :free]) and torch.equal(l1[:, :, :free], l0[:, :, :free])
+        assert bool(torch.isnan(o1[:, free:]).all()) and bool(torch.isnan(l1[:, :, free:]).all())
+        for b, n in enumerate(p.lens):
+            at = n - 5
+            slot = torch.tensor([int(p.table[b, at // 16]) * 16 + at % 16], device=DEV)
+            x = torch.full_like(p.k[b + 1][at:at + 1], NAN)
+            api.attn_kv_write(x, p.v[b + 1][at:at + 1], slot, p.cache)
+        o2, l2 = p.run()
+        assert torch.equal(o2[:, :free], o0[:, :free]) and torch.equal(l2[:, :, :free], l0[:, :, :free])
+        assert bool(torch.isnan(o2[:, free:]).all()) and bool(torch.isnan(l2[:, :, free:]).all())
+        assert api.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_bad_pages_and_lengths_are_refused_and_reported(fp8):
     """A page outside the cache hides its tokens, a length beyond the table is cut
     to it, a slot beyond the cache is skipped; each is reported once."""
