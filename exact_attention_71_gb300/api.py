@@ -693,7 +693,8 @@ def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, 
     page_size),); prefix_len: host int.  causal: query i sees own keys j <=
     seq_lens[b] - Nq + i (all of them otherwise), and the whole prefix.
     workspace: optional uint8 CUDA tensor of at least paged_workspace_bytes(...)
-    bytes, scratch.  Returns (O (B, Nq, H, d) bf16, LSE (B, H, Nq) float32).
+    bytes, scratch.  out, lse and workspace that are not given are allocated on
+    the launch's stream.  Returns (O (B, Nq, H, d) bf16, LSE (B, H, Nq) float32).
     """
     pages, Hkv, ps, d, dtype, dev, ptrs = _check_cache(cache)
     shape = q.shape
