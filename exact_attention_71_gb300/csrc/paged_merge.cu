@@ -31,11 +31,12 @@ double tile_step_us(int d) { return d == 256 ? 1.3 : 1.6; }
 // starts beside it on the SMs that it leaves free, and is bound by memory where
 // the tile kernel is bound by the tensor cores: with `other` SM-microseconds of
 // streaming work the total is what counts, and fewer, longer CTAs may serve it
-// better (64 sequences x 4 query heads a key/value head, d = 128, behind a bf16
-// prefix of 8192 with 1024 tokens of their own: 9 CTAs for each of the 16 units of
-// the prefix, and the own tokens after them, 75 us; 6, with the own tokens beside
-// them, 62).  That work is an estimate (the lengths are not known here), so
-// the tile kernel itself may become at most half as slow again by it.
+// better (128 sequences x 4 query heads a key/value head, d = 128, behind a bf16
+// prefix of 16384 with up to 512 tokens of their own: 9 CTAs for each of the 16
+// units of the prefix, and the own tokens after them, 75 us; 6, with the own tokens
+// beside them, 62).  That work is an estimate (the lengths are not known here), so
+// the tile kernel itself may become at most half as slow again by it.  More CTAs
+// have to be 2 % better: each writes a partial result that is read again.
 int tile_ctas(int d, long long units, long long steps, double other) {
     const auto alone = [&](long long s) {
         return static_cast<double>(up(units * s, kPlanSms)) * (static_cast<double>(up(steps, s)) * tile_step_us(d) + kTileFixedUs);
@@ -51,7 +52,7 @@ int tile_ctas(int d, long long units, long long steps, double other) {
         const double free_sms = units * s < kPlanSms ? static_cast<double>(kPlanSms - units * s) : 0.0;
         const double rest = other - free_sms * t;
         const double total = rest > 0.0 ? t + rest / kPlanSms : std::max(t, free_sms > 0.0 ? other / free_sms : t);
-        if (best_total < 0.0 || total < best_total) {
+        if (best_total < 0.0 || total < 0.98 * best_total) {
             best = static_cast<int>(s);
             best_total = total;
         }
