@@ -604,8 +604,22 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 #pragma unroll
                         for (int z = 0; z < 2; ++z)
                             if (skip || key >= limit[n][z]) s[h][n][2 * x + z] = -INFINITY;
-                    // (scales of rows that are not there)
-                    if (FP8 && (skip || key >= k1)) vscale[h][x] = 0.0f;
+                    if constexpr (FP8) {
+                        // Scales of rows that are not there, and those that are not
+                        // finite where some query may not see the row: vref must not
+                        // follow them, and the rows that do see it become NaN as a
+                        // whole, as they do for a code that is NaN (below).
+                        if (skip || key >= k1) {
+                            vscale[h][x] = 0.0f;
+                        } else if (key >= diag && !(vscale[h][x] < INFINITY)) {
+                            vscale[h][x] = 0.0f;
+#pragma unroll
+                            for (int n = 0; n < R; ++n)
+#pragma unroll
+                                for (int z = 0; z < 2; ++z)
+                                    if (key < limit[n][z]) l[n][z] = __uint_as_float(0x7fc00000u);
+                        }
+                    }
                 }
             }
         }
