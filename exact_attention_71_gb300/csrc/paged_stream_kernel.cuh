@@ -478,9 +478,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             }
         }
     }
-    // From this key on some row of the tile may not see what another does.
-    int diag = len;
-    if (!prefix && p.causal) diag = max(0, len - p.Nq + 1 + static_cast<int>(p.by_G.div(tile * Cfg::ROWS)));
+    // From this key on some query of the sequence does not see what another does
+    // (of the sequence, not of the tile: which rows become NaN beside a value that is
+    // not finite must not depend on the tiles).
+    const int diag = !prefix && p.causal ? max(0, len - p.Nq + 1) : len;
     // Steps that reach it (or the range's end) are masked key by key.
     const int plain_end = min(diag, k1);
 

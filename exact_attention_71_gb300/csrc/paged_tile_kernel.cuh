@@ -384,6 +384,29 @@ __device__ __forceinline__ int tile_slot(const TileItem& w, int t, int u) {
     return u + (t == 0 ? min(u, w.n[1]) : min(u + 1, w.n[0]));
 }
 
+// Whether a V row of the keys [lo, hi) is not finite (whole warp; rows of pages
+// outside the cache, which are hidden, do not count).
+template <class Cfg>
+__device__ __forceinline__ bool v_rows_not_finite(const PagedParams& p, const TileItem& w, int lo, int hi, int lane) {
+    constexpr int CPR = Cfg::FP8 ? Cfg::D / 16 : Cfg::D / 8;       // 16-byte chunks of a row (32 at most)
+    bool bad = false;
+#pragma unroll 1
+    for (int key = lo + lane / CPR; key < hi; key += 32 / CPR) {
+        const int page = __ldg(w.table + (key >> p.page_shift));
+        if (page < 0 || page >= p.num_pages) continue;
+        const long long at = ((static_cast<long long>(page) * p.H_kv + w.kvh) << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.v_cache) + at * (CPR * 16)) + lane % CPR);
+        const uint32_t* x = &v.x;
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            if constexpr (Cfg::FP8) bad |= __vcmpeq4(x[y] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+            else bad |= (((x[y] & 0x7f807f80u) + 0x00800080u) & 0x80008000u) != 0;
+        }
+        if constexpr (Cfg::FP8) bad |= !(__ldg(p.v_scale + at) < INFINITY);
+    }
+    return __any_sync(0xffffffffu, bad);
+}
+
 
 template <class Cfg, bool DIRECT>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
@@ -1096,6 +1119,31 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         const uint32_t bits = bars->poison[min(x - diag, Cfg::DIAG_TILES - 1)][c];
                         if (bits & (n == 32 ? 0xffffffffu : (1u << n) - 1u)) l = __uint_as_float(0x7fc00000u);
                     }
+                }
+            }
+            // Keys that all of these rows see but some earlier query of the sequence
+            // does not: a V row among them that is not finite makes the rows NaN, as
+            // the poison bits do for keys that only some of the rows see, so that a
+            // query's result does not depend on the CTA that has it.  All rows' O then
+            // shows it; so the values are read again only if O is not finite in all of
+            // a warp's rows, and not by their scores alone.
+            if (!w.prefix && p.causal) {
+                const int lo = max(max(0, w.len - p.Nq + 1), j0 * BN), hi = min(diag_key, (j0 + nt) * BN);
+                if (lo < hi) {
+                    bool finite = true;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o_tmem + c * 32, o);
+                        tmem_wait_ld();
+                        reg_fence32(o);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) finite = finite && (o[x] & 0x7f800000u) != 0x7f800000u;
+                    }
+                    const bool other = l - l == 0.0f;              // (l is neither an infinity nor NaN)
+                    if (__all_sync(0xffffffffu, !in || !finite) && __any_sync(0xffffffffu, in && other) &&
+                        v_rows_not_finite<Cfg>(p, w, lo, hi, lane))
+                        l = __uint_as_float(0x7fc00000u);
                 }
             }
             float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (FP8 ? vref : 1.0f);

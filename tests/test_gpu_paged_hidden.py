@@ -14,6 +14,14 @@ def place(p, b, at):
     return int(p.table[b, at // p.ps]), at % p.ps
 
 
+def write_value(p, b, at, value):
+    """Token `at` of sequence b gets a value row with `value` in column 3."""
+    page, row = place(p, b, at)
+    y = p.v[b + 1][at:at + 1].clone()
+    y[..., 3] = value
+    api.attn_kv_write(p.k[b + 1][at:at + 1], y, torch.tensor([page * p.ps + row], device=DEV), p.cache)
+
+
 # (lens, Nq, H, H_kv, d, tokens before the end) of both kernels: drafts and chunks, the
 # key among the last ones.
 NEAR = [
@@ -23,6 +31,19 @@ NEAR = [
     ([170, 93], 80, 4, 2, 128, 5),
     ([170, 93], 80, 2, 2, 64, 5),
     ([170, 93], 80, 4, 2, 256, 1),
+]
+# The key lies among the last Nq - 1, but before the limit of every row of a CTA that
+# sees it: some key tiles before it (or within one, of the streaming kernel's tiles of
+# 16 rows).
+FAR = [
+    ([700, 600], 512, 8, 2, 128, 300),       # pairs of row tiles
+    ([700, 640], 512, 2, 2, 64, 500),
+    ([700, 640], 512, 4, 2, 256, 130),
+    ([700, 640], 300, 2, 2, 128, 129),       # an odd number of row tiles
+    ([300, 260], 100, 1, 1, 128, 60),        # one row tile
+    ([300, 260], 16, 4, 2, 128, 11),         # streaming kernel, several row tiles
+    ([90, 260], 16, 2, 1, 64, 12),
+    ([300, 33], 16, 1, 1, 256, 9),
 ]
 
 
@@ -62,3 +83,61 @@ def check_code_or_scale(shape, what):
 @pytest.mark.parametrize("shape", NEAR, ids=shape_id)
 def test_a_value_code_or_scale_that_is_not_finite(shape, what):
     check_code_or_scale(shape, what)
+
+
+@pytest.mark.parametrize("what", ["code", "nan_scale", "inf_scale"])
+@pytest.mark.parametrize("shape", FAR, ids=shape_id)
+def test_the_same_far_before_the_limits_of_the_queries_that_see_it(shape, what):
+    check_code_or_scale(shape, what)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("shape", NEAR + FAR, ids=shape_id)
+def test_every_query_that_sees_a_value_row_that_is_not_finite_is_nan(shape, fp8):
+    lens, Nq, H, hkv, d, back = shape
+    p = Problem(lens, 40, Nq, H, hkv, d, 16, fp8, seed=51)
+    before = p.run()
+    check_row(p, back, before, lambda b, at: write_value(p, b, at, NAN if b == 0 else INF))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("shape", FAR, ids=shape_id)
+def test_a_query_that_is_not_finite_stays_alone(shape, fp8):
+    """Its row of O says nothing about the values."""
+    lens, Nq, H, hkv, d, back = shape
+    p = Problem(lens, 40, Nq, H, hkv, d, 16, fp8, seed=55)
+    o0, l0 = p.run()
+    p.q[:, Nq - 2] = NAN
+    o1, l1 = p.run()
+    assert bool(torch.isnan(o1[:, Nq - 2]).all()) and bool(torch.isnan(l1[:, :, Nq - 2]).all())
+    o1[:, Nq - 2] = o0[:, Nq - 2]
+    l1[:, :, Nq - 2] = l0[:, :, Nq - 2]
+    assert torch.equal(o1, o0) and torch.equal(l1, l0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("shape", FAR, ids=shape_id)
+def test_a_value_row_that_every_query_sees_stays_in_its_columns(shape, fp8):
+    """The last key before the queries' own, and one of the prefix: LSE does not
+    depend on the values; a bf16 infinity reaches its own column alone."""
+    lens, Nq, H, hkv, d, _ = shape
+    for where in ("own", "prefix"):
+        p = Problem(lens, 40, Nq, H, hkv, d, 16, fp8, seed=53)
+        o0, l0 = p.run()
+        for b, n in enumerate(p.lens):
+            if where == "own":
+                if n > Nq:
+                    write_value(p, b, n - Nq, INF)
+            elif b == 0:
+                slot = int(p.prefix_table[1]) * 16 + 3
+                y = p.v[0][19:20].clone()
+                y[..., 3] = INF
+                api.attn_kv_write(p.k[0][19:20], y, torch.tensor([slot], device=DEV), p.cache)
+        o1, l1 = p.run()
+        assert torch.equal(l1, l0)
+        if fp8:
+            assert bool(torch.isnan(o1).all())          # the row's scale is NaN
+        else:
+            assert not bool(torch.isfinite(o1[..., 3]).any())
+            for x, y in ((o1[..., :3], o0[..., :3]), (o1[..., 4:], o0[..., 4:])):
+                assert torch.equal(x, y)
