@@ -1121,31 +1121,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     }
                 }
             }
-            // Keys that all of these rows see but some earlier query of the sequence
-            // does not: a V row among them that is not finite makes the rows NaN, as
-            // the poison bits do for keys that only some of the rows see, so that a
-            // query's result does not depend on the CTA that has it.  All rows' O then
-            // shows it; so the values are read again only if O is not finite in all of
-            // a warp's rows, and not by their scores alone.
-            if (!w.prefix && p.causal) {
-                const int lo = max(max(0, w.len - p.Nq + 1), j0 * BN), hi = min(diag_key, (j0 + nt) * BN);
-                if (lo < hi) {
-                    bool finite = true;
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(o_tmem + c * 32, o);
-                        tmem_wait_ld();
-                        reg_fence32(o);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) finite = finite && (o[x] & 0x7f800000u) != 0x7f800000u;
-                    }
-                    const bool other = l - l == 0.0f;              // (l is neither an infinity nor NaN)
-                    if (__all_sync(0xffffffffu, !in || !finite) && __any_sync(0xffffffffu, in && other) &&
-                        v_rows_not_finite<Cfg>(p, w, lo, hi, lane))
-                        l = __uint_as_float(0x7fc00000u);
-                }
-            }
             float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (FP8 ? vref : 1.0f);
             float lse2 = l == 0.0f ? -INFINITY : m + __log2f(l);
             const bool some = nt > 0;
@@ -1212,6 +1187,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             const int mine = in && take && (DIRECT || lse2 != -INFINITY) ? out : -1;
             const bool add = __any_sync(0xffffffffu, weight1 != 0.0f);
             constexpr int COLS = DIRECT ? 64 : 32;             // columns per 128 bytes
+            float2 not_finite = make_float2(0.0f, 0.0f);       // NaN once an element was not
 #pragma unroll 1
             for (int c = 0; c < D / COLS; ++c) {         // (not unrolled: its code is fetched cold, once)
                 if (!take) break;
@@ -1238,6 +1214,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                             if (weight1 != 0.0f) o[4 * y + z] = __float_as_uint(__uint_as_float(o[4 * y + z]) + e[z] * weight1);
                     }
                 }
+#pragma unroll
+                for (int y = 0; y < COLS; y += 2)
+                    not_finite = __ffma2_rn(make_float2(__uint_as_float(o[y]), __uint_as_float(o[y + 1])), make_float2(0.0f, 0.0f), not_finite);
                 __syncwarp();
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
@@ -1261,6 +1240,31 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                             reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + static_cast<long long>(dst) * D + c * COLS)[ch] = v;
                         else
                             reinterpret_cast<uint4*>(p.part_o + (part * rows_all + dst) * D + c * COLS)[ch] = v;
+                    }
+                }
+            }
+            // Keys that all of these rows see but some earlier query of the sequence
+            // does not: a V row among them that is not finite makes the rows NaN, as
+            // the poison bits do for keys that only some of the rows see, so that a
+            // query's result does not depend on the CTA that has it.  All rows' O then
+            // shows it; so the values are read again only if O is not finite in all of
+            // a warp's rows, and not by their scores alone.
+            if (take && !w.prefix && p.causal) {
+                const int lo = max(max(0, w.len - p.Nq + 1), j0 * BN);
+                const int hi = min(diag_key, (alt ? max(j0 + nt, w.j0[1] + w.n[1]) : j0 + nt) * BN);
+                const bool odd = not_finite.x + not_finite.y != 0.0f, known = lse2 - lse2 == 0.0f;
+                if (lo < hi && __all_sync(0xffffffffu, !in || odd) && __any_sync(0xffffffffu, in && known) &&
+                    v_rows_not_finite<Cfg>(p, w, lo, hi, lane)) {
+                    __syncwarp();
+                    if (in) {
+                        if constexpr (DIRECT) {
+                            p.lse[lse_at] = __uint_as_float(0x7fc00000u);
+                            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + static_cast<long long>(out) * D);
+#pragma unroll 1
+                            for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+                        } else {
+                            p.part_lse[part * rows_all + out] = __uint_as_float(0x7fc00000u);   // (the join does the rest)
+                        }
                     }
                 }
             }
