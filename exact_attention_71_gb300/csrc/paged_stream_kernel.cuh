@@ -434,10 +434,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             }
         }
     }
+    __shared__ uint32_t loud;              // e4m3: keys from diag on (32 at most) whose values are added at the end
     if constexpr (FP8) {
         // To fp16, once per CTA: a warp takes 2R rows, eight lanes a row, and
         // writes them as fragments (chunk half, row tile, lane).
         __shared__ float row_log2[Cfg::ROWS];
+        if (tid == 0) loud = 0;
         const int r = warp * (2 * R) + (lane >> 3);
         const bool mine = (lane >> 3) < 2 * R;
         uint4 v[D / 64];
@@ -605,23 +607,45 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 #pragma unroll
                         for (int z = 0; z < 2; ++z)
                             if (skip || key >= limit[n][z]) s[h][n][2 * x + z] = -INFINITY;
-                    if constexpr (FP8) {
-                        // Scales of rows that are not there, and those that are not
-                        // finite where some query may not see the row: vref must not
-                        // follow them, and the rows that do see it become NaN as a
-                        // whole, as they do for a code that is NaN (below).
-                        if (skip || key >= k1) {
-                            vscale[h][x] = 0.0f;
-                        } else if (key >= diag && !(vscale[h][x] < INFINITY)) {
-                            vscale[h][x] = 0.0f;
+                    // (scales of rows that are not there)
+                    if (FP8 && (skip || key >= k1)) vscale[h][x] = 0.0f;
+                }
+            }
+            if (FP8 && key0 + STEP > diag && diag < len) {
+                // vref must not follow a scale that some row does not see.  Every row
+                // that sees a key of this warp sees the warp's first one, and those
+                // before diag: these are what it starts from and follows.
+                const int both = max(diag, first + 1);
+                if (vref == 0.0f) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int h = 0; h < H; ++h)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            if (key0 + 16 * h + 8 * x + pig < both && vscale[h][x] < INFINITY) top = fmaxf(top, vscale[h][x]);
+                    top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+                    if (top > 0.0f) vref = vref_of(top);
+                }
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        // A scale far above vref: left out here, added at the end.  One
+                        // that is not finite makes the rows that see it NaN as a whole,
+                        // as a code that is NaN does (below).
+                        const int key = key0 + 16 * h + 8 * x + pig;
+                        if (key < diag || vscale[h][x] <= 64.0f * vref) continue;
+                        if (vscale[h][x] < INFINITY) {
+                            atomicOr(&loud, 1u << (key - diag));
+                        } else {
 #pragma unroll
                             for (int n = 0; n < R; ++n)
 #pragma unroll
                                 for (int z = 0; z < 2; ++z)
                                     if (key < limit[n][z]) l[n][z] = __uint_as_float(0x7fc00000u);
                         }
+                        vscale[h][x] = 0.0f;
                     }
-                }
             }
         }
         // ------------------------------------------------------ running maximum
@@ -825,7 +849,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         const int rr = x / (D / 4), c4 = x % (D / 4);
         long long out;
         int lse_at;
-        row_of(rr, out, lse_at);
+        const int i = row_of(rr, out, lse_at);
         float mm = jm[rr];
 #pragma unroll
         for (int w = 1; w < Cfg::WARPS; ++w) mm = fmaxf(mm, jm[w * Cfg::ROWS + rr]);
@@ -841,6 +865,36 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             acc.y += a * v.y;
             acc.z += a * v.z;
             acc.w += a * v.w;
+        }
+        if (FP8 && !prefix) {
+            // (rare) Values whose scale is far above those that other rows of the tile
+            // see; l has their weights.
+#pragma unroll 1
+            for (uint32_t bits = loud; bits; bits &= bits - 1) {
+                const int key = diag + __ffs(bits) - 1;
+                if (key >= max(0, len - p.Nq + 1 + i)) break;
+                const long long at = ((static_cast<long long>(__ldg(table + (key >> p.page_shift))) * p.H_kv + kvh) << p.page_shift) +
+                                     (key & ((1 << p.page_shift) - 1));
+                const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache) + at * D;
+                float dot = 0.0f;
+#pragma unroll 1
+                for (int y = 0; y < D; y += 4) {
+                    const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(kc + y));
+                    const uint2 qq = __ldg(reinterpret_cast<const uint2*>(q + out * D + y));
+                    const float2 lo = f16x2_to_float2(f16x2_of_lo(codes)), hi = f16x2_to_float2(f16x2_of_hi(codes));
+                    dot = fmaf(__uint_as_float(qq.x << 16), lo.x, dot);
+                    dot = fmaf(__uint_as_float(qq.x & 0xffff0000u), lo.y, dot);
+                    dot = fmaf(__uint_as_float(qq.y << 16), hi.x, dot);
+                    dot = fmaf(__uint_as_float(qq.y & 0xffff0000u), hi.y, dot);
+                }
+                const float e = ex2_approx(dot * __ldg(p.k_scale + at) * p.scale_log2 - ref) * __ldg(p.v_scale + at);
+                const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.v_cache) + at * D + c4 * 4));
+                const float2 lo = f16x2_to_float2(f16x2_of_lo(codes)), hi = f16x2_to_float2(f16x2_of_hi(codes));
+                acc.x = fmaf(e, lo.x, acc.x);
+                acc.y = fmaf(e, lo.y, acc.y);
+                acc.z = fmaf(e, hi.x, acc.z);
+                acc.w = fmaf(e, hi.y, acc.w);
+            }
         }
         // l = 0: the row sees no key of this range (O = 0, lse = -inf)
         const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;

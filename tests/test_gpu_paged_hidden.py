@@ -1,9 +1,10 @@
 """What a query row of the paged attention sees and does not see, at its edges:
-value rows that are not finite."""
+value rows that are not finite, and value scales far above the others."""
 import pytest
 import torch
 
 from exact_attention_71_gb300 import api
+from tests import paged_ref as ref
 from tests.test_gpu_paged import DEV, INF, NAN, Problem
 
 pytestmark = pytest.mark.gpu
@@ -45,6 +46,12 @@ FAR = [
     ([90, 260], 16, 2, 1, 64, 12),
     ([300, 33], 16, 1, 1, 256, 9),
 ]
+
+
+def streamed(s):
+    """Whether few rows of a key/value head, which the streaming kernel takes."""
+    lens, Nq, H, hkv, d, back = s
+    return Nq * (H // hkv) <= 32
 
 
 def shape_id(s):
@@ -141,3 +148,78 @@ def test_a_value_row_that_every_query_sees_stays_in_its_columns(shape, fp8):
             assert not bool(torch.isfinite(o1[..., 3]).any())
             for x, y in ((o1[..., :3], o0[..., :3]), (o1[..., 4:], o0[..., 4:])):
                 assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("exponent", [20, 60])
+@pytest.mark.parametrize("shape", [x for x in NEAR + FAR if streamed(x)], ids=shape_id)
+def test_a_large_value_scale_reaches_only_the_queries_that_see_it(shape, exponent):
+    """e4m3: a row's values may be 2^20 or 2^60 times the others'.  Queries before it
+    keep every bit; the others have it, and LSE is the same for all."""
+    lens, Nq, H, hkv, d, back = shape
+    p = Problem(lens, 40, Nq, H, hkv, d, 32, True, seed=54)
+    o0, l0 = p.run()
+    big = []
+    for b, n in enumerate(p.lens):
+        page, row = place(p, b, n - back)
+        p.cache.v_scale[page, :, row] *= 2.0 ** exponent
+        v = p.values("v", b)
+        v[n - back] *= 2.0 ** exponent
+        big.append(v)
+    o1, l1 = p.run()
+    assert api.device_status()[0] == 0
+    free = Nq - back
+    assert torch.equal(o1[:, :free], o0[:, :free]) and torch.equal(l1, l0)
+    for b, n in enumerate(p.lens):
+        k = torch.cat([p.values("k", -1), p.values("k", b)])
+        v = torch.cat([p.values("v", -1), big[b]])
+        q = p.q[b, free:].double()
+        sees = [p.prefix + max(0, n - Nq + 1 + i) for i in range(free, Nq)]
+        want, wl, spread, size = ref.attend(q, k, v, sees)
+        to, _ = ref.tolerances(want, wl, spread, size, d)
+        assert bool(((o1[b, free:].double() - want).abs() <= to).all()), b
+
+
+def check_against_scaled_values(p, exponents, o, lse):
+    """The plain form with the value rows of sequence b times 2^exponents[b]."""
+    for b, n in enumerate(p.lens):
+        k = torch.cat([p.values("k", -1), p.values("k", b)])
+        v = torch.cat([p.values("v", -1), p.values("v", b) * torch.exp2(exponents[b].double())[:, None, None]])
+        sees = [p.prefix + max(0, n - p.Nq + 1 + i) for i in range(p.Nq)]
+        want, wl, spread, size = ref.attend(p.q[b].double(), k, v, sees)
+        to, tl = ref.tolerances(want, wl, spread, size, p.d)
+        for i in range(p.Nq):
+            # weights or ratios of scales that fp16 rounds to a multiple of 2^-24, 2^-29
+            # of the largest that the query sees at most, for each of its keys
+            if sees[i]:
+                to[i] += sees[i] * 2.0 ** -29 * float(v[:sees[i]].abs().max())
+        assert bool(((o[b].double() - want).abs() <= to).all()), b
+        seen = torch.isfinite(wl)
+        assert bool(((lse[b].double() - wl).abs()[seen] <= tl[seen]).all()), b
+
+
+def check_random_scales(shape, back):
+    lens, Nq, H, hkv, d, _ = shape
+    p = Problem(lens, 40, Nq, H, hkv, d, 16, True, seed=56)
+    g = torch.Generator(device=DEV).manual_seed(57)
+    exponents = []
+    for b, n in enumerate(lens):
+        e = torch.zeros(n, device=DEV)
+        tail = max(0, n - Nq - back)
+        e[tail:] = torch.randint(-30, 61, (n - tail,), generator=g, device=DEV).float()
+        for at in range(tail, n):
+            page, row = place(p, b, at)
+            p.cache.v_scale[page, :, row] *= 2.0 ** float(e[at])
+        exponents.append(e)
+    o, lse = p.run()
+    assert api.device_status()[0] == 0
+    check_against_scaled_values(p, exponents, o, lse)
+
+
+@pytest.mark.parametrize("back", [-1, 3, 40])
+@pytest.mark.parametrize("shape", [x for x in NEAR + FAR if streamed(x)] + [([9, 3], 12, 2, 1, 128, 1), ([20, 1], 32, 1, 1, 64, 1)],
+                         ids=shape_id)
+def test_value_scales_of_the_last_tokens_from_2_to_the_minus_30_to_2_to_the_60(shape, back):
+    """Each query against the plain form over the keys that it sees: from the second
+    query's key on, from some keys before, and with sequences shorter than the
+    queries."""
+    check_random_scales(shape, back)
