@@ -102,7 +102,7 @@ struct TileCfg {
     static constexpr int CONV_REGS = FP8 ? 80 : 0, LOW_REGS = FP8 ? 64 : 104;
     static constexpr int HIGH_RAW = (LAUNCH_REGS * THREADS - (CONV_REGS + LOW_REGS) * 128) / (NS * 128) / 8 * 8;
     static constexpr int HIGH_REGS = HIGH_RAW > 248 ? 248 : HIGH_RAW;
-    static constexpr int BAR_BYTES = 2048;
+    static constexpr int BAR_BYTES = FP8 ? 3072 : 2048;           // (of TileBarriers)
     // Output staging: 4 KB per softmax warp, over query tiles that no product
     // reads any more (d = 64: its query tiles are too small for that).
     static constexpr int EPI_BYTES = D == 64 ? NS * 16384 : 0;
@@ -119,6 +119,7 @@ struct TileCfg {
     static_assert(NS == 1 || NH * HALF_BYTES >= BM * D * 4, "the streams' join");
 };
 
+template <bool FP8>
 struct TileBarriers {
     uint64_t q_full, loaded, drain[2], fix, joined;
     uint64_t s_full[2], p_full[2], o_full[2];
@@ -129,7 +130,7 @@ struct TileBarriers {
     uint32_t poison[8][4];         // per diagonal tile: bit per key whose V row is not finite
     float vref[8];                 // e4m3, per slot: the slot's V scales are divided by it
     float red[2][4];               // e4m3: the converting warps' maxima
-    float q_log2[128 * 2];         // e4m3: raw score -> log2 units, per query row
+    float q_log2[FP8 ? 128 * 2 : 1];   // e4m3: raw score -> log2 units, per query row
     float lse1[128];               // alt mode: stream 1's result
     uint32_t tmem_base;
     int abort_flag;
@@ -422,7 +423,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     uint8_t* sRaw = sK + Cfg::NK * Cfg::RAW_BYTES;             // e4m3: V tiles
     float* sScale = reinterpret_cast<float*>(sRaw + Cfg::NR * Cfg::RAW_BYTES);     // (slot, k / v, BN)
     uint8_t* sEpi = reinterpret_cast<uint8_t*>(sScale) + Cfg::SC_BYTES;            // d = 64: output staging
-    TileBarriers* bars = reinterpret_cast<TileBarriers*>(sEpi + Cfg::EPI_BYTES);
+    using Barriers = TileBarriers<FP8>;
+    static_assert(sizeof(Barriers) <= Cfg::BAR_BYTES, "barrier block");
+    Barriers* bars = reinterpret_cast<Barriers*>(sEpi + Cfg::EPI_BYTES);
     volatile int* abort_flag = &bars->abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
