@@ -146,6 +146,15 @@ __device__ __forceinline__ void q_split(const uint4& v, float factor, uint2& q1,
     q2 = make_uint2(e4m3_of_bits(b[0], b[1]), e4m3_of_bits(b[2], b[3]));
 }
 
+// sum + four bf16 times four e4m3 codes.
+__device__ __forceinline__ float dot4(const uint2& q, uint32_t codes, float sum) {
+    const float2 lo = f16x2_to_float2(f16x2_of_lo(codes)), hi = f16x2_to_float2(f16x2_of_hi(codes));
+    sum = fmaf(__uint_as_float(q.x << 16), lo.x, sum);
+    sum = fmaf(__uint_as_float(q.x & 0xffff0000u), lo.y, sum);
+    sum = fmaf(__uint_as_float(q.y << 16), hi.x, sum);
+    return fmaf(__uint_as_float(q.y & 0xffff0000u), hi.y, sum);
+}
+
 // Eight bf16 times a power of two -> eight fp16.
 __device__ __forceinline__ uint4 q_to_f16(const uint4& v, float factor) {
     uint4 r;
@@ -878,15 +887,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache) + at * D;
                 float dot = 0.0f;
 #pragma unroll 1
-                for (int y = 0; y < D; y += 4) {
-                    const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(kc + y));
-                    const uint2 qq = __ldg(reinterpret_cast<const uint2*>(q + out * D + y));
-                    const float2 lo = f16x2_to_float2(f16x2_of_lo(codes)), hi = f16x2_to_float2(f16x2_of_hi(codes));
-                    dot = fmaf(__uint_as_float(qq.x << 16), lo.x, dot);
-                    dot = fmaf(__uint_as_float(qq.x & 0xffff0000u), lo.y, dot);
-                    dot = fmaf(__uint_as_float(qq.y << 16), hi.x, dot);
-                    dot = fmaf(__uint_as_float(qq.y & 0xffff0000u), hi.y, dot);
-                }
+                for (int y = 0; y < D; y += 4)
+                    dot = dot4(__ldg(reinterpret_cast<const uint2*>(q + out * D + y)), __ldg(reinterpret_cast<const uint32_t*>(kc + y)), dot);
                 const float e = ex2_approx(dot * __ldg(p.k_scale + at) * p.scale_log2 - ref) * __ldg(p.v_scale + at);
                 const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.v_cache) + at * D + c4 * 4));
                 const float2 lo = f16x2_to_float2(f16x2_of_lo(codes)), hi = f16x2_to_float2(f16x2_of_hi(codes));

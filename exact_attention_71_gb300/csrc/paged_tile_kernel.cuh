@@ -127,7 +127,10 @@ struct TileBarriers {
     uint64_t raw_full[8], raw_empty[8], k_full[8], k_empty[8];
     uint64_t sc_full[8], vs_ready[8];
     uint32_t valid[8][4];          // per slot: bit per key of the tile
-    uint32_t poison[8][4];         // per diagonal tile: bit per key whose V row is not finite
+    // Per diagonal tile, bit per key: its V row is not finite (poison); from 8 on, e4m3:
+    // it is left out of the products and added at the end (loud).
+    uint32_t poison[FP8 ? 16 : 8][4];
+    float most[2];                 // e4m3, streams that begin with a diagonal tile: V scales that may move vref there
     float vref[8];                 // e4m3, per slot: the slot's V scales are divided by it
     float red[2][4];               // e4m3: the converting warps' maxima
     float q_log2[FP8 ? 128 * 2 : 1];   // e4m3: raw score -> log2 units, per query row
@@ -408,6 +411,59 @@ __device__ __forceinline__ bool v_rows_not_finite(const PagedParams& p, const Ti
     return __any_sync(0xffffffffu, bad);
 }
 
+// O of a warp's rows, one a lane, comes in units of vref and leaves in units of
+// kLoudUnit (a weight may be 2^15), with the values of the loud keys of the tiles
+// [x0, x1) that each row sees: weights exp2(s - m) from the cache, in binary32.  Whole
+// warp; out: the row's index in q, limit: the keys that it sees.
+constexpr float kLoudUnit = 0x1p20f;
+template <class Cfg>
+__device__ __noinline__ void add_loud(const PagedParams& p, const int* table, int kvh, const uint32_t (*loud)[4], int diag,
+                                      int x0, int x1, int limit, int out, float m, float vref, uint32_t o_tmem) {
+    constexpr int D = Cfg::D;
+    auto update = [&](auto&& f) {
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_tmem + c * 32, o);
+            tmem_wait_ld();
+            reg_fence32(o);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(f(c * 32 + y, __uint_as_float(o[y])));
+            tmem_st32(o_tmem + c * 32, o);
+            tmem_wait_st();
+        }
+    };
+    update([&](int, float o) { return o * (vref * (1.0f / kLoudUnit)); });
+#pragma unroll 1
+    for (int x = x0; x < x1; ++x) {
+#pragma unroll 1
+        for (int c = 0; c < Cfg::BN / 32; ++c) {
+#pragma unroll 1
+            for (uint32_t bits = loud[min(x - diag, Cfg::DIAG_TILES - 1)][c]; bits; bits &= bits - 1) {
+                const int key = x * Cfg::BN + c * 32 + __ffs(bits) - 1;
+                const long long at = ((static_cast<long long>(__ldg(table + (key >> p.page_shift))) * p.H_kv + kvh) << p.page_shift) +
+                                     (key & ((1 << p.page_shift) - 1));
+                const uint32_t* kc = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.k_cache) + at * D);
+                const uint32_t* vc = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.v_cache) + at * D);
+                float e = 0.0f;
+                if (key < limit) {
+                    const uint2* q = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) + static_cast<long long>(out) * D);
+                    float dot = 0.0f;
+#pragma unroll 1
+                    for (int y = 0; y < D / 4; ++y) dot = dot4(__ldg(q + y), __ldg(kc + y), dot);
+                    e = ex2_approx(dot * __ldg(p.k_scale + at) * p.scale_log2 - m) * (__ldg(p.v_scale + at) * (1.0f / kLoudUnit));
+                }
+                __syncwarp();
+                // (a row that does not see the key keeps what it has)
+                update([&](int y, float o) {
+                    const uint32_t codes = __ldg(vc + y / 4);
+                    const float2 v = f16x2_to_float2(y & 2 ? f16x2_of_hi(codes) : f16x2_of_lo(codes));
+                    return e == 0.0f ? o : fmaf(e, y & 1 ? v.y : v.x, o);
+                });
+            }
+        }
+    }
+}
 
 template <class Cfg, bool DIRECT>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
@@ -472,7 +528,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             mbar_init(&bars->k_empty[s], w.pair ? 2 : 1);
             mbar_init(&bars->sc_full[s], 1);
             mbar_init(&bars->vs_ready[s], 128);
-            for (int x = 0; x < 4; ++x) bars->poison[s][x] = 0;
+            for (int x = 0; x < 4; ++x) {
+                bars->poison[s][x] = 0;
+                if (FP8) bars->poison[FP8 ? 8 + s : 0][x] = 0;
+            }
         }
         bars->abort_flag = 0;
         bars->turn = 0;
@@ -589,6 +648,18 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 const bool any = u < (w.pair ? max(w.n[0], w.n[1]) : t == 0 ? w.n[0] : w.n[1]);
                 return any && lane < boxes && key < w.len ? __ldg(w.table + (key >> p.page_shift)) : -1;
             };
+            if (FP8 && lane < NS) {
+                // (a stream that begins with a diagonal tile: see the converting warps)
+                const int key = (lane == 0 ? w.j0[0] : w.j0[1]) * BN;
+                float v = 0.0f;
+                if (key / BN >= diag && key < w.len) {
+                    const int page = __ldg(w.table + (key >> p.page_shift));
+                    if (page >= 0 && page < p.num_pages)
+                        v = __ldg(p.v_scale + (((static_cast<long long>(page) * p.H_kv + w.kvh) << p.page_shift) + (key & (ps - 1))));
+                }
+                bars->most[lane] = v < INFINITY ? 16.0f * v : 0.0f;
+            }
+            __syncwarp();
             int page0 = -1, page1 = -1, next0 = page_of(0, 0), next1 = NS > 1 && !w.pair ? page_of(1, 0) : -1;
             tile_entries<Cfg>(w, [&](int t, int u, bool is_v) -> bool {
                 const int key0 = ((t == 0 ? w.j0[0] : w.j0[1]) + u) * BN;
@@ -721,8 +792,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 // their maximum).  0 for keys that are not there (stale) and where
                 // only some query rows see a key with a NaN scale: those rows learn
                 // it from the poison bits, since a weight of 0 beside it must stay
-                // 0.  Every thread reaches the one barrier of a tile, whatever its
-                // waits say; all leave together.
+                // 0.  A scale that only some rows see must not move vref, in which the
+                // others' weights would vanish: its key is left out (loud), and the
+                // rows that see it add its values at the end.  In a stream's first
+                // tile vref may follow up to 16 times the scale of its first key,
+                // which every row sees that sees one of the stream's: that is still
+                // below it.  Every thread reaches the one barrier of a tile,
+                // whatever its waits say; all leave together.
                 bool ok = tile_wait(&bars->sc_full[slot], (e / Cfg::SLOTS) & 1, abort_flag, p, SITE_TILE_SCALE);
                 const uint32_t* valid = bars->valid[slot];
                 uint32_t all = valid[0] & valid[1];
@@ -733,9 +809,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 float v = 0.0f;
                 if (ct < BN && ((valid[ct >> 5] >> (ct & 31)) & 1u)) {
                     v = sScale[slot * 2 * BN + BN + ct];
-                    if (diagonal && key0 + ct >= diag_key && !(v < INFINITY)) {
-                        v = 0.0f;
-                        atomicOr(&poison[ct >> 5], 1u << (ct & 31));
+                    if (diagonal && key0 + ct >= diag_key) {
+                        const float ref = w.pair || t == 0 ? vref0 : vref1;
+                        const float most = fmaxf(64.0f * ref, bars->most[t]);
+                        if (!(v <= most)) {
+                            atomicOr(&poison[(v < INFINITY ? 32 : 0) + (ct >> 5)], 1u << (ct & 31));
+                            v = 0.0f;
+                        }
                     }
                 }
                 const uint32_t top = __reduce_max_sync(0xffffffffu, v > 0.0f && v < INFINITY ? __float_as_uint(v) : 0u);
@@ -758,8 +838,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 const uint8_t* src = sRaw + (e % NR) * Cfg::RAW_BYTES + r0 * D + c * 16;
                 uint8_t* dst = sRing + (e % NH) * Cfg::HALF_BYTES;
                 const float* vs = sScale + slot * 2 * BN + BN;
+                // (d < 256: two chunks at a time.  The kernel is at the limit of the
+                // instruction caches: a chunk of 512 queries over 8192 keys took 151 us
+                // with all eight unrolled, 139.6 with two.)
                 auto convert = [&](auto check) {
-#pragma unroll
+#pragma unroll (D == 256 ? BN / RPP : 2)
                     for (int i = 0; i < BN / RPP; ++i) {
                         const int r = r0 + i * RPP;
                         uint4 v = *reinterpret_cast<const uint4*>(src + i * RPP * D);
@@ -1122,6 +1205,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         const uint32_t bits = bars->poison[min(x - diag, Cfg::DIAG_TILES - 1)][c];
                         if (bits & (n == 32 ? 0xffffffffu : (1u << n) - 1u)) l = __uint_as_float(0x7fc00000u);
                     }
+                }
+            }
+            if constexpr (FP8) {
+                // (rare) Values that were left out of the products; l has their weights.
+                bool any = false;
+                for (int x = max(diag, j0); x < j0 + nt; ++x)
+#pragma unroll
+                    for (int c = 0; c < BN / 32; ++c) any |= bars->poison[FP8 ? 8 + min(x - diag, Cfg::DIAG_TILES - 1) : 0][c] != 0;
+                if (any) {
+                    add_loud<Cfg>(p, w.table, w.kvh, bars->poison + 8, diag, max(diag, j0), j0 + nt, in ? limit : 0, out, m, vref, o_tmem);
+                    vref = kLoudUnit;
                 }
             }
             float inv = (l == 0.0f ? 0.0f : 1.0f / l) * (FP8 ? vref : 1.0f);

@@ -428,19 +428,19 @@ int attn_kv_read(const void* k_cache, const void* v_cache, const float* k_scale,
  * O = 0 and LSE = -inf.  A page index outside the cache hides its tokens
  * (recorded); a length is cut as in attn_kv_read.  Cache rows that are not
  * visible to a query row (past the length, or behind the causal limit) do not
- * reach it whatever they hold, NaN included (but see Precision for the V scales
- * of an e4m3 cache behind the causal limit).  A bf16 V row with an infinity or a
- * NaN among the own tokens that not every query sees (the last Nq - 1 under
- * the causal mask) makes the whole O row and the LSE of the queries that do see
- * it NaN; likewise an e4m3 V row with a NaN code or a scale that is not finite.
+ * reach it whatever they hold, NaN and scales of any size included.  A bf16 V row
+ * with an infinity or a NaN among the own tokens that not every query sees (the last
+ * Nq - 1 under the causal mask) makes the whole O row and the LSE of the queries
+ * that do see it NaN; likewise an e4m3 V row with a NaN code or a scale that is not
+ * finite.
  * Precision: scores and sums are float32.  bf16 cache: the weights are rounded
  * to bf16 (2^-8) for the product with V, as in attn_fwd.  e4m3 cache: q and the
  * codes enter the products exactly, but for elements of q below 2^-9 of the
  * largest of their row, which may be rounded, by 2^-17 of it at most, and the
  * products with K's scales stay finite for scales below 2^90; weights and scaled
  * V rows are rounded to fp16 (2^-11 each, three roundings at most), and where a V
- * row's scale is below 2^-18 of the largest V scale among the own tokens, or those
- * of the prefix, by up to 2^-29 of that.
+ * row's scale is below 2^-14 of the largest V scale that the query sees among the
+ * own tokens, or those of the prefix, by up to 2^-25 of that.
  * The workspace size depends on its arguments alone.  prefix_len, max_pages
  * and the launches are the host's: a captured graph replays them with new
  * table entries, lengths, queries and cache contents.  Errors: before any

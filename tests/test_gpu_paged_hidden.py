@@ -48,12 +48,6 @@ FAR = [
 ]
 
 
-def streamed(s):
-    """Whether few rows of a key/value head, which the streaming kernel takes."""
-    lens, Nq, H, hkv, d, back = s
-    return Nq * (H // hkv) <= 32
-
-
 def shape_id(s):
     return f"{s[1]}x{s[2]}x{s[4]}_{s[5]}"
 
@@ -151,7 +145,7 @@ def test_a_value_row_that_every_query_sees_stays_in_its_columns(shape, fp8):
 
 
 @pytest.mark.parametrize("exponent", [20, 60])
-@pytest.mark.parametrize("shape", [x for x in NEAR + FAR if streamed(x)], ids=shape_id)
+@pytest.mark.parametrize("shape", NEAR + FAR, ids=shape_id)
 def test_a_large_value_scale_reaches_only_the_queries_that_see_it(shape, exponent):
     """e4m3: a row's values may be 2^20 or 2^60 times the others'.  Queries before it
     keep every bit; the others have it, and LSE is the same for all."""
@@ -188,10 +182,10 @@ def check_against_scaled_values(p, exponents, o, lse):
         want, wl, spread, size = ref.attend(p.q[b].double(), k, v, sees)
         to, tl = ref.tolerances(want, wl, spread, size, p.d)
         for i in range(p.Nq):
-            # weights or ratios of scales that fp16 rounds to a multiple of 2^-24, 2^-29
-            # of the largest that the query sees at most, for each of its keys
+            # weights or ratios of scales that fp16 rounds to a multiple of 2^-24, off
+            # by 2^-25 of the largest that the query sees at most, for each of its keys
             if sees[i]:
-                to[i] += sees[i] * 2.0 ** -29 * float(v[:sees[i]].abs().max())
+                to[i] += sees[i] * 2.0 ** -25 * float(v[:sees[i]].abs().max())
         assert bool(((o[b].double() - want).abs() <= to).all()), b
         seen = torch.isfinite(wl)
         assert bool(((lse[b].double() - wl).abs()[seen] <= tl[seen]).all()), b
@@ -216,7 +210,7 @@ def check_random_scales(shape, back):
 
 
 @pytest.mark.parametrize("back", [-1, 3, 40])
-@pytest.mark.parametrize("shape", [x for x in NEAR + FAR if streamed(x)] + [([9, 3], 12, 2, 1, 128, 1), ([20, 1], 32, 1, 1, 64, 1)],
+@pytest.mark.parametrize("shape", NEAR + FAR + [([9, 3], 12, 2, 1, 128, 1), ([20, 1], 32, 1, 1, 64, 1), ([60, 130], 129, 2, 2, 128, 1)],
                          ids=shape_id)
 def test_value_scales_of_the_last_tokens_from_2_to_the_minus_30_to_2_to_the_60(shape, back):
     """Each query against the plain form over the keys that it sees: from the second
