@@ -99,6 +99,8 @@ def library() -> ctypes.CDLL:
         L.attn_kv_read.restype = i
         L.attn_fwd_paged_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
         L.attn_fwd_paged_workspace_size.restype = sz
+        L.attn_fwd_paged_plan.argtypes = [i, i, i, i, i, i, i, i, P, i]
+        L.attn_fwd_paged_plan.restype = i
         L.attn_fwd_paged.argtypes = [P, P, P, P, P, P, i, P, i64, i, P, P, P, i, i, i, i, i, i, i, i, i, f, P, sz, P]
         L.attn_fwd_paged.restype = i
         _lib = L
@@ -659,6 +661,32 @@ def attn_kv_read(cache: KVCache, block_table, seq_lens, N: int, out_k=None, out_
 def paged_workspace_bytes(B: int, Nq: int, H: int, H_kv: int, d: int, prefix_len: int, max_pages: int,
                           page_size: int) -> int:
     return int(library().attn_fwd_paged_workspace_size(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size))
+
+
+class PagedPlan(NamedTuple):
+    """How attn_fwd_paged cuts up a call: the kernel ("stream", "tile" or None) of the
+    prefix and of the own tokens, their key ranges, the query rows of a streaming
+    CTA, the 128-row tiles of a key/value head in the tile kernel, and whether the
+    one range there is is written without a join."""
+    prefix_kernel: str | None
+    own_kernel: str
+    prefix_parts: int
+    own_parts: int
+    stream_rows: int
+    prefix_row_tiles: int
+    own_row_tiles: int
+    direct: bool
+
+
+def paged_plan(B: int, Nq: int, H: int, H_kv: int, d: int, prefix_len: int, max_pages: int,
+               page_size: int) -> PagedPlan | None:
+    """Host only: the plan of a call of these sizes; None for empty or refused ones."""
+    buf = (ctypes.c_int * 8)()
+    if library().attn_fwd_paged_plan(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size,
+                                     ctypes.cast(buf, ctypes.c_void_p), 8) != 8:
+        return None
+    kernels = (None, "stream", "tile")
+    return PagedPlan(kernels[buf[0]], kernels[buf[1]], *buf[2:7], bool(buf[7]))
 
 
 def _paged_buffers(out, lse, workspace, need, B, Nq, H, d, dev):

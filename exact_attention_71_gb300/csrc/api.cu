@@ -1099,6 +1099,24 @@ size_t attn_fwd_paged_workspace_size(int B, int Nq, int H, int H_kv, int d, int 
     return attn::paged_plan(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size).bytes;
 }
 
+int attn_fwd_paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size, int* out,
+                        int capacity) {
+    if (!out || capacity < 8) return 0;
+    if (check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size) != ATTN_OK) return 0;
+    if (static_cast<long long>(B) * Nq * H == 0) return 0;
+    const attn::PagedPlan plan = attn::paged_plan(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size);
+    const long long rows = static_cast<long long>(Nq) * (H / H_kv);
+    out[0] = plan.prefix_items > 0 ? 2 : plan.prefix_stream ? 1 : 0;
+    out[1] = plan.own_items > 0 ? 2 : 1;
+    out[2] = plan.prefix_parts;
+    out[3] = plan.own_parts;
+    out[4] = out[0] == 1 || out[1] == 1 ? plan.stream_tile : 0;
+    out[5] = out[0] == 2 ? static_cast<int>((B * rows + 127) / 128) : 0;
+    out[6] = out[1] == 2 ? static_cast<int>((rows + 127) / 128) : 0;
+    out[7] = plan.direct ? 1 : 0;
+    return 8;
+}
+
 int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
                    const int* prefix_table, int prefix_len, const int* block_table, long long table_stride,
                    int max_pages, const int* seq_lens, void* o, float* lse, int B, int Nq, int H, int H_kv, int d,

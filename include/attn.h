@@ -496,6 +496,23 @@ int attn_set_wait_limit(unsigned long long cycles);
  */
 int attn_fwd_work_order(int n_mblocks, int BH, int grid, unsigned int* out, int capacity);
 
+/*
+ * attn_fwd_paged_plan -- how attn_fwd_paged cuts up a call of these sizes; host
+ * code only, no GPU needed (inspection and testing).
+ *   out : HOST array of `capacity` >= 8 ints:
+ *         [0], [1]  the kernel of the prefix and that of the own tokens: 0 none, 1
+ *                   streaming (few query rows), 2 tiles (tcgen05)
+ *         [2], [3]  key ranges of the prefix and of a sequence's own tokens
+ *         [4]       query rows of a streaming CTA (8 or 16; 0 without one)
+ *         [5], [6]  tiles of 128 query rows of a key/value head over the prefix and
+ *                   over a sequence's own tokens (tile kernel; else 0)
+ *         [7]       1: one range in all, written to o and lse without a join
+ * Returns 8, or 0 for sizes that attn_fwd_paged refuses, for empty problems, or
+ * when `capacity` is too small.
+ */
+int attn_fwd_paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages,
+                        int page_size, int* out, int capacity);
+
 /* Text of the last error of the calling thread ("" if none). */
 const char* attn_last_error_string(void);
 

@@ -1,0 +1,92 @@
+"""The paged attention in the modes that the shapes of test_gpu_paged.py leave out
+(tests/test_paged_plan_cpu.py derives which there are): one range written without
+a join, by either kernel; 16-row streaming CTAs at head dim 256; several row tiles
+of head dim 256 over own tokens in ranges, one of head dim 64 over a prefix."""
+import pytest
+import torch
+
+from exact_attention_71_gb300 import api
+from tests.test_gpu_paged import INF, NAN, Problem
+from tests.test_gpu_paged_hidden import check_row, write_value
+
+pytestmark = pytest.mark.gpu
+
+MODES = [
+    # lens, prefix, Nq, H, H_kv, d, page
+    # tile kernel, written without a join: two row tiles, one, an odd number of them
+    ([100, 90], 0, 80, 2, 1, 64, 16),
+    ([100, 0, 61], 0, 60, 2, 2, 64, 32),
+    ([100, 90], 0, 80, 2, 1, 128, 16),
+    ([100, 0, 61], 0, 60, 2, 2, 128, 32),
+    ([110, 97], 0, 100, 3, 1, 128, 16),
+    ([44, 33], 0, 80, 2, 1, 256, 16),
+    ([40, 0, 17], 0, 20, 2, 2, 256, 16),
+    # the same over several key tiles
+    ([300] * 9 + [131], 0, 64, 32, 8, 128, 16),
+    ([300] * 19 + [77], 0, 40, 8, 8, 128, 16),
+    ([300] * 19 + [77], 0, 20, 8, 8, 256, 16),
+    ([300] * 19 + [77], 0, 40, 8, 8, 64, 16),
+    # streaming kernel, written without a join
+    ([100, 3, 0], 0, 1, 2, 1, 256, 64),
+    ([100, 90], 0, 12, 2, 2, 64, 16),
+    ([100, 90], 0, 3, 16, 4, 128, 16),
+    ([100, 3], 0, 12, 2, 2, 256, 64),
+    # 16-row CTAs at d = 256, over the prefix and over own tokens, some and many ranges
+    ([300], 100, 12, 2, 2, 256, 64),
+    ([3000], 1500, 5, 6, 2, 256, 128),
+    ([300, 90], 100, 12, 2, 2, 256, 64),
+    # two row tiles of d = 256 over own tokens in ranges, one of d = 64 over a prefix
+    ([200, 133], 0, 80, 2, 1, 256, 16),
+    ([40, 90], 500, 20, 4, 2, 64, 16),
+]
+
+
+def plan(shape):
+    lens, prefix, Nq, H, hkv, d, ps = shape
+    per = max(1, -(-max(lens + [1]) // ps)) + 1                # (pages of a row of Problem's table)
+    return api.paged_plan(len(lens), Nq, H, hkv, d, prefix, per, ps)
+
+
+def shape_id(s):
+    return "x".join(map(str, s[1:])) + "_" + str(len(s[0]))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("shape", MODES, ids=shape_id)
+def test_attention_matches_the_plain_form(shape, fp8):
+    p = Problem(*shape, fp8=fp8, seed=61)
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("shape", MODES[:7] + MODES[11:16], ids=shape_id)
+def test_without_the_causal_mask_every_own_key_is_seen(shape, fp8):
+    p = Problem(*shape, fp8=fp8, seed=62)
+    p.check(*p.run(causal=False), causal=False)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("shape, back", [
+    (([260, 140] * 5, 0, 130, 32, 8, 128, 16), 60), (([260, 140] * 5, 0, 130, 32, 8, 64, 16), 100),
+    (([100, 130] * 10, 0, 96, 16, 8, 256, 16), 70), (([90, 100], 0, 60, 4, 4, 128, 16), 20), (([60, 90], 0, 8, 4, 2, 256, 32), 5),
+    (([60, 90], 0, 16, 4, 2, 64, 32), 12),
+], ids=lambda x: str(x) if isinstance(x, int) else shape_id(x))
+def test_rows_that_see_a_value_row_that_is_not_finite_are_written_as_nan(shape, back, fp8):
+    assert plan(shape).direct
+    p = Problem(*shape, fp8=fp8, seed=63)
+    before = p.run()
+    check_row(p, back, before, lambda b, at: write_value(p, b, at, NAN if b % 2 == 0 else -INF))
+    assert api.device_status()[0] == 0
+
+
+@pytest.mark.parametrize("shape", [MODES[2], MODES[4], MODES[11], MODES[15]], ids=shape_id)
+def test_outputs_around_the_result_are_left_alone(shape):
+    """o and lse inside larger buffers: nothing before or behind them is written."""
+    p = Problem(*shape, fp8=True, seed=64)
+    want = p.run()
+    room = [torch.full((x.numel() + 256,), 7.0, dtype=x.dtype, device=x.device) for x in want]
+    got = [r[128:-128].view(x.shape) for r, x in zip(room, want)]
+    p.run(out=got[0], lse=got[1])
+    for r, g, x in zip(room, got, want):
+        assert torch.equal(g, x)
+        assert bool((r[:128] == 7.0).all()) and bool((r[-128:] == 7.0).all())

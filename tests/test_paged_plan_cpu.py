@@ -1,0 +1,63 @@
+"""How paged attention calls are cut up (host arithmetic), and that the GPU tests'
+shapes between them reach every kernel in every mode."""
+import ctypes
+
+import pytest
+
+from exact_attention_71_gb300 import api, build
+from tests import test_gpu_paged as paged
+from tests import test_gpu_paged_modes as modes
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return api.library()
+
+
+def modes_of(shape):
+    """(head dim, kernel, rows of a streaming CTA or one / several row tiles, segment,
+    written without a join) of a call."""
+    p, d, out = modes.plan(shape), shape[5], set()
+    for segment, kernel, tiles in (("prefix", p.prefix_kernel, p.prefix_row_tiles), ("own", p.own_kernel, p.own_row_tiles)):
+        if kernel == "stream":
+            out.add((d, kernel, p.stream_rows, segment, p.direct))
+        elif kernel == "tile":
+            out.add((d, kernel, "one" if tiles == 1 else "several", segment, p.direct))
+    return out
+
+
+def test_the_gpu_tests_reach_every_kernel_in_every_mode():
+    want = {(d, kernel, rows, segment, direct)
+            for d in (64, 128, 256)
+            for kernel, all_rows in (("stream", (8, 16)), ("tile", ("one", "several")))
+            for rows in all_rows
+            for segment, direct in (("prefix", False), ("own", False), ("own", True))}
+    have = set().union(*map(modes_of, paged.SHAPES + modes.MODES))
+    assert want <= have, sorted(map(str, want - have))
+
+
+def test_many_ranges_are_joined():
+    parts = {p.prefix_parts + p.own_parts for p in map(modes.plan, paged.SHAPES + modes.MODES)}
+    assert any(n > 128 for n in parts) and any(32 < n <= 128 for n in parts) and 2 in parts
+
+
+def test_plan_and_workspace_agree():
+    up = lambda x: (x + 255) // 256 * 256
+    for shape in paged.SHAPES + modes.MODES:
+        lens, prefix, Nq, H, hkv, d, ps = shape
+        args = (len(lens), Nq, H, hkv, d, prefix, max(1, -(-max(lens + [1]) // ps)) + 1, ps)
+        p = api.paged_plan(*args)
+        n = (p.prefix_parts + p.own_parts) * len(lens) * Nq * H
+        assert p.direct == (p.prefix_parts + p.own_parts == 1)
+        assert api.paged_workspace_bytes(*args) == (0 if p.direct else up(n * d * 4) + up(n * 4))
+
+
+def test_refused_sizes_have_no_plan(lib):
+    assert api.paged_plan(0, 1, 4, 2, 64, 0, 1, 16) is None
+    assert api.paged_plan(1, 1, 3, 2, 64, 0, 1, 16) is None
+    assert api.paged_plan(1, 1, 4, 2, 96, 0, 1, 16) is None
+    assert api.paged_plan(1, 1, 4, 2, 64, -1, 1, 16) is None
+    buf = (ctypes.c_int * 8)()
+    assert lib.attn_fwd_paged_plan(1, 1, 4, 2, 64, 0, 1, 16, ctypes.cast(buf, ctypes.c_void_p), 7) == 0
+    assert lib.attn_fwd_paged_plan(1, 1, 4, 2, 64, 0, 1, 16, None, 8) == 0
