@@ -991,7 +991,9 @@ int check_table(const int* table, long long table_stride, int max_pages, int pag
     return ATTN_OK;
 }
 
-int check_paged_sizes(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size) {
+// Sizes of an attention call, and its plan (empty problems: as it is).
+int check_paged_sizes(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size,
+                      attn::PagedPlan* plan) {
     if (B < 0 || Nq < 0 || H < 0 || prefix_len < 0 || max_pages < 0)
         return fail(ATTN_ERR_INVALID_ARG, "negative size (B=%d Nq=%d H=%d prefix_len=%d max_pages=%d)", B, Nq, H,
                     prefix_len, max_pages);
@@ -1002,11 +1004,12 @@ int check_paged_sizes(int B, int Nq, int H, int H_kv, int d, int prefix_len, int
         return fail(ATTN_ERR_UNSUPPORTED, "page_size %d (supported: 16, 32, 64, 128, 256)", page_size);
     if (prefix_len > kMaxKeys || static_cast<long long>(max_pages) * page_size > kMaxKeys)
         return fail(ATTN_ERR_INVALID_ARG, "more than 2^30 tokens in a prefix or a page table");
-    // Row indices are ints with headroom for the last tile, B a grid dimension
-    // of at most 65535.  (Row tiles x heads x parts then stay below 2^31: there
-    // are several parts only where there are fewer than 1216 tiles.)
-    if (B > 65535 || static_cast<long long>(B) * Nq > (1ll << 30) || static_cast<long long>(B) * Nq * H > (1ll << 30))
+    // Row indices are ints with headroom for the last tile.  CTAs are counted in
+    // long long by the plan: their indices are ints too.
+    if (static_cast<long long>(B) * Nq > (1ll << 30) || static_cast<long long>(B) * Nq * std::max(H, 1) > (1ll << 30))
         return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
+    if (static_cast<long long>(B) * Nq * H > 0) *plan = attn::paged_plan(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size);
+    if (plan->blocks > 0x7fffffffll) return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
     return ATTN_OK;
 }
 
@@ -1094,17 +1097,16 @@ int attn_kv_read(const void* k_cache, const void* v_cache, const float* k_scale,
 
 size_t attn_fwd_paged_workspace_size(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages,
                                      int page_size) {
-    if (check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size) != ATTN_OK) return 0;
-    if (static_cast<long long>(B) * Nq * H == 0) return 0;
-    return attn::paged_plan(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size).bytes;
+    attn::PagedPlan plan;
+    return check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan) == ATTN_OK ? plan.bytes : 0;
 }
 
 int attn_fwd_paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size, int* out,
                         int capacity) {
     if (!out || capacity < 8) return 0;
-    if (check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size) != ATTN_OK) return 0;
+    attn::PagedPlan plan;
+    if (check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan) != ATTN_OK) return 0;
     if (static_cast<long long>(B) * Nq * H == 0) return 0;
-    const attn::PagedPlan plan = attn::paged_plan(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size);
     const long long rows = static_cast<long long>(Nq) * (H / H_kv);
     out[0] = plan.prefix_items > 0 ? 2 : plan.prefix_stream ? 1 : 0;
     out[1] = plan.own_items > 0 ? 2 : 1;
@@ -1125,7 +1127,8 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
     g_err[0] = '\0';
     int rc = check_cache(k_cache, v_cache, k_scale, v_scale, H_kv, d, num_pages, page_size, cache_dtype);
     if (rc != ATTN_OK) return rc;
-    if ((rc = check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size)) != ATTN_OK) return rc;
+    attn::PagedPlan plan;
+    if ((rc = check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan)) != ATTN_OK) return rc;
     if (static_cast<long long>(B) * Nq * H == 0) return ATTN_OK;
     if ((rc = check_table(block_table, table_stride, max_pages, page_size, seq_lens)) != ATTN_OK) return rc;
     if (!q || !o || !lse || (prefix_len > 0 && !prefix_table)) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
@@ -1133,7 +1136,6 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
         return fail(ATTN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
     if ((reinterpret_cast<uintptr_t>(prefix_table) & 3u) != 0)
         return fail(ATTN_ERR_INVALID_ARG, "page tables and lengths must be 4-byte aligned");
-    const attn::PagedPlan plan = attn::paged_plan(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size);
     if (plan.bytes > 0) {
         if (!workspace) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
         if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)

@@ -122,6 +122,7 @@ struct PagedPlan {
     bool prefix_stream = false;  // the streaming kernel has the prefix
     int stream_tile = 8;         // query rows of a streaming CTA
     bool direct = false;         // one part in all: the kernel writes o and lse itself
+    long long blocks = 0;        // CTAs of the larger launch (an entry refuses 2^31 or more)
     size_t part_o_bytes = 0, bytes = 0;
 };
 

@@ -94,14 +94,17 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     // Steps of a CTA over `keys`: two streams halve the tiles of a single row tile.
     const auto steps_of = [&](long long keys, long long tiles) { return up(keys, bn * (d != 256 && tiles == 1 ? 2 : 1)); };
     double streaming = 0.0;                                              // SM-microseconds
+    long long tile_items = 0, stream_blocks = 0;
     if (!own_stream) {
         const long long tiles = up(rows, 128), groups = d == 256 ? tiles : up(tiles, 2);
         plan.own_ctas = tile_ctas(d, B * static_cast<long long>(H_kv) * groups, steps_of(own, tiles), 0.0);
-        plan.own_items = static_cast<int>(B * static_cast<long long>(H_kv) * groups * plan.own_ctas);
+        tile_items = B * static_cast<long long>(H_kv) * groups * plan.own_ctas;
+        plan.own_items = static_cast<int>(tile_items);
         plan.own_parts = plan.own_ctas;
     } else {
         const long long units = B * static_cast<long long>(H_kv) * up(rows, plan.stream_tile);
         plan.own_parts = stream_parts(own, units);
+        stream_blocks = units * plan.own_parts;
         // (sequences fill three quarters of their tables, say; a key of one head
         // takes an SM 0.08 d nanoseconds)
         streaming = 0.75 * static_cast<double>(units) * static_cast<double>(own) * 0.08e-3 * d;
@@ -111,11 +114,15 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
             const long long tiles = up(all, 128), groups = d == 256 ? tiles : up(tiles, 2);
             plan.prefix_ctas = tile_ctas(d, H_kv * groups, steps_of(prefix_len, tiles), streaming);
             plan.prefix_items = static_cast<int>(H_kv * groups * plan.prefix_ctas);
+            tile_items += H_kv * groups * plan.prefix_ctas;
             plan.prefix_parts = plan.prefix_ctas;
         } else {
-            plan.prefix_parts = stream_parts(prefix_len, H_kv * up(all, plan.stream_tile));
+            const long long units = H_kv * up(all, plan.stream_tile);
+            plan.prefix_parts = stream_parts(prefix_len, units);
+            stream_blocks += units * plan.prefix_parts;
         }
     }
+    plan.blocks = std::max(tile_items, stream_blocks);
     const int parts = plan.prefix_parts + plan.own_parts;
     plan.direct = parts == 1;
     if (!plan.direct) {

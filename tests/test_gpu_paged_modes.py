@@ -2,6 +2,8 @@
 (tests/test_paged_plan_cpu.py derives which there are): one range written without
 a join, by either kernel; 16-row streaming CTAs at head dim 256; several row tiles
 of head dim 256 over own tokens in ranges, one of head dim 64 over a prefix."""
+import math
+
 import pytest
 import torch
 
@@ -90,3 +92,33 @@ def test_outputs_around_the_result_are_left_alone(shape):
     for r, g, x in zip(room, got, want):
         assert torch.equal(g, x)
         assert bool((r[:128] == 7.0).all()) and bool((r[-128:] == 7.0).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("prefix", [0, 16])
+def test_more_sequences_than_a_grid_dimension_has(prefix, fp8):
+    """70000 sequences of one token each (of its own: every result is that token's
+    values, behind a prefix of another page: of the two)."""
+    B, d = 70000, 64
+    cache = api.kv_cache(B + 1, 16, 1, d, e4m3=fp8)
+    g = torch.Generator(device="cuda").manual_seed(71)
+    x = torch.randn((B, 1, d), generator=g, device="cuda").to(torch.bfloat16)
+    api.attn_kv_write(x, x, torch.arange(B, device="cuda") * 16, cache)
+    table = torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous()
+    lens = torch.ones(B, dtype=torch.int32, device="cuda")
+    own = api.attn_kv_read(cache, table[:60000], lens[:60000], 1)[1][:, 0]
+    if prefix:           # a page of zeros: 16 more keys with score 0 and value 0
+        pages = torch.full((1,), B, dtype=torch.int32, device="cuda")
+        q = torch.zeros((B, 1, 1, d), dtype=torch.bfloat16, device="cuda")
+        o, lse = api.attn_fwd_paged(q, cache, table, lens, pages, prefix)
+        want = own.double() / 17
+        assert bool(((lse.double() - math.log(17.0)).abs() <= 2.0 ** -18).all())
+    else:
+        o, lse = api.attn_fwd_paged(x[:, None], cache, table, lens)
+        want = own.double()
+    assert api.device_status()[0] == 0
+    # one weight of 1 (or 17 equal ones): values of the cache as they are, two
+    # roundings to fp16 on the way at most and one to bf16; read back, one to bf16
+    tol = 2 * 2.0 ** -8 + 2 * 2.0 ** -11 + 2.0 ** -20
+    assert bool(((o[:60000, 0].double() - want).abs() <= tol * want.abs() + 1e-30).all())
+    assert bool((o[60000:].float().abs().amax(-1) > 0).all())

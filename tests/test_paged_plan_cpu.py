@@ -61,3 +61,50 @@ def test_refused_sizes_have_no_plan(lib):
     buf = (ctypes.c_int * 8)()
     assert lib.attn_fwd_paged_plan(1, 1, 4, 2, 64, 0, 1, 16, ctypes.cast(buf, ctypes.c_void_p), 7) == 0
     assert lib.attn_fwd_paged_plan(1, 1, 4, 2, 64, 0, 1, 16, None, 8) == 0
+
+
+def ctas(args):
+    """CTAs of a call's two launches, from its plan."""
+    B, Nq, H, hkv, d, prefix, pages, ps = args
+    p = api.paged_plan(*args)
+    if p is None:
+        return None
+    up = lambda a, b: -(-a // b)
+    groups = lambda tiles: tiles if d == 256 else up(tiles, 2)
+    rows = Nq * (H // hkv)
+    tile = stream = 0
+    if p.prefix_kernel == "tile":
+        tile += hkv * groups(p.prefix_row_tiles) * p.prefix_parts
+    elif p.prefix_kernel == "stream":
+        stream += hkv * up(B * rows, p.stream_rows) * p.prefix_parts
+    if p.own_kernel == "tile":
+        tile += B * hkv * groups(p.own_row_tiles) * p.own_parts
+    else:
+        stream += B * hkv * up(rows, p.stream_rows) * p.own_parts
+    return max(tile, stream)
+
+
+def test_large_problems_have_fewer_than_2_to_the_31_ctas():
+    """Block indices are ints: the sizes that are accepted stay below, with many
+    ranges and many sequences together."""
+    most = 0
+    for d in (64, 128, 256):
+        for log_b in range(0, 31, 2):
+            for hkv in (1, 8, 1 << 10):
+                for Nq, group in ((1, 1), (1, 8), (5, 4), (64, 4), (512, 1)):
+                    for prefix, pages in ((0, 1), (0, 1 << 22), (1 << 30, 1 << 22), (1 << 20, 1 << 10)):
+                        n = ctas((1 << log_b, Nq, hkv * group, hkv, d, prefix, pages, 256))
+                        if n is not None:
+                            most = max(most, n)
+                            assert n < 1 << 31
+    assert most > 1 << 28                              # (the largest accepted ones are among these)
+
+
+def test_more_sequences_than_a_grid_dimension_has(lib):
+    """The attention's grids have one dimension; reading back is a grid row a
+    sequence, and says so."""
+    assert api.paged_plan(70000, 1, 1, 1, 64, 0, 1, 16) is not None
+    fake = ctypes.c_void_p(1 << 20)
+    assert lib.attn_kv_read(fake, fake, fake, fake, fake, 4, 4, fake, fake, fake, 70000, 5, 1, 64, 10, 16, 1, None) == -1
+    assert b"too large" in lib.attn_last_error_string()
+    assert api.paged_plan(1 << 30, 2, 1, 1, 64, 0, 1, 16) is None
