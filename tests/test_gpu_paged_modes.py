@@ -122,3 +122,38 @@ def test_more_sequences_than_a_grid_dimension_has(prefix, fp8):
     tol = 2 * 2.0 ** -8 + 2 * 2.0 ** -11 + 2.0 ** -20
     assert bool(((o[:60000, 0].double() - want).abs() <= tol * want.abs() + 1e-30).all())
     assert bool((o[60000:].float().abs().amax(-1) > 0).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kernel, B, N, Nq, sites", [("stream", 48, 8192, 1, (0xb1,)),
+                                                     ("tile", 2, 2048, 90, tuple(range(0xa1, 0xac)))])
+def test_a_wait_that_runs_out_is_reported_by_its_kernel(kernel, B, N, Nq, sites, fp8):
+    """With a limit of one cycle the first hardware wait that ends without its copy (or
+    product) gives up: the call is reported, by a site of the kernel that has all of
+    its work, and the next one is right.  (Hardware waits last some microseconds: it
+    takes a cache of a gigabyte for a copy of the streaming kernel to be that late.)"""
+    H, hkv, d, ps = 32, 8, 128, 64
+    p = api.paged_plan(B, Nq, H, hkv, d, 0, N // ps, ps)
+    assert p.prefix_kernel is None and p.own_kernel == kernel
+    cache = api.kv_cache(B * N // ps, ps, hkv, d, e4m3=fp8)
+    g = torch.Generator(device="cuda").manual_seed(65)
+    for t in cache[:2]:
+        if fp8:
+            t.random_(0, 0x70, generator=g)
+        else:
+            t.normal_(generator=g)
+    q = torch.randn((B, Nq, H, d), generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.arange(B * N // ps, dtype=torch.int32, device="cuda").view(B, -1)
+    lens = torch.full((B,), N, dtype=torch.int32, device="cuda")
+    want = api.attn_fwd_paged(q, cache, table, lens)
+    assert api.device_status()[0] == 0
+    assert api.library().attn_set_wait_limit(1) == 0
+    try:
+        api.attn_fwd_paged(q, cache, table, lens)
+        rc, site = api.device_status()
+    finally:
+        api.library().attn_set_wait_limit(0)
+    assert rc == -4 and site in sites, (rc, hex(site))
+    got = api.attn_fwd_paged(q, cache, table, lens)
+    assert api.device_status()[0] == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
