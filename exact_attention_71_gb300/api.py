@@ -577,23 +577,36 @@ def _check_table(block_table, seq_lens, B, dev):
     return max_pages, stride
 
 
-# Entries of torch that may go away; without them the public ones are called (an
-# attention call of 19 us on the host then takes 26: the dispatcher's part of a
-# torch.empty costs more than the allocation).
+# Entries of torch that are not public and may go away or change; without them the
+# public ones are called (an attention call of 19 us on the host then takes 26: the
+# dispatcher's part of a torch.empty costs more than the allocation).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _raw_empty = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_watchers = [getattr(torch._C, n, None) for n in ("_len_torch_dispatch_stack", "_len_torch_function_stack")]
+
+
+def _unwatched() -> bool:
+    """Whether nothing is to see or fill the memory that is allocated: no dispatch or
+    function mode is active, and torch fills no uninitialised memory."""
+    try:
+        return not torch.are_deterministic_algorithms_enabled() and not any(n() for n in _watchers)
+    except TypeError:
+        return False
+
+
+def _current_raw_stream(dev: int) -> int:
+    if _raw_stream is not None:
+        try:
+            return _raw_stream(dev)
+        except TypeError:
+            pass
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _launch(fn, name, dev, stream, args):
     """Calls entry `fn` with `args` and the stream, with device `dev` current."""
-    if stream is not None:
-        raw = _stream(stream)
-    elif _raw_stream is not None:
-        raw = _raw_stream(dev)
-    else:
-        raw = torch.cuda.current_stream(dev).cuda_stream
-    if _current_device() == dev:
+    raw = _current_raw_stream(dev) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev:
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -691,21 +704,24 @@ def paged_plan(B: int, Nq: int, H: int, H_kv: int, d: int, prefix_len: int, max_
 
 def _paged_buffers(out, lse, workspace, need, B, Nq, H, d, dev):
     """out, lse and a workspace of `need` bytes, allocated where they are None."""
-    if _raw_empty is not None and _current_device() == dev:
-        if out is None:
-            out = _raw_empty((B, Nq, H, d), (Nq * H * d, H * d, d, 1), _BF16)
-        if lse is None:
-            lse = _raw_empty((B, H, Nq), (H * Nq, Nq, 1), _F32)
-        if workspace is None and need:
-            workspace = _raw_empty((need,), (1,), _U8)
-    else:
-        device = torch.device("cuda", dev)
-        if out is None:
-            out = torch.empty((B, Nq, H, d), dtype=_BF16, device=device)
-        if lse is None:
-            lse = torch.empty((B, H, Nq), dtype=_F32, device=device)
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=_U8, device=device)
+    if _raw_empty is not None and torch.cuda.current_device() == dev and _unwatched():
+        try:
+            if out is None:
+                out = _raw_empty((B, Nq, H, d), (Nq * H * d, H * d, d, 1), _BF16)
+            if lse is None:
+                lse = _raw_empty((B, H, Nq), (H * Nq, Nq, 1), _F32)
+            if workspace is None and need:
+                workspace = _raw_empty((need,), (1,), _U8)
+            return out, lse, workspace
+        except TypeError:            # (another signature: the public way, below)
+            pass
+    device = torch.device("cuda", dev)
+    if out is None:
+        out = torch.empty((B, Nq, H, d), dtype=_BF16, device=device)
+    if lse is None:
+        lse = torch.empty((B, H, Nq), dtype=_F32, device=device)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=_U8, device=device)
     return out, lse, workspace
 
 

@@ -157,3 +157,57 @@ def test_a_wait_that_runs_out_is_reported_by_its_kernel(kernel, B, N, Nq, sites,
     got = api.attn_fwd_paged(q, cache, table, lens)
     assert api.device_status()[0] == 0
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_allocations_are_seen_by_modes_and_filled_where_torch_fills(monkeypatch):
+    """The binding's quick way to allocate is taken only where nobody could tell."""
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Seen(TorchDispatchMode):
+        def __init__(self):
+            super().__init__()
+            self.made = []
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            r = func(*args, **(kwargs or {}))
+            if "empty" in str(func):
+                self.made.append(tuple(r.shape))
+            return r
+
+    p = Problem([300, 77, 0], 900, 3, 8, 2, 128, 16, True, seed=66)
+    want = p.run()
+    with Seen() as mode:
+        got = p.run()
+    assert tuple(want[0].shape) in mode.made and tuple(want[1].shape) in mode.made and len(mode.made) == 3
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # (without the launch: what the outputs are allocated as)
+    monkeypatch.setattr(api, "_launch", lambda *args: None)
+    torch.use_deterministic_algorithms(True)
+    try:
+        o, lse = p.run()
+        assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
+    finally:
+        torch.use_deterministic_algorithms(False)
+
+
+@pytest.mark.parametrize("name", ["_raw_empty", "_raw_stream"])
+def test_a_changed_signature_of_a_private_entry_costs_time_only(monkeypatch, name):
+    p = Problem([300, 77, 0], 900, 3, 8, 2, 128, 16, True, seed=67)
+    want = p.run()
+    calls = []
+
+    def changed(*args):
+        calls.append(args)
+        raise TypeError("one more argument")
+
+    monkeypatch.setattr(api, name, changed)
+    got = p.run()
+    assert calls and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # a mode's entry that changed: the public way
+    monkeypatch.undo()
+    monkeypatch.setattr(api, "_watchers", [changed])
+    got = p.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    monkeypatch.setattr(api, "_watchers", [None])
+    got = p.run()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
