@@ -939,7 +939,8 @@ int check_cache(const void* k_cache, const void* v_cache, const float* k_scale, 
         if (cache_dtype == ATTN_CACHE_E4M3 && (!k_scale || !v_scale))
             return fail(ATTN_ERR_INVALID_ARG, "null scale pointer (an e4m3 cache has a scale per row)");
     }
-    if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_scale) || !aligned16(v_scale))
+    if (!aligned16(k_cache) || !aligned16(v_cache) ||
+        (cache_dtype == ATTN_CACHE_E4M3 && (!aligned16(k_scale) || !aligned16(v_scale))))
         return fail(ATTN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
     return ATTN_OK;
 }

@@ -108,3 +108,11 @@ def test_more_sequences_than_a_grid_dimension_has(lib):
     assert lib.attn_kv_read(fake, fake, fake, fake, fake, 4, 4, fake, fake, fake, 70000, 5, 1, 64, 10, 16, 1, None) == -1
     assert b"too large" in lib.attn_last_error_string()
     assert api.paged_plan(1 << 30, 2, 1, 1, 64, 0, 1, 16) is None
+
+
+def test_the_scales_of_a_bf16_cache_are_ignored(lib):
+    """Whatever their pointers are; those of an e4m3 cache have to be aligned."""
+    fake, odd = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 4)
+    write = lambda dtype: lib.attn_kv_write(fake, fake, 64, 64, fake, fake, fake, odd, odd, 0, 1, 64, 4, 16, dtype, None)
+    assert write(api.CACHE_BF16) == 0
+    assert write(api.CACHE_E4M3) == -1 and b"aligned" in lib.attn_last_error_string()
