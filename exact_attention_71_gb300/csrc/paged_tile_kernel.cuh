@@ -1345,10 +1345,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             // the poison bits do for keys that only some of the rows see, so that a
             // query's result does not depend on the CTA that has it.  All rows' O then
             // shows it; so the values are read again only if O is not finite in all of
-            // a warp's rows, and not by their scores alone.
-            if (take && !w.prefix && p.causal) {
-                const int lo = max(max(0, w.len - p.Nq + 1), j0 * BN);
-                const int hi = min(diag_key, (alt ? max(j0 + nt, w.j0[1] + w.n[1]) : j0 + nt) * BN);
+            // a warp's rows, and not by their scores alone.  (alt: the one row tile has
+            // the first query; there are no such keys.)
+            if (take && !alt && !w.prefix && p.causal) {
+                const int lo = max(max(0, w.len - p.Nq + 1), j0 * BN), hi = min(diag_key, (j0 + nt) * BN);
                 const bool odd = not_finite.x + not_finite.y != 0.0f, known = lse2 - lse2 == 0.0f;
                 if (lo < hi && __all_sync(0xffffffffu, !in || odd) && __any_sync(0xffffffffu, in && known) &&
                     v_rows_not_finite<Cfg>(p, w, lo, hi, lane)) {

@@ -217,3 +217,26 @@ def test_value_scales_of_the_last_tokens_from_2_to_the_minus_30_to_2_to_the_60(s
     query's key on, from some keys before, and with sequences shorter than the
     queries."""
     check_random_scales(shape, back)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("prefix", [0, 40])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_value_row_that_is_not_finite_counts_however_small_its_weight_is(d, prefix, fp8):
+    """One row tile, the keys in two halves: the second half's scores are 200 below the
+    first's, so that its weights are 0 in binary32.  Its infinity still makes the
+    queries that see it NaN."""
+    Nq, n, back = 60, 500, 40
+    p = Problem([n, n - 30], prefix, Nq, 1, 1, d, 16, fp8, seed=58)
+    p.q[..., 0] = 40.0
+    for b, ks in enumerate(p.k):
+        ks[..., 0] = 0.0
+        if b:
+            ks[len(ks) // 2:, :, 0] = -5.0 * d ** 0.5
+        t = p.prefix_table if b == 0 else p.table[b - 1]
+        at = torch.arange(len(ks), device=DEV)
+        if len(ks):
+            api.attn_kv_write(ks, p.v[b], t.long()[at // 16] * 16 + at % 16, p.cache)
+    before = p.run()
+    assert bool(torch.isfinite(before[0]).all())
+    check_row(p, back, before, lambda b, at: write_value(p, b, at, INF))
