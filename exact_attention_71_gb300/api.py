@@ -582,6 +582,8 @@ def _check_table(block_table, seq_lens, B, dev):
 # dispatcher's part of a torch.empty costs more than the allocation).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _raw_empty = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_fills = torch.are_deterministic_algorithms_enabled
 _watchers = [getattr(torch._C, n, None) for n in ("_len_torch_dispatch_stack", "_len_torch_function_stack")]
 
 
@@ -589,9 +591,12 @@ def _unwatched() -> bool:
     """Whether nothing is to see or fill the memory that is allocated: no dispatch or
     function mode is active, and torch fills no uninitialised memory."""
     try:
-        return not torch.are_deterministic_algorithms_enabled() and not any(n() for n in _watchers)
+        for active in _watchers:
+            if active():
+                return False
     except TypeError:
         return False
+    return not _fills()
 
 
 def _current_raw_stream(dev: int) -> int:
@@ -606,7 +611,7 @@ def _current_raw_stream(dev: int) -> int:
 def _launch(fn, name, dev, stream, args):
     """Calls entry `fn` with `args` and the stream, with device `dev` current."""
     raw = _current_raw_stream(dev) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         rc = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -704,7 +709,7 @@ def paged_plan(B: int, Nq: int, H: int, H_kv: int, d: int, prefix_len: int, max_
 
 def _paged_buffers(out, lse, workspace, need, B, Nq, H, d, dev):
     """out, lse and a workspace of `need` bytes, allocated where they are None."""
-    if _raw_empty is not None and torch.cuda.current_device() == dev and _unwatched():
+    if _raw_empty is not None and _current_device() == dev and _unwatched():
         try:
             if out is None:
                 out = _raw_empty((B, Nq, H, d), (Nq * H * d, H * d, d, 1), _BF16)
