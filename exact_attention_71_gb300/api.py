@@ -740,7 +740,8 @@ def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, 
     may be strided, e.g. a full table without its shared columns); seq_lens:
     int32 (B,), the own tokens; prefix_table: int32 (>= ceil(prefix_len /
     page_size),); prefix_len: host int.  causal: query i sees own keys j <=
-    seq_lens[b] - Nq + i (all of them otherwise), and the whole prefix.
+    seq_lens[b] - Nq + i (all of them otherwise), and the whole prefix; there is no
+    sliding window.
     workspace: optional uint8 CUDA tensor of at least paged_workspace_bytes(...)
     bytes, scratch.  out, lse and workspace that are not given are allocated on
     the launch's stream.  Returns (O (B, Nq, H, d) bf16, LSE (B, H, Nq) float32).

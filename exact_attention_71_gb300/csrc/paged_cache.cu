@@ -6,8 +6,8 @@
 // d / 16 lanes, each with eight elements of either half of the row (so that the
 // lanes of a load or a store instruction are next to one another); K and V of a row
 // go through the same thread, which keeps four independent loads in flight.
-// Measured, e4m3, 8 heads of 128: writing 32768 tokens 31.1 us, 6.6 TB/s (98 % of
-// the copy rate), reading 16 sequences of up to 8192 back 91.5 us, 6.7 TB/s (the
+// Measured, e4m3, 8 heads of 128: writing 32768 tokens 31.4 us, 6.5 TB/s (97 % of
+// the copy rate), reading 16 sequences of up to 8192 back 91.7 us, 6.7 TB/s (the
 // copy rate; with 16 elements in a row a lane, 107 us).  A call of a few tokens is
 // one launch, 2.1 us on the GPU.
 #include <cuda_bf16.h>

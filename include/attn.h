@@ -416,7 +416,7 @@ int attn_kv_read(const void* k_cache, const void* v_cache, const float* k_scale,
  *                   prefix is not counted)
  *   causal        : nonzero: query i of sequence b sees the own keys
  *                   j <= seq_lens[b] - Nq + i; 0: all own keys.  The prefix is
- *                   visible to every query.
+ *                   visible to every query.  (There is no sliding window.)
  *   o             : bf16 (B, Nq, H, d), written
  *   lse           : float32 (B, H, Nq), written (natural log)
  *   workspace     : device, at least attn_fwd_paged_workspace_size(...) bytes
