@@ -102,7 +102,7 @@ struct TileCfg {
     static constexpr int CONV_REGS = FP8 ? 80 : 0, LOW_REGS = FP8 ? 64 : 104;
     static constexpr int HIGH_RAW = (LAUNCH_REGS * THREADS - (CONV_REGS + LOW_REGS) * 128) / (NS * 128) / 8 * 8;
     static constexpr int HIGH_REGS = HIGH_RAW > 248 ? 248 : HIGH_RAW;
-    static constexpr int BAR_BYTES = FP8 ? 3072 : 2048;           // (of TileBarriers)
+    static constexpr int BAR_BYTES = FP8 ? 2688 : 2048;           // (of TileBarriers)
     // Output staging: 4 KB per softmax warp, over query tiles that no product
     // reads any more (d = 64: its query tiles are too small for that).
     static constexpr int EPI_BYTES = D == 64 ? NS * 16384 : 0;

@@ -392,6 +392,7 @@ int attn_kv_write(const void* k, const void* v, long long k_stride, long long v_
  *   k, v        : bf16 (B, N, H_kv, d).  Rows from the sequence's length on,
  *                 and rows whose page index is outside the cache (recorded),
  *                 are left as they were.
+ * At most 65535 sequences a call (a grid row each).
  */
 int attn_kv_read(const void* k_cache, const void* v_cache, const float* k_scale,
                  const float* v_scale, const int* block_table, long long table_stride,
