@@ -103,6 +103,18 @@ def library() -> ctypes.CDLL:
         L.attn_fwd_paged_plan.restype = i
         L.attn_fwd_paged.argtypes = [P, P, P, P, P, P, i, P, i64, i, P, P, P, i, i, i, i, i, i, i, i, i, f, P, sz, P]
         L.attn_fwd_paged.restype = i
+        L.attn_rope.argtypes = [P, i64, P, i64, P, i64, P, i64, P, i64, i, P, P, P, i64, i, i, i, i, i, i, i, i, P]
+        L.attn_rope.restype = i
+        L.attn_kv_append.argtypes = [P, i64, P, i64, P, P, i64, i64, P, i64, i, P, P, P, i64, i, i, P, P, P, P, P, i, i,
+                                     i, i, i, i, i, P]
+        L.attn_kv_append.restype = i
+        L.attn_fwd_paged_tree_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
+        L.attn_fwd_paged_tree_workspace_size.restype = sz
+        L.attn_fwd_paged_tree.argtypes = [P, P, P, P, P, P, i, P, i64, i, P, P, i64, P, P, i, i, i, i, i, i, i, i, f, P,
+                                          sz, P]
+        L.attn_fwd_paged_tree.restype = i
+        L.attn_kv_accept.argtypes = [P, P, P, P, P, i64, i, P, P, i, i, i, i, i, i, i, i, P]
+        L.attn_kv_accept.restype = i
         _lib = L
         return _lib
 
@@ -681,6 +693,12 @@ def paged_workspace_bytes(B: int, Nq: int, H: int, H_kv: int, d: int, prefix_len
     return int(library().attn_fwd_paged_workspace_size(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size))
 
 
+@functools.lru_cache(maxsize=1024)
+def paged_tree_workspace_bytes(B: int, Nq: int, H: int, H_kv: int, d: int, prefix_len: int, max_pages: int,
+                               page_size: int) -> int:
+    return int(library().attn_fwd_paged_tree_workspace_size(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size))
+
+
 class PagedPlan(NamedTuple):
     """How attn_fwd_paged cuts up a call: the kernel ("stream", "tile" or None) of the
     prefix and of the own tokens, their key ranges, the query rows of a streaming
@@ -746,6 +764,31 @@ def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, 
     bytes, scratch.  out, lse and workspace that are not given are allocated on
     the launch's stream.  Returns (O (B, Nq, H, d) bf16, LSE (B, H, Nq) float32).
     """
+    return _attend_paged(q, cache, block_table, seq_lens, None, prefix_table, prefix_len, causal, scale, out, lse,
+                         workspace, stream)
+
+
+def attn_fwd_paged_tree(q, cache: KVCache, block_table, seq_lens, parents, prefix_table=None, prefix_len: int = 0,
+                        scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
+    """attn_fwd_paged for drafts that form a tree: the queries, the last Nq own
+    tokens of each sequence, are its nodes.  A node sees the prefix, the own tokens
+    before the drafts, its ancestors and itself.
+
+    parents: int32 (B, Nq), or (Nq,) for one tree of all sequences: the index of a
+    node's parent; -1: it has none; below -1: not a node (its row is O = 0, LSE =
+    -inf).  Nq is 512 at most.  workspace: as in attn_fwd_paged, of at least
+    paged_tree_workspace_bytes(...) bytes.  A path that leaves the tree or runs in a
+    circle is reported by device_status(), its node treated as none.
+    Returns (O (B, Nq, H, d) bf16, LSE (B, H, Nq) float32).
+    """
+    if parents is None:
+        raise ValueError("parents must be a contiguous int32 (B, Nq) or (Nq,) tensor on the cache's device")
+    return _attend_paged(q, cache, block_table, seq_lens, parents, prefix_table, prefix_len, False, scale, out, lse,
+                         workspace, stream)
+
+
+def _attend_paged(q, cache, block_table, seq_lens, parents, prefix_table, prefix_len, causal, scale, out, lse, workspace,
+                  stream):
     pages, Hkv, ps, d, dtype, dev, ptrs = _check_cache(cache)
     shape = q.shape
     if len(shape) != 4 or q.dtype != _BF16 or q.get_device() != dev or not q.is_contiguous():
@@ -772,7 +815,8 @@ def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, 
         raise ValueError("workspace must be a contiguous tensor on the cache's device")
     need = 0
     if workspace is None:
-        need = paged_workspace_bytes(B, Nq, H, Hkv, d, prefix_len, max_pages, ps)
+        size = paged_workspace_bytes if parents is None else paged_tree_workspace_bytes
+        need = size(B, Nq, H, Hkv, d, prefix_len, max_pages, ps)
     if stream is None:
         out, lse, workspace = _paged_buffers(out, lse, workspace, need, B, Nq, H, d, dev)
     else:
@@ -784,11 +828,209 @@ def attn_fwd_paged(q, cache: KVCache, block_table, seq_lens, prefix_table=None, 
         ws = workspace.data_ptr()
         if need == 0:
             need = workspace.numel() * workspace.element_size()
-    _launch(library().attn_fwd_paged, "attn_fwd_paged", dev, stream,
+    if parents is None:
+        _launch(library().attn_fwd_paged, "attn_fwd_paged", dev, stream,
+                (q.data_ptr(), *ptrs, prefix, prefix_len, block_table.data_ptr(), stride, max_pages, seq_lens.data_ptr(),
+                 out.data_ptr(), lse.data_ptr(), B, Nq, H, Hkv, d, pages, ps, dtype, 1 if causal else 0,
+                 float(scale or 0.0), ws, need))
+        return out, lse
+    one = len(parents.shape) == 1
+    if (parents.shape != ((Nq,) if one else (B, Nq)) or parents.dtype != _I32 or parents.get_device() != dev
+            or not parents.is_contiguous()):
+        raise ValueError("parents must be a contiguous int32 (B, Nq) or (Nq,) tensor on the cache's device")
+    _launch(library().attn_fwd_paged_tree, "attn_fwd_paged_tree", dev, stream,
             (q.data_ptr(), *ptrs, prefix, prefix_len, block_table.data_ptr(), stride, max_pages, seq_lens.data_ptr(),
-             out.data_ptr(), lse.data_ptr(), B, Nq, H, Hkv, d, pages, ps, dtype, 1 if causal else 0,
+             parents.data_ptr(), 0 if one else Nq, out.data_ptr(), lse.data_ptr(), B, Nq, H, Hkv, d, pages, ps, dtype,
              float(scale or 0.0), ws, need))
     return out, lse
+
+
+def attn_kv_accept(cache: KVCache, block_table, seq_lens, accepted, Nq: int, stream=None) -> None:
+    """The accepted nodes' rows of the cache move up behind the context: own token
+    seq_lens[b] - Nq + j becomes what own token seq_lens[b] - Nq + accepted[b, j] was
+    (seq_lens as they were for the tree's attention; the next ones are seq_lens - Nq
+    + the number accepted).
+
+    accepted: int32 (B, M), M at most Nq and 128: nodes, usually a path; negative
+    entries are padding.  All rows of a sequence are read before one is written.  A
+    node outside the drafts is not moved and reported by device_status().
+    """
+    pages, Hkv, ps, d, dtype, dev, ptrs = _check_cache(cache)
+    B = block_table.shape[0]
+    max_pages, stride = _check_table(block_table, seq_lens, B, dev)
+    shape = accepted.shape
+    if (len(shape) != 2 or shape[0] != B or accepted.dtype != _I32 or accepted.get_device() != dev
+            or not accepted.is_contiguous()):
+        raise ValueError("accepted must be a contiguous int32 (B, M) tensor on the cache's device")
+    _launch(library().attn_kv_accept, "attn_kv_accept", dev, stream,
+            (*ptrs, block_table.data_ptr(), stride, max_pages, seq_lens.data_ptr(), accepted.data_ptr(), B, int(Nq),
+             shape[1], Hkv, d, pages, ps, dtype))
+
+
+@functools.lru_cache(maxsize=64)
+def _axis_bytes(pair_axis):
+    """(host array of a pair's axis, number of axes)"""
+    n = max(pair_axis) + 1
+    if min(pair_axis) < 0 or n > 4:
+        raise ValueError("pair_axis must have axes from 0 to 3")
+    return bytes(pair_axis), n
+
+
+def _check_rope(rope_cos, rope_sin, pair_axis, d, dev):
+    """(table rows, rotary elements, host array of the pairs' axes, number of axes)"""
+    shape = rope_cos.shape
+    for t in (rope_cos, rope_sin):
+        if t.dtype != _F32 or t.shape != shape or len(shape) != 2 or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("rope_cos and rope_sin must be contiguous float32 (rows, rot / 2) tensors on q's device")
+    half = shape[1]
+    if pair_axis is None:
+        return shape[0], 2 * half, None, 1
+    if len(pair_axis) != half:
+        raise ValueError("pair_axis must have an axis for each of the tables' columns")
+    axes, n = _axis_bytes(pair_axis if type(pair_axis) is tuple else tuple(int(a) for a in pair_axis))
+    return shape[0], 2 * half, axes, n
+
+
+def _rows(t, name, dev):
+    """(tokens, heads, d, token stride) of (.., heads, d) rows whose tokens are evenly spaced."""
+    shape, st = t.shape, t.stride()
+    if t.dtype != _BF16 or t.get_device() != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor on one device with the others")
+    if len(shape) == 3:
+        T, H, d = shape
+        stride = st[0]
+    elif len(shape) == 4:
+        T, H, d = shape[0] * shape[1], shape[2], shape[3]
+        stride = st[1] if shape[1] > 1 else st[0]
+        if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
+            raise ValueError(f"the tokens of {name} must be evenly spaced")
+    else:
+        raise ValueError(f"{name} must be (B, N, heads, d) or (tokens, heads, d)")
+    if T and H and (st[-1] != 1 or (H > 1 and st[-2] != d)):
+        raise ValueError(f"a token's heads must be contiguous in {name}")
+    return T, H, d, stride if T > 1 else H * d
+
+
+def attn_rope(q, k, rope_cos, rope_sin, positions=None, pair_axis=None, interleaved: bool = False,
+              inverse: bool = False, out_q=None, out_k=None, stream=None):
+    """Rotary positions of q and k (k may be None), one launch; inverse: the
+    transposed rotation, which takes the gradients of the turned rows back to q's
+    and k's.
+
+    q: bf16 (B, N, H, d) or (tokens, H, d), k alike with H_kv heads; a token's heads
+    are contiguous, tokens may be strided (columns of one projection).
+    rope_cos, rope_sin: float32 (rows, rot / 2); the first rot elements of a head
+    are turned, pairs (i, i + rot / 2), or (2i, 2i + 1) when interleaved.
+    positions: int64, one of q's token shape ((B, N) or (tokens,)) or (N,) for all
+    sequences alike; None: token n of a sequence stands at position n.
+    pair_axis: several axes: a sequence of rot / 2 axes (0 to 3), one for each pair;
+    positions then have a leading dimension of axes.  A position outside the tables
+    gives a row of zeros and is reported by device_status().
+    out_q, out_k: outputs (q and k themselves: in place).  Returns (q', k').
+    """
+    dev = q.get_device()
+    T, H, d, q_stride = _rows(q, "q", dev)
+    lead = q.shape[:-2]
+    Hkv, k_stride = 0, 0
+    if k is not None:
+        Tk, Hkv, dk, k_stride = _rows(k, "k", dev)
+        if k.shape[:-2] != lead or dk != d:
+            raise ValueError("k must have q's tokens and head dim")
+    rows, rot, axes, n_axes = _check_rope(rope_cos, rope_sin, pair_axis, d, dev)
+    N = lead[-1]
+    period, axis_stride, at = 0, T, None
+    if positions is None:
+        if axes is not None:
+            raise ValueError("several axes need positions")
+        period = N
+    else:
+        shape = positions.shape
+        if axes is not None:
+            if len(shape) == 0 or shape[0] < n_axes:
+                raise ValueError("positions must have a leading dimension of pair_axis's axes")
+            shape = shape[1:]
+        if shape != lead:
+            if shape != lead[-1:]:
+                raise ValueError("positions must be int64 of q's tokens (several axes: (axes, tokens)), or of one sequence's")
+            period, axis_stride = N, N
+        if positions.dtype != _I64 or positions.get_device() != dev or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous int64 tensor on q's device")
+        at = positions.data_ptr()
+    outs = []
+    for x, out, heads in ((q, out_q, H), (k, out_k, Hkv)):
+        if x is None:
+            outs.append((None, None, 0))
+            continue
+        if out is None:
+            if stream is None:
+                out = torch.empty(x.shape, dtype=_BF16, device=x.device)
+            else:       # (memory of the launch's stream: that of another may still be in use there)
+                with torch.cuda.stream(_torch_stream(stream, x.device)):
+                    out = torch.empty(x.shape, dtype=_BF16, device=x.device)
+            outs.append((out, out.data_ptr(), heads * d))
+            continue
+        if out.shape != x.shape:
+            raise ValueError("out_q and out_k must have the shapes of q and k")
+        outs.append((out, out.data_ptr(), _rows(out, "an output", dev)[3]))
+    (out_q, q_to, q_out_stride), (out_k, k_to, k_out_stride) = outs
+    _launch(library().attn_rope, "attn_rope", dev, stream,
+            (q.data_ptr(), q_stride, q_to, q_out_stride, None if k is None else k.data_ptr(), k_stride, k_to, k_out_stride,
+             at, axis_stride, n_axes, axes, rope_cos.data_ptr(), rope_sin.data_ptr(), rows, rot, 1 if interleaved else 0,
+             1 if inverse else 0, T, period, H, Hkv, d))
+    return out_q, out_k
+
+
+def attn_kv_append(q, k, v, positions, slots, cache: KVCache, rope_cos, rope_sin, pair_axis=None,
+                   interleaved: bool = False, out_q=None, stream=None):
+    """attn_kv_write with the rotary positions on the way, one launch: returns q
+    turned, turns k and writes it and v into their slots (quantised for an e4m3
+    cache, once, after the rotation).
+
+    q: bf16 (T, H, d) or None; k, v: bf16 (T, H_kv, d); a token's heads are
+    contiguous, tokens may be strided.  positions: int64 (T,), several axes: (axes,
+    T); rope_cos, rope_sin, pair_axis, interleaved: as in attn_rope; slots: as in
+    attn_kv_write.  Padding (a negative slot) leaves the cache alone and gives q' =
+    0; so does a slot or a position out of range, which device_status() reports.
+    out_q: the output (q itself: in place).
+    """
+    pages, Hkv, ps, d, dtype, dev, ptrs = _check_cache(cache)
+    T, heads, dk, k_stride = _rows(k, "k", dev)
+    if len(k.shape) != 3 or v.shape != k.shape or heads != Hkv or dk != d:
+        raise ValueError(f"k and v must be (T, {Hkv}, {d}) tensors")
+    v_stride = _rows(v, "v", dev)[3]
+    H, q_at, q_stride, q_to, q_out_stride = 0, None, 0, None, 0
+    if q is not None:
+        Tq, H, dq, q_stride = _rows(q, "q", dev)
+        if len(q.shape) != 3 or Tq != T or dq != d:
+            raise ValueError(f"q must be a ({T}, H, {d}) tensor")
+        q_at = q.data_ptr()
+    elif out_q is not None:
+        raise ValueError("out_q without q")
+    rows, rot, axes, n_axes = _check_rope(rope_cos, rope_sin, pair_axis, d, dev)
+    shape = positions.shape
+    if (positions.dtype != _I64 or positions.get_device() != dev or not positions.is_contiguous() or shape[-1:] != (T,)
+            or len(shape) != (1 if axes is None else 2) or (axes is not None and shape[0] < n_axes)):
+        raise ValueError("positions must be a contiguous int64 (T,) tensor (several axes: (axes, T)) on the cache's device")
+    if slots.shape != (T,) or slots.dtype != _I64 or slots.get_device() != dev or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous int64 (T,) tensor on the cache's device")
+    if q is not None:
+        if out_q is None:
+            if stream is None:
+                out_q = torch.empty((T, H, d), dtype=_BF16, device=q.device)
+            else:       # (memory of the launch's stream: that of another may still be in use there)
+                with torch.cuda.stream(_torch_stream(stream, q.device)):
+                    out_q = torch.empty((T, H, d), dtype=_BF16, device=q.device)
+            q_out_stride = H * d
+        else:
+            if out_q.shape != q.shape:
+                raise ValueError("out_q must have the shape of q")
+            q_out_stride = _rows(out_q, "out_q", dev)[3]
+        q_to = out_q.data_ptr()
+    _launch(library().attn_kv_append, "attn_kv_append", dev, stream,
+            (q_at, q_stride, q_to, q_out_stride, k.data_ptr(), v.data_ptr(), k_stride, v_stride, positions.data_ptr(), T,
+             n_axes, axes, rope_cos.data_ptr(), rope_sin.data_ptr(), rows, rot, 1 if interleaved else 0,
+             slots.data_ptr(), *ptrs, T, H, Hkv, d, pages, ps, dtype))
+    return out_q
 
 
 def device_status(stream=None):

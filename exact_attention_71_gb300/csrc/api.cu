@@ -1014,6 +1014,181 @@ int check_paged_sizes(int B, int Nq, int H, int H_kv, int d, int prefix_len, int
     return ATTN_OK;
 }
 
+// A tree's call: its plan (never empty parts), and the sizes that it adds.
+int check_tree(int B, int Nq, int H, int H_kv, int d, attn::PagedPlan* plan) {
+    if (Nq > attn::kMaxTree) return fail(ATTN_ERR_UNSUPPORTED, "a tree of %d nodes (at most %d)", Nq, attn::kMaxTree);
+    if (static_cast<long long>(B) * Nq * H == 0) return ATTN_OK;
+    attn::paged_plan_tree(*plan, B, Nq, H, d);
+    if (static_cast<long long>(B) * H_kv * ((static_cast<long long>(Nq) * (H / H_kv) + 15) / 16) > 0x7fffffffll)
+        return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
+    return ATTN_OK;
+}
+
+// attn_fwd_paged, and attn_fwd_paged_tree where `name` is that (parents: its trees).
+int paged_call(const char* name, bool tree, const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+               const float* v_scale, const int* prefix_table, int prefix_len, const int* block_table,
+               long long table_stride, int max_pages, const int* seq_lens, const int* parents, long long parents_stride,
+               void* o, float* lse, int B, int Nq, int H, int H_kv, int d, int num_pages, int page_size,
+               int cache_dtype, int causal, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+    g_err[0] = '\0';
+    int rc = check_cache(k_cache, v_cache, k_scale, v_scale, H_kv, d, num_pages, page_size, cache_dtype);
+    if (rc != ATTN_OK) return rc;
+    attn::PagedPlan plan;
+    if ((rc = check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan)) != ATTN_OK) return rc;
+    if (tree && (rc = check_tree(B, Nq, H, H_kv, d, &plan)) != ATTN_OK) return rc;
+    if (static_cast<long long>(B) * Nq * H == 0) return ATTN_OK;
+    if ((rc = check_table(block_table, table_stride, max_pages, page_size, seq_lens)) != ATTN_OK) return rc;
+    if (!q || !o || !lse || (prefix_len > 0 && !prefix_table)) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(q) || !aligned16(o) || !aligned16(lse))
+        return fail(ATTN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(prefix_table) & 3u) != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "page tables and lengths must be 4-byte aligned");
+    if (tree) {
+        if (!parents) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+        if ((reinterpret_cast<uintptr_t>(parents) & 3u) != 0)
+            return fail(ATTN_ERR_INVALID_ARG, "parents must be 4-byte aligned");
+        if (parents_stride != 0 && parents_stride < Nq)
+            return fail(ATTN_ERR_INVALID_ARG, "parents_stride %lld (0, or at least Nq = %d)", parents_stride, Nq);
+    }
+    if (plan.bytes > 0) {
+        if (!workspace) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+        if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+            return fail(ATTN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+        if (workspace_bytes < plan.bytes)
+            return fail(ATTN_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu bytes needed",
+                        workspace_bytes, plan.bytes);
+    }
+    attn::PagedParams p{};
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.prefix_table = prefix_table;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.seq_lens = seq_lens;
+    p.o = o;
+    p.lse = lse;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_o_bytes);
+    p.B = B;
+    p.Nq = Nq;
+    p.H = H;
+    p.H_kv = H_kv;
+    p.G = H / H_kv;
+    p.d = d;
+    p.num_pages = num_pages;
+    p.page_shift = log2_of(page_size);
+    p.max_pages = max_pages;
+    p.prefix_len = prefix_len;
+    p.causal = causal ? 1 : 0;
+    p.prefix_parts = plan.prefix_parts;
+    p.own_parts = plan.own_parts;
+    p.prefix_items = plan.prefix_items;
+    p.prefix_ctas = plan.prefix_ctas;
+    p.own_items = plan.own_items;
+    p.own_ctas = plan.own_ctas;
+    p.stream_tile = plan.stream_tile;
+    p.drafts = tree ? Nq : 0;
+    p.parents = parents;
+    p.parents_stride = parents_stride;
+    attn::paged_divisors(p);
+    p.scale_log2 = resolve_scale(scale, d) * 1.4426950408889634f;
+    p.fp8 = cache_dtype == ATTN_CACHE_E4M3;
+    p.wait_limit = g_wait_limit.load();
+    if ((rc = status_ptr(&p.status)) != ATTN_OK) return rc;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const auto rows = d == 64 ? attn::run_paged_stream_d64 : d == 128 ? attn::run_paged_stream_d128 : attn::run_paged_stream_d256;
+    const auto tiles = d == 64 ? attn::run_paged_tile_d64 : d == 128 ? attn::run_paged_tile_d128 : attn::run_paged_tile_d256;
+    cudaError_t e = cudaSuccess;
+    attn::PagedMaps maps{};
+    const int es = p.fp8 ? 1 : 2;
+    if (plan.prefix_items + plan.own_items > 0) {
+        const int bn = d == 256 ? 64 : 128;
+        if ((rc = make_cache_maps(&maps, k_cache, v_cache, num_pages, H_kv, page_size, d, es,
+                                  page_size < bn ? page_size : bn)) != ATTN_OK)
+            return rc;
+        e = tiles(maps, p, plan.direct, s);
+    }
+    if (e == cudaSuccess && (plan.prefix_stream || plan.own_items == 0)) {
+        if ((rc = make_cache_maps(&maps, k_cache, v_cache, num_pages, H_kv, page_size, d, es, 16)) != ATTN_OK) return rc;
+        e = rows(maps, p, plan.prefix_stream, plan.own_items == 0, plan.direct, plan.prefix_items + plan.own_items > 0, s);
+    }
+    if (e == cudaSuccess && !plan.direct) e = tree ? attn::run_paged_tree(p, s) : attn::run_paged_merge(p, s);
+    if (e != cudaSuccess) return cuda_fail(e, name);
+    return ATTN_OK;
+}
+
+// What attn_rope and attn_kv_append share: sizes, tables, positions.
+int check_rope(attn::RopeParams* p, int T, int H, int H_kv, int d, const long long* positions, long long axis_stride,
+               int n_axes, const unsigned char* pair_axis, const float* rope_cos, const float* rope_sin,
+               long long table_rows, int rot, int interleaved) {
+    if (T < 0 || H < 0 || H_kv < 0) return fail(ATTN_ERR_INVALID_ARG, "negative size (T=%d H=%d H_kv=%d)", T, H, H_kv);
+    if (d != 64 && d != 128 && d != 256) return fail(ATTN_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 128, 256)", d);
+    if (rot < 16 || rot > d || rot % 16 != 0)
+        return fail(ATTN_ERR_UNSUPPORTED, "%d rotary elements of %d (supported: multiples of 16 from 16 on)", rot, d);
+    if (n_axes < 1 || n_axes > 4) return fail(ATTN_ERR_UNSUPPORTED, "%d axes (supported: 1 to 4)", n_axes);
+    if (table_rows < 0) return fail(ATTN_ERR_INVALID_ARG, "negative size (table_rows=%lld)", table_rows);
+    if (n_axes > 1 && !pair_axis) return fail(ATTN_ERR_INVALID_ARG, "null pair_axis (%d axes)", n_axes);
+    for (int i = 0; i < rot / 2; ++i) {
+        const int a = pair_axis ? pair_axis[i] : 0;
+        if (a >= n_axes) return fail(ATTN_ERR_INVALID_ARG, "pair %d turns by axis %d of %d", i, a, n_axes);
+        p->axes[i >> 4] |= static_cast<uint32_t>(a) << (2 * (i & 15));
+    }
+    if (static_cast<long long>(T) * (static_cast<long long>(H) + H_kv) > (1ll << 30))
+        return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
+    if (T == 0) return ATTN_OK;
+    if (!rope_cos || !rope_sin) return fail(ATTN_ERR_INVALID_ARG, "null rope table");
+    if (!aligned16(rope_cos) || !aligned16(rope_sin)) return fail(ATTN_ERR_INVALID_ARG, "rope tables must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(positions) & 7u) != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "positions must be 8-byte aligned");
+    p->positions = positions;
+    p->axis_stride = axis_stride;
+    p->cos = rope_cos;
+    p->sin = rope_sin;
+    p->rows = table_rows;
+    p->T = T;
+    p->d = d;
+    p->rot = rot;
+    p->n_axes = n_axes;
+    p->interleaved = interleaved != 0;
+    p->by_period = attn::FastDiv(1);
+    return ATTN_OK;
+}
+
+// Rows of T tokens: `row` elements each, `stride` elements apart.
+struct Rows {
+    const void* at;
+    long long stride, row;
+};
+
+// Whether written rows `out` meet rows `other` (columns of one buffer do not).
+bool rows_meet(const Rows& out, const Rows& other, int T) {
+    if (out.row == 0 || other.row == 0) return false;
+    const long long a = static_cast<long long>(reinterpret_cast<uintptr_t>(out.at)), b = static_cast<long long>(reinterpret_cast<uintptr_t>(other.at));
+    const long long a1 = a + 2 * ((T - 1) * out.stride + out.row), b1 = b + 2 * ((T - 1) * other.stride + other.row);
+    if (a >= b1 || b >= a1) return false;
+    if (T == 1 || out.stride != other.stride) return true;
+    const long long s = 2 * out.stride, off = ((b - a) % s + s) % s;
+    return off < 2 * out.row || s - off < 2 * other.row;
+}
+
+// q or k and its output: pointers, strides, and that they are the same rows or apart.
+int check_rows(const char* what, const Rows& in, const Rows& out, int T) {
+    if (in.row == 0) return ATTN_OK;
+    if (!in.at || !out.at) return fail(ATTN_ERR_INVALID_ARG, "null pointer (%s)", what);
+    if (!aligned16(in.at) || !aligned16(out.at)) return fail(ATTN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    if (in.stride % 8 != 0 || out.stride % 8 != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "token strides (%lld, %lld elements) must be multiples of 8", in.stride, out.stride);
+    if (in.stride < 0) return fail(ATTN_ERR_INVALID_ARG, "negative token stride (%lld)", in.stride);
+    if (T > 1 && out.stride < out.row)
+        return fail(ATTN_ERR_INVALID_ARG, "output rows of %s overlap (stride %lld < %lld)", what, out.stride, out.row);
+    if (in.at == out.at && (T == 1 || in.stride == out.stride)) return ATTN_OK;
+    if (rows_meet(out, in, T)) return fail(ATTN_ERR_INVALID_ARG, "%s's output overlaps its input and is not the same rows", what);
+    return ATTN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1125,82 +1300,158 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
                    int max_pages, const int* seq_lens, void* o, float* lse, int B, int Nq, int H, int H_kv, int d,
                    int num_pages, int page_size, int cache_dtype, int causal, float scale, void* workspace,
                    size_t workspace_bytes, void* stream) {
+    return paged_call("attn_fwd_paged launch", false, q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_len,
+                      block_table, table_stride, max_pages, seq_lens, nullptr, 0, o, lse, B, Nq, H, H_kv, d, num_pages,
+                      page_size, cache_dtype, causal, scale, workspace, workspace_bytes, stream);
+}
+
+size_t attn_fwd_paged_tree_workspace_size(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages,
+                                          int page_size) {
+    attn::PagedPlan plan;
+    if (check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan) != ATTN_OK) return 0;
+    return check_tree(B, Nq, H, H_kv, d, &plan) == ATTN_OK ? plan.bytes : 0;
+}
+
+int attn_fwd_paged_tree(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                        const float* v_scale, const int* prefix_table, int prefix_len, const int* block_table,
+                        long long table_stride, int max_pages, const int* seq_lens, const int* parents,
+                        long long parents_stride, void* o, float* lse, int B, int Nq, int H, int H_kv, int d,
+                        int num_pages, int page_size, int cache_dtype, float scale, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    return paged_call("attn_fwd_paged_tree launch", true, q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_len,
+                      block_table, table_stride, max_pages, seq_lens, parents, parents_stride, o, lse, B, Nq, H, H_kv, d,
+                      num_pages, page_size, cache_dtype, 0, scale, workspace, workspace_bytes, stream);
+}
+
+int attn_kv_accept(void* k_cache, void* v_cache, float* k_scale, float* v_scale, const int* block_table,
+                   long long table_stride, int max_pages, const int* seq_lens, const int* accepted, int B, int Nq, int M,
+                   int H_kv, int d, int num_pages, int page_size, int cache_dtype, void* stream) {
     g_err[0] = '\0';
+    if (B < 0 || Nq < 0 || M < 0) return fail(ATTN_ERR_INVALID_ARG, "negative size (B=%d Nq=%d M=%d)", B, Nq, M);
     int rc = check_cache(k_cache, v_cache, k_scale, v_scale, H_kv, d, num_pages, page_size, cache_dtype);
     if (rc != ATTN_OK) return rc;
-    attn::PagedPlan plan;
-    if ((rc = check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan)) != ATTN_OK) return rc;
-    if (static_cast<long long>(B) * Nq * H == 0) return ATTN_OK;
+    if (M > Nq) return fail(ATTN_ERR_INVALID_ARG, "%d accepted of %d drafts", M, Nq);
+    if (M > attn::kMaxAccepted) return fail(ATTN_ERR_UNSUPPORTED, "%d accepted drafts (at most %d)", M, attn::kMaxAccepted);
+    if (B == 0 || M == 0) return ATTN_OK;
     if ((rc = check_table(block_table, table_stride, max_pages, page_size, seq_lens)) != ATTN_OK) return rc;
-    if (!q || !o || !lse || (prefix_len > 0 && !prefix_table)) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
-    if (!aligned16(q) || !aligned16(o) || !aligned16(lse))
-        return fail(ATTN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
-    if ((reinterpret_cast<uintptr_t>(prefix_table) & 3u) != 0)
-        return fail(ATTN_ERR_INVALID_ARG, "page tables and lengths must be 4-byte aligned");
-    if (plan.bytes > 0) {
-        if (!workspace) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
-        if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-            return fail(ATTN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-        if (workspace_bytes < plan.bytes)
-            return fail(ATTN_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu bytes needed",
-                        workspace_bytes, plan.bytes);
-    }
-    attn::PagedParams p{};
-    p.q = q;
+    if (!accepted) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+    if ((reinterpret_cast<uintptr_t>(accepted) & 3u) != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "accepted must be 4-byte aligned");
+    if (static_cast<long long>(B) * H_kv > (1ll << 29)) return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
+    attn::KvAcceptParams p{};
     p.k_cache = k_cache;
     p.v_cache = v_cache;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
-    p.prefix_table = prefix_table;
     p.table = block_table;
     p.table_stride = table_stride;
     p.seq_lens = seq_lens;
-    p.o = o;
-    p.lse = lse;
-    p.part_o = static_cast<float*>(workspace);
-    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_o_bytes);
+    p.accepted = accepted;
     p.B = B;
     p.Nq = Nq;
-    p.H = H;
+    p.M = M;
     p.H_kv = H_kv;
-    p.G = H / H_kv;
+    p.by_heads = attn::FastDiv(H_kv);
     p.d = d;
     p.num_pages = num_pages;
     p.page_shift = log2_of(page_size);
     p.max_pages = max_pages;
-    p.prefix_len = prefix_len;
-    p.causal = causal ? 1 : 0;
-    p.prefix_parts = plan.prefix_parts;
-    p.own_parts = plan.own_parts;
-    p.prefix_items = plan.prefix_items;
-    p.prefix_ctas = plan.prefix_ctas;
-    p.own_items = plan.own_items;
-    p.own_ctas = plan.own_ctas;
-    p.stream_tile = plan.stream_tile;
-    attn::paged_divisors(p);
-    p.scale_log2 = resolve_scale(scale, d) * 1.4426950408889634f;
     p.fp8 = cache_dtype == ATTN_CACHE_E4M3;
-    p.wait_limit = g_wait_limit.load();
     if ((rc = status_ptr(&p.status)) != ATTN_OK) return rc;
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const auto rows = d == 64 ? attn::run_paged_stream_d64 : d == 128 ? attn::run_paged_stream_d128 : attn::run_paged_stream_d256;
-    const auto tiles = d == 64 ? attn::run_paged_tile_d64 : d == 128 ? attn::run_paged_tile_d128 : attn::run_paged_tile_d256;
-    cudaError_t e = cudaSuccess;
-    attn::PagedMaps maps{};
-    const int es = p.fp8 ? 1 : 2;
-    if (plan.prefix_items + plan.own_items > 0) {
-        const int bn = d == 256 ? 64 : 128;
-        if ((rc = make_cache_maps(&maps, k_cache, v_cache, num_pages, H_kv, page_size, d, es,
-                                  page_size < bn ? page_size : bn)) != ATTN_OK)
-            return rc;
-        e = tiles(maps, p, plan.direct, s);
+    cudaError_t e = attn::run_kv_accept(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "attn_kv_accept launch");
+    return ATTN_OK;
+}
+
+int attn_rope(const void* q, long long q_stride, void* q_out, long long q_out_stride, const void* k, long long k_stride,
+              void* k_out, long long k_out_stride, const long long* positions, long long axis_stride, int n_axes,
+              const unsigned char* pair_axis, const float* rope_cos, const float* rope_sin, long long table_rows, int rot,
+              int interleaved, int inverse, int T, int period, int H, int H_kv, int d, void* stream) {
+    g_err[0] = '\0';
+    attn::RopeParams p{};
+    int rc = check_rope(&p, T, H, H_kv, d, positions, axis_stride, n_axes, pair_axis, rope_cos, rope_sin, table_rows, rot,
+                        interleaved);
+    if (rc != ATTN_OK) return rc;
+    if (period < 0) return fail(ATTN_ERR_INVALID_ARG, "negative size (period=%d)", period);
+    if (T == 0 || H + H_kv == 0) return ATTN_OK;
+    if (!positions) {
+        if (n_axes > 1) return fail(ATTN_ERR_INVALID_ARG, "null positions (%d axes)", n_axes);
+        if (table_rows < (period > 0 && period < T ? period : T))
+            return fail(ATTN_ERR_INVALID_ARG, "rope tables of %lld rows are shorter than the tokens", table_rows);
     }
-    if (e == cudaSuccess && (plan.prefix_stream || plan.own_items == 0)) {
-        if ((rc = make_cache_maps(&maps, k_cache, v_cache, num_pages, H_kv, page_size, d, es, 16)) != ATTN_OK) return rc;
-        e = rows(maps, p, plan.prefix_stream, plan.own_items == 0, plan.direct, plan.prefix_items + plan.own_items > 0, s);
-    }
-    if (e == cudaSuccess && !plan.direct) e = attn::run_paged_merge(p, s);
-    if (e != cudaSuccess) return cuda_fail(e, "attn_fwd_paged launch");
+    const long long qw = static_cast<long long>(H) * d, kw = static_cast<long long>(H_kv) * d;
+    const Rows qi{q, q_stride, qw}, qo{q_out, q_out_stride, qw}, ki{k, k_stride, kw}, ko{k_out, k_out_stride, kw};
+    if ((rc = check_rows("q", qi, qo, T)) != ATTN_OK || (rc = check_rows("k", ki, ko, T)) != ATTN_OK) return rc;
+    if (rows_meet(qo, ki, T) || rows_meet(ko, qi, T) || rows_meet(qo, ko, T))
+        return fail(ATTN_ERR_INVALID_ARG, "q's rows overlap k's, and are written");
+    p.q = q;
+    p.k = k;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_out_stride = k_out_stride;
+    p.H = H;
+    p.H_kv = H_kv;
+    p.period = static_cast<unsigned>(period);
+    if (period > 0) p.by_period = attn::FastDiv(period);
+    p.inverse = inverse != 0;
+    if ((rc = status_ptr(&p.status)) != ATTN_OK) return rc;
+    cudaError_t e = attn::run_rope(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "attn_rope launch");
+    return ATTN_OK;
+}
+
+int attn_kv_append(const void* q, long long q_stride, void* q_out, long long q_out_stride, const void* k, const void* v,
+                   long long k_stride, long long v_stride, const long long* positions, long long axis_stride, int n_axes,
+                   const unsigned char* pair_axis, const float* rope_cos, const float* rope_sin, long long table_rows,
+                   int rot, int interleaved, const long long* slots, void* k_cache, void* v_cache, float* k_scale,
+                   float* v_scale, int T, int H, int H_kv, int d, int num_pages, int page_size, int cache_dtype,
+                   void* stream) {
+    g_err[0] = '\0';
+    int rc = check_cache(k_cache, v_cache, k_scale, v_scale, H_kv, d, num_pages, page_size, cache_dtype);
+    if (rc != ATTN_OK) return rc;
+    attn::RopeParams p{};
+    rc = check_rope(&p, T, H, H_kv, d, positions, axis_stride, n_axes, pair_axis, rope_cos, rope_sin, table_rows, rot,
+                    interleaved);
+    if (rc != ATTN_OK) return rc;
+    if (T == 0) return ATTN_OK;
+    if (!k || !v || !slots || !positions) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
+    if (!aligned16(k) || !aligned16(v)) return fail(ATTN_ERR_INVALID_ARG, "pointers must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "slots must be 8-byte aligned");
+    if (k_stride % 8 != 0 || v_stride % 8 != 0)
+        return fail(ATTN_ERR_INVALID_ARG, "token strides (%lld, %lld elements) must be multiples of 8", k_stride,
+                    v_stride);
+    const long long qw = static_cast<long long>(H) * d, kw = static_cast<long long>(H_kv) * d;
+    const Rows qo{q_out, q_out_stride, qw};
+    if ((rc = check_rows("q", {q, q_stride, qw}, qo, T)) != ATTN_OK) return rc;
+    if (k_stride < 0 || v_stride < 0) return fail(ATTN_ERR_INVALID_ARG, "negative token stride (%lld, %lld)", k_stride, v_stride);
+    if (rows_meet(qo, {k, k_stride, kw}, T) || rows_meet(qo, {v, v_stride, kw}, T))
+        return fail(ATTN_ERR_INVALID_ARG, "q's output overlaps the new keys or values");
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_out = q_out;
+    p.q_stride = q_stride;
+    p.q_out_stride = q_out_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.H = H;
+    p.H_kv = H_kv;
+    p.slots = slots;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.num_slots = static_cast<long long>(num_pages) * page_size;
+    p.page_shift = log2_of(page_size);
+    p.append = true;
+    p.fp8 = cache_dtype == ATTN_CACHE_E4M3;
+    if ((rc = status_ptr(&p.status)) != ATTN_OK) return rc;
+    cudaError_t e = attn::run_rope(p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "attn_kv_append launch");
     return ATTN_OK;
 }
 

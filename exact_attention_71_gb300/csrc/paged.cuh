@@ -27,7 +27,14 @@ enum : int {
     SITE_PAGED_SLOT = 0x101,     // attn_kv_write: slot beyond the cache
     SITE_PAGED_PAGE = 0x102,     // a page index outside [0, num_pages)
     SITE_PAGED_LENGTH = 0x103,   // a sequence length beyond its table
+    SITE_ROPE_POSITION = 0x104,  // a position outside the cosine and sine tables
+    SITE_TREE_PARENT = 0x105,    // attn_fwd_paged_tree: a parent that is no node, or a cycle
+    SITE_TREE_NODE = 0x106,      // attn_kv_accept: a node outside the drafts, or before the sequence
 };
+
+// Drafts of a sequence (nodes of a tree), and accepted ones of a call, at most.
+constexpr int kMaxTree = 512;
+constexpr int kMaxAccepted = 128;
 
 // n / d for n < 2^31 by a multiplication (d from the host; Granlund and
 // Montgomery): with 2^s >= d and m = floor(2^32 (2^s - d) / d) + 1, n / d = (n +
@@ -77,6 +84,54 @@ struct KvReadParams {
     int* status;
 };
 
+// Rows of q and k turned by their tokens' positions; with a cache, k's (turned) and
+// v's go to their slots.
+struct RopeParams {
+    const void* q;               // bf16 rows: token t, head h at q + t * q_stride + h * d
+    const void* k;
+    const void* v;               // (append)
+    void* q_out;
+    void* k_out;                 // (attn_rope)
+    long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride;
+    const long long* positions;  // (axes, ...): axis a of token t at a * axis_stride + t (mod period); NULL: t mod period
+    long long axis_stride;
+    const float* cos;            // (rows, rot / 2)
+    const float* sin;
+    long long rows;
+    uint32_t axes[8];            // two bits a pair: its axis
+    int T, H, H_kv, d, rot, n_axes;
+    unsigned period;             // 0: positions are not repeated
+    bool interleaved, inverse;
+    FastDiv by_period, by_q_groups, by_k_groups;
+    unsigned q_blocks;
+    // append
+    bool append;
+    const long long* slots;
+    void* k_cache;
+    void* v_cache;
+    float* k_scale;
+    float* v_scale;
+    long long num_slots;
+    int page_shift;
+    bool fp8;
+    int* status;
+};
+
+struct KvAcceptParams {
+    void* k_cache;
+    void* v_cache;
+    float* k_scale;
+    float* v_scale;
+    const int* table;            // (B, max_pages), row stride table_stride
+    long long table_stride;
+    const int* seq_lens;         // (B,)
+    const int* accepted;         // (B, M)
+    int B, Nq, M, H_kv, d, num_pages, page_shift, max_pages;
+    FastDiv by_heads;            // H_kv
+    bool fp8;
+    int* status;
+};
+
 // The attention.  A query row is (sequence b, query token i, head h); the rows
 // of one key/value head's group share its keys.  Row index in q, o and the
 // partial results: (b * Nq + i) * H + h.
@@ -102,6 +157,11 @@ struct PagedParams {
     int prefix_items, prefix_ctas;   // tile kernel: work items of the prefix; CTAs that share a row tile's keys
     int own_items, own_ctas;         // the same for the own tokens (0: the streaming kernel has them)
     int stream_tile;             // query rows of a streaming CTA: 8 or 16
+    // Trees: the last `drafts` own tokens are nodes and no keys of the parts (0: no
+    // tree; causal is 0 then); parents of sequence b at b * parents_stride.
+    int drafts;
+    const int* parents;
+    long long parents_stride;
     FastDiv by_G, by_per, by_heads;              // G, Nq G, H_kv
     FastDiv by_prefix_parts, by_own_parts;
     FastDiv by_prefix_rows, by_own_rows;         // streaming CTAs that share keys
@@ -164,6 +224,9 @@ constexpr int kMaxParts = 256;
 // A streaming CTA's fixed cost, in keys.
 constexpr double kStreamFixed = 300.0;
 
+// A tree's call always has partial results.
+void paged_plan_tree(PagedPlan& plan, int B, int Nq, int H, int d);
+
 // Fills in the divisors, from the other parameters.
 void paged_divisors(PagedParams& p);
 
@@ -204,6 +267,8 @@ inline cudaError_t launch_kernel(void (*kernel)(Params...), unsigned grid, unsig
 
 cudaError_t run_kv_write(const KvWriteParams& p, cudaStream_t stream);
 cudaError_t run_kv_read(const KvReadParams& p, cudaStream_t stream);
+cudaError_t run_kv_accept(const KvAcceptParams& p, cudaStream_t stream);
+cudaError_t run_rope(const RopeParams& p, cudaStream_t stream);
 // K and V of the cache as 4-D {d, page_size, H_kv, num_pages} tensors.  Box of the
 // streaming kernel: 16 rows of up to 128 bytes; of the tile kernel: min(page_size,
 // key tile) such rows.  128-byte swizzle (64-byte rows: 64).
@@ -225,5 +290,7 @@ cudaError_t run_paged_tile_d64(const PagedMaps& m, const PagedParams& p, bool di
 cudaError_t run_paged_tile_d128(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream);
 cudaError_t run_paged_tile_d256(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream);
 cudaError_t run_paged_merge(const PagedParams& p, cudaStream_t stream);
+// The drafts of a tree, and the join with the partial results (in place of the merge).
+cudaError_t run_paged_tree(const PagedParams& p, cudaStream_t stream);
 
 }  // namespace attn

@@ -10,107 +10,13 @@
 // the copy rate), reading 16 sequences of up to 8192 back 91.7 us, 6.7 TB/s (the
 // copy rate; with 16 elements in a row a lane, 107 us).  A call of a few tokens is
 // one launch, 2.1 us on the GPU.
-#include <cuda_bf16.h>
-
+#include "kv_rows.cuh"
 #include "paged.cuh"
-#include "sm103_ptx.cuh"
 
 namespace attn {
 namespace {
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ void report(int* status, int site) { atomicCAS(status, 0, site); }
-
-__device__ __forceinline__ float bf16_lo(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-
-struct Row16 {
-    uint4 lo, hi;                  // 16 bf16
-};
-
-template <int D>
-__device__ __forceinline__ Row16 load_row(const void* base, long long at, int lane) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at) + lane;
-    return {__ldg(src), __ldg(src + D / 16)};
-}
-
-template <int D>
-__device__ __forceinline__ void store_row(void* base, long long at, int lane, const Row16& x) {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at) + lane;
-    dst[0] = x.lo;
-    dst[D / 16] = x.hi;
-}
-
-template <int D>
-__device__ __forceinline__ void store_codes(void* base, long long at, int lane, const uint4& c) {
-    uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + at) + lane;
-    dst[0] = make_uint2(c.x, c.y);
-    dst[D / 16] = make_uint2(c.z, c.w);
-}
-
-template <int D>
-__device__ __forceinline__ uint4 load_codes(const void* base, long long at, int lane) {
-    const uint2* src = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(base) + at) + lane;
-    const uint2 a = __ldg(src), b = __ldg(src + D / 16);
-    return make_uint4(a.x, a.y, b.x, b.y);
-}
-
-// The largest |x| of a row held by LANES lanes, as bf16 bits.  Unsigned
-// comparison of the bits orders finite < inf < NaN, so an infinity or a NaN in
-// the row is the result.
-template <int LANES>
-__device__ __forceinline__ uint32_t row_amax_bits(const Row16& x) {
-    constexpr uint32_t kAbs = 0x7fff7fffu;
-    const uint32_t a = __vmaxu2(__vmaxu2(x.lo.x & kAbs, x.lo.y & kAbs), __vmaxu2(x.lo.z & kAbs, x.lo.w & kAbs));
-    const uint32_t b = __vmaxu2(__vmaxu2(x.hi.x & kAbs, x.hi.y & kAbs), __vmaxu2(x.hi.z & kAbs, x.hi.w & kAbs));
-    uint32_t m = __vmaxu2(a, b);
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-    return max(m & 0xffffu, m >> 16);
-}
-
-// Four bf16 (two words) over the scale -> four codes.  x / scale is rounded once
-// to binary32: q0 + (x - q0 scale) / scale, two elements an instruction, rounds to
-// the quotient that division rounds to (the FP8 prep's div_by_scale).  The sign bits are
-// or-ed in at the end, so that -0 stays -0.
-__device__ __forceinline__ uint32_t quantise4(uint32_t a, uint32_t b, float2 neg_scale, float2 inv) {
-    float q[4];
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-        const uint32_t w = y ? b : a;
-        const float2 x = make_float2(bf16_lo(w), bf16_hi(w));
-        const float2 q0 = __fmul2_rn(x, inv);
-        const float2 r = __ffma2_rn(__ffma2_rn(q0, neg_scale, x), inv, q0);
-        q[2 * y] = r.x;
-        q[2 * y + 1] = r.y;
-    }
-    return pack_e4m3x4(q[0], q[1], q[2], q[3]) | (__byte_perm(a, b, 0x7531) & 0x80808080u);
-}
-
-// scale = amax / 448, 1 for a row of zeros, NaN for a row with an infinity or a
-// NaN (every element of it then reads back as NaN).  Each quotient is rounded once
-// to binary32 and once to e4m3, to nearest even, saturating at +-448.
-template <int LANES>
-__device__ __forceinline__ uint4 quantise_row(const Row16& x, float& scale) {
-    const uint32_t bits = row_amax_bits<LANES>(x);
-    const float amax = __uint_as_float(bits << 16);
-    scale = bits >= 0x7f80u ? __uint_as_float(0x7fc00000u) : (bits ? __fdiv_rn(amax, 448.0f) : 1.0f);
-    if (scale < 0x1p-100f) {
-        // The reciprocal, or the residual, would leave the normal range.
-        const uint32_t w[8] = {x.lo.x, x.lo.y, x.lo.z, x.lo.w, x.hi.x, x.hi.y, x.hi.z, x.hi.w};
-        uint32_t c[4];
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-            c[y] = pack_e4m3x4(__fdiv_rn(bf16_lo(w[2 * y]), scale), __fdiv_rn(bf16_hi(w[2 * y]), scale),
-                               __fdiv_rn(bf16_lo(w[2 * y + 1]), scale), __fdiv_rn(bf16_hi(w[2 * y + 1]), scale));
-        return make_uint4(c[0], c[1], c[2], c[3]);
-    }
-    const float inv = __frcp_rn(scale);
-    const float2 n2 = make_float2(-scale, -scale), i2 = make_float2(inv, inv);
-    return make_uint4(quantise4(x.lo.x, x.lo.y, n2, i2), quantise4(x.lo.z, x.lo.w, n2, i2),
-                      quantise4(x.hi.x, x.hi.y, n2, i2), quantise4(x.hi.z, x.hi.w, n2, i2));
-}
 
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(const KvWriteParams p) {
@@ -200,6 +106,76 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p)
     store_row<D>(p.v, to, lane, v);
 }
 
+// The accepted drafts' rows move up behind the context: one CTA per sequence,
+// key/value head and tensor reads all of them into shared memory before it writes
+// one, since a row may be another's place.  ROW: bytes of a row.
+constexpr int kAcceptThreads = 128;
+
+template <int ROW>
+__global__ void __launch_bounds__(kAcceptThreads) kv_accept_kernel(const KvAcceptParams p) {
+    constexpr int CH = ROW / 16;
+    extern __shared__ uint4 rows[];                        // (M, CH)
+    __shared__ long long from[kMaxAccepted], to[kMaxAccepted];
+    __shared__ float scales[kMaxAccepted];
+    const bool is_v = blockIdx.x & 1u;
+    const unsigned x = blockIdx.x >> 1;
+    const int b = p.by_heads.div(x), h = x - b * p.H_kv;
+    int len = max(0, __ldg(p.seq_lens + b));
+    const long long room = static_cast<long long>(p.max_pages) << p.page_shift;
+    if (len > room) {
+        report(p.status, SITE_PAGED_LENGTH);
+        len = static_cast<int>(room);
+    }
+    const int start = len - p.Nq;
+    for (int j = threadIdx.x; j < p.M; j += kAcceptThreads) {
+        from[j] = -1;
+        const int node = __ldg(p.accepted + static_cast<long long>(b) * p.M + j);
+        if (node < 0 || (node == j && start >= 0)) continue;       // (padding, or it stays)
+        if (node >= p.Nq || start < 0) {
+            report(p.status, SITE_TREE_NODE);
+            continue;
+        }
+        const int* table = p.table + b * p.table_stride;
+        const auto row_of = [&](int pos) -> long long {
+            const int page = __ldg(table + (pos >> p.page_shift));
+            if (page < 0 || page >= p.num_pages) return -1;
+            return ((static_cast<long long>(page) * p.H_kv + h) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
+        };
+        const long long src = row_of(start + node), dst = row_of(start + j);
+        if (src < 0 || dst < 0) {
+            report(p.status, SITE_PAGED_PAGE);
+            continue;
+        }
+        from[j] = src;
+        to[j] = dst;
+    }
+    __syncthreads();
+    uint8_t* cache = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache);
+    float* scale = is_v ? p.v_scale : p.k_scale;
+    for (int y = threadIdx.x; y < p.M * CH; y += kAcceptThreads)
+        if (from[y / CH] >= 0) rows[y] = reinterpret_cast<const uint4*>(cache + from[y / CH] * ROW)[y % CH];
+    if (p.fp8)
+        for (int j = threadIdx.x; j < p.M; j += kAcceptThreads)
+            if (from[j] >= 0) scales[j] = scale[from[j]];
+    __syncthreads();
+    for (int y = threadIdx.x; y < p.M * CH; y += kAcceptThreads)
+        if (from[y / CH] >= 0) reinterpret_cast<uint4*>(cache + to[y / CH] * ROW)[y % CH] = rows[y];
+    if (p.fp8)
+        for (int j = threadIdx.x; j < p.M; j += kAcceptThreads)
+            if (from[j] >= 0) scale[to[j]] = scales[j];
+}
+
+template <int ROW>
+cudaError_t accept_row(const KvAcceptParams& p, cudaStream_t stream) {
+    static std::atomic<unsigned long long> ready{0};
+    cudaError_t e = once_per_device(ready, [] {
+        return cudaFuncSetAttribute(kv_accept_kernel<ROW>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxAccepted * ROW);
+    });
+    if (e != cudaSuccess) return e;
+    kv_accept_kernel<ROW><<<static_cast<unsigned>(2 * p.B * p.H_kv), kAcceptThreads, p.M * ROW, stream>>>(p);
+    return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t write_d(const KvWriteParams& p, cudaStream_t stream) {
     const long long threads = static_cast<long long>(p.T) * p.H_kv * (D / 16);
@@ -222,6 +198,15 @@ cudaError_t read_d(const KvReadParams& p, cudaStream_t stream) {
 
 cudaError_t run_kv_write(const KvWriteParams& p, cudaStream_t stream) {
     return p.d == 64 ? write_d<64>(p, stream) : p.d == 128 ? write_d<128>(p, stream) : write_d<256>(p, stream);
+}
+
+cudaError_t run_kv_accept(const KvAcceptParams& p, cudaStream_t stream) {
+    switch (p.d * (p.fp8 ? 1 : 2)) {
+        case 64: return accept_row<64>(p, stream);
+        case 128: return accept_row<128>(p, stream);
+        case 256: return accept_row<256>(p, stream);
+        default: return accept_row<512>(p, stream);
+    }
 }
 
 cudaError_t run_kv_read(const KvReadParams& p, cudaStream_t stream) {

@@ -60,6 +60,12 @@ int tile_ctas(int d, long long units, long long steps, double other) {
     return best;
 }
 
+void part_buffers(PagedPlan& plan, int B, int Nq, int H, int d) {
+    const size_t r = static_cast<size_t>(plan.prefix_parts + plan.own_parts) * B * Nq * H;
+    plan.part_o_bytes = (r * d * 4 + 255) / 256 * 256;
+    plan.bytes = plan.part_o_bytes + (r * 4 + 255) / 256 * 256;
+}
+
 }  // namespace
 
 PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size) {
@@ -129,12 +135,13 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     plan.blocks = std::max(tile_items, stream_blocks);
     const int parts = plan.prefix_parts + plan.own_parts;
     plan.direct = parts == 1;
-    if (!plan.direct) {
-        const size_t r = static_cast<size_t>(parts) * B * Nq * H;
-        plan.part_o_bytes = (r * d * 4 + 255) / 256 * 256;
-        plan.bytes = plan.part_o_bytes + (r * 4 + 255) / 256 * 256;
-    }
+    if (!plan.direct) part_buffers(plan, B, Nq, H, d);
     return plan;
+}
+
+void paged_plan_tree(PagedPlan& plan, int B, int Nq, int H, int d) {
+    plan.direct = false;
+    part_buffers(plan, B, Nq, H, d);
 }
 
 void paged_divisors(PagedParams& p) {

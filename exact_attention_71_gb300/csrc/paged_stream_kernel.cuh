@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             if (tid == 0) atomicCAS(p.status, 0, SITE_PAGED_LENGTH);
             len = static_cast<int>(room);
         }
-        len = max(len, 0);
+        len = max(max(len, 0) - p.drafts, 0);
     }
     const int chunk = max((static_cast<int>(by_parts.div(len + parts - 1)) + 63) / 64 * 64, own_chunk(D));
     const int k0 = static_cast<int>(min(static_cast<long long>(part) * chunk, static_cast<long long>(len)));

@@ -317,6 +317,7 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
             if (threadIdx.x == 0) atomicCAS(p.status, 0, SITE_PAGED_LENGTH);
             len = static_cast<int>(room);
         }
+        len = max(len - p.drafts, 0);
     }
     w.len = len;
     w.part = (w.prefix ? 0 : p.prefix_parts) + split;

@@ -1,6 +1,7 @@
 /*
  * attn.h -- C ABI of the GB300 (sm_103a) fused exact attention (forward,
- * FP8 prep, backward, attention over a paged key/value cache).
+ * FP8 prep, backward, rotary positions, attention of tokens and of trees of
+ * drafts over a paged key/value cache).
  *
  * What is computed (FlashAttention-3 deep-reading report, "第三层" intro and
  * §3.1-§3.3; "Efficient Attention & FlashAttention", "数学机理"):
@@ -35,8 +36,8 @@
  *    error of the calling thread is available from attn_last_error_string().
  *  - Under the causal and window masks alone every query sees at least
  *    itself.  attn_fwd_sparse (its block mask hides every key block of the
- *    row's query tile) and attn_fwd_paged (an empty sequence) can leave a row
- *    with no visible key; such rows get O = 0 and LSE = -inf.
+ *    row's query tile), attn_fwd_paged (an empty sequence) and
+ *    attn_fwd_paged_tree (a row that is no node) can leave a row with no visible key; such rows get O = 0 and LSE = -inf.
  */
 #ifndef ATTN_GB300_H
 #define ATTN_GB300_H
@@ -53,7 +54,8 @@ typedef enum {
     ATTN_ERR_UNSUPPORTED = -2,    /* head_dim / device not supported           */
     ATTN_ERR_CUDA = -3,           /* a CUDA runtime / driver call failed       */
     ATTN_ERR_DEVICE_TIMEOUT = -4, /* a kernel gave up waiting (see below)      */
-    ATTN_ERR_BAD_INDEX = -5       /* a kernel refused a page, slot or length   */
+    ATTN_ERR_BAD_INDEX = -5       /* a kernel refused a page, slot, length,
+                                     position or node                          */
 } attn_status;
 
 /*
@@ -180,6 +182,44 @@ int attn_fp8_prep_qkv(const void* q, const void* k, const void* v, void* q8, voi
 int attn_fp8_prep_rope(const void* x, void* x8, float* scales, const float* rope_cos,
                        const float* rope_sin, int B, int H, int N, int d, int block_rows,
                        int mode, unsigned long long sign_seed, int interleaved, void* stream);
+
+/*
+ * attn_rope -- rotary position embedding of bf16 q and k rows (Su et al.,
+ * "RoFormer", 2021), for attn_fwd and the other bf16 entries, with one launch for
+ * both; with inverse != 0 its transpose, which takes the gradients of the turned
+ * rows to those of q and k (no counterpart in the pages).  Pair i < rot / 2 of
+ * token t is turned by row p of the tables,
+ *     a' = a cos[p][i] - b sin[p][i],   b' = a sin[p][i] + b cos[p][i],
+ *     p = positions[axis(i)][t]
+ * (inverse: sin negated); the products and sums are float32, each rounded, and the
+ * result is rounded once to bf16.  The pair is elements (i, i + rot / 2), or
+ * (2i, 2i + 1) when interleaved != 0; the elements from rot on are copied.
+ *   q, k            : const bf16 rows: token t, head h at q + t * q_stride + h * d
+ *                     (strides in elements, multiples of 8: q and k may be columns
+ *                     of one projection); H or H_kv may be 0 (then its pointers
+ *                     are ignored)
+ *   q_out, k_out    : bf16 rows, written: the input's own rows (same pointer and
+ *                     stride), or rows that overlap no other of the call
+ *   positions       : const int64, device: token t's position on axis a at
+ *                     a * axis_stride + t (period > 0: + t % period, so that the
+ *                     sequences of a batch share them); NULL (one axis only):
+ *                     token t stands at position t (t % period)
+ *   n_axes          : 1 to 4 (text: 1; rows and columns of an image: 2; time,
+ *                     height and width: 3)
+ *   pair_axis       : HOST array of rot / 2 axes, one per pair, read before the
+ *                     call returns; may be NULL for one axis
+ *   rope_cos,
+ *   rope_sin        : const float32 (table_rows, rot / 2), device, 16-byte aligned
+ *   rot             : a multiple of 16, at most d
+ * A token with a position outside [0, table_rows) on any axis gets rows of 0 and is
+ * recorded (ATTN_ERR_BAD_INDEX from attn_device_status).  d must be 64, 128 or
+ * 256.  T tokens; T * (H + H_kv) at most 2^30.
+ */
+int attn_rope(const void* q, long long q_stride, void* q_out, long long q_out_stride, const void* k,
+              long long k_stride, void* k_out, long long k_out_stride, const long long* positions,
+              long long axis_stride, int n_axes, const unsigned char* pair_axis,
+              const float* rope_cos, const float* rope_sin, long long table_rows, int rot,
+              int interleaved, int inverse, int T, int period, int H, int H_kv, int d, void* stream);
 
 /*
  * attn_fwd_sparse -- bf16 forward with a block-sparse key mask (the
@@ -338,8 +378,9 @@ int attn_bwd_noalloc(const void* q, const void* k, const void* v, const void* o,
                      int N, int d, int causal, float scale, int window, void* stream);
 
 /*
- * The paged key/value cache: attn_kv_write, attn_kv_read, attn_fwd_paged (no
- * counterpart in the pages; what a decoding loop needs next to attn_fwd).
+ * The paged key/value cache: attn_kv_write, attn_kv_append, attn_kv_read,
+ * attn_kv_accept, attn_fwd_paged, attn_fwd_paged_tree (no counterpart in the pages;
+ * what a decoding loop needs next to attn_fwd).
  *
  *   k_cache, v_cache : (num_pages, H_kv, page_size, d), contiguous, device;
  *                      bf16 (ATTN_CACHE_BF16) or e4m3 (ATTN_CACHE_E4M3)
@@ -380,6 +421,28 @@ int attn_kv_write(const void* k, const void* v, long long k_stride, long long v_
                   const long long* slots, void* k_cache, void* v_cache, float* k_scale,
                   float* v_scale, int T, int H_kv, int d, int num_pages, int page_size,
                   int cache_dtype, void* stream);
+
+/*
+ * attn_kv_append -- attn_kv_write with the rotary positions on the way, in one
+ * launch: q comes back turned, k is turned and written to its slots, v is written as
+ * it is.  A row is turned as by attn_rope and rounded once: to bf16, or by the
+ * quantiser of an e4m3 cache (scale = amax / 448 of the turned row in float32, 1
+ * where that is 0; otherwise as attn_kv_write).
+ *   q, q_out        : as in attn_rope, T tokens of H heads; H = 0: no queries
+ *   k, v, slots     : as in attn_kv_write
+ *   positions, axis_stride, n_axes, pair_axis, rope_cos, rope_sin, table_rows, rot,
+ *   interleaved     : as in attn_rope (positions is required; no period)
+ * A negative slot is padding: nothing is written to the cache, the token's q_out
+ * rows become 0, its positions are not read.  A slot beyond the cache or a position
+ * outside the tables is recorded and its token treated as padding.
+ */
+int attn_kv_append(const void* q, long long q_stride, void* q_out, long long q_out_stride,
+                   const void* k, const void* v, long long k_stride, long long v_stride,
+                   const long long* positions, long long axis_stride, int n_axes,
+                   const unsigned char* pair_axis, const float* rope_cos, const float* rope_sin,
+                   long long table_rows, int rot, int interleaved, const long long* slots,
+                   void* k_cache, void* v_cache, float* k_scale, float* v_scale, int T, int H,
+                   int H_kv, int d, int num_pages, int page_size, int cache_dtype, void* stream);
 
 /*
  * attn_kv_read -- the first min(seq_lens[b], N) tokens of every sequence back
@@ -457,6 +520,59 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
                    const int* seq_lens, void* o, float* lse, int B, int Nq, int H, int H_kv, int d,
                    int num_pages, int page_size, int cache_dtype, int causal, float scale,
                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_fwd_paged_tree_workspace_size / attn_fwd_paged_tree -- attn_fwd_paged for
+ * drafts that form a tree: the queries, the last Nq own tokens of each sequence, are
+ * its nodes.  Node i sees the prefix, the own tokens before the drafts, and of the
+ * drafts its ancestors and itself:
+ *   parents         : const int32, device: node i's parent at parents + b *
+ *                     parents_stride + i (stride 0: one tree for all sequences,
+ *                     otherwise at least Nq).  A node's parent may stand anywhere in the row.
+ *                     -1: node i has none; < -1: i is no node (a smaller tree):
+ *                     it sees nothing (O = 0, LSE = -inf) and no node may have
+ *                     it as its parent
+ *   Nq              : at most 512
+ * The other arguments as in attn_fwd_paged.  A sequence of fewer than Nq tokens has
+ * the last drafts of the tree only; the others are queries without a token of their
+ * own.  A node whose path leaves the drafts, meets a row that is no node, or runs in
+ * a circle is recorded (ATTN_ERR_BAD_INDEX) and treated as no node.
+ * Rows of the cache that a node does not see do not reach it.  Cache rows of drafts
+ * that no node sees are not read, nor is their page.  A V row of a draft with an
+ * infinity or a NaN (e4m3: a NaN code, or a scale that is not finite) makes the
+ * whole O row and the LSE of the nodes that see it NaN.
+ * Precision: as attn_fwd_paged over the prefix and the tokens before the drafts;
+ * over the drafts the weights enter the products as two bf16 parts (2^-17).
+ */
+size_t attn_fwd_paged_tree_workspace_size(int B, int Nq, int H, int H_kv, int d, int prefix_len,
+                                          int max_pages, int page_size);
+int attn_fwd_paged_tree(const void* q, const void* k_cache, const void* v_cache,
+                        const float* k_scale, const float* v_scale, const int* prefix_table,
+                        int prefix_len, const int* block_table, long long table_stride,
+                        int max_pages, const int* seq_lens, const int* parents,
+                        long long parents_stride, void* o, float* lse, int B, int Nq, int H,
+                        int H_kv, int d, int num_pages, int page_size, int cache_dtype,
+                        float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * attn_kv_accept -- after a tree was verified, the accepted drafts' rows of the
+ * cache move up behind the context: own token start + j of sequence b becomes what
+ * own token start + accepted[b][j] was, start = seq_lens[b] - Nq (the lengths still
+ * count the drafts; the caller's next lengths are start + the number accepted).
+ *   accepted        : const int32 (B, M), device, contiguous: nodes, a path from a
+ *                     root on in the usual case; a negative entry moves nothing
+ *                     (padding).  M at most Nq and at most 128
+ *   block_table, table_stride, max_pages, seq_lens : as in attn_kv_read; the pages
+ *                     of the moved tokens must not be shared by two sequences
+ * All rows of a sequence are read before the first is written, so any order and any
+ * overlap of nodes and places is allowed, the same node twice too.  e4m3 rows move
+ * with their scales.  A node that is not in [0, Nq), or drafts of a sequence of fewer
+ * than Nq tokens, or a page outside the cache: recorded, that row is not moved.
+ */
+int attn_kv_accept(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                   const int* block_table, long long table_stride, int max_pages,
+                   const int* seq_lens, const int* accepted, int B, int Nq, int M, int H_kv,
+                   int d, int num_pages, int page_size, int cache_dtype, void* stream);
 
 /*
  * attn_device_status -- waits for `stream`, then reads and clears the
