@@ -102,8 +102,8 @@ struct RopeParams {
     int T, H, H_kv, d, rot, n_axes;
     unsigned period;             // 0: positions are not repeated
     bool interleaved, inverse;
-    FastDiv by_period, by_q_groups, by_k_groups;
-    unsigned q_blocks;
+    FastDiv by_period, by_q_groups, by_k_groups, by_half;
+    unsigned k_blocks;
     // append
     bool append;
     const long long* slots;

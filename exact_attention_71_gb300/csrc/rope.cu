@@ -10,12 +10,21 @@
 // One rounding follows: to bf16, or the quantiser of an e4m3 cache.
 //
 // Both are streams, bound by memory bandwidth.  A row is D / 16 lanes with two
-// chunks of eight elements each: half-split pairs lie in the two chunks of one
-// lane, neighbouring pairs in one chunk, so nothing crosses lanes but the largest
-// magnitude that a row's scale needs.  A lane serves one head or several heads of a
-// token: cosines and sines (twice the bytes of a head's row) are then loaded once for
-// them.  CTAs of q and of k (append: of k and v together) follow one another in one
-// launch, so no warp has both.
+// chunks of eight elements each: half-split pairs lie in the two chunks of one lane,
+// neighbouring pairs in one chunk, so nothing crosses lanes but the largest
+// magnitude that a row's scale needs.  A lane has up to four heads of a token (two of k
+// and v together), which share its pairs' angles.  One axis: they are two float4 each
+// of the tables.  Several: a warp fetches its tokens' angles a pair a lane, whatever the
+// pair's axis, and hands them round in shared memory (with float4 loads where four
+// pairs share an axis, and single ones elsewhere: 4999 tokens of 24 heads on three
+// alternating axes 15.8 us against 12.7, 7007 of 32 on sections 24.9 against 19.3; a
+// CTA's angles together, behind a barrier: 13.4 and 20.7, and one axis 30 against 26).
+//
+// Order of the loads: positions and angles first, since the rows' loads would queue
+// before them (32768 tokens of 48 heads into an e4m3 cache 145 us the other way round,
+// 125 this way), then all rows, then the arithmetic.
+// Measured: 8192 tokens of 40 heads of 128, one axis, 26.3 us, 6.46 TB/s (95 % of the
+// copy rate); the 32768 tokens 125 us, 6.06 TB/s (89 %); 32 tokens 2.6 us.
 #include <algorithm>
 
 #include "kv_rows.cuh"
@@ -24,14 +33,15 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128, kBlocks = 7;                 // of a CTA; CTAs an SM (72 registers)
+constexpr int kHeads = 4, kHeadsKv = 2;                    // heads a lane where there are many rows
 
 enum : int { ROPE = 0, APPEND_BF16 = 1, APPEND_E4M3 = 2 };
 
-// The chunks of a lane and the pairs in them.
+// The chunks of a lane and the pairs that turn them.
 struct LaneMap {
     int c0, c1;                    // chunks (of eight elements)
-    int p0, p1;                    // first pairs of their cosines' two groups of four
+    int p0, p1;                    // first pairs of their angles' two quads
     bool r0, r1;                   // half-split: the lane's pairs turn; else: chunk c0's, chunk c1's do
 };
 
@@ -56,58 +66,82 @@ __device__ __forceinline__ LaneMap lane_map(int lane, int rot, bool interleaved)
     return m;
 }
 
-// Cosines (or sines) of four pairs from pair i on.
-template <bool AXES>
-__device__ __forceinline__ float4 angles(const float* table, const RopeParams& p, const long long (&row)[4], int i) {
-    if constexpr (!AXES) {
-        return __ldg(reinterpret_cast<const float4*>(table + row[0] + i));
-    } else {
-        const uint32_t bits = (p.axes[i >> 4] >> (2 * (i & 15))) & 0xffu;
-        const auto of = [&](uint32_t a) { return a == 0 ? row[0] : a == 1 ? row[1] : a == 2 ? row[2] : row[3]; };
-        if (bits == (bits & 3u) * 0x55u) return __ldg(reinterpret_cast<const float4*>(table + of(bits & 3u) + i));
-        return make_float4(__ldg(table + of(bits & 3u) + i), __ldg(table + of((bits >> 2) & 3u) + i + 1),
-                           __ldg(table + of((bits >> 4) & 3u) + i + 2), __ldg(table + of(bits >> 6) + i + 3));
-    }
+// Two pairs: a' = a c - b s, b' = a s + b c.
+__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
+    const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+    b = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
+    a = x;
 }
 
-// The lane's elements of a row in binary32, turned.
-__device__ __forceinline__ void turn(const Row16& x, const LaneMap& m, bool interleaved, const float (&cs)[8],
-                                     const float (&sn)[8], float (&v)[16]) {
-    const uint32_t w[8] = {x.lo.x, x.lo.y, x.lo.z, x.lo.w, x.hi.x, x.hi.y, x.hi.z, x.hi.w};
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        v[2 * e] = bf16_lo(w[e]);
-        v[2 * e + 1] = bf16_hi(w[e]);
-    }
-    const auto pair = [&](float& a, float& b, int i) {
-        const float x0 = __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(b, sn[i]));
-        b = __fadd_rn(__fmul_rn(a, sn[i]), __fmul_rn(b, cs[i]));
-        a = x0;
-    };
+// Two pairs of a row, packed: half-split: (x, y) are elements (i, i + 1) and those
+// rot / 2 further on; neighbouring pairs: x and y are a pair each.
+__device__ __forceinline__ void turn2(float (&v)[4], bool interleaved, float c0, float s0, float c1, float s1) {
     if (interleaved) {
-        if (m.r0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pair(v[2 * i], v[2 * i + 1], i);
-        }
-        if (m.r1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) pair(v[8 + 2 * i], v[8 + 2 * i + 1], 4 + i);
-        }
-    } else if (m.r0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) pair(v[i], v[8 + i], i);
+        turn_pair(v[0], v[1], c0, s0);
+        turn_pair(v[2], v[3], c1, s1);
+    } else {
+        turn_pair(v[0], v[2], c0, s0);
+        turn_pair(v[1], v[3], c1, s1);
     }
 }
 
-__device__ __forceinline__ Row16 to_bf16(const float (&v)[16]) {
-    return {make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])),
-            make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]), pack_bf16x2(v[14], v[15]))};
+// f(w0, w1, c, s, ..) for every two words of the lane's sixteen elements that turn
+// together, and their two pairs' angles; a chunk that does not turn: f's last argument is
+// false.
+template <class F>
+__device__ __forceinline__ void each_two(const LaneMap& m, bool interleaved, const float4 (&cos)[2], const float4 (&sin)[2], F&& f) {
+    // words 0 .. 4 are chunk c0, 4 .. 8 chunk c1
+    if (interleaved) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            f(4 * y, 4 * y + 1, cos[y].x, sin[y].x, cos[y].y, sin[y].y, y ? m.r1 : m.r0);
+            f(4 * y + 2, 4 * y + 3, cos[y].z, sin[y].z, cos[y].w, sin[y].w, y ? m.r1 : m.r0);
+        }
+    } else {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            f(2 * y, 2 * y + 4, cos[y].x, sin[y].x, cos[y].y, sin[y].y, m.r0);
+            f(2 * y + 1, 2 * y + 5, cos[y].z, sin[y].z, cos[y].w, sin[y].w, m.r0);
+        }
+    }
 }
 
-// (plain loads: out may be the input itself; a thread reads what it writes first)
+// A row turned and rounded to bf16 in place.
+__device__ __forceinline__ void turn_bf16(Row16& x, const LaneMap& m, bool interleaved, const float4 (&cos)[2],
+                                          const float4 (&sin)[2]) {
+    uint32_t w[8] = {x.lo.x, x.lo.y, x.lo.z, x.lo.w, x.hi.x, x.hi.y, x.hi.z, x.hi.w};
+    each_two(m, interleaved, cos, sin, [&](int a, int b, float c0, float s0, float c1, float s1, bool turns) {
+        float v[4] = {bf16_lo(w[a]), bf16_hi(w[a]), bf16_lo(w[b]), bf16_hi(w[b])};
+        turn2(v, interleaved, c0, s0, c1, s1);
+        w[a] = turns ? pack_bf16x2(v[0], v[1]) : w[a];
+        w[b] = turns ? pack_bf16x2(v[2], v[3]) : w[b];
+    });
+    x = {make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7])};
+}
+
+// A row turned, in binary32.
+__device__ __forceinline__ void turn_f32(const Row16& x, const LaneMap& m, bool interleaved, const float4 (&cos)[2],
+                                         const float4 (&sin)[2], float (&out)[16]) {
+    const uint32_t w[8] = {x.lo.x, x.lo.y, x.lo.z, x.lo.w, x.hi.x, x.hi.y, x.hi.z, x.hi.w};
+    each_two(m, interleaved, cos, sin, [&](int a, int b, float c0, float s0, float c1, float s1, bool turns) {
+        float v[4] = {bf16_lo(w[a]), bf16_hi(w[a]), bf16_lo(w[b]), bf16_hi(w[b])};
+        if (turns) turn2(v, interleaved, c0, s0, c1, s1);
+        out[2 * a] = v[0], out[2 * a + 1] = v[1], out[2 * b] = v[2], out[2 * b + 1] = v[3];
+    });
+}
+
+// 16 bytes that are read once.  (Not a read-only load: out may be the input itself, a
+// thread reads what it writes first.  volatile: the compiler moves plain loads down to
+// the rows' use, one after the other: three axes 22.2 us against 19.3.)
+__device__ __forceinline__ uint4 load_once(const void* at) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+    return v;
+}
+
 __device__ __forceinline__ Row16 load_chunks(const void* base, long long at, const LaneMap& m) {
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
-    return {src[m.c0], src[m.c1]};
+    return {load_once(src + m.c0), load_once(src + m.c1)};
 }
 
 __device__ __forceinline__ void store_chunks(void* base, long long at, const LaneMap& m, const Row16& x) {
@@ -124,115 +158,134 @@ __device__ __forceinline__ void store_chunks8(void* base, long long at, const La
 
 // HQ heads a lane of q (and k of attn_rope), HK of the cache's k and v.
 template <int D, int HQ, int HK, bool AXES, int MODE>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-    constexpr int LANES = D / 16;
-    const bool second = blockIdx.x >= p.q_blocks;          // k (append: k and v)
+__global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int LANES = D / 16, PASS = kThreads / LANES, WARP = 32 / LANES;      // rows of a CTA, of a warp
+    constexpr int HM = HQ > 2 * HK ? HQ : 2 * HK;          // rows in registers
+    const bool second = blockIdx.x < p.k_blocks;           // k (append: k and v)
     const FastDiv by = second ? p.by_k_groups : p.by_q_groups;
-    const unsigned x = (blockIdx.x - (second ? p.q_blocks : 0u)) * (kThreads / LANES) + threadIdx.x / LANES;
-    const int lane = threadIdx.x % LANES;
-    unsigned t = by.div(x);
-    const unsigned group = x - t * by.d;
+    const unsigned x = (blockIdx.x - (second ? 0u : p.k_blocks)) * PASS + threadIdx.x / LANES;
+    const int lane = threadIdx.x % LANES, half = p.rot / 2;
+    const unsigned t = by.div(x), group = x - t * by.d;
     const bool in = t < static_cast<unsigned>(p.T);
-    if (!in) t = 0;
     const LaneMap m = lane_map<D>(lane, p.rot, p.interleaved);
+    const bool rows_of_one = MODE == ROPE || !second;      // (else: a head's k and v)
+    const int heads = second ? p.H_kv : p.H, h0 = group * (rows_of_one ? HQ : HK);
 
-    // Positions, and whether the token takes part (all lanes of a row alike).
-    long long slot = 0;
+    // Whether the token takes part (all lanes of a row alike).
+    const auto position = [&](unsigned token, int axis) -> long long {
+        const unsigned n = p.period ? token - p.by_period.div(token) * p.by_period.d : token;
+        return p.positions == nullptr ? static_cast<long long>(n) : __ldg(p.positions + axis * p.axis_stride + n);
+    };
+    long long slot = 0, at = 0;
     bool take = in;
     if constexpr (MODE != ROPE) {
         slot = in ? __ldg(p.slots + t) : -1;
-        take = slot >= 0;
+        if (slot >= p.num_slots) report(p.status, SITE_PAGED_SLOT);
+        take = slot >= 0 && slot < p.num_slots;
     }
     bool fine = true;
-    long long row[4] = {0, 0, 0, 0};                       // (offsets of table rows)
-    const unsigned n = p.period ? t - p.by_period.div(t) * p.by_period.d : t;
-    if (p.positions == nullptr) {
-        row[0] = static_cast<long long>(n) * (p.rot / 2);
-    } else {
 #pragma unroll
-        for (int a = 0; a < (AXES ? 4 : 1); ++a) {
-            if (a < p.n_axes && take) {
-                const long long at = __ldg(p.positions + a * p.axis_stride + n);
-                const bool ok = at >= 0 && at < p.rows;
-                fine = fine && ok;
-                row[a] = ok ? at * (p.rot / 2) : 0;
+    for (int a = 0; a < (AXES ? 4 : 1); ++a) {
+        if (in && a < p.n_axes) {
+            at = position(t, a);
+            fine = fine && at >= 0 && at < p.rows;
+        }
+    }
+    if (take && !fine) report(p.status, SITE_ROPE_POSITION);
+    take = take && fine;
+
+    float4 cs[2], sn[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) cs[y] = sn[y] = make_float4(0, 0, 0, 0);
+    if constexpr (AXES) {
+        // A pair a lane, whatever its axis, for the warp's tokens; handed round in shared
+        // memory.  (Half-split: a lane needs quads 2l and 2l + 1; the even ones stand
+        // before the odd ones, so that the lanes of a load are next to one another.)
+        __shared__ float4 angles[kThreads / 32][WARP * D / 4];             // (token, cos / sin, pair)
+        float* mine = reinterpret_cast<float*>(angles[threadIdx.x / 32]);
+        const unsigned first = __shfl_sync(0xffffffffu, t, 0), last = min(__shfl_sync(0xffffffffu, t, 31), p.T - 1u);
+        const int pairs = in || first < static_cast<unsigned>(p.T) ? static_cast<int>(last - first + 1) * half : 0;
+        const auto place = [&](int i) { return p.interleaved ? i : ((i >> 2) & 1) * (half / 2) + ((i >> 3) << 2) + (i & 3); };
+        for (int y = threadIdx.x % 32; y < pairs; y += 32) {
+            const int token = p.by_half.div(y), i = y - token * half;
+            const long long row = position(first + token, (p.axes[i >> 4] >> (2 * (i & 15))) & 3u);
+            if (row >= 0 && row < p.rows) {
+                mine[token * p.rot + place(i)] = __ldg(p.cos + row * half + i);
+                mine[token * p.rot + half + place(i)] = __ldg(p.sin + row * half + i);
             }
         }
-    }
-    if (MODE != ROPE && slot >= p.num_slots) {
-        report(p.status, SITE_PAGED_SLOT);
-        take = false;
-    }
-    if (take && !fine) {
-        report(p.status, SITE_ROPE_POSITION);
-        take = false;
-    }
-    float cs[8], sn[8];
-    const bool turns = take && (m.r0 || m.r1);
-    {
-        float4 c[2], s[2];
+        __syncwarp();
+        if (take) {
+            const float* c = mine + (t - first) * p.rot;
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                if (!(y ? m.r1 : m.r0)) continue;
+                cs[y] = *reinterpret_cast<const float4*>(c + place(y ? m.p1 : m.p0));
+                sn[y] = *reinterpret_cast<const float4*>(c + half + place(y ? m.p1 : m.p0));
+            }
+        }
+    } else if (take) {
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-            const bool want = turns && (y ? m.r1 : m.r0);
-            c[y] = want ? angles<AXES>(p.cos, p, row, y ? m.p1 : m.p0) : make_float4(0, 0, 0, 0);
-            s[y] = want ? angles<AXES>(p.sin, p, row, y ? m.p1 : m.p0) : make_float4(0, 0, 0, 0);
-        }
-        const float f = p.inverse ? -1.0f : 1.0f;
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            cs[4 * y] = c[y].x, cs[4 * y + 1] = c[y].y, cs[4 * y + 2] = c[y].z, cs[4 * y + 3] = c[y].w;
-            sn[4 * y] = f * s[y].x, sn[4 * y + 1] = f * s[y].y, sn[4 * y + 2] = f * s[y].z, sn[4 * y + 3] = f * s[y].w;
+            if (!(y ? m.r1 : m.r0)) continue;
+            cs[y] = __ldg(reinterpret_cast<const float4*>(p.cos + at * half + (y ? m.p1 : m.p0)));
+            sn[y] = __ldg(reinterpret_cast<const float4*>(p.sin + at * half + (y ? m.p1 : m.p0)));
         }
     }
-    if (MODE == ROPE || !second) {
+    if (p.inverse) {
+#pragma unroll
+        for (int y = 0; y < 2; ++y) sn[y] = make_float4(-sn[y].x, -sn[y].y, -sn[y].z, -sn[y].w);
+    }
+
+    // The rows, once the angles' loads are on their way.
+    Row16 r[HM];
+    if (rows_of_one) {
         const void* src = second ? p.k : p.q;
-        void* dst = second ? p.k_out : p.q_out;
-        const int heads = second ? p.H_kv : p.H;
-        const long long from = t * (second ? p.k_stride : p.q_stride), to = t * (second ? p.k_out_stride : p.q_out_stride);
-        const int h0 = group * HQ;
-        Row16 r[HQ];
+        const long long from = t * (second ? p.k_stride : p.q_stride);
 #pragma unroll
-        for (int i = 0; i < HQ; ++i)
-            if (take && h0 + i < heads) r[i] = load_chunks(src, from + (h0 + i) * D, m);
-            else r[i] = Row16{};
+        for (int i = 0; i < HQ; ++i) r[i] = in && h0 + i < heads ? load_chunks(src, from + (h0 + i) * D, m) : Row16{};
+    } else {
+#pragma unroll
+        for (int i = 0; i < HK; ++i) {
+            const bool have = in && h0 + i < heads;
+            r[2 * i] = have ? load_chunks(p.k, t * p.k_stride + (h0 + i) * D, m) : Row16{};
+            r[2 * i + 1] = have ? load_chunks(p.v, t * p.v_stride + (h0 + i) * D, m) : Row16{};
+        }
+    }
+
+    if (rows_of_one) {
+        void* dst = second ? p.k_out : p.q_out;
+        const long long to = t * (second ? p.k_out_stride : p.q_out_stride);
 #pragma unroll
         for (int i = 0; i < HQ; ++i) {
             if (!in || h0 + i >= heads) continue;
-            float v[16];
-            turn(r[i], m, p.interleaved, cs, sn, v);
-            store_chunks(dst, to + (h0 + i) * D, m, to_bf16(v));
+            if (take) turn_bf16(r[i], m, p.interleaved, cs, sn);
+            else r[i] = Row16{};
+            store_chunks(dst, to + (h0 + i) * D, m, r[i]);
         }
     } else {
         const long long page = slot >> p.page_shift, in_page = slot & ((1ll << p.page_shift) - 1);
-        const int h0 = group * HK;
-        Row16 k[HK], v[HK];
 #pragma unroll
         for (int i = 0; i < HK; ++i) {
-            const bool have = take && h0 + i < p.H_kv;
-            k[i] = have ? load_chunks(p.k, t * p.k_stride + (h0 + i) * D, m) : Row16{};
-            v[i] = have ? load_chunks(p.v, t * p.v_stride + (h0 + i) * D, m) : Row16{};
-        }
-#pragma unroll
-        for (int i = 0; i < HK; ++i) {
-            float f[16];
-            turn(k[i], m, p.interleaved, cs, sn, f);
-            const bool store = take && h0 + i < p.H_kv;
-            const long long at = ((page * p.H_kv + h0 + i) << p.page_shift) + in_page;
+            const bool store = take && h0 + i < heads;
+            const long long to = ((page * p.H_kv + h0 + i) << p.page_shift) + in_page;
             if constexpr (MODE == APPEND_E4M3) {
                 // The shuffles inside need every lane; rows that are not stored take part.
-                float ks, vs;
-                const uint4 kc = quantise_row<LANES>(f, ks), vc = quantise_row<LANES>(v[i], vs);
+                float f[16], ks, vs;
+                turn_f32(r[2 * i], m, p.interleaved, cs, sn, f);
+                const uint4 kc = quantise_row<LANES>(f, ks), vc = quantise_row<LANES>(r[2 * i + 1], vs);
                 if (store) {
-                    store_chunks8(p.k_cache, at * D, m, kc);
-                    store_chunks8(p.v_cache, at * D, m, vc);
+                    store_chunks8(p.k_cache, to * D, m, kc);
+                    store_chunks8(p.v_cache, to * D, m, vc);
                     if (lane == 0) {
-                        p.k_scale[at] = ks;
-                        p.v_scale[at] = vs;
+                        p.k_scale[to] = ks;
+                        p.v_scale[to] = vs;
                     }
                 }
             } else if (store) {
-                store_chunks(p.k_cache, at * D, m, to_bf16(f));
-                store_chunks(p.v_cache, at * D, m, v[i]);
+                turn_bf16(r[2 * i], m, p.interleaved, cs, sn);
+                store_chunks(p.k_cache, to * D, m, r[2 * i]);
+                store_chunks(p.v_cache, to * D, m, r[2 * i + 1]);
             }
         }
     }
@@ -240,15 +293,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 
 template <int D, int HQ, int HK, bool AXES, int MODE>
 cudaError_t launch(RopeParams p, cudaStream_t stream) {
+    constexpr int PASS = kThreads / (D / 16);
     const auto groups = [](int heads, int per) { return (heads + per - 1) / per; };
     const int qg = groups(p.H, HQ), kg = groups(p.H_kv, MODE == ROPE ? HQ : HK);
-    const auto blocks = [&](int g) {
-        return static_cast<unsigned>((static_cast<long long>(p.T) * g * (D / 16) + kThreads - 1) / kThreads);
-    };
+    const auto blocks = [&](int g) { return static_cast<unsigned>((static_cast<long long>(p.T) * g + PASS - 1) / PASS); };
     p.by_q_groups = FastDiv(std::max(qg, 1));
     p.by_k_groups = FastDiv(std::max(kg, 1));
-    p.q_blocks = blocks(qg);
-    rope_kernel<D, HQ, HK, AXES, MODE><<<p.q_blocks + blocks(kg), kThreads, 0, stream>>>(p);
+    p.by_half = FastDiv(p.rot / 2);
+    p.k_blocks = blocks(kg);
+    rope_kernel<D, HQ, HK, AXES, MODE><<<blocks(qg) + p.k_blocks, kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -258,8 +311,8 @@ cudaError_t launch_mode(const RopeParams& p, cudaStream_t stream) {
     const long long lanes = static_cast<long long>(p.T) * (p.H + p.H_kv) * (D / 16);
     const bool many = lanes >= 2ll * kPlanSms * 2048;
     if (p.n_axes > 1)
-        return many ? launch<D, 4, 2, true, MODE>(p, stream) : launch<D, 1, 1, true, MODE>(p, stream);
-    return many ? launch<D, 4, 2, false, MODE>(p, stream) : launch<D, 1, 1, false, MODE>(p, stream);
+        return many ? launch<D, kHeads, kHeadsKv, true, MODE>(p, stream) : launch<D, 1, 1, true, MODE>(p, stream);
+    return many ? launch<D, kHeads, kHeadsKv, false, MODE>(p, stream) : launch<D, 1, 1, false, MODE>(p, stream);
 }
 
 template <int D>
