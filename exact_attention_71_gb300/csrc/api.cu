@@ -1014,13 +1014,9 @@ int check_paged_sizes(int B, int Nq, int H, int H_kv, int d, int prefix_len, int
     return ATTN_OK;
 }
 
-// A tree's call: its plan (never empty parts), and the sizes that it adds.
-int check_tree(int B, int Nq, int H, int H_kv, int d, attn::PagedPlan* plan) {
+// The size that a tree's call adds.
+int check_tree(int Nq) {
     if (Nq > attn::kMaxTree) return fail(ATTN_ERR_UNSUPPORTED, "a tree of %d nodes (at most %d)", Nq, attn::kMaxTree);
-    if (static_cast<long long>(B) * Nq * H == 0) return ATTN_OK;
-    attn::paged_plan_tree(*plan, B, Nq, H, d);
-    if (static_cast<long long>(B) * H_kv * ((static_cast<long long>(Nq) * (H / H_kv) + 15) / 16) > 0x7fffffffll)
-        return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
     return ATTN_OK;
 }
 
@@ -1035,7 +1031,7 @@ int paged_call(const char* name, bool tree, const void* q, const void* k_cache, 
     if (rc != ATTN_OK) return rc;
     attn::PagedPlan plan;
     if ((rc = check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan)) != ATTN_OK) return rc;
-    if (tree && (rc = check_tree(B, Nq, H, H_kv, d, &plan)) != ATTN_OK) return rc;
+    if (tree && (rc = check_tree(Nq)) != ATTN_OK) return rc;
     if (static_cast<long long>(B) * Nq * H == 0) return ATTN_OK;
     if ((rc = check_table(block_table, table_stride, max_pages, page_size, seq_lens)) != ATTN_OK) return rc;
     if (!q || !o || !lse || (prefix_len > 0 && !prefix_table)) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
@@ -1090,7 +1086,6 @@ int paged_call(const char* name, bool tree, const void* q, const void* k_cache, 
     p.own_items = plan.own_items;
     p.own_ctas = plan.own_ctas;
     p.stream_tile = plan.stream_tile;
-    p.drafts = tree ? Nq : 0;
     p.parents = parents;
     p.parents_stride = parents_stride;
     attn::paged_divisors(p);
@@ -1099,8 +1094,11 @@ int paged_call(const char* name, bool tree, const void* q, const void* k_cache, 
     p.wait_limit = g_wait_limit.load();
     if ((rc = status_ptr(&p.status)) != ATTN_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const auto rows = d == 64 ? attn::run_paged_stream_d64 : d == 128 ? attn::run_paged_stream_d128 : attn::run_paged_stream_d256;
-    const auto tiles = d == 64 ? attn::run_paged_tile_d64 : d == 128 ? attn::run_paged_tile_d128 : attn::run_paged_tile_d256;
+    const auto pick = [&](auto d64, auto d128, auto d256) { return d == 64 ? d64 : d == 128 ? d128 : d256; };
+    const auto rows = tree ? pick(attn::run_paged_stream_tree_d64, attn::run_paged_stream_tree_d128, attn::run_paged_stream_tree_d256)
+                           : pick(attn::run_paged_stream_d64, attn::run_paged_stream_d128, attn::run_paged_stream_d256);
+    const auto tiles = tree ? pick(attn::run_paged_tile_tree_d64, attn::run_paged_tile_tree_d128, attn::run_paged_tile_tree_d256)
+                            : pick(attn::run_paged_tile_d64, attn::run_paged_tile_d128, attn::run_paged_tile_d256);
     cudaError_t e = cudaSuccess;
     attn::PagedMaps maps{};
     const int es = p.fp8 ? 1 : 2;
@@ -1115,7 +1113,7 @@ int paged_call(const char* name, bool tree, const void* q, const void* k_cache, 
         if ((rc = make_cache_maps(&maps, k_cache, v_cache, num_pages, H_kv, page_size, d, es, 16)) != ATTN_OK) return rc;
         e = rows(maps, p, plan.prefix_stream, plan.own_items == 0, plan.direct, plan.prefix_items + plan.own_items > 0, s);
     }
-    if (e == cudaSuccess && !plan.direct) e = tree ? attn::run_paged_tree(p, s) : attn::run_paged_merge(p, s);
+    if (e == cudaSuccess && !plan.direct) e = attn::run_paged_merge(p, s);
     if (e != cudaSuccess) return cuda_fail(e, name);
     return ATTN_OK;
 }
@@ -1309,7 +1307,7 @@ size_t attn_fwd_paged_tree_workspace_size(int B, int Nq, int H, int H_kv, int d,
                                           int page_size) {
     attn::PagedPlan plan;
     if (check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan) != ATTN_OK) return 0;
-    return check_tree(B, Nq, H, H_kv, d, &plan) == ATTN_OK ? plan.bytes : 0;
+    return check_tree(Nq) == ATTN_OK ? plan.bytes : 0;
 }
 
 int attn_fwd_paged_tree(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,

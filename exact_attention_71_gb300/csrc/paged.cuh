@@ -157,9 +157,8 @@ struct PagedParams {
     int prefix_items, prefix_ctas;   // tile kernel: work items of the prefix; CTAs that share a row tile's keys
     int own_items, own_ctas;         // the same for the own tokens (0: the streaming kernel has them)
     int stream_tile;             // query rows of a streaming CTA: 8 or 16
-    // Trees: the last `drafts` own tokens are nodes and no keys of the parts (0: no
-    // tree; causal is 0 then); parents of sequence b at b * parents_stride.
-    int drafts;
+    // Trees (the kernels' TREE instantiations; causal is 0): parents of sequence b's Nq
+    // last own tokens at b * parents_stride; NULL: no tree.
     const int* parents;
     long long parents_stride;
     FastDiv by_G, by_per, by_heads;              // G, Nq G, H_kv
@@ -224,9 +223,6 @@ constexpr int kMaxParts = 256;
 // A streaming CTA's fixed cost, in keys.
 constexpr double kStreamFixed = 300.0;
 
-// A tree's call always has partial results.
-void paged_plan_tree(PagedPlan& plan, int B, int Nq, int H, int d);
-
 // Fills in the divisors, from the other parameters.
 void paged_divisors(PagedParams& p);
 
@@ -265,6 +261,11 @@ inline cudaError_t launch_kernel(void (*kernel)(Params...), unsigned grid, unsig
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// A tree's rows that are no nodes have this in place of the log2 sum of their own
+// tokens' parts: the join leaves them empty.  (No sum is +infinity: where a score is,
+// the sum is NaN.)
+constexpr float kNoNode = __builtin_huge_valf();
+
 cudaError_t run_kv_write(const KvWriteParams& p, cudaStream_t stream);
 cudaError_t run_kv_read(const KvReadParams& p, cudaStream_t stream);
 cudaError_t run_kv_accept(const KvAcceptParams& p, cudaStream_t stream);
@@ -278,19 +279,19 @@ struct PagedMaps {
 
 // The streaming kernel over the prefix and / or the own tokens, one translation
 // unit per head dim; direct: it writes o and lse itself; after: the tile kernel
-// runs before it.
-cudaError_t run_paged_stream_d64(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct, bool after,
-                                 cudaStream_t stream);
-cudaError_t run_paged_stream_d128(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct, bool after,
-                                  cudaStream_t stream);
-cudaError_t run_paged_stream_d256(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct, bool after,
-                                  cudaStream_t stream);
-// The tile kernel over its prefix_items and own_items.
-cudaError_t run_paged_tile_d64(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream);
-cudaError_t run_paged_tile_d128(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream);
-cudaError_t run_paged_tile_d256(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream);
+// runs before it; tree: the instantiations for trees.
+#define ATTN_PAGED_KERNELS(name)                                                                                           \
+    cudaError_t run_paged_stream_##name(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct,      \
+                                        bool after, cudaStream_t stream);                                                  \
+    cudaError_t run_paged_tile_##name(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream);
+// (the tile kernel: over its prefix_items and own_items)
+ATTN_PAGED_KERNELS(d64)
+ATTN_PAGED_KERNELS(d128)
+ATTN_PAGED_KERNELS(d256)
+ATTN_PAGED_KERNELS(tree_d64)
+ATTN_PAGED_KERNELS(tree_d128)
+ATTN_PAGED_KERNELS(tree_d256)
+#undef ATTN_PAGED_KERNELS
 cudaError_t run_paged_merge(const PagedParams& p, cudaStream_t stream);
-// The drafts of a tree, and the join with the partial results (in place of the merge).
-cudaError_t run_paged_tree(const PagedParams& p, cudaStream_t stream);
 
 }  // namespace attn

@@ -60,12 +60,6 @@ int tile_ctas(int d, long long units, long long steps, double other) {
     return best;
 }
 
-void part_buffers(PagedPlan& plan, int B, int Nq, int H, int d) {
-    const size_t r = static_cast<size_t>(plan.prefix_parts + plan.own_parts) * B * Nq * H;
-    plan.part_o_bytes = (r * d * 4 + 255) / 256 * 256;
-    plan.bytes = plan.part_o_bytes + (r * 4 + 255) / 256 * 256;
-}
-
 }  // namespace
 
 PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size) {
@@ -135,13 +129,12 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     plan.blocks = std::max(tile_items, stream_blocks);
     const int parts = plan.prefix_parts + plan.own_parts;
     plan.direct = parts == 1;
-    if (!plan.direct) part_buffers(plan, B, Nq, H, d);
+    if (!plan.direct) {
+        const size_t r = static_cast<size_t>(parts) * B * Nq * H;
+        plan.part_o_bytes = (r * d * 4 + 255) / 256 * 256;
+        plan.bytes = plan.part_o_bytes + (r * 4 + 255) / 256 * 256;
+    }
     return plan;
-}
-
-void paged_plan_tree(PagedPlan& plan, int B, int Nq, int H, int d) {
-    plan.direct = false;
-    part_buffers(plan, B, Nq, H, d);
 }
 
 void paged_divisors(PagedParams& p) {
@@ -237,11 +230,14 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
                     for (int v = 0; v < V; ++v) acc[v] += g[y] * f[y][v];
             }
         };
-        add(0, l2[0]);
-        if (parts > 32) add(1, l2[1]);
-        if (parts > 64) add(2, l2[2]);
-        if (parts > 96) add(3, l2[3]);
-        for (int k = 4; 32 * k < parts; ++k) add(k, part_lse(k));
+        // (a row that is no node stays empty)
+        if (!(p.parents && mm == kNoNode)) {
+            add(0, l2[0]);
+            if (parts > 32) add(1, l2[1]);
+            if (parts > 64) add(2, l2[2]);
+            if (parts > 96) add(3, l2[3]);
+            for (int k = 4; 32 * k < parts; ++k) add(k, part_lse(k));
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }

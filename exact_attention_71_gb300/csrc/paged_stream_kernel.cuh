@@ -286,10 +286,32 @@ __device__ __noinline__ uint32_t fix_v_step(uint8_t* tile, int n, int diag, int 
     return __reduce_or_sync(0xffffffffu, hit);
 }
 
+// The paths of a tree of up to 32 nodes: lane j has node j's parent; the result is
+// lane j's nodes (its ancestors and itself; bit: node), 0 where j is no node.  Whole
+// warp.  A path that leaves the tree, meets no node or runs in a circle is reported.
+__device__ __forceinline__ uint32_t tree_paths32(const PagedParams& p, int seq, int lane, bool tell) {
+    int parent = -2;
+    if (lane < p.Nq) parent = __ldg(p.parents + seq * p.parents_stride + lane);
+    uint32_t path = 1u << lane;
+    int at = parent;
+    for (int steps = 0; steps < p.Nq; ++steps) {
+        const bool on = at >= 0 && at < p.Nq;
+        if (!__any_sync(0xffffffffu, on)) break;
+        const int next = __shfl_sync(0xffffffffu, parent, at & 31);
+        if (on) {
+            path |= 1u << at;
+            at = next;
+        }
+    }
+    if (at != -1 && parent >= -1 && tell) atomicCAS(p.status, 0, SITE_TREE_PARENT);
+    return at == -1 ? path : 0;
+}
+
 // DIRECT: the own tokens are one part and there is no prefix: o and lse are
 // written; otherwise partial results.  Blocks below prefix_blocks have the
 // prefix and all sequences' rows, the others one sequence's own tokens.
-template <class Cfg, bool DIRECT>
+// TREE: the last Nq own tokens are nodes of a tree: a row sees those of its path.
+template <class Cfg, bool DIRECT, bool TREE>
 __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     paged_stream_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                         const __grid_constant__ PagedParams p, const unsigned prefix_blocks) {
@@ -328,7 +350,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             if (tid == 0) atomicCAS(p.status, 0, SITE_PAGED_LENGTH);
             len = static_cast<int>(room);
         }
-        len = max(max(len, 0) - p.drafts, 0);
+        len = max(len, 0);
     }
     const int chunk = max((static_cast<int>(by_parts.div(len + parts - 1)) + 63) / 64 * 64, own_chunk(D));
     const int k0 = static_cast<int>(min(static_cast<long long>(part) * chunk, static_cast<long long>(len)));
@@ -409,6 +431,26 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
         return i;
     };
     int limit[R][2];               // keys that rows 8n + 2t and 8n + 2t + 1 see
+    // TREE: and of the keys from `nodes` on (< 0: the first nodes are not there) those of
+    // these bits.
+    const int nodes = len - p.Nq, start = TREE && !prefix ? max(nodes, 0) : len;
+    uint32_t path[TREE ? R : 1][2];
+    __shared__ uint32_t row_path[TREE ? Cfg::ROWS : 1];
+    if constexpr (TREE) {
+        const uint32_t paths = prefix ? 0 : tree_paths32(p, seq, lane, warp == 0);
+#pragma unroll
+        for (int n = 0; n < R; ++n)
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const int r = 8 * n + 2 * t + z;
+                long long out;
+                int at, i = 0;
+                if (!prefix && r < live) i = row_of(r, out, at);
+                path[n][z] = __shfl_sync(0xffffffffu, paths, i & 31);
+                if (r >= live) path[n][z] = 0;
+                if (warp == 0 && g == 0) row_path[r] = path[n][z];
+            }
+    }
     float to_log2[R][2];           // raw score -> log2 units
     uint32_t qb[R][Cfg::QREG ? D / 8 : 1];         // row 8n + g: chunk c of the k permutation, elements [c * 4E + t * E, + E)
     uint4* sq = reinterpret_cast<uint4*>(smem + Cfg::MAIN_BYTES + Cfg::SCALE_BYTES);
@@ -428,7 +470,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             long long out;
             int at, i = 0;
             if (r < live) i = row_of(r, out, at);
-            limit[n][z] = r >= live ? 0 : min(prefix || !p.causal ? len : max(0, len - p.Nq + 1 + i), k1);
+            if constexpr (TREE) limit[n][z] = r >= live || (!prefix && path[n][z] == 0) ? 0 : min(start, k1);
+            else limit[n][z] = r >= live ? 0 : min(prefix || !p.causal ? len : max(0, len - p.Nq + 1 + i), k1);
             to_log2[n][z] = p.scale_log2;
         }
         if constexpr (!FP8) {
@@ -443,6 +486,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
             }
         }
     }
+    // Whether row 8n + 2t + z sees a key of the range.
+    const auto visible = [&](int key, int n, int z) {
+        if constexpr (TREE)
+            return key < limit[n][z] || (key >= start && key < k1 && ((path[n][z] >> ((key - nodes) & 31)) & 1u));
+        else
+            return key < limit[n][z];
+    };
     __shared__ uint32_t loud;              // e4m3: keys from diag on (32 at most) whose values are added at the end
     if constexpr (FP8) {
         // To fp16, once per CTA: a warp takes 2R rows, eight lanes a row, and
@@ -492,7 +542,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     // From this key on some query of the sequence does not see what another does
     // (of the sequence, not of the tile: which rows become NaN beside a value that is
     // not finite must not depend on the tiles).
-    const int diag = !prefix && p.causal ? max(0, len - p.Nq + 1) : len;
+    const int diag = TREE ? start : !prefix && p.causal ? max(0, len - p.Nq + 1) : len;
     // Steps that reach it (or the range's end) are masked key by key.
     const int plain_end = min(diag, k1);
 
@@ -615,7 +665,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                     for (int n = 0; n < R; ++n)
 #pragma unroll
                         for (int z = 0; z < 2; ++z)
-                            if (skip || key >= limit[n][z]) s[h][n][2 * x + z] = -INFINITY;
+                            if (skip || !visible(key, n, z)) s[h][n][2 * x + z] = -INFINITY;
                     // (scales of rows that are not there)
                     if (FP8 && (skip || key >= k1)) vscale[h][x] = 0.0f;
                 }
@@ -624,7 +674,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                 // vref must not follow a scale that some row does not see.  Every row
                 // that sees a key of this warp sees the warp's first one, and those
                 // before diag: these are what it starts from and follows.
-                const int both = max(diag, first + 1);
+                // (TREE: no node is seen by all that see another.  Where there are only
+                // nodes, the smallest of their scales: no row's own are below it.)
+                const int both = TREE ? diag : max(diag, first + 1);
                 if (vref == 0.0f) {
                     float top = 0.0f;
 #pragma unroll
@@ -633,6 +685,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                         for (int x = 0; x < 2; ++x)
                             if (key0 + 16 * h + 8 * x + pig < both && vscale[h][x] < INFINITY) top = fmaxf(top, vscale[h][x]);
                     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+                    if (TREE && top == 0.0f) {
+                        uint32_t low = 0x7f800000u;
+#pragma unroll
+                        for (int h = 0; h < H; ++h)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                if (vscale[h][x] > 0.0f) low = min(low, __float_as_uint(vscale[h][x]));
+                        low = __reduce_min_sync(0xffffffffu, low);
+                        if (low < 0x7f800000u) top = __uint_as_float(low);
+                    }
                     if (top > 0.0f) vref = vref_of(top);
                 }
 #pragma unroll
@@ -651,7 +713,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                             for (int n = 0; n < R; ++n)
 #pragma unroll
                                 for (int z = 0; z < 2; ++z)
-                                    if (key < limit[n][z]) l[n][z] = __uint_as_float(0x7fc00000u);
+                                    if (visible(key, n, z)) l[n][z] = __uint_as_float(0x7fc00000u);
                         }
                         vscale[h][x] = 0.0f;
                     }
@@ -756,7 +818,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 #pragma unroll
                     for (int z = 0; z < 2; ++z) {
                         const int seen = min(max(limit[n][z] - at, 0), 16);
-                        if (hit & ((1u << seen) - 1u)) l[n][z] = __uint_as_float(0x7fc00000u);
+                        uint32_t sees = (1u << seen) - 1u;
+                        if constexpr (TREE) {
+                            // (key at + x is node at - nodes + x)
+                            const int y = at - nodes;
+                            if (!prefix) sees |= y >= 0 ? (y < 32 ? path[n][z] >> y : 0u) : (y > -16 ? path[n][z] << -y : 0u);
+                        }
+                        if (hit & sees) l[n][z] = __uint_as_float(0x7fc00000u);
                     }
             }
         }
@@ -881,7 +949,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
 #pragma unroll 1
             for (uint32_t bits = loud; bits; bits &= bits - 1) {
                 const int key = diag + __ffs(bits) - 1;
-                if (key >= max(0, len - p.Nq + 1 + i)) break;
+                if constexpr (TREE) {
+                    if (!((row_path[rr] >> ((key - nodes) & 31)) & 1u)) continue;
+                } else if (key >= max(0, len - p.Nq + 1 + i)) {
+                    break;
+                }
                 const long long at = ((static_cast<long long>(__ldg(table + (key >> p.page_shift))) * p.H_kv + kvh) << p.page_shift) +
                                      (key & ((1 << p.page_shift) - 1));
                 const uint8_t* kc = static_cast<const uint8_t*>(p.k_cache) + at * D;
@@ -914,7 +986,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
                                      (static_cast<long long>(p.B) * p.Nq * p.H) + out;
             // An empty part's O is not read by the join.
             if (lse2 != -INFINITY) reinterpret_cast<float4*>(p.part_o + pr * D)[c4] = acc;
-            if (c4 == 0) p.part_lse[pr] = lse2;
+            if (c4 == 0) p.part_lse[pr] = TREE && !prefix && row_path[rr] == 0 ? kNoNode : lse2;
         }
     }
     // The join is launched after this kernel and waits for it alone, so this

@@ -5,10 +5,10 @@
 
 namespace attn {
 
-template <class Cfg, bool DIRECT>
+template <class Cfg, bool DIRECT, bool TREE>
 cudaError_t launch_paged_stream_one(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool after,
                                     cudaStream_t stream) {
-    auto kernel = paged_stream_kernel<Cfg, DIRECT>;
+    auto kernel = paged_stream_kernel<Cfg, DIRECT, TREE>;
     static std::atomic<unsigned long long> ready{0};
     cudaError_t e = once_per_device(ready, [&] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
@@ -21,21 +21,21 @@ cudaError_t launch_paged_stream_one(const PagedMaps& m, const PagedParams& p, bo
                          prefix_blocks);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool TREE>
 cudaError_t launch_paged_stream_rows(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct,
                                      bool after, cudaStream_t stream) {
     if (p.stream_tile == 8)
-        return direct ? launch_paged_stream_one<StreamCfg<D, FP8, 1>, true>(m, p, prefix, own, after, stream)
-                      : launch_paged_stream_one<StreamCfg<D, FP8, 1>, false>(m, p, prefix, own, after, stream);
-    return direct ? launch_paged_stream_one<StreamCfg<D, FP8, 2>, true>(m, p, prefix, own, after, stream)
-                  : launch_paged_stream_one<StreamCfg<D, FP8, 2>, false>(m, p, prefix, own, after, stream);
+        return direct ? launch_paged_stream_one<StreamCfg<D, FP8, 1>, true, TREE>(m, p, prefix, own, after, stream)
+                      : launch_paged_stream_one<StreamCfg<D, FP8, 1>, false, TREE>(m, p, prefix, own, after, stream);
+    return direct ? launch_paged_stream_one<StreamCfg<D, FP8, 2>, true, TREE>(m, p, prefix, own, after, stream)
+                  : launch_paged_stream_one<StreamCfg<D, FP8, 2>, false, TREE>(m, p, prefix, own, after, stream);
 }
 
-template <int D>
+template <int D, bool TREE>
 cudaError_t launch_paged_stream(const PagedMaps& m, const PagedParams& p, bool prefix, bool own, bool direct,
                                 bool after, cudaStream_t stream) {
-    return p.fp8 ? launch_paged_stream_rows<D, true>(m, p, prefix, own, direct, after, stream)
-                 : launch_paged_stream_rows<D, false>(m, p, prefix, own, direct, after, stream);
+    return p.fp8 ? launch_paged_stream_rows<D, true, TREE>(m, p, prefix, own, direct, after, stream)
+                 : launch_paged_stream_rows<D, false, TREE>(m, p, prefix, own, direct, after, stream);
 }
 
 }  // namespace attn

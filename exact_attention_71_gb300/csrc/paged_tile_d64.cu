@@ -4,7 +4,7 @@
 namespace attn {
 
 cudaError_t run_paged_tile_d64(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream) {
-    return launch_paged_tile<64>(m, p, direct, stream);
+    return launch_paged_tile<64, false>(m, p, direct, stream);
 }
 
 }  // namespace attn

@@ -94,7 +94,7 @@ struct TileCfg {
     static constexpr int SWK = D >= 128 ? 128 : 64;                // e4m3 K and q: swizzle span, 64-byte rows at d = 64
     static constexpr int SLOTS = 8;                                // key tiles whose scales are held
     static constexpr int SC_BYTES = FP8 ? SLOTS * 2 * BN * 4 : 0;
-    static constexpr int DIAG_TILES = 8;
+    static constexpr int DIAG_TILES = D == 256 ? 10 : 8;           // (a tree of 512 nodes lies in nine tiles of 64)
     static constexpr int CONV_WARP = 4 * NS;                       // e4m3: 4 converting warps
     static constexpr int LOAD_WARP = 4 * NS + (FP8 ? 4 : 0), MMA_WARP = LOAD_WARP + 1;   // one MMA warp per stream
     static constexpr int THREADS = NS * 128 + (FP8 ? 256 : 128);
@@ -102,7 +102,7 @@ struct TileCfg {
     static constexpr int CONV_REGS = FP8 ? 80 : 0, LOW_REGS = FP8 ? 64 : 104;
     static constexpr int HIGH_RAW = (LAUNCH_REGS * THREADS - (CONV_REGS + LOW_REGS) * 128) / (NS * 128) / 8 * 8;
     static constexpr int HIGH_REGS = HIGH_RAW > 248 ? 248 : HIGH_RAW;
-    static constexpr int BAR_BYTES = FP8 ? 2688 : 2048;           // (of TileBarriers)
+    static constexpr int BAR_BYTES = FP8 ? (D == 256 ? 2816 : 2688) : 2048;     // (of TileBarriers)
     // Output staging: 4 KB per softmax warp, over query tiles that no product
     // reads any more (d = 64: its query tiles are too small for that).
     static constexpr int EPI_BYTES = D == 64 ? NS * 16384 : 0;
@@ -119,7 +119,7 @@ struct TileCfg {
     static_assert(NS == 1 || NH * HALF_BYTES >= BM * D * 4, "the streams' join");
 };
 
-template <bool FP8>
+template <bool FP8, int DIAG>
 struct TileBarriers {
     uint64_t q_full, loaded, drain[2], fix, joined;
     uint64_t s_full[2], p_full[2], o_full[2];
@@ -127,12 +127,13 @@ struct TileBarriers {
     uint64_t raw_full[8], raw_empty[8], k_full[8], k_empty[8];
     uint64_t sc_full[8], vs_ready[8];
     uint32_t valid[8][4];          // per slot: bit per key of the tile
-    // Per diagonal tile, bit per key: its V row is not finite (poison); from 8 on, e4m3:
+    // Per diagonal tile, bit per key: its V row is not finite (poison); from DIAG on, e4m3:
     // it is left out of the products and added at the end (loud).
-    uint32_t poison[FP8 ? 16 : 8][4];
+    uint32_t poison[FP8 ? 2 * DIAG : DIAG][4];
     float most[2];                 // e4m3, streams that begin with a diagonal tile: V scales that may move vref there
     float vref[8];                 // e4m3, per slot: the slot's V scales are divided by it
     float red[2][4];               // e4m3: the converting warps' maxima
+    float low[4];                  // e4m3, trees: their minima
     float q_log2[FP8 ? 128 * 2 : 1];   // e4m3: raw score -> log2 units, per query row
     float lse1[128];               // alt mode: stream 1's result
     uint32_t tmem_base;
@@ -317,7 +318,6 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
             if (threadIdx.x == 0) atomicCAS(p.status, 0, SITE_PAGED_LENGTH);
             len = static_cast<int>(room);
         }
-        len = max(len - p.drafts, 0);
     }
     w.len = len;
     w.part = (w.prefix ? 0 : p.prefix_parts) + split;
@@ -412,14 +412,57 @@ __device__ __forceinline__ bool v_rows_not_finite(const PagedParams& p, const Ti
     return __any_sync(0xffffffffu, bad);
 }
 
+// The path of a tree's node, as the softmax threads keep it (in local memory: it is read
+// for the tiles that hold nodes): bit j of the words: node j is i or an ancestor of i.
+struct TreePath {
+    uint32_t words[kMaxTree / 32];
+    int nodes;                     // key of node 0 (< 0: the first nodes are not there)
+    // Of the 32 keys from `key` on.
+    __device__ __forceinline__ uint32_t bits(int key) const {
+        const int j = key - nodes;
+        if (j <= -32) return 0;
+        const int x = j >> 5;
+        const uint32_t lo = x >= 0 && x < kMaxTree / 32 ? words[x] : 0, hi = x + 1 < kMaxTree / 32 ? words[x + 1] : 0;
+        return __funnelshift_r(lo, hi, j & 31);
+    }
+};
+
+// Node i's path; false where i is no node (all words 0), and with a report where its
+// path leaves the tree, meets no node or runs in a circle.
+static __device__ __noinline__ bool tree_path(const PagedParams& p, int seq, int i, int len, TreePath& path) {
+    const int* parents = p.parents + seq * p.parents_stride;
+    path.nodes = len - p.Nq;
+    for (int x = 0; x < kMaxTree / 32; ++x) path.words[x] = 0;
+    int at = i, word = i >> 5;
+    uint32_t bits = 0;
+    const int parent = __ldg(parents + i);
+    if (parent < -1) return false;
+    for (int steps = 0; steps < p.Nq && at >= 0 && at < p.Nq; ++steps) {
+        if ((at >> 5) != word) {
+            path.words[word] |= bits;
+            word = at >> 5;
+            bits = 0;
+        }
+        bits |= 1u << (at & 31);
+        at = __ldg(parents + at);
+    }
+    path.words[word] |= bits;
+    if (at == -1) return true;
+    atomicCAS(p.status, 0, SITE_TREE_PARENT);
+    for (int x = 0; x < kMaxTree / 32; ++x) path.words[x] = 0;
+    return false;
+}
+
 // O of a warp's rows, one a lane, comes in units of vref and leaves in units of
 // kLoudUnit (a weight may be 2^15), with the values of the loud keys of the tiles
 // [x0, x1) that each row sees: weights exp2(s - m) from the cache, in binary32.  Whole
-// warp; out: the row's index in q, limit: the keys that it sees.
+// warp; out: the row's index in q, limit: the keys that it sees, and in a tree those of
+// its path.
 constexpr float kLoudUnit = 0x1p20f;
-template <class Cfg>
+template <class Cfg, bool TREE>
 __device__ __noinline__ void add_loud(const PagedParams& p, const int* table, int kvh, const uint32_t (*loud)[4], int diag,
-                                      int x0, int x1, int limit, int out, float m, float vref, uint32_t o_tmem) {
+                                      int x0, int x1, int limit, const TreePath& path, int out, float m, float vref,
+                                      uint32_t o_tmem) {
     constexpr int D = Cfg::D;
     auto update = [&](auto&& f) {
 #pragma unroll 1
@@ -447,7 +490,7 @@ __device__ __noinline__ void add_loud(const PagedParams& p, const int* table, in
                 const uint32_t* kc = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.k_cache) + at * D);
                 const uint32_t* vc = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p.v_cache) + at * D);
                 float e = 0.0f;
-                if (key < limit) {
+                if (key < limit || (TREE && out >= 0 && (path.bits(key) & 1u))) {
                     const uint2* q = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) + static_cast<long long>(out) * D);
                     float dot = 0.0f;
 #pragma unroll 1
@@ -466,7 +509,8 @@ __device__ __noinline__ void add_loud(const PagedParams& p, const int* table, in
     }
 }
 
-template <class Cfg, bool DIRECT>
+// TREE: the last Nq own tokens are nodes of a tree: a row sees those of its path.
+template <class Cfg, bool DIRECT, bool TREE>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     paged_tile_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                       const __grid_constant__ PagedParams p) {
@@ -480,7 +524,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     uint8_t* sRaw = sK + Cfg::NK * Cfg::RAW_BYTES;             // e4m3: V tiles
     float* sScale = reinterpret_cast<float*>(sRaw + Cfg::NR * Cfg::RAW_BYTES);     // (slot, k / v, BN)
     uint8_t* sEpi = reinterpret_cast<uint8_t*>(sScale) + Cfg::SC_BYTES;            // d = 64: output staging
-    using Barriers = TileBarriers<FP8>;
+    using Barriers = TileBarriers<FP8, Cfg::DIAG_TILES>;
     static_assert(sizeof(Barriers) <= Cfg::BAR_BYTES, "barrier block");
     Barriers* bars = reinterpret_cast<Barriers*>(sEpi + Cfg::EPI_BYTES);
     volatile int* abort_flag = &bars->abort_flag;
@@ -490,7 +534,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const TileItem w = tile_item<Cfg>(p);
     // From this key on the CTA's rows may see different keys; its tile.
     int diag_key = w.len;
-    if (!w.prefix && p.causal) diag_key = row_limit(p, w, max(w.rt[0], 0) * BM);
+    if (TREE && !w.prefix) diag_key = max(0, w.len - p.Nq);
+    else if (!w.prefix && p.causal) diag_key = row_limit(p, w, max(w.rt[0], 0) * BM);
     const int diag = diag_key < w.len ? diag_key / BN : w.len / BN + 1;
 
     // Softmax threads: their query row.
@@ -498,6 +543,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const int row = (stream == 0 ? w.rt[0] : w.rt[1]) * BM + (tid & 127);
     bool in = false;
     int out = -1, lse_at = 0;      // row index in q, o and the partials; in lse
+    int node_of = 0;               // TREE: the row's node
     if (warp < 4 * NS) {
         in = (stream == 0 ? w.rt[0] : w.rt[1]) >= 0 && row < w.rows;
         if (in) {
@@ -507,6 +553,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             const int h = w.kvh * p.G + z - i * p.G;
             out = (b * p.Nq + i) * p.H + h;
             lse_at = (b * p.H + h) * p.Nq + i;
+            node_of = i;
         }
     }
     if (tid == Cfg::LOAD_WARP * 32) {
@@ -529,11 +576,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             mbar_init(&bars->k_empty[s], w.pair ? 2 : 1);
             mbar_init(&bars->sc_full[s], 1);
             mbar_init(&bars->vs_ready[s], 128);
-            for (int x = 0; x < 4; ++x) {
-                bars->poison[s][x] = 0;
-                if (FP8) bars->poison[FP8 ? 8 + s : 0][x] = 0;
-            }
         }
+        for (int s = 0; s < (FP8 ? 2 : 1) * Cfg::DIAG_TILES; ++s)
+            for (int x = 0; x < 4; ++x) bars->poison[s][x] = 0;
         bars->abort_flag = 0;
         bars->turn = 0;
         fence_barrier_init();
@@ -658,7 +703,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     if (page >= 0 && page < p.num_pages)
                         v = __ldg(p.v_scale + (((static_cast<long long>(page) * p.H_kv + w.kvh) << p.page_shift) + (key & (ps - 1))));
                 }
-                bars->most[lane] = v < INFINITY ? 16.0f * v : 0.0f;
+                // (trees: a node's may not count; see there)
+                bars->most[lane] = v < INFINITY && !(TREE && key >= diag_key) ? 16.0f * v : 0.0f;
             }
             __syncwarp();
             int page0 = -1, page1 = -1, next0 = page_of(0, 0), next1 = NS > 1 && !w.pair ? page_of(1, 0) : -1;
@@ -798,8 +844,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 // rows that see it add its values at the end.  In a stream's first
                 // tile vref may follow up to 16 times the scale of its first key,
                 // which every row sees that sees one of the stream's: that is still
-                // below it.  Every thread reaches the one barrier of a tile,
-                // whatever its waits say; all leave together.
+                // below it.  (In a tree no node is seen by all that see another; where the
+                // first tile has nodes only, vref may follow up to 16 times the smallest of
+                // their scales.)  Every thread reaches the one barrier of a tile (that tile:
+                // the two), whatever its waits say; all leave together.
                 bool ok = tile_wait(&bars->sc_full[slot], (e / Cfg::SLOTS) & 1, abort_flag, p, SITE_TILE_SCALE);
                 const uint32_t* valid = bars->valid[slot];
                 uint32_t all = valid[0] & valid[1];
@@ -807,14 +855,26 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 const bool whole = all == 0xffffffffu;
                 const bool diagonal = key0 / BN >= diag;
                 uint32_t* poison = bars->poison[min(max(key0 / BN - diag, 0), Cfg::DIAG_TILES - 1)];
-                float v = 0.0f;
+                float v = 0.0f, most0 = diagonal ? bars->most[t] : 0.0f;
+                if (TREE && u == 0 && !w.prefix && key0 >= diag_key) {
+                    uint32_t least = 0x7f800000u;
+                    if (ct < BN && ((valid[ct >> 5] >> (ct & 31)) & 1u)) {
+                        const float x = sScale[slot * 2 * BN + BN + ct];
+                        if (x > 0.0f) least = __float_as_uint(x);
+                    }
+                    least = __reduce_min_sync(0xffffffffu, least);
+                    if (lane == 0) bars->low[ct >> 5] = __uint_as_float(least);
+                    if (!named_barrier_and(1, 128, ok)) return false;
+                    const float x = fminf(fminf(bars->low[0], bars->low[1]), fminf(bars->low[2], bars->low[3]));
+                    most0 = x < INFINITY ? 16.0f * x : 0.0f;
+                }
                 if (ct < BN && ((valid[ct >> 5] >> (ct & 31)) & 1u)) {
                     v = sScale[slot * 2 * BN + BN + ct];
                     if (diagonal && key0 + ct >= diag_key) {
                         const float ref = w.pair || t == 0 ? vref0 : vref1;
-                        const float most = fmaxf(64.0f * ref, bars->most[t]);
+                        const float most = fmaxf(64.0f * ref, most0);
                         if (!(v <= most)) {
-                            atomicOr(&poison[(v < INFINITY ? 32 : 0) + (ct >> 5)], 1u << (ct & 31));
+                            atomicOr(&poison[(v < INFINITY ? 4 * Cfg::DIAG_TILES : 0) + (ct >> 5)], 1u << (ct & 31));
                             v = 0.0f;
                         }
                     }
@@ -887,7 +947,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const uint32_t s_tmem = tmem + lane_off + t * 128, o_tmem = tmem + lane_off + 256 + t * D;
         const int nt = t == 0 ? w.n[0] : w.n[1];
         const int j0 = t == 0 ? w.j0[0] : w.j0[1], part = w.part;
-        const int limit = in ? row_limit(p, w, row) : w.len;   // (a row that is not there needs no mask)
+        int limit = in ? row_limit(p, w, row) : w.len;         // (a row that is not there needs no mask)
         // A warp brings in its 32 query rows, swizzled, zero where there is none;
         // in alt mode both streams use stream 0's tile.  A lane has chunk qc of the
         // rows q_row(x).
@@ -906,6 +966,27 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             }
         }
         cp_async_commit();
+        // TREE: a row that is no node is computed without a mask (its neighbours then need
+        // none either), and left out at the end.
+        TreePath path;
+        bool none = false;
+        if constexpr (TREE) {
+            if (in && !w.prefix) {
+                none = !tree_path(p, w.seq, node_of, w.len, path);
+                if (!none) limit = diag_key;
+            } else {
+                for (int x = 0; x < kMaxTree / 32; ++x) path.words[x] = 0;
+                path.nodes = w.len;
+            }
+        }
+        // Which of the 32 keys from `key` on the row sees.
+        const auto sees = [&](int key) -> uint32_t {
+            const int n = min(max(limit - key, 0), 32);
+            const uint32_t bits = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+            if constexpr (TREE)
+                if (n < 32) return bits | path.bits(key);
+            return bits;
+        };
         cp_async_wait<0>();
         if constexpr (FP8) {
             // Into two e4m3 parts, in place.  (A loop of few instructions: with a
@@ -986,8 +1067,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             } else {
 #pragma unroll
                 for (int c = 0; c < BN / 32; ++c) {
-                    const int n = min(max(limit - key0 - c * 32, 0), 32);
-                    seen[c] = bars->valid[slot][c] & (n == 32 ? 0xffffffffu : (1u << n) - 1u);
+                    seen[c] = bars->valid[slot][c] & sees(key0 + c * 32);
                     all &= seen[c];
                 }
             }
@@ -1027,7 +1107,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         e[1] = __float_as_uint(v.y);
                     }
                 }
-                if (masked) {
+                if (TREE && masked) {
+                    // (a lane has its own row's bits; here it has four other rows)
+#pragma unroll
+                    for (int c = 0; c < BN / 32; ++c) {
+                        const uint32_t mine = bars->valid[slot][c] & sees(key0 + c * 32);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t bits = __shfl_sync(0xffffffffu, mine, (lane >> 2) + 8 * i) >> (2 * (lane & 3));
+#pragma unroll
+                            for (int g = 4 * c; g < 4 * c + 4; ++g) {
+                                uint32_t* e = sr + (i >> 1) * 4 * NG + g * 4 + (i & 1) * 2;
+                                if (!((bits >> (8 * (g & 3))) & 1u)) e[0] = 0xff800000u;
+                                if (!((bits >> (8 * (g & 3))) & 2u)) e[1] = 0xff800000u;
+                            }
+                        }
+                    }
+                } else if (masked) {
 #pragma unroll
                     for (int g = 0; g < NG; ++g) {
                         const int key = 8 * g + 2 * (lane & 3);
@@ -1202,9 +1298,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 for (int x = max(diag, j0); x < j0 + nt; ++x) {
 #pragma unroll
                     for (int c = 0; c < BN / 32; ++c) {
-                        const int n = min(max(limit - x * BN - c * 32, 0), 32);
                         const uint32_t bits = bars->poison[min(x - diag, Cfg::DIAG_TILES - 1)][c];
-                        if (bits & (n == 32 ? 0xffffffffu : (1u << n) - 1u)) l = __uint_as_float(0x7fc00000u);
+                        if (bits & sees(x * BN + c * 32)) l = __uint_as_float(0x7fc00000u);
                     }
                 }
             }
@@ -1213,9 +1308,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 bool any = false;
                 for (int x = max(diag, j0); x < j0 + nt; ++x)
 #pragma unroll
-                    for (int c = 0; c < BN / 32; ++c) any |= bars->poison[FP8 ? 8 + min(x - diag, Cfg::DIAG_TILES - 1) : 0][c] != 0;
+                    for (int c = 0; c < BN / 32; ++c) any |= bars->poison[FP8 ? Cfg::DIAG_TILES + min(x - diag, Cfg::DIAG_TILES - 1) : 0][c] != 0;
                 if (any) {
-                    add_loud<Cfg>(p, w.table, w.kvh, bars->poison + 8, diag, max(diag, j0), j0 + nt, in ? limit : 0, out, m, vref, o_tmem);
+                    add_loud<Cfg, TREE>(p, w.table, w.kvh, bars->poison + Cfg::DIAG_TILES, diag, max(diag, j0), j0 + nt, in ? limit : 0,
+                                        path, out, m, vref, o_tmem);
                     vref = kLoudUnit;
                 }
             }
@@ -1269,9 +1365,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             }
             if (take) {
                 if constexpr (DIRECT) {
-                    if (in) p.lse[lse_at] = lse2 * 0.69314718055994530942f;
+                    if (in) p.lse[lse_at] = none ? -INFINITY : lse2 * 0.69314718055994530942f;
                 } else {
-                    if (in) p.part_lse[part * rows_all + out] = lse2;
+                    if (in) p.part_lse[part * rows_all + out] = none ? kNoNode : lse2;
                 }
             }
             // O leaves through this warp's 4 KB of shared memory (32 rows x 128
@@ -1297,7 +1393,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
                     for (int y = 0; y < COLS; y += 32) reg_fence32(o + y);
 #pragma unroll
-                    for (int y = 0; y < COLS; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * inv);
+                    for (int y = 0; y < COLS; ++y) o[y] = TREE && DIRECT && none ? 0u : __float_as_uint(__uint_as_float(o[y]) * inv);
                 } else {
 #pragma unroll
                     for (int y = 0; y < COLS; ++y) o[y] = 0u;
@@ -1309,7 +1405,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                         const float* e = &v.x;
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
-                            if (weight1 != 0.0f) o[4 * y + z] = __float_as_uint(__uint_as_float(o[4 * y + z]) + e[z] * weight1);
+                            if (weight1 != 0.0f && !(TREE && none)) o[4 * y + z] = __float_as_uint(__uint_as_float(o[4 * y + z]) + e[z] * weight1);
                     }
                 }
 #pragma unroll

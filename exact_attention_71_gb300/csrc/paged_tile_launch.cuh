@@ -5,9 +5,9 @@
 
 namespace attn {
 
-template <class Cfg, bool DIRECT>
+template <class Cfg, bool DIRECT, bool TREE>
 cudaError_t launch_paged_tile_one(const PagedMaps& m, const PagedParams& p, cudaStream_t stream) {
-    auto kernel = paged_tile_kernel<Cfg, DIRECT>;
+    auto kernel = paged_tile_kernel<Cfg, DIRECT, TREE>;
     static std::atomic<unsigned long long> ready{0};
     cudaError_t e = once_per_device(ready, [&] {
         // The register split (setmaxnreg) assumes exactly LAUNCH_REGS registers
@@ -23,14 +23,14 @@ cudaError_t launch_paged_tile_one(const PagedMaps& m, const PagedParams& p, cuda
     return launch_kernel(kernel, p.prefix_items + p.own_items, Cfg::THREADS, Cfg::SMEM_BYTES, false, stream, m.k, m.v, p);
 }
 
-template <int D>
+template <int D, bool TREE>
 cudaError_t launch_paged_tile(const PagedMaps& m, const PagedParams& p, bool direct, cudaStream_t stream) {
     if (p.fp8) {
         using C = TileCfg<D, true>;
-        return direct ? launch_paged_tile_one<C, true>(m, p, stream) : launch_paged_tile_one<C, false>(m, p, stream);
+        return direct ? launch_paged_tile_one<C, true, TREE>(m, p, stream) : launch_paged_tile_one<C, false, TREE>(m, p, stream);
     }
     using C = TileCfg<D, false>;
-    return direct ? launch_paged_tile_one<C, true>(m, p, stream) : launch_paged_tile_one<C, false>(m, p, stream);
+    return direct ? launch_paged_tile_one<C, true, TREE>(m, p, stream) : launch_paged_tile_one<C, false, TREE>(m, p, stream);
 }
 
 }  // namespace attn

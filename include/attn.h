@@ -537,12 +537,11 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
  * the last drafts of the tree only; the others are queries without a token of their
  * own.  A node whose path leaves the drafts, meets a row that is no node, or runs in
  * a circle is recorded (ATTN_ERR_BAD_INDEX) and treated as no node.
- * Rows of the cache that a node does not see do not reach it.  Cache rows of drafts
- * that no node sees are not read, nor is their page.  A V row of a draft with an
- * infinity or a NaN (e4m3: a NaN code, or a scale that is not finite) makes the
- * whole O row and the LSE of the nodes that see it NaN.
- * Precision: as attn_fwd_paged over the prefix and the tokens before the drafts;
- * over the drafts the weights enter the products as two bf16 parts (2^-17).
+ * Rows of the cache that a node does not see do not reach it.  A V row of a draft
+ * with an infinity or a NaN (e4m3: a NaN code, or a scale that is not finite) makes
+ * the whole O row and the LSE of the nodes that see it NaN.
+ * Precision: as attn_fwd_paged; where that names the largest V scale that a query
+ * sees, 16 times the smallest of the drafts' counts as well.
  */
 size_t attn_fwd_paged_tree_workspace_size(int B, int Nq, int H, int H_kv, int d, int prefix_len,
                                           int max_pages, int page_size);

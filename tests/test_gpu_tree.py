@@ -179,13 +179,14 @@ def test_what_a_node_does_not_see_cannot_reach_it(d, Nq, G, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-def test_drafts_that_no_node_sees_are_not_read(fp8):
-    """Their pages may be anything; those of seen ones are refused and hidden."""
+def test_pages_of_drafts_outside_the_cache_are_reported_and_hidden(fp8):
+    """Of drafts that no node sees (the results are the same), then of the nodes'."""
     parents = torch.tensor([-1, 0, 1, -2, -2, -2] + [-2] * 14, dtype=torch.int32, device=DEV)
     p = Tree([52], 0, 20, 4, 2, 128, 16, fp8, seed=12, parents=parents)          # drafts: tokens 32 to 51
+    p.check(*p.run())
     p.table[0, 3] = -5                                 # tokens 48 to 51, no nodes
     o, lse = p.run()
-    p.check(o, lse)
+    p.check(o, lse, status=-5)
     p.table[0, 2] = p.cache.k.shape[0]                 # the nodes' page
     o2, l2 = p.run()
     assert api.device_status() == (-5, 0x102)
