@@ -911,6 +911,23 @@ def _rows(t, name, dev):
     return T, H, d, stride if T > 1 else H * d
 
 
+def _new_rows(x, dev, stream):
+    """A contiguous bf16 tensor of x's shape, memory of the launch's stream (that of
+    another may still be in use there)."""
+    if stream is None:
+        if _raw_empty is not None and _current_device() == dev and _unwatched():
+            shape = tuple(x.shape)
+            row = shape[-1] * shape[-2]
+            strides = (row, shape[-1], 1) if len(shape) == 3 else (row * shape[1], row, shape[-1], 1)
+            try:
+                return _raw_empty(shape, strides, _BF16)
+            except TypeError:        # (another signature: the public way, below)
+                pass
+        return torch.empty(x.shape, dtype=_BF16, device=x.device)
+    with torch.cuda.stream(_torch_stream(stream, x.device)):
+        return torch.empty(x.shape, dtype=_BF16, device=x.device)
+
+
 def attn_rope(q, k, rope_cos, rope_sin, positions=None, pair_axis=None, interleaved: bool = False,
               inverse: bool = False, out_q=None, out_k=None, stream=None):
     """Rotary positions of q and k (k may be None), one launch; inverse: the
@@ -962,11 +979,7 @@ def attn_rope(q, k, rope_cos, rope_sin, positions=None, pair_axis=None, interlea
             outs.append((None, None, 0))
             continue
         if out is None:
-            if stream is None:
-                out = torch.empty(x.shape, dtype=_BF16, device=x.device)
-            else:       # (memory of the launch's stream: that of another may still be in use there)
-                with torch.cuda.stream(_torch_stream(stream, x.device)):
-                    out = torch.empty(x.shape, dtype=_BF16, device=x.device)
+            out = _new_rows(x, dev, stream)
             outs.append((out, out.data_ptr(), heads * d))
             continue
         if out.shape != x.shape:
@@ -1015,11 +1028,7 @@ def attn_kv_append(q, k, v, positions, slots, cache: KVCache, rope_cos, rope_sin
         raise ValueError("slots must be a contiguous int64 (T,) tensor on the cache's device")
     if q is not None:
         if out_q is None:
-            if stream is None:
-                out_q = torch.empty((T, H, d), dtype=_BF16, device=q.device)
-            else:       # (memory of the launch's stream: that of another may still be in use there)
-                with torch.cuda.stream(_torch_stream(stream, q.device)):
-                    out_q = torch.empty((T, H, d), dtype=_BF16, device=q.device)
+            out_q = _new_rows(q, dev, stream)
             q_out_stride = H * d
         else:
             if out_q.shape != q.shape:

@@ -1129,8 +1129,8 @@ int check_rope(attn::RopeParams* p, int T, int H, int H_kv, int d, const long lo
     if (n_axes < 1 || n_axes > 4) return fail(ATTN_ERR_UNSUPPORTED, "%d axes (supported: 1 to 4)", n_axes);
     if (table_rows < 0) return fail(ATTN_ERR_INVALID_ARG, "negative size (table_rows=%lld)", table_rows);
     if (n_axes > 1 && !pair_axis) return fail(ATTN_ERR_INVALID_ARG, "null pair_axis (%d axes)", n_axes);
-    for (int i = 0; i < rot / 2; ++i) {
-        const int a = pair_axis ? pair_axis[i] : 0;
+    for (int i = 0; pair_axis && i < rot / 2; ++i) {
+        const int a = pair_axis[i];
         if (a >= n_axes) return fail(ATTN_ERR_INVALID_ARG, "pair %d turns by axis %d of %d", i, a, n_axes);
         p->axes[i >> 4] |= static_cast<uint32_t>(a) << (2 * (i & 15));
     }
@@ -1335,7 +1335,7 @@ int attn_kv_accept(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
     if (!accepted) return fail(ATTN_ERR_INVALID_ARG, "null pointer");
     if ((reinterpret_cast<uintptr_t>(accepted) & 3u) != 0)
         return fail(ATTN_ERR_INVALID_ARG, "accepted must be 4-byte aligned");
-    if (static_cast<long long>(B) * H_kv > (1ll << 29)) return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
+    if (static_cast<long long>(B) * H_kv > (1ll << 28)) return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
     attn::KvAcceptParams p{};
     p.k_cache = k_cache;
     p.v_cache = v_cache;
@@ -1349,7 +1349,6 @@ int attn_kv_accept(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
     p.Nq = Nq;
     p.M = M;
     p.H_kv = H_kv;
-    p.by_heads = attn::FastDiv(H_kv);
     p.d = d;
     p.num_pages = num_pages;
     p.page_shift = log2_of(page_size);

@@ -127,7 +127,7 @@ struct KvAcceptParams {
     const int* seq_lens;         // (B,)
     const int* accepted;         // (B, M)
     int B, Nq, M, H_kv, d, num_pages, page_shift, max_pages;
-    FastDiv by_heads;            // H_kv
+    FastDiv by_blocks;           // CTAs of a sequence
     bool fp8;
     int* status;
 };

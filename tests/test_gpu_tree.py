@@ -103,6 +103,89 @@ def test_one_tree_for_all_sequences_in_any_order_of_nodes(fp8):
     assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
+# lens, prefix, Nq, H, H_kv, d, page; the plan: every way in which a row that is no node
+# leaves the kernels (written at once, or told to either form of the join).
+EMPTIES = [
+    ([5 + b % 3 for b in range(300)], 0, 4, 8, 2, 64, 16, ("stream", True)),
+    ([60 + b % 5 for b in range(160)], 0, 40, 2, 2, 128, 16, ("tile", True)),
+    ([90, 41], 70, 4, 8, 2, 128, 16, ("stream", False)),
+    ([9000, 70], 0, 6, 4, 1, 64, 16, ("stream", False)),               # many ranges
+    ([5000, 300], 200, 40, 4, 1, 128, 64, ("tile", False)),
+    ([700], 90, 130, 1, 1, 256, 64, ("tile", False)),
+]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("case", EMPTIES, ids=lambda c: "x".join(map(str, c[1:])) + "_" + str(len(c[0])))
+def test_rows_that_are_no_nodes_are_empty_in_every_mode(case, fp8):
+    *shape, plan = case
+    lens, _, Nq = shape[:3]
+    parents = random_parents(gen(5), len(lens), Nq, 3)
+    parents[:, Nq - Nq // 3:] = -2
+    parents[-1] = -2                                   # a whole sequence without a tree
+    p = Tree(*shape, fp8=fp8, seed=21, parents=parents)
+    got = api.paged_plan(len(lens), Nq, shape[3], shape[4], shape[5], shape[1], p.table.shape[1], shape[6])
+    assert (got.own_kernel, got.direct) == plan
+    o, lse = p.run()
+    p.check(o, lse)
+    none = parents < -1
+    assert bool((o[none] == 0).all()) and bool((lse.transpose(1, 2)[none] == -math.inf).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 256])
+def test_the_largest_tree_and_a_value_that_is_not_finite_in_each_of_its_tiles(d, fp8):
+    """512 nodes that begin inside a tile of keys; bad values 64 keys apart: each makes the
+    nodes NaN that see it, and no other."""
+    Nq, n = 512, 512 + 77
+    p = Tree([n], 0, Nq, 1, 1, d, 32, fp8, seed=22, width=40)
+    p.check(*p.run())
+    o0, l0 = p.run()
+    paths = p.rows(0)
+    seen_by = lambda node: torch.tensor([node in s for s in paths], device=DEV)
+    for node in range(13, Nq, 64):
+        at = n - Nq + node
+        slot = torch.tensor([int(p.table[0, at // 32]) * 32 + at % 32], device=DEV)
+        v = p.v[1][at:at + 1].clone()
+        v[..., 1] = NAN
+        api.attn_kv_write(p.k[1][at:at + 1], v, slot, p.cache)
+        o, l = p.run()
+        sees = seen_by(node)
+        assert bool(torch.isnan(o[0][sees]).all()) and torch.equal(o[0][~sees], o0[0][~sees])
+        assert bool(torch.isnan(l[0, 0][sees]).all()) and torch.equal(l[0, 0][~sees], l0[0, 0][~sees])
+        api.attn_kv_write(p.k[1][at:at + 1], p.v[1][at:at + 1], slot, p.cache)
+    assert api.device_status()[0] == 0
+
+
+def test_bad_parents_of_larger_trees():
+    """The tile kernel's walk: out of range, circles, children of rows that are no nodes."""
+    parents = torch.arange(-1, 79, dtype=torch.int32, device=DEV)
+    for i, to in ((10, 200), (30, 40), (50, 50), (60, -2), (70, 1 << 30)):
+        parents[i] = to
+    for fp8 in (False, True):
+        p = Tree([200, 81], 50, 80, 2, 1, 128, 16, fp8, seed=23, parents=parents)
+        p.check(*p.run(), status=-5)
+        p.run()
+        assert api.device_status() == (-5, 0x105)
+
+
+@pytest.mark.parametrize("case", [([168], 0, 40, 1, 1, 128, 16), ([168, 128 + 33], 0, 33, 4, 2, 64, 32), ([192], 0, 64, 1, 1, 256, 16),
+                                  ([12, 9], 30, 8, 4, 2, 128, 16), ([40], 0, 32, 1, 1, 64, 16)])
+def test_ranges_of_nodes_alone_with_scales_of_any_size(case):
+    """A stream, a range or a warp that begins with nodes has no key that all rows see."""
+    p = Tree(*case, fp8=True, seed=35, width=3)
+    g = gen(36)
+    for b, vs in enumerate(p.v):
+        if b == 0:
+            continue
+        nodes = vs[-p.Nq:]
+        nodes *= torch.exp2(torch.randint(-20, 21, (len(nodes), 1, 1), generator=g, device=DEV).float()).to(torch.bfloat16)
+        nodes[::7] = 0.0
+        i = torch.arange(len(vs), device=DEV)
+        api.attn_kv_write(p.k[b], vs, p.table[b - 1].long()[i // p.ps] * p.ps + i % p.ps, p.cache)
+    p.check(*p.run())
+
+
 def test_a_chain_is_the_causal_mask():
     """The same tokens through attn_fwd_paged: each is within its own rounding of the
     same values (bf16 weights on one side, results in bf16 on both)."""
