@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.cuh"
 #include "sm103_bulk.cuh"
@@ -162,7 +163,8 @@ namespace {
 // W warps per row, D / 32 columns a lane; lane x of a warp has the weight of part
 // 32 k + x; the warp sums the parts x = w, w + W, .., four at a time (independent
 // loads), and the warps' sums meet in shared memory.
-template <int D, int W>
+// TREE: a row that is no node stays empty.
+template <int D, int W, bool TREE>
 __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant__ PagedParams p) {
     constexpr int V = D / 32;
     __shared__ float joined[4][D];
@@ -230,8 +232,7 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
                     for (int v = 0; v < V; ++v) acc[v] += g[y] * f[y][v];
             }
         };
-        // (a row that is no node stays empty)
-        if (!(p.parents && mm == kNoNode)) {
+        if (!(TREE && mm == kNoNode)) {
             add(0, l2[0]);
             if (parts > 32) add(1, l2[1]);
             if (parts > 64) add(2, l2[2]);
@@ -263,21 +264,25 @@ __global__ void __launch_bounds__(128) paged_merge_kernel(const __grid_constant_
     }
 }
 
-template <int D>
+template <int D, bool TREE>
 cudaError_t merge_d(const PagedParams& p, cudaStream_t stream) {
     const long long rows = static_cast<long long>(p.B) * p.Nq * p.H;
     // A warp sums 8 parts in two rounds of loads; with more, four warps share
     // a row (16 rows of 28 parts: 25.5 us against 28.1 for the whole call; 32768
     // rows of 2 parts: 169 us with four warps, 149 with one).
     if (p.prefix_parts + p.own_parts > 8)
-        return launch_kernel(paged_merge_kernel<D, 4>, static_cast<unsigned>(rows), 128, 0, true, stream, p);
-    return launch_kernel(paged_merge_kernel<D, 1>, static_cast<unsigned>((rows + 3) / 4), 128, 0, true, stream, p);
+        return launch_kernel(paged_merge_kernel<D, 4, TREE>, static_cast<unsigned>(rows), 128, 0, true, stream, p);
+    return launch_kernel(paged_merge_kernel<D, 1, TREE>, static_cast<unsigned>((rows + 3) / 4), 128, 0, true, stream, p);
 }
 
 }  // namespace
 
 cudaError_t run_paged_merge(const PagedParams& p, cudaStream_t stream) {
-    return p.d == 64 ? merge_d<64>(p, stream) : p.d == 128 ? merge_d<128>(p, stream) : merge_d<256>(p, stream);
+    const auto merge = [&](auto tree) {
+        constexpr bool TREE = decltype(tree)::value;
+        return p.d == 64 ? merge_d<64, TREE>(p, stream) : p.d == 128 ? merge_d<128, TREE>(p, stream) : merge_d<256, TREE>(p, stream);
+    };
+    return p.parents ? merge(std::true_type{}) : merge(std::false_type{});
 }
 
 }  // namespace attn

@@ -855,7 +855,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 const bool whole = all == 0xffffffffu;
                 const bool diagonal = key0 / BN >= diag;
                 uint32_t* poison = bars->poison[min(max(key0 / BN - diag, 0), Cfg::DIAG_TILES - 1)];
-                float v = 0.0f, most0 = diagonal ? bars->most[t] : 0.0f;
+                float v = 0.0f, least_node = 0.0f;
                 if (TREE && u == 0 && !w.prefix && key0 >= diag_key) {
                     uint32_t least = 0x7f800000u;
                     if (ct < BN && ((valid[ct >> 5] >> (ct & 31)) & 1u)) {
@@ -866,13 +866,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     if (lane == 0) bars->low[ct >> 5] = __uint_as_float(least);
                     if (!named_barrier_and(1, 128, ok)) return false;
                     const float x = fminf(fminf(bars->low[0], bars->low[1]), fminf(bars->low[2], bars->low[3]));
-                    most0 = x < INFINITY ? 16.0f * x : 0.0f;
+                    least_node = x < INFINITY ? 16.0f * x : 0.0f;
                 }
                 if (ct < BN && ((valid[ct >> 5] >> (ct & 31)) & 1u)) {
                     v = sScale[slot * 2 * BN + BN + ct];
                     if (diagonal && key0 + ct >= diag_key) {
                         const float ref = w.pair || t == 0 ? vref0 : vref1;
-                        const float most = fmaxf(64.0f * ref, most0);
+                        const float most = fmaxf(64.0f * ref, TREE ? fmaxf(least_node, bars->most[t]) : bars->most[t]);
                         if (!(v <= most)) {
                             atomicOr(&poison[(v < INFINITY ? 4 * Cfg::DIAG_TILES : 0) + (ct >> 5)], 1u << (ct & 31));
                             v = 0.0f;
