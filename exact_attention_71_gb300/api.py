@@ -879,34 +879,36 @@ def _axis_bytes(pair_axis):
 def _check_rope(rope_cos, rope_sin, pair_axis, d, dev):
     """(table rows, rotary elements, host array of the pairs' axes, number of axes)"""
     shape = rope_cos.shape
-    for t in (rope_cos, rope_sin):
-        if t.dtype != _F32 or t.shape != shape or len(shape) != 2 or t.get_device() != dev or not t.is_contiguous():
-            raise ValueError("rope_cos and rope_sin must be contiguous float32 (rows, rot / 2) tensors on q's device")
-    half = shape[1]
+    if (len(shape) != 2 or rope_sin.shape != shape or rope_cos.dtype != _F32 or rope_sin.dtype != _F32
+            or rope_cos.get_device() != dev or rope_sin.get_device() != dev or not rope_cos.is_contiguous()
+            or not rope_sin.is_contiguous()):
+        raise ValueError("rope_cos and rope_sin must be contiguous float32 (rows, rot / 2) tensors on q's device")
+    rows, half = shape
     if pair_axis is None:
-        return shape[0], 2 * half, None, 1
+        return rows, 2 * half, None, 1
     if len(pair_axis) != half:
         raise ValueError("pair_axis must have an axis for each of the tables' columns")
     axes, n = _axis_bytes(pair_axis if type(pair_axis) is tuple else tuple(int(a) for a in pair_axis))
-    return shape[0], 2 * half, axes, n
+    return rows, 2 * half, axes, n
 
 
 def _rows(t, name, dev):
     """(tokens, heads, d, token stride) of (.., heads, d) rows whose tokens are evenly spaced."""
-    shape, st = t.shape, t.stride()
-    if t.dtype != _BF16 or t.get_device() != dev or not t.is_cuda:
+    if dev < 0 or t.dtype != _BF16 or t.get_device() != dev:
         raise ValueError(f"{name} must be a bf16 CUDA tensor on one device with the others")
+    shape, st = t.shape, t.stride()
     if len(shape) == 3:
         T, H, d = shape
-        stride = st[0]
+        stride, head, step = st
     elif len(shape) == 4:
-        T, H, d = shape[0] * shape[1], shape[2], shape[3]
-        stride = st[1] if shape[1] > 1 else st[0]
-        if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * st[1]:
+        B, N, H, d = shape
+        T, head, step = B * N, st[2], st[3]
+        stride = st[1] if N > 1 else st[0]
+        if B > 1 and N > 1 and st[0] != N * stride:
             raise ValueError(f"the tokens of {name} must be evenly spaced")
     else:
         raise ValueError(f"{name} must be (B, N, heads, d) or (tokens, heads, d)")
-    if T and H and (st[-1] != 1 or (H > 1 and st[-2] != d)):
+    if (step != 1 or (H > 1 and head != d)) and T and H:
         raise ValueError(f"a token's heads must be contiguous in {name}")
     return T, H, d, stride if T > 1 else H * d
 

@@ -17,14 +17,15 @@
 // of the tables.  Several: a warp fetches its tokens' angles a pair a lane, whatever the
 // pair's axis, and hands them round in shared memory (with float4 loads where four
 // pairs share an axis, and single ones elsewhere: 4999 tokens of 24 heads on three
-// alternating axes 15.8 us against 12.7, 7007 of 32 on sections 24.9 against 19.3; a
+// alternating axes 15.8 us against 12.3, 7007 of 32 on sections 24.9 against 19.1; a
 // CTA's angles together, behind a barrier: 13.4 and 20.7, and one axis 30 against 26).
 //
-// Order of the loads: positions and angles first, since the rows' loads would queue
-// before them (32768 tokens of 48 heads into an e4m3 cache 145 us the other way round,
-// 125 this way), then all rows, then the arithmetic.
-// Measured: 8192 tokens of 40 heads of 128, one axis, 26.3 us, 6.46 TB/s (95 % of the
-// copy rate); the 32768 tokens 125 us, 6.06 TB/s (89 %); 32 tokens 2.6 us.
+// Order of the loads: positions first, since the rows' loads would queue before them
+// (32768 tokens of 48 heads into an e4m3 cache 145 us the other way round).
+// Measured: 8192 tokens of 40 heads of 128, one axis, 26.0 us, 6.53 TB/s (96 % of the
+// copy rate); those 32768 tokens 119.8 us, 6.32 TB/s (93 %), bf16 122.0 us, 6.74 TB/s;
+// on three axes 155 and 151 us (a warp's chain of position, angles, rows); 32 tokens
+// 2.9 us, a launch.
 #include <algorithm>
 
 #include "kv_rows.cuh"
@@ -33,7 +34,7 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 128, kBlocks = 7;                 // of a CTA; CTAs an SM (72 registers)
+constexpr int kThreads = 128;
 constexpr int kHeads = 4, kHeadsKv = 2;                    // heads a lane where there are many rows
 
 enum : int { ROPE = 0, APPEND_BF16 = 1, APPEND_E4M3 = 2 };
@@ -139,10 +140,20 @@ __device__ __forceinline__ uint4 load_once(const void* at) {
     return v;
 }
 
+template <bool ONCE>
 __device__ __forceinline__ Row16 load_chunks(const void* base, long long at, const LaneMap& m) {
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
-    return {load_once(src + m.c0), load_once(src + m.c1)};
+    if constexpr (ONCE) return {load_once(src + m.c0), load_once(src + m.c1)};
+    else return {src[m.c0], src[m.c1]};
 }
+
+// Whether a lane's rows are loaded between its position and its angles, by plain loads
+// and with eight CTAs an SM (64 registers) instead of seven: appending with one axis.  Microseconds,
+// this way | the other: 32768 tokens of 48 heads of 128 bf16 cache 122.0 | 126.7, e4m3
+// 119.8 | 125.5; of 64 65.2 | 65.1, 63.7 | 65.1; attn_rope's 8192 tokens of 40 heads 27.3 |
+// 26.0; three axes: 7007 tokens of 32 heads 25.1 | 19.1, appending 4999 of 24 14.6 | 12.3.
+template <bool AXES, int MODE>
+constexpr bool kRowsEarly = MODE != ROPE && !AXES;
 
 __device__ __forceinline__ void store_chunks(void* base, long long at, const LaneMap& m, const Row16& x) {
     uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at);
@@ -158,9 +169,10 @@ __device__ __forceinline__ void store_chunks8(void* base, long long at, const La
 
 // HQ heads a lane of q (and k of attn_rope), HK of the cache's k and v.
 template <int D, int HQ, int HK, bool AXES, int MODE>
-__global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kThreads, kRowsEarly<AXES, MODE> ? 8 : 7) rope_kernel(const __grid_constant__ RopeParams p) {
     constexpr int LANES = D / 16, PASS = kThreads / LANES, WARP = 32 / LANES;      // rows of a CTA, of a warp
     constexpr int HM = HQ > 2 * HK ? HQ : 2 * HK;          // rows in registers
+    constexpr bool EARLY = kRowsEarly<AXES, MODE>;
     const bool second = blockIdx.x < p.k_blocks;           // k (append: k and v)
     const FastDiv by = second ? p.by_k_groups : p.by_q_groups;
     const unsigned x = (blockIdx.x - (second ? 0u : p.k_blocks)) * PASS + threadIdx.x / LANES;
@@ -194,6 +206,23 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
     if (take && !fine) report(p.status, SITE_ROPE_POSITION);
     take = take && fine;
 
+    Row16 r[HM];
+    const auto load_rows = [&] {
+        if (rows_of_one) {
+            const void* src = second ? p.k : p.q;
+            const long long from = t * (second ? p.k_stride : p.q_stride);
+#pragma unroll
+            for (int i = 0; i < HQ; ++i) r[i] = in && h0 + i < heads ? load_chunks<!EARLY>(src, from + (h0 + i) * D, m) : Row16{};
+        } else {
+#pragma unroll
+            for (int i = 0; i < HK; ++i) {
+                const bool have = in && h0 + i < heads;
+                r[2 * i] = have ? load_chunks<!EARLY>(p.k, t * p.k_stride + (h0 + i) * D, m) : Row16{};
+                r[2 * i + 1] = have ? load_chunks<!EARLY>(p.v, t * p.v_stride + (h0 + i) * D, m) : Row16{};
+            }
+        }
+    };
+    if constexpr (EARLY) load_rows();
     float4 cs[2], sn[2];
 #pragma unroll
     for (int y = 0; y < 2; ++y) cs[y] = sn[y] = make_float4(0, 0, 0, 0);
@@ -206,13 +235,34 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
         const unsigned first = __shfl_sync(0xffffffffu, t, 0), last = min(__shfl_sync(0xffffffffu, t, 31), p.T - 1u);
         const int pairs = in || first < static_cast<unsigned>(p.T) ? static_cast<int>(last - first + 1) * half : 0;
         const auto place = [&](int i) { return p.interleaved ? i : ((i >> 2) & 1) * (half / 2) + ((i >> 3) << 2) + (i & 3); };
-        for (int y = threadIdx.x % 32; y < pairs; y += 32) {
+        // Where pair y's angles stand in the tables (-1: nowhere), and in `mine`.
+        const auto table_at = [&](int y) -> long long {
             const int token = p.by_half.div(y), i = y - token * half;
             const long long row = position(first + token, (p.axes[i >> 4] >> (2 * (i & 15))) & 3u);
-            if (row >= 0 && row < p.rows) {
-                mine[token * p.rot + place(i)] = __ldg(p.cos + row * half + i);
-                mine[token * p.rot + half + place(i)] = __ldg(p.sin + row * half + i);
-            }
+            return row >= 0 && row < p.rows ? row * half + i : -1;
+        };
+        const auto put = [&](int y, long long from, float c, float s) {
+            const int token = p.by_half.div(y), i = y - token * half;
+            if (from < 0) return;
+            mine[token * p.rot + place(i)] = c;
+            mine[token * p.rot + half + place(i)] = s;
+        };
+        // The first two pairs of a lane (one token's, at 128 elements) together.
+        const int y0 = threadIdx.x % 32;
+        long long from[2];
+        float c2[2], s2[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) from[k] = y0 + 32 * k < pairs ? table_at(y0 + 32 * k) : -1;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            c2[k] = from[k] >= 0 ? __ldg(p.cos + from[k]) : 0.0f;
+            s2[k] = from[k] >= 0 ? __ldg(p.sin + from[k]) : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) put(y0 + 32 * k, from[k], c2[k], s2[k]);
+        for (int y = y0 + 64; y < pairs; y += 32) {
+            const long long at = table_at(y);
+            if (at >= 0) put(y, at, __ldg(p.cos + at), __ldg(p.sin + at));
         }
         __syncwarp();
         if (take) {
@@ -237,21 +287,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
         for (int y = 0; y < 2; ++y) sn[y] = make_float4(-sn[y].x, -sn[y].y, -sn[y].z, -sn[y].w);
     }
 
-    // The rows, once the angles' loads are on their way.
-    Row16 r[HM];
-    if (rows_of_one) {
-        const void* src = second ? p.k : p.q;
-        const long long from = t * (second ? p.k_stride : p.q_stride);
-#pragma unroll
-        for (int i = 0; i < HQ; ++i) r[i] = in && h0 + i < heads ? load_chunks(src, from + (h0 + i) * D, m) : Row16{};
-    } else {
-#pragma unroll
-        for (int i = 0; i < HK; ++i) {
-            const bool have = in && h0 + i < heads;
-            r[2 * i] = have ? load_chunks(p.k, t * p.k_stride + (h0 + i) * D, m) : Row16{};
-            r[2 * i + 1] = have ? load_chunks(p.v, t * p.v_stride + (h0 + i) * D, m) : Row16{};
-        }
-    }
+    if constexpr (!EARLY) load_rows();
 
     if (rows_of_one) {
         void* dst = second ? p.k_out : p.q_out;
@@ -307,9 +343,12 @@ cudaError_t launch(RopeParams p, cudaStream_t stream) {
 
 template <int D, int MODE>
 cudaError_t launch_mode(const RopeParams& p, cudaStream_t stream) {
-    // Several heads a lane once the rows fill the machine.
+    // Several heads a lane once there are rows enough.  Microseconds, one head a lane |
+    // several: attn_rope, 40 heads of 128, 64 tokens 2.3 | 2.6, 512 3.3 | 3.1, 1024 4.6 | 3.8,
+    // 4096 13.7 | 11.5, 32 heads on three axes, 512 4.5 | 4.3, 4096 20.3 | 12.2; appending, 40 and
+    // 8 heads, 32 tokens 2.8 | 3.8, 512 3.8 | 4.6, 1024 5.8 | 5.5, 2048 11.1 | 9.7.
     const long long lanes = static_cast<long long>(p.T) * (p.H + p.H_kv) * (D / 16);
-    const bool many = lanes >= 2ll * kPlanSms * 2048;
+    const bool many = lanes >= kPlanSms * (MODE == ROPE ? 1024ll : 2048ll);
     if (p.n_axes > 1)
         return many ? launch<D, kHeads, kHeadsKv, true, MODE>(p, stream) : launch<D, 1, 1, true, MODE>(p, stream);
     return many ? launch<D, kHeads, kHeadsKv, false, MODE>(p, stream) : launch<D, 1, 1, false, MODE>(p, stream);

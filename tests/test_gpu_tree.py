@@ -107,7 +107,10 @@ def test_one_tree_for_all_sequences_in_any_order_of_nodes(fp8):
 # leaves the kernels (written at once, or told to either form of the join).
 EMPTIES = [
     ([5 + b % 3 for b in range(300)], 0, 4, 8, 2, 64, 16, ("stream", True)),
+    ([60 + b % 9 for b in range(70)], 0, 7, 16, 4, 64, 16, ("stream", True)),
+    ([150 + b % 5 for b in range(160)], 0, 5, 8, 2, 128, 16, ("stream", True)),
     ([60 + b % 5 for b in range(160)], 0, 40, 2, 2, 128, 16, ("tile", True)),
+    ([290 + b % 5 for b in range(160)], 0, 40, 2, 2, 128, 16, ("tile", True)),
     ([90, 41], 70, 4, 8, 2, 128, 16, ("stream", False)),
     ([9000, 70], 0, 6, 4, 1, 64, 16, ("stream", False)),               # many ranges
     ([5000, 300], 200, 40, 4, 1, 128, 64, ("tile", False)),
