@@ -1088,6 +1088,8 @@ int paged_call(const char* name, bool tree, const void* q, const void* k_cache, 
     p.stream_tile = plan.stream_tile;
     p.parents = parents;
     p.parents_stride = parents_stride;
+    // (CTAs replace one another as they finish: see the tile kernel)
+    p.longest_first = tree && B > 1 && B <= 128 && plan.prefix_items + plan.own_items > attn::kPlanSms;
     attn::paged_divisors(p);
     p.scale_log2 = resolve_scale(scale, d) * 1.4426950408889634f;
     p.fp8 = cache_dtype == ATTN_CACHE_E4M3;

@@ -161,6 +161,7 @@ struct PagedParams {
     // last own tokens at b * parents_stride; NULL: no tree.
     const int* parents;
     long long parents_stride;
+    bool longest_first;          // the tile kernel takes long sequences before short ones
     FastDiv by_G, by_per, by_heads;              // G, Nq G, H_kv
     FastDiv by_prefix_parts, by_own_parts;
     FastDiv by_prefix_rows, by_own_rows;         // streaming CTAs that share keys

@@ -52,10 +52,12 @@
 // Trees (attn_fwd_paged_tree): a row sees the tokens before the drafts and its node's
 // path, which its softmax thread walks once, beside the copy of its query row, into
 // bits in local memory; only key tiles that hold drafts read them.  64 drafts x 32 heads of
-// 128 for each of 32 sequences of up to 4096 tokens: 106.8 us, a chain of as many 101,
-// 944 TFLOP/s.  (The drafts in a kernel of their own, joined with partial results over the
-// tokens before them, took 130: 65536 rows written and read once more, and the
-// latency of lists, pages and rows one after the other.)
+// 128 for each of 32 sequences of up to 4096 tokens: 101.8 us, 990 TFLOP/s and 4.3 TB/s (a
+// chain of as many 101): 256 CTAs, of which 152 at a time ask for 6.7 TB/s, and a CTA's
+// start and end.  Sequences go to the CTAs the longest first, where there are more CTAs
+// than SMs (in their order: 106.6).  (The drafts in a kernel of their own, joined with
+// partial results over the tokens before them, took 130: 65536 rows written and read
+// once more, and the latency of lists, pages and rows one after the other.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -297,7 +299,34 @@ __device__ __forceinline__ int row_limit(const PagedParams& p, const TileItem& w
     return max(0, w.len - p.Nq + 1 + static_cast<int>(p.by_G.div(r)));
 }
 
-template <class Cfg>
+// The sequence that is n-th by its key tiles, the longest first (of 128 at most; equally
+// long ones in their order).  Whole warp: the n-th largest of distinct keys, four a
+// lane, bit by bit.
+__device__ __forceinline__ int nth_longest(const PagedParams& p, int n) {
+    const int lane = threadIdx.x & 31;
+    const int room = p.max_pages << p.page_shift;
+    uint32_t key[4], top = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int b = lane + 32 * k;
+        key[k] = 0;
+        if (b < p.B) key[k] = ((static_cast<uint32_t>(min(max(__ldg(p.seq_lens + b), 0), room)) + 127u) >> 7 << 7 | (127 - b)) + 1;
+        top = max(top, key[k]);
+    }
+    uint32_t found = 0;
+    for (int bit = 31 - __clz(__reduce_max_sync(0xffffffffu, top)); bit >= 0; --bit) {
+        const uint32_t want = (found | 1u << bit) >> bit;
+        int count = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (32 * k < p.B) count += __popc(__ballot_sync(0xffffffffu, key[k] >> bit == want));
+        if (count > n) found |= 1u << bit;
+        else n -= count;
+    }
+    return 127 - static_cast<int>((found - 1) & 127u);
+}
+
+template <class Cfg, bool TREE>
 __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
     TileItem w;
     unsigned x = blockIdx.x;
@@ -317,6 +346,8 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
     y = by_ctas.div(x);
     const int split = x - y * by_ctas.d;
     w.seq = w.prefix ? 0 : y;
+    if constexpr (TREE)
+        if (!w.prefix && p.longest_first) w.seq = nth_longest(p, y);
     w.table = w.prefix ? p.prefix_table : p.table + w.seq * p.table_stride;
     int len = p.prefix_len;
     if (!w.prefix) {
@@ -539,7 +570,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     launch_dependents();           // (nothing of this call that follows reads what precedes it)
-    const TileItem w = tile_item<Cfg>(p);
+    const TileItem w = tile_item<Cfg, TREE>(p);
     // From this key on the CTA's rows may see different keys; its tile.
     int diag_key = w.len;
     if (TREE && !w.prefix) diag_key = max(0, w.len - p.Nq);
