@@ -994,7 +994,7 @@ int check_table(const int* table, long long table_stride, int max_pages, int pag
 
 // Sizes of an attention call, and its plan (empty problems: as it is).
 int check_paged_sizes(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size,
-                      attn::PagedPlan* plan) {
+                      attn::PagedPlan* plan, bool tree = false) {
     if (B < 0 || Nq < 0 || H < 0 || prefix_len < 0 || max_pages < 0)
         return fail(ATTN_ERR_INVALID_ARG, "negative size (B=%d Nq=%d H=%d prefix_len=%d max_pages=%d)", B, Nq, H,
                     prefix_len, max_pages);
@@ -1009,7 +1009,7 @@ int check_paged_sizes(int B, int Nq, int H, int H_kv, int d, int prefix_len, int
     // long long by the plan: their indices are ints too.
     if (static_cast<long long>(B) * Nq > (1ll << 30) || static_cast<long long>(B) * Nq * std::max(H, 1) > (1ll << 30))
         return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
-    if (static_cast<long long>(B) * Nq * H > 0) *plan = attn::paged_plan(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size);
+    if (static_cast<long long>(B) * Nq * H > 0) *plan = attn::paged_plan(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, tree);
     if (plan->blocks > 0x7fffffffll) return fail(ATTN_ERR_INVALID_ARG, "problem too large for one launch");
     return ATTN_OK;
 }
@@ -1030,7 +1030,7 @@ int paged_call(const char* name, bool tree, const void* q, const void* k_cache, 
     int rc = check_cache(k_cache, v_cache, k_scale, v_scale, H_kv, d, num_pages, page_size, cache_dtype);
     if (rc != ATTN_OK) return rc;
     attn::PagedPlan plan;
-    if ((rc = check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan)) != ATTN_OK) return rc;
+    if ((rc = check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan, tree)) != ATTN_OK) return rc;
     if (tree && (rc = check_tree(Nq)) != ATTN_OK) return rc;
     if (static_cast<long long>(B) * Nq * H == 0) return ATTN_OK;
     if ((rc = check_table(block_table, table_stride, max_pages, page_size, seq_lens)) != ATTN_OK) return rc;
@@ -1308,7 +1308,7 @@ int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, cons
 size_t attn_fwd_paged_tree_workspace_size(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages,
                                           int page_size) {
     attn::PagedPlan plan;
-    if (check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan) != ATTN_OK) return 0;
+    if (check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan, true) != ATTN_OK) return 0;
     return check_tree(Nq) == ATTN_OK ? plan.bytes : 0;
 }
 

@@ -227,7 +227,17 @@ constexpr double kStreamFixed = 300.0;
 // Fills in the divisors, from the other parameters.
 void paged_divisors(PagedParams& p);
 
-PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size);
+// A tree's short prefix streams beside the own tokens, more rows than stream_rows or
+// not: one launch less, and a tile CTA's start and end (6 us, 9 with an e4m3 cache) is
+// most of what it would take.  By 2^x = H_kv x rows x keys x d, where the prefix has 64 row
+// tiles of 16 in all heads together at most; microseconds of a call with the tile kernel |
+// streaming, 8 heads, 128 rows, d = 128: 2^25 bf16 13.4 | 10.1, e4m3 16.8 | 10.6; 2^26 13.5 |
+// 11.8, 16.9 | 12.0; 2^27 14.2 | 15.6, 17.6 | 15.9; at 2^26 64 rows, d = 256, 13.6 | 12.5,
+// 18.2 | 12.5; 2 heads, 512 rows, d = 64, 10.8 | 9.8, 14.6 | 12.3.  With more row tiles (16
+// heads, 320 rows, d = 128, 2^26) 16.4 | 22.3, 18.7 | 22.3.
+constexpr long long kTreeStreamWork = 1ll << 26, kTreeStreamTiles = 64;
+
+PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size, bool tree);
 
 // Runs `set` once per device (bit per ordinal; racing threads may run it twice,
 // which is harmless).

@@ -63,14 +63,16 @@ int tile_ctas(int d, long long units, long long steps, double other) {
 
 }  // namespace
 
-PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size) {
+PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size, bool tree) {
     PagedPlan plan;
     const long long rows = static_cast<long long>(Nq) * (H / H_kv);      // of one sequence and key/value head
     const long long own = static_cast<long long>(max_pages) * page_size;
     const int bn = d == 256 ? 64 : 128;
     const long long all = B * rows;                                      // the prefix's rows of a key/value head
     const bool own_stream = rows <= stream_rows(d);
-    plan.prefix_stream = prefix_len > 0 && all <= stream_rows(d);
+    const bool tree_stream = tree && own_stream && H_kv * up(all, 16) <= kTreeStreamTiles &&
+                             H_kv * all * prefix_len * d <= kTreeStreamWork;
+    plan.prefix_stream = prefix_len > 0 && (all <= stream_rows(d) || tree_stream);
     // (one launch for both, so one kind of CTA)
     plan.stream_tile = (own_stream ? rows : 0) > 8 || (plan.prefix_stream && all > 8) ? 16 : 8;
     // Streaming kernel.  A CTA's time is its keys plus a fixed cost (page table,
