@@ -227,15 +227,24 @@ constexpr double kStreamFixed = 300.0;
 // Fills in the divisors, from the other parameters.
 void paged_divisors(PagedParams& p);
 
-// A tree's short prefix streams beside the own tokens, more rows than stream_rows or
-// not: one launch less, and a tile CTA's start and end (6 us, 9 with an e4m3 cache) is
-// most of what it would take.  By 2^x = H_kv x rows x keys x d, where the prefix has 64 row
-// tiles of 16 in all heads together at most; microseconds of a call with the tile kernel |
-// streaming, 8 heads, 128 rows, d = 128: 2^25 bf16 13.4 | 10.1, e4m3 16.8 | 10.6; 2^26 13.5 |
-// 11.8, 16.9 | 12.0; 2^27 14.2 | 15.6, 17.6 | 15.9; at 2^26 64 rows, d = 256, 13.6 | 12.5,
-// 18.2 | 12.5; 2 heads, 512 rows, d = 64, 10.8 | 9.8, 14.6 | 12.3.  With more row tiles (16
-// heads, 320 rows, d = 128, 2^26) 16.4 | 22.3, 18.7 | 22.3.
-constexpr long long kTreeStreamWork = 1ll << 26, kTreeStreamTiles = 64;
+// Trees: few and short ones stream, more rows than stream_rows or not (32 nodes at
+// most: the streaming kernel has a path in a word): a tile CTA's start and end (6 us, 9
+// with an e4m3 cache) is most of what they take, and where prefix and own tokens both
+// stream it is one launch.  By the row tiles of 16 (of all heads, own tokens: of all
+// sequences), and by work = their rows x keys x d.  Microseconds of a call with the tile
+// kernel | streaming:
+//   own tokens, 128 tiles and 2^27 at most (d = 256: 2^25)
+//     d = 64   32 tiles 2^25 bf16 11.6 | 8.9, e4m3 14.4 | 10.1; 128 tiles 2^27 13.5 | 11.5, 15.7 | 13.2
+//     d = 128  32 tiles 2^26 14.9 | 11.4, 16.5 | 11.5; 128 tiles 2^25.6 14.4 | 10.8, 14.2 | 11.0;
+//              64 tiles 2^29 18.5 | 21.2, 18.7 | 20.2; 512 tiles 2^27.6 15.1 | 18.7, 14.9 | 17.9
+//     d = 256  32 tiles 2^24.6 14.2 | 12.8, 16.1 | 11.8; 2^27 15.3 | 15.9, 17.3 | 14.7
+//   prefix, beside own tokens that stream, 64 tiles and 2^26 at most
+//     d = 128  64 tiles 2^25 13.4 | 10.1, 16.8 | 10.6; 2^26 13.5 | 11.8, 16.9 | 12.0; 2^27 14.2 |
+//              15.6, 17.6 | 15.9; 320 tiles 2^26 16.4 | 22.3, 18.7 | 22.3
+//     d = 64   64 tiles 2^26 10.8 | 9.8, 14.6 | 12.3;  d = 256  32 tiles 2^26 13.6 | 12.5, 18.2 | 12.5
+constexpr long long kTreeOwnTiles = 128, kTreePrefixTiles = 64, kTreePrefixWork = 1ll << 26;
+constexpr long long tree_own_work(int d) { return d == 256 ? 1ll << 25 : 1ll << 27; }
+constexpr int kTreeStreamNodes = 32;
 
 PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size, bool tree);
 

@@ -69,10 +69,13 @@ PagedPlan paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int 
     const long long own = static_cast<long long>(max_pages) * page_size;
     const int bn = d == 256 ? 64 : 128;
     const long long all = B * rows;                                      // the prefix's rows of a key/value head
-    const bool own_stream = rows <= stream_rows(d);
-    const bool tree_stream = tree && own_stream && H_kv * up(all, 16) <= kTreeStreamTiles &&
-                             H_kv * all * prefix_len * d <= kTreeStreamWork;
-    plan.prefix_stream = prefix_len > 0 && (all <= stream_rows(d) || tree_stream);
+    const long long heads = static_cast<long long>(B) * H_kv;
+    const bool short_own = tree && Nq <= kTreeStreamNodes && heads * up(rows, 16) <= kTreeOwnTiles &&
+                           heads * rows * own * d <= tree_own_work(d);
+    const bool short_prefix = tree && H_kv * up(all, 16) <= kTreePrefixTiles && H_kv * all * prefix_len * d <= kTreePrefixWork;
+    const bool own_stream = rows <= stream_rows(d) ||
+                            (short_own && (prefix_len == 0 || all <= stream_rows(d) || short_prefix));
+    plan.prefix_stream = prefix_len > 0 && (all <= stream_rows(d) || (own_stream && short_prefix));
     // (one launch for both, so one kind of CTA)
     plan.stream_tile = (own_stream ? rows : 0) > 8 || (plan.prefix_stream && all > 8) ? 16 : 8;
     // Streaming kernel.  A CTA's time is its keys plus a fixed cost (page table,

@@ -80,6 +80,11 @@ SHAPES = [
     ([100] * 40, 2000, 4, 4, 2, 128, 16, 2),         # many rows behind the prefix
     ([60, 45], 4100, 33, 3, 1, 256, 256, 8),
     ([20000], 0, 2, 1, 1, 256, 64, 1),
+    ([3000, 2900, 40], 0, 24, 16, 2, 128, 64, 4),    # up to 32 nodes in the tile kernel
+    ([1500, 33], 3000, 32, 8, 1, 64, 32, 5),
+    ([900, 800], 100, 20, 8, 2, 256, 32, 3),
+    ([100, 70, 300], 40, 32, 16, 2, 64, 16, 6),      # and many rows of few, short ones, streaming
+    ([41, 64], 300, 16, 24, 2, 256, 16, 3),
 ]
 
 
