@@ -163,6 +163,7 @@ struct PagedParams {
     long long parents_stride;
     bool longest_first;          // the tile kernel takes long sequences before short ones
     FastDiv by_G, by_per, by_heads;              // G, Nq G, H_kv
+    FastDiv by_node;                             // B G: rows of a node, where the nodes come first (tile kernel, prefix)
     FastDiv by_prefix_parts, by_own_parts;
     FastDiv by_prefix_rows, by_own_rows;         // streaming CTAs that share keys
     FastDiv by_prefix_groups, by_own_groups;     // tile kernel: CTAs that share keys,

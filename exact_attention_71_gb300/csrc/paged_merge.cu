@@ -147,6 +147,7 @@ void paged_divisors(PagedParams& p) {
     const unsigned per = static_cast<unsigned>(p.Nq * p.G), all = static_cast<unsigned>(p.B) * per;
     p.by_G = FastDiv(p.G);
     p.by_per = FastDiv(per);
+    p.by_node = FastDiv(static_cast<unsigned>(p.B) * p.G);
     p.by_heads = FastDiv(p.H_kv);
     p.by_prefix_parts = FastDiv(std::max(p.prefix_parts, 1));
     p.by_own_parts = FastDiv(p.own_parts);

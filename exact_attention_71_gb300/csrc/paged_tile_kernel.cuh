@@ -326,6 +326,36 @@ __device__ __forceinline__ int nth_longest(const PagedParams& p, int n) {
     return 127 - static_cast<int>((found - 1) & 127u);
 }
 
+// Sequence and query token (node) of row r of a segment, and its head of the key/value head's
+// group.  A tree's rows over the prefix are ordered by node, sequence, head, all others
+// by sequence, token, head: the trees of a batch are padded to the largest at their ends,
+// so whole tiles of the last nodes' rows may be none.
+struct TileRow {
+    int b, i, g;
+};
+template <bool TREE>
+__device__ __forceinline__ TileRow tile_row(const PagedParams& p, const TileItem& w, int r) {
+    if (TREE && w.prefix) {
+        const int i = p.by_node.div(r), y = r - i * p.B * p.G, b = p.by_G.div(y);
+        return {b, i, y - b * p.G};
+    }
+    const int y = w.prefix ? p.by_per.div(r) : 0, z = r - y * p.Nq * p.G, i = p.by_G.div(z);
+    return {w.prefix ? y : w.seq, i, z - i * p.G};
+}
+
+// Whether a row of a prefix tile is a tree's node (whole warp).
+__device__ __forceinline__ bool tile_has_node(const PagedParams& p, const TileItem& w, int tile) {
+    bool has = false;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int r = tile * 128 + x * 32 + static_cast<int>(threadIdx.x & 31);
+        if (r >= w.rows) continue;
+        const TileRow at = tile_row<true>(p, w, r);
+        has |= __ldg(p.parents + at.b * p.parents_stride + at.i) >= -1;
+    }
+    return __any_sync(0xffffffffu, has);
+}
+
 template <class Cfg, bool TREE>
 __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
     TileItem w;
@@ -383,6 +413,8 @@ __device__ __forceinline__ TileItem tile_item(const PagedParams& p) {
             j1 = min(j1, (row_limit(p, w, last) + Cfg::BN - 1) / Cfg::BN);
         }
         w.n[t] = w.rt[t] >= 0 ? max(0, j1 - w.j0[t]) : 0;
+        if constexpr (TREE)
+            if (w.prefix && w.n[t] > 0 && !tile_has_node(p, w, w.rt[t])) w.n[t] = 0;       // (its rows stay empty)
     }
     return w;
 }
@@ -586,13 +618,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     if (warp < 4 * NS) {
         in = (stream == 0 ? w.rt[0] : w.rt[1]) >= 0 && row < w.rows;
         if (in) {
-            const int per = p.Nq * p.G;
-            const int y = w.prefix ? p.by_per.div(row) : 0, z = row - y * per;             // row z of its sequence
-            const int b = w.prefix ? y : w.seq, i = p.by_G.div(z);
-            const int h = w.kvh * p.G + z - i * p.G;
-            out = (b * p.Nq + i) * p.H + h;
-            lse_at = (b * p.H + h) * p.Nq + i;
-            node_of = i;
+            const TileRow r = tile_row<TREE>(p, w, row);
+            const int h = w.kvh * p.G + r.g;
+            out = (r.b * p.Nq + r.i) * p.H + h;
+            lse_at = (r.b * p.H + h) * p.Nq + r.i;
+            node_of = r.i;
         }
     }
     if (tid == Cfg::LOAD_WARP * 32) {
