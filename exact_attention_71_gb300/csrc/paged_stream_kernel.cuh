@@ -299,14 +299,14 @@ __device__ __noinline__ uint32_t fix_v_step(uint8_t* tile, int n, int diag, int 
 __device__ __forceinline__ uint32_t tree_paths32(const PagedParams& p, int seq, int lane, bool tell) {
     int parent = -2;
     if (lane < p.Nq) parent = __ldg(p.parents + seq * p.parents_stride + lane);
+    // After r rounds: the first 2^r nodes of the path, and the one that follows.
     uint32_t path = 1u << lane;
-    int at = parent;
-    for (int steps = 0; steps < p.Nq; ++steps) {
-        const bool on = at >= 0 && at < p.Nq;
-        if (!__any_sync(0xffffffffu, on)) break;
-        const int next = __shfl_sync(0xffffffffu, parent, at & 31);
-        if (on) {
-            path |= 1u << at;
+    int at = parent < p.Nq ? parent : -2;
+    for (int span = 1; span < p.Nq; span <<= 1) {
+        const uint32_t more = __shfl_sync(0xffffffffu, path, at & 31);
+        const int next = __shfl_sync(0xffffffffu, at, at & 31);
+        if (at >= 0) {
+            path |= more;
             at = next;
         }
     }

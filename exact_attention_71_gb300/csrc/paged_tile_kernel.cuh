@@ -50,12 +50,14 @@
 // would be NaN).
 //
 // Trees (attn_fwd_paged_tree): a row sees the tokens before the drafts and its node's
-// path, which its softmax thread walks once, beside the copy of its query row, into
-// bits in local memory; only key tiles that hold drafts read them.  64 drafts x 32 heads of
-// 128 for each of 32 sequences of up to 4096 tokens: 101.8 us, 990 TFLOP/s and 4.3 TB/s (a
-// chain of as many 101): 256 CTAs, of which 152 at a time ask for 6.7 TB/s, and a CTA's
-// start and end.  Sequences go to the CTAs the longest first, where there are more CTAs
-// than SMs (in their order: 106.6).  (The drafts in a kernel of their own, joined with
+// path, which its softmax warp finds once, beside the copy of its query rows (32 nodes
+// at most: by doubling, from lane to lane; more: a thread walks its row's), as bits in
+// local memory; only key tiles that hold drafts read them.  64 drafts x 32 heads of 128
+// for each of 32 sequences of up to 4096 tokens: 101 us, 990 TFLOP/s and 4.3 TB/s (a
+// chain of as many 100): 256 CTAs, of which 152 at a time ask for 6.7 TB/s, and a CTA's
+// start and end.  Sequences go to the CTAs the longest first (in their order: 105.3).
+// 64 sequences of up to 1024 tokens, 33 drafts, e4m3: 97 us, a chain 87: 512 CTAs, each
+// of which starts 1 us later.  (The drafts in a kernel of their own, joined with
 // partial results over the tokens before them, took 130: 65536 rows written and read
 // once more, and the latency of lists, pages and rows one after the other.)
 #pragma once
@@ -299,31 +301,43 @@ __device__ __forceinline__ int row_limit(const PagedParams& p, const TileItem& w
     return max(0, w.len - p.Nq + 1 + static_cast<int>(p.by_G.div(r)));
 }
 
-// The sequence that is n-th by its key tiles, the longest first (of 128 at most; equally
-// long ones in their order).  Whole warp: the n-th largest of distinct keys, four a
-// lane, bit by bit.
+// The n-th sequence by length, longest first (of 64 at most), lengths in sixteenths of a
+// power of two, equally long ones in their order.  Whole warp: a selection bit by bit over
+// keys of 1 to 16, two a lane (0.4 us; over distinct keys of 18 bits, four a lane, 1.2).
 __device__ __forceinline__ int nth_longest(const PagedParams& p, int n) {
     const int lane = threadIdx.x & 31;
     const int room = p.max_pages << p.page_shift;
-    uint32_t key[4], top = 0;
+    uint32_t key[2], top = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
         const int b = lane + 32 * k;
-        key[k] = 0;
-        if (b < p.B) key[k] = ((static_cast<uint32_t>(min(max(__ldg(p.seq_lens + b), 0), room)) + 127u) >> 7 << 7 | (127 - b)) + 1;
+        key[k] = b < p.B ? min(max(__ldg(p.seq_lens + b), 0), room) : 0;
         top = max(top, key[k]);
     }
+    const int shift = max(28 - __clz(__reduce_max_sync(0xffffffffu, top)), 0);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) key[k] = lane + 32 * k < p.B ? (key[k] >> shift) + 1 : 0;
     uint32_t found = 0;
-    for (int bit = 31 - __clz(__reduce_max_sync(0xffffffffu, top)); bit >= 0; --bit) {
+#pragma unroll
+    for (int bit = 4; bit >= 0; --bit) {
         const uint32_t want = (found | 1u << bit) >> bit;
         int count = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 2; ++k)
             if (32 * k < p.B) count += __popc(__ballot_sync(0xffffffffu, key[k] >> bit == want));
         if (count > n) found |= 1u << bit;
         else n -= count;
     }
-    return 127 - static_cast<int>((found - 1) & 127u);
+    int seq = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (32 * k >= p.B) break;
+        const uint32_t same = __ballot_sync(0xffffffffu, key[k] == found);
+        const uint32_t at = __ballot_sync(0xffffffffu, ((same >> lane) & 1u) && __popc(same & ((1u << lane) - 1u)) == n);
+        if (at) seq = 32 * k + __ffs(at) - 1;
+        n -= __popc(same);                      // (negative from here on: no lane of the others)
+    }
+    return seq;
 }
 
 // Sequence and query token (node) of row r of a segment, and its head of the key/value head's
@@ -488,22 +502,30 @@ __device__ __forceinline__ bool v_rows_not_finite(const PagedParams& p, const Ti
 struct TreePath {
     uint32_t words[kMaxTree / 32];
     int nodes;                     // key of node 0 (< 0: the first nodes are not there)
+    int used;                      // words
     // Of the 32 keys from `key` on.
     __device__ __forceinline__ uint32_t bits(int key) const {
         const int j = key - nodes;
         if (j <= -32) return 0;
         const int x = j >> 5;
-        const uint32_t lo = x >= 0 && x < kMaxTree / 32 ? words[x] : 0, hi = x + 1 < kMaxTree / 32 ? words[x + 1] : 0;
+        const uint32_t lo = x >= 0 && x < used ? words[x] : 0, hi = x + 1 < used ? words[x + 1] : 0;
         return __funnelshift_r(lo, hi, j & 31);
     }
 };
 
-// Node i's path; false where i is no node (all words 0), and with a report where its
-// path leaves the tree, meets no node or runs in a circle.
+// Node i's path, i < 0: none; false where i is no node (all words 0), and with a report where
+// its path leaves the tree, meets no node or runs in a circle.  Whole warp.
 static __device__ __noinline__ bool tree_path(const PagedParams& p, int seq, int i, int len, TreePath& path) {
-    const int* parents = p.parents + seq * p.parents_stride;
     path.nodes = len - p.Nq;
-    for (int x = 0; x < kMaxTree / 32; ++x) path.words[x] = 0;
+    path.used = (p.Nq + 31) / 32;
+    if (p.Nq <= 32) {
+        const uint32_t bits = __shfl_sync(0xffffffffu, tree_paths32(p, seq, threadIdx.x & 31, true), i & 31);
+        path.words[0] = i < 0 ? 0u : bits;
+        return path.words[0] != 0;
+    }
+    for (int x = 0; x < path.used; ++x) path.words[x] = 0;
+    if (i < 0) return false;
+    const int* parents = p.parents + seq * p.parents_stride;
     int at = i, word = i >> 5;
     uint32_t bits = 0;
     const int parent = __ldg(parents + i);
@@ -520,7 +542,7 @@ static __device__ __noinline__ bool tree_path(const PagedParams& p, int seq, int
     path.words[word] |= bits;
     if (at == -1) return true;
     atomicCAS(p.status, 0, SITE_TREE_PARENT);
-    for (int x = 0; x < kMaxTree / 32; ++x) path.words[x] = 0;
+    for (int x = 0; x < path.used; ++x) path.words[x] = 0;
     return false;
 }
 
@@ -1040,12 +1062,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         TreePath path;
         bool none = false;
         if constexpr (TREE) {
-            if (in && !w.prefix) {
-                none = !tree_path(p, w.seq, node_of, w.len, path);
-                if (!none) limit = diag_key;
+            if (!w.prefix) {
+                none = !tree_path(p, w.seq, in ? node_of : -1, w.len, path) && in;
+                if (in && !none) limit = diag_key;
             } else {
-                for (int x = 0; x < kMaxTree / 32; ++x) path.words[x] = 0;
                 path.nodes = w.len;
+                path.used = 0;
             }
         }
         // Which of the 32 keys from `key` on the row sees.

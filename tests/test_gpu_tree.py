@@ -141,6 +141,32 @@ def test_rows_that_are_no_nodes_are_empty_in_every_mode(case, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B", [2, 33, 64])
+def test_many_sequences_of_any_lengths(B, fp8):
+    """More CTAs than multiprocessors: long sequences are taken first, each of them once."""
+    lens = [(0, 700, 41, 333, 700, 699, 5, 128)[(5 * b + b // 8) % 8] for b in range(B)]
+    H = 128 if B == 2 else 8
+    p = Tree(lens, 0, 40, H, H, 64, 16, fp8, seed=21, width=6)
+    assert api.paged_plan(B, 40, H, H, 64, 0, p.table.shape[1], 16).own_kernel == "tile"
+    p.check(*p.run())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d, B, Nq, G", [(64, 20, 16, 4), (128, 37, 9, 2), (256, 3, 40, 5), (128, 130, 4, 1)])
+def test_padded_trees_behind_a_prefix(d, B, Nq, G, fp8):
+    """Tiles of the prefix's rows that are all padding are left out, also where every row is."""
+    p = Tree([Nq + 3 * (b % 7) for b in range(B)], 700, Nq, 2 * G, 2, d, 16, fp8, seed=22, width=3)
+    for b in range(B):
+        p.parents[b, max(1, Nq - Nq // 3 - b % 3):] = -2
+    p.parents[B // 2] = -2                                  # a slot without a tree
+    p.parents[0, Nq - 1] = 0                                # one of the last nodes is there
+    p.check(*p.run())
+    p.parents[:] = -2
+    o, lse = p.run()
+    assert bool((o == 0).all()) and bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("d", [64, 256])
 def test_the_largest_tree_and_a_value_that_is_not_finite_in_each_of_its_tiles(d, fp8):
     """512 nodes that begin inside a tile of keys; bad values 64 keys apart: each makes the
