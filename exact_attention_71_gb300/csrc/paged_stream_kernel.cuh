@@ -293,12 +293,10 @@ __device__ __noinline__ uint32_t fix_v_step(uint8_t* tile, int n, int diag, int 
     return __reduce_or_sync(0xffffffffu, hit);
 }
 
-// The paths of a tree of up to 32 nodes: lane j has node j's parent; the result is
+// The paths of a tree of up to 32 nodes: lane j has node j's parent (past them: -2); the result is
 // lane j's nodes (its ancestors and itself; bit: node), 0 where j is no node.  Whole
 // warp.  A path that leaves the tree, meets no node or runs in a circle is reported.
-__device__ __forceinline__ uint32_t tree_paths32(const PagedParams& p, int seq, int lane, bool tell) {
-    int parent = -2;
-    if (lane < p.Nq) parent = __ldg(p.parents + seq * p.parents_stride + lane);
+__device__ __forceinline__ uint32_t tree_paths32(const PagedParams& p, int parent, int lane, bool tell) {
     // After r rounds: the first 2^r nodes of the path, and the one that follows.
     uint32_t path = 1u << lane;
     int at = parent < p.Nq ? parent : -2;
@@ -444,7 +442,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, Cfg::CTAS)
     uint32_t path[TREE ? R : 1][2];
     __shared__ uint32_t row_path[TREE ? Cfg::ROWS : 1];
     if constexpr (TREE) {
-        const uint32_t paths = prefix ? 0 : tree_paths32(p, seq, lane, warp == 0);
+        const int parent = !prefix && lane < p.Nq ? __ldg(p.parents + seq * p.parents_stride + lane) : -2;
+        const uint32_t paths = prefix ? 0 : tree_paths32(p, parent, lane, warp == 0);
 #pragma unroll
         for (int n = 0; n < R; ++n)
 #pragma unroll

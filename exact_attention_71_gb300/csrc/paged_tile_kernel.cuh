@@ -53,11 +53,11 @@
 // path, which its softmax warp finds once, beside the copy of its query rows (32 nodes
 // at most: by doubling, from lane to lane; more: a thread walks its row's), as bits in
 // local memory; only key tiles that hold drafts read them.  64 drafts x 32 heads of 128
-// for each of 32 sequences of up to 4096 tokens: 101 us, 990 TFLOP/s and 4.3 TB/s (a
-// chain of as many 100): 256 CTAs, of which 152 at a time ask for 6.7 TB/s, and a CTA's
-// start and end.  Sequences go to the CTAs the longest first (in their order: 105.3).
-// 64 sequences of up to 1024 tokens, 33 drafts, e4m3: 97 us, a chain 87: 512 CTAs, each
-// of which starts 1 us later.  (The drafts in a kernel of their own, joined with
+// for each of 32 sequences of up to 4096 tokens: 97 us, 1040 TFLOP/s and 4.5 TB/s (a
+// chain of as many 98.5): 256 CTAs, of which 152 at a time ask for 6.7 TB/s, and a CTA's
+// start and end.  Sequences go to the CTAs the longest first (in their order: 101).
+// 64 sequences of up to 1024 tokens, 33 drafts, e4m3: 95.5 us, a chain 88: 512 CTAs, each
+// of which starts later.  (The drafts in a kernel of their own, joined with
 // partial results over the tokens before them, took 130: 65536 rows written and read
 // once more, and the latency of lists, pages and rows one after the other.)
 #pragma once
@@ -214,6 +214,12 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
     return static_cast<uint32_t>((c >> 3) * (Cfg::BN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// V rows of a key tile that its product reads (bf16; whole instructions of 16): the rows
+// past them need not be cleared.  (One warp clears and checks rows, 5000 cycles for
+// a whole tile: 64 sequences of 16 x 4 rows and 64 tokens took 38.6 us, now 30.5.)
+template <class Cfg>
+__device__ __forceinline__ int tile_v_rows(int keys) { return min(max(keys + 15, 0) & ~15, Cfg::BN); }
+
 // One warp's pass over a bf16 V tile in shared memory: rows that were not
 // copied, or lie past the range (row >= len), become 0; in rows from `diag` on
 // infinities and NaN become 0 and the row's bit in poison is set.
@@ -223,6 +229,7 @@ __device__ __noinline__ void fix_v_tile(uint8_t* tile, uint32_t copies, int log2
     constexpr int CPR = Cfg::D / 8, LPR = CPR < 32 ? CPR : 32;     // 16-byte chunks, lanes of a row
     // Rows below `from` are as they should be.
     int from = max(min(len, diag), 0);
+    const int end = tile_v_rows<Cfg>(len);
     const uint32_t missing = ~copies & ((1u << (Cfg::BN >> log2_box)) - 1u);
     if (missing) from = min(from, (__ffs(missing) - 1) << log2_box);
     // One warp does this while the products wait, so the usual case, finite rows, is
@@ -230,17 +237,17 @@ __device__ __noinline__ void fix_v_tile(uint8_t* tile, uint32_t copies, int log2
     // exponent field of ones carries into the sign bit.  (A row group after the
     // other, with comparisons, held up a tile of 128 rows by 12000 cycles.)
     constexpr int AT = 8, RPI = 32 / LPR;
-    for (int r0 = from + lane / LPR; r0 < Cfg::BN; r0 += AT * RPI) {
+    for (int r0 = from + lane / LPR; r0 < end; r0 += AT * RPI) {
 #pragma unroll
         for (int c = lane % LPR; c < CPR; c += LPR) {
             uint4 v[AT];
 #pragma unroll
             for (int i = 0; i < AT; ++i) {
                 const int r = r0 + i * RPI;
-                const bool have = r < len && r < Cfg::BN && ((copies >> (r >> log2_box)) & 1u);
+                const bool have = r < len && r < end && ((copies >> (r >> log2_box)) & 1u);
                 if (have) v[i] = *reinterpret_cast<const uint4*>(tile + tile_offset<Cfg>(r, c));
                 else v[i] = make_uint4(0, 0, 0, 0);
-                if (!have && r < Cfg::BN) *reinterpret_cast<uint4*>(tile + tile_offset<Cfg>(r, c)) = v[i];
+                if (!have && r < end) *reinterpret_cast<uint4*>(tile + tile_offset<Cfg>(r, c)) = v[i];
             }
             uint32_t bad[AT], any = 0;
 #pragma unroll
@@ -514,12 +521,13 @@ struct TreePath {
 };
 
 // Node i's path, i < 0: none; false where i is no node (all words 0), and with a report where
-// its path leaves the tree, meets no node or runs in a circle.  Whole warp.
-static __device__ __noinline__ bool tree_path(const PagedParams& p, int seq, int i, int len, TreePath& path) {
+// its path leaves the tree, meets no node or runs in a circle.  Whole warp; parent: of up to
+// 32 nodes the lane's, of more node i's.
+static __device__ __noinline__ bool tree_path(const PagedParams& p, int seq, int i, int parent, int len, TreePath& path) {
     path.nodes = len - p.Nq;
     path.used = (p.Nq + 31) / 32;
     if (p.Nq <= 32) {
-        const uint32_t bits = __shfl_sync(0xffffffffu, tree_paths32(p, seq, threadIdx.x & 31, true), i & 31);
+        const uint32_t bits = __shfl_sync(0xffffffffu, tree_paths32(p, parent, threadIdx.x & 31, true), i & 31);
         path.words[0] = i < 0 ? 0u : bits;
         return path.words[0] != 0;
     }
@@ -528,7 +536,6 @@ static __device__ __noinline__ bool tree_path(const PagedParams& p, int seq, int
     const int* parents = p.parents + seq * p.parents_stride;
     int at = i, word = i >> 5;
     uint32_t bits = 0;
-    const int parent = __ldg(parents + i);
     if (parent < -1) return false;
     for (int steps = 0; steps < p.Nq && at >= 0 && at < p.Nq; ++steps) {
         if ((at >> 5) != word) {
@@ -537,7 +544,7 @@ static __device__ __noinline__ bool tree_path(const PagedParams& p, int seq, int
             bits = 0;
         }
         bits |= 1u << (at & 31);
-        at = __ldg(parents + at);
+        at = steps == 0 ? parent : __ldg(parents + at);
     }
     path.words[word] |= bits;
     if (at == -1) return true;
@@ -609,6 +616,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                       const __grid_constant__ PagedParams p) {
     constexpr int D = Cfg::D, BN = Cfg::BN, BM = Cfg::BM, NS = Cfg::NS, NH = Cfg::NH;
     constexpr bool FP8 = Cfg::FP8;
+    // alt: both streams' warps bring in the one tile of query rows.  (e4m3, 64 sequences of
+    // 16 x 4 rows and 64 tokens: 48.0 us with one stream's, 41.8.  Trees alone: the code of the
+    // others is at its limit; a chunk of 512 queries over 8192 keys took 148 us instead of 140.)
+    constexpr bool SHARE_Q = NS == 2 && TREE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
@@ -636,7 +647,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const int row = (stream == 0 ? w.rt[0] : w.rt[1]) * BM + (tid & 127);
     bool in = false;
     int out = -1, lse_at = 0;      // row index in q, o and the partials; in lse
-    int node_of = 0;               // TREE: the row's node
+    int node_of = 0, parent = -2;  // TREE: the row's node; what tree_path starts from
     if (warp < 4 * NS) {
         in = (stream == 0 ? w.rt[0] : w.rt[1]) >= 0 && row < w.rows;
         if (in) {
@@ -646,6 +657,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             lse_at = (r.b * p.H + h) * p.Nq + r.i;
             node_of = r.i;
         }
+        if (TREE && !w.prefix && (p.Nq <= 32 ? lane < p.Nq : in))
+            parent = __ldg(p.parents + w.seq * p.parents_stride + (p.Nq <= 32 ? lane : node_of));
     }
     if (tid == Cfg::LOAD_WARP * 32) {
         mbar_init(&bars->q_full, NS * 128);
@@ -725,10 +738,17 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     if (has_v) {
                         if (u <= nt) {
                             const uint64_t vd = sdesc_sw128(ring + (xv % NH) * Cfg::HALF_BYTES, BN * 128, 1024);
+                            const int v_rows = FP8 ? BN : tile_v_rows<Cfg>(w.len - ((t == 0 ? w.j0[0] : w.j0[1]) + u - 1) * BN);
+                            const auto block = [&](int kk) {
+                                mma_f16_ts(o_tmem, s_tmem + kk * 8, vd + ((kk * 16 * 128) >> 4), idesc_o, (kk > 0 || u > 1) ? 1u : 0u);
+                            };
+                            if (v_rows == BN) {
 #pragma unroll
-                            for (int kk = 0; kk < BN / 16; ++kk)
-                                mma_f16_ts(o_tmem, s_tmem + kk * 8, vd + ((kk * 16 * 128) >> 4), idesc_o,
-                                           (kk > 0 || u > 1) ? 1u : 0u);
+                                for (int kk = 0; kk < BN / 16; ++kk) block(kk);
+                            } else {
+#pragma unroll 1
+                                for (int kk = 0; kk * 16 < v_rows; ++kk) block(kk);
+                            }
                             if (u == nt) mma_commit(&bars->o_full[t]);
                             mma_commit(&bars->ring_empty[xv % NH]);
                         } else {
@@ -1039,21 +1059,34 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         const int nt = t == 0 ? w.n[0] : w.n[1];
         const int j0 = t == 0 ? w.j0[0] : w.j0[1], part = w.part;
         int limit = in ? row_limit(p, w, row) : w.len;         // (a row that is not there needs no mask)
-        // A warp brings in its 32 query rows, swizzled, zero where there is none;
-        // in alt mode both streams use stream 0's tile.  A lane has chunk qc of the
-        // rows q_row(x).
+        // A warp brings in its query rows, swizzled, zero where there is none: its 32 of
+        // the stream's tile; in alt mode, where both streams use one tile, every eighth
+        // row of it.  A lane has chunk qc of the rows q0 + x * qs.
         constexpr int LPR = D / 8 < 32 ? D / 8 : 32, RPI = 32 / LPR;   // lanes per row (16 bytes each), rows at a time
-        const int qc = lane % LPR;
-        auto q_row = [&](int x) { return (warp & 3) * 32 + x * RPI + lane / LPR; };
+        const bool by_eight = SHARE_Q && !w.pair, bring = w.pair || t == 0 || by_eight;
+        const int qc = lane % LPR, tq = by_eight ? 0 : t;
+        const int q0 = by_eight ? lane / LPR * 8 + t * 4 + (warp & 3) : (warp & 3) * 32 + lane / LPR;
+        const int qs = by_eight ? RPI * 8 : RPI, qx = by_eight ? LPR / 2 : LPR;
         auto q_at = [&](int r) -> uint32_t { return (qc >> 3) * (BM * 128) + r * 128 + (((qc & 7) ^ (r & 7)) << 4); };
         // (e4m3, d = 64: a row's two parts do not lie where its bf16 elements would)
-        uint8_t* const rows16 = FP8 && D == 64 ? sEpi + t * 16384 : sQ + t * Cfg::Q_BYTES;
-        if (w.pair || t == 0) {
+        uint8_t* const rows16 = FP8 && D == 64 ? sEpi + tq * 16384 : sQ + tq * Cfg::Q_BYTES;
+        {
             const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + qc * 8;
+            const uint32_t to = smem_u32(rows16);
+            if (by_eight) {
+#pragma unroll 1
+                for (int x = 0; x < LPR / 2; ++x) {
+                    const int r = q0 + x * qs;
+                    const TileRow at = tile_row<TREE>(p, w, min(r, w.rows - 1));
+                    const long long src = (at.b * p.Nq + at.i) * p.H + w.kvh * p.G + at.g;
+                    cp_async16(to + q_at(r), q + src * D, r < w.rows);
+                }
+            } else if (bring) {
 #pragma unroll 8
-            for (int x = 0; x < LPR; ++x) {
-                const int src = __shfl_sync(0xffffffffu, out, x * RPI + lane / LPR);
-                cp_async16(smem_u32(rows16) + q_at(q_row(x)), q + static_cast<long long>(max(src, 0)) * D, src >= 0);
+                for (int x = 0; x < LPR; ++x) {
+                    const int src = __shfl_sync(0xffffffffu, out, x * RPI + lane / LPR);
+                    cp_async16(to + q_at(q0 + x * RPI), q + static_cast<long long>(max(src, 0)) * D, src >= 0);
+                }
             }
         }
         cp_async_commit();
@@ -1063,7 +1096,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         bool none = false;
         if constexpr (TREE) {
             if (!w.prefix) {
-                none = !tree_path(p, w.seq, in ? node_of : -1, w.len, path) && in;
+                none = !tree_path(p, w.seq, in ? node_of : -1, parent, w.len, path) && in;
                 if (in && !none) limit = diag_key;
             } else {
                 path.nodes = w.len;
@@ -1083,38 +1116,39 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             // Into two e4m3 parts, in place.  (A loop of few instructions: with a
             // row a thread and everything unrolled, fetching the code took most of
             // 21000 cycles.)
-            if (w.pair || t == 0) {
-                uint8_t* tile = sQ + t * Cfg::Q_BYTES;
-                constexpr int AT = 4;                              // row groups at a time (latency)
+            uint8_t* tile = sQ + tq * Cfg::Q_BYTES;
+            // Row groups at a time (latency; trees: the code is at its limit).
+            constexpr int AT = TREE ? 2 : 4;
 #pragma unroll 1
-                for (int x = 0; x < LPR; x += AT) {
-                    uint4 v[AT];
-                    uint32_t top[AT];
+            for (int x = 0; x < (bring ? qx : 0); x += AT) {
+                if (TREE && D != 64 && q0 - lane / LPR * (qs / RPI) + x * qs >= w.rows - max(t == 0 ? w.rt[0] : w.rt[1], 0) * BM)
+                    break;                                     // (no more rows: zeros already)
+                uint4 v[AT];
+                uint32_t top[AT];
 #pragma unroll
-                    for (int i = 0; i < AT; ++i) {
-                        v[i] = *reinterpret_cast<const uint4*>(rows16 + q_at(q_row(x + i)));
-                        top[i] = bf16x8_amax(v[i]);
-                    }
-#pragma unroll
-                    for (int y = 1; y < LPR; y <<= 1)
-#pragma unroll
-                        for (int i = 0; i < AT; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], y));
-#pragma unroll
-                    for (int i = 0; i < AT; ++i) {
-                        const int r = q_row(x + i), shift = q_shift(top[i], 7);
-                        uint2 q1, q2;
-                        q_split(v[i], top[i] >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2f(shift), q1, q2);
-                        const int c = qc >> 1;                     // 16 codes
-                        constexpr int PER = Cfg::SWK / 16;
-                        const int z = Cfg::SWK == 128 ? (c % PER) ^ (r & 7) : (c % PER) ^ ((r >> 1) & 3);
-                        uint8_t* at = tile + (c / PER) * (BM * Cfg::SWK) + r * Cfg::SWK + (z << 4) + (qc & 1) * 8;
-                        *reinterpret_cast<uint2*>(at) = q1;
-                        *reinterpret_cast<uint2*>(at + BM * D) = q2;
-                        // (not 0: -inf, the masked score, stays -inf when multiplied)
-                        if (qc == 0) bars->q_log2[t * 128 + r] = fmaxf(p.scale_log2 * pow2f(-shift), 0x1p-126f);
-                    }
-                    __syncwarp();
+                for (int i = 0; i < AT; ++i) {
+                    v[i] = *reinterpret_cast<const uint4*>(rows16 + q_at(q0 + (x + i) * qs));
+                    top[i] = bf16x8_amax(v[i]);
                 }
+#pragma unroll
+                for (int y = 1; y < LPR; y <<= 1)
+#pragma unroll
+                    for (int i = 0; i < AT; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], y));
+#pragma unroll
+                for (int i = 0; i < AT; ++i) {
+                    const int r = q0 + (x + i) * qs, shift = q_shift(top[i], 7);
+                    uint2 q1, q2;
+                    q_split(v[i], top[i] >= 0x7f80u ? __uint_as_float(0x7fc00000u) : pow2f(shift), q1, q2);
+                    const int c = qc >> 1;                     // 16 codes
+                    constexpr int PER = Cfg::SWK / 16;
+                    const int z = Cfg::SWK == 128 ? (c % PER) ^ (r & 7) : (c % PER) ^ ((r >> 1) & 3);
+                    uint8_t* at = tile + (c / PER) * (BM * Cfg::SWK) + r * Cfg::SWK + (z << 4) + (qc & 1) * 8;
+                    *reinterpret_cast<uint2*>(at) = q1;
+                    *reinterpret_cast<uint2*>(at + BM * D) = q2;
+                    // (not 0: -inf, the masked score, stays -inf when multiplied)
+                    if (qc == 0) bars->q_log2[tq * 128 + r] = fmaxf(p.scale_log2 * pow2f(-shift), 0x1p-126f);
+                }
+                __syncwarp();
             }
         }
         fence_proxy_async_smem();
@@ -1175,7 +1209,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 // quarter of them; one row a thread read 512 bytes of K scales and 512
                 // of V scales a tile, which with the conversion's traffic bounded the
                 // kernel by shared memory (6300 cycles a step of two tiles).
-                if (u == 0) {                      // (in alt mode stream 0's threads wrote it: S comes after)
+                if (u == 0) {                      // (in alt mode all threads wrote it: S comes after)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         tl4[i] = bars->q_log2[(w.pair ? t * 128 : 0) + (warp & 3) * 32 + (lane >> 2) + 8 * i];
