@@ -46,10 +46,10 @@
 //
 // Trees (attn_fwd_paged_tree): the mask of a row is a limit, the tokens before the
 // drafts, and a word of bits, its node's path: up to 32 rows have up to 32 nodes.  Every
-// warp walks the paths by itself, a node a lane, in as many shuffles as the tree is
-// deep, while its first copies are on their way; steps before the drafts are not
-// masked, so a tree costs what a chain of as many drafts does (27 drafts x 16 heads of
-// 64 for each of 7 sequences of up to 2333 tokens 20.5 us, a chain 19.2).
+// warp finds the paths by itself, a node a lane, by doubling, while its first copies are
+// on their way; steps before the drafts are not masked, so a tree costs what a chain of as
+// many drafts does (27 drafts x 16 heads of 64 for each of 7 sequences of up to 2333
+// tokens 19.9 us, a chain 19.3).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -152,6 +152,22 @@ def test_many_sequences_of_any_lengths(B, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("B, Nq, H, hkv, prefix", [(3, 5, 8, 2, 200), (3, 5, 8, 2, 9000), (40, 20, 8, 2, 700), (2, 70, 8, 2, 90),
+                                                   (1, 33, 64, 1, 40)])
+def test_empty_sequences_behind_a_prefix(B, Nq, H, hkv, prefix, fp8):
+    """No own tokens: nodes see the prefix, other rows nothing; also with a table of no columns."""
+    p = Tree([0] * B, prefix, Nq, H, hkv, 128, 16, fp8, seed=23, width=3)
+    p.parents[:, Nq - Nq // 4:] = -2
+    p.parents[B // 2, 0] = -2 if B > 1 else -1
+    p.parents[B // 2, 1:] = torch.where(p.parents[B // 2, 1:] == -2, -2, -1).int()
+    o, lse = p.run()
+    p.check(o, lse)
+    p.table = p.table[:, :0]
+    o2, l2 = p.run()
+    p.check(o2, l2)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("d, B, Nq, G", [(64, 20, 16, 4), (128, 37, 9, 2), (256, 3, 40, 5), (128, 130, 4, 1)])
 def test_padded_trees_behind_a_prefix(d, B, Nq, G, fp8):
     """Tiles of the prefix's rows that are all padding are left out, also where every row is."""
