@@ -724,3 +724,32 @@ def test_speculative_steps_equal_a_run_without_speculation(fp8, graph):
             y = api.attn_kv_read(plain, order[b:b + 1], new, n)
             assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
         lens = lens + torch.tensor([len(x) for x in kept], device=DEV)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("prefix", [0, 135])
+def test_ranges_of_every_length_in_the_tile_kernel(prefix, d, fp8):
+    """A key tile's products leave out its last rows, which hold anything: chains with and
+    without the mask, and trees."""
+    lens = list(range(40, 57)) + list(range(120, 137)) + [250, 256, 257]
+    p = Tree(lens, prefix, 40, 2, 2, d, 64, fp8, seed=24, width=4)
+    assert api.paged_plan(len(lens), 40, 2, 2, d, prefix, p.table.shape[1], 64).own_kernel == "tile"
+    got = []
+    for stale in (0x7f, 0x7e):                          # NaN, and large values
+        for b, n in enumerate(lens):                    # the rest of a sequence's last page
+            page, row = int(p.table[b, (n - 1) // 64]), (n - 1) % 64 + 1
+            for x in (p.cache.k, p.cache.v):
+                x[page, :, row:] = stale if fp8 else (NAN if stale == 0x7f else 1e38)
+            if fp8:
+                for x in (p.cache.k_scale, p.cache.v_scale):
+                    x[page, :, row:] = NAN if stale == 0x7f else 1e30
+        now = []
+        for causal in (True, False):
+            o, lse = Problem.run(p, causal=causal)
+            Problem.check(p, o, lse, causal=causal)
+            now += [o, lse]
+        o, lse = p.run()
+        p.check(o, lse)
+        got.append(now + [o, lse])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
