@@ -853,7 +853,8 @@ def attn_kv_accept(cache: KVCache, block_table, seq_lens, accepted, Nq: int, str
 
     accepted: int32 (B, M), M at most Nq and 128: nodes, usually a path; negative
     entries are padding.  All rows of a sequence are read before one is written.  A
-    node outside the drafts is not moved and reported by device_status().
+    node outside the drafts is not moved, a sequence longer than its table has none
+    moved; both are reported by device_status().
     """
     pages, Hkv, ps, d, dtype, dev, ptrs = _check_cache(cache)
     B = block_table.shape[0]

@@ -117,17 +117,17 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p)
 constexpr int kAcceptThreads = 128, kAcceptRows = 16;
 
 // Cache rows of head 0 that accepted draft j of sequence b moves from and to (-1: it does
-// not move): the first M threads; then a barrier.
+// not move): the first M threads; then a barrier.  A length beyond the table is not cut
+// to it, as where rows are only read: the drafts would then be other tokens, rows of the
+// context, and those would be overwritten.
 __device__ __forceinline__ void accept_rows(const KvAcceptParams& p, int b, long long* from, long long* to) {
-    int len = max(0, __ldg(p.seq_lens + b));
-    const long long room = static_cast<long long>(p.max_pages) << p.page_shift;
-    if (len > room) {
-        report(p.status, SITE_PAGED_LENGTH);
-        len = static_cast<int>(room);
-    }
+    const int len = max(0, __ldg(p.seq_lens + b));
+    const bool beyond = len > (static_cast<long long>(p.max_pages) << p.page_shift);
+    if (beyond) report(p.status, SITE_PAGED_LENGTH);
     const int start = len - p.Nq;
     for (int j = threadIdx.x; j < p.M; j += kAcceptThreads) {
         from[j] = -1;
+        if (beyond) continue;
         const int node = __ldg(p.accepted + static_cast<long long>(b) * p.M + j);
         if (node < 0 || (node == j && start >= 0)) continue;       // (padding, or it stays)
         if (node >= p.Nq || start < 0) {

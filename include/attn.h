@@ -561,12 +561,15 @@ int attn_fwd_paged_tree(const void* q, const void* k_cache, const void* v_cache,
  *   accepted        : const int32 (B, M), device, contiguous: nodes, a path from a
  *                     root on in the usual case; a negative entry moves nothing
  *                     (padding).  M at most Nq and at most 128
- *   block_table, table_stride, max_pages, seq_lens : as in attn_kv_read; the pages
- *                     of the moved tokens must not be shared by two sequences
+ *   block_table, table_stride, max_pages, seq_lens : as in attn_kv_read, but that no
+ *                     length is cut (below); the pages of the moved tokens must not
+ *                     be shared by two sequences
  * All rows of a sequence are read before the first is written, so any order and any
  * overlap of nodes and places is allowed, the same node twice too.  e4m3 rows move
  * with their scales.  A node that is not in [0, Nq), or drafts of a sequence of fewer
- * than Nq tokens, or a page outside the cache: recorded, that row is not moved.
+ * than Nq tokens, or a page outside the cache: recorded, that row is not moved.  A
+ * length beyond the table (max_pages * page_size): recorded, no row of that sequence is
+ * moved.
  */
 int attn_kv_accept(void* k_cache, void* v_cache, float* k_scale, float* v_scale,
                    const int* block_table, long long table_stride, int max_pages,
