@@ -195,15 +195,16 @@ __global__ void __launch_bounds__(kThreads, kRowsEarly<AXES, MODE> ? 8 : 7) rope
         if (slot >= p.num_slots) report(p.status, SITE_PAGED_SLOT);
         take = slot >= 0 && slot < p.num_slots;
     }
+    // (Padding's positions are not read: there may be none.)
     bool fine = true;
 #pragma unroll
     for (int a = 0; a < (AXES ? 4 : 1); ++a) {
-        if (in && a < p.n_axes) {
+        if (take && a < p.n_axes) {
             at = position(t, a);
             fine = fine && at >= 0 && at < p.rows;
         }
     }
-    if (take && !fine) report(p.status, SITE_ROPE_POSITION);
+    if (!fine) report(p.status, SITE_ROPE_POSITION);
     take = take && fine;
 
     Row16 r[HM];
@@ -238,6 +239,10 @@ __global__ void __launch_bounds__(kThreads, kRowsEarly<AXES, MODE> ? 8 : 7) rope
         // Where pair y's angles stand in the tables (-1: nowhere), and in `mine`.
         const auto table_at = [&](int y) -> long long {
             const int token = p.by_half.div(y), i = y - token * half;
+            if constexpr (MODE != ROPE) {
+                const long long slot = __ldg(p.slots + first + token);
+                if (slot < 0 || slot >= p.num_slots) return -1;
+            }
             const long long row = position(first + token, (p.axes[i >> 4] >> (2 * (i & 15))) & 3u);
             return row >= 0 && row < p.rows ? row * half + i : -1;
         };

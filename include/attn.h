@@ -433,8 +433,9 @@ int attn_kv_write(const void* k, const void* v, long long k_stride, long long v_
  *   positions, axis_stride, n_axes, pair_axis, rope_cos, rope_sin, table_rows, rot,
  *   interleaved     : as in attn_rope (positions is required; no period)
  * A negative slot is padding: nothing is written to the cache, the token's q_out
- * rows become 0, its positions are not read.  A slot beyond the cache or a position
- * outside the tables is recorded and its token treated as padding.
+ * rows become 0, its positions are not read (those of padding behind the last token
+ * need not be there).  A slot beyond the cache or a position outside the tables is
+ * recorded and its token treated as padding.
  */
 int attn_kv_append(const void* q, long long q_stride, void* q_out, long long q_out_stride,
                    const void* k, const void* v, long long k_stride, long long v_stride,
