@@ -110,6 +110,8 @@ def library() -> ctypes.CDLL:
         L.attn_kv_append.restype = i
         L.attn_fwd_paged_tree_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
         L.attn_fwd_paged_tree_workspace_size.restype = sz
+        L.attn_fwd_paged_tree_plan.argtypes = [i, i, i, i, i, i, i, i, P, i]
+        L.attn_fwd_paged_tree_plan.restype = i
         L.attn_fwd_paged_tree.argtypes = [P, P, P, P, P, P, i, P, i64, i, P, P, i64, P, P, i, i, i, i, i, i, i, i, f, P,
                                           sz, P]
         L.attn_fwd_paged_tree.restype = i
@@ -717,9 +719,18 @@ class PagedPlan(NamedTuple):
 def paged_plan(B: int, Nq: int, H: int, H_kv: int, d: int, prefix_len: int, max_pages: int,
                page_size: int) -> PagedPlan | None:
     """Host only: the plan of a call of these sizes; None for empty or refused ones."""
+    return _plan(library().attn_fwd_paged_plan, B, Nq, H, H_kv, d, prefix_len, max_pages, page_size)
+
+
+def paged_tree_plan(B: int, Nq: int, H: int, H_kv: int, d: int, prefix_len: int, max_pages: int,
+                    page_size: int) -> PagedPlan | None:
+    """paged_plan of attn_fwd_paged_tree."""
+    return _plan(library().attn_fwd_paged_tree_plan, B, Nq, H, H_kv, d, prefix_len, max_pages, page_size)
+
+
+def _plan(entry, *sizes):
     buf = (ctypes.c_int * 8)()
-    if library().attn_fwd_paged_plan(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size,
-                                     ctypes.cast(buf, ctypes.c_void_p), 8) != 8:
+    if entry(*sizes, ctypes.cast(buf, ctypes.c_void_p), 8) != 8:
         return None
     kernels = (None, "stream", "tile")
     return PagedPlan(kernels[buf[0]], kernels[buf[1]], *buf[2:7], bool(buf[7]))

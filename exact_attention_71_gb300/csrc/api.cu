@@ -1124,6 +1124,26 @@ int paged_call(const char* name, bool tree, const void* q, const void* k_cache, 
     return ATTN_OK;
 }
 
+// The plan of a call, as attn_fwd_paged_plan gives it (0: refused or empty).
+int paged_plan_out(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size, bool tree, int* out,
+                   int capacity) {
+    if (!out || capacity < 8) return 0;
+    attn::PagedPlan plan;
+    if (check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan, tree) != ATTN_OK) return 0;
+    if (tree && check_tree(Nq) != ATTN_OK) return 0;
+    if (static_cast<long long>(B) * Nq * H == 0) return 0;
+    const long long rows = static_cast<long long>(Nq) * (H / H_kv);
+    out[0] = plan.prefix_items > 0 ? 2 : plan.prefix_stream ? 1 : 0;
+    out[1] = plan.own_items > 0 ? 2 : 1;
+    out[2] = plan.prefix_parts;
+    out[3] = plan.own_parts;
+    out[4] = out[0] == 1 || out[1] == 1 ? plan.stream_tile : 0;
+    out[5] = out[0] == 2 ? static_cast<int>((B * rows + 127) / 128) : 0;
+    out[6] = out[1] == 2 ? static_cast<int>((rows + 127) / 128) : 0;
+    out[7] = plan.direct ? 1 : 0;
+    return 8;
+}
+
 // What attn_rope and attn_kv_append share: sizes, tables, positions.
 int check_rope(attn::RopeParams* p, int T, int H, int H_kv, int d, const long long* positions, long long axis_stride,
                int n_axes, const unsigned char* pair_axis, const float* rope_cos, const float* rope_sin,
@@ -1283,20 +1303,12 @@ size_t attn_fwd_paged_workspace_size(int B, int Nq, int H, int H_kv, int d, int 
 
 int attn_fwd_paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size, int* out,
                         int capacity) {
-    if (!out || capacity < 8) return 0;
-    attn::PagedPlan plan;
-    if (check_paged_sizes(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, &plan) != ATTN_OK) return 0;
-    if (static_cast<long long>(B) * Nq * H == 0) return 0;
-    const long long rows = static_cast<long long>(Nq) * (H / H_kv);
-    out[0] = plan.prefix_items > 0 ? 2 : plan.prefix_stream ? 1 : 0;
-    out[1] = plan.own_items > 0 ? 2 : 1;
-    out[2] = plan.prefix_parts;
-    out[3] = plan.own_parts;
-    out[4] = out[0] == 1 || out[1] == 1 ? plan.stream_tile : 0;
-    out[5] = out[0] == 2 ? static_cast<int>((B * rows + 127) / 128) : 0;
-    out[6] = out[1] == 2 ? static_cast<int>((rows + 127) / 128) : 0;
-    out[7] = plan.direct ? 1 : 0;
-    return 8;
+    return paged_plan_out(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, false, out, capacity);
+}
+
+int attn_fwd_paged_tree_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages, int page_size, int* out,
+                             int capacity) {
+    return paged_plan_out(B, Nq, H, H_kv, d, prefix_len, max_pages, page_size, true, out, capacity);
 }
 
 int attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,

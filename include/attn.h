@@ -617,8 +617,8 @@ int attn_set_wait_limit(unsigned long long cycles);
 int attn_fwd_work_order(int n_mblocks, int BH, int grid, unsigned int* out, int capacity);
 
 /*
- * attn_fwd_paged_plan -- how attn_fwd_paged cuts up a call of these sizes; host
- * code only, no GPU needed (inspection and testing).
+ * attn_fwd_paged_plan / attn_fwd_paged_tree_plan -- how attn_fwd_paged cuts up a
+ * call of these sizes; host code only, no GPU needed (inspection and testing).
  *   out : HOST array of `capacity` >= 8 ints:
  *         [0], [1]  the kernel of the prefix and that of the own tokens: 0 none, 1
  *                   streaming (few query rows), 2 tiles (tcgen05)
@@ -628,10 +628,14 @@ int attn_fwd_work_order(int n_mblocks, int BH, int grid, unsigned int* out, int 
  *                   over a sequence's own tokens (tile kernel; else 0)
  *         [7]       1: one range in all, written to o and lse without a join
  * Returns 8, or 0 for sizes that attn_fwd_paged refuses, for empty problems, or
- * when `capacity` is too small.
+ * when `capacity` is too small.  attn_fwd_paged_tree_plan: the same of
+ * attn_fwd_paged_tree, whose plans differ (few and short prefixes and own tokens
+ * stream with more rows, and where both stream their ranges are planned together).
  */
 int attn_fwd_paged_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages,
                         int page_size, int* out, int capacity);
+int attn_fwd_paged_tree_plan(int B, int Nq, int H, int H_kv, int d, int prefix_len, int max_pages,
+                             int page_size, int* out, int capacity);
 
 /* Text of the last error of the calling thread ("" if none). */
 const char* attn_last_error_string(void);
