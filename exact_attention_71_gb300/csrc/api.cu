@@ -1091,7 +1091,8 @@ int paged_call(const char* name, bool tree, const void* q, const void* k_cache, 
     // (CTAs replace one another as they finish.  It takes a CTA 0.4 us to find its sequence: 33
     // drafts x 24 sequences of up to 256, 512 and 1024 tokens, d = 128, bf16, in their order |
     // the longest first, lengths from all to half 24.4 | 26.1, 30.0 | 30.4, 41.3 | 36.3; from all
-    // to 33 25.3 | 23.2, 28.4 | 26.0, 36.5 | 32.0.  128 sequences of up to 1024: 146 | 147, 123 | 125.)
+    // to 33 25.3 | 23.2, 28.4 | 26.0, 36.5 | 32.0.  More than 64 stay in their order: with four
+    // keys a lane 128 sequences of up to 1024 took 146 | 147 and 123 | 125.)
     p.longest_first = tree && B > 1 && B <= 64 && (static_cast<long long>(max_pages) << p.page_shift) >= 512 &&
                       plan.prefix_items + plan.own_items > attn::kPlanSms;
     attn::paged_divisors(p);

@@ -238,11 +238,14 @@ void paged_divisors(PagedParams& p);
 //     d = 64   32 tiles 2^25 bf16 11.6 | 8.9, e4m3 14.4 | 10.1; 128 tiles 2^27 13.5 | 11.5, 15.7 | 13.2
 //     d = 128  32 tiles 2^26 14.9 | 11.4, 16.5 | 11.5; 128 tiles 2^25.6 14.4 | 10.8, 14.2 | 11.0;
 //              64 tiles 2^29 18.5 | 21.2, 18.7 | 20.2; 512 tiles 2^27.6 15.1 | 18.7, 14.9 | 17.9
-//     d = 256  32 tiles 2^24.6 14.2 | 12.8, 16.1 | 11.8; 2^27 15.3 | 15.9, 17.3 | 14.7
+//     d = 256  32 tiles 2^24.6 14.2 | 12.8, 16.1 | 11.8; 2^27 15.3 | 15.9, 17.3 | 14.7;
+//              8 tiles 2^25 (long own tokens of few heads) 13.5 | 14.9, 16.9 | 14.5
 //   prefix, beside own tokens that stream, 64 tiles and 2^26 at most
 //     d = 128  64 tiles 2^25 13.4 | 10.1, 16.8 | 10.6; 2^26 13.5 | 11.8, 16.9 | 12.0; 2^27 14.2 |
 //              15.6, 17.6 | 15.9; 320 tiles 2^26 16.4 | 22.3, 18.7 | 22.3
 //     d = 64   64 tiles 2^26 10.8 | 9.8, 14.6 | 12.3;  d = 256  32 tiles 2^26 13.6 | 12.5, 18.2 | 12.5
+// (One edge for both types: from 2^26 to 2^27 an e4m3 prefix would still gain, a bf16 one
+// lose.  Between 64 and 320 tiles of a prefix nothing was measured.)
 constexpr long long kTreeOwnTiles = 128, kTreePrefixTiles = 64, kTreePrefixWork = 1ll << 26;
 constexpr long long tree_own_work(int d) { return d == 256 ? 1ll << 25 : 1ll << 27; }
 constexpr int kTreeStreamNodes = 32;

@@ -53,13 +53,16 @@
 // path, which its softmax warp finds once, beside the copy of its query rows (32 nodes
 // at most: by doubling, from lane to lane; more: a thread walks its row's), as bits in
 // local memory; only key tiles that hold drafts read them.  64 drafts x 32 heads of 128
-// for each of 32 sequences of up to 4096 tokens: 97 us, 1040 TFLOP/s and 4.5 TB/s (a
+// for each of 32 sequences of up to 4096 tokens: 98 us, 1030 TFLOP/s and 4.4 TB/s (a
 // chain of as many 98.5): 256 CTAs, of which 152 at a time ask for 6.7 TB/s, and a CTA's
 // start and end.  Sequences go to the CTAs the longest first (in their order: 101).
 // 64 sequences of up to 1024 tokens, 33 drafts, e4m3: 95.5 us, a chain 88: 512 CTAs, each
-// of which starts later.  (The drafts in a kernel of their own, joined with
-// partial results over the tokens before them, took 130: 65536 rows written and read
-// once more, and the latency of lists, pages and rows one after the other.)
+// of which starts later.  The walk is one dependent load a node, before the first product:
+// 8 sequences of 4096 tokens, 32 / 8 heads of 128, bf16, 128, 256 and 512 nodes in one
+// chain 69, 156 and 386 us, in a binary tree 61, 126 and 289, through attn_fwd_paged 58, 111
+// and 209.  (The drafts in a kernel of their own, joined with partial results over the
+// tokens before them, took 130: 65536 rows written and read once more, and the latency of
+// lists, pages and rows one after the other.)
 #pragma once
 
 #include <cuda_bf16.h>

@@ -20,8 +20,9 @@
 // alternating axes 15.8 us against 12.3, 7007 of 32 on sections 24.9 against 19.1; a
 // CTA's angles together, behind a barrier: 13.4 and 20.7, and one axis 30 against 26).
 //
-// Order of the loads: positions first, since the rows' loads would queue before them
-// (32768 tokens of 48 heads into an e4m3 cache 145 us the other way round).
+// Order of the loads: the slot (padding has no position) and positions first, since the
+// rows' loads would queue before them (32768 tokens of 48 heads into an e4m3 cache 145 us
+// the other way round).
 // Measured: 8192 tokens of 40 heads of 128, one axis, 26.0 us, 6.53 TB/s (96 % of the
 // copy rate); those 32768 tokens 119.8 us, 6.32 TB/s (93 %), bf16 122.0 us, 6.74 TB/s;
 // on three axes 155 and 151 us (a warp's chain of position, angles, rows); 32 tokens
@@ -67,15 +68,15 @@ __device__ __forceinline__ LaneMap lane_map(int lane, int rot, bool interleaved)
     return m;
 }
 
-// Two pairs: a' = a c - b s, b' = a s + b c.
+// A pair: a' = a c - b s, b' = a s + b c.
 __device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
     const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
     b = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
     a = x;
 }
 
-// Two pairs of a row, packed: half-split: (x, y) are elements (i, i + 1) and those
-// rot / 2 further on; neighbouring pairs: x and y are a pair each.
+// Two pairs of a row, in two words: half-split: v[0] and v[1] are elements i and i + 1,
+// v[2] and v[3] those rot / 2 further on; neighbouring pairs: each word is one.
 __device__ __forceinline__ void turn2(float (&v)[4], bool interleaved, float c0, float s0, float c1, float s1) {
     if (interleaved) {
         turn_pair(v[0], v[1], c0, s0);
@@ -148,7 +149,8 @@ __device__ __forceinline__ Row16 load_chunks(const void* base, long long at, con
 }
 
 // Whether a lane's rows are loaded between its position and its angles, by plain loads
-// and with eight CTAs an SM (64 registers) instead of seven: appending with one axis.  Microseconds,
+// and with eight CTAs an SM instead of seven (64 registers: several heads a lane then spill 88
+// bytes and read back 128, e4m3, 32 and 52, bf16): appending with one axis.  Microseconds,
 // this way | the other: 32768 tokens of 48 heads of 128 bf16 cache 122.0 | 126.7, e4m3
 // 119.8 | 125.5; of 64 65.2 | 65.1, 63.7 | 65.1; attn_rope's 8192 tokens of 40 heads 27.3 |
 // 26.0; three axes: 7007 tokens of 32 heads 25.1 | 19.1, appending 4999 of 24 14.6 | 12.3.
